@@ -32,6 +32,22 @@ class PlanArrays(C.Structure):
                 ("bwd_items", c_int32_p)]
 
 
+class DecodeOpts(C.Structure):
+    _fields_ = [("chunk_pages", C.c_int32)]
+
+
+class DecodeInfo(C.Structure):
+    _fields_ = [("n_fresh_tokens", C.c_int64), ("n_entries", C.c_int64), ("n_combine", C.c_int64),
+                ("n_part_rows", C.c_int64), ("workspace_bytes", C.c_int64), ("n_write_jobs", C.c_int32),
+                ("n_items", C.c_int32), ("n_live", C.c_int32), ("n_sub", C.c_int32), ("rows_per_sub", C.c_int32),
+                ("chunk_pages", C.c_int32)]
+
+
+class DecodeArrays(C.Structure):
+    _fields_ = [("entries", c_int32_p), ("items", c_int32_p), ("query_order", c_int32_p),
+                ("combine_ptr", c_int32_p), ("combine_row", c_int32_p), ("write_jobs", c_int32_p)]
+
+
 # name -> (restype, argtypes); every symbol include/*.h declares
 SIGNATURES = {
     "tree_attn_plan": (C.c_int, [c_int32_p, c_int32_p, C.c_int32, C.POINTER(PlanOpts), C.POINTER(C.c_void_p)]),
@@ -75,6 +91,21 @@ SIGNATURES = {
     "tree_attn_linear_bwd": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
                                        C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_int32,
                                        C.c_float, C.c_void_p, C.c_size_t, C.c_void_p]),
+    # include/tree_decode.h
+    "tree_attn_decode_plan": (C.c_int, [c_int32_p, c_int32_p, c_int32_p, C.c_int32, c_int32_p, C.c_int32, c_uint8_p,
+                                        c_int32_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.POINTER(DecodeOpts),
+                                        C.POINTER(C.c_void_p)]),
+    "tree_attn_decode_plan_info": (C.c_int, [C.c_void_p, C.POINTER(DecodeInfo)]),
+    "tree_attn_decode_plan_export": (C.c_int, [C.c_void_p, C.POINTER(DecodeArrays)]),
+    "tree_attn_decode_plan_upload": (C.c_int, [C.c_void_p]),
+    "tree_attn_decode_plan_destroy": (None, [C.c_void_p]),
+    "tree_attn_cache_write": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_int64, C.c_void_p,
+                                        C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "tree_attn_cache_append": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64,
+                                         C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "tree_attn_decode": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
+                                   C.c_void_p, C.c_void_p, C.c_void_p, C.c_float, C.c_void_p, C.c_size_t,
+                                   C.c_void_p]),
     # include/tree_loss.h
     "tree_attn_plan_trajectory_info": (C.c_int, [C.c_void_p, c_int32_p, c_int64_p]),
     "tree_attn_plan_trajectories": (C.c_int, [C.c_void_p, c_int32_p, c_int64_p, c_int32_p]),

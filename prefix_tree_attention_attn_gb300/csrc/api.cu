@@ -10,6 +10,7 @@
 
 #include "kernels.h"
 #include "plan.h"
+#include "tree_decode.h"
 
 namespace treeattn {
 
@@ -80,6 +81,19 @@ int launch_main(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUten
 
 int make_tensor_map(CUtensorMap* m, const void* base, int64_t rows, int heads, int d) {
     return make_tmap(m, base, rows, heads, d);
+}
+
+int make_byte_map(CUtensorMap* m, const void* base, int64_t rows, int box_rows) {
+    EncodeTiledFn enc = get_encode();
+    if (!enc) return TREE_ATTN_ERR_CUDA;
+    cuuint64_t dims[2] = {128, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {128};
+    cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA;
 }
 
 int current_device(int* dev) {
@@ -659,6 +673,7 @@ const char* tree_attn_strerror(int s) {
         case TREE_ATTN_ERR_DEVICE_TIMEOUT: return "a bounded device wait ran out";
         case TREE_ATTN_ERR_INVALID_DECAY: return "linear-attention decay outside (0, 1]";
         case TREE_ATTN_ERR_DEVICE_BOUNDS: return "a debug bounds check failed";
+        case TREE_ATTN_ERR_CACHE_FULL: return "a token was appended to a node without room";
         default:
             // status words with a site: code - 1000 * site
             if (s <= -1000 && (-s) % 1000 == -TREE_ATTN_ERR_DEVICE_TIMEOUT) return "a bounded device wait ran out";

@@ -109,6 +109,8 @@ int current_device(int* dev);
 // TMA map of a bf16 [rows, heads, d] tensor: boxes of 64 features x 1 head x
 // 128 rows, 128-byte swizzle.
 int make_tensor_map(CUtensorMap* m, const void* base, int64_t rows, int heads, int d);
+// TMA map of [rows, 128] bytes: boxes of box_rows whole rows, 128-byte swizzle.
+int make_byte_map(CUtensorMap* m, const void* base, int64_t rows, int box_rows);
 // Device address of the current device's status word (kernels' bounded waits).
 int get_status_ptr(int dev, int** out);
 }  // namespace treeattn

@@ -1,0 +1,194 @@
+"""The decode planner on the host: every page of a query's path is covered once, the
+tables stay in range, and bad arguments are refused (CPU only)."""
+import ctypes as C
+
+import numpy as np
+import pytest
+
+from prefix_tree_attention_attn_gb300 import _binding as B
+from prefix_tree_attention_attn_gb300.decode import PAGE, DecodePlan
+from workloads import trees as WT
+
+
+def random_case(rng):
+    n = int(rng.integers(1, 14))
+    t = WT.random_tree(rng, n, [1, 2, 63, 64, 65, 130, 300], n_roots=int(rng.integers(1, min(n, 3) + 1)))
+    seg = [0 if rng.random() < 0.15 else x for x in t.seg_len]
+    cap = [x + int(rng.choice([0, 0, 1, 64, 100])) for x in seg]
+    need = sum(-(-c // PAGE) for c in cap)
+    pool = need + int(rng.integers(0, 5))
+    pages = rng.permutation(pool)[:need]
+    queries = [int(x) for x in rng.integers(-1, n, size=int(rng.integers(1, 12)))]
+    group = int(rng.choice([1, 2, 5, 8, 64, 65, 130]))
+    return t.parent, seg, cap, pages, pool, queries, group
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_items_cover_every_path_once(lib, seed):
+    rng = np.random.default_rng(seed)
+    parent, seg, cap, pages, pool, queries, group = random_case(rng)
+    chunk = int(rng.choice([0, 1, 3, 256]))
+    fresh = rng.random(len(parent)) < 0.7
+    p = DecodePlan(parent, seg, queries, 2 * group, 2, 64, capacity=cap, pages=pages, n_pages=pool, fresh=fresh,
+                   chunk_pages=chunk)
+    x, info = p.export(), p.info
+    first = np.concatenate([[0], np.cumsum([-(-c // PAGE) for c in cap])])
+    live = [r for r, u in enumerate(queries) if u >= 0]
+    assert sorted(x["query_order"]) == live
+    sub, rows = info["n_sub"], info["rows_per_sub"]
+    assert rows <= 64 and (sub - 1) * rows < group <= sub * rows
+    # a page entry names its node, its first token and the room behind it
+    for page, node, at, room in x["entries"]:
+        assert at % PAGE == 0 and 0 < room <= PAGE and room == min(PAGE, cap[node] - at)
+        assert pages[first[node] + at // PAGE] == page
+    seen = {}
+    part_rows = []
+    for e0, e1, g0, g1, part, _ in x["items"]:
+        assert 0 <= e0 < e1 <= info["n_entries"] and 0 <= g0 < g1 <= len(live) * sub
+        assert (g1 - g0) * rows <= 64 and (chunk == 0 or e1 - e0 <= chunk)
+        for g in range(g0, g1):
+            for e in range(e0, e1):
+                key = (g, int(x["entries"][e][0]))
+                assert key not in seen
+                seen[key] = True
+        if part >= 0:
+            part_rows.append((part, part + (g1 - g0) * rows))
+    # partial rows: disjoint and all inside the workspace
+    part_rows.sort()
+    assert all(a[1] <= b[0] for a, b in zip(part_rows, part_rows[1:]))
+    assert not part_rows or part_rows[-1][1] <= info["n_part_rows"]
+    assert info["workspace_bytes"] >= info["n_part_rows"] * 2 * (64 + 2) * 4
+    want = set()
+    for s, r in enumerate(x["query_order"]):
+        u = queries[r]
+        while u >= 0:
+            for pg in pages[first[u]:first[u + 1]]:
+                want |= {(s * sub + j, int(pg)) for j in range(sub)}
+            u = parent[u]
+    assert set(seen) == want
+    # every row group finds its items' partial rows, -1 only where one item writes the output
+    items_of = {g: [] for g in range(len(live) * sub)}
+    for e0, e1, g0, g1, part, _ in x["items"]:
+        for g in range(g0, g1):
+            items_of[g].append(-1 if part < 0 else part + (g - g0) * rows)
+    for g, parts in items_of.items():
+        got = list(x["combine_row"][x["combine_ptr"][g]:x["combine_ptr"][g + 1]])
+        assert sorted(got) == sorted(parts)
+        assert -1 not in got or len(got) == 1
+    # write jobs: the fresh nodes' tokens in depth-first order
+    kids = {v: [c for c in range(len(parent)) if parent[c] == v] for v in range(-1, len(parent))}
+    order, stack = [], list(reversed(kids[-1]))
+    while stack:
+        v = stack.pop()
+        order.append(v)
+        stack.extend(reversed(kids[v]))
+    want_jobs, row = [], 0
+    for v in order:
+        if fresh[v]:
+            for t in range(0, seg[v], PAGE):
+                n = min(PAGE, seg[v] - t)
+                want_jobs.append([pages[first[v] + t // PAGE], row, n, 0])
+                row += n
+    assert x["write_jobs"].tolist() == want_jobs and info["n_fresh_tokens"] == row
+
+
+def test_shared_prefix_is_one_run(lib):
+    """A prompt under 8 siblings is in one item per chunk, not one per sibling; a chain
+    that one query reads is one run."""
+    p = DecodePlan([-1] + [0] * 8, [256] + [64] * 8, range(1, 9), 8, 1, 128, chunk_pages=256)
+    assert p.info["n_items"] == 1 + 8 and p.info["n_entries"] == 4 + 8
+    c = DecodePlan([-1, 0, 1, 2], [64, 64, 64, 10], [3], 8, 1, 128, chunk_pages=256)
+    assert c.info["n_items"] == 1 and c.info["n_part_rows"] == 0 and c.workspace_bytes == 0
+
+
+def status(lib, parent, seg, queries, hq=2, hkv=1, d=64, cap=None, pages=None, n_pages=None, chunk=0):
+    a = lambda x: None if x is None else np.asarray(x, np.int32).ctypes.data_as(B.c_int32_p)  # noqa: E731
+    keep = [np.asarray(x, np.int32) if x is not None else None for x in (parent, seg, cap, pages, queries)]
+    ptr = [None if x is None else x.ctypes.data_as(B.c_int32_p) for x in keep]
+    h = C.c_void_p()
+    pool = 1000 if n_pages is None else n_pages
+    st = lib.tree_attn_decode_plan(ptr[0], ptr[1], ptr[2], len(parent), ptr[3], pool, None, ptr[4], len(queries), hq, hkv,
+                                   d, C.byref(B.DecodeOpts(chunk)), C.byref(h))
+    assert (st == 0) == bool(h.value)
+    lib.tree_attn_decode_plan_destroy(h)
+    return st
+
+
+def test_plan_refusals(lib):
+    ok = dict(parent=[-1, 0], seg=[100, 3], queries=[1])
+    assert status(lib, **ok) == 0
+    assert status(lib, **{**ok, "seg": [0, 0]}) == 0                        # nodes may be empty
+    for bad in ([0, 0], [-1, 2], [-1, -2], [1, 0]):
+        assert status(lib, **{**ok, "parent": bad}) == -2
+    assert status(lib, [-1, 2, 1], [1, 1, 1], [0]) == -2                    # a cycle beside a root
+    assert status(lib, **{**ok, "seg": [100, -1]}) == -2
+    assert status(lib, **ok, cap=[100, 2]) == -2                            # room below the tokens
+    for q in ([2], [-2]):
+        assert status(lib, **{**ok, "queries": q}) == -1
+    assert status(lib, [], [], [0]) == -1 and status(lib, [-1], [1], []) == -1
+    assert status(lib, **ok, pages=[0, 1, 1]) == -1                         # a page twice
+    assert status(lib, **ok, pages=[0, 1, 7], n_pages=7) == -1              # behind the pool
+    assert status(lib, **ok, pages=[0, 1, -1]) == -1
+    assert status(lib, **ok, n_pages=2) == -1                               # three are needed
+    assert status(lib, **ok, n_pages=3) == 0
+    for chunk in (-1, 257):
+        assert status(lib, **ok, chunk=chunk) == -1
+    for hq, hkv, d in ((3, 2, 64), (0, 1, 64), (2, 0, 64), (2, 1, 96), (2, 1, 256)):
+        assert status(lib, **ok, hq=hq, hkv=hkv, d=d) == -4
+    assert status(lib, **ok, hkv=2, n_pages=2 ** 31 - 1) == -3              # page rows pass 31 bits
+    assert status(lib, [-1, 0], [2 ** 31 - 1, 2 ** 31 - 1], [1]) != 0
+    assert lib.tree_attn_decode_plan(None, None, None, 1, None, 1, None, None, 1, 1, 1, 64, None, None) == -1
+    assert lib.tree_attn_decode_plan_info(None, None) == -1 and lib.tree_attn_decode_plan_export(None, None) == -1
+    assert lib.tree_attn_decode_plan_upload(None) == -1
+    lib.tree_attn_decode_plan_destroy(None)
+    assert lib.tree_attn_strerror(-14).decode() == "a token was appended to a node without room"
+    with pytest.raises(ValueError):
+        DecodePlan([-1, 0], [100, 3], [1], 2, 1, 64, pages=[0, 1])          # three pages are needed
+    with pytest.raises(ValueError):
+        DecodePlan([-1, 0], [100], [1], 2, 1, 64)
+    with pytest.raises(ValueError):
+        DecodePlan([-1, 0], [100, 3], [1], 2, 1, 64, fresh=[True])
+
+
+def test_calls_validate_before_touching_the_device(lib):
+    p = DecodePlan([-1, 0, 0], [100, 60, 60], [1, 2], 4, 2, 128, chunk_pages=1)
+    f, odd = C.c_void_p(0x1000), C.c_void_p(0x1008)
+    w = lib.tree_attn_cache_write
+    assert w(None, f, f, 256, 256, f, f, f, f, None) == -1
+    assert w(p.handle, None, f, 256, 256, f, f, f, f, None) == -1
+    assert w(p.handle, f, f, 248, 256, f, f, f, f, None) == -1              # rows overlap
+    assert w(p.handle, f, f, 256, 260, f, f, f, f, None) == -1              # not a multiple of 8
+    assert w(p.handle, odd, f, 256, 256, f, f, f, f, None) == -5
+    assert w(p.handle, f, f, 256, 256, f, f, f, C.c_void_p(0x1001), None) == -5
+    a = lib.tree_attn_cache_append
+    assert a(p.handle, None, f, f, f, 256, 256, f, f, f, f, None) == -1
+    assert a(p.handle, f, f, f, f, 128, 256, f, f, f, f, None) == -1
+    assert a(p.handle, f, f, f, odd, 256, 256, f, f, f, f, None) == -5
+    twice = DecodePlan([-1, 0], [100, 60], [1, 1], 4, 2, 128)
+    assert a(twice.handle, f, f, f, f, 256, 256, f, f, f, f, None) == -1    # one node, two tokens
+    dec = lib.tree_attn_decode
+    big = 1 << 30
+    assert p.workspace_bytes > 0
+    assert dec(p.handle, f, None, 512, f, f, f, f, f, f, 1.0, f, big, None) == -1
+    assert dec(p.handle, f, f, 504, f, f, f, f, f, f, 1.0, f, big, None) == -1
+    assert dec(p.handle, f, f, 516, f, f, f, f, f, f, 1.0, f, big, None) == -1
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        assert dec(p.handle, f, f, 512, f, f, f, f, f, f, scale, f, big, None) == -1
+    assert dec(p.handle, f, odd, 512, f, f, f, f, f, f, 1.0, f, big, None) == -5
+    assert dec(p.handle, f, f, 512, f, f, f, f, f, f, 1.0, None, big, None) == -6
+    assert dec(p.handle, f, f, 512, f, f, f, f, f, f, 1.0, f, 16, None) == -6
+    assert dec(p.handle, f, f, 512, f, f, f, f, f, f, 1.0, C.c_void_p(0x1080), big, None) == -5
+
+
+def test_encode_is_the_format(lib):
+    """The oracle's codes against the framework's e4m3 type, and its page scales."""
+    import torch
+    from oracle import decode as OD
+    rng = np.random.default_rng(5)
+    x = np.concatenate([rng.standard_normal(4000) * 2.0 ** rng.integers(-14, 10, 4000), OD.VALUES[:127],
+                        (OD.VALUES[:126] + OD.VALUES[1:127]) / 2, [0.0, -0.0, 2.0 ** -10, 2.0 ** -11]])
+    x = np.clip(x.astype(np.float32), -448, 448)
+    assert np.array_equal(OD.encode(x), torch.from_numpy(x).to(torch.float8_e4m3fn).view(torch.uint8).numpy())
+    assert OD.encode([1e9, -np.inf]).tolist() == [126, 254] and OD.encode([np.nan])[0] & 127 == 127
+    assert OD.page_exp([448.0]) == 0 and OD.page_exp([448.1]) == 1 and OD.page_exp([0.0]) == -100
+    assert OD.page_exp([np.inf, 3.5, np.nan]) == -7
