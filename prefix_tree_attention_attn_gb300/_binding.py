@@ -48,6 +48,12 @@ class DecodeArrays(C.Structure):
                 ("combine_ptr", c_int32_p), ("combine_row", c_int32_p), ("write_jobs", c_int32_p)]
 
 
+class Sampling(C.Structure):
+    """A parameter of every row: one value, or an array of one per row."""
+    _fields_ = [("temperatures", C.c_void_p), ("top_ks", C.c_void_p), ("top_ps", C.c_void_p), ("min_ps", C.c_void_p),
+                ("temperature", C.c_float), ("top_k", C.c_int32), ("top_p", C.c_float), ("min_p", C.c_float)]
+
+
 # name -> (restype, argtypes); every symbol include/*.h declares
 SIGNATURES = {
     "tree_attn_plan": (C.c_int, [c_int32_p, c_int32_p, C.c_int32, C.POINTER(PlanOpts), C.POINTER(C.c_void_p)]),
@@ -106,6 +112,9 @@ SIGNATURES = {
     "tree_attn_decode": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
                                    C.c_void_p, C.c_void_p, C.c_void_p, C.c_float, C.c_void_p, C.c_size_t,
                                    C.c_void_p]),
+    # include/tree_sample.h
+    "tree_attn_sample": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.POINTER(Sampling),
+                                   C.c_void_p, C.c_void_p, C.c_void_p]),
     # include/tree_loss.h
     "tree_attn_plan_trajectory_info": (C.c_int, [C.c_void_p, c_int32_p, c_int64_p]),
     "tree_attn_plan_trajectories": (C.c_int, [C.c_void_p, c_int32_p, c_int64_p, c_int32_p]),
