@@ -122,7 +122,9 @@ struct Meta {
     float kf[kDecodeMaxChunk];      // k_scale * softmax_scale * log2(e)
     float lv[kDecodeMaxChunk];      // log2(v_scale)
     int32_t n;
-    uint64_t full[16], empty[16];
+    uint64_t full[kDecodeMaxChunk];   // one per page, used once: pages land out of order, and a
+                                      // warp may come to a stage whose last use it had no part in
+    uint64_t empty[16];               // one per stage
     float m[kWarps][16], l[kWarps][16];
 };
 
@@ -140,13 +142,9 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     const int split = kWarps / tiles;                        // warps that share a tile's pages
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(smem_u32(&M.full[i]), 1);
-            mbar_init(smem_u32(&M.empty[i]), tiles);
-        }
-        fence_mbar_init();
-    }
+    for (int i = threadIdx.x; i < e1 - e0; i += kThreads) mbar_init(smem_u32(&M.full[i]), 1);
+    if (threadIdx.x < S::kStages) mbar_init(smem_u32(&M.empty[threadIdx.x]), tiles);
+    fence_mbar_init();
     grid_dep_wait();
     grid_dep_launch();
     if (warp == kWarps) {
@@ -234,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
             for (; i < n; ++i) {
                 const int s = i % S::kStages;
                 if (i >= S::kStages && !mbar_wait(smem_u32(&M.empty[s]), ((i / S::kStages) - 1) & 1, p.status, 301)) break;
-                const uint32_t dst = ring + s * S::kStage, bar = smem_u32(&M.full[s]);
+                const uint32_t dst = ring + s * S::kStage, bar = smem_u32(&M.full[i]);
                 const int64_t ph = (int64_t)M.page[i] * p.hkv + h;
                 mbar_expect_tx(bar, S::kStage);
                 if constexpr (D == 128) {
@@ -249,12 +247,12 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
             }
             // no copy is in flight once the ring is reused, whatever ended the loop
             for (int j = max(0, i - S::kStages); j < i; ++j)
-                mbar_wait(smem_u32(&M.full[j % S::kStages]), (j / S::kStages) & 1, p.status, 303);
+                mbar_wait(smem_u32(&M.full[j]), 0, p.status, 303);
         }
     } else {
         for (int i = turn; i < n; i += split) {
             const int s = i % S::kStages;
-            if (!mbar_wait(smem_u32(&M.full[s]), (i / S::kStages) & 1, p.status, 302)) break;
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&M.full[i]), 0, p.status, 302))) break;
             const uint32_t kb = ring + s * S::kStage, vb = kb + S::kHalf;
             const int valid = M.valid[i];
             float c[8][4];
@@ -411,14 +409,17 @@ template <int D>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
     const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
-    if (w >= (int64_t)p.live * p.hq) return;
+    if (w >= (int64_t)p.live * p.hq) {
+        grid_dep_wait();   // the next kernel counts on this one to end after the items
+        return;
+    }
     const int place = (int)(w / p.hq), head = (int)(w % p.hq);
     const int h = head / p.group, gi = head % p.group;
     const int rg = place * p.n_sub + gi / p.gsub, off = gi % p.gsub;
     const int c0 = p.ptr[rg], c1 = p.ptr[rg + 1];
     const int64_t qi = p.order[place];
-    if (c1 == c0 + 1 && p.row[c0] < 0) return;         // written by its item
     grid_dep_wait();
+    if (c1 == c0 + 1 && p.row[c0] < 0) return;         // written by its item
     constexpr int PL = D / 32;
     const int64_t base = h * p.part_rows + off;
     float top = -INFINITY;

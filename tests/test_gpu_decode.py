@@ -337,6 +337,22 @@ def test_graph_and_streams(lib, cuda_device):
     assert device_status() == 0
 
 
+def test_many_pages_in_flight(lib, cuda_device):
+    """Pages land in any order and the warps of an item take them in turn: long items of
+    one row tile and of several, called back to back, give the same bits every time."""
+    rng = np.random.default_rng(13)
+    parent, seg = [-1] + [0] * 24, [64 * 150 + 5] + [64 * int(x) + 9 for x in rng.integers(5, 90, 24)]
+    for hq, queries in ((4, [3]), (8, [1, 2, 3, 4, 5]), (8, list(range(1, 25)))):
+        plan, cache, ref, pages = build(rng, parent, seg, queries, hq, 2, 128, cuda_device, chunk=151)
+        q, ln = rows(rng, len(queries), hq, 128, cuda_device), plan.lens()
+        outs = [TD.tree_decode(plan, cache, ln, q, 0.09) for _ in range(150)]
+        assert device_status() == 0
+        assert all(torch.equal(a, outs[0][0]) and torch.equal(b, outs[0][1]) for a, b in outs)
+        sub = [queries[-1]]
+        wo = OD.decode(ref, parent, seg, seg, pages, sub, q[-1:].float().cpu().numpy(), 0.09)[0]
+        assert np.abs(outs[0][0][-1].float().cpu().numpy() - wo[0]).max() <= 2e-2
+
+
 def test_refused_tensors(lib, cuda_device):
     plan = TD.DecodePlan([-1, 0], [70, 5], [1, 0], 4, 2, 64)
     cache = TD.TreeCache.empty(plan.n_pages, 2, 64, cuda_device)
