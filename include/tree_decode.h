@@ -56,7 +56,7 @@ extern "C" {
 typedef struct tree_decode_plan_s* tree_decode_plan_t;
 
 typedef struct {
-    int32_t chunk_pages;   /* most pages per work item of the attention, 1..256; 0 = automatic */
+    int32_t chunk_pages;   /* most pages per work item of the attention, 1..128; 0 = automatic */
 } tree_attn_decode_opts_t;
 
 typedef struct {

@@ -1,31 +1,44 @@
 // Attention of one new token per query over the tree's 8-bit cache
 // (include/tree_decode.h).
 //
-// A work item is a run of pages and a block of at most 64 query rows (queries
-// under the run x the heads that share a kv-head); a CTA takes one item of one
-// kv-head.  Rows of one shared prefix sit in one tile, so its pages are read once
-// for all of them.  One producer thread streams pages (K and V of one kv-head,
-// 64 * d bytes each) through a ring in shared memory by bulk copies; four consumer
-// warps hold 16 rows each, or, with fewer rows, take the pages in turn with
-// accumulators of their own that are joined at the end.
+// A work item is a run of pages and a block of query rows (queries under the run x
+// the heads that share a kv-head); a CTA takes one item of one kv-head, so pages of
+// a shared prefix are read once for all the rows of its block.  Pages (K and V of one
+// kv-head, 64 * d bytes each) come by bulk copies into a ring of shared memory; the
+// warp (or CTA) that has emptied a stage refills it.
 //
 // Per page, with fp32 accumulation on the tensor cores:
-//   S = Q K8^T        A = query rows, f16; B = the page's codes, f16 (exact: e4m3 values)
+//   S = Q K8^T        Q in f16; K8 the page's codes in f16 (exact: e4m3 values)
 //   x = S * (softmax_scale * log2(e) * k_scale * row factor) + log2(v_scale)
-//   P = 2^(14 + x - M),  M = running maximum of x,   O += P V8,   l += rowsum(P) / v_scale
+//   P = 2^(12 + x - M),  M a running reference,   O += P V8,   l += rowsum(P) / v_scale
 // Folding log2(v_scale) into the exponent makes P the weight of the page's
-// *codes*, so one accumulator serves pages of different scales.  The largest weight
-// is 2^14 whatever the scales (f16 ends at 2^16): P rounds by 2^-11, and what falls
-// below f16's normal numbers, 2^-28 of the largest weight, by 2^-39 of it.  The query row is
-// brought to [1, 2) by a power of two before its rounding to f16: 11 bits hold
+// *codes*, so one accumulator serves pages of different scales.  M follows the row's
+// maximum of x but is moved only when that passes M + 3.5: O is then rescaled, which
+// random logits ask for on the first pages only.  The largest weight so lies in
+// [2^12, 2^15.5] whatever the scales (f16 ends at 2^16): P rounds by 2^-11, and what
+// falls below f16's normal numbers by at most 2^-37 of the largest weight.  The query
+// row is brought to [1, 2) by a power of two before its rounding to f16: 11 bits hold
 // bf16's 8, and what falls below 2^-14 of the row's largest value loses at most
 // 2^-25 of it.  l sums the unrounded fp32 weights.
 //
-// Fragments straight from the pages.  m16n8k16 wants, per lane (g = lane / 4,
-// t = lane % 4), pairs of neighbouring k for column n = g.  The order of k is free
-// as long as both operands agree, so lane t takes features 32t .. 32t+31 of a
-// key (two 16-byte loads for d = 128) and keys 16t .. 16t+15 of a value feature (one):
-// no shuffles, and the S accumulators are already the A fragments of P V.
+// Two bodies, by the item's rows:
+//
+// At most 8 rows (a leaf's own pages) -- `narrow`, bound by HBM.  Each of eight warps
+// takes whole pages in turn with accumulators of its own, joined at the end.  The
+// products run transposed, S^T = K Q^T and O^T = V^T P^T, with m16n8k16: the codes
+// are the 16-row operand and the 8 columns are the query rows, so no half of the tensor
+// product is padding (rows as the 16-row operand, which a leaf of 8 rows half
+// fills, took 2.4 times the instructions).  Fragments come straight from the pages:
+// the order of k is free as long as both operands agree, so lane t of a quad takes
+// features 32t .. 32t+31 of a key (two 16-byte loads for d = 128) and keys 16t .. 16t+15
+// of a value feature (one).  P^T changes from accumulator to operand layout by
+// 8x8 transposes (movmatrix).
+//
+// 9 to 128 rows (shared prefixes) -- `wide`, bound by instruction issue: the same
+// pages would cost a leaf's instructions once per 8 rows.  The codes are expanded
+// once per page to f16 tiles in shared memory and the products are tcgen05.mma with
+// M = 128 rows, accumulators in TMEM, P written back over S as the second product's
+// operand.  Expansion of a page's V overlaps S, of the next page's K overlaps P V.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -37,11 +50,12 @@ namespace treeattn {
 
 namespace {
 
-constexpr int kWarps = 4;                        // consumer warps
-constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLift = 14.f;                    // log2 of the largest weight in P
+constexpr float kLift = 12.f;                    // log2 of the weight of x = M
+constexpr float kSlack = 3.5f;                   // how far x may pass M before M is moved
 
 struct DecodeParams {
     const int32_t* entries;
@@ -100,307 +114,594 @@ __device__ __forceinline__ float quad_max(float x) {
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
     return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
 }
-__device__ __forceinline__ float quad_sum(float x) {
-    x += __shfl_xor_sync(0xffffffffu, x, 1);
-    return x + __shfl_xor_sync(0xffffffffu, x, 2);
+// 8x8 matrix of 16-bit values, row g in lanes 4g .. 4g+3: its transpose, laid out the same
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+// Power of two that brings a row to [1, 2); infinities and NaN stay what they are.
+__device__ __forceinline__ void row_factor(float amax, float& down, float& up) {
+    int e = (int)(__float_as_uint(amax) >> 23);
+    e = (e == 0 || e == 255) ? 127 : min(max(e, 8), 246);
+    down = __uint_as_float((uint32_t)(254 - e) << 23);
+    up = __uint_as_float((uint32_t)e << 23);
+}
+__device__ __forceinline__ float abs_max2(uint32_t w) {
+    return fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u)));
+}
+// two bf16 times a power of two, as f16
+__device__ __forceinline__ uint32_t scaled_f16(uint32_t w, float down) {
+    return pack_f16(__uint_as_float(w << 16) * down, __uint_as_float(w & 0xffff0000u) * down);
 }
 
 template <int D>
 struct Shape {
-    static constexpr int kHalf = kPage * D;          // bytes of K (or V) in a stage
+    static constexpr int kHalf = kPage * D;          // bytes of K (or V) of a page
     static constexpr int kStage = 2 * kHalf;
-    static constexpr int kStages = D == 128 ? 6 : 10;
-    static constexpr int kJoin = kWarps * 16 * (D + 4) * 4;   // fp32 rows of every warp, padded
-    static constexpr int kRing = kStages * kStage;
-    static_assert(kJoin <= kRing, "the join reuses the ring");
+    // narrow: the ring alone; its join reuses it
+    static constexpr int kStages = D == 128 ? 6 : 12;
+    static constexpr int kPitch = D + 4;
+    static_assert(kWarps * 8 * kPitch * 4 <= kStages * kStage, "the join reuses the ring");
+    // wide: two stages, then the f16 tiles of Q, K, V
+    static constexpr int kWideStages = 2;
+    static constexpr int kQ = kWideStages * kStage, kK = kQ + 128 * D * 2, kV = kK + kPage * D * 2;
+    static constexpr int kWide = kV + kPage * D * 2;
+    static constexpr int kRing = kStages * kStage > kWide ? kStages * kStage : kWide;
     static constexpr int kSmem = kRing + 1024;       // + alignment slack
 };
 
 struct Meta {
     int32_t page[kDecodeMaxChunk];
     int32_t valid[kDecodeMaxChunk];
-    float kf[kDecodeMaxChunk];      // k_scale * softmax_scale * log2(e)
-    float lv[kDecodeMaxChunk];      // log2(v_scale)
-    int32_t n;
-    uint64_t full[kDecodeMaxChunk];   // one per page, used once: pages land out of order, and a
-                                      // warp may come to a stage whose last use it had no part in
-    uint64_t empty[16];               // one per stage
-    float m[kWarps][16], l[kWarps][16];
+    float kf[kDecodeMaxChunk];        // k_scale * softmax_scale * log2(e)
+    float lv[kDecodeMaxChunk];        // log2(v_scale)
+    uint64_t full[kDecodeMaxChunk];   // one per page, used once: pages land out of order
+    uint64_t s_done, o_done;          // wide: a tensor product of the page has finished
+    int32_t count[kDecodeMaxChunk / 32];
+    uint32_t tmem;
+    union {
+        struct {
+            float m[kWarps][8], l[kWarps][8];        // narrow: per warp and row
+        };
+        struct {
+            float top[2][128], sum[2][128], qf[128];   // wide: per half of the keys and row
+        };
+    };
+};
+
+// An item's rows: place in the output, and where its query row starts.
+struct Rows {
+    int rg0, rows, gsub, n_sub, group, h;
+    __device__ __forceinline__ bool at(int r, int& place, int& head) const {
+        const int rg = rg0 + r / gsub, gi = (rg % n_sub) * gsub + r % gsub;
+        place = rg / n_sub;
+        head = h * group + gi;
+        return r < rows && gi < group;
+    }
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeParams p) {
+__device__ __forceinline__ void load_page(const CUtensorMap* tk, const DecodeParams& p, int page, int h, uint32_t dst,
+                                          uint32_t bar) {
     using S = Shape<D>;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ Meta M;
-    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const int item = blockIdx.x / p.hkv, h = blockIdx.x % p.hkv;
-    const int32_t* it = p.items + 6 * (int64_t)item;
-    const int e0 = it[0], e1 = it[1], rg0 = it[2], rg1 = it[3], part = it[4];
-    const int rows = (rg1 - rg0) * p.gsub;
-    const int tiles = rows > 32 ? 4 : rows > 16 ? 2 : 1;     // 16-row tiles
-    const int split = kWarps / tiles;                        // warps that share a tile's pages
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-    for (int i = threadIdx.x; i < e1 - e0; i += kThreads) mbar_init(smem_u32(&M.full[i]), 1);
-    if (threadIdx.x < S::kStages) mbar_init(smem_u32(&M.empty[threadIdx.x]), tiles);
-    fence_mbar_init();
-    grid_dep_wait();
-    grid_dep_launch();
-    if (warp == kWarps) {
-        // pages that hold tokens now, packed
-        int n = 0;
-        for (int e = e0; e < e1; e += 32) {
-            int page = 0, valid = 0;
-            if (e + lane < e1) {
-                const int4 x = *reinterpret_cast<const int4*>(p.entries + 4 * (int64_t)(e + lane));
-                page = x.x;
-                valid = max(0, min(max(p.lens[x.y], 0) - x.z, x.w));
-            }
-            const uint32_t has = __ballot_sync(0xffffffffu, valid > 0);
-            if (valid > 0) {
-                const int at = n + __popc(has & ((1u << lane) - 1u));
-                const int64_t ph = (int64_t)page * p.hkv + h;
-                M.page[at] = page;
-                M.valid[at] = valid;
-                M.kf[at] = p.ks[ph] * p.scale_log2;
-                M.lv[at] = (float)((int)(__float_as_uint(p.vs[ph]) >> 23) - 127);
-            }
-            n += __popc(has);
-        }
-        if (lane == 0) M.n = n;
+    const int64_t ph = (int64_t)page * p.hkv + h;
+    mbar_expect_tx(bar, S::kStage);
+    if constexpr (D == 128) {
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tk)), "r"(0),
+            "r"((int)(ph * kPage)), "r"(bar) : "memory");
+    } else {
+        bulk_load(dst, p.k8 + ph * S::kHalf, S::kHalf, bar);
     }
+    bulk_load(dst + S::kHalf, p.v8 + ph * S::kHalf, S::kHalf, bar);
+}
 
-    // query fragments (consumer warps): rows g and g + 8 of the warp's tile
-    const int g = lane >> 2, t = lane & 3;
-    const int tile = warp % tiles, turn = warp / tiles;
-    uint32_t qa[D / 16][4];
-    float qf[2] = {0.f, 0.f};
-    if (warp < kWarps) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int r = tile * 16 + g + 8 * u;
-            const int rg = rg0 + r / p.gsub, gi = (rg % p.n_sub) * p.gsub + r % p.gsub;
-            const bool ok = r < rows && gi < p.group;
-            uint4 w[D / 32];
-            if (ok) {
-                const uint16_t* src = p.q + (int64_t)p.order[rg / p.n_sub] * p.q_stride + (h * p.group + gi) * D + t * (D / 4);
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) w[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
-            } else {
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) w[i] = make_uint4(0, 0, 0, 0);
-            }
-            float amax = 0.f;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[j] << 16)), fabsf(__uint_as_float(x[j] & 0xffff0000u))));
-            }
-            amax = quad_max(amax);
-            // power of two that brings the row to [1, 2); infinities and NaN stay what they are
-            int e = (int)(__float_as_uint(amax) >> 23);
-            e = (e == 0 || e == 255) ? 127 : min(max(e, 8), 246);
-            const float down = __uint_as_float((uint32_t)(254 - e) << 23);
-            qf[u] = __uint_as_float((uint32_t)e << 23);
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {   // word 4i+j: features 2(4i+j), +1 of this lane
-                    const uint32_t f = pack_f16(__uint_as_float(x[j] << 16) * down, __uint_as_float(x[j] & 0xffff0000u) * down);
-                    qa[(4 * i + j) / 2][u + 2 * (j & 1)] = f;
-                }
-            }
-        }
-    }
+// byte address of 16 codes c of key r in a K stage (swizzled by the tensor map for d = 128)
+template <int D>
+__device__ __forceinline__ uint32_t key_chunk(uint32_t base, int r, int c) {
+    return D == 128 ? base + sw128_offset(r, c) : base + r * D + 16 * c;
+}
+// bits of four codes from key k on that lie before `valid`
+__device__ __forceinline__ uint32_t keep_bytes(int k, int valid) {
+    const int n = valid - k;
+    return n >= 4 ? 0xffffffffu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+}
+
+// After a wait that ran out: gives the copies still in flight time to land (their
+// barriers complete) before shared memory is given up.
+__device__ __noinline__ void drain(Meta& M, int n) {
+    for (int i = threadIdx.x; i < n; i += kThreads)
+        for (int k = 0; k < 4096 && !mbar_try_wait(smem_u32(&M.full[i]), 0); ++k) {}
     __syncthreads();
-    const int n = M.n;
+}
 
-    float acc[D / 8][4];
-    float mx[2] = {-INFINITY, -INFINITY}, ls[2] = {0.f, 0.f};
+__device__ __forceinline__ float out_lse(float m, float l) {
+    return l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m - kLift) + log2f(l)) * kLn2;
+}
+
+// ---- at most 8 rows --------------------------------------------------------------
+template <int D>
+__device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint32_t ring, float* buf, const Rows& R,
+                       int part, int n) {
+    using S = Shape<D>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    // the first pages, a warp's own
+    if (lane == 0 && warp < S::kStages)
+        for (int i = warp; i < min(n, S::kStages); i += kWarps)
+            load_page<D>(&tk, p, M.page[i], R.h, ring + i * S::kStage, smem_u32(&M.full[i]));
+
+    // query row g: features t * D/4 .., as the second operand
+    uint32_t qb[D / 16][2];
+    float qf;
+    {
+        int place, head;
+        const bool ok = R.at(g, place, head);
+        uint4 w[D / 32];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+        for (int i = 0; i < D / 32; ++i) w[i] = make_uint4(0, 0, 0, 0);
+        if (ok) {
+            const uint16_t* src = p.q + (int64_t)p.order[place] * p.q_stride + head * D + t * (D / 4);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) w[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
+        }
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+            amax = fmaxf(fmaxf(amax, fmaxf(abs_max2(w[i].x), abs_max2(w[i].y))), fmaxf(abs_max2(w[i].z), abs_max2(w[i].w)));
+        float down;
+        row_factor(quad_max(amax), down, qf);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            qb[2 * i][0] = scaled_f16(w[i].x, down);
+            qb[2 * i][1] = scaled_f16(w[i].y, down);
+            qb[2 * i + 1][0] = scaled_f16(w[i].z, down);
+            qb[2 * i + 1][1] = scaled_f16(w[i].w, down);
+        }
+    }
+    // factors of the accumulators' columns: rows 2t and 2t + 1
+    const float qf0 = __shfl_sync(0xffffffffu, qf, 8 * t), qf1 = __shfl_sync(0xffffffffu, qf, 8 * t + 4);
+
+    float acc[D / 16][4];
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
 
-    if (warp == kWarps) {
-        if (lane == 0) {
-            int i = 0;
-            for (; i < n; ++i) {
-                const int s = i % S::kStages;
-                if (i >= S::kStages && !mbar_wait(smem_u32(&M.empty[s]), ((i / S::kStages) - 1) & 1, p.status, 301)) break;
-                const uint32_t dst = ring + s * S::kStage, bar = smem_u32(&M.full[i]);
-                const int64_t ph = (int64_t)M.page[i] * p.hkv + h;
-                mbar_expect_tx(bar, S::kStage);
-                if constexpr (D == 128) {
-                    asm volatile(
-                        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(&tk)), "r"(0),
-                        "r"((int)(ph * kPage)), "r"(bar) : "memory");
-                } else {
-                    bulk_load(dst, p.k8 + ph * S::kHalf, S::kHalf, bar);
-                }
-                bulk_load(dst + S::kHalf, p.v8 + ph * S::kHalf, S::kHalf, bar);
+    bool ok = true;
+    for (int i = warp; i < n; i += kWarps) {
+        const int s = i % S::kStages;
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&M.full[i]), 0, p.status, 302));
+        if (!ok) break;
+        const uint32_t kb = ring + s * S::kStage, vb = kb + S::kHalf;
+        const int valid = M.valid[i];
+        // tile x: keys 16 (g/2) + 4x + (g & 1) and two further on
+        float c[4][4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int key = 16 * (g >> 1) + 4 * x + (g & 1);
+            uint32_t w0[D / 16], w1[D / 16];
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+                lds128(key_chunk<D>(kb, key, (D / 64) * t + j), *reinterpret_cast<uint32_t(*)[4]>(&w0[4 * j]));
+                lds128(key_chunk<D>(kb, key + 2, (D / 64) * t + j), *reinterpret_cast<uint32_t(*)[4]>(&w1[4 * j]));
             }
-            // no copy is in flight once the ring is reused, whatever ended the loop
-            for (int j = max(0, i - S::kStages); j < i; ++j)
-                mbar_wait(smem_u32(&M.full[j]), 0, p.status, 303);
+            c[x][0] = c[x][1] = c[x][2] = c[x][3] = 0.f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                uint32_t a[4];
+                codes_f16(w0[j], a[0], a[2]);
+                codes_f16(w1[j], a[1], a[3]);
+                mma16816(c[x], a, qb[j][0], qb[j][1]);
+            }
         }
-    } else {
-        for (int i = turn; i < n; i += split) {
-            const int s = i % S::kStages;
-            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&M.full[i]), 0, p.status, 302))) break;
-            const uint32_t kb = ring + s * S::kStage, vb = kb + S::kHalf;
-            const int valid = M.valid[i];
-            float c[8][4];
+        const float lv = M.lv[i], kf = M.kf[i];
+        const float f0 = kf * qf0, f1 = kf * qf1;
+        float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const int key = 16 * (g >> 1) + 2 * x + (g & 1);
-                uint32_t w[D / 16];
-                if constexpr (D == 128) {
-                    uint32_t a[4], b[4];
-                    lds128(kb + sw128_offset(key, 2 * t), a);
-                    lds128(kb + sw128_offset(key, 2 * t + 1), b);
+        for (int x = 0; x < 4; ++x) {
+            const int key = 16 * (g >> 1) + 4 * x + (g & 1);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        w[j] = a[j];
-                        w[(D / 32) + j] = b[j];
-                    }
-                } else {
-                    uint32_t a[4];
-                    lds128(kb + key * D + 16 * t, a);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) w[j] = a[j];
-                }
-                c[x][0] = c[x][1] = c[x][2] = c[x][3] = 0.f;
-#pragma unroll
-                for (int j = 0; j < D / 16; ++j) {
-                    uint32_t b0, b1;
-                    codes_f16(w[j], b0, b1);
-                    mma16816(c[x], qa[j], b0, b1);
-                }
+            for (int j = 0; j < 4; ++j) {
+                c[x][j] = (j & 1 ? f1 : f0) * c[x][j] + lv;
+                if (valid < kPage && key + (j & 2) >= valid) c[x][j] = -INFINITY;
             }
-            const float lv = M.lv[i], kf = M.kf[i];
-            const float f0 = kf * qf[0], f1 = kf * qf[1];
-            // element (x, j): key 16t + 2x + (j & 1), row g + 8 (j >> 1)
-            float top0 = -INFINITY, top1 = -INFINITY;
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    c[x][j] = (j < 2 ? f0 : f1) * c[x][j] + lv;
-                    if (valid < kPage && 16 * t + 2 * x + (j & 1) >= valid) c[x][j] = -INFINITY;
-                }
-                top0 = fmax3(top0, c[x][0], c[x][1]);
-                top1 = fmax3(top1, c[x][2], c[x][3]);
-            }
-            const float m0 = fmaxf(mx[0], quad_max(top0)), m1 = fmaxf(mx[1], quad_max(top1));
-            if (__any_sync(0xffffffffu, m0 != mx[0] || m1 != mx[1])) {
-                const float a0 = m0 == -INFINITY ? 1.f : fast_exp2(mx[0] - m0);
-                const float a1 = m1 == -INFINITY ? 1.f : fast_exp2(mx[1] - m1);
-                ls[0] *= a0;
-                ls[1] *= a1;
-#pragma unroll
-                for (int y = 0; y < D / 8; ++y) {
-                    acc[y][0] *= a0;
-                    acc[y][1] *= a0;
-                    acc[y][2] *= a1;
-                    acc[y][3] *= a1;
-                }
-                mx[0] = m0;
-                mx[1] = m1;
-            }
-            const float r0 = m0 == -INFINITY ? 0.f : m0 - kLift, r1 = m1 == -INFINITY ? 0.f : m1 - kLift;
-            float s0 = 0.f, s1 = 0.f;
-            uint32_t pa[4][4];
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const float p0 = fast_exp2(c[x][0] - r0), p1 = fast_exp2(c[x][1] - r0);
-                const float p2 = fast_exp2(c[x][2] - r1), p3 = fast_exp2(c[x][3] - r1);
-                s0 += p0 + p1;
-                s1 += p2 + p3;
-                pa[x >> 1][2 * (x & 1)] = pack_f16(p0, p1);
-                pa[x >> 1][2 * (x & 1) + 1] = pack_f16(p2, p3);
-            }
-            const float iv = fast_exp2(-lv);
-            ls[0] += s0 * iv;
-            ls[1] += s1 * iv;
-            uint32_t keep[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {       // bytes of the lane's keys 16t + 4j .. that hold tokens
-                const int k = valid - 16 * t - 4 * j;
-                keep[j] = k >= 4 ? 0xffffffffu : k <= 0 ? 0u : (1u << (8 * k)) - 1u;
-            }
-#pragma unroll
-            for (int y = 0; y < D / 8; ++y) {
-                uint32_t w[4];
-                lds128(vb + (8 * y + g) * kPage + 16 * t, w);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t b0, b1;
-                    codes_f16(w[j] & keep[j], b0, b1);
-                    mma16816(acc[y], pa[j], b0, b1);
-                }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&M.empty[s]));
+            top0 = fmax3(top0, c[x][0], c[x][2]);
+            top1 = fmax3(top1, c[x][1], c[x][3]);
         }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, o));
+            top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, o));
+        }
+        const bool up0 = top0 > m0 + kSlack, up1 = top1 > m1 + kSlack;
+        if (__any_sync(0xffffffffu, up0 || up1)) {
+            const float a0 = up0 ? fast_exp2(m0 - top0) : 1.f, a1 = up1 ? fast_exp2(m1 - top1) : 1.f;
+            l0 *= a0;
+            l1 *= a1;
+#pragma unroll
+            for (int y = 0; y < D / 16; ++y) {
+                acc[y][0] *= a0;
+                acc[y][1] *= a1;
+                acc[y][2] *= a0;
+                acc[y][3] *= a1;
+            }
+            m0 = up0 ? top0 : m0;
+            m1 = up1 ? top1 : m1;
+        }
+        const float r0 = m0 == -INFINITY ? 0.f : m0 - kLift, r1 = m1 == -INFINITY ? 0.f : m1 - kLift;
+        float s0 = 0.f, s1 = 0.f;
+        uint32_t pb[4][2];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float p0 = fast_exp2(c[x][0] - r0), p1 = fast_exp2(c[x][1] - r1);
+            const float p2 = fast_exp2(c[x][2] - r0), p3 = fast_exp2(c[x][3] - r1);
+            s0 += p0 + p2;
+            s1 += p1 + p3;
+            pb[x][0] = transpose8(pack_f16(p0, p1));
+            pb[x][1] = transpose8(pack_f16(p2, p3));
+        }
+        const float iv = fast_exp2(-lv);
+        l0 += s0 * iv;
+        l1 += s1 * iv;
+        // what is behind the last token may be anything, NaN included
+        uint32_t keep[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) keep[j] = keep_bytes(16 * t + 4 * j, valid);
+        const bool part_page = valid < kPage;
+#pragma unroll
+        for (int y = 0; y < D / 16; ++y) {
+            uint32_t w0[4], w1[4];
+            lds128(vb + (16 * y + g) * kPage + 16 * t, w0);
+            lds128(vb + (16 * y + g + 8) * kPage + 16 * t, w1);
+            if (part_page) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    w0[x] &= keep[x];
+                    w1[x] &= keep[x];
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                uint32_t a[4];
+                codes_f16(w0[x], a[0], a[2]);
+                codes_f16(w1[x], a[1], a[3]);
+                mma16816(acc[y], a, pb[x][0], pb[x][1]);
+            }
+        }
+        __syncwarp();
+        if (lane == 0 && i + S::kStages < n)
+            load_page<D>(&tk, p, M.page[i + S::kStages], R.h, kb, smem_u32(&M.full[i + S::kStages]));
     }
-    __syncthreads();      // every page has been consumed: the ring is free
-
-    // join: every warp's rows to shared memory, then row by row over the warps of a tile
-    float* buf = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)));
-    constexpr int kPitch = D + 4;
-    if (warp < kWarps) {
-        ls[0] = quad_sum(ls[0]);
-        ls[1] = quad_sum(ls[1]);
-        if (t == 0) {
-            M.m[warp][g] = mx[0];
-            M.m[warp][g + 8] = mx[1];
-            M.l[warp][g] = ls[0];
-            M.l[warp][g + 8] = ls[1];
-        }
-        float* b = buf + warp * 16 * kPitch;
+    // every page was waited for by its warp: the ring is free
+    if (!__syncthreads_and(ok)) {
+        drain(M, n);
+        return;
+    }
 #pragma unroll
-        for (int y = 0; y < D / 8; ++y) {
-            *reinterpret_cast<float2*>(b + g * kPitch + 8 * y + 2 * t) = make_float2(acc[y][0], acc[y][1]);
-            *reinterpret_cast<float2*>(b + (g + 8) * kPitch + 8 * y + 2 * t) = make_float2(acc[y][2], acc[y][3]);
-        }
+    for (int o = 4; o < 32; o <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+    }
+    if (g == 0) {
+        M.m[warp][2 * t] = m0;
+        M.m[warp][2 * t + 1] = m1;
+        M.l[warp][2 * t] = l0;
+        M.l[warp][2 * t + 1] = l1;
+    }
+    float* b = buf + warp * 8 * S::kPitch;
+#pragma unroll
+    for (int y = 0; y < D / 16; ++y) {
+        b[(2 * t) * S::kPitch + 16 * y + g] = acc[y][0];
+        b[(2 * t + 1) * S::kPitch + 16 * y + g] = acc[y][1];
+        b[(2 * t) * S::kPitch + 16 * y + g + 8] = acc[y][2];
+        b[(2 * t + 1) * S::kPitch + 16 * y + g + 8] = acc[y][3];
     }
     __syncthreads();
-    for (int x = threadIdx.x; x < rows * (D / 4); x += kThreads) {
+    const int warps = min(n, kWarps);
+    for (int x = threadIdx.x; x < R.rows * (D / 4); x += kThreads) {
         const int r = x / (D / 4), c = 4 * (x % (D / 4));
-        const int rg = rg0 + r / p.gsub, gi = (rg % p.n_sub) * p.gsub + r % p.gsub;
-        if (gi >= p.group) continue;
+        int place, head;
+        if (!R.at(r, place, head)) continue;
         float top = -INFINITY;
-        for (int u = 0; u < split; ++u) top = fmaxf(top, M.m[(r >> 4) + u * tiles][r & 15]);
+        for (int w = 0; w < warps; ++w) top = fmaxf(top, M.m[w][r]);
         const float ref = top == -INFINITY ? 0.f : top;
         float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int u = 0; u < split; ++u) {
-            const int w = (r >> 4) + u * tiles;
-            const float f = fast_exp2(M.m[w][r & 15] - ref);
-            const float4 v = *reinterpret_cast<const float4*>(buf + (w * 16 + (r & 15)) * kPitch + c);
-            l += f * M.l[w][r & 15];
+        for (int w = 0; w < warps; ++w) {
+            const float f = fast_exp2(M.m[w][r] - ref);
+            const float4 v = *reinterpret_cast<const float4*>(buf + (w * 8 + r) * S::kPitch + c);
+            l += f * M.l[w][r];
             o[0] += f * v.x;
             o[1] += f * v.y;
             o[2] += f * v.z;
             o[3] += f * v.w;
         }
         if (part >= 0) {
-            const int64_t at = h * p.part_rows + part + r;
+            const int64_t at = R.h * p.part_rows + part + r;
             *reinterpret_cast<float4*>(p.part_o + at * D + c) = make_float4(o[0], o[1], o[2], o[3]);
             if (c == 0) p.part_ml[at] = make_float2(top, l);
         } else {
-            const int64_t qi = p.order[rg / p.n_sub];
-            const int head = h * p.group + gi;
+            const int64_t qi = p.order[place];
             const float inv = l == 0.f ? 0.f : 1.f / l;
             *reinterpret_cast<uint2*>(p.o + (qi * p.hq + head) * D + c) =
                 make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-            if (c == 0) p.lse[(int64_t)head * p.R + qi] = l == 0.f ? -INFINITY : (ref - kLift + log2f(l)) * kLn2;
+            if (c == 0) p.lse[(int64_t)head * p.R + qi] = out_lse(top, l);
         }
+    }
+}
+
+// ---- 9 to 128 rows -----------------------------------------------------------------
+// Instruction descriptor, kind::f16: f16 A and B, fp32 accumulator, both K-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24); }
+
+// 16 codes to 32 bytes of f16: chunks c, c + 1 of row r of a 128-byte-swizzled tile
+__device__ __forceinline__ void expand16(const uint32_t (&w)[4], uint32_t tile, int r, int c) {
+    uint32_t f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) codes_f16(w[j], f[2 * j], f[2 * j + 1]);
+    st_shared_v4(tile + sw128_offset(r, c), f[0], f[1], f[2], f[3]);
+    st_shared_v4(tile + sw128_offset(r, c + 1), f[4], f[5], f[6], f[7]);
+}
+
+template <int D>
+__device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint32_t ring, const Rows& R, int part, int n) {
+    using S = Shape<D>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = 32 * (warp & 3) + lane, half = warp >> 2;   // TMEM lane; keys 32 half ..
+    const uint32_t qs = ring + S::kQ, ks = ring + S::kK, vs = ring + S::kV;
+    const uint32_t tmem = M.tmem;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t o_col = tmem + 128;                          // S tiles at columns 0 and 64, O from 128
+    if (threadIdx.x == 0)
+        for (int i = 0; i < min(n, S::kWideStages); ++i)
+            load_page<D>(&tk, p, M.page[i], R.h, ring + i * S::kStage, smem_u32(&M.full[i]));
+    // Q to f16, two threads per row
+    {
+        const int r = threadIdx.x >> 1, hf = threadIdx.x & 1;
+        int place, head;
+        const bool ok = R.at(r, place, head);
+        uint4 w[D / 16];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) w[i] = make_uint4(0, 0, 0, 0);
+        if (ok) {
+            const uint16_t* src = p.q + (int64_t)p.order[place] * p.q_stride + head * D + hf * (D / 2);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) w[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
+        }
+        float amax = 0.f, down, up;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+            amax = fmaxf(fmaxf(amax, fmaxf(abs_max2(w[i].x), abs_max2(w[i].y))), fmaxf(abs_max2(w[i].z), abs_max2(w[i].w)));
+        row_factor(fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1)), down, up);
+        if (hf == 0) M.qf[r] = up;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            const int c = hf * (D / 16) + i;                    // 8 features
+            st_shared_v4(qs + (c >> 3) * 16384 + sw128_offset(r, c & 7), scaled_f16(w[i].x, down), scaled_f16(w[i].y, down),
+                         scaled_f16(w[i].z, down), scaled_f16(w[i].w, down));
+        }
+    }
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+        const int st = i % S::kWideStages;
+        const uint32_t kb = ring + st * S::kStage, vb = kb + S::kHalf, s_col = tmem + 64 * (i & 1);
+        const int valid = M.valid[i];
+        ok = ok && mbar_wait(smem_u32(&M.full[i]), 0, p.status, 304);
+        // K to f16.  Eight lanes take four chunks of two rows that differ in bits 0 and 2, so
+        // that loads (swizzled by the row's 3 bits over 8 chunks) and stores both spread over
+        // all banks.
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) {
+            uint32_t w[4];
+            if constexpr (D == 128) {
+                const int c = 4 * x + (threadIdx.x & 3), q = threadIdx.x >> 2;
+                const int r = (q & ~5) | (((q & 1) * 5) ^ (q & 4));
+                lds128(kb + sw128_offset(r, c), w);
+                expand16(w, ks + x * 8192, r, 2 * (c & 3));
+            } else {
+                lds128(kb + threadIdx.x * 16, w);
+                expand16(w, ks, threadIdx.x >> 2, 2 * (threadIdx.x & 3));
+            }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        ok = __syncthreads_and(ok);
+        if (!ok) break;
+        if (threadIdx.x == 0) {
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+                mma_bf16_ss(s_col, sdesc_sw128(qs + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024),
+                            sdesc_sw128(ks + (k >> 2) * 8192 + (k & 3) * 32, 16, 1024), idesc_f16(128, kPage), k > 0);
+            mma_commit(smem_u32(&M.s_done));
+        }
+        // V to f16, once the previous page's P V has read the tile
+        if (i > 0) ok = mbar_wait(smem_u32(&M.o_done), (i - 1) & 1, p.status, 305);
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) {
+            const int at = threadIdx.x + x * kThreads;
+            uint32_t w[4];
+            lds128(vb + at * 16, w);
+            if (valid < kPage) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] &= keep_bytes(16 * (at & 3) + 4 * j, valid);
+            }
+            expand16(w, vs, at >> 2, 2 * (at & 3));
+        }
+        fence_proxy_async_smem();
+        // softmax over this thread's 32 keys of its row
+        ok = mbar_wait(smem_u32(&M.s_done), i & 1, p.status, 306) && ok;
+        tc_fence_after();
+        const float lv = M.lv[i], f = M.kf[i] * M.qf[row];
+        float c[32];
+        tmem_ld32(s_col + lanes + 32 * half, c);
+        tmem_wait_ld();
+        float top = -INFINITY;
+        const uint64_t f2 = f32x2(f, f), lv2 = f32x2(lv, lv);
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) f32x2_split(fma_f32x2(f32x2(c[j], c[j + 1]), f2, lv2), c[j], c[j + 1]);
+        if (valid < kPage) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (32 * half + j >= valid) c[j] = -INFINITY;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) top = fmax3(top, c[j], c[j + 1]);
+        // everyone has read its part of S (P goes over it), and whether a row has to move its
+        // reference
+        tc_fence_before();
+        if (__syncthreads_or(top > m + kSlack)) {
+            M.top[half][row] = top;
+            __syncthreads();
+            const float both = fmaxf(top, M.top[1 - half][row]);
+            const bool up = both > m + kSlack;
+            const float a = up ? fast_exp2(m - both) : 1.f;
+            tc_fence_after();
+            if (i > 0 && __any_sync(0xffffffffu, up)) {
+#pragma unroll
+                for (int x = 0; x < D / 64; ++x) {
+                    float v[32];
+                    tmem_ld32(o_col + lanes + half * (D / 2) + 32 * x, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] *= a;
+                    tmem_st32(o_col + lanes + half * (D / 2) + 32 * x, v);
+                }
+                tmem_wait_st();
+            }
+            l *= a;
+            m = up ? both : m;
+        }
+        tc_fence_after();
+        const float base = m == -INFINITY ? 0.f : m - kLift;
+        uint32_t pw[16];
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float a = fast_exp2(c[2 * j] - base), b = fast_exp2(c[2 * j + 1] - base);
+            sum += a + b;
+            pw[j] = pack_f16(a, b);
+        }
+        l += sum * fast_exp2(-lv);
+        tmem_st16(s_col + lanes + 16 * half, pw);
+        tmem_wait_st();
+        tc_fence_before();
+        ok = __syncthreads_and(ok);
+        if (!ok) break;
+        if (threadIdx.x == 0) {
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < kPage / 16; ++k)
+                mma_bf16_ts(o_col, s_col + 8 * k, sdesc_sw128(vs + k * 32, 16, 1024), idesc_f16(128, D), (i > 0 || k > 0) ? 1u : 0u);
+            mma_commit(smem_u32(&M.o_done));
+            if (i + S::kWideStages < n)
+                load_page<D>(&tk, p, M.page[i + S::kWideStages], R.h, kb, smem_u32(&M.full[i + S::kWideStages]));
+        }
+    }
+    if (n > 0 && ok) ok = mbar_wait(smem_u32(&M.o_done), (n - 1) & 1, p.status, 307);
+    if (!__syncthreads_and(ok)) {
+        // the products issued end by themselves; so do the copies
+        drain(M, n);
+        return;
+    }
+    tc_fence_after();
+    M.sum[half][row] = l;
+    __syncthreads();
+    int place, head;
+    if (!R.at(row, place, head)) place = -1;
+    l += M.sum[1 - half][row];
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t at = R.h * p.part_rows + part + row;
+    const int64_t qi = place < 0 ? 0 : p.order[place];
+    if (place >= 0 && half == 0) {
+        if (part >= 0) p.part_ml[at] = make_float2(m, l);
+        else p.lse[(int64_t)head * p.R + qi] = out_lse(m, l);
+    }
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x) {
+        const int col = half * (D / 2) + 32 * x;
+        float v[32];
+        tmem_ld32(o_col + lanes + col, v);                      // whole warps only
+        tmem_wait_ld();
+        if (place < 0) continue;
+        if (part >= 0) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+                *reinterpret_cast<float4*>(p.part_o + at * D + col + j) =
+                    n ? make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8)
+                *reinterpret_cast<uint4*>(p.o + (qi * p.hq + head) * D + col + j) =
+                    n ? make_uint4(pack_bf16x2(v[j] * inv, v[j + 1] * inv), pack_bf16x2(v[j + 2] * inv, v[j + 3] * inv),
+                                   pack_bf16x2(v[j + 4] * inv, v[j + 5] * inv), pack_bf16x2(v[j + 6] * inv, v[j + 7] * inv))
+                      : make_uint4(0, 0, 0, 0);
+        }
+    }
+    tc_fence_before();
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Meta M;
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int item = blockIdx.x / p.hkv, h = blockIdx.x % p.hkv;
+    const int32_t* it = p.items + 6 * (int64_t)item;
+    const int e0 = it[0], e1 = it[1], part = it[4];
+    const Rows R = {it[2], (it[3] - it[2]) * p.gsub, p.gsub, p.n_sub, p.group, h};
+    const bool is_wide = R.rows > 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if ((int)threadIdx.x < e1 - e0) mbar_init(smem_u32(&M.full[threadIdx.x]), 1);
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&M.s_done), 1);
+        mbar_init(smem_u32(&M.o_done), 1);
+    }
+    fence_mbar_init();
+    if (is_wide && warp == kWarps - 1) tmem_alloc(smem_u32(&M.tmem), 256);
+    int4 entry = make_int4(0, 0, 0, 0);
+    if ((int)threadIdx.x < e1 - e0) entry = *reinterpret_cast<const int4*>(p.entries + 4 * (int64_t)(e0 + threadIdx.x));
+    grid_dep_wait();
+    grid_dep_launch();
+    // pages that hold tokens now, packed
+    int valid = 0;
+    float kf = 0.f, lv = 0.f;
+    if ((int)threadIdx.x < e1 - e0) {
+        const int64_t ph = (int64_t)entry.x * p.hkv + h;
+        kf = p.ks[ph] * p.scale_log2;
+        lv = (float)((int)(__float_as_uint(p.vs[ph]) >> 23) - 127);
+        valid = max(0, min(max(p.lens[entry.y], 0) - entry.z, entry.w));
+    }
+    const uint32_t has = __ballot_sync(0xffffffffu, valid > 0);
+    if (lane == 0 && warp < kDecodeMaxChunk / 32) M.count[warp] = __popc(has);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int n = 0, at = __popc(has & ((1u << lane) - 1u));
+    for (int w = 0; w < kDecodeMaxChunk / 32; ++w) {
+        if (w < warp) at += M.count[w];
+        n += M.count[w];
+    }
+    if (valid > 0) {
+        M.page[at] = entry.x;
+        M.valid[at] = valid;
+        M.kf[at] = kf;
+        M.lv[at] = lv;
+    }
+    __syncthreads();
+    if (is_wide) {
+        wide<D>(tk, p, M, ring, R, part, n);
+        __syncthreads();
+        if (warp == kWarps - 1) {
+            tc_fence_after();
+            tmem_dealloc(M.tmem, 256);
+        }
+    } else {
+        narrow<D>(tk, p, M, ring, reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw))), R, part, n);
     }
 }
 
@@ -452,7 +753,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
     uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (qi * p.hq + head) * D) + lane * (PL / 2);
 #pragma unroll
     for (int j = 0; j < PL / 2; ++j) dst[j] = pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
-    if (lane == 0) p.lse[(int64_t)head * p.R + qi] = l == 0.f ? -INFINITY : (ref - kLift + log2f(l)) * kLn2;
+    if (lane == 0) p.lse[(int64_t)head * p.R + qi] = out_lse(top, l);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

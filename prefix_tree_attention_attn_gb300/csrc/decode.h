@@ -12,8 +12,8 @@
 namespace treeattn {
 
 constexpr int kPage = TREE_DECODE_PAGE;
-constexpr int kDecodeRows = 64;          // query rows (query x head of the group) per work item at most
-constexpr int kDecodeMaxChunk = 256;     // pages per work item at most
+constexpr int kDecodeRows = 128;         // query rows (query x head of the group) per work item at most
+constexpr int kDecodeMaxChunk = 128;     // pages per work item at most
 
 // Device copy of the tables (one per device; pointers into one buffer).
 struct DeviceDecode {

@@ -22,8 +22,8 @@ namespace treeattn {
 namespace {
 
 constexpr int64_t kMaxCombine = (int64_t)1 << 27;
-// work items (over all kv-heads) that keep every SM busy to the end
-constexpr int64_t kTargetItems = 152 * 6;
+// CTAs of the attention that run at one time: two per SM
+constexpr int64_t kSlots = 152 * 2;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -148,9 +148,12 @@ int build(const int32_t* parent, const int32_t* seg_len, const int32_t* capacity
         for (int32_t v : run_nodes[k]) run_pages[k] += first[v + 1] - first[v];
         units += run_pages[k] * ceil_div((int64_t)(run_hi[k] - run_lo[k]) * P->n_sub, per_block);
     }
+    // Small trees: one wave of items.  From 16 pages an item on, up to four waves, so that
+    // the last items to finish are short.
+    const int64_t total = units * P->hkv;
+    const int64_t waves = std::min<int64_t>(4, std::max<int64_t>(1, total / (kSlots * 16)));
     P->chunk = opt_chunk ? opt_chunk
-                         : (int32_t)std::min<int64_t>(kDecodeMaxChunk / 2,
-                                                      std::max<int64_t>(4, ceil_div(units * P->hkv, kTargetItems)));
+                         : (int32_t)std::min<int64_t>(kDecodeMaxChunk, std::max<int64_t>(4, ceil_div(total, kSlots * waves)));
     const int32_t groups = P->live * P->n_sub;
     std::vector<int32_t> count(groups, 0);
     int64_t combine = 0, n_items = 0;
@@ -207,10 +210,7 @@ int build(const int32_t* parent, const int32_t* seg_len, const int32_t* capacity
     const int64_t ni = (int64_t)P->items.size() / 6;
     std::vector<int32_t> by(ni);
     for (int64_t i = 0; i < ni; ++i) by[i] = (int32_t)i;
-    auto cost = [&](int32_t i) {
-        const int32_t* it = &P->items[6 * (size_t)i];
-        return (int64_t)(it[1] - it[0]) * (16 + (it[3] - it[2]) * P->gsub);
-    };
+    auto cost = [&](int32_t i) { return P->items[6 * (size_t)i + 1] - P->items[6 * (size_t)i]; };
     std::stable_sort(by.begin(), by.end(), [&](int32_t a, int32_t b) { return cost(a) > cost(b); });
     std::vector<int32_t> sorted(P->items.size());
     for (int64_t i = 0; i < ni; ++i) std::memcpy(&sorted[6 * i], &P->items[6 * (size_t)by[i]], 6 * sizeof(int32_t));

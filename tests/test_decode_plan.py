@@ -19,7 +19,7 @@ def random_case(rng):
     pool = need + int(rng.integers(0, 5))
     pages = rng.permutation(pool)[:need]
     queries = [int(x) for x in rng.integers(-1, n, size=int(rng.integers(1, 12)))]
-    group = int(rng.choice([1, 2, 5, 8, 64, 65, 130]))
+    group = int(rng.choice([1, 2, 5, 8, 64, 65, 130, 200]))
     return t.parent, seg, cap, pages, pool, queries, group
 
 
@@ -27,7 +27,7 @@ def random_case(rng):
 def test_items_cover_every_path_once(lib, seed):
     rng = np.random.default_rng(seed)
     parent, seg, cap, pages, pool, queries, group = random_case(rng)
-    chunk = int(rng.choice([0, 1, 3, 256]))
+    chunk = int(rng.choice([0, 1, 3, 128]))
     fresh = rng.random(len(parent)) < 0.7
     p = DecodePlan(parent, seg, queries, 2 * group, 2, 64, capacity=cap, pages=pages, n_pages=pool, fresh=fresh,
                    chunk_pages=chunk)
@@ -36,7 +36,7 @@ def test_items_cover_every_path_once(lib, seed):
     live = [r for r, u in enumerate(queries) if u >= 0]
     assert sorted(x["query_order"]) == live
     sub, rows = info["n_sub"], info["rows_per_sub"]
-    assert rows <= 64 and (sub - 1) * rows < group <= sub * rows
+    assert rows <= 128 and (sub - 1) * rows < group <= sub * rows
     # a page entry names its node, its first token and the room behind it
     for page, node, at, room in x["entries"]:
         assert at % PAGE == 0 and 0 < room <= PAGE and room == min(PAGE, cap[node] - at)
@@ -45,7 +45,7 @@ def test_items_cover_every_path_once(lib, seed):
     part_rows = []
     for e0, e1, g0, g1, part, _ in x["items"]:
         assert 0 <= e0 < e1 <= info["n_entries"] and 0 <= g0 < g1 <= len(live) * sub
-        assert (g1 - g0) * rows <= 64 and (chunk == 0 or e1 - e0 <= chunk)
+        assert (g1 - g0) * rows <= 128 and (chunk == 0 or e1 - e0 <= chunk)
         for g in range(g0, g1):
             for e in range(e0, e1):
                 key = (g, int(x["entries"][e][0]))
@@ -95,9 +95,9 @@ def test_items_cover_every_path_once(lib, seed):
 def test_shared_prefix_is_one_run(lib):
     """A prompt under 8 siblings is in one item per chunk, not one per sibling; a chain
     that one query reads is one run."""
-    p = DecodePlan([-1] + [0] * 8, [256] + [64] * 8, range(1, 9), 8, 1, 128, chunk_pages=256)
+    p = DecodePlan([-1] + [0] * 8, [256] + [64] * 8, range(1, 9), 8, 1, 128, chunk_pages=128)
     assert p.info["n_items"] == 1 + 8 and p.info["n_entries"] == 4 + 8
-    c = DecodePlan([-1, 0, 1, 2], [64, 64, 64, 10], [3], 8, 1, 128, chunk_pages=256)
+    c = DecodePlan([-1, 0, 1, 2], [64, 64, 64, 10], [3], 8, 1, 128, chunk_pages=128)
     assert c.info["n_items"] == 1 and c.info["n_part_rows"] == 0 and c.workspace_bytes == 0
 
 
@@ -131,7 +131,7 @@ def test_plan_refusals(lib):
     assert status(lib, **ok, pages=[0, 1, -1]) == -1
     assert status(lib, **ok, n_pages=2) == -1                               # three are needed
     assert status(lib, **ok, n_pages=3) == 0
-    for chunk in (-1, 257):
+    for chunk in (-1, 129):
         assert status(lib, **ok, chunk=chunk) == -1
     for hq, hkv, d in ((3, 2, 64), (0, 1, 64), (2, 0, 64), (2, 1, 96), (2, 1, 256)):
         assert status(lib, **ok, hq=hq, hkv=hkv, d=d) == -4

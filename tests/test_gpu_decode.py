@@ -6,9 +6,9 @@ A = sum_j p_j |v_j| and X = max_j scale * sum_f |q_f k_jf|:
   * bf16 output: half a step, 2^-8 relative to the value (2^-9 plus the next terms);
   * P rounded to f16: 2^-11 of A (half a step of 11 bits);
   * P below f16's normal numbers: the weights are lifted so that the largest
-    p_j s_j (s_j the page's scale, the weight of j's codes) is 2^14, f16's subnormals are
-    multiples of 2^-24, so rounding them moves a weight by at most 2^-25, that is 2^-39 of
-    the largest; times the codes: 2^-39 * max_j(p_j s_j) * sum_j |v_j / s_j|;
+    p_j s_j (s_j the page's scale, the weight of j's codes) is at least 2^12, f16's
+    subnormals are multiples of 2^-24, so rounding them moves a weight by at most 2^-25,
+    that is 2^-37 of the largest; times the codes: 2^-37 * max_j(p_j s_j) * sum_j |v_j / s_j|;
   * the query row in f16 after a power of two: exact but for features below 2^-14 of
     the row's largest, which lose 2^-25 of it: 2^-25 * d * X' inside the fp32 bound;
   * logits in fp32: products are exact, d / 16 accumulations that may truncate, and the
@@ -82,7 +82,7 @@ def check(plan, cache, ref, parent, lens, cap, pages, queries, q, scale, o, lse)
     tol = (x + 2.0 ** -20 * (1 + np.abs(np.where(fine, wl, 0))))[:, live]
     assert (err <= tol).all(), f"LSE: {(err / tol).max():.2f} of the bound"
     err = np.abs(go - wo)[live]
-    tol = (2.0 ** -8 * np.abs(wo) + (2.0 ** -11 + 2.0 ** -13 + 4 * x.T[:, :, None]) * mass + 2.0 ** -39 * coarse)[live]
+    tol = (2.0 ** -8 * np.abs(wo) + (2.0 ** -11 + 2.0 ** -13 + 4 * x.T[:, :, None]) * mass + 2.0 ** -37 * coarse)[live]
     assert (err <= tol + 1e-30).all(), f"O: {(err / (tol + 1e-30)).max():.2f} of the bound"
 
 
@@ -111,7 +111,7 @@ TREES = {
 }
 
 
-@pytest.mark.parametrize("heads", [(2, 2, 64), (8, 1, 128), (14, 2, 128), (3, 3, 128), (67, 1, 64), (130, 1, 128)])
+@pytest.mark.parametrize("heads", [(2, 2, 64), (8, 1, 128), (14, 2, 128), (3, 3, 128), (67, 1, 64), (130, 1, 128), (20, 2, 64)])
 @pytest.mark.parametrize("name", list(TREES))
 def test_write_and_decode(lib, cuda_device, name, heads):
     parent, seg, queries = TREES[name]
@@ -129,7 +129,7 @@ def test_write_and_decode(lib, cuda_device, name, heads):
     check(plan, cache, ref, parent, seg, seg, pages, queries, q, d ** -0.5, o, lse)
 
 
-@pytest.mark.parametrize("chunk", [0, 1, 5, 256])
+@pytest.mark.parametrize("chunk", [0, 1, 5, 128])
 @pytest.mark.parametrize("seed", range(6))
 def test_random_trees(lib, cuda_device, seed, chunk):
     """Random forests, inner and repeated queries, spare room, lengths of the moment
@@ -343,7 +343,7 @@ def test_many_pages_in_flight(lib, cuda_device):
     rng = np.random.default_rng(13)
     parent, seg = [-1] + [0] * 24, [64 * 150 + 5] + [64 * int(x) + 9 for x in rng.integers(5, 90, 24)]
     for hq, queries in ((4, [3]), (8, [1, 2, 3, 4, 5]), (8, list(range(1, 25)))):
-        plan, cache, ref, pages = build(rng, parent, seg, queries, hq, 2, 128, cuda_device, chunk=151)
+        plan, cache, ref, pages = build(rng, parent, seg, queries, hq, 2, 128, cuda_device, chunk=128)
         q, ln = rows(rng, len(queries), hq, 128, cuda_device), plan.lens()
         outs = [TD.tree_decode(plan, cache, ln, q, 0.09) for _ in range(150)]
         assert device_status() == 0
