@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -98,12 +99,15 @@ int make_byte_map(CUtensorMap* m, const void* base, int64_t rows, int box_rows) 
 }
 
 int current_device(int* dev) {
+    static std::atomic<bool> usable[kMaxDevices];   // a device's capability does not change: asked once
     if (cudaGetDevice(dev) != cudaSuccess) return TREE_ATTN_ERR_NO_DEVICE;
     if (*dev < 0 || *dev >= kMaxDevices) return TREE_ATTN_ERR_NO_DEVICE;
+    if (usable[*dev].load(std::memory_order_relaxed)) return TREE_ATTN_OK;
     int major = 0, minor = 0;
     cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, *dev);
     cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, *dev);
     if (major != 10 || minor != 3) return TREE_ATTN_ERR_NO_DEVICE;
+    usable[*dev].store(true, std::memory_order_relaxed);
     return TREE_ATTN_OK;
 }
 

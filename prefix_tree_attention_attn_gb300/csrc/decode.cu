@@ -38,7 +38,8 @@
 // pages would cost a leaf's instructions once per 8 rows.  The codes are expanded
 // once per page to f16 tiles in shared memory and the products are tcgen05.mma with
 // M = 128 rows, accumulators in TMEM, P written back over S as the second product's
-// operand.  Expansion of a page's V overlaps S, of the next page's K overlaps P V.
+// operand.  Four warps expand and issue, four do the softmax (one row per thread), so
+// the softmax of a page overlaps the expansion and the scores of the next.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -143,10 +144,11 @@ struct Shape {
     static constexpr int kStages = D == 128 ? 6 : 12;
     static constexpr int kPitch = D + 4;
     static_assert(kWarps * 8 * kPitch * 4 <= kStages * kStage, "the join reuses the ring");
-    // wide: two stages, then the f16 tiles of Q, K, V
-    static constexpr int kWideStages = 2;
-    static constexpr int kQ = kWideStages * kStage, kK = kQ + 128 * D * 2, kV = kK + kPage * D * 2;
-    static constexpr int kWide = kV + kPage * D * 2;
+    // wide: f16 tiles of Q, K (two) and V, then a ring of K or V halves
+    static constexpr int kWideStages = 3;
+    static constexpr int kTile = kPage * D * 2;
+    static constexpr int kQ = 0, kK = kQ + 128 * D * 2, kV = kK + 2 * kTile, kCodes = kV + kTile;
+    static constexpr int kWide = kCodes + kWideStages * kHalf;
     static constexpr int kRing = kStages * kStage > kWide ? kStages * kStage : kWide;
     static constexpr int kSmem = kRing + 1024;       // + alignment slack
 };
@@ -157,7 +159,10 @@ struct Meta {
     float kf[kDecodeMaxChunk];        // k_scale * softmax_scale * log2(e)
     float lv[kDecodeMaxChunk];        // log2(v_scale)
     uint64_t full[kDecodeMaxChunk];   // one per page, used once: pages land out of order
-    uint64_t s_done, o_done;          // wide: a tensor product of the page has finished
+    uint64_t full_v[kDecodeMaxChunk]; // wide: V apart from K
+    // wide: the scores of a page are there, its P is in TMEM (one barrier per S buffer: with
+    // one for both, a wait for page i could meet the parity of page i + 2), P V has finished
+    uint64_t s_done[2], p_full[2], o_done;
     int32_t count[kDecodeMaxChunk / 32];
     uint32_t tmem;
     union {
@@ -165,7 +170,7 @@ struct Meta {
             float m[kWarps][8], l[kWarps][8];        // narrow: per warp and row
         };
         struct {
-            float top[2][128], sum[2][128], qf[128];   // wide: per half of the keys and row
+            float top[128], sum[128], qf[128];       // wide: per row
         };
     };
 };
@@ -182,20 +187,28 @@ struct Rows {
 };
 
 template <int D>
-__device__ __forceinline__ void load_page(const CUtensorMap* tk, const DecodeParams& p, int page, int h, uint32_t dst,
-                                          uint32_t bar) {
-    using S = Shape<D>;
+__device__ __forceinline__ void load_k(const CUtensorMap* tk, const DecodeParams& p, int page, int h, uint32_t dst,
+                                       uint32_t bar) {
     const int64_t ph = (int64_t)page * p.hkv + h;
-    mbar_expect_tx(bar, S::kStage);
     if constexpr (D == 128) {
         asm volatile(
             "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
             " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tk)), "r"(0),
             "r"((int)(ph * kPage)), "r"(bar) : "memory");
     } else {
-        bulk_load(dst, p.k8 + ph * S::kHalf, S::kHalf, bar);
+        bulk_load(dst, p.k8 + ph * Shape<D>::kHalf, Shape<D>::kHalf, bar);
     }
-    bulk_load(dst + S::kHalf, p.v8 + ph * S::kHalf, S::kHalf, bar);
+}
+template <int D>
+__device__ __forceinline__ void load_v(const DecodeParams& p, int page, int h, uint32_t dst, uint32_t bar) {
+    bulk_load(dst, p.v8 + ((int64_t)page * p.hkv + h) * Shape<D>::kHalf, Shape<D>::kHalf, bar);
+}
+template <int D>
+__device__ __forceinline__ void load_page(const CUtensorMap* tk, const DecodeParams& p, int page, int h, uint32_t dst,
+                                          uint32_t bar) {
+    mbar_expect_tx(bar, Shape<D>::kStage);
+    load_k<D>(tk, p, page, h, dst, bar);
+    load_v<D>(p, page, h, dst + Shape<D>::kHalf, bar);
 }
 
 // byte address of 16 codes c of key r in a K stage (swizzled by the tensor map for d = 128)
@@ -213,7 +226,7 @@ __device__ __forceinline__ uint32_t keep_bytes(int k, int valid) {
 // barriers complete) before shared memory is given up.
 __device__ __noinline__ void drain(Meta& M, int n) {
     for (int i = threadIdx.x; i < n; i += kThreads)
-        for (int k = 0; k < 4096 && !mbar_try_wait(smem_u32(&M.full[i]), 0); ++k) {}
+        for (int k = 0; k < 4096 && !(mbar_try_wait(smem_u32(&M.full[i]), 0) && mbar_try_wait(smem_u32(&M.full_v[i]), 0)); ++k) {}
     __syncthreads();
 }
 
@@ -449,14 +462,24 @@ template <int D>
 __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint32_t ring, const Rows& R, int part, int n) {
     using S = Shape<D>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = 32 * (warp & 3) + lane, half = warp >> 2;   // TMEM lane; keys 32 half ..
-    const uint32_t qs = ring + S::kQ, ks = ring + S::kK, vs = ring + S::kV;
+    const int row = 32 * (warp & 3) + lane;                     // TMEM lane
+    const uint32_t qs = ring + S::kQ, vs = ring + S::kV;
     const uint32_t tmem = M.tmem;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t o_col = tmem + 128;                          // S tiles at columns 0 and 64, O from 128
-    if (threadIdx.x == 0)
-        for (int i = 0; i < min(n, S::kWideStages); ++i)
-            load_page<D>(&tk, p, M.page[i], R.h, ring + i * S::kStage, smem_u32(&M.full[i]));
+    // Halves in the order they are expanded: K0, K1, V0, K2, V1, ..., V(n-1).
+    auto load_half = [&](int x) {
+        if (x >= 2 * n) return;
+        const bool is_v = x == 2 * n - 1 || (x >= 2 && !(x & 1));
+        const int i = x == 2 * n - 1 ? n - 1 : is_v ? x / 2 - 1 : (x + 1) / 2;
+        const uint32_t dst = ring + S::kCodes + (x % S::kWideStages) * S::kHalf;
+        const uint32_t bar = smem_u32(is_v ? &M.full_v[i] : &M.full[i]);
+        mbar_expect_tx(bar, S::kHalf);
+        if (is_v) load_v<D>(p, M.page[i], R.h, dst, bar);
+        else load_k<D>(&tk, p, M.page[i], R.h, dst, bar);
+    };
+    if (threadIdx.x == 128)
+        for (int x = 0; x < S::kWideStages; ++x) load_half(x);
     // Q to f16, two threads per row
     {
         const int r = threadIdx.x >> 1, hf = threadIdx.x & 1;
@@ -483,136 +506,184 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint
                          scaled_f16(w[i].z, down), scaled_f16(w[i].w, down));
         }
     }
+    fence_proxy_async_smem();
+    __syncthreads();
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int i = 0; i < n; ++i) {
-        const int st = i % S::kWideStages;
-        const uint32_t kb = ring + st * S::kStage, vb = kb + S::kHalf, s_col = tmem + 64 * (i & 1);
-        const int valid = M.valid[i];
-        ok = ok && mbar_wait(smem_u32(&M.full[i]), 0, p.status, 304);
-        // K to f16.  Eight lanes take four chunks of two rows that differ in bits 0 and 2, so
-        // that loads (swizzled by the row's 3 bits over 8 chunks) and stores both spread over
-        // all banks.
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x) {
-            uint32_t w[4];
+    if (warp >= 4) {
+        // ------------------------ expansion and products ------------------------
+        const int ct = threadIdx.x - 128;
+        int x = 0;                                              // half at hand
+        bool mine = true;                                       // this thread's waits outside the common ones
+        // The four warps run in step: after a barrier the half's slot is free and its tile
+        // is complete.
+        auto done_half = [&](bool good) {
+            fence_proxy_async_smem();
+            good = named_bar_and(1, 128, good && mine);         // the same for all 128 threads
+            if (good && ct == 0) load_half(x + S::kWideStages);
+            ++x;
+            return good;
+        };
+        auto expand_k = [&](int i) {
+            bool good = mbar_wait(smem_u32(&M.full[i]), 0, p.status, 304);
+            // the tile's previous reader was S of page i - 2
+            if (i > 1) good = mbar_wait(smem_u32(&M.s_done[i & 1]), (i / 2 - 1) & 1, p.status, 305) && good;
+            const uint32_t from = ring + S::kCodes + (x % S::kWideStages) * S::kHalf, ks = ring + S::kK + (i & 1) * S::kTile;
             if constexpr (D == 128) {
-                const int c = 4 * x + (threadIdx.x & 3), q = threadIdx.x >> 2;
-                const int r = (q & ~5) | (((q & 1) * 5) ^ (q & 4));
-                lds128(kb + sw128_offset(r, c), w);
-                expand16(w, ks + x * 8192, r, 2 * (c & 3));
+                // Eight lanes take four chunks of two rows that differ in bits 0 and 2, so that
+                // loads (swizzled by the row's 3 bits over 8 chunks) and stores both spread over
+                // all banks.
+                const int q = ct >> 2, r = (q & ~5) | (((q & 1) * 5) ^ (q & 4));
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    uint32_t w[4];
+                    const int rr = r + 32 * (y >> 1);
+                    lds128(from + sw128_offset(rr, 4 * (y & 1) + (ct & 3)), w);
+                    expand16(w, ks + (y & 1) * 8192, rr, 2 * (ct & 3));
+                }
             } else {
-                lds128(kb + threadIdx.x * 16, w);
-                expand16(w, ks, threadIdx.x >> 2, 2 * (threadIdx.x & 3));
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    uint32_t w[4];
+                    const int at = ct + 128 * y;
+                    lds128(from + at * 16, w);
+                    expand16(w, ks, at >> 2, 2 * (at & 3));
+                }
+            }
+            good = done_half(good);
+            if (good && ct == 0) {
+                // S over the buffer that held P of page i - 2, which P V has read: products
+                // of one thread run in order
+                const uint32_t s_col = tmem + 64 * (i & 1);
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    mma_bf16_ss(s_col, sdesc_sw128(qs + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024),
+                                sdesc_sw128(ks + (k >> 2) * 8192 + (k & 3) * 32, 16, 1024), idesc_f16(128, kPage), k > 0);
+                mma_commit(smem_u32(&M.s_done[i & 1]));
+            }
+            return good;
+        };
+        ok = n > 0 ? expand_k(0) : true;
+        for (int i = 0; i < n && ok; ++i) {
+            if (i + 1 < n) ok = expand_k(i + 1);
+            if (!ok) break;
+            const int valid = M.valid[i];
+            ok = mbar_wait(smem_u32(&M.full_v[i]), 0, p.status, 306);
+            if (i > 0) ok = mbar_wait(smem_u32(&M.o_done), (i - 1) & 1, p.status, 307) && ok;   // P V has read the tile
+            const uint32_t from = ring + S::kCodes + (x % S::kWideStages) * S::kHalf;
+#pragma unroll
+            for (int y = 0; y < D / 32; ++y) {
+                const int at = ct + 128 * y;
+                uint32_t w[4];
+                lds128(from + at * 16, w);
+                if (valid < kPage) {   // what is behind the last token may be anything, NaN included
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] &= keep_bytes(16 * (at & 3) + 4 * j, valid);
+                }
+                expand16(w, vs, at >> 2, 2 * (at & 3));
+            }
+            ok = done_half(ok);
+            if (ok && ct == 0) {
+                mine = mbar_wait(smem_u32(&M.p_full[i & 1]), (i / 2) & 1, p.status, 308);
+                if (mine) {
+                    const uint32_t s_col = tmem + 64 * (i & 1);
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < kPage / 16; ++k)
+                        mma_bf16_ts(o_col, s_col + 8 * k, sdesc_sw128(vs + k * 32, 16, 1024), idesc_f16(128, D),
+                                    (i > 0 || k > 0) ? 1u : 0u);
+                    mma_commit(smem_u32(&M.o_done));
+                }
             }
         }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        ok = __syncthreads_and(ok);
-        if (!ok) break;
-        if (threadIdx.x == 0) {
+        ok = ok && mine;
+    } else {
+        // ------------------------------- softmax ---------------------------------
+        const float qf = M.qf[row];
+        for (int i = 0; i < n; ++i) {
+            const uint32_t s_col = tmem + 64 * (i & 1) + lanes;
+            const int valid = M.valid[i];
+            const float lv = M.lv[i], f = M.kf[i] * qf;
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&M.s_done[i & 1]), (i / 2) & 1, p.status, 309));
+            if (!ok) break;
             tc_fence_after();
+            float c[64];
+            tmem_ld32(s_col, *reinterpret_cast<float(*)[32]>(&c[0]));
+            tmem_ld32(s_col + 32, *reinterpret_cast<float(*)[32]>(&c[32]));
+            tmem_wait_ld();
+            const uint64_t f2 = f32x2(f, f), lv2 = f32x2(lv, lv);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-                mma_bf16_ss(s_col, sdesc_sw128(qs + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024),
-                            sdesc_sw128(ks + (k >> 2) * 8192 + (k & 3) * 32, 16, 1024), idesc_f16(128, kPage), k > 0);
-            mma_commit(smem_u32(&M.s_done));
-        }
-        // V to f16, once the previous page's P V has read the tile
-        if (i > 0) ok = mbar_wait(smem_u32(&M.o_done), (i - 1) & 1, p.status, 305);
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x) {
-            const int at = threadIdx.x + x * kThreads;
-            uint32_t w[4];
-            lds128(vb + at * 16, w);
+            for (int j = 0; j < 64; j += 2) f32x2_split(fma_f32x2(f32x2(c[j], c[j + 1]), f2, lv2), c[j], c[j + 1]);
             if (valid < kPage) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] &= keep_bytes(16 * (at & 3) + 4 * j, valid);
+                for (int j = 0; j < 64; ++j)
+                    if (j >= valid) c[j] = -INFINITY;
             }
-            expand16(w, vs, at >> 2, 2 * (at & 3));
-        }
-        fence_proxy_async_smem();
-        // softmax over this thread's 32 keys of its row
-        ok = mbar_wait(smem_u32(&M.s_done), i & 1, p.status, 306) && ok;
-        tc_fence_after();
-        const float lv = M.lv[i], f = M.kf[i] * M.qf[row];
-        float c[32];
-        tmem_ld32(s_col + lanes + 32 * half, c);
-        tmem_wait_ld();
-        float top = -INFINITY;
-        const uint64_t f2 = f32x2(f, f), lv2 = f32x2(lv, lv);
+            float top = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) f32x2_split(fma_f32x2(f32x2(c[j], c[j + 1]), f2, lv2), c[j], c[j + 1]);
-        if (valid < kPage) {
+            for (int j = 0; j < 64; j += 2) top = fmax3(top, c[j], c[j + 1]);
+            const bool up = top > m + kSlack;
+            if (__any_sync(0xffffffffu, up)) {
+                const float a = up ? fast_exp2(m - top) : 1.f;
+                if (i > 0) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&M.o_done), (i - 1) & 1, p.status, 310));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int x = 0; x < D / 16; ++x) {
+                        float v[16];
+                        tmem_ld16(o_col + lanes + 16 * x, v);
+                        tmem_wait_ld();
+                        uint32_t w[16];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (32 * half + j >= valid) c[j] = -INFINITY;
-        }
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) top = fmax3(top, c[j], c[j + 1]);
-        // everyone has read its part of S (P goes over it), and whether a row has to move its
-        // reference
-        tc_fence_before();
-        if (__syncthreads_or(top > m + kSlack)) {
-            M.top[half][row] = top;
-            __syncthreads();
-            const float both = fmaxf(top, M.top[1 - half][row]);
-            const bool up = both > m + kSlack;
-            const float a = up ? fast_exp2(m - both) : 1.f;
-            tc_fence_after();
-            if (i > 0 && __any_sync(0xffffffffu, up)) {
-#pragma unroll
-                for (int x = 0; x < D / 64; ++x) {
-                    float v[32];
-                    tmem_ld32(o_col + lanes + half * (D / 2) + 32 * x, v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] *= a;
-                    tmem_st32(o_col + lanes + half * (D / 2) + 32 * x, v);
+                        for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(v[j] * a);
+                        tmem_st16(o_col + lanes + 16 * x, w);
+                    }
+                    tmem_wait_st();
                 }
-                tmem_wait_st();
+                l *= a;
+                m = up ? top : m;
             }
-            l *= a;
-            m = up ? both : m;
-        }
-        tc_fence_after();
-        const float base = m == -INFINITY ? 0.f : m - kLift;
-        uint32_t pw[16];
-        float sum = 0.f;
+            const float base = m == -INFINITY ? 0.f : m - kLift;
+            uint64_t sum = f32x2(0.f, 0.f);
+            const uint64_t one2 = f32x2(1.f, 1.f), nb2 = f32x2(-base, -base);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float a = fast_exp2(c[2 * j] - base), b = fast_exp2(c[2 * j + 1] - base);
-            sum += a + b;
-            pw[j] = pack_f16(a, b);
-        }
-        l += sum * fast_exp2(-lv);
-        tmem_st16(s_col + lanes + 16 * half, pw);
-        tmem_wait_st();
-        tc_fence_before();
-        ok = __syncthreads_and(ok);
-        if (!ok) break;
-        if (threadIdx.x == 0) {
-            tc_fence_after();
+            for (int x = 0; x < 2; ++x) {
+                uint32_t pw[16];
 #pragma unroll
-            for (int k = 0; k < kPage / 16; ++k)
-                mma_bf16_ts(o_col, s_col + 8 * k, sdesc_sw128(vs + k * 32, 16, 1024), idesc_f16(128, D), (i > 0 || k > 0) ? 1u : 0u);
-            mma_commit(smem_u32(&M.o_done));
-            if (i + S::kWideStages < n)
-                load_page<D>(&tk, p, M.page[i + S::kWideStages], R.h, kb, smem_u32(&M.full[i + S::kWideStages]));
+                for (int j = 0; j < 16; ++j) {
+                    float a, b;
+                    f32x2_split(fma_f32x2(f32x2(c[32 * x + 2 * j], c[32 * x + 2 * j + 1]), one2, nb2), a, b);
+                    a = fast_exp2(a);
+                    b = fast_exp2(b);
+                    sum = add_f32x2(sum, f32x2(a, b));
+                    pw[j] = pack_f16(a, b);
+                }
+                tmem_st16(s_col + 16 * x, pw);
+            }
+            float sa, sb;
+            f32x2_split(sum, sa, sb);
+            l += (sa + sb) * fast_exp2(-lv);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(smem_u32(&M.p_full[i & 1]));
         }
+        M.top[row] = m;
+        M.sum[row] = l;
+        if (n > 0 && ok) ok = mbar_wait(smem_u32(&M.o_done), (n - 1) & 1, p.status, 311);
     }
-    if (n > 0 && ok) ok = mbar_wait(smem_u32(&M.o_done), (n - 1) & 1, p.status, 307);
     if (!__syncthreads_and(ok)) {
         // the products issued end by themselves; so do the copies
         drain(M, n);
         return;
     }
     tc_fence_after();
-    M.sum[half][row] = l;
-    __syncthreads();
+    const int half = warp >> 2;                                 // columns D / 2 * half ..
+    m = M.top[row];
+    l = M.sum[row];
     int place, head;
     if (!R.at(row, place, head)) place = -1;
-    l += M.sum[1 - half][row];
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int64_t at = R.h * p.part_rows + part + row;
     const int64_t qi = place < 0 ? 0 : p.order[place];
@@ -656,9 +727,15 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     const bool is_wide = R.rows > 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    if ((int)threadIdx.x < e1 - e0) mbar_init(smem_u32(&M.full[threadIdx.x]), 1);
+    if ((int)threadIdx.x < e1 - e0) {
+        mbar_init(smem_u32(&M.full[threadIdx.x]), 1);
+        if (is_wide) mbar_init(smem_u32(&M.full_v[threadIdx.x]), 1);
+    }
     if (threadIdx.x == 0) {
-        mbar_init(smem_u32(&M.s_done), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&M.s_done[i]), 1);
+            mbar_init(smem_u32(&M.p_full[i]), 128);
+        }
         mbar_init(smem_u32(&M.o_done), 1);
     }
     fence_mbar_init();

@@ -19,6 +19,7 @@ import ctypes as C
 from typing import Dict, Optional, Sequence
 
 import numpy as np
+import torch
 
 from . import _i32, _ptr_i32
 from . import _binding as B
@@ -74,7 +75,6 @@ class DecodePlan:
 
     def lens(self, device=None):
         """The nodes' lengths at plan time as the device array the calls read."""
-        import torch
         return torch.from_numpy(self.seg_len.copy()).to(device or torch.device("cuda", torch.cuda.current_device()))
 
     def export(self) -> Dict[str, np.ndarray]:
@@ -109,7 +109,6 @@ class TreeCache:
     float8_e4m3fn, ``k_scale`` / ``v_scale`` [n_pages, hkv] fp32 powers of two."""
 
     def __init__(self, k, v, k_scale, v_scale):
-        import torch
         P, hkv, page, d = k.shape
         if page != PAGE:
             raise ValueError(f"k: pages of {PAGE} tokens expected, got shape {tuple(k.shape)}")
@@ -128,7 +127,6 @@ class TreeCache:
 
     @classmethod
     def empty(cls, n_pages: int, hkv: int, d: int, device=None) -> "TreeCache":
-        import torch
         dev = device or torch.device("cuda", torch.cuda.current_device())
         code = {"dtype": torch.float8_e4m3fn, "device": dev}
         real = {"dtype": torch.float32, "device": dev}
@@ -136,25 +134,31 @@ class TreeCache:
                    torch.empty((n_pages, hkv), **real), torch.empty((n_pages, hkv), **real))
 
 
+# The calls below run once per token and layer: their checks read attributes only.
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
 def _check_cache(plan: DecodePlan, cache: TreeCache) -> int:
     """The call's device (the cache's, which must be the current one)."""
-    import torch
     if cache.n_pages < plan.n_pages or cache.hkv != plan.hkv or cache.d != plan.d:
         raise ValueError(f"cache: [{cache.n_pages}, {cache.hkv}, {PAGE}, {cache.d}] does not fit the plan's "
                          f"{plan.n_pages} pages of {plan.hkv} kv-heads of {plan.d}")
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     if cache.device.index != dev:
         raise ValueError(f"cache: on {cache.device}, the current device is cuda:{dev}")
     return dev
 
 
+def _expected(x, name: str, dtype, shape, dev: int, what: str = "contiguous ") -> ValueError:
+    return ValueError(f"{name}: expected {what}cuda:{dev} {dtype} {tuple(shape)}, got {x.device} {x.dtype} "
+                      f"{tuple(x.shape)} with strides {x.stride()}")
+
+
 def _check_rows(x, name: str, rows: int, heads: int, d: int, dev: int) -> int:
     """Row stride of a bf16 [rows, heads, d] tensor whose rows are contiguous."""
-    import torch
-    if not x.is_cuda or x.dtype != torch.bfloat16 or x.shape != (rows, heads, d) or x.get_device() != dev:
-        raise ValueError(f"{name}: expected cuda:{dev} {torch.bfloat16} {(rows, heads, d)}, got "
-                         f"{x.device} {x.dtype} {tuple(x.shape)}")
-    if rows == 0:
+    if x.dtype is not torch.bfloat16 or x.shape != (rows, heads, d) or x.get_device() != dev:   # -1 on the CPU
+        raise _expected(x, name, torch.bfloat16, (rows, heads, d), dev, "")
+    if x.is_contiguous():
         return heads * d
     s = x.stride()
     if s[2] != 1 or (s[1] != d and heads > 1):
@@ -166,17 +170,15 @@ def _check_rows(x, name: str, rows: int, heads: int, d: int, dev: int) -> int:
     return s[0]
 
 
-def _check_vec(x, name: str, n: int, dtype, dev: int) -> None:
-    if not x.is_cuda or x.dtype != dtype or x.shape != (n,) or not x.is_contiguous() or x.get_device() != dev:
-        raise ValueError(f"{name}: expected contiguous cuda:{dev} {dtype} ({n},), got {x.device} {x.dtype} "
-                         f"{tuple(x.shape)}")
+def _check_dense(x, name: str, shape, dtype, dev: int) -> None:
+    if x.dtype is not dtype or x.shape != shape or x.get_device() != dev or not x.is_contiguous():
+        raise _expected(x, name, dtype, shape, dev)
 
 
-def _stream_of(stream, *owned):
+def _stream_of(stream, dev: int, *owned):
     """The stream's handle; tensors this call allocated are kept until it is done with them."""
-    import torch
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(dev)
     if stream != torch.cuda.current_stream():
         for t in owned:
             if t is not None:
@@ -189,8 +191,8 @@ def tree_cache_write(plan: DecodePlan, cache: TreeCache, k, v, stream=None) -> N
     order (``tree_attn_cache_write``)."""
     dev = _check_cache(plan, cache)
     n = plan.info["n_fresh_tokens"]
-    ks, vs = (_check_rows(x, nm, n, plan.hkv, plan.d, dev) for nm, x in (("k", k), ("v", v)))
-    st = plan._lib.tree_attn_cache_write(plan._h, k.data_ptr(), v.data_ptr(), ks, vs, *cache._ptrs, _stream_of(stream))
+    ks, vs = _check_rows(k, "k", n, plan.hkv, plan.d, dev), _check_rows(v, "v", n, plan.hkv, plan.d, dev)
+    st = plan._lib.tree_attn_cache_write(plan._h, k.data_ptr(), v.data_ptr(), ks, vs, *cache._ptrs, _stream_of(stream, dev))
     if st:
         B.check(st, "tree_attn_cache_write")
 
@@ -199,14 +201,15 @@ def tree_cache_append(plan: DecodePlan, cache: TreeCache, lens, k, v, lens_out=N
     """Append one token per query to its node: k, v [R, hkv, d] bf16.  Returns the
     lengths with the new tokens: ``lens_out``, by default ``lens`` itself
     (``tree_attn_cache_append``)."""
-    import torch
     dev = _check_cache(plan, cache)
     lens_out = lens if lens_out is None else lens_out
-    _check_vec(lens, "lens", plan.n_nodes, torch.int32, dev)
-    _check_vec(lens_out, "lens_out", plan.n_nodes, torch.int32, dev)
-    ks, vs = (_check_rows(x, nm, plan.n_queries, plan.hkv, plan.d, dev) for nm, x in (("k", k), ("v", v)))
+    _check_dense(lens, "lens", (plan.n_nodes,), torch.int32, dev)
+    if lens_out is not lens:
+        _check_dense(lens_out, "lens_out", (plan.n_nodes,), torch.int32, dev)
+    ks = _check_rows(k, "k", plan.n_queries, plan.hkv, plan.d, dev)
+    vs = _check_rows(v, "v", plan.n_queries, plan.hkv, plan.d, dev)
     st = plan._lib.tree_attn_cache_append(plan._h, lens.data_ptr(), lens_out.data_ptr(), k.data_ptr(), v.data_ptr(), ks,
-                                          vs, *cache._ptrs, _stream_of(stream))
+                                          vs, *cache._ptrs, _stream_of(stream, dev))
     if st:
         B.check(st, "tree_attn_cache_append")
     return lens_out
@@ -217,26 +220,26 @@ def tree_decode(plan: DecodePlan, cache: TreeCache, lens, q, softmax_scale: floa
     """O [R, hq, d] bf16 and LSE [hq, R] fp32 of one new token per query over the
     tokens of its node and the node's ancestors (``tree_attn_decode``).  Rows of
     padding queries are left as they were: pass ``o`` and ``lse`` to keep them."""
-    import torch
     dev = _check_cache(plan, cache)
     R, hq, d = plan.n_queries, plan.hq, plan.d
-    _check_vec(lens, "lens", plan.n_nodes, torch.int32, dev)
+    _check_dense(lens, "lens", (plan.n_nodes,), torch.int32, dev)
     qs = _check_rows(q, "q", R, hq, d, dev)
-    o = torch.empty((R, hq, d), dtype=torch.bfloat16, device=q.device) if o is None else o
-    lse = torch.empty((hq, R), dtype=torch.float32, device=q.device) if lse is None else lse
-    for name, x, shape, dtype in (("o", o, (R, hq, d), torch.bfloat16), ("lse", lse, (hq, R), torch.float32)):
-        if not x.is_cuda or x.dtype != dtype or x.shape != shape or not x.is_contiguous() or x.get_device() != dev:
-            raise ValueError(f"{name}: expected contiguous cuda:{dev} {dtype} {shape}, got {x.device} {x.dtype} "
-                             f"{tuple(x.shape)}")
+    if o is None:
+        o = torch.empty((R, hq, d), dtype=torch.bfloat16, device=q.device)
+    else:
+        _check_dense(o, "o", (R, hq, d), torch.bfloat16, dev)
+    if lse is None:
+        lse = torch.empty((hq, R), dtype=torch.float32, device=q.device)
+    else:
+        _check_dense(lse, "lse", (hq, R), torch.float32, dev)
     own = None
     if workspace is None:
         workspace = own = torch.empty(max(plan.workspace_bytes, 1), dtype=torch.uint8, device=q.device)
-    elif not workspace.is_cuda or workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
-            workspace.get_device() != dev:
+    elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected contiguous cuda:{dev} uint8, got {workspace.device} {workspace.dtype}")
     st = plan._lib.tree_attn_decode(plan._h, lens.data_ptr(), q.data_ptr(), qs, *cache._ptrs, o.data_ptr(),
                                     lse.data_ptr(), softmax_scale, workspace.data_ptr(), workspace.numel(),
-                                    _stream_of(stream, own, o, lse))
+                                    _stream_of(stream, dev, own, o, lse))
     if st:
         B.check(st, "tree_attn_decode")
     return o, lse
