@@ -77,7 +77,8 @@ typedef struct {
  * NULL.  A "row group" is one part of one query's heads: row group s * n_sub + p
  * is part p of the query at place s of the depth-first query order. */
 typedef struct {
-    int32_t* entries;        /* [4 * n_entries]    {page, node, first token in node, room}  */
+    int32_t* entries;        /* [4 * n_entries]    {page, node, first token in node, room +
+                                                   65536 if it holds tokens at plan time}   */
     int32_t* items;          /* [6 * n_items]      {first entry, end entry, first row group,
                                                    end row group, first partial row or -1, 0} */
     int32_t* query_order;    /* [n_live]           query index at each place                */

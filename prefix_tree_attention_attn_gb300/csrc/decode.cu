@@ -155,7 +155,7 @@ struct Shape {
 
 struct Meta {
     int32_t page[kDecodeMaxChunk];
-    int32_t valid[kDecodeMaxChunk];
+    int32_t valid[kDecodeMaxChunk];   // tokens; narrow: -1 = empty, but loaded
     float kf[kDecodeMaxChunk];        // k_scale * softmax_scale * log2(e)
     float lv[kDecodeMaxChunk];        // log2(v_scale)
     uint64_t full[kDecodeMaxChunk];   // one per page, used once: pages land out of order
@@ -164,6 +164,7 @@ struct Meta {
     // one for both, a wait for page i could meet the parity of page i + 2), P V has finished
     uint64_t s_done[2], p_full[2], o_done;
     int32_t count[kDecodeMaxChunk / 32];
+    int32_t early;                    // wide: the first halves are on their way
     uint32_t tmem;
     union {
         struct {
@@ -224,9 +225,11 @@ __device__ __forceinline__ uint32_t keep_bytes(int k, int valid) {
 
 // After a wait that ran out: gives the copies still in flight time to land (their
 // barriers complete) before shared memory is given up.
-__device__ __noinline__ void drain(Meta& M, int n) {
-    for (int i = threadIdx.x; i < n; i += kThreads)
-        for (int k = 0; k < 4096 && !(mbar_try_wait(smem_u32(&M.full[i]), 0) && mbar_try_wait(smem_u32(&M.full_v[i]), 0)); ++k) {}
+__device__ __noinline__ void drain(Meta& M, int n, bool is_wide) {
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        for (int k = 0; k < 4096 && !mbar_try_wait(smem_u32(&M.full[i]), 0); ++k) {}
+        for (int k = 0; is_wide && k < 4096 && !mbar_try_wait(smem_u32(&M.full_v[i]), 0); ++k) {}
+    }
     __syncthreads();
 }
 
@@ -234,31 +237,57 @@ __device__ __forceinline__ float out_lse(float m, float l) {
     return l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m - kLift) + log2f(l)) * kLn2;
 }
 
+// What a thread knows of page `threadIdx.x` of the item before it reads anything that
+// an earlier kernel may have written.
+struct Entry {
+    int page, node, from, room;
+    bool sure;           // held tokens when the plan was made: worth loading before its length is known
+};
+// Tokens of the page now, and its factors.
+struct Factors {
+    int valid;
+    float kf, lv;
+};
+__device__ __forceinline__ Factors factors(const DecodeParams& p, const Entry& e, int h) {
+    const int64_t ph = (int64_t)e.page * p.hkv + h;
+    const int len = p.lens[e.node];
+    const float ks = p.ks[ph], vs = p.vs[ph];
+    return {max(0, min(max(len, 0) - e.from, e.room)), ks * p.scale_log2,
+            (float)((int)(__float_as_uint(vs) >> 23) - 127)};
+}
+
 // ---- at most 8 rows --------------------------------------------------------------
+// n pages in the plan's order, some perhaps empty; qi: query of row (lane / 4) or -1.
 template <int D>
 __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint32_t ring, float* buf, const Rows& R,
-                       int part, int n) {
+                       const Entry& e, int qi, int head, int part, int n) {
     using S = Shape<D>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    // the first pages, a warp's own
-    if (lane == 0 && warp < S::kStages)
-        for (int i = warp; i < min(n, S::kStages); i += kWarps)
-            load_page<D>(&tk, p, M.page[i], R.h, ring + i * S::kStage, smem_u32(&M.full[i]));
-
     // query row g: features t * D/4 .., as the second operand
+    uint4 w[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) w[i] = make_uint4(0, 0, 0, 0);
+    if (qi >= 0) {
+        const uint16_t* src = p.q + (int64_t)qi * p.q_stride + head * D + t * (D / 4);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) w[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
+    }
+    // the first pages: at once, or when they turn out to hold tokens
+    if ((int)threadIdx.x < n) {
+        const int i = threadIdx.x;
+        const bool early = i < S::kStages && e.sure;
+        if (early) load_page<D>(&tk, p, e.page, R.h, ring + i * S::kStage, smem_u32(&M.full[i]));
+        const Factors f = factors(p, e, R.h);
+        if (i < S::kStages && !early && f.valid > 0)
+            load_page<D>(&tk, p, e.page, R.h, ring + i * S::kStage, smem_u32(&M.full[i]));
+        M.page[i] = e.page;
+        M.valid[i] = f.valid > 0 ? f.valid : early ? -1 : 0;   // -1: empty, but on its way
+        M.kf[i] = f.kf;
+        M.lv[i] = f.lv;
+    }
     uint32_t qb[D / 16][2];
     float qf;
     {
-        int place, head;
-        const bool ok = R.at(g, place, head);
-        uint4 w[D / 32];
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) w[i] = make_uint4(0, 0, 0, 0);
-        if (ok) {
-            const uint16_t* src = p.q + (int64_t)p.order[place] * p.q_stride + head * D + t * (D / 4);
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) w[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
-        }
         float amax = 0.f;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
@@ -273,6 +302,7 @@ __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Meta& M, ui
             qb[2 * i + 1][1] = scaled_f16(w[i].w, down);
         }
     }
+    __syncthreads();
     // factors of the accumulators' columns: rows 2t and 2t + 1
     const float qf0 = __shfl_sync(0xffffffffu, qf, 8 * t), qf1 = __shfl_sync(0xffffffffu, qf, 8 * t + 4);
 
@@ -285,29 +315,61 @@ __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Meta& M, ui
 
     bool ok = true;
     for (int i = warp; i < n; i += kWarps) {
-        const int s = i % S::kStages;
+        const uint32_t kb = ring + (i % S::kStages) * S::kStage, vb = kb + S::kHalf;
+        const int valid = M.valid[i];
+        // The stage's next page with tokens.  Called by whoever emptied the stage, or, for a
+        // first page that was never loaded, found it empty.
+        auto refill = [&]() {
+            if (lane != 0) return;
+            for (int x = i + S::kStages; x < n; x += S::kStages)
+                if (M.valid[x] > 0) {
+                    load_page<D>(&tk, p, M.page[x], R.h, kb, smem_u32(&M.full[x]));
+                    break;
+                }
+        };
+        if (valid == 0) {
+            if (i < S::kStages) refill();
+            continue;
+        }
         ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&M.full[i]), 0, p.status, 302));
         if (!ok) break;
-        const uint32_t kb = ring + s * S::kStage, vb = kb + S::kHalf;
-        const int valid = M.valid[i];
+        if (valid < 0) {
+            refill();
+            continue;
+        }
         // tile x: keys 16 (g/2) + 4x + (g & 1) and two further on
+        // (two tiles and two partial sums each: four independent chains of products)
         float c[4][4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < 4; x += 2) {
             const int key = 16 * (g >> 1) + 4 * x + (g & 1);
-            uint32_t w0[D / 16], w1[D / 16];
+            uint32_t w0[2][D / 16], w1[2][D / 16];
 #pragma unroll
-            for (int j = 0; j < D / 64; ++j) {
-                lds128(key_chunk<D>(kb, key, (D / 64) * t + j), *reinterpret_cast<uint32_t(*)[4]>(&w0[4 * j]));
-                lds128(key_chunk<D>(kb, key + 2, (D / 64) * t + j), *reinterpret_cast<uint32_t(*)[4]>(&w1[4 * j]));
-            }
-            c[x][0] = c[x][1] = c[x][2] = c[x][3] = 0.f;
+            for (int y = 0; y < 2; ++y)
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-                uint32_t a[4];
-                codes_f16(w0[j], a[0], a[2]);
-                codes_f16(w1[j], a[1], a[3]);
-                mma16816(c[x], a, qb[j][0], qb[j][1]);
+                for (int j = 0; j < D / 64; ++j) {
+                    lds128(key_chunk<D>(kb, key + 4 * y, (D / 64) * t + j), *reinterpret_cast<uint32_t(*)[4]>(&w0[y][4 * j]));
+                    lds128(key_chunk<D>(kb, key + 4 * y + 2, (D / 64) * t + j), *reinterpret_cast<uint32_t(*)[4]>(&w1[y][4 * j]));
+                }
+            float odd[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[x][j] = c[x + 1][j] = 0.f;
+#pragma unroll
+            for (int j = 0; j < D / 16; j += 2)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    uint32_t a[4];
+                    codes_f16(w0[y][j], a[0], a[2]);
+                    codes_f16(w1[y][j], a[1], a[3]);
+                    mma16816(c[x + y], a, qb[j][0], qb[j][1]);
+                    codes_f16(w0[y][j + 1], a[0], a[2]);
+                    codes_f16(w1[y][j + 1], a[1], a[3]);
+                    mma16816(odd[y], a, qb[j + 1][0], qb[j + 1][1]);
+                }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                c[x][j] += odd[0][j];
+                c[x + 1][j] += odd[1][j];
             }
         }
         const float lv = M.lv[i], kf = M.kf[i];
@@ -385,12 +447,11 @@ __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Meta& M, ui
             }
         }
         __syncwarp();
-        if (lane == 0 && i + S::kStages < n)
-            load_page<D>(&tk, p, M.page[i + S::kStages], R.h, kb, smem_u32(&M.full[i + S::kStages]));
+        refill();
     }
     // every page was waited for by its warp: the ring is free
     if (!__syncthreads_and(ok)) {
-        drain(M, n);
+        drain(M, n, false);
         return;
     }
 #pragma unroll
@@ -458,41 +519,72 @@ __device__ __forceinline__ void expand16(const uint32_t (&w)[4], uint32_t tile, 
     st_shared_v4(tile + sw128_offset(r, c + 1), f[4], f[5], f[6], f[7]);
 }
 
+// n pages in the plan's order; qi: query of row (thread / 2) or -1.
 template <int D>
-__device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint32_t ring, const Rows& R, int part, int n) {
+__device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint32_t ring, const Rows& R, const Entry& e,
+                     int qi, int head, int part, int n) {
     using S = Shape<D>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row = 32 * (warp & 3) + lane;                     // TMEM lane
     const uint32_t qs = ring + S::kQ, vs = ring + S::kV;
-    const uint32_t tmem = M.tmem;
-    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t o_col = tmem + 128;                          // S tiles at columns 0 and 64, O from 128
+    // Q, two threads per row
+    uint4 w[D / 16];
+    {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) w[i] = make_uint4(0, 0, 0, 0);
+        if (qi >= 0) {
+            const uint16_t* src = p.q + (int64_t)qi * p.q_stride + head * D + (threadIdx.x & 1) * (D / 2);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) w[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
+        }
+    }
     // Halves in the order they are expanded: K0, K1, V0, K2, V1, ..., V(n-1).
+    auto half_to = [&](bool is_v, int i, int page, int slot) {
+        const uint32_t dst = ring + S::kCodes + slot * S::kHalf;
+        const uint32_t bar = smem_u32(is_v ? &M.full_v[i] : &M.full[i]);
+        mbar_expect_tx(bar, S::kHalf);
+        if (is_v) load_v<D>(p, page, R.h, dst, bar);
+        else load_k<D>(&tk, p, page, R.h, dst, bar);
+    };
     auto load_half = [&](int x) {
         if (x >= 2 * n) return;
         const bool is_v = x == 2 * n - 1 || (x >= 2 && !(x & 1));
         const int i = x == 2 * n - 1 ? n - 1 : is_v ? x / 2 - 1 : (x + 1) / 2;
-        const uint32_t dst = ring + S::kCodes + (x % S::kWideStages) * S::kHalf;
-        const uint32_t bar = smem_u32(is_v ? &M.full_v[i] : &M.full[i]);
-        mbar_expect_tx(bar, S::kHalf);
-        if (is_v) load_v<D>(p, M.page[i], R.h, dst, bar);
-        else load_k<D>(&tk, p, M.page[i], R.h, dst, bar);
+        half_to(is_v, i, M.page[i], x % S::kWideStages);
     };
-    if (threadIdx.x == 128)
-        for (int x = 0; x < S::kWideStages; ++x) load_half(x);
-    // Q to f16, two threads per row
+    // Pages worth loading (sure to have held tokens, or holding some now), packed; the first
+    // three halves at once where the first two pages are sure.
+    bool early = false;
+    {
+        Factors f = {0, 0.f, 0.f};
+        if (warp < kDecodeMaxChunk / 32) {
+            if (warp == 0) {
+                early = (__ballot_sync(0xffffffffu, e.sure) & 3u) == 3u;
+                if (early && lane == 0) {
+                    half_to(false, 0, e.page, 0);
+                    half_to(true, 0, e.page, 2);
+                }
+                if (early && lane == 1) half_to(false, 1, e.page, 1);
+            }
+            if ((int)threadIdx.x < n) f = factors(p, e, R.h);
+        }
+        const uint32_t has = __ballot_sync(0xffffffffu, e.sure || f.valid > 0);
+        int at = __popc(has & ((1u << lane) - 1u));
+        if (lane == 0 && warp < kDecodeMaxChunk / 32) M.count[warp] = __popc(has);
+        if (threadIdx.x == 0) M.early = early;
+        if (n > 32) {
+            __syncthreads();
+            for (int x = 0; x < warp && x < kDecodeMaxChunk / 32; ++x) at += M.count[x];
+        }
+        if (e.sure || f.valid > 0) {
+            M.page[at] = e.page;
+            M.valid[at] = f.valid;
+            M.kf[at] = f.kf;
+            M.lv[at] = f.lv;
+        }
+    }
     {
         const int r = threadIdx.x >> 1, hf = threadIdx.x & 1;
-        int place, head;
-        const bool ok = R.at(r, place, head);
-        uint4 w[D / 16];
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) w[i] = make_uint4(0, 0, 0, 0);
-        if (ok) {
-            const uint16_t* src = p.q + (int64_t)p.order[place] * p.q_stride + head * D + hf * (D / 2);
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) w[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
-        }
         float amax = 0.f, down, up;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
@@ -507,7 +599,16 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint
         }
     }
     fence_proxy_async_smem();
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    n = 0;
+    for (int x = 0; x < kDecodeMaxChunk / 32; ++x) n += M.count[x];
+    const uint32_t tmem = M.tmem;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t o_col = tmem + 128;                          // S tiles at columns 0 and 64, O from 128
+    if (threadIdx.x == 128 && !M.early)
+        for (int x = 0; x < S::kWideStages; ++x) load_half(x);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     if (warp >= 4) {
@@ -675,21 +776,21 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint
     }
     if (!__syncthreads_and(ok)) {
         // the products issued end by themselves; so do the copies
-        drain(M, n);
+        drain(M, n, true);
         return;
     }
     tc_fence_after();
     const int half = warp >> 2;                                 // columns D / 2 * half ..
     m = M.top[row];
     l = M.sum[row];
-    int place, head;
-    if (!R.at(row, place, head)) place = -1;
+    int place, out_head;
+    if (!R.at(row, place, out_head)) place = -1;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int64_t at = R.h * p.part_rows + part + row;
-    const int64_t qi = place < 0 ? 0 : p.order[place];
+    const int64_t out = place < 0 ? 0 : p.order[place];
     if (place >= 0 && half == 0) {
         if (part >= 0) p.part_ml[at] = make_float2(m, l);
-        else p.lse[(int64_t)head * p.R + qi] = out_lse(m, l);
+        else p.lse[(int64_t)out_head * p.R + out] = out_lse(m, l);
     }
 #pragma unroll
     for (int x = 0; x < D / 64; ++x) {
@@ -706,7 +807,7 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint
         } else {
 #pragma unroll
             for (int j = 0; j < 32; j += 8)
-                *reinterpret_cast<uint4*>(p.o + (qi * p.hq + head) * D + col + j) =
+                *reinterpret_cast<uint4*>(p.o + (out * p.hq + out_head) * D + col + j) =
                     n ? make_uint4(pack_bf16x2(v[j] * inv, v[j + 1] * inv), pack_bf16x2(v[j + 2] * inv, v[j + 3] * inv),
                                    pack_bf16x2(v[j + 4] * inv, v[j + 5] * inv), pack_bf16x2(v[j + 6] * inv, v[j + 7] * inv))
                       : make_uint4(0, 0, 0, 0);
@@ -722,15 +823,21 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int item = blockIdx.x / p.hkv, h = blockIdx.x % p.hkv;
     const int32_t* it = p.items + 6 * (int64_t)item;
-    const int e0 = it[0], e1 = it[1], part = it[4];
+    const int e0 = it[0], n = it[1] - e0, part = it[4];
     const Rows R = {it[2], (it[3] - it[2]) * p.gsub, p.gsub, p.n_sub, p.group, h};
     const bool is_wide = R.rows > 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    if ((int)threadIdx.x < e1 - e0) {
+    // the plan's tables: nothing an earlier kernel writes
+    Entry e = {0, 0, 0, 0, false};
+    if ((int)threadIdx.x < n) {
+        const int4 x = *reinterpret_cast<const int4*>(p.entries + 4 * (int64_t)(e0 + threadIdx.x));
+        e = {x.x, x.y, x.z, x.w & 0xffff, x.w >> 16 != 0};
         mbar_init(smem_u32(&M.full[threadIdx.x]), 1);
         if (is_wide) mbar_init(smem_u32(&M.full_v[threadIdx.x]), 1);
     }
+    int place, head, qi = -1;
+    if (R.at(is_wide ? threadIdx.x >> 1 : lane >> 2, place, head)) qi = p.order[place];
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&M.s_done[i]), 1);
@@ -740,92 +847,82 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     }
     fence_mbar_init();
     if (is_wide && warp == kWarps - 1) tmem_alloc(smem_u32(&M.tmem), 256);
-    int4 entry = make_int4(0, 0, 0, 0);
-    if ((int)threadIdx.x < e1 - e0) entry = *reinterpret_cast<const int4*>(p.entries + 4 * (int64_t)(e0 + threadIdx.x));
     grid_dep_wait();
     grid_dep_launch();
-    // pages that hold tokens now, packed
-    int valid = 0;
-    float kf = 0.f, lv = 0.f;
-    if ((int)threadIdx.x < e1 - e0) {
-        const int64_t ph = (int64_t)entry.x * p.hkv + h;
-        kf = p.ks[ph] * p.scale_log2;
-        lv = (float)((int)(__float_as_uint(p.vs[ph]) >> 23) - 127);
-        valid = max(0, min(max(p.lens[entry.y], 0) - entry.z, entry.w));
-    }
-    const uint32_t has = __ballot_sync(0xffffffffu, valid > 0);
-    if (lane == 0 && warp < kDecodeMaxChunk / 32) M.count[warp] = __popc(has);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    int n = 0, at = __popc(has & ((1u << lane) - 1u));
-    for (int w = 0; w < kDecodeMaxChunk / 32; ++w) {
-        if (w < warp) at += M.count[w];
-        n += M.count[w];
-    }
-    if (valid > 0) {
-        M.page[at] = entry.x;
-        M.valid[at] = valid;
-        M.kf[at] = kf;
-        M.lv[at] = lv;
-    }
-    __syncthreads();
     if (is_wide) {
-        wide<D>(tk, p, M, ring, R, part, n);
+        wide<D>(tk, p, M, ring, R, e, qi, head, part, n);
         __syncthreads();
         if (warp == kWarps - 1) {
             tc_fence_after();
             tmem_dealloc(M.tmem, 256);
         }
     } else {
-        narrow<D>(tk, p, M, ring, reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw))), R, part, n);
+        narrow<D>(tk, p, M, ring, reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw))), R, e, qi, head, part, n);
     }
 }
 
-// One warp per (query, head): joins the partial rows of the query's items.
+// One warp per (query, head): joins the partial rows of the query's items.  Up to 32
+// of them, their places are read before the items are waited for.
 template <int D>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
     const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
-    if (w >= (int64_t)p.live * p.hq) {
-        grid_dep_wait();   // the next kernel counts on this one to end after the items
-        return;
-    }
-    const int place = (int)(w / p.hq), head = (int)(w % p.hq);
-    const int h = head / p.group, gi = head % p.group;
-    const int rg = place * p.n_sub + gi / p.gsub, off = gi % p.gsub;
-    const int c0 = p.ptr[rg], c1 = p.ptr[rg + 1];
-    const int64_t qi = p.order[place];
-    grid_dep_wait();
-    if (c1 == c0 + 1 && p.row[c0] < 0) return;         // written by its item
     constexpr int PL = D / 32;
+    int c0 = 0, c1 = 0, h = 0, off = 0, head = 0, mine = 0;
+    int64_t qi = 0;
+    if (w < (int64_t)p.live * p.hq) {
+        const int place = (int)(w / p.hq);
+        head = (int)(w % p.hq);
+        h = head / p.group;
+        const int gi = head % p.group, rg = place * p.n_sub + gi / p.gsub;
+        off = gi % p.gsub;
+        c0 = p.ptr[rg];
+        c1 = p.ptr[rg + 1];
+        qi = p.order[place];
+        if (c0 + lane < c1) mine = p.row[c0 + lane];
+    }
+    // the next kernel may start; it counts on this one to end after the items
+    grid_dep_wait();
+    grid_dep_launch();
+    if (w >= (int64_t)p.live * p.hq) return;
+    if (c1 == c0 + 1 && __shfl_sync(0xffffffffu, mine, 0) < 0) return;         // written by its item
     const int64_t base = h * p.part_rows + off;
-    float top = -INFINITY;
-    for (int c = c0 + lane; c < c1; c += 32) top = fmaxf(top, p.part_ml[base + p.row[c]].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float ref = top == -INFINITY ? 0.f : top;
-    float l = 0.f, o[PL];
+    float top = -INFINITY, l = 0.f, o[PL];
 #pragma unroll
     for (int j = 0; j < PL; ++j) o[j] = 0.f;
+    for (int b = c0; b < c1; b += 32) {
+        if (b > c0) mine = b + lane < c1 ? p.row[b + lane] : 0;
+        const int k = min(32, c1 - b);
+        const float2 ml = lane < k ? p.part_ml[base + mine] : make_float2(-INFINITY, 0.f);
+        float t = ml.x;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
+        t = fmaxf(t, top);
+        const float ref = t == -INFINITY ? 0.f : t;
+        const float again = fast_exp2(top - ref), f = fast_exp2(ml.x - ref);
+        l = l * again + f * ml.y;                                              // this lane's parts
+#pragma unroll
+        for (int j = 0; j < PL; ++j) o[j] *= again;
+        top = t;
 #pragma unroll 4
-    for (int c = c0; c < c1; ++c) {
-        const int64_t at = base + p.row[c];
-        const float2 ml = p.part_ml[at];
-        const float f = fast_exp2(ml.x - ref);
-        l += f * ml.y;
-        if constexpr (PL == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * D + lane * 4);
-            o[0] += f * v.x;
-            o[1] += f * v.y;
-            o[2] += f * v.z;
-            o[3] += f * v.w;
-        } else {
-            const float2 v = *reinterpret_cast<const float2*>(p.part_o + at * D + lane * 2);
-            o[0] += f * v.x;
-            o[1] += f * v.y;
+        for (int c = 0; c < k; ++c) {
+            const int64_t at = base + __shfl_sync(0xffffffffu, mine, c);
+            const float fc = __shfl_sync(0xffffffffu, f, c);
+            if constexpr (PL == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * D + lane * 4);
+                o[0] += fc * v.x;
+                o[1] += fc * v.y;
+                o[2] += fc * v.z;
+                o[3] += fc * v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2*>(p.part_o + at * D + lane * 2);
+                o[0] += fc * v.x;
+                o[1] += fc * v.y;
+            }
         }
     }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
     const float inv = l == 0.f ? 0.f : 1.f / l;
     uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (qi * p.hq + head) * D) + lane * (PL / 2);
 #pragma unroll

@@ -180,7 +180,8 @@ int build(const int32_t* parent, const int32_t* seg_len, const int32_t* capacity
         for (int32_t v : run_nodes[k])
             for (int64_t i = first[v]; i < first[v + 1]; ++i) {
                 const int32_t at = (int32_t)(i - first[v]) * kPage;
-                P->entries.insert(P->entries.end(), {P->page_tab[i], v, at, std::min(kPage, P->room[v] - at)});
+                const int32_t sure = at < seg_len[v] ? 1 << 16 : 0;
+                P->entries.insert(P->entries.end(), {P->page_tab[i], v, at, std::min(kPage, P->room[v] - at) | sure});
             }
         const int64_t cuts = ceil_div(run_pages[k], P->chunk);
         const int32_t g0 = run_lo[k] * P->n_sub, g1 = run_hi[k] * P->n_sub;

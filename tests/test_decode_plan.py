@@ -39,6 +39,8 @@ def test_items_cover_every_path_once(lib, seed):
     assert rows <= 128 and (sub - 1) * rows < group <= sub * rows
     # a page entry names its node, its first token and the room behind it
     for page, node, at, room in x["entries"]:
+        assert (room >> 16 == 1) == (at < seg[node])
+        room &= 0xFFFF
         assert at % PAGE == 0 and 0 < room <= PAGE and room == min(PAGE, cap[node] - at)
         assert pages[first[node] + at // PAGE] == page
     seen = {}
