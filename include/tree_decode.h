@@ -56,7 +56,9 @@ extern "C" {
 typedef struct tree_decode_plan_s* tree_decode_plan_t;
 
 typedef struct {
-    int32_t chunk_pages;   /* most pages per work item of the attention, 1..128; 0 = automatic */
+    int32_t cta_pages;     /* most pages per CTA's work item of the attention (runs read by more
+                              than 8 query rows), 1..128; 0 = automatic */
+    int32_t warp_pages;    /* the same for a warp's item (at most 8 rows), 1..32; 0 = automatic */
 } tree_attn_decode_opts_t;
 
 typedef struct {
@@ -66,11 +68,12 @@ typedef struct {
     int64_t n_part_rows;      /* partial rows per kv-head                     */
     int64_t workspace_bytes;  /* device workspace tree_attn_decode needs      */
     int32_t n_write_jobs;     /* pages tree_attn_cache_write fills            */
-    int32_t n_items;          /* work items of the attention, per kv-head     */
+    int32_t n_ctas;           /* CTAs of the attention, per kv-head           */
     int32_t n_live;           /* queries that are not padding                 */
     int32_t n_sub;            /* parts a query's head group is cut into       */
     int32_t rows_per_sub;     /* query heads per part                         */
-    int32_t chunk_pages;      /* chunk size in force                          */
+    int32_t cta_pages;        /* pages per item in force                      */
+    int32_t warp_pages;
 } tree_attn_decode_info_t;
 
 /* Caller-allocated destinations for tree_attn_decode_plan_export; any may be
@@ -79,12 +82,13 @@ typedef struct {
 typedef struct {
     int32_t* entries;        /* [4 * n_entries]    {page, node, first token in node, room +
                                                    65536 if it holds tokens at plan time}   */
-    int32_t* items;          /* [6 * n_items]      {first entry, end entry, first row group,
-                                                   end row group, first partial row or -1, 0} */
+    int32_t* items;          /* [n_ctas * 6 * 8]  six items per CTA {first entry, entries, first
+                                                   row group, end row group, first partial row, 1 if
+                                                   the whole CTA's (then the only one), 0, 0}; no
+                                                   entries: none */
     int32_t* query_order;    /* [n_live]           query index at each place                */
     int32_t* combine_ptr;    /* [n_live*n_sub + 1] CSR offsets into combine_row             */
-    int32_t* combine_row;    /* [n_combine]        first partial row of each (row group, item),
-                                                   -1 where the item writes the output      */
+    int32_t* combine_row;    /* [n_combine]        first partial row of each (row group, item) */
     int32_t* write_jobs;     /* [4 * n_write_jobs] {page, first source row, tokens, 0}      */
 } tree_attn_decode_arrays_t;
 

@@ -33,14 +33,14 @@ class PlanArrays(C.Structure):
 
 
 class DecodeOpts(C.Structure):
-    _fields_ = [("chunk_pages", C.c_int32)]
+    _fields_ = [("cta_pages", C.c_int32), ("warp_pages", C.c_int32)]
 
 
 class DecodeInfo(C.Structure):
     _fields_ = [("n_fresh_tokens", C.c_int64), ("n_entries", C.c_int64), ("n_combine", C.c_int64),
                 ("n_part_rows", C.c_int64), ("workspace_bytes", C.c_int64), ("n_write_jobs", C.c_int32),
-                ("n_items", C.c_int32), ("n_live", C.c_int32), ("n_sub", C.c_int32), ("rows_per_sub", C.c_int32),
-                ("chunk_pages", C.c_int32)]
+                ("n_ctas", C.c_int32), ("n_live", C.c_int32), ("n_sub", C.c_int32), ("rows_per_sub", C.c_int32),
+                ("cta_pages", C.c_int32), ("warp_pages", C.c_int32)]
 
 
 class DecodeArrays(C.Structure):

@@ -2,10 +2,10 @@
 // (include/tree_decode.h).
 //
 // A work item is a run of pages and a block of query rows (queries under the run x
-// the heads that share a kv-head); a CTA takes one item of one kv-head, so pages of
-// a shared prefix are read once for all the rows of its block.  Pages (K and V of one
-// kv-head, 64 * d bytes each) come by bulk copies into a ring of shared memory; the
-// warp (or CTA) that has emptied a stage refills it.
+// the heads that share a kv-head), of one kv-head; pages of a shared prefix are read
+// once for all the rows of a block.  Pages (K and V of one kv-head, 64 * d bytes each)
+// come by bulk copies into shared memory, refilled by whoever emptied it.  An item
+// leaves partial rows (O in fp32, M, l), which a second kernel joins per query.
 //
 // Per page, with fp32 accumulation on the tensor cores:
 //   S = Q K8^T        Q in f16; K8 the page's codes in f16 (exact: e4m3 values)
@@ -23,9 +23,13 @@
 //
 // Two bodies, by the item's rows:
 //
-// At most 8 rows (a leaf's own pages) -- `narrow`, bound by HBM.  Each of eight warps
-// takes whole pages in turn with accumulators of its own, joined at the end.  The
-// products run transposed, S^T = K Q^T and O^T = V^T P^T, with m16n8k16: the codes
+// At most 8 rows (a leaf's own pages) -- `narrow`, bound by HBM.  The item is one
+// warp's, six to a CTA, 12 to an SM, with nothing between the warps: loads of some
+// overlap the products of others, and no warp waits for a slower one (with a CTA's
+// warps on one item, joined at its end, every item cost 8 us of its SM slot besides its
+// pages).  A warp has room for one page: the next K is under way from the scores on,
+// the next V from the end of P V; 192 KB in flight per SM.
+// The products run transposed, S^T = K Q^T and O^T = V^T P^T, with m16n8k16: the codes
 // are the 16-row operand and the 8 columns are the query rows, so no half of the tensor
 // product is padding (rows as the 16-row operand, which a leaf of 8 rows half
 // fills, took 2.4 times the instructions).  Fragments come straight from the pages:
@@ -69,12 +73,10 @@ struct DecodeParams {
     const uint8_t* v8;
     const float* ks;
     const float* vs;
-    uint16_t* o;
-    float* lse;
     float* part_o;       // [hkv, part_rows, d]
     float2* part_ml;     // [hkv, part_rows] {M, l}
     int64_t part_rows;
-    int32_t R, hq, hkv, group, n_sub, gsub;
+    int32_t hkv, group, n_sub, gsub;
     float scale_log2;
     int* status;
 };
@@ -140,40 +142,35 @@ template <int D>
 struct Shape {
     static constexpr int kHalf = kPage * D;          // bytes of K (or V) of a page
     static constexpr int kStage = 2 * kHalf;
-    // narrow: the ring alone; its join reuses it
-    static constexpr int kStages = D == 128 ? 6 : 12;
-    static constexpr int kPitch = D + 4;
-    static_assert(kWarps * 8 * kPitch * 4 <= kStages * kStage, "the join reuses the ring");
+    static constexpr int kNarrow = kDecodeWarps * kStage;   // a page per warp
     // wide: f16 tiles of Q, K (two) and V, then a ring of K or V halves
     static constexpr int kWideStages = 3;
     static constexpr int kTile = kPage * D * 2;
     static constexpr int kQ = 0, kK = kQ + 128 * D * 2, kV = kK + 2 * kTile, kCodes = kV + kTile;
     static constexpr int kWide = kCodes + kWideStages * kHalf;
-    static constexpr int kRing = kStages * kStage > kWide ? kStages * kStage : kWide;
+    static constexpr int kRing = kNarrow > kWide ? kNarrow : kWide;
     static constexpr int kSmem = kRing + 1024;       // + alignment slack
 };
 
+// Wide items.
 struct Meta {
     int32_t page[kDecodeMaxChunk];
-    int32_t valid[kDecodeMaxChunk];   // tokens; narrow: -1 = empty, but loaded
+    int32_t valid[kDecodeMaxChunk];
     float kf[kDecodeMaxChunk];        // k_scale * softmax_scale * log2(e)
     float lv[kDecodeMaxChunk];        // log2(v_scale)
-    uint64_t full[kDecodeMaxChunk];   // one per page, used once: pages land out of order
-    uint64_t full_v[kDecodeMaxChunk]; // wide: V apart from K
-    // wide: the scores of a page are there, its P is in TMEM (one barrier per S buffer: with
+    // K and V of each page, used once
+    uint64_t full[kDecodeMaxChunk], full_v[kDecodeMaxChunk];
+    // the scores of a page are there, its P is in TMEM (one barrier per S buffer: with
     // one for both, a wait for page i could meet the parity of page i + 2), P V has finished
     uint64_t s_done[2], p_full[2], o_done;
     int32_t count[kDecodeMaxChunk / 32];
-    int32_t early;                    // wide: the first halves are on their way
+    int32_t early;                    // the first halves are on their way
     uint32_t tmem;
-    union {
-        struct {
-            float m[kWarps][8], l[kWarps][8];        // narrow: per warp and row
-        };
-        struct {
-            float top[128], sum[128], qf[128];       // wide: per row
-        };
-    };
+    float top[128], sum[128], qf[128];
+};
+// Narrow items: a warp's barriers for K and V.
+struct Pair {
+    uint64_t k, v;
 };
 
 // An item's rows: place in the output, and where its query row starts.
@@ -204,14 +201,6 @@ template <int D>
 __device__ __forceinline__ void load_v(const DecodeParams& p, int page, int h, uint32_t dst, uint32_t bar) {
     bulk_load(dst, p.v8 + ((int64_t)page * p.hkv + h) * Shape<D>::kHalf, Shape<D>::kHalf, bar);
 }
-template <int D>
-__device__ __forceinline__ void load_page(const CUtensorMap* tk, const DecodeParams& p, int page, int h, uint32_t dst,
-                                          uint32_t bar) {
-    mbar_expect_tx(bar, Shape<D>::kStage);
-    load_k<D>(tk, p, page, h, dst, bar);
-    load_v<D>(p, page, h, dst + Shape<D>::kHalf, bar);
-}
-
 // byte address of 16 codes c of key r in a K stage (swizzled by the tensor map for d = 128)
 template <int D>
 __device__ __forceinline__ uint32_t key_chunk(uint32_t base, int r, int c) {
@@ -223,18 +212,10 @@ __device__ __forceinline__ uint32_t keep_bytes(int k, int valid) {
     return n >= 4 ? 0xffffffffu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
 }
 
-// After a wait that ran out: gives the copies still in flight time to land (their
-// barriers complete) before shared memory is given up.
-__device__ __noinline__ void drain(Meta& M, int n, bool is_wide) {
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        for (int k = 0; k < 4096 && !mbar_try_wait(smem_u32(&M.full[i]), 0); ++k) {}
-        for (int k = 0; is_wide && k < 4096 && !mbar_try_wait(smem_u32(&M.full_v[i]), 0); ++k) {}
-    }
-    __syncthreads();
-}
-
-__device__ __forceinline__ float out_lse(float m, float l) {
-    return l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m - kLift) + log2f(l)) * kLn2;
+// After a wait that ran out: gives a copy still in flight time to land before its shared
+// memory is given up.
+__device__ __noinline__ void drain(uint64_t* bar, uint32_t parity) {
+    for (int k = 0; k < 4096 && !mbar_try_wait(smem_u32(bar), parity); ++k) {}
 }
 
 // What a thread knows of page `threadIdx.x` of the item before it reads anything that
@@ -257,12 +238,28 @@ __device__ __forceinline__ Factors factors(const DecodeParams& p, const Entry& e
 }
 
 // ---- at most 8 rows --------------------------------------------------------------
-// n pages in the plan's order, some perhaps empty; qi: query of row (lane / 4) or -1.
+// One warp.  n <= 32 pages, one per lane (e), some perhaps empty; qi: query of row
+// (lane / 4) or -1.
 template <int D>
-__device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint32_t ring, float* buf, const Rows& R,
-                       const Entry& e, int qi, int head, int part, int n) {
+__device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Pair& bar, uint32_t kb, const Rows& R, const Entry& e,
+                       int qi, int head, int part) {
     using S = Shape<D>;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t vb = kb + S::kHalf;
+    auto load_k = [&](int page) {
+        mbar_expect_tx(smem_u32(&bar.k), S::kHalf);
+        treeattn::load_k<D>(&tk, p, page, R.h, kb, smem_u32(&bar.k));
+    };
+    auto load_v = [&](int page) {
+        mbar_expect_tx(smem_u32(&bar.v), S::kHalf);
+        treeattn::load_v<D>(p, page, R.h, vb, smem_u32(&bar.v));
+    };
+    // the first page at once when it is sure to have held tokens
+    const bool early = __shfl_sync(0xffffffffu, e.sure, 0);
+    if (early && lane == 0) {
+        load_k(e.page);
+        load_v(e.page);
+    }
     // query row g: features t * D/4 .., as the second operand
     uint4 w[D / 32];
 #pragma unroll
@@ -272,18 +269,13 @@ __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Meta& M, ui
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) w[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
     }
-    // the first pages: at once, or when they turn out to hold tokens
-    if ((int)threadIdx.x < n) {
-        const int i = threadIdx.x;
-        const bool early = i < S::kStages && e.sure;
-        if (early) load_page<D>(&tk, p, e.page, R.h, ring + i * S::kStage, smem_u32(&M.full[i]));
-        const Factors f = factors(p, e, R.h);
-        if (i < S::kStages && !early && f.valid > 0)
-            load_page<D>(&tk, p, e.page, R.h, ring + i * S::kStage, smem_u32(&M.full[i]));
-        M.page[i] = e.page;
-        M.valid[i] = f.valid > 0 ? f.valid : early ? -1 : 0;   // -1: empty, but on its way
-        M.kf[i] = f.kf;
-        M.lv[i] = f.lv;
+    Factors f = {0, 0.f, 0.f};
+    if (e.room > 0) f = factors(p, e, R.h);
+    // pages to go: those with tokens, and the one that is on its way whatever it holds
+    uint32_t left = __ballot_sync(0xffffffffu, f.valid > 0 || (early && lane == 0));
+    if (!early && left && lane == __ffs(left) - 1) {
+        load_k(e.page);
+        load_v(e.page);
     }
     uint32_t qb[D / 16][2];
     float qf;
@@ -302,7 +294,6 @@ __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Meta& M, ui
             qb[2 * i + 1][1] = scaled_f16(w[i].w, down);
         }
     }
-    __syncthreads();
     // factors of the accumulators' columns: rows 2t and 2t + 1
     const float qf0 = __shfl_sync(0xffffffffu, qf, 8 * t), qf1 = __shfl_sync(0xffffffffu, qf, 8 * t + 4);
 
@@ -314,29 +305,13 @@ __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Meta& M, ui
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
 
     bool ok = true;
-    for (int i = warp; i < n; i += kWarps) {
-        const uint32_t kb = ring + (i % S::kStages) * S::kStage, vb = kb + S::kHalf;
-        const int valid = M.valid[i];
-        // The stage's next page with tokens.  Called by whoever emptied the stage, or, for a
-        // first page that was never loaded, found it empty.
-        auto refill = [&]() {
-            if (lane != 0) return;
-            for (int x = i + S::kStages; x < n; x += S::kStages)
-                if (M.valid[x] > 0) {
-                    load_page<D>(&tk, p, M.page[x], R.h, kb, smem_u32(&M.full[x]));
-                    break;
-                }
-        };
-        if (valid == 0) {
-            if (i < S::kStages) refill();
-            continue;
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&M.full[i]), 0, p.status, 302));
+    uint32_t turn = 0;
+    for (; left; ++turn) {
+        const int i = __ffs(left) - 1;
+        left &= left - 1;
+        const int valid = __shfl_sync(0xffffffffu, f.valid, i);
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar.k), turn & 1, p.status, 302));
         if (!ok) break;
-        if (valid < 0) {
-            refill();
-            continue;
-        }
         // tile x: keys 16 (g/2) + 4x + (g & 1) and two further on
         // (two tiles and two partial sums each: four independent chains of products)
         float c[4][4];
@@ -372,7 +347,12 @@ __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Meta& M, ui
                 c[x + 1][j] += odd[1][j];
             }
         }
-        const float lv = M.lv[i], kf = M.kf[i];
+        // K's place is free: the next page's
+        __syncwarp();
+        const int after = left ? __ffs(left) - 1 : -1;
+        const int next = __shfl_sync(0xffffffffu, e.page, max(after, 0));
+        if (lane == 0 && after >= 0) load_k(next);
+        const float lv = __shfl_sync(0xffffffffu, f.lv, i), kf = __shfl_sync(0xffffffffu, f.kf, i);
         const float f0 = kf * qf0, f1 = kf * qf1;
         float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
@@ -426,6 +406,8 @@ __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Meta& M, ui
 #pragma unroll
         for (int j = 0; j < 4; ++j) keep[j] = keep_bytes(16 * t + 4 * j, valid);
         const bool part_page = valid < kPage;
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar.v), turn & 1, p.status, 303));
+        if (!ok) break;
 #pragma unroll
         for (int y = 0; y < D / 16; ++y) {
             uint32_t w0[4], w1[4];
@@ -447,11 +429,11 @@ __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Meta& M, ui
             }
         }
         __syncwarp();
-        refill();
+        if (lane == 0 && after >= 0) load_v(next);
     }
-    // every page was waited for by its warp: the ring is free
-    if (!__syncthreads_and(ok)) {
-        drain(M, n, false);
+    if (!ok) {
+        drain(&bar.k, turn & 1);
+        drain(&bar.v, turn & 1);
         return;
     }
 #pragma unroll
@@ -459,49 +441,23 @@ __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Meta& M, ui
         l0 += __shfl_xor_sync(0xffffffffu, l0, o);
         l1 += __shfl_xor_sync(0xffffffffu, l1, o);
     }
-    if (g == 0) {
-        M.m[warp][2 * t] = m0;
-        M.m[warp][2 * t + 1] = m1;
-        M.l[warp][2 * t] = l0;
-        M.l[warp][2 * t + 1] = l1;
-    }
-    float* b = buf + warp * 8 * S::kPitch;
+    // rows 2t and 2t + 1 of the block; eight lanes write 32 bytes of a row
+    const int64_t at = R.h * p.part_rows + part + 2 * t;
+    float* o = p.part_o + at * D + g;
+    if (2 * t < R.rows) {
+        if (g == 0) p.part_ml[at] = make_float2(m0, l0);
 #pragma unroll
-    for (int y = 0; y < D / 16; ++y) {
-        b[(2 * t) * S::kPitch + 16 * y + g] = acc[y][0];
-        b[(2 * t + 1) * S::kPitch + 16 * y + g] = acc[y][1];
-        b[(2 * t) * S::kPitch + 16 * y + g + 8] = acc[y][2];
-        b[(2 * t + 1) * S::kPitch + 16 * y + g + 8] = acc[y][3];
-    }
-    __syncthreads();
-    const int warps = min(n, kWarps);
-    for (int x = threadIdx.x; x < R.rows * (D / 4); x += kThreads) {
-        const int r = x / (D / 4), c = 4 * (x % (D / 4));
-        int place, head;
-        if (!R.at(r, place, head)) continue;
-        float top = -INFINITY;
-        for (int w = 0; w < warps; ++w) top = fmaxf(top, M.m[w][r]);
-        const float ref = top == -INFINITY ? 0.f : top;
-        float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int w = 0; w < warps; ++w) {
-            const float f = fast_exp2(M.m[w][r] - ref);
-            const float4 v = *reinterpret_cast<const float4*>(buf + (w * 8 + r) * S::kPitch + c);
-            l += f * M.l[w][r];
-            o[0] += f * v.x;
-            o[1] += f * v.y;
-            o[2] += f * v.z;
-            o[3] += f * v.w;
+        for (int y = 0; y < D / 16; ++y) {
+            o[16 * y] = acc[y][0];
+            o[16 * y + 8] = acc[y][2];
         }
-        if (part >= 0) {
-            const int64_t at = R.h * p.part_rows + part + r;
-            *reinterpret_cast<float4*>(p.part_o + at * D + c) = make_float4(o[0], o[1], o[2], o[3]);
-            if (c == 0) p.part_ml[at] = make_float2(top, l);
-        } else {
-            const int64_t qi = p.order[place];
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            *reinterpret_cast<uint2*>(p.o + (qi * p.hq + head) * D + c) =
-                make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-            if (c == 0) p.lse[(int64_t)head * p.R + qi] = out_lse(top, l);
+    }
+    if (2 * t + 1 < R.rows) {
+        if (g == 0) p.part_ml[at + 1] = make_float2(m1, l1);
+#pragma unroll
+        for (int y = 0; y < D / 16; ++y) {
+            o[D + 16 * y] = acc[y][1];
+            o[D + 16 * y + 8] = acc[y][3];
         }
     }
 }
@@ -776,7 +732,11 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint
     }
     if (!__syncthreads_and(ok)) {
         // the products issued end by themselves; so do the copies
-        drain(M, n, true);
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            drain(&M.full[i], 0);
+            drain(&M.full_v[i], 0);
+        }
+        __syncthreads();
         return;
     }
     tc_fence_after();
@@ -784,60 +744,72 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint
     m = M.top[row];
     l = M.sum[row];
     int place, out_head;
-    if (!R.at(row, place, out_head)) place = -1;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const bool live = R.at(row, place, out_head);
     const int64_t at = R.h * p.part_rows + part + row;
-    const int64_t out = place < 0 ? 0 : p.order[place];
-    if (place >= 0 && half == 0) {
-        if (part >= 0) p.part_ml[at] = make_float2(m, l);
-        else p.lse[(int64_t)out_head * p.R + out] = out_lse(m, l);
-    }
+    if (live && half == 0) p.part_ml[at] = make_float2(m, l);
 #pragma unroll
     for (int x = 0; x < D / 64; ++x) {
         const int col = half * (D / 2) + 32 * x;
         float v[32];
         tmem_ld32(o_col + lanes + col, v);                      // whole warps only
         tmem_wait_ld();
-        if (place < 0) continue;
-        if (part >= 0) {
+        if (!live) continue;
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-                *reinterpret_cast<float4*>(p.part_o + at * D + col + j) =
-                    n ? make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; j += 8)
-                *reinterpret_cast<uint4*>(p.o + (out * p.hq + out_head) * D + col + j) =
-                    n ? make_uint4(pack_bf16x2(v[j] * inv, v[j + 1] * inv), pack_bf16x2(v[j + 2] * inv, v[j + 3] * inv),
-                                   pack_bf16x2(v[j + 4] * inv, v[j + 5] * inv), pack_bf16x2(v[j + 6] * inv, v[j + 7] * inv))
-                      : make_uint4(0, 0, 0, 0);
-        }
+        for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4*>(p.part_o + at * D + col + j) =
+                n ? make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     tc_fence_before();
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeParams p) {
+    using S = Shape<D>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ Meta M;
+    __shared__ union {
+        Meta M;
+        Pair pairs[kDecodeWarps];
+    } sm;
+    Meta& M = sm.M;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const int item = blockIdx.x / p.hkv, h = blockIdx.x % p.hkv;
-    const int32_t* it = p.items + 6 * (int64_t)item;
-    const int e0 = it[0], n = it[1] - e0, part = it[4];
-    const Rows R = {it[2], (it[3] - it[2]) * p.gsub, p.gsub, p.n_sub, p.group, h};
-    const bool is_wide = R.rows > 8;
+    const int cta = blockIdx.x / p.hkv, h = blockIdx.x % p.hkv;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
     // the plan's tables: nothing an earlier kernel writes
+    const int4* slots = reinterpret_cast<const int4*>(p.items) + 2 * kDecodeWarps * (int64_t)cta;
+    const int4 a0 = slots[0], b0 = slots[1];
+    const int mine = warp < kDecodeWarps ? 2 * warp : 0;
+    int4 a = slots[mine], b = slots[mine + 1];
+    const bool is_wide = b0.y != 0;
+    if (is_wide) {
+        a = a0;
+        b = b0;
+    }
+    const int n = a.y, part = b.x;
+    const Rows R = {a.z, (a.w - a.z) * p.gsub, p.gsub, p.n_sub, p.group, h};
     Entry e = {0, 0, 0, 0, false};
-    if ((int)threadIdx.x < n) {
-        const int4 x = *reinterpret_cast<const int4*>(p.entries + 4 * (int64_t)(e0 + threadIdx.x));
+    const int at = is_wide ? threadIdx.x : lane;
+    if (at < n) {
+        const int4 x = *reinterpret_cast<const int4*>(p.entries + 4 * (int64_t)(a.x + at));
         e = {x.x, x.y, x.z, x.w & 0xffff, x.w >> 16 != 0};
-        mbar_init(smem_u32(&M.full[threadIdx.x]), 1);
-        if (is_wide) mbar_init(smem_u32(&M.full_v[threadIdx.x]), 1);
     }
     int place, head, qi = -1;
     if (R.at(is_wide ? threadIdx.x >> 1 : lane >> 2, place, head)) qi = p.order[place];
+    if (!is_wide) {
+        if (lane == 0 && warp < kDecodeWarps) {
+            mbar_init(smem_u32(&sm.pairs[warp].k), 1);
+            mbar_init(smem_u32(&sm.pairs[warp].v), 1);
+        }
+        fence_mbar_init();
+        __syncwarp();
+        grid_dep_wait();
+        grid_dep_launch();
+        if (warp < kDecodeWarps && n > 0) narrow<D>(tk, p, sm.pairs[warp], ring + warp * S::kStage, R, e, qi, head, part);
+        return;
+    }
+    if (at < n) {
+        mbar_init(smem_u32(&M.full[at]), 1);
+        mbar_init(smem_u32(&M.full_v[at]), 1);
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&M.s_done[i]), 1);
@@ -846,19 +818,19 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
         mbar_init(smem_u32(&M.o_done), 1);
     }
     fence_mbar_init();
-    if (is_wide && warp == kWarps - 1) tmem_alloc(smem_u32(&M.tmem), 256);
+    if (warp == kWarps - 1) tmem_alloc(smem_u32(&M.tmem), 256);
     grid_dep_wait();
     grid_dep_launch();
-    if (is_wide) {
-        wide<D>(tk, p, M, ring, R, e, qi, head, part, n);
-        __syncthreads();
-        if (warp == kWarps - 1) {
-            tc_fence_after();
-            tmem_dealloc(M.tmem, 256);
-        }
-    } else {
-        narrow<D>(tk, p, M, ring, reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw))), R, e, qi, head, part, n);
+    wide<D>(tk, p, M, ring, R, e, qi, head, part, n);
+    __syncthreads();
+    if (warp == kWarps - 1) {
+        tc_fence_after();
+        tmem_dealloc(M.tmem, 256);
     }
+}
+
+__device__ __forceinline__ float out_lse(float m, float l) {
+    return l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m - kLift) + log2f(l)) * kLn2;
 }
 
 // One warp per (query, head): joins the partial rows of the query's items.  Up to 32
@@ -885,7 +857,6 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
     grid_dep_wait();
     grid_dep_launch();
     if (w >= (int64_t)p.live * p.hq) return;
-    if (c1 == c0 + 1 && __shfl_sync(0xffffffffu, mine, 0) < 0) return;         // written by its item
     const int64_t base = h * p.part_rows + off;
     float top = -INFINITY, l = 0.f, o[PL];
 #pragma unroll
@@ -935,8 +906,8 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 template <int D>
 int launch(const tree_decode_plan_s* P, const CUtensorMap& tk, const DecodeParams& a, const CombineParams& b,
            cudaStream_t s) {
-    const int64_t items = (int64_t)P->items.size() / 6;
-    if (items) {
+    const int64_t ctas = (int64_t)P->items.size() / (8 * kDecodeWarps);
+    if (ctas) {
         static std::once_flag once[kMaxDevices];
         static cudaError_t attr[kMaxDevices];
         int dev;
@@ -946,11 +917,11 @@ int launch(const tree_decode_plan_s* P, const CUtensorMap& tk, const DecodeParam
             attr[dev] = cudaFuncSetAttribute(decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
         });
         if (attr[dev] != cudaSuccess) return TREE_ATTN_ERR_CUDA;
-        if (launch_pdl(decode_kernel<D>, dim3((unsigned)(items * P->hkv)), dim3(kThreads), Shape<D>::kSmem, s, tk, a) !=
+        if (launch_pdl(decode_kernel<D>, dim3((unsigned)(ctas * P->hkv)), dim3(kThreads), Shape<D>::kSmem, s, tk, a) !=
             cudaSuccess)
             return TREE_ATTN_ERR_CUDA;
     }
-    if (P->any_combine && P->live) {
+    if (P->live) {
         const int64_t blocks = ((int64_t)P->live * P->hq + 7) / 8;
         if (launch_pdl(combine_kernel<D>, dim3((unsigned)blocks), dim3(256), 0, s, b) != cudaSuccess)
             return TREE_ATTN_ERR_CUDA;
@@ -988,8 +959,8 @@ extern "C" int tree_attn_decode(tree_decode_plan_t P, const int32_t* lens, const
     float2* part_ml = reinterpret_cast<float2*>(part_o + P->part_rows * P->hkv * P->d);
     const DecodeParams a = {D->entries, D->items, D->order, lens, static_cast<const uint16_t*>(q), q_stride,
                             static_cast<const uint8_t*>(k8), static_cast<const uint8_t*>(v8), k_scale, v_scale,
-                            static_cast<uint16_t*>(o), lse, part_o, part_ml, P->part_rows, P->R, P->hq, P->hkv,
-                            P->group, P->n_sub, P->gsub, softmax_scale * kLog2e, status};
+                            part_o, part_ml, P->part_rows, P->hkv, P->group, P->n_sub, P->gsub,
+                            softmax_scale * kLog2e, status};
     const CombineParams b = {D->order, D->combine_ptr, D->combine_row, static_cast<uint16_t*>(o), lse, part_o, part_ml,
                              P->part_rows, P->R, P->hq, P->hkv, P->group, P->n_sub, P->gsub, P->live};
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -6,9 +6,10 @@
 //
 // Runs.  A node whose query range equals its parent's continues its parent's
 // run: a chain that one set of queries reads is one list of pages, however many
-// nodes it was grown in.  A run's pages and its row groups (a query's heads that
-// share a kv-head) are cut into work items of at most kDecodeRows rows and `chunk`
-// pages; each page of a run is read by one item per block of rows, whatever the
+// nodes it was grown in.  A run's rows are its row groups (a query's heads that share
+// a kv-head).  Runs of at most 8 rows are cut into items for single warps, kDecodeWarps
+// of them to a CTA; larger runs into blocks of at most kDecodeRows rows and items for
+// whole CTAs.  Each page of a run is read by one item per block of rows, whatever the
 // number of rollouts behind it.
 #include <algorithm>
 #include <cmath>
@@ -24,12 +25,15 @@ namespace {
 constexpr int64_t kMaxCombine = (int64_t)1 << 27;
 // CTAs of the attention that run at one time: two per SM
 constexpr int64_t kSlots = 152 * 2;
+// Time of a page in a warp's item, in times of a page in a CTA's item (about 4 us at
+// full bandwidth, 12 warps to the SM, against 1.3 us, two CTAs to the SM).
+constexpr int64_t kWarpPage = 3;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 int build(const int32_t* parent, const int32_t* seg_len, const int32_t* capacity, int32_t n, const int32_t* pages,
-          int32_t n_pages, const uint8_t* fresh, const int32_t* query_node, int32_t R, int32_t opt_chunk,
-          tree_decode_plan_s* P) {
+          int32_t n_pages, const uint8_t* fresh, const int32_t* query_node, int32_t R, int32_t opt_cta,
+          int32_t opt_warp, tree_decode_plan_s* P) {
     // ---- the tree: depth-first numbers, children by ascending id -------------------
     std::vector<int32_t> head(n, -1), next(n, -1), order, number(n, -1), subtree_end(n, 0);
     int32_t roots = -1;
@@ -139,40 +143,45 @@ int build(const int32_t* parent, const int32_t* seg_len, const int32_t* capacity
         run_nodes[run_of[v]].push_back(v);
     }
 
-    // ---- chunk size, then items ------------------------------------------------------------
+    // ---- pages per item, then the items ------------------------------------------------------
     const int32_t per_block = std::max(1, kDecodeRows / P->gsub);   // row groups per item
     const size_t n_runs = run_lo.size();
-    std::vector<int64_t> run_pages(n_runs, 0);
-    int64_t units = 0;
+    std::vector<int64_t> run_pages(n_runs, 0), blocks(n_runs, 0);   // blocks = 0: items for warps
+    int64_t cost = 0;                                               // of all items, in CTA-pages
     for (size_t k = 0; k < n_runs; ++k) {
         for (int32_t v : run_nodes[k]) run_pages[k] += first[v + 1] - first[v];
-        units += run_pages[k] * ceil_div((int64_t)(run_hi[k] - run_lo[k]) * P->n_sub, per_block);
+        const int64_t rg = (int64_t)(run_hi[k] - run_lo[k]) * P->n_sub;
+        blocks[k] = rg * P->gsub <= kDecodeNarrow ? 0 : ceil_div(rg, per_block);
+        cost += blocks[k] ? run_pages[k] * blocks[k] * kDecodeWarps : run_pages[k] * kWarpPage;
     }
-    // Small trees: one wave of items.  From 16 pages an item on, up to four waves, so that
+    // Small trees: one wave of CTAs.  From 48 pages a CTA on, up to four waves, so that
     // the last items to finish are short.
-    const int64_t total = units * P->hkv;
-    const int64_t waves = std::min<int64_t>(4, std::max<int64_t>(1, total / (kSlots * 16)));
-    P->chunk = opt_chunk ? opt_chunk
-                         : (int32_t)std::min<int64_t>(kDecodeMaxChunk, std::max<int64_t>(4, ceil_div(total, kSlots * waves)));
+    cost = ceil_div(cost * P->hkv, kDecodeWarps);
+    const int64_t waves = std::min<int64_t>(4, std::max<int64_t>(1, cost / (kSlots * 24)));
+    const int64_t target = ceil_div(cost, kSlots * waves);
+    P->chunk = opt_cta ? opt_cta : (int32_t)std::min<int64_t>(kDecodeMaxChunk, std::max<int64_t>(2, target));
+    P->warp_chunk = opt_warp ? opt_warp : (int32_t)std::min<int64_t>(kDecodeMaxWarp, std::max<int64_t>(1, ceil_div(target, kWarpPage)));
+    auto cuts_of = [&](size_t k) { return ceil_div(run_pages[k], blocks[k] ? P->chunk : P->warp_chunk); };
     const int32_t groups = P->live * P->n_sub;
     std::vector<int32_t> count(groups, 0);
-    int64_t combine = 0, n_items = 0;
+    int64_t combine = 0, slots = 0;
     for (size_t k = 0; k < n_runs; ++k) {
-        const int64_t cuts = ceil_div(run_pages[k], P->chunk), rg = (int64_t)(run_hi[k] - run_lo[k]) * P->n_sub;
+        const int64_t cuts = cuts_of(k), rg = (int64_t)(run_hi[k] - run_lo[k]) * P->n_sub;
         combine += cuts * rg;
-        n_items += cuts * ceil_div(rg, per_block);
-        if (combine > kMaxCombine || n_items * P->hkv > INT32_MAX) return TREE_ATTN_ERR_TOO_LARGE;
+        slots += cuts * std::max<int64_t>(1, blocks[k]) * (blocks[k] ? kDecodeWarps : 1) + kDecodeWarps;
+        if (combine > kMaxCombine || slots * P->hkv > INT32_MAX) return TREE_ATTN_ERR_TOO_LARGE;
         for (int64_t s = (int64_t)run_lo[k] * P->n_sub; s < (int64_t)run_hi[k] * P->n_sub; ++s)
             count[s] += (int32_t)cuts;
     }
     if (combine * P->gsub * P->hkv > ((int64_t)1 << 40)) return TREE_ATTN_ERR_TOO_LARGE;
     P->combine_ptr.assign(groups + 1, 0);
-    for (int32_t s = 0; s < groups; ++s) {
-        P->combine_ptr[s + 1] = P->combine_ptr[s] + count[s];
-        if (count[s] != 1) P->any_combine = true;
-    }
-    P->combine_row.assign(combine, -1);
+    for (int32_t s = 0; s < groups; ++s) P->combine_ptr[s + 1] = P->combine_ptr[s] + count[s];
+    P->combine_row.assign(combine, 0);
     std::vector<int32_t> fill(P->combine_ptr.begin(), P->combine_ptr.end() - 1);
+    struct Item {
+        int32_t e0, n, g0, g1, part, wide;
+    };
+    std::vector<Item> ctas, warps;
     int64_t part = 0;
     for (size_t k = 0; k < n_runs; ++k) {
         if (!run_pages[k]) continue;
@@ -183,39 +192,37 @@ int build(const int32_t* parent, const int32_t* seg_len, const int32_t* capacity
                 const int32_t sure = at < seg_len[v] ? 1 << 16 : 0;
                 P->entries.insert(P->entries.end(), {P->page_tab[i], v, at, std::min(kPage, P->room[v] - at) | sure});
             }
-        const int64_t cuts = ceil_div(run_pages[k], P->chunk);
-        const int32_t g0 = run_lo[k] * P->n_sub, g1 = run_hi[k] * P->n_sub;
+        const int64_t cuts = cuts_of(k), nb = std::max<int64_t>(1, blocks[k]);
+        const int64_t g0 = (int64_t)run_lo[k] * P->n_sub, rg = (int64_t)(run_hi[k] - run_lo[k]) * P->n_sub;
         for (int64_t c = 0; c < cuts; ++c)
-            for (int32_t s = g0; s < g1; s += per_block) {
-                const int32_t end = std::min(g1, s + per_block);
-                // A row group with this item alone gets its output from it.  Row groups
-                // of one block have the same number of items unless a query sits at an
-                // inner node; then the whole block goes through partial rows.
-                bool direct = true;
-                for (int32_t x = s; x < end; ++x) direct = direct && count[x] == 1;
-                const int64_t rows = (int64_t)(end - s) * P->gsub;
-                if (!direct && part + rows > INT32_MAX) return TREE_ATTN_ERR_TOO_LARGE;
-                P->items.insert(P->items.end(), {(int32_t)(e0 + run_pages[k] * c / cuts),
-                                                 (int32_t)(e0 + run_pages[k] * (c + 1) / cuts), s, end,
-                                                 direct ? -1 : (int32_t)part, 0});
-                for (int32_t x = s; x < end; ++x)
-                    P->combine_row[fill[x]++] = direct ? -1 : (int32_t)(part + (int64_t)(x - s) * P->gsub);
-                if (!direct) {
-                    part += rows;
-                    P->any_combine = true;
-                }
+            for (int64_t b = 0; b < nb; ++b) {
+                const int64_t p0 = run_pages[k] * c / cuts, p1 = run_pages[k] * (c + 1) / cuts;
+                const int64_t s = g0 + rg * b / nb, end = g0 + rg * (b + 1) / nb;   // even blocks
+                const int64_t rows = (end - s) * P->gsub;
+                if (part + rows > INT32_MAX) return TREE_ATTN_ERR_TOO_LARGE;
+                (blocks[k] ? ctas : warps).push_back({(int32_t)(e0 + p0), (int32_t)(p1 - p0), (int32_t)s, (int32_t)end,
+                                                      (int32_t)part, blocks[k] ? 1 : 0});
+                for (int64_t x = s; x < end; ++x) P->combine_row[fill[x]++] = (int32_t)(part + (x - s) * P->gsub);
+                part += rows;
             }
     }
     P->part_rows = part;
-    // longest items first: the tail of the launch is made of short ones
-    const int64_t ni = (int64_t)P->items.size() / 6;
-    std::vector<int32_t> by(ni);
-    for (int64_t i = 0; i < ni; ++i) by[i] = (int32_t)i;
-    auto cost = [&](int32_t i) { return P->items[6 * (size_t)i + 1] - P->items[6 * (size_t)i]; };
-    std::stable_sort(by.begin(), by.end(), [&](int32_t a, int32_t b) { return cost(a) > cost(b); });
-    std::vector<int32_t> sorted(P->items.size());
-    for (int64_t i = 0; i < ni; ++i) std::memcpy(&sorted[6 * i], &P->items[6 * (size_t)by[i]], 6 * sizeof(int32_t));
-    P->items.swap(sorted);
+    // Slots of kDecodeWarps items per CTA, longest CTAs first: the tail of the launch is
+    // made of short ones.  Warps of one CTA get items of like length.
+    auto longer = [](const Item& a, const Item& b) { return a.n > b.n; };
+    std::stable_sort(warps.begin(), warps.end(), longer);
+    std::stable_sort(ctas.begin(), ctas.end(), longer);
+    size_t w = 0, t = 0;
+    auto put = [&](const Item& x) { P->items.insert(P->items.end(), {x.e0, x.n, x.g0, x.g1, x.part, x.wide, 0, 0}); };
+    const Item none = {0, 0, 0, 0, 0, 0};
+    while (w < warps.size() || t < ctas.size()) {
+        const bool wide = w >= warps.size() || (t < ctas.size() && ctas[t].n > warps[w].n * kWarpPage);
+        for (int32_t i = 0; i < kDecodeWarps; ++i) {
+            if (wide) put(i == 0 ? ctas[t] : none);
+            else put(w < warps.size() ? warps[w++] : none);
+        }
+        t += wide;
+    }
     P->ws_bytes = ((size_t)part * P->hkv * (P->d + 2) * sizeof(float) + 255) / 256 * 256;
     return TREE_ATTN_OK;
 }
@@ -236,8 +243,9 @@ int tree_attn_decode_plan(const int32_t* parent, const int32_t* seg_len, const i
     *out = nullptr;
     if (!parent || !seg_len || !query_node || n_nodes < 1 || n_queries < 1 || n_pages < 0)
         return TREE_ATTN_ERR_INVALID_ARG;
-    const int32_t chunk = opts ? opts->chunk_pages : 0;
-    if (chunk < 0 || chunk > kDecodeMaxChunk) return TREE_ATTN_ERR_INVALID_ARG;
+    const int32_t chunk = opts ? opts->cta_pages : 0, warp_chunk = opts ? opts->warp_pages : 0;
+    if (chunk < 0 || chunk > kDecodeMaxChunk || warp_chunk < 0 || warp_chunk > kDecodeMaxWarp)
+        return TREE_ATTN_ERR_INVALID_ARG;
     if (hq <= 0 || hkv <= 0 || hq % hkv != 0 || (d != 64 && d != 128)) return TREE_ATTN_ERR_UNSUPPORTED;
     if (hq > 65536 || n_queries > (1 << 24) || n_nodes > (1 << 26)) return TREE_ATTN_ERR_TOO_LARGE;
     if ((int64_t)n_pages * hkv * kPage > INT32_MAX) return TREE_ATTN_ERR_TOO_LARGE;   // row coordinate of a page
@@ -256,7 +264,8 @@ int tree_attn_decode_plan(const int32_t* parent, const int32_t* seg_len, const i
         if ((int64_t)n_queries * P->n_sub > (1 << 24)) st = TREE_ATTN_ERR_TOO_LARGE;
         else {
             try {
-                st = build(parent, seg_len, capacity, n_nodes, pages, n_pages, fresh, query_node, n_queries, chunk, P);
+                st = build(parent, seg_len, capacity, n_nodes, pages, n_pages, fresh, query_node, n_queries, chunk,
+                           warp_chunk, P);
             } catch (const std::exception&) {
                 st = TREE_ATTN_ERR_OUT_OF_MEMORY;
             }
@@ -280,11 +289,12 @@ int tree_attn_decode_plan_info(tree_decode_plan_t P, tree_attn_decode_info_t* o)
     o->n_part_rows = P->part_rows;
     o->workspace_bytes = (int64_t)P->ws_bytes;
     o->n_write_jobs = (int32_t)(P->jobs.size() / 4);
-    o->n_items = (int32_t)(P->items.size() / 6);
+    o->n_ctas = (int32_t)(P->items.size() / (8 * kDecodeWarps));
     o->n_live = P->live;
     o->n_sub = P->n_sub;
     o->rows_per_sub = P->gsub;
-    o->chunk_pages = P->chunk;
+    o->cta_pages = P->chunk;
+    o->warp_pages = P->warp_chunk;
     return TREE_ATTN_OK;
 }
 

@@ -39,7 +39,8 @@ class DecodePlan:
 
     def __init__(self, parent: Sequence[int], seg_len: Sequence[int], query_nodes: Sequence[int], hq: int, hkv: int,
                  d: int, capacity: Optional[Sequence[int]] = None, pages: Optional[Sequence[int]] = None,
-                 n_pages: Optional[int] = None, fresh: Optional[Sequence[bool]] = None, chunk_pages: int = 0):
+                 n_pages: Optional[int] = None, fresh: Optional[Sequence[bool]] = None,
+                 cta_pages: int = 0, warp_pages: int = 0):
         self._lib = B.load()
         self._h = None
         par, sl, qn = _i32(parent), _i32(seg_len), _i32(query_nodes)
@@ -55,7 +56,7 @@ class DecodePlan:
         fr = None if fresh is None else np.ascontiguousarray(np.asarray(fresh, dtype=np.uint8))
         if fr is not None and fr.shape != par.shape:
             raise ValueError("fresh must have one entry per node")
-        opts, h = B.DecodeOpts(chunk_pages), C.c_void_p()
+        opts, h = B.DecodeOpts(cta_pages, warp_pages), C.c_void_p()
         B.check(self._lib.tree_attn_decode_plan(
             _ptr_i32(par), _ptr_i32(sl), _ptr_i32(cap), len(par), None if pg is None else _ptr_i32(pg), int(n_pages),
             None if fr is None else fr.ctypes.data_as(B.c_uint8_p), _ptr_i32(qn), len(qn), hq, hkv, d, C.byref(opts),
@@ -80,7 +81,7 @@ class DecodePlan:
     def export(self) -> Dict[str, np.ndarray]:
         """Copies of the plan arrays (``tree_attn_decode_plan_export``)."""
         i = self.info
-        sizes = {"entries": (i["n_entries"], 4), "items": (i["n_items"], 6), "query_order": (i["n_live"],),
+        sizes = {"entries": (i["n_entries"], 4), "items": (i["n_ctas"], 6, 8), "query_order": (i["n_live"],),
                  "combine_ptr": (i["n_live"] * i["n_sub"] + 1,), "combine_row": (i["n_combine"],),
                  "write_jobs": (i["n_write_jobs"], 4)}
         out, arr = {f: np.zeros(s, dtype=np.int32) for f, s in sizes.items()}, B.DecodeArrays()

@@ -27,10 +27,10 @@ def random_case(rng):
 def test_items_cover_every_path_once(lib, seed):
     rng = np.random.default_rng(seed)
     parent, seg, cap, pages, pool, queries, group = random_case(rng)
-    chunk = int(rng.choice([0, 1, 3, 128]))
+    cta, warp = int(rng.choice([0, 1, 3, 128])), int(rng.choice([0, 1, 2, 32]))
     fresh = rng.random(len(parent)) < 0.7
     p = DecodePlan(parent, seg, queries, 2 * group, 2, 64, capacity=cap, pages=pages, n_pages=pool, fresh=fresh,
-                   chunk_pages=chunk)
+                   cta_pages=cta, warp_pages=warp)
     x, info = p.export(), p.info
     first = np.concatenate([[0], np.cumsum([-(-c // PAGE) for c in cap])])
     live = [r for r, u in enumerate(queries) if u >= 0]
@@ -45,16 +45,21 @@ def test_items_cover_every_path_once(lib, seed):
         assert pages[first[node] + at // PAGE] == page
     seen = {}
     part_rows = []
-    for e0, e1, g0, g1, part, _ in x["items"]:
-        assert 0 <= e0 < e1 <= info["n_entries"] and 0 <= g0 < g1 <= len(live) * sub
-        assert (g1 - g0) * rows <= 128 and (chunk == 0 or e1 - e0 <= chunk)
+    items = []
+    for slots in x["items"]:
+        assert slots[0][1] > 0 and all(not y[1] or y[5] == slots[0][5] for y in slots)
+        assert not slots[0][5] or not slots[1:, 1].any()               # a CTA's item is alone
+        items += [y for y in slots if y[1]]
+    for e0, n, g0, g1, part, wide, _, _ in items:
+        assert 0 <= e0 and 0 < n and e0 + n <= info["n_entries"] and 0 <= g0 < g1 <= len(live) * sub
+        assert (g1 - g0) * rows <= (128 if wide else 8)
+        assert n <= ((cta or 128) if wide else (warp or 32))
         for g in range(g0, g1):
-            for e in range(e0, e1):
+            for e in range(e0, e0 + n):
                 key = (g, int(x["entries"][e][0]))
                 assert key not in seen
                 seen[key] = True
-        if part >= 0:
-            part_rows.append((part, part + (g1 - g0) * rows))
+        part_rows.append((part, part + (g1 - g0) * rows))
     # partial rows: disjoint and all inside the workspace
     part_rows.sort()
     assert all(a[1] <= b[0] for a, b in zip(part_rows, part_rows[1:]))
@@ -68,15 +73,13 @@ def test_items_cover_every_path_once(lib, seed):
                 want |= {(s * sub + j, int(pg)) for j in range(sub)}
             u = parent[u]
     assert set(seen) == want
-    # every row group finds its items' partial rows, -1 only where one item writes the output
+    # every row group finds its items' partial rows
     items_of = {g: [] for g in range(len(live) * sub)}
-    for e0, e1, g0, g1, part, _ in x["items"]:
+    for _, _, g0, g1, part, _, _, _ in items:
         for g in range(g0, g1):
-            items_of[g].append(-1 if part < 0 else part + (g - g0) * rows)
+            items_of[g].append(part + (g - g0) * rows)
     for g, parts in items_of.items():
-        got = list(x["combine_row"][x["combine_ptr"][g]:x["combine_ptr"][g + 1]])
-        assert sorted(got) == sorted(parts)
-        assert -1 not in got or len(got) == 1
+        assert sorted(x["combine_row"][x["combine_ptr"][g]:x["combine_ptr"][g + 1]]) == sorted(parts)
     # write jobs: the fresh nodes' tokens in depth-first order
     kids = {v: [c for c in range(len(parent)) if parent[c] == v] for v in range(-1, len(parent))}
     order, stack = [], list(reversed(kids[-1]))
@@ -95,22 +98,24 @@ def test_items_cover_every_path_once(lib, seed):
 
 
 def test_shared_prefix_is_one_run(lib):
-    """A prompt under 8 siblings is in one item per chunk, not one per sibling; a chain
-    that one query reads is one run."""
-    p = DecodePlan([-1] + [0] * 8, [256] + [64] * 8, range(1, 9), 8, 1, 128, chunk_pages=128)
-    assert p.info["n_items"] == 1 + 8 and p.info["n_entries"] == 4 + 8
-    c = DecodePlan([-1, 0, 1, 2], [64, 64, 64, 10], [3], 8, 1, 128, chunk_pages=128)
-    assert c.info["n_items"] == 1 and c.info["n_part_rows"] == 0 and c.workspace_bytes == 0
+    """A prompt under 8 siblings is in one item, not one per sibling; a chain that one
+    query reads is one run."""
+    p = DecodePlan([-1] + [0] * 8, [256] + [64] * 8, range(1, 9), 16, 1, 128, cta_pages=128, warp_pages=32)
+    x = p.export()["items"].reshape(-1, 8)
+    assert sorted(x[x[:, 1] > 0][:, 1].tolist()) == [1] * 8 + [4] and p.info["n_entries"] == 4 + 8
+    c = DecodePlan([-1, 0, 1, 2], [64, 64, 64, 10], [3], 8, 1, 128, warp_pages=32)
+    x = c.export()["items"].reshape(-1, 8)
+    assert x[x[:, 1] > 0][:, 1].tolist() == [4] and c.info["n_part_rows"] == 8
 
 
-def status(lib, parent, seg, queries, hq=2, hkv=1, d=64, cap=None, pages=None, n_pages=None, chunk=0):
+def status(lib, parent, seg, queries, hq=2, hkv=1, d=64, cap=None, pages=None, n_pages=None, cta=0, warp=0):
     a = lambda x: None if x is None else np.asarray(x, np.int32).ctypes.data_as(B.c_int32_p)  # noqa: E731
     keep = [np.asarray(x, np.int32) if x is not None else None for x in (parent, seg, cap, pages, queries)]
     ptr = [None if x is None else x.ctypes.data_as(B.c_int32_p) for x in keep]
     h = C.c_void_p()
     pool = 1000 if n_pages is None else n_pages
     st = lib.tree_attn_decode_plan(ptr[0], ptr[1], ptr[2], len(parent), ptr[3], pool, None, ptr[4], len(queries), hq, hkv,
-                                   d, C.byref(B.DecodeOpts(chunk)), C.byref(h))
+                                   d, C.byref(B.DecodeOpts(cta, warp)), C.byref(h))
     assert (st == 0) == bool(h.value)
     lib.tree_attn_decode_plan_destroy(h)
     return st
@@ -133,8 +138,8 @@ def test_plan_refusals(lib):
     assert status(lib, **ok, pages=[0, 1, -1]) == -1
     assert status(lib, **ok, n_pages=2) == -1                               # three are needed
     assert status(lib, **ok, n_pages=3) == 0
-    for chunk in (-1, 129):
-        assert status(lib, **ok, chunk=chunk) == -1
+    for kw in ({"cta": -1}, {"cta": 129}, {"warp": -1}, {"warp": 33}):
+        assert status(lib, **ok, **kw) == -1
     for hq, hkv, d in ((3, 2, 64), (0, 1, 64), (2, 0, 64), (2, 1, 96), (2, 1, 256)):
         assert status(lib, **ok, hq=hq, hkv=hkv, d=d) == -4
     assert status(lib, **ok, hkv=2, n_pages=2 ** 31 - 1) == -3              # page rows pass 31 bits
@@ -153,7 +158,7 @@ def test_plan_refusals(lib):
 
 
 def test_calls_validate_before_touching_the_device(lib):
-    p = DecodePlan([-1, 0, 0], [100, 60, 60], [1, 2], 4, 2, 128, chunk_pages=1)
+    p = DecodePlan([-1, 0, 0], [100, 60, 60], [1, 2], 4, 2, 128)
     f, odd = C.c_void_p(0x1000), C.c_void_p(0x1008)
     w = lib.tree_attn_cache_write
     assert w(None, f, f, 256, 256, f, f, f, f, None) == -1

@@ -86,12 +86,12 @@ def check(plan, cache, ref, parent, lens, cap, pages, queries, q, scale, o, lse)
     assert (err <= tol + 1e-30).all(), f"O: {(err / (tol + 1e-30)).max():.2f} of the bound"
 
 
-def build(rng, parent, seg, queries, hq, hkv, d, dev, cap=None, chunk=0, spread=0.0, spare=3):
+def build(rng, parent, seg, queries, hq, hkv, d, dev, cap=None, items=(0, 0), spread=0.0, spare=3):
     cap = seg if cap is None else cap
     need = sum(-(-int(c) // 64) for c in cap)
     pages = rng.permutation(need + spare)[:need]
     plan = TD.DecodePlan(parent, seg, queries, hq, hkv, d, capacity=cap, pages=pages, n_pages=need + spare,
-                         chunk_pages=chunk)
+                         cta_pages=items[0], warp_pages=items[1])
     cache, ref = cache_pair(need + spare, hkv, d, dev)
     n = plan.info["n_fresh_tokens"]
     k, v = rows(rng, n, hkv, d, dev, spread), rows(rng, n, hkv, d, dev, spread)
@@ -129,9 +129,9 @@ def test_write_and_decode(lib, cuda_device, name, heads):
     check(plan, cache, ref, parent, seg, seg, pages, queries, q, d ** -0.5, o, lse)
 
 
-@pytest.mark.parametrize("chunk", [0, 1, 5, 128])
+@pytest.mark.parametrize("items", [(0, 0), (1, 1), (5, 3), (128, 32)])
 @pytest.mark.parametrize("seed", range(6))
-def test_random_trees(lib, cuda_device, seed, chunk):
+def test_random_trees(lib, cuda_device, seed, items):
     """Random forests, inner and repeated queries, spare room, lengths of the moment
     below, at and beyond the room, and pages whose magnitudes differ widely."""
     rng = np.random.default_rng(seed)
@@ -140,7 +140,7 @@ def test_random_trees(lib, cuda_device, seed, chunk):
     cap = [x + int(rng.choice([0, 1, 70])) for x in t.seg_len]
     queries = [int(x) for x in rng.integers(-1, n, size=int(rng.integers(1, 40)))]
     hq, hkv, d = [(8, 2, 64), (16, 2, 128), (5, 1, 128)][seed % 3]
-    plan, cache, ref, pages = build(rng, t.parent, t.seg_len, queries, hq, hkv, d, cuda_device, cap=cap, chunk=chunk,
+    plan, cache, ref, pages = build(rng, t.parent, t.seg_len, queries, hq, hkv, d, cuda_device, cap=cap, items=items,
                                     spread=3.0)
     lens = [int(rng.choice([x, x, max(0, x - 1), x // 2, 0])) for x in t.seg_len]
     q = rows(rng, len(queries), hq, d, cuda_device)
@@ -343,7 +343,7 @@ def test_many_pages_in_flight(lib, cuda_device):
     rng = np.random.default_rng(13)
     parent, seg = [-1] + [0] * 24, [64 * 150 + 5] + [64 * int(x) + 9 for x in rng.integers(5, 90, 24)]
     for hq, queries in ((4, [3]), (8, [1, 2, 3, 4, 5]), (8, list(range(1, 25)))):
-        plan, cache, ref, pages = build(rng, parent, seg, queries, hq, 2, 128, cuda_device, chunk=128)
+        plan, cache, ref, pages = build(rng, parent, seg, queries, hq, 2, 128, cuda_device, items=(128, 32))
         q, ln = rows(rng, len(queries), hq, 128, cuda_device), plan.lens()
         outs = [TD.tree_decode(plan, cache, ln, q, 0.09) for _ in range(150)]
         assert device_status() == 0
