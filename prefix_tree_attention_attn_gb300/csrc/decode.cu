@@ -42,8 +42,10 @@
 // pages would cost a leaf's instructions once per 8 rows.  The codes are expanded
 // once per page to f16 tiles in shared memory and the products are tcgen05.mma with
 // M = 128 rows, accumulators in TMEM, P written back over S as the second product's
-// operand.  Four warps expand and issue, four do the softmax (one row per thread), so
-// the softmax of a page overlaps the expansion and the scores of the next.
+// operand.  Four warps do the softmax (one row per thread), three expand, one issues
+// products and copies: no step of a page waits for another page's.  (With the four
+// non-softmax warps taking turns at expanding and one of them issuing, a page took 3,300
+// cycles of its CTA, half of them barriers and issue.)
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -143,11 +145,11 @@ struct Shape {
     static constexpr int kHalf = kPage * D;          // bytes of K (or V) of a page
     static constexpr int kStage = 2 * kHalf;
     static constexpr int kNarrow = kDecodeWarps * kStage;   // a page per warp
-    // wide: f16 tiles of Q, K (two) and V, then a ring of K or V halves
-    static constexpr int kWideStages = 3;
+    // wide: f16 tiles of Q, K and V, then a ring of K or V halves
+    static constexpr int kHalves = 5;
     static constexpr int kTile = kPage * D * 2;
-    static constexpr int kQ = 0, kK = kQ + 128 * D * 2, kV = kK + 2 * kTile, kCodes = kV + kTile;
-    static constexpr int kWide = kCodes + kWideStages * kHalf;
+    static constexpr int kQ = 0, kK = kQ + 128 * D * 2, kV = kK + kTile, kCodes = kV + kTile;
+    static constexpr int kWide = kCodes + kHalves * kHalf;
     static constexpr int kRing = kNarrow > kWide ? kNarrow : kWide;
     static constexpr int kSmem = kRing + 1024;       // + alignment slack
 };
@@ -160,9 +162,10 @@ struct Meta {
     float lv[kDecodeMaxChunk];        // log2(v_scale)
     // K and V of each page, used once
     uint64_t full[kDecodeMaxChunk], full_v[kDecodeMaxChunk];
-    // the scores of a page are there, its P is in TMEM (one barrier per S buffer: with
-    // one for both, a wait for page i could meet the parity of page i + 2), P V has finished
-    uint64_t s_done[2], p_full[2], o_done;
+    // K, V of a page are expanded; its scores are there, its P is in TMEM (one barrier per S
+    // buffer: with one for both, a wait for page i could meet the parity of page i + 2); P V
+    // has finished
+    uint64_t k_ready, v_ready, s_done[2], p_full[2], o_done;
     int32_t count[kDecodeMaxChunk / 32];
     int32_t early;                    // the first halves are on their way
     uint32_t tmem;
@@ -463,6 +466,30 @@ __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Pair& bar, 
 }
 
 // ---- 9 to 128 rows -----------------------------------------------------------------
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+// Products and their commit by the one lane with `lead`; the warp stays together, so that the
+// operands are uniform registers.
+__device__ __forceinline__ void mma_ss(bool lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"((uint32_t)acc), "r"((uint32_t)lead) : "memory");
+}
+__device__ __forceinline__ void mma_ts(bool lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+        "r"((uint32_t)acc), "r"((uint32_t)lead) : "memory");
+}
+
 // Instruction descriptor, kind::f16: f16 A and B, fp32 accumulator, both K-major.
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24); }
 
@@ -506,10 +533,10 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint
         if (x >= 2 * n) return;
         const bool is_v = x == 2 * n - 1 || (x >= 2 && !(x & 1));
         const int i = x == 2 * n - 1 ? n - 1 : is_v ? x / 2 - 1 : (x + 1) / 2;
-        half_to(is_v, i, M.page[i], x % S::kWideStages);
+        half_to(is_v, i, M.page[i], x % S::kHalves);
     };
     // Pages worth loading (sure to have held tokens, or holding some now), packed; the first
-    // three halves at once where the first two pages are sure.
+    // halves at once where the first two pages are sure.
     bool early = false;
     {
         Factors f = {0, 0.f, 0.f};
@@ -563,75 +590,94 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint
     const uint32_t tmem = M.tmem;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t o_col = tmem + 128;                          // S tiles at columns 0 and 64, O from 128
-    if (threadIdx.x == 128 && !M.early)
-        for (int x = 0; x < S::kWideStages; ++x) load_half(x);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    if (warp >= 4) {
-        // ------------------------ expansion and products ------------------------
-        const int ct = threadIdx.x - 128;
-        int x = 0;                                              // half at hand
-        bool mine = true;                                       // this thread's waits outside the common ones
-        // The four warps run in step: after a barrier the half's slot is free and its tile
-        // is complete.
-        auto done_half = [&](bool good) {
-            fence_proxy_async_smem();
-            good = named_bar_and(1, 128, good && mine);         // the same for all 128 threads
-            if (good && ct == 0) load_half(x + S::kWideStages);
-            ++x;
-            return good;
-        };
-        auto expand_k = [&](int i) {
-            bool good = mbar_wait(smem_u32(&M.full[i]), 0, p.status, 304);
-            // the tile's previous reader was S of page i - 2
-            if (i > 1) good = mbar_wait(smem_u32(&M.s_done[i & 1]), (i / 2 - 1) & 1, p.status, 305) && good;
-            const uint32_t from = ring + S::kCodes + (x % S::kWideStages) * S::kHalf, ks = ring + S::kK + (i & 1) * S::kTile;
-            if constexpr (D == 128) {
-                // Eight lanes take four chunks of two rows that differ in bits 0 and 2, so that
-                // loads (swizzled by the row's 3 bits over 8 chunks) and stores both spread over
-                // all banks.
-                const int q = ct >> 2, r = (q & ~5) | (((q & 1) * 5) ^ (q & 4));
+    if (warp == 4) {
+        // --------------------------- products and copies ---------------------------
+        const bool lead = elect_one();
+        if (lead)
+            for (int x = M.early ? 3 : 0; x < S::kHalves; ++x) load_half(x);
+        __syncwarp();
+        const uint64_t qd = sdesc_sw128(qs, 16, 1024), kd = sdesc_sw128(ring + S::kK, 16, 1024), vd = sdesc_sw128(vs, 16, 1024);
+        int x = S::kHalves;                                     // next half to load
+        for (int i = 0; i <= n && ok; ++i) {
+            if (i < n) {
+                // S over the buffer that held P of page i - 2, which P V has read: products of
+                // one thread run in order
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&M.k_ready), i & 1, p.status, 305));
+                if (!ok) break;
+                tc_fence_after();
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    uint32_t w[4];
-                    const int rr = r + 32 * (y >> 1);
-                    lds128(from + sw128_offset(rr, 4 * (y & 1) + (ct & 3)), w);
-                    expand16(w, ks + (y & 1) * 8192, rr, 2 * (ct & 3));
+                for (int k = 0; k < D / 16; ++k)
+                    mma_ss(lead, tmem + 64 * (i & 1), qd + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
+                           kd + (((k >> 2) * 8192 + (k & 3) * 32) >> 4), idesc_f16(128, kPage), k > 0);
+                if (lead) {
+                    mma_commit(smem_u32(&M.s_done[i & 1]));
+                    load_half(x);
                 }
-            } else {
+                ++x;
+                __syncwarp();
+            }
+            if (i > 0) {
+                const int j = i - 1;
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&M.v_ready), j & 1, p.status, 307) &&
+                                                 mbar_wait(smem_u32(&M.p_full[j & 1]), (j / 2) & 1, p.status, 308));
+                if (!ok) break;
+                tc_fence_after();
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    uint32_t w[4];
-                    const int at = ct + 128 * y;
+                for (int k = 0; k < kPage / 16; ++k)
+                    mma_ts(lead, o_col, tmem + 64 * (j & 1) + 8 * k, vd + ((k * 32) >> 4), idesc_f16(128, D), j > 0 || k > 0);
+                if (lead) {
+                    mma_commit(smem_u32(&M.o_done));
+                    load_half(x);
+                }
+                ++x;
+                __syncwarp();
+            }
+        }
+    } else if (warp > 4) {
+        // -------------------------------- expansion --------------------------------
+        const int ct = threadIdx.x - 160;                       // of 96
+        auto expand_k = [&](int i, int x) {
+            bool good = mbar_wait(smem_u32(&M.full[i]), 0, p.status, 304);
+            // the tile's previous reader was S of page i - 1
+            if (i > 0) good = mbar_wait(smem_u32(&M.s_done[(i - 1) & 1]), ((i - 1) / 2) & 1, p.status, 306) && good;
+            if (!__all_sync(0xffffffffu, good)) return false;
+            const uint32_t from = ring + S::kCodes + (x % S::kHalves) * S::kHalf, ks = ring + S::kK;
+#pragma unroll 6
+            for (int at = ct; at < 4 * D; at += 96) {
+                uint32_t w[4];
+                if constexpr (D == 128) {
+                    // Eight lanes take four chunks of two rows that differ in bits 0 and 2, so that
+                    // loads (swizzled by the row's 3 bits over 8 chunks) and stores both spread
+                    // over all banks.
+                    const int q = at >> 2 & 63, y = at >> 8, r = (q & ~5) | (((q & 1) * 5) ^ (q & 4));
+                    lds128(from + sw128_offset(r, 4 * y + (at & 3)), w);
+                    expand16(w, ks + y * 8192, r, 2 * (at & 3));
+                } else {
                     lds128(from + at * 16, w);
                     expand16(w, ks, at >> 2, 2 * (at & 3));
                 }
             }
-            good = done_half(good);
-            if (good && ct == 0) {
-                // S over the buffer that held P of page i - 2, which P V has read: products
-                // of one thread run in order
-                const uint32_t s_col = tmem + 64 * (i & 1);
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_bf16_ss(s_col, sdesc_sw128(qs + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024),
-                                sdesc_sw128(ks + (k >> 2) * 8192 + (k & 3) * 32, 16, 1024), idesc_f16(128, kPage), k > 0);
-                mma_commit(smem_u32(&M.s_done[i & 1]));
-            }
-            return good;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&M.k_ready));
+            return true;
         };
-        ok = n > 0 ? expand_k(0) : true;
+        int x = 0;                                              // half at hand
+        ok = n > 0 ? expand_k(0, x++) : true;
         for (int i = 0; i < n && ok; ++i) {
-            if (i + 1 < n) ok = expand_k(i + 1);
+            if (i + 1 < n) ok = expand_k(i + 1, x++);
             if (!ok) break;
             const int valid = M.valid[i];
-            ok = mbar_wait(smem_u32(&M.full_v[i]), 0, p.status, 306);
-            if (i > 0) ok = mbar_wait(smem_u32(&M.o_done), (i - 1) & 1, p.status, 307) && ok;   // P V has read the tile
-            const uint32_t from = ring + S::kCodes + (x % S::kWideStages) * S::kHalf;
-#pragma unroll
-            for (int y = 0; y < D / 32; ++y) {
-                const int at = ct + 128 * y;
+            bool good = mbar_wait(smem_u32(&M.full_v[i]), 0, p.status, 312);
+            if (i > 0) good = mbar_wait(smem_u32(&M.o_done), (i - 1) & 1, p.status, 313) && good;   // P V has read the tile
+            ok = __all_sync(0xffffffffu, good);
+            if (!ok) break;
+            const uint32_t from = ring + S::kCodes + (x % S::kHalves) * S::kHalf;
+            ++x;
+#pragma unroll 6
+            for (int at = ct; at < 4 * D; at += 96) {
                 uint32_t w[4];
                 lds128(from + at * 16, w);
                 if (valid < kPage) {   // what is behind the last token may be anything, NaN included
@@ -640,21 +686,10 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint
                 }
                 expand16(w, vs, at >> 2, 2 * (at & 3));
             }
-            ok = done_half(ok);
-            if (ok && ct == 0) {
-                mine = mbar_wait(smem_u32(&M.p_full[i & 1]), (i / 2) & 1, p.status, 308);
-                if (mine) {
-                    const uint32_t s_col = tmem + 64 * (i & 1);
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = 0; k < kPage / 16; ++k)
-                        mma_bf16_ts(o_col, s_col + 8 * k, sdesc_sw128(vs + k * 32, 16, 1024), idesc_f16(128, D),
-                                    (i > 0 || k > 0) ? 1u : 0u);
-                    mma_commit(smem_u32(&M.o_done));
-                }
-            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&M.v_ready));
         }
-        ok = ok && mine;
     } else {
         // ------------------------------- softmax ---------------------------------
         const float qf = M.qf[row];
@@ -816,6 +851,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
             mbar_init(smem_u32(&M.p_full[i]), 128);
         }
         mbar_init(smem_u32(&M.o_done), 1);
+        mbar_init(smem_u32(&M.k_ready), 3);
+        mbar_init(smem_u32(&M.v_ready), 3);
     }
     fence_mbar_init();
     if (warp == kWarps - 1) tmem_alloc(smem_u32(&M.tmem), 256);
