@@ -638,26 +638,41 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint
     } else if (warp > 4) {
         // -------------------------------- expansion --------------------------------
         const int ct = threadIdx.x - 160;                       // of 96
+        constexpr int kRounds = (4 * D + 95) / 96;              // 16 codes each
         auto expand_k = [&](int i, int x) {
             bool good = mbar_wait(smem_u32(&M.full[i]), 0, p.status, 304);
             // the tile's previous reader was S of page i - 1
             if (i > 0) good = mbar_wait(smem_u32(&M.s_done[(i - 1) & 1]), ((i - 1) / 2) & 1, p.status, 306) && good;
             if (!__all_sync(0xffffffffu, good)) return false;
             const uint32_t from = ring + S::kCodes + (x % S::kHalves) * S::kHalf, ks = ring + S::kK;
-#pragma unroll 6
-            for (int at = ct; at < 4 * D; at += 96) {
-                uint32_t w[4];
+            // All loads, then all conversions.
+            auto place = [&](int u, int& r, int& y, int& c) {
+                const int at = ct + 96 * u;
+                c = at & 3;
                 if constexpr (D == 128) {
                     // Eight lanes take four chunks of two rows that differ in bits 0 and 2, so that
                     // loads (swizzled by the row's 3 bits over 8 chunks) and stores both spread
                     // over all banks.
-                    const int q = at >> 2 & 63, y = at >> 8, r = (q & ~5) | (((q & 1) * 5) ^ (q & 4));
-                    lds128(from + sw128_offset(r, 4 * y + (at & 3)), w);
-                    expand16(w, ks + y * 8192, r, 2 * (at & 3));
+                    const int q = at >> 2 & 63;
+                    y = at >> 8;
+                    r = (q & ~5) | (((q & 1) * 5) ^ (q & 4));
                 } else {
-                    lds128(from + at * 16, w);
-                    expand16(w, ks, at >> 2, 2 * (at & 3));
+                    y = 0;
+                    r = at >> 2;
                 }
+            };
+            uint32_t w[kRounds][4];
+#pragma unroll
+            for (int u = 0; u < kRounds; ++u) {
+                int r, y, c;
+                place(u, r, y, c);
+                if (ct + 96 * u < 4 * D) lds128(D == 128 ? from + sw128_offset(r, 4 * y + c) : from + r * 64 + c * 16, w[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kRounds; ++u) {
+                int r, y, c;
+                place(u, r, y, c);
+                if (ct + 96 * u < 4 * D) expand16(w[u], ks + y * 8192, r, 2 * c);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -676,15 +691,20 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint
             if (!ok) break;
             const uint32_t from = ring + S::kCodes + (x % S::kHalves) * S::kHalf;
             ++x;
-#pragma unroll 6
-            for (int at = ct; at < 4 * D; at += 96) {
-                uint32_t w[4];
-                lds128(from + at * 16, w);
-                if (valid < kPage) {   // what is behind the last token may be anything, NaN included
+            uint32_t w[kRounds][4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) w[j] &= keep_bytes(16 * (at & 3) + 4 * j, valid);
-                }
-                expand16(w, vs, at >> 2, 2 * (at & 3));
+            for (int u = 0; u < kRounds; ++u)
+                if (ct + 96 * u < 4 * D) lds128(from + (ct + 96 * u) * 16, w[u]);
+            if (valid < kPage) {       // what is behind the last token may be anything, NaN included
+#pragma unroll
+                for (int u = 0; u < kRounds; ++u)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[u][j] &= keep_bytes(16 * (ct & 3) + 4 * j, valid);
+            }
+#pragma unroll
+            for (int u = 0; u < kRounds; ++u) {
+                const int at = ct + 96 * u;
+                if (at < 4 * D) expand16(w[u], vs, at >> 2, 2 * (at & 3));
             }
             fence_proxy_async_smem();
             __syncwarp();
