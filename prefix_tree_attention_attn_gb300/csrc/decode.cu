@@ -95,8 +95,13 @@ struct CombineParams {
     int32_t R, hq, hkv, group, n_sub, gsub, live;
 };
 
-__device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&w)[4]) {
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+// 16 bytes of shared memory, by a plain load that the compiler may move.
+__device__ __forceinline__ void lds128(const uint8_t* at, uint32_t (&w)[4]) {
+    const uint4 x = *reinterpret_cast<const uint4*>(at);
+    w[0] = x.x;
+    w[1] = x.y;
+    w[2] = x.z;
+    w[3] = x.w;
 }
 // four e4m3 codes to two f16 pairs
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -110,7 +115,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return r;
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -206,7 +211,7 @@ __device__ __forceinline__ void load_v(const DecodeParams& p, int page, int h, u
 }
 // byte address of 16 codes c of key r in a K stage (swizzled by the tensor map for d = 128)
 template <int D>
-__device__ __forceinline__ uint32_t key_chunk(uint32_t base, int r, int c) {
+__device__ __forceinline__ const uint8_t* key_chunk(const uint8_t* base, int r, int c) {
     return D == 128 ? base + sw128_offset(r, c) : base + r * D + 16 * c;
 }
 // bits of four codes from key k on that lie before `valid`
@@ -244,18 +249,18 @@ __device__ __forceinline__ Factors factors(const DecodeParams& p, const Entry& e
 // One warp.  n <= 32 pages, one per lane (e), some perhaps empty; qi: query of row
 // (lane / 4) or -1.
 template <int D>
-__device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Pair& bar, uint32_t kb, const Rows& R, const Entry& e,
+__device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Pair& bar, const uint8_t* kb, const Rows& R, const Entry& e,
                        int qi, int head, int part) {
     using S = Shape<D>;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint32_t vb = kb + S::kHalf;
+    const uint8_t* vb = kb + S::kHalf;
     auto load_k = [&](int page) {
         mbar_expect_tx(smem_u32(&bar.k), S::kHalf);
-        treeattn::load_k<D>(&tk, p, page, R.h, kb, smem_u32(&bar.k));
+        treeattn::load_k<D>(&tk, p, page, R.h, smem_u32(kb), smem_u32(&bar.k));
     };
     auto load_v = [&](int page) {
         mbar_expect_tx(smem_u32(&bar.v), S::kHalf);
-        treeattn::load_v<D>(p, page, R.h, vb, smem_u32(&bar.v));
+        treeattn::load_v<D>(p, page, R.h, smem_u32(vb), smem_u32(&bar.v));
     };
     // the first page at once when it is sure to have held tokens
     const bool early = __shfl_sync(0xffffffffu, e.sure, 0);
@@ -504,12 +509,12 @@ __device__ __forceinline__ void expand16(const uint32_t (&w)[4], uint32_t tile, 
 
 // n pages in the plan's order; qi: query of row (thread / 2) or -1.
 template <int D>
-__device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint32_t ring, const Rows& R, const Entry& e,
+__device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, const uint8_t* base, const Rows& R, const Entry& e,
                      int qi, int head, int part, int n) {
     using S = Shape<D>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row = 32 * (warp & 3) + lane;                     // TMEM lane
-    const uint32_t qs = ring + S::kQ, vs = ring + S::kV;
+    const uint32_t ring = smem_u32(base), qs = ring + S::kQ, vs = ring + S::kV;
     // Q, two threads per row
     uint4 w[D / 16];
     {
@@ -644,7 +649,8 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint
             // the tile's previous reader was S of page i - 1
             if (i > 0) good = mbar_wait(smem_u32(&M.s_done[(i - 1) & 1]), ((i - 1) / 2) & 1, p.status, 306) && good;
             if (!__all_sync(0xffffffffu, good)) return false;
-            const uint32_t from = ring + S::kCodes + (x % S::kHalves) * S::kHalf, ks = ring + S::kK;
+            const uint8_t* from = base + S::kCodes + (x % S::kHalves) * S::kHalf;
+            const uint32_t ks = ring + S::kK;
             // All loads, then all conversions.
             auto place = [&](int u, int& r, int& y, int& c) {
                 const int at = ct + 96 * u;
@@ -689,7 +695,7 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, uint
             if (i > 0) good = mbar_wait(smem_u32(&M.o_done), (i - 1) & 1, p.status, 313) && good;   // P V has read the tile
             ok = __all_sync(0xffffffffu, good);
             if (!ok) break;
-            const uint32_t from = ring + S::kCodes + (x % S::kHalves) * S::kHalf;
+            const uint8_t* from = base + S::kCodes + (x % S::kHalves) * S::kHalf;
             ++x;
             uint32_t w[kRounds][4];
 #pragma unroll
@@ -826,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
         Pair pairs[kDecodeWarps];
     } sm;
     Meta& M = sm.M;
-    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* base = smem_raw + (-smem_u32(smem_raw) & 1023u);
     const int cta = blockIdx.x / p.hkv, h = blockIdx.x % p.hkv;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // the plan's tables: nothing an earlier kernel writes
@@ -858,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
         __syncwarp();
         grid_dep_wait();
         grid_dep_launch();
-        if (warp < kDecodeWarps && n > 0) narrow<D>(tk, p, sm.pairs[warp], ring + warp * S::kStage, R, e, qi, head, part);
+        if (warp < kDecodeWarps && n > 0) narrow<D>(tk, p, sm.pairs[warp], base + warp * S::kStage, R, e, qi, head, part);
         return;
     }
     if (at < n) {
@@ -878,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     if (warp == kWarps - 1) tmem_alloc(smem_u32(&M.tmem), 256);
     grid_dep_wait();
     grid_dep_launch();
-    wide<D>(tk, p, M, ring, R, e, qi, head, part, n);
+    wide<D>(tk, p, M, base, R, e, qi, head, part, n);
     __syncthreads();
     if (warp == kWarps - 1) {
         tc_fence_after();

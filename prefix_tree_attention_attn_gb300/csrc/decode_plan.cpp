@@ -25,9 +25,9 @@ namespace {
 constexpr int64_t kMaxCombine = (int64_t)1 << 27;
 // CTAs of the attention that run at one time: two per SM
 constexpr int64_t kSlots = 152 * 2;
-// Time of a page in a warp's item, in times of a page in a CTA's item (about 4 us at
-// full bandwidth, 12 warps to the SM, against 1.3 us, two CTAs to the SM).
-constexpr int64_t kWarpPage = 3;
+// Time of a page in a warp's item, in times of a page in a CTA's item: 1.2 us against
+// 0.75 us alone on an SM, 4.8 us against 1.4 us with every slot taken.
+constexpr int64_t kWarpPage = 2;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -154,13 +154,17 @@ int build(const int32_t* parent, const int32_t* seg_len, const int32_t* capacity
         blocks[k] = rg * P->gsub <= kDecodeNarrow ? 0 : ceil_div(rg, per_block);
         cost += blocks[k] ? run_pages[k] * blocks[k] * kDecodeWarps : run_pages[k] * kWarpPage;
     }
-    // Small trees: one wave of CTAs.  From 48 pages a CTA on, up to four waves, so that
-    // the last items to finish are short.
+    // One wave of CTAs for small trees; from 32 pages a CTA on more, up to four, so that the
+    // last to finish are short.  A quarter more than an even share, because every run ends in
+    // a remainder.  At least four pages: a CTA takes some 5 us before its first page is done
+    // and each item adds a partial row to join.  Measured (pages per CTA : per warp): group
+    // star of 16, 5:1 16 us, 4:4 11.6, 8:8 15; irregular tree of 80 nodes, 16:8 52, 32:16 47,
+    // 64:32 65; 64 branches on 32,768 tokens, 16:8 261, 48:24 224, 128:24 272.
     cost = ceil_div(cost * P->hkv, kDecodeWarps);
-    const int64_t waves = std::min<int64_t>(4, std::max<int64_t>(1, cost / (kSlots * 24)));
-    const int64_t target = ceil_div(cost, kSlots * waves);
-    P->chunk = opt_cta ? opt_cta : (int32_t)std::min<int64_t>(kDecodeMaxChunk, std::max<int64_t>(2, target));
-    P->warp_chunk = opt_warp ? opt_warp : (int32_t)std::min<int64_t>(kDecodeMaxWarp, std::max<int64_t>(1, ceil_div(target, kWarpPage)));
+    const int64_t waves = std::min<int64_t>(4, std::max<int64_t>(1, cost / (kSlots * 32)));
+    const int64_t target = ceil_div(cost * 5, kSlots * waves * 4);
+    P->chunk = opt_cta ? opt_cta : (int32_t)std::min<int64_t>(kDecodeMaxChunk, std::max<int64_t>(4, target));
+    P->warp_chunk = opt_warp ? opt_warp : (int32_t)std::min<int64_t>(kDecodeMaxWarp, std::max<int64_t>(4, ceil_div(target, kWarpPage)));
     auto cuts_of = [&](size_t k) { return ceil_div(run_pages[k], blocks[k] ? P->chunk : P->warp_chunk); };
     const int32_t groups = P->live * P->n_sub;
     std::vector<int32_t> count(groups, 0);
@@ -207,16 +211,24 @@ int build(const int32_t* parent, const int32_t* seg_len, const int32_t* capacity
             }
     }
     P->part_rows = part;
-    // Slots of kDecodeWarps items per CTA, longest CTAs first: the tail of the launch is
-    // made of short ones.  Warps of one CTA get items of like length.
+    // Slots of kDecodeWarps items per CTA.  Each kind's longest first, so that the tail of
+    // the launch is made of short ones; the kinds in proportion to their cost, so that
+    // CTAs bound by instructions and CTAs bound by HBM share the SMs all along.  Warps of
+    // one CTA get items of like length.
     auto longer = [](const Item& a, const Item& b) { return a.n > b.n; };
     std::stable_sort(warps.begin(), warps.end(), longer);
     std::stable_sort(ctas.begin(), ctas.end(), longer);
     size_t w = 0, t = 0;
     auto put = [&](const Item& x) { P->items.insert(P->items.end(), {x.e0, x.n, x.g0, x.g1, x.part, x.wide, 0, 0}); };
     const Item none = {0, 0, 0, 0, 0, 0};
+    int64_t warp_cost = 0, cta_cost = 0, warp_done = 0, cta_done = 0;   // of each kind: all, and placed
+    for (size_t i = 0; i < warps.size(); i += kDecodeWarps) warp_cost += warps[i].n * kWarpPage;
+    for (const Item& x : ctas) cta_cost += x.n;
     while (w < warps.size() || t < ctas.size()) {
-        const bool wide = w >= warps.size() || (t < ctas.size() && ctas[t].n > warps[w].n * kWarpPage);
+        const bool wide = w >= warps.size() ||
+                          (t < ctas.size() && (double)cta_done * warp_cost <= (double)warp_done * cta_cost);
+        if (wide) cta_done += ctas[t].n;
+        else warp_done += warps[w].n * kWarpPage;
         for (int32_t i = 0; i < kDecodeWarps; ++i) {
             if (wide) put(i == 0 ? ctas[t] : none);
             else put(w < warps.size() ? warps[w++] : none);
