@@ -13,15 +13,17 @@
 //             row through the full range in windows, several passes, by one CTA.
 //   groups    32 bins; a group's count and mass are one entry of a block-wide prefix
 //             sum, a search finds the group, then one warp the bin.
-//   cluster   C CTAs count a slice of the row each; each then weighs a share of the
-//             groups (counts summed over the C histograms through distributed shared
-//             memory), and the first one searches.
+//   cluster   C CTAs count a slice of the row each; each then weighs every C-th pair of groups
+//             (counts summed over the C histograms through distributed shared memory),
+//             and the first one searches.
 //   index     the r-th token with the drawn value, found by the CTA whose slice holds
 //             it.
 //
-// Memory-bound in principle (2 bytes per logit); in practice paced by the shared
-// memory atomics and the few cluster barriers of a short row.
+// Two bytes per logit from HBM; paced by the instructions of the count (a dozen per
+// logit with every case checked, now seven, with the checks made once for eight
+// logits), and for a few rows by the cluster's barriers and the chain of searches.
 #include <cooperative_groups.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -36,7 +38,7 @@ namespace treeattn {
 
 namespace {
 
-constexpr int kNT = 256;                       // threads per CTA
+constexpr int kNT = 512;                       // threads per CTA
 constexpr int kBase = (127 - 32) << 7;         // bits of 2^-32
 constexpr int kSide = 48 << 7;                 // values per sign: 2^-32 .. 2^16
 constexpr int kBins = 2 * kSide + 1;
@@ -98,18 +100,17 @@ __device__ __forceinline__ Rate rate_of(float T) {
 // 2^45 * 2^(d * c), d = x - top <= 0: n + j/64 + r = d * c in pairs of floats (48 bits),
 // 2^(j/64) from the table, 2^r - 1 by its series (|r ln 2| < 0.0055: five terms), then
 // integers.
-__device__ __forceinline__ uint64_t weight(float x, float top, Rate c) {
+__device__ __forceinline__ uint64_t weight(const uint64_t* pow, float x, float top, Rate c) {
     const float diff = x - top;
-    if (diff == 0.f) return 1ull << kOneBits;
     // the rounding error of x - top
     const float b = diff - x;
     const float dl = ((x - (diff - b)) - (top + b)) * c.pre;
     const float d = diff * c.pre;
     const float y = d * c.hi;
-    if (!(y > -64.f)) return 0;
+    const bool none = !(y > -64.f), full = diff == 0.f;   // (no branches: callers interleave several)
     const float yl = fmaf(d, c.hi, -y) + fmaf(d, c.lo, dl * c.hi);
-    const float n = rintf(y);
-    const float f = y - n;                       // exact
+    const float n = none ? 0.f : rintf(y);
+    const float f = none ? 0.f : y - n;          // exact
     const float j = rintf(f * 64.f);
     const float r = fmaf(j, -0.015625f, f);      // exact
     const float rh = r + yl;
@@ -121,12 +122,14 @@ __device__ __forceinline__ uint64_t weight(float x, float top, Rate c) {
     const float t = z * z * fmaf(z, fmaf(z, fmaf(z, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f);
     const float e = z + t;
     const float el = (t - (e - z)) + zl;
-    const int64_t E = __float2ll_rn(e * 0x1p62f) + __float2ll_rn(el * 0x1p62f);
-    const uint64_t p = kPow[(int)j + 32];
+    // (e + el) 2^62 from two 32-bit conversions
+    const float eh = rintf(e * 0x1p37f);
+    const int lo = __float2int_rn((e * 0x1p37f - eh) * 0x1p25f + el * 0x1p62f);
+    const int64_t E = ((int64_t)__float2int_rn(eh) << 25) + lo;
+    const uint64_t p = pow[(int)j + 32];
     const uint64_t w = p + 4 * (uint64_t)__mul64hi((int64_t)p, E);
-    const int shift = 61 - kOneBits - (int)n;
-    if (shift > 62) return 0;
-    return (w + (1ull << (shift - 1))) >> shift;
+    const int shift = min(61 - kOneBits - (int)n, 63);
+    return full ? 1ull << kOneBits : none ? 0 : (w + (1ull << (shift - 1))) >> shift;
 }
 
 // a * s for a non-negative float a < 2: the integer part, and whether something is left
@@ -153,43 +156,120 @@ __device__ __forceinline__ uint64_t times(float a, uint64_t s, bool& rest) {
     return hi >> (shift - 64);
 }
 
+// How a row's weights are made, and which of them min_p keeps.
+struct Weigher {
+    float top;
+    Rate rate;
+    bool same;           // the untempered weights are the same
+    uint64_t least;      // 0: no min_p
+};
+
+// What the weighing of groups adds up besides their masses.
+struct Sums {
+    uint64_t one;                                // untempered weight
+    uint64_t mass;                               // weight and number of the tokens that min_p keeps
+    uint32_t many;
+};
+
 struct Shared {
     uint32_t hist[kGroups * 32];
+    uint64_t pow[65];                            // kPow: lanes look up different entries
     uint32_t gcnt[kGroups], pcnt[kGroups];       // tokens of a group, of the groups before it
     uint64_t gmass[kGroups], pmass[kGroups];     // their weight
-    uint64_t one[kNT / 32];                      // untempered weight, by warp
+    Sums sums[8][kNT / 32];                      // by CTA of the cluster and warp
     uint32_t wcnt[kNT / 32];
     uint64_t wmass[kNT / 32];
-    float top;
-    uint32_t flags;                              // of the slice
+    float tops[8];                               // of the slices
+    uint32_t flags[8];
+    Weigher weigher;
+    Sums total;
     // the leader's search
     uint32_t tot_cnt;
     uint64_t tot_mass, tot_one;
-    int found;
+    int found[2];                                // group, -1 for none; searches alternate
     uint32_t f_cnt, f_rank;
     uint64_t f_mass;
     int f_bin;
     // the index search
     int key;                                     // bits of the drawn value, or -1
-    uint32_t rank, owner;
+    uint32_t rank, owner, matches;               // place among the owner's tokens of this value, and how many
+    uint32_t listed;
 };
 
 enum { kNaN = 1, kRare = 2, kLow = 4 };
 
-// Bin of a bf16 value, or -1 with the reason in `flags`.
-__device__ __forceinline__ int bin_of(uint32_t b, uint32_t& flags) {
-    const uint32_t mag = b & 0x7fffu, t = mag - kBase;
-    if (t < (uint32_t)kSide) return (b & 0x8000u) ? kSide + 1 + (int)t : kSide - 1 - (int)t;
-    if (mag == 0) return kSide;
-    flags |= mag > 0x7f80u ? kNaN : (t < 0x8000u && (b & 0x8000u)) ? kLow : kRare;
-    return -1;
+// Where a value of the short range is counted: magnitudes upwards from 0 for positive
+// values and from kSide for negative ones, then zero.
+constexpr int kZero = 2 * kSide;
+
+// Why a value outside the short range (and not zero) does not count.
+__device__ __forceinline__ uint32_t why(uint32_t b) {
+    const uint32_t mag = b & 0x7fffu;
+    return mag > 0x7f80u ? kNaN : (mag >= kBase && (b & 0x8000u)) ? kLow : kRare;
 }
 
-// bits of the value of a bin; win < 0: the short range, else window `win` of the full one
+// Position in `hist` of the bin-th largest value; win < 0: the short range, else a window of
+// the full one
+__device__ __forceinline__ int place_of(int bin, int win) {
+    if (win >= 0) return bin;
+    return bin < kSide ? kSide - 1 - bin : bin == kSide ? kZero : bin < kBins ? bin - 1 : bin;
+}
+// bits of that value
 __device__ __forceinline__ uint32_t bits_of(int bin, int win) {
     if (win < 0) return bin < kSide ? kBase + (kSide - 1 - bin) : bin == kSide ? 0u : 0x8000u | (kBase + (bin - kSide - 1));
     const uint32_t o = 65535u - (uint32_t)(win * kWindow + bin);
     return o & 0x8000u ? o ^ 0x8000u : o ^ 0xffffu;
+}
+
+// Counts elements [lo, hi) of a row and takes their maximum.
+__device__ __forceinline__ void count(Shared& S, const uint16_t* row, int64_t lo, int64_t hi, uint32_t& flags, float& top) {
+    const uint16_t* a = row + lo;
+    const int64_t n = hi - lo;
+    auto slow = [&](uint32_t b) {                // any value
+        const uint32_t mag = b & 0x7fffu, t = mag - kBase;
+        if (t < (uint32_t)kSide) atomicAdd(&S.hist[t + (b >> 15) * kSide], 1u);
+        else if (mag == 0) atomicAdd(&S.hist[kZero], 1u);
+        else flags |= why(b);
+        top = fmaxf(top, __uint_as_float(b << 16));
+    };
+    const int64_t head = min(n, (int64_t)((16 - (reinterpret_cast<uintptr_t>(a) & 15)) & 15) / 2);
+    if ((int64_t)threadIdx.x < head) slow(a[threadIdx.x]);
+    const uint4* v = reinterpret_cast<const uint4*>(a + head);
+    const int64_t nv = (n - head) / 8;
+    __nv_bfloat162 m2 = __floats2bfloat162_rn(-INFINITY, -INFINITY);
+    auto vec = [&](const uint4& x) {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t worst = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t mags = w[i] & 0x7fff7fffu;
+            const uint32_t t0 = (mags & 0xffffu) - kBase, t1 = (mags >> 16) - kBase;
+            worst = max(worst, max(t0, t1));
+            if (t0 < (uint32_t)kSide) atomicAdd(&S.hist[t0 + (w[i] >> 15 & 1) * kSide], 1u);
+            if (t1 < (uint32_t)kSide) atomicAdd(&S.hist[t1 + (w[i] >> 31) * kSide], 1u);
+            m2 = __hmax2(m2, *reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+        }
+        if (worst >= (uint32_t)kSide) {          // zeros, and what does not count
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t b = i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu, mag = b & 0x7fffu;
+                if (mag == 0) atomicAdd(&S.hist[kZero], 1u);
+                else if (mag - kBase >= (uint32_t)kSide) flags |= why(b);
+            }
+        }
+    };
+    int64_t i = threadIdx.x;
+    for (; i + 3 * kNT < nv; i += 4 * kNT) {
+        const uint4 x0 = __ldg(v + i), x1 = __ldg(v + i + kNT), x2 = __ldg(v + i + 2 * kNT), x3 = __ldg(v + i + 3 * kNT);
+        vec(x0);
+        vec(x1);
+        vec(x2);
+        vec(x3);
+    }
+    for (; i < nv; i += kNT) vec(__ldg(v + i));
+    const int64_t done = head + nv * 8;
+    if ((int64_t)threadIdx.x < n - done) slow(a[done + threadIdx.x]);
+    top = fmaxf(top, fmaxf(__low2float(m2), __high2float(m2)));
 }
 
 // Applies f(bits) to elements [lo, hi) of a row, 16 bytes at a time.
@@ -241,43 +321,78 @@ __device__ __forceinline__ T warp_scan(T x) {    // inclusive
     return x;
 }
 
-// The counts of one bin over the cluster's histograms.
+// The counts at one place over the cluster's histograms: the CTA's own, then the others'
+// (a load from another SM takes several times as long).
 struct Counts {
-    const uint32_t* h[8];
-    int n;
-    __device__ __forceinline__ uint32_t operator()(int bin) const {
-        uint32_t c = 0;
-        for (int i = 0; i < n; ++i) c += h[i][bin];
+    const uint32_t* own;
+    const uint32_t* other[7];
+    int n;               // CTAs
+    __device__ __forceinline__ uint32_t operator()(int at) const {
+        uint32_t c = own[at];
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (i + 1 < n) c += other[i][at];
         return c;
     }
 };
 
-// Weighs groups [g0, g1): count and mass of each into `to`'s arrays, and this warp's
-// share of the untempered mass.
-__device__ void weigh(const Counts& counts, int g0, int g1, int win, float top, Rate c, bool same, Shared* to,
-                      uint64_t& one) {
+// Weighs the g0-th, (g0 + step)-th, .. pair of groups: count and mass of each into `to`'s arrays, the rest into
+// `sums`, this warp's.
+__device__ __forceinline__ void weigh(const Counts& counts, int g0, int step, int win, const Weigher& W, const uint64_t* pow, Shared* to,
+                      Sums& sums) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Rate unit = {1.44269502162933349609f, 1.92596299112661746887e-8f, 1.f};   // log2(e)
-    for (int g = g0 + warp; g < g1; g += kNT / 32) {
-        const int bin = 32 * g + lane;
-        const uint32_t n = counts(bin);
-        uint32_t cn = 0;
-        uint64_t m = 0;
-        if (__any_sync(0xffffffffu, n)) {
-            if (n) {
-                const float x = __uint_as_float(bits_of(bin, win) << 16);
-                const uint64_t w = weight(x, top, c);
-                m = n * w;
-                one += same ? m : n * weight(x, top, unit);
+    // Two neighbours at a time, without branches between them: their loads, perhaps from other
+    // SMs, and the long chains of the weights overlap.  Most far from the row's usual
+    // magnitudes are empty, and neighbours together.
+    constexpr int kAhead = 2, stride = 1;
+    for (int ga = kAhead * (g0 + step * warp); ga < kGroups; ga += kAhead * step * (kNT / 32)) {
+        uint32_t n[kAhead], cn[kAhead];
+        uint64_t m[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) n[i] = ga + i * stride < kGroups ? counts(place_of(32 * (ga + i * stride) + lane, win)) : 0;
+        uint32_t some = 0;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            cn[i] = __reduce_add_sync(0xffffffffu, n[i]);
+            some |= cn[i];
+            m[i] = 0;
+        }
+        if (some) {
+            uint64_t w[kAhead], one[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const float x = __uint_as_float(bits_of(32 * (ga + i * stride) + lane, win) << 16);
+                w[i] = weight(pow, x, W.top, W.rate);
+                one[i] = W.same ? w[i] : weight(pow, x, W.top, unit);
             }
-            cn = warp_sum(n);
-            m = warp_sum(m);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                m[i] = n[i] ? n[i] * w[i] : 0;
+                sums.one += n[i] ? n[i] * one[i] : 0;
+                if (w[i] >= W.least) {
+                    sums.mass += m[i];
+                    sums.many += n[i];
+                }
+                // below 2^63: limbs of 26 bits, so that 32 of them do not overflow
+                const uint64_t l0 = __reduce_add_sync(0xffffffffu, (uint32_t)m[i] & 0x3ffffffu);
+                const uint64_t l1 = __reduce_add_sync(0xffffffffu, (uint32_t)(m[i] >> 26) & 0x3ffffffu);
+                const uint64_t l2 = __reduce_add_sync(0xffffffffu, (uint32_t)(m[i] >> 52));
+                m[i] = l0 + (l1 << 26) + (l2 << 52);
+            }
         }
         if (lane == 0) {
-            to->gcnt[g] = cn;
-            to->gmass[g] = m;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (ga + i * stride < kGroups) {
+                    to->gcnt[ga + i * stride] = cn[i];
+                    to->gmass[ga + i * stride] = m[i];
+                }
         }
     }
+    sums.one = warp_sum(sums.one);
+    sums.mass = warp_sum(sums.mass);
+    sums.many = __reduce_add_sync(0xffffffffu, sums.many);
 }
 
 // Prefix sums over the groups, starting from (cnt, mass); all threads.
@@ -326,32 +441,37 @@ __device__ void prefix(Shared& S, uint32_t cnt, uint64_t mass) {
 // The token at which the cumulated mass reaches `mass` (by_mass), or the cnt-th token:
 // its 1-based position, value bin, place among equal values, and the cumulated mass up
 // to it.  False when it lies behind this window's groups.  All threads.
-__device__ bool locate(Shared& S, const Counts& counts, int win, float top, Rate c, bool by_mass, uint64_t mass,
-                       uint32_t cnt) {
-    if (threadIdx.x == 0) S.found = -1;
-    __syncthreads();
+__device__ __forceinline__ bool locate(Shared& S, const Counts& counts, int win, const Weigher& W, bool by_mass, uint64_t mass,
+                       uint32_t cnt, int slot) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int g = threadIdx.x * kPer + i;
         if (g >= kGroups) continue;
         const bool in = by_mass ? S.pmass[g] < mass && mass <= S.pmass[g] + S.gmass[g]
                                 : S.pcnt[g] < cnt && cnt <= S.pcnt[g] + S.gcnt[g];
-        if (in) S.found = g;
+        if (in) S.found[slot] = g;
     }
     __syncthreads();
-    const int g = S.found;
+    const int g = S.found[slot];
+    if (threadIdx.x == 0) S.found[slot ^ 1] = -1;   // for the next search, a barrier away
     if (g < 0) return false;
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x, bin = 32 * g + lane;
-        const uint32_t n = counts(bin);
-        const uint64_t w = n ? weight(__uint_as_float(bits_of(bin, win) << 16), top, c) : 0;
+        const uint32_t n = counts(place_of(bin, win));
+        const uint64_t w = n ? weight(S.pow, __uint_as_float(bits_of(bin, win) << 16), W.top, W.rate) : 0;
         const uint32_t ci = warp_scan(n) + S.pcnt[g];
         const uint64_t mi = warp_scan(n * w) + S.pmass[g];
         const uint32_t cb = ci - n;
         const uint64_t mb = mi - n * w;
         const bool in = by_mass ? mb < mass && mass <= mi : cb < cnt && cnt <= ci;
         if (in) {
-            const uint32_t k = by_mass ? (uint32_t)((mass - mb + w - 1) / w) : cnt - cb;   // 1 .. n
+            uint32_t k = cnt - cb;                   // 1 .. n
+            if (by_mass) {                           // the smallest with k w >= mass - mb; n < 2^18
+                const uint64_t need = mass - mb;
+                k = min(max((uint32_t)((float)need / (float)w), 1u), n);
+                while (k * w < need) ++k;
+                while (k > 1 && (k - 1) * w >= need) --k;
+            }
             S.f_cnt = cb + k;
             S.f_mass = mb + k * w;
             S.f_bin = bin;
@@ -362,110 +482,171 @@ __device__ bool locate(Shared& S, const Counts& counts, int win, float top, Rate
     return true;
 }
 
-// First token at which the cumulated mass exceeds what the row's u asks for: cuts and
-// draw over the windows of a row.  `load(win)` puts a window's groups and prefix sums
-// (from a carry) in place.  Leader CTA, all threads; leaves the draw in S.f_bin,
-// S.f_rank and returns its window, or -1 when nothing has weight.
+// Cuts and draw over the windows of a row.  `load(win, cnt, mass)` puts a window's groups
+// and prefix sums (from a carry) in place; S.total says what min_p keeps once every window
+// has been loaded.  A cut is a number of tokens and their mass.  Leader CTA, all threads;
+// leaves the draw in S.f_bin, S.f_rank and the window in `at`; false when nothing has weight.
 template <typename Load>
-__device__ int draw(Shared& S, const Counts& counts, int first, int windows, float top, Rate c, int32_t k, float p,
-                    float min_p, float u, bool greedy, Load load) {
-    // total count and mass; the mass of the first k tokens
-    uint64_t kept = 0, all = 0;
-    uint32_t n = 0, total = 0;
-    bool cut = false;
-    if (greedy) {
-        k = 1;
-        p = 1.f;
-        min_p = 0.f;
-        u = 0.f;
-    }
-    for (int w = 0; w < windows; ++w) {
-        load(first + w, total, all);
-        if (k > 0 && !cut && locate(S, counts, first + w, top, c, false, 0, (uint32_t)k)) {
-            cut = true;
-            kept = S.f_mass;
+__device__ bool draw(Shared& S, const Counts& counts, int first, int windows, const Weigher& W, int32_t k, float p,
+                     float u, Load load, int& at) {
+    uint64_t mass = 0;
+    uint32_t total = 0;
+    int slot = 0;
+    // the search for one token, window by window
+    auto seek = [&](bool by_mass, uint64_t need, uint32_t cnt) {
+        uint32_t c = 0;
+        uint64_t m = 0;
+        for (int w = 0; w < windows; ++w) {
+            if (windows > 1) load(first + w, c, m);
+            if (locate(S, counts, first + w, W, by_mass, need, cnt, slot)) {
+                slot ^= 1;
+                at = first + w;
+                return true;
+            }
+            slot ^= 1;
+            c = S.tot_cnt;
+            m = S.tot_mass;
+            __syncthreads();
         }
+        return false;
+    };
+    for (int w = 0; w < windows; ++w) {
+        load(first + w, total, mass);
         total = S.tot_cnt;
-        all = S.tot_mass;
+        mass = S.tot_mass;
         __syncthreads();
     }
-    if (!cut) kept = all;
-    n = cut ? (uint32_t)k : total;
-    // the shortest prefix that reaches p
+    if (!mass) return false;
+    uint32_t n = total;
+    if (k > 0 && (uint32_t)k < total && seek(false, 0, (uint32_t)k)) {
+        n = (uint32_t)k;
+        mass = S.f_mass;
+    }
+    // the shortest prefix that reaches p; min_p's is known
+    const uint64_t all = mass;
     if (p < 1.f) {
         bool rest;
-        uint64_t need = times(p, kept, rest) + 0;
+        uint64_t need = times(p, all, rest);
         need = max(need + (rest ? 1 : 0), (uint64_t)1);
-        uint32_t cc = 0;
-        uint64_t mm = 0;
-        for (int w = 0; w < windows; ++w) {
-            if (windows > 1) load(first + w, cc, mm);
-            if (locate(S, counts, first + w, top, c, true, need, 0)) {
-                n = min(n, S.f_cnt);
-                break;
-            }
-            cc = S.tot_cnt;
-            mm = S.tot_mass;
-            __syncthreads();
+        if (seek(true, need, 0) && S.f_cnt < n) {
+            n = S.f_cnt;
+            mass = S.f_mass;
         }
     }
-    // tokens of weight at least min_p: the first token below it ends the prefix
-    if (min_p > 0.f) {
-        bool rest;
-        uint64_t least = times(fminf(min_p, 1.f), 1ull << kOneBits, rest);
-        least += rest ? 1 : 0;
-        uint32_t cc = 0, many = 0;
-        uint64_t mm = 0;
-        for (int w = 0; w < windows; ++w) {
-            if (windows > 1) load(first + w, cc, mm);
-            uint32_t mine = 0;
-            for (int bin = threadIdx.x; bin < kGroups * 32; bin += kNT) {
-                const uint32_t x = S.gcnt[bin / 32] ? counts(bin) : 0;
-                if (x && weight(__uint_as_float(bits_of(bin, first + w) << 16), top, c) >= least) mine += x;
-            }
-            mine = warp_sum(mine);
-            if ((threadIdx.x & 31) == 0) S.wcnt[threadIdx.x >> 5] = mine;
-            __syncthreads();
-            for (int i = 0; i < kNT / 32; ++i) many += S.wcnt[i];
-            cc = S.tot_cnt;
-            mm = S.tot_mass;
-            __syncthreads();
-        }
-        n = min(n, many);
-    }
-    // mass of the first n tokens, then the draw
-    uint64_t sum = kept;
-    if (!(cut && n == (uint32_t)k) && n < total) {
-        uint32_t cc = 0;
-        uint64_t mm = 0;
-        for (int w = 0; w < windows; ++w) {
-            if (windows > 1) load(first + w, cc, mm);
-            if (locate(S, counts, first + w, top, c, false, 0, n)) {
-                sum = S.f_mass;
-                break;
-            }
-            cc = S.tot_cnt;
-            mm = S.tot_mass;
-            __syncthreads();
+    if (W.least) {
+        if (S.total.many < n) {
+            n = S.total.many;
+            mass = S.total.mass;
         }
     }
-    if (!sum) return -1;
     bool rest;
-    uint64_t at = u < 1.f ? times(u, sum, rest) + 1 : sum;   // cumulated mass > u * sum
-    at = min(at, sum);
-    uint32_t cc = 0;
-    uint64_t mm = 0;
-    for (int w = 0; w < windows; ++w) {
-        if (windows > 1) load(first + w, cc, mm);
-        if (locate(S, counts, first + w, top, c, true, at, 0)) return first + w;
-        cc = S.tot_cnt;
-        mm = S.tot_mass;
-        __syncthreads();
-    }
-    return -1;
+    const uint64_t goal = u < 1.f ? times(u, mass, rest) + 1 : mass;   // cumulated mass > u * mass
+    return seek(true, min(goal, mass), 0);
 }
 
-__global__ void __launch_bounds__(kNT, 3) sample_kernel(const Params p) {
+// The rank-th token (from 0) of elements [a, b) of a row with bits `key` (0: also -0), of
+// `matches`, by a whole CTA.  Warps take contiguous parts, a lane eight elements at a time.
+// Few matches are listed (the histogram's place is free by now) and the rank-th smallest is
+// picked; many are counted, and the warp that has the token goes through its part again.
+constexpr uint32_t kListed = 2048;
+
+__device__ void find(Shared& S, const uint16_t* row, int a, int b, uint32_t key, uint32_t rank, uint32_t matches,
+                     int32_t* out) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // Parts begin where memory's 16-byte blocks do, so that a lane's eight elements are one
+    // load: block k holds elements 8 k - skew .. 8 k - skew + 7; blocks in0 .. in1 - 1 lie inside.
+    const int skew = (int)(reinterpret_cast<uintptr_t>(row) & 15) / 2;
+    const int first = (a + skew) / 8, blocks = (b + skew + 7) / 8 - first;
+    const int b0 = first + (int)((int64_t)blocks * warp / (kNT / 32)), b1 = first + (int)((int64_t)blocks * (warp + 1) / (kNT / 32));
+    const int in0 = (a + skew + 7) / 8, in1 = (b + skew) / 8;
+    const uint4* mem = reinterpret_cast<const uint4*>(row - skew);
+    const uint32_t other = key ? key : 0x8000u, mask = key ? 0xffffffffu : 0x7fff7fffu, twice = key | key << 16;
+    auto some_half = [&](const uint4& x) {           // of (w & mask) ^ twice is zero
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t any = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t y = (w[i] & mask) ^ twice;
+            any |= (y - 0x00010001u) & ~y;
+        }
+        return (any & 0x80008000u) != 0;
+    };
+    // bit i: element i of the block matches
+    auto exact = [&](const uint4& x) {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = w[i] & 0xffffu, hi = w[i] >> 16;
+            m |= (uint32_t)(lo == key || lo == other) << (2 * i) | (uint32_t)(hi == key || hi == other) << (2 * i + 1);
+        }
+        return m;
+    };
+    auto hits = [&](int k) {
+        uint32_t m = 0;
+        if (k >= b1) return m;
+        if (k >= in0 && k < in1) {
+            const uint4 x = __ldg(mem + k);
+            return some_half(x) ? exact(x) : 0u;
+        }
+        for (int i = 0; i < 8; ++i) {
+            const int e = 8 * k - skew + i;
+            if (e >= a && e < b) m |= (uint32_t)(row[e] == key || row[e] == other) << i;
+        }
+        return m;
+    };
+    if (matches <= kListed) {
+        auto list = [&](int k, uint32_t m) {
+            while (m) {
+                const int32_t at = 8 * k - skew + __ffs(m) - 1;
+                m &= m - 1;
+                S.hist[min(atomicAdd(&S.listed, 1u), kListed - 1)] = (uint32_t)at;
+            }
+        };
+        constexpr int kBatch = 8;                    // loads under way
+        int k = max(b0, in0) + lane;
+        if (lane == 0 && b0 < in0) list(b0, hits(b0));                       // the row's ragged ends
+        if (lane == 0 && b1 > in1 && in1 >= max(b0, in0)) list(in1, hits(in1));
+        const int end = min(b1, in1);
+        for (; k + (kBatch - 1) * 32 < end; k += kBatch * 32) {
+            uint4 x[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) x[i] = __ldg(mem + k + 32 * i);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (some_half(x[i])) list(k + 32 * i, exact(x[i]));
+        }
+        for (; k < end; k += 32) list(k, hits(k));
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < matches; i += kNT) {
+            const uint32_t mine = S.hist[i];
+            uint32_t smaller = 0;
+#pragma unroll 8
+            for (uint32_t j = 0; j < matches; ++j) smaller += S.hist[j] < mine;
+            if (smaller == rank) *out = (int32_t)mine;
+        }
+        return;
+    }
+    uint32_t n = 0;
+#pragma unroll 4
+    for (int k = b0 + lane; k < b1; k += 32) n += __popc(hits(k));
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) S.wcnt[warp] = n;
+    __syncthreads();
+    uint32_t before = 0;
+    for (int w = 0; w < warp; ++w) before += S.wcnt[w];
+    if (rank < before || rank >= before + n) return;
+    uint32_t left = rank - before;
+    for (int k = b0; k < b1; k += 32) {
+        const uint32_t m = hits(k + lane), c = __popc(m), upto = warp_scan(c);
+        if (left < upto && left >= upto - c) *out = 8 * (k + lane) - skew + (int)__fns(m, 0, (int)(left - (upto - c)) + 1);
+        const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
+        if (left < all) return;
+        left -= all;
+    }
+}
+
+__global__ void __launch_bounds__(kNT, 2) sample_kernel(const Params p) {
     extern __shared__ __align__(16) uint8_t raw[];
     Shared& S = *reinterpret_cast<Shared*>(raw);
     cg::cluster_group cluster = cg::this_cluster();
@@ -475,6 +656,7 @@ __global__ void __launch_bounds__(kNT, 3) sample_kernel(const Params p) {
     const int64_t lo = p.vocab * me / C, hi = p.vocab * (me + 1) / C;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i < kGroups * 32 / 4; i += kNT) reinterpret_cast<uint4*>(S.hist)[i] = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x < 65) S.pow[threadIdx.x] = kPow[threadIdx.x];
     grid_dep_wait();
     grid_dep_launch();
     const float T = p.s.temperatures ? p.s.temperatures[r] : p.s.temperature;
@@ -482,33 +664,39 @@ __global__ void __launch_bounds__(kNT, 3) sample_kernel(const Params p) {
     const float top_p = p.s.top_ps ? p.s.top_ps[r] : p.s.top_p;
     const float min_p = p.s.min_ps ? p.s.min_ps[r] : p.s.min_p;
     const float u = p.u[r];
+    const bool greedy = T == 0.f;
+    if (threadIdx.x == kNT - 1) {                   // once: double precision is slow
+        bool rest = false;
+        uint64_t least = 0;
+        if (min_p > 0.f && !greedy) {
+            least = times(fminf(min_p, 1.f), 1ull << kOneBits, rest);
+            least = max(least + (rest ? 1 : 0), (uint64_t)1);
+        }
+        S.weigher = {0.f, rate_of(greedy ? 1.f : T), greedy || T == 1.f, least};
+        S.found[0] = -1;
+    }
     __syncthreads();
 
     // ---- count the slice ----------------------------------------------------------
     uint32_t flags = 0;
     float top = -INFINITY;
-    each(row, lo, hi, [&](uint32_t b) {
-        const int bin = bin_of(b, flags);
-        if (bin >= 0) atomicAdd(&S.hist[bin], 1u);
-        top = fmaxf(top, __uint_as_float(b << 16));
-    });
+    count(S, row, lo, hi, flags, top);
+    flags = __reduce_or_sync(0xffffffffu, flags);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        flags |= __shfl_xor_sync(0xffffffffu, flags, o);
-    }
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) {
         S.wcnt[warp] = flags;
-        S.one[warp] = __float_as_uint(top);
+        S.wmass[warp] = __float_as_uint(top);
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kNT / 32; ++w) {
+    if ((int)threadIdx.x < C) {                    // to every CTA of the cluster
+        for (int w = 0; w < kNT / 32; ++w) {
             flags |= S.wcnt[w];
-            top = fmaxf(top, __uint_as_float((uint32_t)S.one[w]));
+            top = fmaxf(top, __uint_as_float((uint32_t)S.wmass[w]));
         }
-        S.flags = flags;
-        S.top = top;
+        Shared* to = cluster.map_shared_rank(&S, (int)threadIdx.x);
+        to->flags[me] = flags;
+        to->tops[me] = top;
     }
     cluster.sync();
 
@@ -518,26 +706,27 @@ __global__ void __launch_bounds__(kNT, 3) sample_kernel(const Params p) {
     flags = 0;
     top = -INFINITY;
     for (int i = 0; i < C; ++i) {
-        const Shared* other = cluster.map_shared_rank(&S, i);
-        counts.h[i] = other->hist;
-        flags |= other->flags;
-        top = fmaxf(top, other->top);
+        flags |= S.flags[i];
+        top = fmaxf(top, S.tops[i]);
     }
+#pragma unroll
+    for (int i = 0; i < 7; ++i) counts.other[i] = cluster.map_shared_rank(&S, i + 1 < C ? (me + i + 1) & (C - 1) : 0)->hist;
+    counts.own = S.hist;
     top += 0.f;                                     // -0 counts as 0
     const bool bad_params = !(T >= 0.f) || isinf(T) || top_p != top_p || min_p != min_p || u != u;
     const bool bad = bad_params || (flags & kNaN) || isinf(top);
-    const bool greedy = T == 0.f;
     // Values below -2^16 have no weight beside a maximum of at least -2^15 when
     // 2^15 / T is above 46 ln 2.
     const bool slow = (flags & kRare) || ((flags & kLow) && !(top >= -32768.f && T <= 512.f));
-    const Rate c = rate_of(greedy ? 1.f : T);
-    const bool same = greedy || T == 1.f;
+    Weigher W = S.weigher;
+    W.top = top;
 
     Shared* leader = cluster.map_shared_rank(&S, 0);
-    uint64_t one = 0;
-    if (!bad && !slow) weigh(counts, kGroups * me / C, kGroups * (me + 1) / C, -1, top, c, same, leader, one);
-    one = warp_sum(one);
-    if (lane == 0) S.one[warp] = one;
+    Sums sums = {0, 0, 0};
+    if (!bad && !slow) {
+        weigh(counts, me, C, -1, W, S.pow, leader, sums);
+        if (lane == 0) leader->sums[me][warp] = sums;
+    }
     cluster.sync();
 
     if (me == 0) {
@@ -545,46 +734,50 @@ __global__ void __launch_bounds__(kNT, 3) sample_kernel(const Params p) {
         bool drawn = false;
         uint32_t rank = 0;
         uint64_t one_all = 0;
-        if (!bad && !slow) {
-            for (int i = 0; i < C; ++i) {
-                const Shared* other = cluster.map_shared_rank(&S, i);
-                for (int w = 0; w < kNT / 32; ++w) one_all += other->one[w];
+        // S.total: the sums of `n` CTAs, by the first warp; all threads wait for it later
+        auto totals = [&](int n) {
+            if (threadIdx.x >= 32) return;
+            Sums t = {0, 0, 0};
+            for (int i = lane; i < n * (kNT / 32); i += 32) {
+                const Sums& x = S.sums[i / (kNT / 32)][i % (kNT / 32)];
+                t = {t.one + x.one, t.mass + x.mass, t.many + x.many};
             }
-            prefix(S, 0, 0);
-            win = draw(S, counts, -1, 1, top, c, k, top_p, min_p, u, greedy,
-                       [&](int, uint32_t, uint64_t) {});
-            drawn = true;
-        } else if (!bad) {
-            // the full range, window by window, counted by this CTA alone
-            counts.n = 1;
-            bool first = true;
-            uint64_t sum = 0;
-            auto load = [&](int w, uint32_t cnt, uint64_t mass) {
-                __syncthreads();
-                for (int i = threadIdx.x; i < kGroups * 32; i += kNT) S.hist[i] = 0;
-                __syncthreads();
-                each(row, 0, p.vocab, [&](uint32_t b) {
-                    b = b == 0x8000u ? 0u : b;
-                    const uint32_t o = 65535u - (b & 0x8000u ? b ^ 0xffffu : b ^ 0x8000u);
-                    const uint32_t at = o - (uint32_t)(w * kWindow);
-                    if (at < (uint32_t)kWindow && b != 0xff80u) atomicAdd(&S.hist[at], 1u);
-                });
-                __syncthreads();
-                uint64_t part = 0;
-                weigh(counts, 0, kGroups, w, top, c, same, &S, part);
-                if (first) {
-                    sum += part;
-                    first = w + 1 < kWindows;
-                }
-                __syncthreads();
-                prefix(S, cnt, mass);
-            };
-            win = draw(S, counts, 0, kWindows, top, c, k, top_p, min_p, u, greedy, load);
-            drawn = win >= 0;
-            sum = warp_sum(sum);
-            if (lane == 0) S.one[warp] = sum;
-            __syncthreads();
-            for (int w = 0; w < kNT / 32; ++w) one_all += S.one[w];
+            t = {warp_sum(t.one), warp_sum(t.mass), __reduce_add_sync(0xffffffffu, t.many)};
+            if (lane == 0) S.total = t;
+        };
+        if (!bad) {
+            const int32_t kk = greedy ? 1 : k;
+            const float pp = greedy ? 1.f : top_p, uu = greedy ? 0.f : u;
+            if (!slow) {
+                totals(C);
+                drawn = draw(S, counts, -1, 1, W, kk, pp, uu, [&](int, uint32_t, uint64_t) { prefix(S, 0, 0); }, win);
+            } else {
+                // the full range, window by window, counted by this CTA alone
+                counts.n = 1;
+                int seen = 0;
+                sums = {0, 0, 0};
+                auto load = [&](int w, uint32_t cnt, uint64_t mass) {
+                    __syncthreads();
+                    for (int i = threadIdx.x; i < kGroups * 32; i += kNT) S.hist[i] = 0;
+                    __syncthreads();
+                    each(row, 0, p.vocab, [&](uint32_t b) {
+                        b = b == 0x8000u ? 0u : b;
+                        const uint32_t o = 65535u - (b & 0x8000u ? b ^ 0xffffu : b ^ 0x8000u);
+                        const uint32_t at = o - (uint32_t)(w * kWindow);
+                        if (at < (uint32_t)kWindow && b != 0xff80u) atomicAdd(&S.hist[at], 1u);
+                    });
+                    __syncthreads();
+                    Sums part = {0, 0, 0};
+                    weigh(counts, 0, 1, w, W, S.pow, &S, part);
+                    if (seen++ < kWindows) sums = {sums.one + part.one, sums.mass + part.mass, sums.many + part.many};
+                    if (lane == 0) S.sums[0][warp] = sums;
+                    __syncthreads();
+                    totals(1);
+                    prefix(S, cnt, mass);
+                };
+                drawn = draw(S, counts, 0, kWindows, W, kk, pp, uu, load, win);
+            }
+            one_all = S.total.one;
         }
         if (drawn) {
             key = (int)bits_of(S.f_bin, win);
@@ -599,13 +792,28 @@ __global__ void __launch_bounds__(kNT, 3) sample_kernel(const Params p) {
                                         : (x - top) - log1pf((float)(one_all - (1ull << kOneBits)) * 0x1p-45f);
             }
             // the slice that holds the rank-th token of this value
-            uint32_t owner = 0;
-            if (key >= 0 && win < 0)
-                while (owner + 1 < (uint32_t)C && rank >= counts.h[owner][S.f_bin]) rank -= counts.h[owner++][S.f_bin];
+            uint32_t owner = 0, matches = kListed + 1;   // the full range: many, for all it is known
+            if (key >= 0 && win < 0) {
+                const int at = place_of(S.f_bin, -1);
+                uint32_t c[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) c[i] = i == 0 ? S.hist[at] : i < C ? counts.other[i - 1][at] : 0;
+#pragma unroll
+                for (int i = 0; i < 7; ++i)
+                    if ((int)owner == i && i + 1 < C && rank >= c[i]) {
+                        rank -= c[i];
+                        ++owner;
+                    }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if ((int)owner == i) matches = c[i];
+            }
             for (int i = 0; i < C; ++i) {
                 Shared* to = cluster.map_shared_rank(&S, i);
                 to->key = key;
                 to->rank = rank;
+                to->matches = matches;
+                to->listed = 0;
                 to->owner = win < 0 ? owner : 0xffffffffu;
             }
         }
@@ -616,31 +824,7 @@ __global__ void __launch_bounds__(kNT, 3) sample_kernel(const Params p) {
     const int key = S.key;
     const bool whole = S.owner == 0xffffffffu;      // the leader searches the whole row
     if (key < 0 || (whole ? me != 0 : (int)S.owner != me)) return;
-    const int64_t a = whole ? 0 : lo, b = whole ? p.vocab : hi;
-    // warps take contiguous parts; a warp's matches, then the place inside the warp's part
-    const int64_t s0 = a + (b - a) * warp / (kNT / 32), s1 = a + (b - a) * (warp + 1) / (kNT / 32);
-    auto hit = [&](int64_t i) {
-        const uint32_t x = i < s1 ? row[i] : 0xffffffffu;
-        return i < s1 && (x == (uint32_t)key || (key == 0 && x == 0x8000u));
-    };
-    uint32_t n = 0;
-    for (int64_t i = s0 + lane; i < s1; i += 32) n += hit(i);
-    n = warp_sum(n);
-    if (lane == 0) S.wcnt[warp] = n;
-    __syncthreads();
-    uint32_t before = 0;
-    for (int w = 0; w < warp; ++w) before += S.wcnt[w];
-    const uint32_t want = S.rank;
-    if (want < before || want >= before + n) return;
-    uint32_t left = want - before;
-    for (int64_t i = s0; i < s1; i += 32) {
-        const uint32_t m = __ballot_sync(0xffffffffu, hit(i + lane));
-        if (left < (uint32_t)__popc(m)) {
-            if (lane == (int)__fns(m, 0, (int)left + 1)) p.tokens[r] = (int32_t)(i + lane);
-            return;
-        }
-        left -= __popc(m);
-    }
+    find(S, row, whole ? 0 : (int)lo, whole ? (int)p.vocab : (int)hi, (uint32_t)key, S.rank, S.matches, p.tokens + r);
 }
 
 }  // namespace
@@ -663,9 +847,20 @@ extern "C" int tree_attn_sample(const void* logits, int64_t row_stride, int64_t 
     int dev, *status;
     int st;
     if ((st = current_device(&dev)) || (st = get_status_ptr(dev, &status))) return st;
-    // CTAs per row: enough to fill the 152 SMs, at least 4,096 logits each
-    int C = 8;
-    while (C > 1 && (n_rows * C > 152 * 4 || vocab < 4096 * (int64_t)C)) C /= 2;
+    // CTAs per row.  A CTA takes about 14 thousand cycles whatever its slice (barriers, the
+    // chain of searches), 60 thousand more for a row of 152,064 alone; two fit an SM.  Measured
+    // at 152,064: 1 row, 8 CTAs 16 us, 1 CTA 43; 64 rows, 4 CTAs 28, 8 CTAs 42, 1 CTA 50; 512
+    // rows, 1 CTA 127, 4 CTAs 165.  At least 4,096 logits each.
+    int C = 1;
+    double best = 0;
+    for (int c = 1; c <= 8; c *= 2) {
+        if (c > 1 && vocab < 4096 * (int64_t)c) break;
+        const double t = (double)((n_rows * c + 303) / 304) * (14 + 60 * (vocab / 152064.0) / c);
+        if (c == 1 || t < best) {
+            C = c;
+            best = t;
+        }
+    }
     if (n_rows * C > INT32_MAX) return TREE_ATTN_ERR_TOO_LARGE;
     static std::once_flag once[kMaxDevices];
     static cudaError_t attr[kMaxDevices];
