@@ -14,7 +14,9 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <functional>
 #include <new>
+#include <queue>
 
 #include "decode.h"
 
@@ -24,7 +26,11 @@ namespace {
 
 constexpr int64_t kMaxCombine = (int64_t)1 << 27;
 // CTAs of the attention that run at one time: two per SM
-constexpr int64_t kSlots = 152 * 2;
+constexpr int32_t kSms = 152;
+constexpr int64_t kSlots = kSms * 2;
+// Cycles of a CTA besides its pages; of a page of a CTA's item, and of a warp's, in a CTA
+// that shares its SM with one of the other kind.
+constexpr int64_t kCtaStart = 9000, kCtaPageCycles = 2100, kWarpPageCycles = 4700;
 // Time of a page in a warp's item, in times of a page in a CTA's item: 1.2 us against
 // 0.75 us alone on an SM, 4.8 us against 1.4 us with every slot taken.
 constexpr int64_t kWarpPage = 2;
@@ -211,24 +217,33 @@ int build(const int32_t* parent, const int32_t* seg_len, const int32_t* capacity
             }
     }
     P->part_rows = part;
-    // Slots of kDecodeWarps items per CTA.  Each kind's longest first, so that the tail of
-    // the launch is made of short ones; the kinds in proportion to their cost, so that
-    // CTAs bound by instructions and CTAs bound by HBM share the SMs all along.  Warps of
-    // one CTA get items of like length.
+    // Slots of kDecodeWarps items per CTA.  Warps of one CTA get items of like length.
+    //
+    // Launch order.  A CTA of warps' items alone on an SM already draws its share of HBM, a
+    // CTA's item is bound by shared memory, so an SM should hold one of each: the first
+    // kSms CTAs launched land on different SMs, the next kSms beside them, and then each goes
+    // where one has ended.  A simulation of that launch, each kind keeping to its own half of
+    // the slots while it lasts, longest first, gives the order.  (Long context, 48 pages an
+    // item: one kind after the other 224 us, mixed at random 222, this way 178.)
     auto longer = [](const Item& a, const Item& b) { return a.n > b.n; };
     std::stable_sort(warps.begin(), warps.end(), longer);
     std::stable_sort(ctas.begin(), ctas.end(), longer);
     size_t w = 0, t = 0;
     auto put = [&](const Item& x) { P->items.insert(P->items.end(), {x.e0, x.n, x.g0, x.g1, x.part, x.wide, 0, 0}); };
     const Item none = {0, 0, 0, 0, 0, 0};
-    int64_t warp_cost = 0, cta_cost = 0, warp_done = 0, cta_done = 0;   // of each kind: all, and placed
-    for (size_t i = 0; i < warps.size(); i += kDecodeWarps) warp_cost += warps[i].n * kWarpPage;
-    for (const Item& x : ctas) cta_cost += x.n;
+    using Heap = std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>>;
+    Heap free_at[2];                                   // of the slots meant for warps' items, for CTAs' items
+    for (int k = 0; k < 2; ++k)
+        for (int32_t i = 0; i < kSms; ++i) free_at[k].push(0);
     while (w < warps.size() || t < ctas.size()) {
-        const bool wide = w >= warps.size() ||
-                          (t < ctas.size() && (double)cta_done * warp_cost <= (double)warp_done * cta_cost);
-        if (wide) cta_done += ctas[t].n;
-        else warp_done += warps[w].n * kWarpPage;
+        const int half = free_at[1].top() <= free_at[0].top() ? 1 : 0;
+        const bool wide = w >= warps.size() || (half == 1 && t < ctas.size());
+        const int64_t cycles = wide ? kCtaStart + ctas[t].n * kCtaPageCycles : kCtaStart + warps[w].n * kWarpPageCycles;
+        for (int32_t h = 0; h < P->hkv; ++h) {
+            const int64_t at = free_at[half].top();
+            free_at[half].pop();
+            free_at[half].push(at + cycles);
+        }
         for (int32_t i = 0; i < kDecodeWarps; ++i) {
             if (wide) put(i == 0 ? ctas[t] : none);
             else put(w < warps.size() ? warps[w++] : none);
