@@ -103,6 +103,11 @@ __device__ __forceinline__ void lds128(const uint8_t* at, uint32_t (&w)[4]) {
     w[2] = x.z;
     w[3] = x.w;
 }
+// The same, kept in program order: several are to be under way before the first is used.
+__device__ __forceinline__ void lds128_now(const uint8_t* at, uint32_t (&w)[4]) {
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(smem_u32(at)));
+}
 // four e4m3 codes to two f16 pairs
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
@@ -672,7 +677,7 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, cons
             for (int u = 0; u < kRounds; ++u) {
                 int r, y, c;
                 place(u, r, y, c);
-                if (ct + 96 * u < 4 * D) lds128(D == 128 ? from + sw128_offset(r, 4 * y + c) : from + r * 64 + c * 16, w[u]);
+                if (ct + 96 * u < 4 * D) lds128_now(D == 128 ? from + sw128_offset(r, 4 * y + c) : from + r * 64 + c * 16, w[u]);
             }
 #pragma unroll
             for (int u = 0; u < kRounds; ++u) {
@@ -700,7 +705,7 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, cons
             uint32_t w[kRounds][4];
 #pragma unroll
             for (int u = 0; u < kRounds; ++u)
-                if (ct + 96 * u < 4 * D) lds128(from + (ct + 96 * u) * 16, w[u]);
+                if (ct + 96 * u < 4 * D) lds128_now(from + (ct + 96 * u) * 16, w[u]);
             if (valid < kPage) {       // what is behind the last token may be anything, NaN included
 #pragma unroll
                 for (int u = 0; u < kRounds; ++u)
