@@ -5,21 +5,25 @@
 // the heads that share a kv-head), of one kv-head; pages of a shared prefix are read
 // once for all the rows of a block.  Pages (K and V of one kv-head, 64 * d bytes each)
 // come by bulk copies into shared memory, refilled by whoever emptied it.  An item
-// leaves partial rows (O in fp32, M, l), which a second kernel joins per query.
+// leaves partial rows (O in fp32, M, m, l), which a second kernel joins per query.
 //
 // Per page, with fp32 accumulation on the tensor cores:
 //   S = Q K8^T        Q in f16; K8 the page's codes in f16 (exact: e4m3 values)
-//   x = S * (softmax_scale * log2(e) * k_scale * row factor) + log2(v_scale)
-//   P = 2^(12 + x - M),  M a running reference,   O += P V8,   l += rowsum(P) / v_scale
-// Folding log2(v_scale) into the exponent makes P the weight of the page's
-// *codes*, so one accumulator serves pages of different scales.  M follows the row's
-// maximum of x but is moved only when that passes M + 3.5: O is then rescaled, which
-// random logits ask for on the first pages only.  The largest weight so lies in
-// [2^12, 2^15.5] whatever the scales (f16 ends at 2^16): P rounds by 2^-11, and what
-// falls below f16's normal numbers by at most 2^-37 of the largest weight.  The query
-// row is brought to [1, 2) by a power of two before its rounding to f16: 11 bits hold
-// bf16's 8, and what falls below 2^-14 of the row's largest value loses at most
-// 2^-25 of it.  l sums the unrounded fp32 weights.
+//   s = S * (softmax_scale * log2(e) * k_scale * row factor),   x = s + log2(v_scale)
+//   P = 2^(12 + x - M),   O += P V8,   l += sum_j 2^(12 + s_j - m)
+// Folding log2(v_scale) into the exponent makes P the weight of the page's *codes*, so
+// one accumulator serves pages of different scales; M is a running reference of x, m one
+// of s.  They follow the row's maxima but are moved only when those pass them by 3.5: O
+// (l) is then rescaled, which random logits ask for on the first pages only.  The largest
+// weight so lies in [2^12, 2^15.5] whatever the scales (f16 ends at 2^16): P rounds by
+// 2^-11, and what falls below f16's normal numbers by at most 2^-37 of the largest weight.
+// l's terms are the unrounded P times 2^(M - log2(v_scale) - m), a factor per page; where
+// a page's values are so small beside another's that its P vanish (a factor above 2^64),
+// they are taken from s.  (With l on M's scale too, 65,536 keys of zero values -- scale
+// 2^-100 -- pass fp32's range.)  Exponents are one multiply-add of the raw product, whose
+// addend 12 + log2(v_scale) - M is small for the terms that count.  The query row is
+// brought to [1, 2) by a power of two before its rounding to f16: 11 bits hold bf16's 8,
+// and what falls below 2^-14 of the row's largest value loses at most 2^-25 of it.
 //
 // Two bodies, by the item's rows:
 //
@@ -32,22 +36,26 @@
 // The products run transposed, S^T = K Q^T and O^T = V^T P^T, with m16n8k16: the codes
 // are the 16-row operand and the 8 columns are the query rows, so no half of the tensor
 // product is padding (rows as the 16-row operand, which a leaf of 8 rows half
-// fills, took 2.4 times the instructions).  Fragments come straight from the pages:
+// fills, took twice the instructions).  Fragments come straight from the pages:
 // the order of k is free as long as both operands agree, so lane t of a quad takes
 // features 32t .. 32t+31 of a key (two 16-byte loads for d = 128) and keys 16t .. 16t+15
 // of a value feature (one).  P^T changes from accumulator to operand layout by
 // 8x8 transposes (movmatrix).
 //
-// 9 to 128 rows (shared prefixes) -- `wide`, bound by instruction issue: the same
-// pages would cost a leaf's instructions once per 8 rows.  The codes are expanded
-// once per page to f16 tiles in shared memory and the products are tcgen05.mma with
+// 9 to 128 rows (shared prefixes) -- `wide`, bound by shared memory: the same pages
+// would cost a leaf's instructions once per 8 rows.  The codes are expanded once per
+// page to f16 tiles in shared memory and the products are tcgen05.mma with
 // M = 128 rows, accumulators in TMEM, P written back over S as the second product's
 // operand.  Four warps do the softmax (one row per thread), three expand, one issues
 // products and copies: no step of a page waits for another page's.  (With the four
 // non-softmax warps taking turns at expanding and one of them issuing, a page took 3,300
-// cycles of its CTA, half of them barriers and issue.)
+// cycles of its CTA, half of them barriers and issue.)  A page of d = 128 takes 1,450
+// cycles of an SM with two CTAs on it, 1,700 to 2,100 with one: the products read 512
+// cycles' worth of shared memory at 128 bytes each, expanding reads and writes 700, the
+// copies write 128.
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 
 #include "decode.h"
@@ -63,6 +71,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLift = 12.f;                    // log2 of the weight of x = M
 constexpr float kSlack = 3.5f;                   // how far x may pass M before M is moved
+constexpr float kFar = 64.f;                     // beyond 2^kFar, l's terms are not taken from the P
+
+__device__ __forceinline__ float finite(float reference) { return reference == -INFINITY ? 0.f : reference; }
 
 struct DecodeParams {
     const int32_t* entries;
@@ -76,7 +87,7 @@ struct DecodeParams {
     const float* ks;
     const float* vs;
     float* part_o;       // [hkv, part_rows, d]
-    float2* part_ml;     // [hkv, part_rows] {M, l}
+    float4* part_ml;     // [hkv, part_rows] {M, m, l, 0}
     int64_t part_rows;
     int32_t hkv, group, n_sub, gsub;
     float scale_log2;
@@ -90,7 +101,7 @@ struct CombineParams {
     uint16_t* o;
     float* lse;
     const float* part_o;
-    const float2* part_ml;
+    const float4* part_ml;
     int64_t part_rows;
     int32_t R, hq, hkv, group, n_sub, gsub, live;
 };
@@ -179,7 +190,7 @@ struct Meta {
     int32_t count[kDecodeMaxChunk / 32];
     int32_t early;                    // the first halves are on their way
     uint32_t tmem;
-    float top[128], sum[128], qf[128];
+    float top[128], mass_top[128], sum[128], qf[128];
 };
 // Narrow items: a warp's barriers for K and V.
 struct Pair {
@@ -311,7 +322,7 @@ __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Pair& bar, 
     const float qf0 = __shfl_sync(0xffffffffu, qf, 8 * t), qf1 = __shfl_sync(0xffffffffu, qf, 8 * t + 4);
 
     float acc[D / 16][4];
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, n0 = -INFINITY, n1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // M, m, l
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -366,16 +377,15 @@ __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Pair& bar, 
         const int next = __shfl_sync(0xffffffffu, e.page, max(after, 0));
         if (lane == 0 && after >= 0) load_k(next);
         const float lv = __shfl_sync(0xffffffffu, f.lv, i), kf = __shfl_sync(0xffffffffu, f.kf, i);
-        const float f0 = kf * qf0, f1 = kf * qf1;
+        // (a factor below fp32's normal numbers leaves no score above 2^-109: never 0, or NaN)
+        const float f0 = fmaxf(kf * qf0, FLT_MIN), f1 = fmaxf(kf * qf1, FLT_MIN);
         float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
             const int key = 16 * (g >> 1) + 4 * x + (g & 1);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                c[x][j] = (j & 1 ? f1 : f0) * c[x][j] + lv;
+            for (int j = 0; j < 4; ++j)
                 if (valid < kPage && key + (j & 2) >= valid) c[x][j] = -INFINITY;
-            }
             top0 = fmax3(top0, c[x][0], c[x][2]);
             top1 = fmax3(top1, c[x][1], c[x][3]);
         }
@@ -384,11 +394,14 @@ __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Pair& bar, 
             top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, o));
             top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, o));
         }
-        const bool up0 = top0 > m0 + kSlack, up1 = top1 > m1 + kSlack;
-        if (__any_sync(0xffffffffu, up0 || up1)) {
-            const float a0 = up0 ? fast_exp2(m0 - top0) : 1.f, a1 = up1 ? fast_exp2(m1 - top1) : 1.f;
-            l0 *= a0;
-            l1 *= a1;
+        top0 *= f0;
+        top1 *= f1;
+        const bool up0 = top0 + lv > m0 + kSlack, up1 = top1 + lv > m1 + kSlack;
+        const bool un0 = top0 > n0 + kSlack, un1 = top1 > n1 + kSlack;
+        if (__any_sync(0xffffffffu, up0 || up1 || un0 || un1)) {
+            const float a0 = up0 ? fast_exp2(m0 - (top0 + lv)) : 1.f, a1 = up1 ? fast_exp2(m1 - (top1 + lv)) : 1.f;
+            l0 *= un0 ? fast_exp2(n0 - top0) : 1.f;
+            l1 *= un1 ? fast_exp2(n1 - top1) : 1.f;
 #pragma unroll
             for (int y = 0; y < D / 16; ++y) {
                 acc[y][0] *= a0;
@@ -396,24 +409,35 @@ __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Pair& bar, 
                 acc[y][2] *= a0;
                 acc[y][3] *= a1;
             }
-            m0 = up0 ? top0 : m0;
-            m1 = up1 ? top1 : m1;
+            m0 = up0 ? top0 + lv : m0;
+            m1 = up1 ? top1 + lv : m1;
+            n0 = un0 ? top0 : n0;
+            n1 = un1 ? top1 : n1;
         }
-        const float r0 = m0 == -INFINITY ? 0.f : m0 - kLift, r1 = m1 == -INFINITY ? 0.f : m1 - kLift;
-        float s0 = 0.f, s1 = 0.f;
+        const float r0 = m0 == -INFINITY ? 0.f : m0 - lv, r1 = m1 == -INFINITY ? 0.f : m1 - lv;
+        const float d0 = r0 - finite(n0), d1 = r1 - finite(n1), e0 = kLift - r0, e1 = kLift - r1;
+        float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
+        const bool far = __any_sync(0xffffffffu, d0 > kFar || d1 > kFar);
+        if (far) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float g0 = kLift - finite(n0), g1 = kLift - finite(n1);
+                t0 += fast_exp2(fmaf(c[x][0], f0, g0)) + fast_exp2(fmaf(c[x][2], f0, g0));
+                t1 += fast_exp2(fmaf(c[x][1], f1, g1)) + fast_exp2(fmaf(c[x][3], f1, g1));
+            }
+        }
         uint32_t pb[4][2];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            const float p0 = fast_exp2(c[x][0] - r0), p1 = fast_exp2(c[x][1] - r1);
-            const float p2 = fast_exp2(c[x][2] - r0), p3 = fast_exp2(c[x][3] - r1);
+            const float p0 = fast_exp2(fmaf(c[x][0], f0, e0)), p1 = fast_exp2(fmaf(c[x][1], f1, e1));
+            const float p2 = fast_exp2(fmaf(c[x][2], f0, e0)), p3 = fast_exp2(fmaf(c[x][3], f1, e1));
             s0 += p0 + p2;
             s1 += p1 + p3;
             pb[x][0] = transpose8(pack_f16(p0, p1));
             pb[x][1] = transpose8(pack_f16(p2, p3));
         }
-        const float iv = fast_exp2(-lv);
-        l0 += s0 * iv;
-        l1 += s1 * iv;
+        l0 += d0 > kFar ? t0 : s0 * fast_exp2(d0);
+        l1 += d1 > kFar ? t1 : s1 * fast_exp2(d1);
         // what is behind the last token may be anything, NaN included
         uint32_t keep[4];
 #pragma unroll
@@ -458,7 +482,7 @@ __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Pair& bar, 
     const int64_t at = R.h * p.part_rows + part + 2 * t;
     float* o = p.part_o + at * D + g;
     if (2 * t < R.rows) {
-        if (g == 0) p.part_ml[at] = make_float2(m0, l0);
+        if (g == 0) p.part_ml[at] = make_float4(m0, n0, l0, 0.f);
 #pragma unroll
         for (int y = 0; y < D / 16; ++y) {
             o[16 * y] = acc[y][0];
@@ -466,7 +490,7 @@ __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Pair& bar, 
         }
     }
     if (2 * t + 1 < R.rows) {
-        if (g == 0) p.part_ml[at + 1] = make_float2(m1, l1);
+        if (g == 0) p.part_ml[at + 1] = make_float4(m1, n1, l1, 0.f);
 #pragma unroll
         for (int y = 0; y < D / 16; ++y) {
             o[D + 16 * y] = acc[y][1];
@@ -600,7 +624,7 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, cons
     const uint32_t tmem = M.tmem;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t o_col = tmem + 128;                          // S tiles at columns 0 and 64, O from 128
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, mn = -INFINITY, l = 0.f;               // M, m, l
     bool ok = true;
     if (warp == 4) {
         // --------------------------- products and copies ---------------------------
@@ -727,7 +751,7 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, cons
         for (int i = 0; i < n; ++i) {
             const uint32_t s_col = tmem + 64 * (i & 1) + lanes;
             const int valid = M.valid[i];
-            const float lv = M.lv[i], f = M.kf[i] * qf;
+            const float lv = M.lv[i], f = fmaxf(M.kf[i] * qf, FLT_MIN);
             ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&M.s_done[i & 1]), (i / 2) & 1, p.status, 309));
             if (!ok) break;
             tc_fence_after();
@@ -735,9 +759,6 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, cons
             tmem_ld32(s_col, *reinterpret_cast<float(*)[32]>(&c[0]));
             tmem_ld32(s_col + 32, *reinterpret_cast<float(*)[32]>(&c[32]));
             tmem_wait_ld();
-            const uint64_t f2 = f32x2(f, f), lv2 = f32x2(lv, lv);
-#pragma unroll
-            for (int j = 0; j < 64; j += 2) f32x2_split(fma_f32x2(f32x2(c[j], c[j + 1]), f2, lv2), c[j], c[j + 1]);
             if (valid < kPage) {
 #pragma unroll
                 for (int j = 0; j < 64; ++j)
@@ -746,7 +767,13 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, cons
             float top = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 64; j += 2) top = fmax3(top, c[j], c[j + 1]);
-            const bool up = top > m + kSlack;
+            const float score = top * f;
+            top = score + lv;
+            const bool up = top > m + kSlack, un = score > mn + kSlack;
+            if (__any_sync(0xffffffffu, un)) {
+                l *= un ? fast_exp2(mn - score) : 1.f;
+                mn = un ? score : mn;
+            }
             if (__any_sync(0xffffffffu, up)) {
                 const float a = up ? fast_exp2(m - top) : 1.f;
                 if (i > 0) {
@@ -765,19 +792,23 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, cons
                     }
                     tmem_wait_st();
                 }
-                l *= a;
                 m = up ? top : m;
             }
-            const float base = m == -INFINITY ? 0.f : m - kLift;
+            const float ref = m == -INFINITY ? 0.f : m - lv, d = ref - finite(mn);
+            const uint64_t f2 = f32x2(f, f), e2 = f32x2(kLift - ref, kLift - ref);
             uint64_t sum = f32x2(0.f, 0.f);
-            const uint64_t one2 = f32x2(1.f, 1.f), nb2 = f32x2(-base, -base);
+            float far = 0.f;
+            if (__any_sync(0xffffffffu, d > kFar)) {
+#pragma unroll
+                for (int j = 0; j < 64; ++j) far += fast_exp2(fmaf(c[j], f, kLift - finite(mn)));
+            }
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 uint32_t pw[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     float a, b;
-                    f32x2_split(fma_f32x2(f32x2(c[32 * x + 2 * j], c[32 * x + 2 * j + 1]), one2, nb2), a, b);
+                    f32x2_split(fma_f32x2(f32x2(c[32 * x + 2 * j], c[32 * x + 2 * j + 1]), f2, e2), a, b);
                     a = fast_exp2(a);
                     b = fast_exp2(b);
                     sum = add_f32x2(sum, f32x2(a, b));
@@ -787,12 +818,13 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, cons
             }
             float sa, sb;
             f32x2_split(sum, sa, sb);
-            l += (sa + sb) * fast_exp2(-lv);
+            l += d > kFar ? far : (sa + sb) * fast_exp2(d);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(smem_u32(&M.p_full[i & 1]));
         }
         M.top[row] = m;
+        M.mass_top[row] = mn;
         M.sum[row] = l;
         if (n > 0 && ok) ok = mbar_wait(smem_u32(&M.o_done), (n - 1) & 1, p.status, 311);
     }
@@ -807,12 +839,10 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, cons
     }
     tc_fence_after();
     const int half = warp >> 2;                                 // columns D / 2 * half ..
-    m = M.top[row];
-    l = M.sum[row];
     int place, out_head;
     const bool live = R.at(row, place, out_head);
     const int64_t at = R.h * p.part_rows + part + row;
-    if (live && half == 0) p.part_ml[at] = make_float2(m, l);
+    if (live && half == 0) p.part_ml[at] = make_float4(M.top[row], M.mass_top[row], M.sum[row], 0.f);
 #pragma unroll
     for (int x = 0; x < D / 64; ++x) {
         const int col = half * (D / 2) + 32 * x;
@@ -926,23 +956,27 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
     grid_dep_launch();
     if (w >= (int64_t)p.live * p.hq) return;
     const int64_t base = h * p.part_rows + off;
-    float top = -INFINITY, l = 0.f, o[PL];
+    float top = -INFINITY, mtop = -INFINITY, l = 0.f, o[PL];
 #pragma unroll
     for (int j = 0; j < PL; ++j) o[j] = 0.f;
     for (int b = c0; b < c1; b += 32) {
         if (b > c0) mine = b + lane < c1 ? p.row[b + lane] : 0;
         const int k = min(32, c1 - b);
-        const float2 ml = lane < k ? p.part_ml[base + mine] : make_float2(-INFINITY, 0.f);
-        float t = ml.x;
+        const float4 ml = lane < k ? p.part_ml[base + mine] : make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+        float t = ml.x, u = ml.y;
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
+        for (int x = 16; x > 0; x >>= 1) {
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
+            u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, x));
+        }
         t = fmaxf(t, top);
-        const float ref = t == -INFINITY ? 0.f : t;
-        const float again = fast_exp2(top - ref), f = fast_exp2(ml.x - ref);
-        l = l * again + f * ml.y;                                              // this lane's parts
+        u = fmaxf(u, mtop);
+        const float again = fast_exp2(top - finite(t)), f = fast_exp2(ml.x - finite(t));
+        l = l * fast_exp2(mtop - finite(u)) + fast_exp2(ml.y - finite(u)) * ml.z;     // this lane's parts
 #pragma unroll
         for (int j = 0; j < PL; ++j) o[j] *= again;
         top = t;
+        mtop = u;
 #pragma unroll 4
         for (int c = 0; c < k; ++c) {
             const int64_t at = base + __shfl_sync(0xffffffffu, mine, c);
@@ -962,11 +996,12 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
     }
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    // the two references differ by about log2 of a page's scale
+    const float inv = l == 0.f ? 0.f : 1.f / l, back = fast_exp2(finite(top) - finite(mtop));
     uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (qi * p.hq + head) * D) + lane * (PL / 2);
 #pragma unroll
-    for (int j = 0; j < PL / 2; ++j) dst[j] = pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
-    if (lane == 0) p.lse[(int64_t)head * p.R + qi] = out_lse(top, l);
+    for (int j = 0; j < PL / 2; ++j) dst[j] = pack_bf16x2(o[2 * j] * inv * back, o[2 * j + 1] * inv * back);
+    if (lane == 0) p.lse[(int64_t)head * p.R + qi] = out_lse(mtop, l);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -1024,7 +1059,7 @@ extern "C" int tree_attn_decode(tree_decode_plan_t P, const int32_t* lens, const
     CUtensorMap tk = {};
     if (P->d == 128 && (st = make_byte_map(&tk, k8, (int64_t)P->n_pages * P->hkv * kPage, kPage))) return st;
     float* part_o = static_cast<float*>(workspace);
-    float2* part_ml = reinterpret_cast<float2*>(part_o + P->part_rows * P->hkv * P->d);
+    float4* part_ml = reinterpret_cast<float4*>(part_o + P->part_rows * P->hkv * P->d);
     const DecodeParams a = {D->entries, D->items, D->order, lens, static_cast<const uint16_t*>(q), q_stride,
                             static_cast<const uint8_t*>(k8), static_cast<const uint8_t*>(v8), k_scale, v_scale,
                             part_o, part_ml, P->part_rows, P->hkv, P->group, P->n_sub, P->gsub,

@@ -184,6 +184,40 @@ def test_page_scales_far_apart(lib, cuda_device, kv):
     check(plan, cache, ref, [-1], seg, seg, list(range(plan.n_pages)), [0], q, d ** -0.5, o, lse)
 
 
+@pytest.mark.parametrize("rows_", [1, 3])
+@pytest.mark.parametrize("apart", [(0, None), (100, None), (None, 100), (100, -90), (None, None)])
+def test_weights_survive_any_scale(lib, cuda_device, rows_, apart):
+    """Pages whose values lie up to 2^200 apart, all zero (scale 2^-100) included: every key
+    counts in the normaliser.  Both bodies; parts joined across items."""
+    rng = np.random.default_rng(15)
+    d, hq, seg = 64, 4 * rows_, [64 * 9 + 5]
+    plan = TD.DecodePlan([-1], seg, [0], hq, 1, d, cta_pages=3, warp_pages=3)
+    cache, ref = cache_pair(plan.n_pages, 1, d, cuda_device)
+    k, v = rows(rng, seg[0], 1, d, cuda_device), rows(rng, seg[0], 1, d, cuda_device)
+    for start, a in zip((0, 64), apart):                # even and odd pages
+        pick = (torch.arange(seg[0], device=cuda_device) // 64 * 64 % 128 == start)[:, None, None]
+        v = torch.where(pick, v * (0.0 if a is None else 2.0 ** a), v)
+    write_all(plan, cache, ref, [-1], seg, seg, range(plan.n_pages), k, v)
+    q = rows(rng, 1, hq, d, cuda_device)
+    o, lse = TD.tree_decode(plan, cache, plan.lens(), q, d ** -0.5)
+    check(plan, cache, ref, [-1], seg, seg, list(range(plan.n_pages)), [0], q, d ** -0.5, o, lse)
+
+
+@pytest.mark.parametrize("hq", [4, 12])
+def test_long_prefix_of_zero_values(lib, cuda_device, hq):
+    """131,072 keys with values of zero: O = 0 exactly, the log-sum-exp that of the scores."""
+    n, d = 131072, 64
+    plan = TD.DecodePlan([-1], [n], [0], hq, 1, d)
+    cache = TD.TreeCache.empty(plan.n_pages, 1, d, cuda_device)
+    k = torch.randn((n, 1, d), device=cuda_device, generator=torch.Generator(cuda_device).manual_seed(1)).bfloat16()
+    TD.tree_cache_write(plan, cache, k, torch.zeros_like(k))
+    o, lse = TD.tree_decode(plan, cache, plan.lens(), torch.zeros((1, hq, d), dtype=torch.bfloat16, device=cuda_device), 0.1)
+    # zero scores: every weight is the same power of two, the sums are exact; the logarithm is
+    # within two units and its product with ln 2 within one
+    assert (o == 0).all() and np.abs(lse.cpu().numpy() - np.log(n)).max() <= 4 * 2.0 ** -23 * np.log(n)
+    assert device_status() == 0
+
+
 @pytest.mark.parametrize("size", [-120, -40, 0, 40, 100])
 def test_query_magnitudes(lib, cuda_device, size):
     """Query rows of any magnitude, one row of zeros, one with a single large feature."""
