@@ -46,6 +46,8 @@ def sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tok
         _check_dense(top_k, "top_k", rows, torch.int32, dev)
         s.top_ks = top_k.data_ptr()
     else:
+        if not -2 ** 31 <= top_k < 2 ** 31:            # ctypes would cut it
+            raise ValueError(f"top_k: {top_k} is not an int32")
         s.top_k = top_k
     if isinstance(top_p, torch.Tensor):
         _check_dense(top_p, "top_p", rows, torch.float32, dev)

@@ -212,3 +212,10 @@ def test_refusals(lib, cuda_device):
                 lambda: sample_tokens(torch.zeros((1, 0), dtype=torch.bfloat16, device=cuda_device), u[:1])):
         with pytest.raises((ValueError, RuntimeError)):
             bad()
+
+
+@pytest.mark.parametrize("k", [2 ** 31, 2 ** 32 + 5, -2 ** 31 - 1])
+def test_top_k_that_is_no_int32_is_refused(lib, cuda_device, k):
+    x, u = torch.zeros((2, 64), dtype=torch.bfloat16, device=cuda_device), torch.zeros(2, device=cuda_device)
+    with pytest.raises(ValueError):
+        sample_tokens(x, u, top_k=k)
