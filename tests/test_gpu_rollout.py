@@ -1,0 +1,134 @@
+"""The rollout calls together, as they are used: a tree's prompt is written to the
+cache, its branches grow token by token (append, attention, logits, sampling) as one
+captured graph, then branch again with a new plan over the same pages; the training
+side's calls on the finished tree give the same attention and log-probs.
+
+Tolerances.  Attention of the training side over the decoded cache's values (bf16 holds a
+code times a power of two exactly): its own bound, 2e-2, plus the decode's for |v| <= 4.5:
+2^-8 |o| + (2^-11 + 2^-13) |v| + 2^-15 for the rest < 2.1e-2.  A page that grew after the
+step rounds codes below 2^-6 of its scale again, by 2^-18 of its largest value: inside
+that 2^-15.  Log-probs: both are x - lse in fp32; a sum of V = 1,000 positive terms in any
+order is within V * 2^-24 < 2^-14, terms and logarithm within 2^-20 (1 + |lse|): 2^-13.
+"""
+import numpy as np
+import pytest
+import torch
+
+from prefix_tree_attention_attn_gb300 import TreePlan, device_status, tree_attn_fwd
+from prefix_tree_attention_attn_gb300 import decode as TD
+from prefix_tree_attention_attn_gb300 import loss as TL
+from prefix_tree_attention_attn_gb300.sample import sample_tokens
+
+pytestmark = pytest.mark.gpu
+
+HQ, HKV, D, V, SCALE = 8, 2, 64, 1000, 0.125
+
+
+class Model:
+    """One attention layer between an embedding and logits."""
+
+    def __init__(self, dev):
+        g = torch.Generator(dev).manual_seed(5)
+        make = lambda *s: torch.randn(s, device=dev, generator=g).clamp(-4, 4).bfloat16()  # noqa: E731
+        self.q, self.k, self.v = make(V, HQ, D), make(V, HKV, D), make(V, HKV, D)
+        self.out = make(HQ * D, V) * 0.25
+
+    def logits(self, o):
+        return o.reshape(-1, HQ * D) @ self.out
+
+
+def dequantised(cache, pages, n):
+    """K, V [n, hkv, d] bf16 of a node's tokens."""
+    k = (cache.k.float() * cache.k_scale[:, :, None, None])[pages].permute(0, 2, 1, 3).reshape(-1, HKV, D)
+    v = (cache.v.float() * cache.v_scale[:, :, None, None])[pages].permute(0, 3, 1, 2).reshape(-1, HKV, D)
+    return k[:n].bfloat16(), v[:n].bfloat16()
+
+
+def test_rollout(lib, cuda_device):
+    m, rng = Model(cuda_device), np.random.default_rng(21)
+    parent, seg, grow = [-1, 0, 0, 0], [100, 1, 1, 1], 80
+    cap = [100] + [1 + grow] * 3
+    at = np.cumsum([0] + [-(-c // 64) for c in cap])
+    pool = 24
+    pages = rng.permutation(pool)[:at[-1]].astype(np.int32)
+    prompt = torch.from_numpy(rng.integers(0, V, 103)).to(cuda_device)        # the last three start a branch each
+    u = torch.from_numpy(rng.random((grow, 3)).astype(np.float32)).to(cuda_device)
+
+    def start():
+        plan = TD.DecodePlan(parent, seg, [1, 2, 3], HQ, HKV, D, capacity=cap, pages=pages, n_pages=pool)
+        cache, lens = TD.TreeCache.empty(pool, HKV, D, cuda_device), plan.lens()
+        TD.tree_cache_write(plan, cache, m.k[prompt], m.v[prompt])
+        tok = prompt[100:].int()
+        o, lse = TD.tree_decode(plan, cache, lens, m.q[tok], SCALE)
+        logits = m.logits(o)
+        return plan, cache, lens, tok, o, logits
+
+    def step(s, draw):
+        plan, cache, lens, tok, o, logits = s
+        t, lp = sample_tokens(logits, draw, temperature=0.9, top_k=200, top_p=0.95, min_p=0.001)
+        TD.tree_cache_append(plan, cache, lens, m.k[t], m.v[t])
+        o2, _ = TD.tree_decode(plan, cache, lens, m.q[t], SCALE)
+        tok.copy_(t), o.copy_(o2), logits.copy_(m.logits(o2))
+        return lp
+
+    a, b = start(), start()
+    seen = {"tok": [a[3].clone()], "o": [a[4].clone()], "logits": [a[5].clone()], "lp": []}
+    draw = u[0].clone()
+    b[0].upload()
+    spare = start()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(spare, draw)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lp_b = step(b, draw)
+    for i in range(grow):
+        seen["lp"].append(step(a, u[i]).clone())
+        for n, x in zip(("tok", "o", "logits"), a[3:]):
+            seen[n].append(x.clone())
+        draw.copy_(u[i])
+        g.replay()
+        assert torch.equal(a[3], b[3]) and torch.equal(a[4], b[4]) and torch.equal(seen["lp"][-1], lp_b), i
+    assert a[2].tolist() == [100, 81, 81, 81] and device_status() == 0
+    assert (a[3] >= 0).all()
+
+    # the training side on the finished tree, packed depth-first
+    full = [100, 81, 81, 81]
+    plan = TreePlan(parent, full)
+    tok = torch.cat([prompt[:100].int()] + [torch.stack([t[r] for t in seen["tok"]]) for r in range(3)])
+    kv = [dequantised(a[1], torch.from_numpy(pages[at[v]:at[v + 1]].astype(np.int64)).to(cuda_device), full[v]) for v in range(4)]
+    k, v = (torch.cat([x[i] for x in kv]).contiguous() for i in (0, 1))
+    o, _ = tree_attn_fwd(plan, m.q[tok].contiguous(), k, v, SCALE)
+    ours = torch.cat([torch.stack([x[r] for x in seen["o"]]) for r in range(3)])
+    assert (o[100:].float() - ours.float()).abs().max() <= 2e-2 + 2.1e-2
+    logits = torch.zeros((len(tok), V), dtype=torch.bfloat16, device=cuda_device)
+    logits[100:] = torch.cat([torch.stack([x[r] for x in seen["logits"]]) for r in range(3)])
+    _, lp = TL.traj_logprobs(plan, logits, tok.contiguous())
+    per = lp.reshape(3, 180)[:, 100:]                    # after the first token of the branch
+    got = torch.stack(seen["lp"]).T
+    assert (per - got).abs().max() <= 2.0 ** -13 * (1 + got.abs().max())
+
+    # branch: two children under node 1, one under node 3, five tokens each brought in
+    parent2, now = parent + [1, 1, 3], full + [5, 5, 5]
+    cap2 = cap + [64] * 3
+    free = np.setdiff1d(np.arange(pool), pages)[:3].astype(np.int32)
+    plan2 = TD.DecodePlan(parent2, now, [4, 5, 6, 2], HQ, HKV, D, capacity=cap2, pages=np.concatenate([pages, free]),
+                          n_pages=pool, fresh=[False] * 4 + [True] * 3)
+    new = torch.from_numpy(rng.integers(0, V, 15)).to(cuda_device)
+    TD.tree_cache_write(plan2, a[1], m.k[new], m.v[new])
+    last = torch.stack([new[4], new[9], new[14], a[3][1].long()])
+    o2, _ = TD.tree_decode(plan2, a[1], plan2.lens(), m.q[last], SCALE)
+    train = TreePlan(parent2, now)                       # depth-first: 0, 1, 4, 5, 2, 3, 6
+    kv += [dequantised(a[1], torch.tensor([int(p)], device=cuda_device), 5) for p in free]
+    order = [0, 1, 4, 5, 2, 3, 6]
+    k, v = (torch.cat([kv[n][i] for n in order]).contiguous() for i in (0, 1))
+    q = torch.zeros((sum(now), HQ, D), dtype=torch.bfloat16, device=cuda_device)
+    ends = np.cumsum([now[n] for n in order]) - 1
+    rows = [int(ends[order.index(n)]) for n in (4, 5, 6, 2)]
+    q[rows] = m.q[last]
+    o, _ = tree_attn_fwd(train, q, k, v, SCALE)
+    assert (o[rows].float() - o2.float()).abs().max() <= 2e-2 + 2.1e-2
+    assert (o2[3].float() - a[4][1].float()).abs().max() <= 2 * 2.1e-2      # an untouched branch answers as before
+    assert device_status() == 0
