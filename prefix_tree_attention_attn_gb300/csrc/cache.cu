@@ -97,7 +97,9 @@ struct WriteParams {
     uint8_t* v8;
     float* ks;
     float* vs;
-    int32_t hkv;
+    int32_t hkv, n_pages;
+    int64_t n_fresh;      // rows, with n_pages for the checks of debug builds
+    int* status;
 };
 
 // ---- write: one CTA per (page, kv-head) -------------------------------------
@@ -113,6 +115,9 @@ __global__ void __launch_bounds__(2 * D) write_kernel(const WriteParams p) {
     __shared__ float red[2][2 * D / 32];
     const int job = blockIdx.x / p.hkv, h = blockIdx.x % p.hkv;
     const int page = p.jobs[4 * job], row0 = p.jobs[4 * job + 1], n = p.jobs[4 * job + 2];
+    if (!(ta_ok(p.status, 521, page, 0, p.n_pages) && ta_ok(p.status, 522, row0, 0, p.n_fresh - n + 1) &&
+          ta_ok(p.status, 523, n, 1, kPage + 1)))
+        return;
     const int fg = threadIdx.x % FG, tg = threadIdx.x / FG;
     uint4 a[4], b[4];
 #pragma unroll
@@ -207,7 +212,7 @@ struct AppendParams {
     uint8_t* v8;
     float* ks;
     float* vs;
-    int32_t hkv;
+    int32_t hkv, n_nodes, n_pages;
     int* status;
 };
 
@@ -235,10 +240,11 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float r) {
 template <int D>
 __global__ void __launch_bounds__(512) append_kernel(const AppendParams p) {
     const int r = blockIdx.x, node = p.tails[2 * r], first = p.tails[2 * r + 1];
-    const int room = node < 0 ? 0 : p.room[node];
+    const bool known = node < 0 || ta_ok(p.status, 531, node, 0, p.n_nodes);
+    const int room = node < 0 || !known ? 0 : p.room[node];
     grid_dep_wait();
     grid_dep_launch();
-    if (node < 0) return;
+    if (node < 0 || !known) return;
     const int at = p.lens[node];
     __syncthreads();                     // every warp has read the length before it may change
     if (at < 0 || at >= room) {
@@ -249,6 +255,7 @@ __global__ void __launch_bounds__(512) append_kernel(const AppendParams p) {
         return;
     }
     const int page = p.page_tab[first + at / kPage], slot = at % kPage;
+    if (!ta_ok(p.status, 532, page, 0, p.n_pages)) return;
     const int lane = threadIdx.x & 31;
     constexpr int PL = D / 32;           // features per lane
     for (int u = threadIdx.x >> 5; u < 2 * p.hkv; u += blockDim.x >> 5) {
@@ -354,8 +361,10 @@ int tree_attn_cache_write(tree_decode_plan_t P, const void* k, const void* v, in
     DeviceDecode* D = nullptr;
     st = ensure_decode(P, &D);
     if (st) return st;
+    int dev, *status;
+    if ((st = current_device(&dev)) || (st = get_status_ptr(dev, &status))) return st;
     const WriteParams p = {D->jobs, static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), k_stride, v_stride,
-                           static_cast<uint8_t*>(k8), static_cast<uint8_t*>(v8), k_scale, v_scale, P->hkv};
+                           static_cast<uint8_t*>(k8), static_cast<uint8_t*>(v8), k_scale, v_scale, P->hkv, P->n_pages, P->n_fresh, status};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (P->d == 128) write_kernel<128><<<(unsigned)grid, 256, 0, s>>>(p);
     else write_kernel<64><<<(unsigned)grid, 128, 0, s>>>(p);
@@ -376,7 +385,7 @@ int tree_attn_cache_append(tree_decode_plan_t P, const int32_t* lens, int32_t* l
     if ((st = current_device(&dev)) || (st = get_status_ptr(dev, &status))) return st;
     const AppendParams p = {D->tails, D->page_tab, D->room, lens, lens_out, static_cast<const uint16_t*>(k),
                             static_cast<const uint16_t*>(v), k_stride, v_stride, static_cast<uint8_t*>(k8),
-                            static_cast<uint8_t*>(v8), k_scale, v_scale, P->hkv, status};
+                            static_cast<uint8_t*>(v8), k_scale, v_scale, P->hkv, P->n_nodes, P->n_pages, status};
     const int threads = std::min(512, 64 * P->hkv);
     const cudaError_t e = P->d == 128 ? launch_pdl(append_kernel<128>, dim3(P->R), dim3(threads), 0,
                                                    static_cast<cudaStream_t>(stream), p)

@@ -91,6 +91,7 @@ struct DecodeParams {
     int64_t part_rows;
     int32_t hkv, group, n_sub, gsub;
     float scale_log2;
+    int32_t n_pages, n_nodes, R, live;   // of the plan, for the checks of debug builds
     int* status;
 };
 
@@ -104,6 +105,7 @@ struct CombineParams {
     const float4* part_ml;
     int64_t part_rows;
     int32_t R, hq, hkv, group, n_sub, gsub, live;
+    int* status;
 };
 
 // 16 bytes of shared memory, by a plain load that the compiler may move.
@@ -886,10 +888,17 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     const int at = is_wide ? threadIdx.x : lane;
     if (at < n) {
         const int4 x = *reinterpret_cast<const int4*>(p.entries + 4 * (int64_t)(a.x + at));
-        e = {x.x, x.y, x.z, x.w & 0xffff, x.w >> 16 != 0};
+        if (ta_ok(p.status, 501, x.x, 0, p.n_pages) && ta_ok(p.status, 502, x.y, 0, p.n_nodes) &&
+            ta_ok(p.status, 503, x.w & 0xffff, 0, kPage + 1))
+            e = {x.x, x.y, x.z, x.w & 0xffff, x.w >> 16 != 0};
     }
     int place, head, qi = -1;
-    if (R.at(is_wide ? threadIdx.x >> 1 : lane >> 2, place, head)) qi = p.order[place];
+    if (R.at(is_wide ? threadIdx.x >> 1 : lane >> 2, place, head) &&
+        ta_ok(p.status, 504, place, 0, p.live)) {
+        qi = p.order[place];
+        if (!ta_ok(p.status, 505, qi, 0, p.R)) qi = -1;
+    }
+    if (n > 0 && !ta_ok(p.status, 506, part, 0, p.part_rows - R.rows + 1)) return;   // whole warps, or the CTA
     if (!is_wide) {
         if (lane == 0 && warp < kDecodeWarps) {
             mbar_init(smem_u32(&sm.pairs[warp].k), 1);
@@ -949,12 +958,13 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
         c0 = p.ptr[rg];
         c1 = p.ptr[rg + 1];
         qi = p.order[place];
+        if (!ta_ok(p.status, 511, qi, 0, p.R)) c1 = -1;
         if (c0 + lane < c1) mine = p.row[c0 + lane];
     }
     // the next kernel may start; it counts on this one to end after the items
     grid_dep_wait();
     grid_dep_launch();
-    if (w >= (int64_t)p.live * p.hq) return;
+    if (w >= (int64_t)p.live * p.hq || c1 < 0) return;
     const int64_t base = h * p.part_rows + off;
     float top = -INFINITY, mtop = -INFINITY, l = 0.f, o[PL];
 #pragma unroll
@@ -962,6 +972,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
     for (int b = c0; b < c1; b += 32) {
         if (b > c0) mine = b + lane < c1 ? p.row[b + lane] : 0;
         const int k = min(32, c1 - b);
+        if (lane < k && !ta_ok(p.status, 512, mine + off, 0, p.part_rows)) mine = 0;
         const float4 ml = lane < k ? p.part_ml[base + mine] : make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
         float t = ml.x, u = ml.y;
 #pragma unroll
@@ -1063,9 +1074,9 @@ extern "C" int tree_attn_decode(tree_decode_plan_t P, const int32_t* lens, const
     const DecodeParams a = {D->entries, D->items, D->order, lens, static_cast<const uint16_t*>(q), q_stride,
                             static_cast<const uint8_t*>(k8), static_cast<const uint8_t*>(v8), k_scale, v_scale,
                             part_o, part_ml, P->part_rows, P->hkv, P->group, P->n_sub, P->gsub,
-                            softmax_scale * kLog2e, status};
+                            softmax_scale * kLog2e, P->n_pages, P->n_nodes, P->R, P->live, status};
     const CombineParams b = {D->order, D->combine_ptr, D->combine_row, static_cast<uint16_t*>(o), lse, part_o, part_ml,
-                             P->part_rows, P->R, P->hq, P->hkv, P->group, P->n_sub, P->gsub, P->live};
+                             P->part_rows, P->R, P->hq, P->hkv, P->group, P->n_sub, P->gsub, P->live, status};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return P->d == 128 ? launch<128>(P, tk, a, b, s) : launch<64>(P, tk, a, b, s);
 }

@@ -23,6 +23,8 @@ import pytest
 import torch
 
 from oracle import decode as OD
+from prefix_tree_attention_attn_gb300 import _binding as B
+from prefix_tree_attention_attn_gb300 import build as _build
 from prefix_tree_attention_attn_gb300 import device_status
 from prefix_tree_attention_attn_gb300 import decode as TD
 from workloads import trees as WT
@@ -414,3 +416,25 @@ def test_refused_tensors(lib, cuda_device):
         with pytest.raises((ValueError, TypeError, RuntimeError)):
             f()
             pytest.fail(f"call {i} was taken", pytrace=False)
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 64), (16, 2, 128)])
+def test_debug_build_is_clean_and_gives_the_same_bits(lib, cuda_device, heads):
+    """Write, append and attention of items of both kinds through the
+    bounds-checked build."""
+    hq, hkv, d = heads
+    parent, seg, queries = [-1, 0, 0, 2, 2], [400, 63, 90, 10, 0], [1, 3, -1, 4]
+    cap, out = [400, 66, 90, 130, 1], []
+    for path in (_build.LIB, _build.build_library(debug=True)):
+        with B.library(path):
+            rng = np.random.default_rng(31)
+            plan, cache, _, _ = build(rng, parent, seg, queries, hq, hkv, d, cuda_device, cap=cap)
+            lens = plan.lens()
+            o, lse = torch.zeros((4, hq, d), dtype=torch.bfloat16, device=cuda_device), torch.zeros((hq, 4), device=cuda_device)
+            TD.tree_cache_append(plan, cache, lens, rows(rng, 4, hkv, d, cuda_device), rows(rng, 4, hkv, d, cuda_device))
+            TD.tree_decode(plan, cache, lens, rows(rng, 4, hq, d, cuda_device), d ** -0.5, o=o, lse=lse)
+            torch.cuda.synchronize()
+            assert device_status() == 0, path
+            out.append((o, lse, cache.k.view(torch.uint8), cache.v.view(torch.uint8), lens))
+            plan.close()
+    assert all(torch.equal(a, b) for a, b in zip(*out))
