@@ -13,7 +13,7 @@
 //             row through the full range in windows, several passes, by one CTA.
 //   groups    32 bins; a group's count and mass are one entry of a block-wide prefix
 //             sum, a search finds the group, then one warp the bin.
-//   cluster   C CTAs count a slice of the row each; each then weighs every C-th pair of groups
+//   cluster   C CTAs count a slice of the row each; each then weighs every C-th group
 //             (counts summed over the C histograms through distributed shared memory),
 //             and the first one searches.
 //   index     the r-th token with the drawn value, found by the CTA whose slice holds
@@ -60,8 +60,8 @@ struct Params {
     int* status;
 };
 
-// round(2^61 * 2^(j / 64)), j = -32 .. 32
-__constant__ uint64_t kPow[65] = {
+// round(2^61 * 2^(j / 64)), j = -32 .. 31
+__constant__ uint64_t kPow[64] = {
     0x16a09e667f3bcc91ull, 0x16dfb23c651a2ef2ull, 0x171f75e8ec5f73ddull, 0x175feb564267c8bfull,
     0x17a11473eb0186d8ull, 0x17e2f336cf4e6210ull, 0x182589994cce128bull, 0x1868d99b4492ec81ull,
     0x18ace5422aa0db5cull, 0x18f1ae991577362cull, 0x193737b0cdc5e4f4ull, 0x197d829fde4e4f8cull,
@@ -78,7 +78,6 @@ __constant__ uint64_t kPow[65] = {
     0x27bd4c982468446bull, 0x282c1443ee5c53f1ull, 0x289c10c0c3125a06ull, 0x290d456b8279a028ull,
     0x297fb5aa6c544e3bull, 0x29f364ed3a594d5aull, 0x2a6856ad3a9f03beull, 0x2ade8e6d6a4fb4ceull,
     0x2b560fba90a852b2ull, 0x2bcede2b5a4290ddull, 0x2c48fd6074ab0964ull, 0x2cc47104aa444922ull,
-    0x2d413cccfe779921ull,
 };
 
 // log2(e) / T as a pair of floats; for temperatures near the ends of fp32's range a
@@ -97,6 +96,8 @@ __device__ __forceinline__ Rate rate_of(float T) {
     return c;
 }
 
+constexpr float kRound = 12582912.f;           // 1.5 * 2^23
+
 // 2^45 * 2^(d * c), d = x - top <= 0: n + j/64 + r = d * c in pairs of floats (48 bits),
 // 2^(j/64) from the table, 2^r - 1 by its series (|r ln 2| < 0.0055: five terms), then
 // integers.
@@ -109,26 +110,31 @@ __device__ __forceinline__ uint64_t weight(const uint64_t* pow, float x, float t
     const float y = d * c.hi;
     const bool none = !(y > -64.f), full = diff == 0.f;   // (no branches: callers interleave several)
     const float yl = fmaf(d, c.hi, -y) + fmaf(d, c.lo, dl * c.hi);
-    const float n = none ? 0.f : rintf(y);
-    const float f = none ? 0.f : y - n;          // exact
-    const float j = rintf(f * 64.f);
-    const float r = fmaf(j, -0.015625f, f);      // exact
+    // k = 64 n + j: adding 1.5 2^23 rounds to an integer, which the sum's low bits are (a
+    // conversion instruction has a quarter of the rate)
+    const float ys = none ? 0.f : y, kf = fmaf(ys, 64.f, kRound);
+    const int k = (int)(__float_as_uint(kf) - __float_as_uint(kRound)), n = (k + 32) >> 6, j = k - 64 * n;
+    const float r = fmaf(kf - kRound, -0.015625f, ys);   // exact
     const float rh = r + yl;
     const float rl = yl - (rh - r);
     // z = r ln 2
     constexpr float kLh = 0x1.62e430p-1f, kLl = -0x1.05c610p-29f;
     const float z = rh * kLh;
     const float zl = fmaf(rh, kLh, -z) + fmaf(rh, kLl, rl * kLh);
-    const float t = z * z * fmaf(z, fmaf(z, fmaf(z, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f);
+    const float zz = z * z, half = 0.5f * zz;
+    const float tl = fmaf(zz * z, fmaf(z, fmaf(z, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), fmaf(z, zl, 0.5f * fmaf(z, z, -zz)));
+    const float t = half + tl;
     const float e = z + t;
-    const float el = (t - (e - z)) + zl;
-    // (e + el) 2^62 from two 32-bit conversions
-    const float eh = rintf(e * 0x1p37f);
-    const int lo = __float2int_rn((e * 0x1p37f - eh) * 0x1p25f + el * 0x1p62f);
-    const int64_t E = ((int64_t)__float2int_rn(eh) << 25) + lo;
-    const uint64_t p = pow[(int)j + 32];
-    const uint64_t w = p + 4 * (uint64_t)__mul64hi((int64_t)p, E);
-    const int shift = min(61 - kOneBits - (int)n, 63);
+    const float el = (t - (e - z)) + (zl + (tl - (t - half)));
+    // (e + el) 2^50: |e| < 2^-7 to multiples of 2^-29, then what is left, below 2^-28
+    const float eh = fmaf(e, 0x1p29f, kRound);
+    const float left = fmaf(eh - kRound, -0x1p-29f, e) + el;
+    const int hi = (int)(__float_as_uint(eh) - __float_as_uint(kRound));
+    const int lo = (int)(__float_as_uint(fmaf(left, 0x1p50f, kRound)) - __float_as_uint(kRound));
+    const int64_t E = ((int64_t)hi << 21) + lo;
+    const uint64_t p = pow[j + 32];
+    const uint64_t w = p + (uint64_t)__mul64hi((int64_t)p, E << 14);
+    const int shift = min(61 - kOneBits - n, 63);
     return full ? 1ull << kOneBits : none ? 0 : (w + (1ull << (shift - 1))) >> shift;
 }
 
@@ -173,7 +179,7 @@ struct Sums {
 
 struct Shared {
     uint32_t hist[kGroups * 32];
-    uint64_t pow[65];                            // kPow: lanes look up different entries
+    uint64_t pow[64];                            // kPow: lanes look up different entries
     uint32_t gcnt[kGroups], pcnt[kGroups];       // tokens of a group, of the groups before it
     uint64_t gmass[kGroups], pmass[kGroups];     // their weight
     Sums sums[8][kNT / 32];                      // by CTA of the cluster and warp
@@ -336,58 +342,70 @@ struct Counts {
     }
 };
 
-// Weighs the g0-th, (g0 + step)-th, .. pair of groups: count and mass of each into `to`'s arrays, the rest into
+// Weighs groups g0, g0 + step, ..: count and mass of each into `to`'s arrays, the rest into
 // `sums`, this warp's.
 __device__ __forceinline__ void weigh(const Counts& counts, int g0, int step, int win, const Weigher& W, const uint64_t* pow, Shared* to,
                       Sums& sums) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Rate unit = {1.44269502162933349609f, 1.92596299112661746887e-8f, 1.f};   // log2(e)
-    // Two neighbours at a time, without branches between them: their loads, perhaps from other
-    // SMs, and the long chains of the weights overlap.  Most far from the row's usual
-    // magnitudes are empty, and neighbours together.
-    constexpr int kAhead = 2, stride = 1;
-    for (int ga = kAhead * (g0 + step * warp); ga < kGroups; ga += kAhead * step * (kNT / 32)) {
-        uint32_t n[kAhead], cn[kAhead];
-        uint64_t m[kAhead];
+    // Most groups, far from the row's usual magnitudes, are empty: a warp loads the counts of
+    // four of its groups at once (perhaps from other SMs) and passes over empty pairs (one
+    // pair loaded at a time, an empty one took 1,000 cycles).  The two long chains of weights
+    // of a pair overlap.
+    constexpr int kBatch = 4;
+    for (int ga = g0 + step * warp; ga < kGroups; ga += kBatch * step * (kNT / 32)) {
+        const int gs = step * (kNT / 32);
+        uint32_t n[kBatch], cn[kBatch];
+        int at[kBatch];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) n[i] = ga + i * stride < kGroups ? counts(place_of(32 * (ga + i * stride) + lane, win)) : 0;
-        uint32_t some = 0;
+        for (int i = 0; i < kBatch; ++i) {
+            at[i] = place_of(32 * min(ga + i * gs, kGroups - 1) + lane, win);
+            n[i] = counts.own[at[i]];
+        }
+        if (counts.n > 1) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
+            for (int x = 0; x < 7; ++x)
+                if (x + 1 < counts.n) {
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) n[i] += counts.other[x][at[i]];
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (ga + i * gs >= kGroups) n[i] = 0;
             cn[i] = __reduce_add_sync(0xffffffffu, n[i]);
-            some |= cn[i];
-            m[i] = 0;
         }
-        if (some) {
-            uint64_t w[kAhead], one[kAhead];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const float x = __uint_as_float(bits_of(32 * (ga + i * stride) + lane, win) << 16);
-                w[i] = weight(pow, x, W.top, W.rate);
-                one[i] = W.same ? w[i] : weight(pow, x, W.top, unit);
-            }
+        for (int j = 0; j < kBatch; j += 2) {
+            uint64_t m[2] = {0, 0};
+            if (cn[j] | cn[j + 1]) {
+                uint64_t w[2], one[2];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                m[i] = n[i] ? n[i] * w[i] : 0;
-                sums.one += n[i] ? n[i] * one[i] : 0;
-                if (w[i] >= W.least) {
-                    sums.mass += m[i];
-                    sums.many += n[i];
+                for (int i = 0; i < 2; ++i) {
+                    const float x = __uint_as_float(bits_of(32 * (ga + (j + i) * gs) + lane, win) << 16);
+                    w[i] = weight(pow, x, W.top, W.rate);
+                    one[i] = W.same ? w[i] : weight(pow, x, W.top, unit);
                 }
-                // below 2^63: limbs of 26 bits, so that 32 of them do not overflow
-                const uint64_t l0 = __reduce_add_sync(0xffffffffu, (uint32_t)m[i] & 0x3ffffffu);
-                const uint64_t l1 = __reduce_add_sync(0xffffffffu, (uint32_t)(m[i] >> 26) & 0x3ffffffu);
-                const uint64_t l2 = __reduce_add_sync(0xffffffffu, (uint32_t)(m[i] >> 52));
-                m[i] = l0 + (l1 << 26) + (l2 << 52);
-            }
-        }
-        if (lane == 0) {
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                if (ga + i * stride < kGroups) {
-                    to->gcnt[ga + i * stride] = cn[i];
-                    to->gmass[ga + i * stride] = m[i];
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t k = n[j + i];
+                    m[i] = k ? k * w[i] : 0;
+                    sums.one += k ? k * one[i] : 0;
+                    if (w[i] >= W.least) {
+                        sums.mass += m[i];
+                        sums.many += k;
+                    }
+                    // below 2^63: limbs of 26 bits, so that 32 of them do not overflow
+                    const uint64_t l0 = __reduce_add_sync(0xffffffffu, (uint32_t)m[i] & 0x3ffffffu);
+                    const uint64_t l1 = __reduce_add_sync(0xffffffffu, (uint32_t)(m[i] >> 26) & 0x3ffffffu);
+                    const uint64_t l2 = __reduce_add_sync(0xffffffffu, (uint32_t)(m[i] >> 52));
+                    m[i] = l0 + (l1 << 26) + (l2 << 52);
                 }
+            }
+            if (lane < 2 && ga + (j + lane) * gs < kGroups) {
+                to->gcnt[ga + (j + lane) * gs] = lane ? cn[j + 1] : cn[j];
+                to->gmass[ga + (j + lane) * gs] = lane ? m[1] : m[0];
+            }
         }
     }
     sums.one = warp_sum(sums.one);
@@ -656,7 +674,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const Params p) {
     const int64_t lo = p.vocab * me / C, hi = p.vocab * (me + 1) / C;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i < kGroups * 32 / 4; i += kNT) reinterpret_cast<uint4*>(S.hist)[i] = make_uint4(0, 0, 0, 0);
-    if (threadIdx.x < 65) S.pow[threadIdx.x] = kPow[threadIdx.x];
+    if (threadIdx.x < 64) S.pow[threadIdx.x] = kPow[threadIdx.x];
     grid_dep_wait();
     grid_dep_launch();
     const float T = p.s.temperatures ? p.s.temperatures[r] : p.s.temperature;
