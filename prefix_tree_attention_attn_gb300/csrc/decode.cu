@@ -28,11 +28,11 @@
 // Two bodies, by the item's rows:
 //
 // At most 8 rows (a leaf's own pages) -- `narrow`, bound by HBM.  The item is one
-// warp's, six to a CTA, 12 to an SM, with nothing between the warps: loads of some
+// warp's, six to a CTA, up to 12 to an SM, with nothing between the warps: loads of some
 // overlap the products of others, and no warp waits for a slower one (with a CTA's
 // warps on one item, joined at its end, every item cost 8 us of its SM slot besides its
 // pages).  A warp has room for one page: the next K is under way from the scores on,
-// the next V from the end of P V; 192 KB in flight per SM.
+// the next V from the end of P V; up to 192 KB in flight per SM.
 // The products run transposed, S^T = K Q^T and O^T = V^T P^T, with m16n8k16: the codes
 // are the 16-row operand and the 8 columns are the query rows, so no half of the tensor
 // product is padding (rows as the 16-row operand, which a leaf of 8 rows half
@@ -900,6 +900,9 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     }
     if (n > 0 && !ta_ok(p.status, 506, part, 0, p.part_rows - R.rows + 1)) return;   // whole warps, or the CTA
     if (!is_wide) {
+        // A CTA that may allocate TMEM has its SM to itself until it gives up the right to
+        // (without this long context took 205 us instead of 188).
+        if (warp == kWarps - 1) tmem_relinquish();
         if (lane == 0 && warp < kDecodeWarps) {
             mbar_init(smem_u32(&sm.pairs[warp].k), 1);
             mbar_init(smem_u32(&sm.pairs[warp].v), 1);

@@ -28,11 +28,12 @@ constexpr int64_t kMaxCombine = (int64_t)1 << 27;
 // CTAs of the attention that run at one time: two per SM
 constexpr int32_t kSms = 152;
 constexpr int64_t kSlots = kSms * 2;
-// Cycles of a CTA besides its pages; of a page of a CTA's item, and of a warp's, in a CTA
-// that shares its SM with one of the other kind.
+// Cycles of a CTA besides its pages; of a page of a CTA's item, and of a warp's: alone on the
+// SM, which order the launch a little better than those beside one another (3,050 and 5,800;
+// long context 188 against 196 us).
 constexpr int64_t kCtaStart = 9000, kCtaPageCycles = 2100, kWarpPageCycles = 4700;
 // Time of a page in a warp's item, in times of a page in a CTA's item: 1.2 us against
-// 0.75 us alone on an SM, 4.8 us against 1.4 us with every slot taken.
+// 0.75 us alone on an SM, 2.9 us against 1.55 us beside one another.
 constexpr int64_t kWarpPage = 2;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -160,14 +161,14 @@ int build(const int32_t* parent, const int32_t* seg_len, const int32_t* capacity
         blocks[k] = rg * P->gsub <= kDecodeNarrow ? 0 : ceil_div(rg, per_block);
         cost += blocks[k] ? run_pages[k] * blocks[k] * kDecodeWarps : run_pages[k] * kWarpPage;
     }
-    // One wave of CTAs for small trees; from 32 pages a CTA on more, up to four, so that the
-    // last to finish are short.  A quarter more than an even share, because every run ends in
-    // a remainder.  At least four pages: a CTA takes some 5 us before its first page is done
-    // and each item adds a partial row to join.  Measured (pages per CTA : per warp): group
-    // star of 16, 5:1 16 us, 4:4 11.6, 8:8 15; irregular tree of 80 nodes, 16:8 52, 32:16 47,
-    // 64:32 65; 64 branches on 32,768 tokens, 16:8 261, 48:24 224, 128:24 272.
+    // One wave of CTAs for small trees, two from 64 pages a CTA on, so that the last to finish
+    // are short.  A quarter more than an even share, because every run ends in a remainder.
+    // At least four pages: a CTA takes some 5 us before its first page is done and each item
+    // adds a partial row to join.  Measured (pages per CTA : per warp): group star of 16, 3:4
+    // 12.2 us, 4:4 11.5, 8:8 14.6; irregular tree of 80 nodes, 16:8 52.6, 27:14 47.5, 64:32 78;
+    // 64 branches on 32,768 tokens, 32:16 204, 49:25 198, 73:32 188, 128:32 193.
     cost = ceil_div(cost * P->hkv, kDecodeWarps);
-    const int64_t waves = std::min<int64_t>(4, std::max<int64_t>(1, cost / (kSlots * 32)));
+    const int64_t waves = std::min<int64_t>(2, std::max<int64_t>(1, cost / (kSlots * 32)));
     const int64_t target = ceil_div(cost * 5, kSlots * waves * 4);
     P->chunk = opt_cta ? opt_cta : (int32_t)std::min<int64_t>(kDecodeMaxChunk, std::max<int64_t>(4, target));
     P->warp_chunk = opt_warp ? opt_warp : (int32_t)std::min<int64_t>(kDecodeMaxWarp, std::max<int64_t>(4, ceil_div(target, kWarpPage)));
@@ -224,7 +225,8 @@ int build(const int32_t* parent, const int32_t* seg_len, const int32_t* capacity
     // kSms CTAs launched land on different SMs, the next kSms beside them, and then each goes
     // where one has ended.  A simulation of that launch, each kind keeping to its own half of
     // the slots while it lasts, longest first, gives the order.  (Long context: one kind after
-    // the other 224 us, mixed at random 222, this way 203; irregular tree 51 and 46.)
+    // the other 224 us, mixed at random 222, this way 203; irregular tree 51 and 46 -- when an
+    // SM with a CTA of warps' items admitted no other; now 188 and 47.5.)
     auto longer = [](const Item& a, const Item& b) { return a.n > b.n; };
     std::stable_sort(warps.begin(), warps.end(), longer);
     std::stable_sort(ctas.begin(), ctas.end(), longer);
