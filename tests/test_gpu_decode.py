@@ -438,3 +438,30 @@ def test_debug_build_is_clean_and_gives_the_same_bits(lib, cuda_device, heads):
             out.append((o, lse, cache.k.view(torch.uint8), cache.v.view(torch.uint8), lens))
             plan.close()
     assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+@pytest.mark.parametrize("hq", [8, 32])
+def test_pages_behind_32_bit_offsets(lib, cuda_device, hq):
+    """Pages whose codes lie behind 2^32 bytes of their pool: write, append and attention of
+    both kinds of item give what the first pages of a small pool give."""
+    rng = np.random.default_rng(41)
+    hkv, d, far = 8, 128, 65600                            # 65,536 bytes per page of K, and of V
+    parent, seg, cap, queries = [-1, 0, 0], [150, 64, 3], [150, 65, 70], [1, 2]
+    k, v = rows(rng, 217, hkv, d, cuda_device), rows(rng, 217, hkv, d, cuda_device)
+    k1, v1, q = (rows(rng, 2, h, d, cuda_device) for h in (hkv, hkv, hq))
+    outs = []
+    for first in (0, far):
+        plan = TD.DecodePlan(parent, seg, queries, hq, hkv, d, capacity=cap, pages=range(first, first + 7))
+        cache, lens = TD.TreeCache.empty(plan.n_pages, hkv, d, cuda_device), plan.lens()
+        assert first == 0 or cache.k.numel() > 2 ** 32
+        for x in (cache.k, cache.v):
+            x[first:].view(torch.uint8).fill_(POISON)
+        TD.tree_cache_write(plan, cache, k, v)
+        TD.tree_cache_append(plan, cache, lens, k1, v1)
+        o, lse = TD.tree_decode(plan, cache, lens, q, 0.09)
+        torch.cuda.synchronize()
+        outs.append((o, lse, lens, cache.k[first:].view(torch.uint8).clone(), cache.v[first:].view(torch.uint8).clone(),
+                     cache.k_scale[first:].clone()))
+    assert torch.isfinite(outs[0][0].float()).all() and device_status() == 0
+    for n, a, b in zip(("o", "lse", "lens", "k", "v"), *outs):
+        assert torch.equal(a, b), n

@@ -219,3 +219,17 @@ def test_top_k_that_is_no_int32_is_refused(lib, cuda_device, k):
     x, u = torch.zeros((2, 64), dtype=torch.bfloat16, device=cuda_device), torch.zeros(2, device=cuda_device)
     with pytest.raises(ValueError):
         sample_tokens(x, u, top_k=k)
+
+
+def test_rows_behind_32_bit_offsets(lib, cuda_device):
+    """The last of 8,200 rows of 262,144 logits (2^31 elements and more before them) draw what
+    they draw alone."""
+    R, V = 8200, 262144
+    g = torch.Generator(cuda_device).manual_seed(7)
+    x = torch.zeros((R, V), dtype=torch.bfloat16, device=cuda_device)
+    x[-4:] = torch.randn((4, V), device=cuda_device, generator=g).bfloat16()
+    u = torch.rand(R, device=cuda_device, generator=g)
+    tok, lp = sample_tokens(x, u, temperature=0.9, top_p=0.8)
+    t2, l2 = sample_tokens(x[-4:].clone(), u[-4:].clone(), temperature=0.9, top_p=0.8)
+    assert torch.equal(tok[-4:], t2) and torch.equal(lp[-4:], l2)
+    assert (tok[:-4] >= 0).all() and (tok[:-4] < 0.81 * V).all()       # equal logits: the first 80 %
