@@ -7,7 +7,7 @@
 // counts: a weight is computed once per value, not once per token, precisely
 // enough to be an integer, and sums of integers do not depend on their order.
 //
-//   bins      value 0 and both signs of 2^-32 <= |x| < 2^16: 12,289 counters, 48 KB.
+//   bins      value 0 and both signs of 2^-32 <= |x| < 2^16: 12,289 counters in 57 KB.
 //             Lower values count as zero weight when the row's maximum and the
 //             temperature allow it (masks, -inf); any other value outside sends the
 //             row through the full range in windows, several passes, by one CTA.
@@ -19,9 +19,11 @@
 //   index     the r-th token with the drawn value, found by the CTA whose slice holds
 //             it.
 //
-// Two bytes per logit from HBM; paced by the instructions of the count (a dozen per
-// logit with every case checked, now seven, with the checks made once for eight
-// logits), and for a few rows by the cluster's barriers and the chain of searches.
+// Two bytes per logit from HBM; paced by the instructions of the count (six per logit,
+// with the range checked once for eight logits; a dozen with every case checked for each) and
+// the shared-memory atomics (3.5 wavefronts each, what 32 random banks give), and for a
+// few rows by the cluster's barriers and the chain of searches.  152,064 logits: 1 row 14 us, 64
+// rows 23, 512 rows 100; half of them -inf: 16, 31, 152.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -43,6 +45,7 @@ constexpr int kBase = (127 - 32) << 7;         // bits of 2^-32
 constexpr int kSide = 48 << 7;                 // values per sign: 2^-32 .. 2^16
 constexpr int kBins = 2 * kSide + 1;
 constexpr int kGroups = (kBins + 31) / 32;
+constexpr int kNegative = 8192;                // where negative values' counters start
 constexpr int kWindow = 12288;                 // bins per window of the full range
 constexpr int kWindows = (65536 + kWindow - 1) / kWindow;
 constexpr int kPer = (kGroups + kNT - 1) / kNT;   // groups per thread in the prefix sums
@@ -178,7 +181,7 @@ struct Sums {
 };
 
 struct Shared {
-    uint32_t hist[kGroups * 32];
+    uint32_t hist[kNegative + kSide];
     uint64_t pow[64];                            // kPow: lanes look up different entries
     uint32_t gcnt[kGroups], pcnt[kGroups];       // tokens of a group, of the groups before it
     uint64_t gmass[kGroups], pmass[kGroups];     // their weight
@@ -204,9 +207,10 @@ struct Shared {
 
 enum { kNaN = 1, kRare = 2, kLow = 4 };
 
-// Where a value of the short range is counted: magnitudes upwards from 0 for positive
-// values and from kSide for negative ones, then zero.
-constexpr int kZero = 2 * kSide;
+// Where a value of the short range is counted: magnitudes upwards from 0 for positive values
+// and from kNegative for negative ones (a power of two: the sign bit, moved, selects it); zero
+// between them.
+constexpr int kZero = kSide, kNone = kSide + 1;   // kNone: nothing is counted there
 
 // Why a value outside the short range (and not zero) does not count.
 __device__ __forceinline__ uint32_t why(uint32_t b) {
@@ -218,7 +222,7 @@ __device__ __forceinline__ uint32_t why(uint32_t b) {
 // the full one
 __device__ __forceinline__ int place_of(int bin, int win) {
     if (win >= 0) return bin;
-    return bin < kSide ? kSide - 1 - bin : bin == kSide ? kZero : bin < kBins ? bin - 1 : bin;
+    return bin < kSide ? kSide - 1 - bin : bin == kSide ? kZero : bin < kBins ? bin - (kSide + 1) + kNegative : kNone;
 }
 // bits of that value
 __device__ __forceinline__ uint32_t bits_of(int bin, int win) {
@@ -233,7 +237,7 @@ __device__ __forceinline__ void count(Shared& S, const uint16_t* row, int64_t lo
     const int64_t n = hi - lo;
     auto slow = [&](uint32_t b) {                // any value
         const uint32_t mag = b & 0x7fffu, t = mag - kBase;
-        if (t < (uint32_t)kSide) atomicAdd(&S.hist[t + (b >> 15) * kSide], 1u);
+        if (t < (uint32_t)kSide) atomicAdd(&S.hist[t + (b >> 15) * kNegative], 1u);
         else if (mag == 0) atomicAdd(&S.hist[kZero], 1u);
         else flags |= why(b);
         top = fmaxf(top, __uint_as_float(b << 16));
@@ -243,24 +247,28 @@ __device__ __forceinline__ void count(Shared& S, const uint16_t* row, int64_t lo
     const uint4* v = reinterpret_cast<const uint4*>(a + head);
     const int64_t nv = (n - head) / 8;
     __nv_bfloat162 m2 = __floats2bfloat162_rn(-INFINITY, -INFINITY);
+    uint8_t* bins = reinterpret_cast<uint8_t*>(S.hist) - 4 * kBase;
     auto vec = [&](const uint4& x) {
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        uint32_t worst = 0;
+        const uint32_t m[4] = {w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu, w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu};
+        const uint32_t most = __vimax3_u16x2(__vimax3_u16x2(m[0], m[1], m[2]), m[3], m[3]);
+        const uint32_t least = __vimin3_u16x2(__vimin3_u16x2(m[0], m[1], m[2]), m[3], m[3]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t mags = w[i] & 0x7fff7fffu;
-            const uint32_t t0 = (mags & 0xffffu) - kBase, t1 = (mags >> 16) - kBase;
-            worst = max(worst, max(t0, t1));
-            if (t0 < (uint32_t)kSide) atomicAdd(&S.hist[t0 + (w[i] >> 15 & 1) * kSide], 1u);
-            if (t1 < (uint32_t)kSide) atomicAdd(&S.hist[t1 + (w[i] >> 31) * kSide], 1u);
-            m2 = __hmax2(m2, *reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-        }
-        if (worst >= (uint32_t)kSide) {          // zeros, and what does not count
-#pragma unroll 1
+        for (int i = 0; i < 4; ++i) m2 = __hmax2(m2, *reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+        if (max(most & 0xffffu, most >> 16) < kBase + kSide && min(least & 0xffffu, least >> 16) >= kBase) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {            // byte offsets: 4 magnitude + 2^15 sign
+                const uint32_t h = w[i] >> 16;
+                atomicAdd(reinterpret_cast<uint32_t*>(bins + (4 * (w[i] & 0x7fffu) + (w[i] & 0x8000u))), 1u);
+                atomicAdd(reinterpret_cast<uint32_t*>(bins + (4 * (h & 0x7fffu) + (h & 0x8000u))), 1u);
+            }
+        } else {                                     // zeros, and what does not count (masks: no loop)
+#pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint32_t b = i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu, mag = b & 0x7fffu;
-                if (mag == 0) atomicAdd(&S.hist[kZero], 1u);
-                else if (mag - kBase >= (uint32_t)kSide) flags |= why(b);
+                const bool in = mag - kBase < (uint32_t)kSide;
+                if (in || mag == 0) atomicAdd(reinterpret_cast<uint32_t*>(bins + (in ? 4 * mag + (b & 0x8000u) : 4u * (kBase + kZero))), 1u);
+                else flags |= why(b);
             }
         }
     };
@@ -673,7 +681,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const Params p) {
     const uint16_t* row = p.logits + r * p.stride;
     const int64_t lo = p.vocab * me / C, hi = p.vocab * (me + 1) / C;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < kGroups * 32 / 4; i += kNT) reinterpret_cast<uint4*>(S.hist)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < (kNegative + kSide) / 4; i += kNT) reinterpret_cast<uint4*>(S.hist)[i] = make_uint4(0, 0, 0, 0);
     if (threadIdx.x < 64) S.pow[threadIdx.x] = kPow[threadIdx.x];
     grid_dep_wait();
     grid_dep_launch();
@@ -776,7 +784,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const Params p) {
                 sums = {0, 0, 0};
                 auto load = [&](int w, uint32_t cnt, uint64_t mass) {
                     __syncthreads();
-                    for (int i = threadIdx.x; i < kGroups * 32; i += kNT) S.hist[i] = 0;
+                    for (int i = threadIdx.x; i < kNegative + kSide; i += kNT) S.hist[i] = 0;
                     __syncthreads();
                     each(row, 0, p.vocab, [&](uint32_t b) {
                         b = b == 0x8000u ? 0u : b;
@@ -865,15 +873,23 @@ extern "C" int tree_attn_sample(const void* logits, int64_t row_stride, int64_t 
     int dev, *status;
     int st;
     if ((st = current_device(&dev)) || (st = get_status_ptr(dev, &status))) return st;
-    // CTAs per row.  A CTA takes about 14 thousand cycles whatever its slice (barriers, the
-    // chain of searches), 60 thousand more for a row of 152,064 alone; two fit an SM.  Measured
-    // at 152,064: 1 row, 8 CTAs 16 us, 1 CTA 43; 64 rows, 4 CTAs 28, 8 CTAs 42, 1 CTA 50; 512
-    // rows, 1 CTA 127, 4 CTAs 165.  At least 4,096 logits each.
+    // CTAs per row, at least 4,096 logits each: the fastest by this model, in thousands of
+    // cycles.  A CTA takes 24 whatever its share (launch, barriers, the chain of searches), 16
+    // for weighing and 24 for counting and finding 152,064 logits alone on an SM; 28, 26 and 46
+    // beside another.  152 CTAs fit one to an SM, 304 two; clusters of 4 or 8 fewer, for they
+    // keep to groups of SMs; beyond that the time grows with the CTAs.  Measured at 152,064, 1 /
+    // 2 / 4 / 8 CTAs: 1 row 33 / 25 / 17 / 15 us, 24 rows 37 / 24 / 19 / 21, 76 rows 37 / 25 / 37 /
+    // 54, 304 rows 63 / 71 / 103 / 171; at 16,384, 76 rows 19 / 16 / 28.  Over 22 numbers of rows
+    // from 1 to 900 and 6 vocabularies the choice is at most 5 % slower than the best.
     int C = 1;
     double best = 0;
+    const double v = vocab / 152064.0;
     for (int c = 1; c <= 8; c *= 2) {
         if (c > 1 && vocab < 4096 * (int64_t)c) break;
-        const double t = (double)((n_rows * c + 303) / 304) * (14 + 60 * (vocab / 152064.0) / c);
+        const double ctas = (double)n_rows * c, full = c <= 2 ? 304 : 256;
+        const double waves = ctas <= full ? 1 : std::max(1.4, ctas / full + 0.1);
+        const bool alone = ctas <= (c <= 2 ? 152 : c == 4 ? 136 : 96);
+        const double t = alone ? 24 + (16 + 24 * v) / c : waves * (28 + (26 + 46 * v) / c);
         if (c == 1 || t < best) {
             C = c;
             best = t;
