@@ -747,8 +747,9 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, cons
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&M.v_ready));
         }
-    } else {
+    } else if (32 * warp < R.rows) {
         // ------------------------------- softmax ---------------------------------
+        // (a warp without rows leaves its part of P as it is: it reaches its rows of O only)
         const float qf = M.qf[row];
         for (int i = 0; i < n; ++i) {
             const uint32_t s_col = tmem + 64 * (i & 1) + lanes;
@@ -921,7 +922,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&M.s_done[i]), 1);
-            mbar_init(smem_u32(&M.p_full[i]), 128);
+            mbar_init(smem_u32(&M.p_full[i]), (R.rows + 31) / 32 * 32);
         }
         mbar_init(smem_u32(&M.o_done), 1);
         mbar_init(smem_u32(&M.k_ready), 3);
