@@ -108,6 +108,10 @@ struct CombineParams {
     int* status;
 };
 
+// One warp: the CTA gives up the right to allocate TMEM.
+__device__ __forceinline__ void tmem_relinquish() {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
 // 16 bytes of shared memory, by a plain load that the compiler may move.
 __device__ __forceinline__ void lds128(const uint8_t* at, uint32_t (&w)[4]) {
     const uint4 x = *reinterpret_cast<const uint4*>(at);
