@@ -189,10 +189,14 @@ struct Meta {
     float lv[kDecodeMaxChunk];        // log2(v_scale)
     // K and V of each page, used once
     uint64_t full[kDecodeMaxChunk], full_v[kDecodeMaxChunk];
-    // K, V of a page are expanded; its scores are there, its P is in TMEM (one barrier per S
-    // buffer: with one for both, a wait for page i could meet the parity of page i + 2); P V
-    // has finished
-    uint64_t k_ready, v_ready, s_done[2], p_full[2], o_done;
+    // K, V of a page are expanded; its scores are there, its P is in TMEM; its P V has finished.
+    // The last three have a barrier for even and one for odd pages.  S of a page is issued before
+    // P V of the page before, so who has seen the scores of page i knows of P V up to page i - 3
+    // only (its phase was waited for before V of page i - 2 was expanded), and a single barrier
+    // could still be two phases short of P V of page i - 1 -- the same parity.  The end of the
+    // item is one further on: it has a barrier that is used once.  (Waiting for every page's
+    // o_done in the softmax instead: long context 193 us against 189.)
+    uint64_t k_ready, v_ready, s_done[2], p_full[2], o_done[2], finished;
     int32_t count[kDecodeMaxChunk / 32];
     int32_t early;                    // the first halves are on their way
     uint32_t tmem;
@@ -668,7 +672,8 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, cons
                 for (int k = 0; k < kPage / 16; ++k)
                     mma_ts(lead, o_col, tmem + 64 * (j & 1) + 8 * k, vd + ((k * 32) >> 4), idesc_f16(128, D), j > 0 || k > 0);
                 if (lead) {
-                    mma_commit(smem_u32(&M.o_done));
+                    mma_commit(smem_u32(&M.o_done[j & 1]));
+                    if (i == n) mma_commit(smem_u32(&M.finished));
                     load_half(x);
                 }
                 ++x;
@@ -727,7 +732,8 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, cons
             if (!ok) break;
             const int valid = M.valid[i];
             bool good = mbar_wait(smem_u32(&M.full_v[i]), 0, p.status, 312);
-            if (i > 0) good = mbar_wait(smem_u32(&M.o_done), (i - 1) & 1, p.status, 313) && good;   // P V has read the tile
+            // P V of the page before has read the tile
+            if (i > 0) good = mbar_wait(smem_u32(&M.o_done[(i - 1) & 1]), ((i - 1) / 2) & 1, p.status, 313) && good;
             ok = __all_sync(0xffffffffu, good);
             if (!ok) break;
             const uint8_t* from = base + S::kCodes + (x % S::kHalves) * S::kHalf;
@@ -784,7 +790,7 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, cons
             if (__any_sync(0xffffffffu, up)) {
                 const float a = up ? fast_exp2(m - top) : 1.f;
                 if (i > 0) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&M.o_done), (i - 1) & 1, p.status, 310));
+                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&M.o_done[(i - 1) & 1]), ((i - 1) / 2) & 1, p.status, 310));
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
@@ -833,7 +839,7 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, cons
         M.top[row] = m;
         M.mass_top[row] = mn;
         M.sum[row] = l;
-        if (n > 0 && ok) ok = mbar_wait(smem_u32(&M.o_done), (n - 1) & 1, p.status, 311);
+        if (n > 0 && ok) ok = mbar_wait(smem_u32(&M.finished), 0, p.status, 311);
     }
     if (!__syncthreads_and(ok)) {
         // the products issued end by themselves; so do the copies
@@ -927,8 +933,9 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&M.s_done[i]), 1);
             mbar_init(smem_u32(&M.p_full[i]), (R.rows + 31) / 32 * 32);
+            mbar_init(smem_u32(&M.o_done[i]), 1);
         }
-        mbar_init(smem_u32(&M.o_done), 1);
+        mbar_init(smem_u32(&M.finished), 1);
         mbar_init(smem_u32(&M.k_ready), 3);
         mbar_init(smem_u32(&M.v_ready), 3);
     }

@@ -465,3 +465,32 @@ def test_pages_behind_32_bit_offsets(lib, cuda_device, hq):
     assert torch.isfinite(outs[0][0].float()).all() and device_status() == 0
     for n, a, b in zip(("o", "lse", "lens", "k", "v"), *outs):
         assert torch.equal(a, b), n
+
+
+@pytest.mark.parametrize("pages", [2, 3, 4, 5])
+@pytest.mark.parametrize("hq,n_queries", [(9, 1), (16, 1), (12, 2), (32, 1), (33, 1), (16, 8)])
+def test_short_items_of_shared_rows_hold_their_last_page(lib, cuda_device, hq, n_queries, pages):
+    """Items of a few pages read by 9 to 128 rows, many of them at once and from memory that is
+    not in L2: every output holds the last page's values, every time.  The last page's keys
+    weigh most, so an output without it would be far outside the bound."""
+    rng = np.random.default_rng([hq, n_queries, pages])
+    d, hkv, runs = 128, 1, 300
+    parent, seg = [-1] * runs, [64 * pages - 9] * runs
+    queries = [u for u in range(runs) for _ in range(n_queries)]
+    plan = TD.DecodePlan(parent, seg, queries, hq, hkv, d, cta_pages=pages, warp_pages=1)
+    assert all(x[0][5] == 1 and x[0][1] == pages for x in plan.export()["items"])
+    cache, ref = cache_pair(plan.n_pages, hkv, d, cuda_device)
+    k, v = (rows(rng, sum(seg), hkv, d, cuda_device) for _ in range(2))
+    last = torch.arange(sum(seg), device=cuda_device) % seg[0] >= 64 * (pages - 1)
+    q = rows(rng, len(queries), hq, d, cuda_device)
+    k[:, 0, 0], q[:, :, 0] = torch.where(last, 4.0, -4.0).bfloat16(), 4.0
+    v[last] += 2
+    write_all(plan, cache, ref, parent, seg, seg, range(plan.n_pages), k, v)
+    ln, flush = plan.lens(), torch.empty(2 ** 27, dtype=torch.int32, device=cuda_device)
+    outs = []
+    for _ in range(12):
+        flush.zero_()
+        outs.append(TD.tree_decode(plan, cache, ln, q, d ** -0.5))
+    assert device_status() == 0
+    assert all(torch.equal(a, outs[0][0]) and torch.equal(b, outs[0][1]) for a, b in outs)
+    check(plan, cache, ref, parent, seg, seg, list(range(plan.n_pages)), queries, q, d ** -0.5, *outs[0])
