@@ -244,14 +244,19 @@ int tree_attn_bwd_noalloc(tree_attn_plan_t plan, const void* q, const void* k, c
 /* Size in bytes of the fixed scratch tree_attn_bwd_noalloc uses. */
 size_t tree_attn_noalloc_scratch_bytes(void);
 
-/* Synchronise `stream`, then read and clear the device status word of the
- * current device: 0 when every kernel's bounded waits finished in time,
- * otherwise TREE_ATTN_ERR_DEVICE_TIMEOUT - 1000 * (site of the wait),
- * TREE_ATTN_ERR_ALIGNMENT (shared memory misaligned) or
- * TREE_ATTN_ERR_INVALID_DECAY (tree_linear.h: a decay outside (0, 1]), or in
- * a debug build TREE_ATTN_ERR_DEVICE_BOUNDS - 1000 * (site of the check).  The
- * first error recorded wins.  Kernels that hit a failed wait return early and
- * leave their outputs incomplete. */
+/* Synchronise `stream`, then read and clear the device status of the current
+ * device: 0 when nothing was recorded, otherwise one of
+ *  - failures: TREE_ATTN_ERR_DEVICE_TIMEOUT - 1000 * (site of the wait),
+ *    TREE_ATTN_ERR_ALIGNMENT (shared memory misaligned), or in a debug build
+ *    TREE_ATTN_ERR_DEVICE_BOUNDS - 1000 * (site of the check).  Kernels that hit
+ *    a failed wait return early and leave their outputs incomplete, and until the
+ *    status is read so may later ones;
+ *  - notices, which touch the named call's rows only, whether they are read or not:
+ *    TREE_ATTN_ERR_INVALID_DECAY (tree_linear.h: a decay outside (0, 1]),
+ *    TREE_ATTN_ERR_CACHE_FULL (tree_decode.h: a token appended to a node without
+ *    room) and TREE_ATTN_ERR_INVALID_SAMPLING (tree_sample.h: a row's parameters).
+ * Of each kind the first one recorded is kept.  A failure is returned before a
+ * notice, which the next call then returns. */
 int tree_attn_get_device_status(void* stream);
 
 /* Self-test of the kernels' failure path: launches one thread that waits on a

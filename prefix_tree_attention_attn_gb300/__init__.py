@@ -201,5 +201,6 @@ def noalloc_scratch_bytes() -> int:
 
 
 def device_status(stream=None) -> int:
-    """Synchronise and read/clear the kernels' device status word (0 = fine)."""
+    """Synchronise and read/clear the kernels' device status (0 = fine): a failure, else a
+    notice about some call's data (``tree_attn_get_device_status``)."""
     return int(B.load().tree_attn_get_device_status(_stream_ptr(stream)))

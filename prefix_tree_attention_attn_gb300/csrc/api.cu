@@ -16,9 +16,9 @@
 
 namespace treeattn {
 
-// Device status word written by the kernels' bounded waits and, in debug
-// builds, their bounds checks (0 = fine).
-__device__ int g_device_status = 0;
+// Device status (0 = fine).  First word: failures, written by the kernels' bounded waits and, in
+// debug builds, their bounds checks; the waits read it.  Second word: notices (report_notice).
+__device__ int g_device_status[2] = {0, 0};
 // Output word of the bounds self-test kernel.
 __device__ int g_selftest_word = 0;
 
@@ -175,7 +175,7 @@ int ensure_device(tree_attn_plan_s* P, DevicePlan** out) {
     return TREE_ATTN_OK;
 }
 
-// Address of the status word on the current device (looked up once per device).
+// Address of the status words on the current device (looked up once per device).
 int status_ptr(int dev, int** out) {
     static int* ptrs[kMaxDevices] = {};
     static std::mutex mu;
@@ -637,10 +637,12 @@ int tree_attn_selftest_bounds(void* stream) {
 
 int tree_attn_get_device_status(void* stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return TREE_ATTN_ERR_CUDA;
-    int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbol(&v, g_device_status, sizeof(int)) != cudaSuccess) return TREE_ATTN_ERR_CUDA;
-    if (v != 0 && cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int)) != cudaSuccess) return TREE_ATTN_ERR_CUDA;
-    return v;
+    int v[2] = {0, 0}, zero = 0;
+    if (cudaMemcpyFromSymbol(v, g_device_status, sizeof(v)) != cudaSuccess) return TREE_ATTN_ERR_CUDA;
+    const int word = v[0] != 0 ? 0 : 1;   // a failure first; the notice is kept for the next call
+    if (v[word] != 0 && cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int), word * sizeof(int)) != cudaSuccess)
+        return TREE_ATTN_ERR_CUDA;
+    return v[word];
 }
 
 void tree_attn_plan_destroy(tree_attn_plan_t P) {

@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(512) append_kernel(const AppendParams p) {
     __syncthreads();                     // every warp has read the length before it may change
     if (at < 0 || at >= room) {
         if (threadIdx.x == 0) {
-            report_status(p.status, TREE_ATTN_ERR_CACHE_FULL);
+            report_notice(p.status, TREE_ATTN_ERR_CACHE_FULL);
             p.lens_out[node] = at;
         }
         return;

@@ -111,6 +111,6 @@ int current_device(int* dev);
 int make_tensor_map(CUtensorMap* m, const void* base, int64_t rows, int heads, int d);
 // TMA map of [rows, 128] bytes: boxes of box_rows whole rows, 128-byte swizzle.
 int make_byte_map(CUtensorMap* m, const void* base, int64_t rows, int box_rows);
-// Device address of the current device's status word (kernels' bounded waits).
+// Device address of the current device's status words (kernels' bounded waits; notices).
 int get_status_ptr(int dev, int** out);
 }  // namespace treeattn

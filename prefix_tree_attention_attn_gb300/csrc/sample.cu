@@ -810,7 +810,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const Params p) {
             rank = S.f_rank;
         }
         if (threadIdx.x == 0) {
-            if (bad_params) report_status(p.status, TREE_ATTN_ERR_INVALID_SAMPLING);
+            if (bad_params) report_notice(p.status, TREE_ATTN_ERR_INVALID_SAMPLING);
             if (key < 0) p.tokens[r] = -1;
             if (p.logprobs) {
                 const float x = __uint_as_float((uint32_t)key << 16);
