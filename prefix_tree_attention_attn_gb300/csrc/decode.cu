@@ -199,6 +199,7 @@ struct Meta {
     uint64_t k_ready, v_ready, s_done[2], p_full[2], o_done[2], finished;
     int32_t count[kDecodeMaxChunk / 32];
     int32_t early;                    // the first halves are on their way
+    int32_t loaded;                   // halves that were, when a wait ran out
     uint32_t tmem;
     float top[128], mass_top[128], sum[128], qf[128];
 };
@@ -246,8 +247,8 @@ __device__ __forceinline__ uint32_t keep_bytes(int k, int valid) {
     return n >= 4 ? 0xffffffffu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
 }
 
-// After a wait that ran out: gives a copy still in flight time to land before its shared
-// memory is given up.
+// After a wait that ran out: gives a copy or a product still in flight time to end before its
+// shared memory or TMEM is given up.  Only for barriers that something is under way to.
 __device__ __noinline__ void drain(uint64_t* bar, uint32_t parity) {
     for (int k = 0; k < 4096 && !mbar_try_wait(smem_u32(bar), parity); ++k) {}
 }
@@ -338,7 +339,7 @@ __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Pair& bar, 
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
 
-    bool ok = true;
+    bool ok = true, k_ahead = false;
     uint32_t turn = 0;
     for (; left; ++turn) {
         const int i = __ffs(left) - 1;
@@ -454,7 +455,10 @@ __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Pair& bar, 
         for (int j = 0; j < 4; ++j) keep[j] = keep_bytes(16 * t + 4 * j, valid);
         const bool part_page = valid < kPage;
         ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar.v), turn & 1, p.status, 303));
-        if (!ok) break;
+        if (!ok) {
+            k_ahead = after >= 0;      // the next K is on its way already
+            break;
+        }
 #pragma unroll
         for (int y = 0; y < D / 16; ++y) {
             uint32_t w0[4], w1[4];
@@ -479,7 +483,7 @@ __device__ void narrow(const CUtensorMap& tk, const DecodeParams& p, Pair& bar, 
         if (lane == 0 && after >= 0) load_v(next);
     }
     if (!ok) {
-        drain(&bar.k, turn & 1);
+        drain(&bar.k, (turn + k_ahead) & 1);
         drain(&bar.v, turn & 1);
         return;
     }
@@ -573,11 +577,12 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, cons
         if (is_v) load_v<D>(p, page, R.h, dst, bar);
         else load_k<D>(&tk, p, page, R.h, dst, bar);
     };
+    auto is_value = [&](int x) { return x == 2 * n - 1 || (x >= 2 && !(x & 1)); };
+    auto page_of = [&](int x) { return x == 2 * n - 1 ? n - 1 : is_value(x) ? x / 2 - 1 : (x + 1) / 2; };
     auto load_half = [&](int x) {
         if (x >= 2 * n) return;
-        const bool is_v = x == 2 * n - 1 || (x >= 2 && !(x & 1));
-        const int i = x == 2 * n - 1 ? n - 1 : is_v ? x / 2 - 1 : (x + 1) / 2;
-        half_to(is_v, i, M.page[i], x % S::kHalves);
+        const int i = page_of(x);
+        half_to(is_value(x), i, M.page[i], x % S::kHalves);
     };
     // Pages worth loading (sure to have held tokens, or holding some now), packed; the first
     // halves at once where the first two pages are sure.
@@ -598,7 +603,10 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, cons
         const uint32_t has = __ballot_sync(0xffffffffu, e.sure || f.valid > 0);
         int at = __popc(has & ((1u << lane) - 1u));
         if (lane == 0 && warp < kDecodeMaxChunk / 32) M.count[warp] = __popc(has);
-        if (threadIdx.x == 0) M.early = early;
+        if (threadIdx.x == 0) {
+            M.early = early;
+            M.loaded = 2 * kDecodeMaxChunk;
+        }
         if (n > 32) {
             __syncthreads();
             for (int x = 0; x < warp && x < kDecodeMaxChunk / 32; ++x) at += M.count[x];
@@ -679,6 +687,10 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, cons
                 ++x;
                 __syncwarp();
             }
+        }
+        if (!ok && lead) {
+            M.loaded = x;
+            mma_commit(smem_u32(&M.finished));
         }
     } else if (warp > 4) {
         // -------------------------------- expansion --------------------------------
@@ -843,10 +855,9 @@ __device__ void wide(const CUtensorMap& tk, const DecodeParams& p, Meta& M, cons
     }
     if (!__syncthreads_and(ok)) {
         // the products issued end by themselves; so do the copies
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-            drain(&M.full[i], 0);
-            drain(&M.full_v[i], 0);
-        }
+        drain(&M.finished, 0);
+        const int loaded = min(M.loaded, 2 * n);   // all of them if the issuer got through
+        for (int x = threadIdx.x; x < loaded; x += kThreads) drain(is_value(x) ? &M.full_v[page_of(x)] : &M.full[page_of(x)], 0);
         __syncthreads();
         return;
     }

@@ -84,3 +84,29 @@ def test_a_failure_is_not_hidden_by_a_notice(lib, cuda_device):
     assert device_status() == -10 - 1000 * 99
     assert device_status() == -15
     assert device_status() == 0
+
+
+def test_abandoned_items_leave_nothing_in_flight(lib, cuda_device):
+    """With a failure recorded, the attention over the cache gives its waits up early and
+    returns, its copies and products ended; the status read, the same calls give their bits
+    again."""
+    g = torch.Generator(cuda_device).manual_seed(4)
+    for d, hkv in ((128, 2), (64, 1)):
+        seg = [9000] + [700 + 137 * i for i in range(40)]
+        plan = TD.DecodePlan([-1] + [0] * 40, seg, range(1, 41), 8 * hkv, hkv, d)
+        kinds = plan.export()["items"][:, 0, 5]
+        assert kinds.any() and not kinds.all()                  # CTAs' items and warps' items
+        cache, lens = TD.TreeCache.empty(plan.n_pages, hkv, d, cuda_device), plan.lens()
+        TD.tree_cache_write(plan, cache, randn(g, sum(seg), hkv, d), randn(g, sum(seg), hkv, d))
+        q = randn(g, 40, 8 * hkv, d)
+        clean = TD.tree_decode(plan, cache, lens, q, 0.09)
+        assert device_status() == 0
+        for _ in range(3):
+            assert B.load().tree_attn_selftest_wait_timeout(10, None) == 0
+            for _ in range(4):
+                TD.tree_decode(plan, cache, lens, q, 0.09)      # incomplete
+            assert device_status() == -10 - 1000 * 99
+            for _ in range(4):
+                for a, b in zip(TD.tree_decode(plan, cache, lens, q, 0.09), clean):
+                    assert torch.equal(a, b)
+        assert device_status() == 0
