@@ -98,6 +98,24 @@ int make_byte_map(CUtensorMap* m, const void* base, int64_t rows, int box_rows) 
     return r == CUDA_SUCCESS ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA;
 }
 
+int upload_words(void** out, const int32_t* words, size_t n) {
+    void* buf = nullptr;
+    if (cudaMalloc(&buf, n * sizeof(int32_t)) != cudaSuccess) {
+        cudaGetLastError();
+        return TREE_ATTN_ERR_OUT_OF_MEMORY;
+    }
+    // A copy from pageable memory may return once its bytes are staged, and what follows on a
+    // non-blocking stream is not ordered after it: wait for the stream it runs on.
+    if (cudaMemcpy(buf, words, n * sizeof(int32_t), cudaMemcpyHostToDevice) != cudaSuccess ||
+        cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) {
+        cudaGetLastError();
+        cudaFree(buf);
+        return TREE_ATTN_ERR_CUDA;
+    }
+    *out = buf;
+    return TREE_ATTN_OK;
+}
+
 int current_device(int* dev) {
     static std::atomic<bool> usable[kMaxDevices];   // a device's capability does not change: asked once
     if (cudaGetDevice(dev) != cudaSuccess) return TREE_ATTN_ERR_NO_DEVICE;
@@ -152,14 +170,7 @@ int ensure_device(tree_attn_plan_s* P, DevicePlan** out) {
     std::copy(P->splits.begin(), P->splits.end(), h.begin() + offs[6]);
     std::copy(P->chunk_ptr.begin(), P->chunk_ptr.end(), h.begin() + offs[7]);
     void* buf = nullptr;
-    if (cudaMalloc(&buf, total * sizeof(int32_t)) != cudaSuccess) {
-        cudaGetLastError();
-        return TREE_ATTN_ERR_OUT_OF_MEMORY;
-    }
-    if (cudaMemcpy(buf, h.data(), total * sizeof(int32_t), cudaMemcpyHostToDevice) != cudaSuccess) {
-        cudaFree(buf);
-        return TREE_ATTN_ERR_CUDA;
-    }
+    if ((st = upload_words(&buf, h.data(), h.size()))) return st;
     int32_t* b = static_cast<int32_t*>(buf);
     D.base = buf;
     D.subend = b + offs[0];
@@ -640,7 +651,8 @@ int tree_attn_get_device_status(void* stream) {
     int v[2] = {0, 0}, zero = 0;
     if (cudaMemcpyFromSymbol(v, g_device_status, sizeof(v)) != cudaSuccess) return TREE_ATTN_ERR_CUDA;
     const int word = v[0] != 0 ? 0 : 1;   // a failure first; the notice is kept for the next call
-    if (v[word] != 0 && cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int), word * sizeof(int)) != cudaSuccess)
+    if (v[word] != 0 && (cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int), word * sizeof(int)) != cudaSuccess ||
+                         cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess))   // see upload_words
         return TREE_ATTN_ERR_CUDA;
     return v[word];
 }

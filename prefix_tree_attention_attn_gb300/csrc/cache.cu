@@ -42,14 +42,7 @@ int ensure_decode(tree_decode_plan_s* P, DeviceDecode** out) {
     }
     for (int k = 0; k < 9; ++k) std::copy(src[k]->begin(), src[k]->end(), h.begin() + offs[k]);
     void* buf = nullptr;
-    if (cudaMalloc(&buf, h.size() * sizeof(int32_t)) != cudaSuccess) {
-        cudaGetLastError();
-        return TREE_ATTN_ERR_OUT_OF_MEMORY;
-    }
-    if (cudaMemcpy(buf, h.data(), h.size() * sizeof(int32_t), cudaMemcpyHostToDevice) != cudaSuccess) {
-        cudaFree(buf);
-        return TREE_ATTN_ERR_CUDA;
-    }
+    if ((st = upload_words(&buf, h.data(), h.size()))) return st;
     for (int k = 0; k < 9; ++k) *dst[k] = static_cast<int32_t*>(buf) + offs[k];
     D.base = buf;
     D.ready = true;

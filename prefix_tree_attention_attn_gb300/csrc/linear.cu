@@ -613,14 +613,7 @@ int ensure_lin_device(tree_attn_plan_s* P, DevicePlan** out) {
         std::copy(P->lin.lvl_nodes.begin(), P->lin.lvl_nodes.end(), h.begin() + a + b);
         std::copy(P->lin.kids.begin(), P->lin.kids.end(), h.begin() + a + b + c);
         void* buf = nullptr;
-        if (cudaMalloc(&buf, h.size() * sizeof(int32_t)) != cudaSuccess) {
-            cudaGetLastError();
-            return TREE_ATTN_ERR_OUT_OF_MEMORY;
-        }
-        if (cudaMemcpy(buf, h.data(), h.size() * sizeof(int32_t), cudaMemcpyHostToDevice) != cudaSuccess) {
-            cudaFree(buf);
-            return TREE_ATTN_ERR_CUDA;
-        }
+        if ((st = upload_words(&buf, h.data(), h.size()))) return st;
         D.lin_base = buf;
         D.chunks = static_cast<int32_t*>(buf);
         D.lnodes = static_cast<int32_t*>(buf) + a;

@@ -245,14 +245,7 @@ int ensure_traj_device(tree_attn_plan_s* P, DevicePlan** out) {
     std::copy(X.nodes.begin(), X.nodes.end(), h.begin() + offs[1]);
     std::copy(X.leaf_of.begin(), X.leaf_of.end(), h.begin() + offs[2]);
     void* buf = nullptr;
-    if (cudaMalloc(&buf, total * sizeof(int32_t)) != cudaSuccess) {
-        cudaGetLastError();
-        return TREE_ATTN_ERR_OUT_OF_MEMORY;
-    }
-    if (cudaMemcpy(buf, h.data(), total * sizeof(int32_t), cudaMemcpyHostToDevice) != cudaSuccess) {
-        cudaFree(buf);
-        return TREE_ATTN_ERR_CUDA;
-    }
+    if ((st = upload_words(&buf, h.data(), h.size()))) return st;
     int32_t* b = static_cast<int32_t*>(buf);
     D.traj_base = buf;
     D.pred = b + offs[0];

@@ -111,6 +111,9 @@ int current_device(int* dev);
 int make_tensor_map(CUtensorMap* m, const void* base, int64_t rows, int heads, int d);
 // TMA map of [rows, 128] bytes: boxes of box_rows whole rows, 128-byte swizzle.
 int make_byte_map(CUtensorMap* m, const void* base, int64_t rows, int box_rows);
+// Device memory with a copy of n words (the caller's to free).  The copy has ended when the call
+// returns, so kernels on any stream may read it.
+int upload_words(void** out, const int32_t* words, size_t n);
 // Device address of the current device's status words (kernels' bounded waits; notices).
 int get_status_ptr(int dev, int** out);
 }  // namespace treeattn

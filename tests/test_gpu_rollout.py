@@ -132,3 +132,39 @@ def test_rollout(lib, cuda_device):
     assert (o[rows].float() - o2.float()).abs().max() <= 2e-2 + 2.1e-2
     assert (o2[3].float() - a[4][1].float()).abs().max() <= 2 * 2.1e-2      # an untouched branch answers as before
     assert device_status() == 0
+
+
+def test_first_call_of_a_plan_on_a_side_stream(lib, cuda_device):
+    """A plan's tables are in place when its first call, on a stream that does not wait for
+    the default one, reads them: fresh plans of every kind, each against one used before."""
+    from prefix_tree_attention_attn_gb300.linear import tree_linear_fwd
+    g = torch.Generator(cuda_device).manual_seed(8)
+    make = lambda *s: torch.randn(s, device=cuda_device, generator=g).bfloat16()  # noqa: E731
+    parent, seg, leaves = [-1] + [0] * 30, [500] + [90 + 7 * i for i in range(30)], range(1, 31)
+    n = sum(seg)
+    q, k, v, q1, logits = make(n, 4, 128), make(n, 2, 128), make(n, 2, 128), make(30, 4, 128), make(n, 504)
+    tokens = torch.randint(0, 504, (n,), device=cuda_device, generator=g, dtype=torch.int32)
+    decay = torch.tensor([0.9, 0.99], device=cuda_device)
+    first = TD.DecodePlan(parent, seg, leaves, 4, 2, 128)
+    cache, lens = TD.TreeCache.empty(first.n_pages, 2, 128, cuda_device), first.lens()
+    TD.tree_cache_write(first, cache, k, v)
+    side = torch.cuda.Stream()
+    grow, train = lambda: TD.DecodePlan(parent, seg, leaves, 4, 2, 128), lambda: TreePlan(parent, seg)  # noqa: E731
+    calls = ((grow, lambda p: TD.tree_decode(p, cache, lens, q1, 0.1, stream=side)),
+             (train, lambda p: tree_attn_fwd(p, q, k, v, 0.1, stream=side)),
+             (train, lambda p: (tree_linear_fwd(p, q, k, v, decay, 0.1, stream=side),)),
+             (train, lambda p: TL.traj_logprobs(p, logits, tokens, stream=side)))
+    for make_plan, call in calls:
+        want = None
+        for _ in range(20):
+            torch.cuda.synchronize()
+            plan = make_plan()
+            got = call(plan)
+            side.synchronize()
+            want = got if want is None else want
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    want, plan = TD.tree_decode(first, cache, lens, q1, 0.1), grow()
+    torch.cuda.synchronize()
+    got = calls[0][1](plan)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and device_status() == 0
