@@ -29,6 +29,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <utility>
 
 #include "kernels.h"
 #include "plan.h"
@@ -677,6 +678,9 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const Params p) {
     Shared& S = *reinterpret_cast<Shared*>(raw);
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), me = (int)cluster.block_rank();
+    // Another CTA's shared memory may be written once that CTA has begun: said here, waited for
+    // after the count.
+    auto begun = cluster.barrier_arrive();
     const int64_t r = blockIdx.x / C;
     const uint16_t* row = p.logits + r * p.stride;
     const int64_t lo = p.vocab * me / C, hi = p.vocab * (me + 1) / C;
@@ -715,6 +719,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const Params p) {
         S.wmass[warp] = __float_as_uint(top);
     }
     __syncthreads();
+    cluster.barrier_wait(std::move(begun));
     if ((int)threadIdx.x < C) {                    // to every CTA of the cluster
         for (int w = 0; w < kNT / 32; ++w) {
             flags |= S.wcnt[w];

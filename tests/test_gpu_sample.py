@@ -233,3 +233,28 @@ def test_rows_behind_32_bit_offsets(lib, cuda_device):
     t2, l2 = sample_tokens(x[-4:].clone(), u[-4:].clone(), temperature=0.9, top_p=0.8)
     assert torch.equal(tok[-4:], t2) and torch.equal(lp[-4:], l2)
     assert (tok[:-4] >= 0).all() and (tok[:-4] < 0.81 * V).all()       # equal logits: the first 80 %
+
+
+@pytest.mark.parametrize("offset", [0, 1, 3, 6])
+@pytest.mark.parametrize("ctas,rows", [(8, 7), (4, 23), (2, 55), (1, 120)])
+def test_rows_split_over_ctas(lib, cuda_device, ctas, rows, offset):
+    """A row's slices start anywhere: 8, 4, 2 and 1 CTAs a row at 33,001 logits (by the model in
+    the call), rows 33,008 elements apart that begin on odd elements, twice each in a row and
+    with a tie that reaches over every slice."""
+    rng = np.random.default_rng([ctas, offset])
+    V, stride = 33001, 33008
+    x = rng.standard_normal((rows, V)) * 3
+    x[1::2] = np.round(x[1::2])                            # thousands of equal logits
+    flat = torch.zeros(offset + rows * stride, dtype=torch.bfloat16, device=cuda_device)
+    full = flat[offset:].view(rows, stride)[:, :V]
+    full.copy_(bf16(x, cuda_device))
+    u = rng.random(rows).astype(np.float32)
+    ud = torch.from_numpy(u).to(cuda_device)
+    outs = [sample_tokens(full, ud, 0.9, 500, 0.95, 0.001) for _ in range(50)]
+    assert all(torch.equal(a, outs[0][0]) and torch.equal(b, outs[0][1]) for a, b in outs)
+    sub = [int(r) for r in rng.permutation(rows)[:7]]
+    want = [OS.draw(full[r].float().cpu().numpy().astype(np.float64), u[r], 0.9, 500, 0.95, 0.001) for r in sub]
+    assert [int(outs[0][0][r]) for r in sub] == [t for t, _ in want]
+    for r, (_, lp) in zip(sub, want):
+        assert abs(float(outs[0][1][r]) - lp) <= 2.0 ** -21 * abs(lp) + V * 2.0 ** -45
+    assert device_status() == 0
