@@ -11,7 +11,10 @@ nodes' new tokens over it.  Marshalling only.
 
 A plan stays valid while its nodes grow inside their capacity, so a whole
 segment is decoded with one plan; branching makes a new plan over the same
-pages.
+pages.  Keep a plan while calls or captured graphs that use it run.
+
+Calls on a ``stream`` other than the current one do not wait for the current
+one: what they read has to be there (``stream.wait_stream``).
 """
 from __future__ import annotations
 
@@ -124,7 +127,8 @@ class TreeCache:
                 raise ValueError(f"{name}: on {x.device}, k on {k.device}")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.hkv, self.d, self.device = P, hkv, d, k.device
-        self._ptrs = tuple(x.data_ptr() for x in (k, v, k_scale, v_scale))
+        self._tensors = (k, v, k_scale, v_scale)
+        self._ptrs = tuple(x.data_ptr() for x in self._tensors)
 
     @classmethod
     def empty(cls, n_pages: int, hkv: int, d: int, device=None) -> "TreeCache":
@@ -176,15 +180,32 @@ def _check_dense(x, name: str, shape, dtype, dev: int) -> None:
         raise _expected(x, name, dtype, shape, dev)
 
 
-def _stream_of(stream, dev: int, *owned):
-    """The stream's handle; tensors this call allocated are kept until it is done with them."""
-    if stream is None:
+def _side(stream):
+    """`stream` where it is not the current one, else None."""
+    return None if stream is None or stream == torch.cuda.current_stream() else stream
+
+
+def _empty(side, shape, dtype, device):
+    """A new tensor for a call on the stream `side`: out of that stream's pool, because work that
+    the current stream still has for a block of its own pool is not waited for; kept, once freed,
+    until the current stream, on which the caller has it, is done with it."""
+    if side is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(side):
+        x = torch.empty(shape, dtype=dtype, device=device)
+    x.record_stream(torch.cuda.current_stream())
+    return x
+
+
+def _stream_of(side, dev: int, *used):
+    """The stream's handle; the memory of what the call uses is kept until a side stream is done
+    with it, whenever the caller lets go of it."""
+    if side is None:
         return torch._C._cuda_getCurrentRawStream(dev)
-    if stream != torch.cuda.current_stream():
-        for t in owned:
-            if t is not None:
-                t.record_stream(stream)
-    return stream.cuda_stream
+    for t in used:
+        if isinstance(t, torch.Tensor):
+            t.record_stream(side)
+    return side.cuda_stream
 
 
 def tree_cache_write(plan: DecodePlan, cache: TreeCache, k, v, stream=None) -> None:
@@ -193,7 +214,8 @@ def tree_cache_write(plan: DecodePlan, cache: TreeCache, k, v, stream=None) -> N
     dev = _check_cache(plan, cache)
     n = plan.info["n_fresh_tokens"]
     ks, vs = _check_rows(k, "k", n, plan.hkv, plan.d, dev), _check_rows(v, "v", n, plan.hkv, plan.d, dev)
-    st = plan._lib.tree_attn_cache_write(plan._h, k.data_ptr(), v.data_ptr(), ks, vs, *cache._ptrs, _stream_of(stream, dev))
+    st = plan._lib.tree_attn_cache_write(plan._h, k.data_ptr(), v.data_ptr(), ks, vs, *cache._ptrs,
+                                         _stream_of(_side(stream), dev, k, v, *cache._tensors))
     if st:
         B.check(st, "tree_attn_cache_write")
 
@@ -210,7 +232,8 @@ def tree_cache_append(plan: DecodePlan, cache: TreeCache, lens, k, v, lens_out=N
     ks = _check_rows(k, "k", plan.n_queries, plan.hkv, plan.d, dev)
     vs = _check_rows(v, "v", plan.n_queries, plan.hkv, plan.d, dev)
     st = plan._lib.tree_attn_cache_append(plan._h, lens.data_ptr(), lens_out.data_ptr(), k.data_ptr(), v.data_ptr(), ks,
-                                          vs, *cache._ptrs, _stream_of(stream, dev))
+                                          vs, *cache._ptrs,
+                                          _stream_of(_side(stream), dev, lens, lens_out, k, v, *cache._tensors))
     if st:
         B.check(st, "tree_attn_cache_append")
     return lens_out
@@ -225,22 +248,22 @@ def tree_decode(plan: DecodePlan, cache: TreeCache, lens, q, softmax_scale: floa
     R, hq, d = plan.n_queries, plan.hq, plan.d
     _check_dense(lens, "lens", (plan.n_nodes,), torch.int32, dev)
     qs = _check_rows(q, "q", R, hq, d, dev)
+    side = _side(stream)
     if o is None:
-        o = torch.empty((R, hq, d), dtype=torch.bfloat16, device=q.device)
+        o = _empty(side, (R, hq, d), torch.bfloat16, q.device)
     else:
         _check_dense(o, "o", (R, hq, d), torch.bfloat16, dev)
     if lse is None:
-        lse = torch.empty((hq, R), dtype=torch.float32, device=q.device)
+        lse = _empty(side, (hq, R), torch.float32, q.device)
     else:
         _check_dense(lse, "lse", (hq, R), torch.float32, dev)
-    own = None
     if workspace is None:
-        workspace = own = torch.empty(max(plan.workspace_bytes, 1), dtype=torch.uint8, device=q.device)
+        workspace = _empty(side, (max(plan.workspace_bytes, 1),), torch.uint8, q.device)
     elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected contiguous cuda:{dev} uint8, got {workspace.device} {workspace.dtype}")
     st = plan._lib.tree_attn_decode(plan._h, lens.data_ptr(), q.data_ptr(), qs, *cache._ptrs, o.data_ptr(),
                                     lse.data_ptr(), softmax_scale, workspace.data_ptr(), workspace.numel(),
-                                    _stream_of(stream, dev, own, o, lse))
+                                    _stream_of(side, dev, lens, q, o, lse, workspace, *cache._tensors))
     if st:
         B.check(st, "tree_attn_decode")
     return o, lse

@@ -13,7 +13,7 @@ import ctypes as C
 import torch
 
 from . import _binding as B
-from .decode import _check_dense, _current_device, _stream_of
+from .decode import _check_dense, _current_device, _empty, _side, _stream_of
 
 ERR_INVALID_SAMPLING = -15      # device status: a row's parameters are invalid (token -1)
 
@@ -59,16 +59,18 @@ def sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tok
         s.min_ps = min_p.data_ptr()
     else:
         s.min_p = min_p
+    side = _side(stream)
     if tokens is None:
-        tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
+        tokens = _empty(side, rows, torch.int32, logits.device)
     else:
         _check_dense(tokens, "tokens", rows, torch.int32, dev)
     if logprobs is None:
-        logprobs = torch.empty(rows, dtype=torch.float32, device=logits.device)
+        logprobs = _empty(side, rows, torch.float32, logits.device)
     else:
         _check_dense(logprobs, "logprobs", rows, torch.float32, dev)
     st = B.load().tree_attn_sample(logits.data_ptr(), stride, R, V, u.data_ptr(), C.byref(s), tokens.data_ptr(),
-                                   logprobs.data_ptr(), _stream_of(stream, dev, tokens, logprobs))
+                                   logprobs.data_ptr(), _stream_of(side, dev, logits, u, tokens, logprobs, temperature,
+                                                                   top_k, top_p, min_p))
     if st:
         B.check(st, "tree_attn_sample")
     return tokens, logprobs

@@ -168,3 +168,39 @@ def test_first_call_of_a_plan_on_a_side_stream(lib, cuda_device):
     got = calls[0][1](plan)
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and device_status() == 0
+
+
+def test_side_stream_memory(lib, cuda_device):
+    """On a side stream, what a call allocates is no block that the current stream may still
+    write, and what the caller frees after the call is not handed out while the stream has yet
+    to read it.  (Addresses only: nothing is overwritten.)"""
+    g = torch.Generator(cuda_device).manual_seed(9)
+    make = lambda *s: torch.randn(s, device=cuda_device, generator=g).bfloat16()  # noqa: E731
+    seg, R, hq, hkv, d, vocab = [640] + [70] * 64, 64, 32, 2, 128, 20000
+    plan = TD.DecodePlan([-1] + [0] * R, seg, range(1, R + 1), hq, hkv, d, capacity=[640] + [200] * R)
+    cache, lens = TD.TreeCache.empty(plan.n_pages, hkv, d, cuda_device), plan.lens()
+    TD.tree_cache_write(plan, cache, make(sum(seg), hkv, d), make(sum(seg), hkv, d))
+    plan.upload()
+    q0, logits0, u0 = make(R, hq, d), make(R, vocab), torch.rand(R, device=cuda_device, generator=g)
+    want = (*TD.tree_decode(plan, cache, lens, q0, 0.1), *sample_tokens(logits0, u0, top_p=0.9))
+    side = torch.cuda.Stream()
+    shapes = [(x.shape, x.dtype) for x in want] + [((plan.workspace_bytes,), torch.uint8)]
+    for _ in range(3):
+        q, logits, u, k, v, n = q0.clone(), logits0.clone(), u0.clone(), make(R, hkv, d), make(R, hkv, d), lens.clone()
+        torch.cuda.synchronize()
+        freed = [torch.empty(s, dtype=t, device=cuda_device) for s, t in shapes]
+        mine = [(x.data_ptr(), x.data_ptr() + x.numel() * x.element_size()) for x in freed]
+        del freed
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)                  # some 50 ms: the calls are still to come
+        got = (*TD.tree_decode(plan, cache, n, q, 0.1, stream=side), *sample_tokens(logits, u, top_p=0.9, stream=side))
+        TD.tree_cache_append(plan, cache, n, k, v, stream=side)
+        for x in got:
+            assert not any(a <= x.data_ptr() < b for a, b in mine)
+        held = {x.data_ptr(): (x.shape, x.dtype) for x in (q, logits, u, k, v, n)}
+        del q, logits, u, k, v, n
+        again = [torch.empty(s, dtype=t, device=cuda_device) for s, t in list(held.values()) * 2]
+        assert not side.query()                             # still to come
+        assert not {x.data_ptr() for x in again} & set(held)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and device_status() == 0
