@@ -125,10 +125,16 @@ class TreeCache:
                                  f"{tuple(x.shape)}")
             if x.device != k.device:
                 raise ValueError(f"{name}: on {x.device}, k on {k.device}")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.n_pages, self.hkv, self.d, self.device = P, hkv, d, k.device
         self._tensors = (k, v, k_scale, v_scale)
-        self._ptrs = tuple(x.data_ptr() for x in self._tensors)
+        self.n_pages, self.hkv, self.d, self.device = P, hkv, d, k.device
+
+    # Read-only: a cache is checked once, other tensors are another TreeCache.
+    k, v, k_scale, v_scale = (property(lambda self, i=i: self._tensors[i]) for i in range(4))
+
+    @property
+    def _ptrs(self):
+        """The addresses of the moment: a program may free the tensors' storage and bring it back."""
+        return [x.data_ptr() for x in self._tensors]
 
     @classmethod
     def empty(cls, n_pages: int, hkv: int, d: int, device=None) -> "TreeCache":

@@ -494,3 +494,33 @@ def test_short_items_of_shared_rows_hold_their_last_page(lib, cuda_device, hq, n
     assert device_status() == 0
     assert all(torch.equal(a, outs[0][0]) and torch.equal(b, outs[0][1]) for a, b in outs)
     check(plan, cache, ref, parent, seg, seg, list(range(plan.n_pages)), queries, q, d ** -0.5, *outs[0])
+
+
+def test_a_cache_is_where_its_tensors_are(lib, cuda_device):
+    """Its tensors cannot be exchanged behind its back; storage given up is refused, and storage
+    brought back elsewhere is found there."""
+    rng = np.random.default_rng(51)
+    parent, seg, queries = [-1, 0, 0], [130, 65, 10], [1, 2]
+    plan, cache, ref, pages = build(rng, parent, seg, queries, 4, 2, 128, cuda_device)
+    q, lens = rows(rng, 2, 4, 128, cuda_device), plan.lens()
+    want = TD.tree_decode(plan, cache, lens, q, 0.1)
+    for name in ("k", "v", "k_scale", "v_scale"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, getattr(cache, name).clone())
+    kept = [x.clone() for x in (cache.k.view(torch.uint8), cache.v.view(torch.uint8), cache.k_scale, cache.v_scale)]
+    torch.cuda.synchronize()
+    mine = (cache.k, cache.v, cache.k_scale, cache.v_scale)
+    size = [x.untyped_storage().nbytes() for x in mine]
+    for x in mine:
+        x.untyped_storage().resize_(0)
+    one = torch.zeros((2, 2, 128), dtype=torch.bfloat16, device=cuda_device)
+    for call in (lambda: TD.tree_decode(plan, cache, lens, q, 0.1), lambda: TD.tree_cache_append(plan, cache, lens, one, one)):
+        with pytest.raises(B.TreeAttnError):
+            call()
+    others = [torch.empty(n, dtype=torch.uint8, device=cuda_device) for n in size]   # in their old places
+    for x, n, b in zip(mine, size, kept):
+        x.untyped_storage().resize_(n)
+        (x.view(torch.uint8) if x.dtype == torch.float8_e4m3fn else x).copy_(b)
+    assert len(others) == 4
+    got = TD.tree_decode(plan, cache, lens, q, 0.1)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and device_status() == 0
