@@ -98,7 +98,7 @@ typedef struct {
  *   capacity[v]  tokens node v has room for (>= seg_len[v]); NULL = seg_len
  *   pages        the nodes' pages, ceil(capacity[v] / 64) for each node in id order, all
  *                different and in [0, n_pages); NULL = 0, 1, 2, ...
- *   n_pages      pages of the pool
+ *   n_pages      pages of the pool; 0 where no node has room (the pool's pointers may then be NULL)
  *   fresh[v]     non-zero: tree_attn_cache_write brings node v's tokens; NULL = every node
  *   query_node   the node each query decodes in; a query attends to every token of its
  *                node and of the node's ancestors.  -1 marks a padding row: nothing of it

@@ -307,7 +307,8 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 int check_cache(const tree_decode_plan_s* P, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
                 const void* k8, const void* v8, const void* ks, const void* vs) {
-    if (!k || !v || !k8 || !v8 || !ks || !vs) return TREE_ATTN_ERR_INVALID_ARG;
+    if (!k || !v) return TREE_ATTN_ERR_INVALID_ARG;
+    if (P->n_pages && (!k8 || !v8 || !ks || !vs)) return TREE_ATTN_ERR_INVALID_ARG;   // a pool of no pages has no address
     const int64_t row = (int64_t)P->hkv * P->d;
     if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8) return TREE_ATTN_ERR_INVALID_ARG;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k8, 16) || !aligned(v8, 16) || !aligned(ks, 4) || !aligned(vs, 4))

@@ -1078,7 +1078,8 @@ using namespace treeattn;
 extern "C" int tree_attn_decode(tree_decode_plan_t P, const int32_t* lens, const void* q, int64_t q_stride,
                                 const void* k8, const void* v8, const float* k_scale, const float* v_scale, void* o,
                                 float* lse, float softmax_scale, void* workspace, size_t ws_bytes, void* stream) {
-    if (!P || !lens || !q || !k8 || !v8 || !k_scale || !v_scale || !o || !lse) return TREE_ATTN_ERR_INVALID_ARG;
+    if (!P || !lens || !q || !o || !lse) return TREE_ATTN_ERR_INVALID_ARG;
+    if (P->n_pages && (!k8 || !v8 || !k_scale || !v_scale)) return TREE_ATTN_ERR_INVALID_ARG;   // a pool of no pages has no address
     if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return TREE_ATTN_ERR_INVALID_ARG;
     if (q_stride < (int64_t)P->hq * P->d || q_stride % 8) return TREE_ATTN_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(k8, 16) || !aligned(v8, 16) || !aligned(o, 16) || !aligned(lens, 4) ||
@@ -1094,7 +1095,7 @@ extern "C" int tree_attn_decode(tree_decode_plan_t P, const int32_t* lens, const
     int dev, *status;
     if ((st = current_device(&dev)) || (st = get_status_ptr(dev, &status))) return st;
     CUtensorMap tk = {};
-    if (P->d == 128 && (st = make_byte_map(&tk, k8, (int64_t)P->n_pages * P->hkv * kPage, kPage))) return st;
+    if (P->d == 128 && !P->items.empty() && (st = make_byte_map(&tk, k8, (int64_t)P->n_pages * P->hkv * kPage, kPage))) return st;
     float* part_o = static_cast<float*>(workspace);
     float4* part_ml = reinterpret_cast<float4*>(part_o + P->part_rows * P->hkv * P->d);
     const DecodeParams a = {D->entries, D->items, D->order, lens, static_cast<const uint16_t*>(q), q_stride,

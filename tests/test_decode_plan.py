@@ -199,3 +199,20 @@ def test_encode_is_the_format(lib):
     assert OD.encode([1e9, -np.inf]).tolist() == [126, 254] and OD.encode([np.nan])[0] & 127 == 127
     assert OD.page_exp([448.0]) == 0 and OD.page_exp([448.1]) == 1 and OD.page_exp([0.0]) == -100
     assert OD.page_exp([np.inf, 3.5, np.nan]) == -7
+
+
+def test_a_pool_of_no_pages_is_taken(lib):
+    """A tree whose nodes have no room at all: its plan has no pages, no items and no workspace,
+    and its calls are not refused for a pool without an address (here: for want of a device)."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the calls would be made")
+    p = DecodePlan([-1, 0], [0, 0], [1, -1, 0], 4, 2, 128)
+    assert p.n_pages == 0 and p.info["n_ctas"] == 0 and p.workspace_bytes == 0
+    f = C.c_void_p(0x1000)
+    assert lib.tree_attn_decode(p.handle, f, f, 512, None, None, None, None, f, f, 1.0, None, 0, None) == -8
+    one = DecodePlan([-1, 0], [0, 0], [1, 0], 4, 2, 128)
+    assert lib.tree_attn_cache_append(one.handle, f, f, f, f, 256, 256, None, None, None, None, None) == -8
+    assert lib.tree_attn_cache_append(one.handle, f, f, f, None, 256, 256, None, None, None, None, None) == -1
+    some = DecodePlan([-1, 0], [0, 0], [1, 0], 4, 2, 128, n_pages=1)
+    assert lib.tree_attn_cache_append(some.handle, f, f, f, f, 256, 256, None, None, None, None, None) == -1

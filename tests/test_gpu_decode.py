@@ -524,3 +524,19 @@ def test_a_cache_is_where_its_tensors_are(lib, cuda_device):
     assert len(others) == 4
     got = TD.tree_decode(plan, cache, lens, q, 0.1)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and device_status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_pool_of_no_pages(lib, cuda_device, d):
+    """Nodes without room: the attention gives O = 0 and LSE = -inf, an append is dropped."""
+    plan = TD.DecodePlan([-1, 0], [0, 0], [1, -1, 0], 4, 2, d)
+    cache, lens = TD.TreeCache.empty(plan.n_pages, 2, d, cuda_device), plan.lens()
+    assert plan.n_pages == 0
+    q = torch.ones((3, 4, d), dtype=torch.bfloat16, device=cuda_device)
+    o, lse = torch.full_like(q, 7), torch.full((4, 3), 7.0, device=cuda_device)
+    TD.tree_cache_write(plan, cache, q[:0, :2], q[:0, :2])
+    TD.tree_decode(plan, cache, lens, q, 0.1, o=o, lse=lse)
+    assert (o[[0, 2]] == 0).all() and (lse[:, [0, 2]] == -float("inf")).all()
+    assert (o[1] == 7).all() and (lse[:, 1] == 7).all() and device_status() == 0
+    TD.tree_cache_append(plan, cache, lens, q[:, :2], q[:, :2])
+    assert lens.tolist() == [0, 0] and device_status() == TD.ERR_CACHE_FULL and device_status() == 0
