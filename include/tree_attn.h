@@ -287,7 +287,9 @@ int tree_attn_debug_checks(void);
  * TREE_ATTN_ERR_UNSUPPORTED and launch nothing. */
 int tree_attn_selftest_bounds(void* stream);
 
-/* Free the plan and its device copies (call after work using it finished). */
+/* Free the plan and its device copies (call after work using it finished, replays
+ * of graphs that captured its calls included).  Allowed while another stream is
+ * being captured. */
 void tree_attn_plan_destroy(tree_attn_plan_t plan);
 
 const char* tree_attn_strerror(int status);

@@ -118,7 +118,9 @@ int tree_attn_decode_plan_export(tree_decode_plan_t plan, const tree_attn_decode
 
 int tree_attn_decode_plan_upload(tree_decode_plan_t plan);
 
-/* Free the plan and its device copies (call after work using it finished). */
+/* Free the plan and its device copies (call after work using it finished, replays
+ * of graphs that captured its calls included).  Allowed while another stream is
+ * being captured. */
 void tree_attn_decode_plan_destroy(tree_decode_plan_t plan);
 
 /* Write the fresh nodes' tokens, e.g. what a prefill with tree_attn_fwd produced:

@@ -116,6 +116,19 @@ int upload_words(void** out, const int32_t* words, size_t n) {
     return TREE_ATTN_OK;
 }
 
+void free_words(int dev, void* words) {
+    int cur = -1;
+    const bool have = cudaGetDevice(&cur) == cudaSuccess;
+    // A plan may be dropped at any time (a binding's garbage collector does); in the usual mode
+    // of a capture the free would be refused and the capture lost.
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    const bool relaxed = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
+    if (cudaSetDevice(dev) == cudaSuccess) cudaFree(words);
+    if (relaxed) cudaThreadExchangeStreamCaptureMode(&mode);
+    if (have) cudaSetDevice(cur);
+    cudaGetLastError();
+}
+
 int current_device(int* dev) {
     static std::atomic<bool> usable[kMaxDevices];   // a device's capability does not change: asked once
     if (cudaGetDevice(dev) != cudaSuccess) return TREE_ATTN_ERR_NO_DEVICE;
@@ -659,18 +672,11 @@ int tree_attn_get_device_status(void* stream) {
 
 void tree_attn_plan_destroy(tree_attn_plan_t P) {
     if (!P) return;
-    int cur = -1;
-    bool have = cudaGetDevice(&cur) == cudaSuccess;
     for (int dev = 0; dev < kMaxDevices; ++dev) {
-        if (!P->dev[dev].ready && !P->dev[dev].traj_ready && !P->dev[dev].lin_ready) continue;
-        if (cudaSetDevice(dev) == cudaSuccess) {
-            if (P->dev[dev].ready) cudaFree(P->dev[dev].base);
-            if (P->dev[dev].traj_ready) cudaFree(P->dev[dev].traj_base);
-            if (P->dev[dev].lin_ready) cudaFree(P->dev[dev].lin_base);
-        }
+        if (P->dev[dev].ready) free_words(dev, P->dev[dev].base);
+        if (P->dev[dev].traj_ready) free_words(dev, P->dev[dev].traj_base);
+        if (P->dev[dev].lin_ready) free_words(dev, P->dev[dev].lin_base);
     }
-    if (have) cudaSetDevice(cur);
-    cudaGetLastError();
     delete P;
 }
 

@@ -332,15 +332,8 @@ int tree_attn_decode_plan_upload(tree_decode_plan_t P) {
 
 void tree_attn_decode_plan_destroy(tree_decode_plan_t P) {
     if (!P) return;
-    int cur = 0;
-    bool have = false;
-    for (int i = 0; i < kMaxDevices; ++i) {
-        if (!P->dev[i].base) continue;
-        if (!have) have = cudaGetDevice(&cur) == cudaSuccess;
-        cudaSetDevice(i);
-        cudaFree(P->dev[i].base);
-    }
-    if (have) cudaSetDevice(cur);
+    for (int i = 0; i < kMaxDevices; ++i)
+        if (P->dev[i].base) free_words(i, P->dev[i].base);
     delete P;
 }
 

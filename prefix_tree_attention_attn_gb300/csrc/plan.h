@@ -114,6 +114,8 @@ int make_byte_map(CUtensorMap* m, const void* base, int64_t rows, int box_rows);
 // Device memory with a copy of n words (the caller's to free).  The copy has ended when the call
 // returns, so kernels on any stream may read it.
 int upload_words(void** out, const int32_t* words, size_t n);
+// Gives it back, on its own device, also while this thread captures a stream.
+void free_words(int dev, void* words);
 // Device address of the current device's status words (kernels' bounded waits; notices).
 int get_status_ptr(int dev, int** out);
 }  // namespace treeattn

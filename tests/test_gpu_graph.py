@@ -50,3 +50,31 @@ def test_graph_replay_matches_eager(lib, cuda_device, name):
             assert float((a.float() - b.float()).norm() / b.float().norm()) <= 1e-3
         else:
             assert torch.equal(a, b), nm
+
+
+def test_plans_dropped_while_a_graph_is_captured(lib, cuda_device):
+    """Plans may be dropped at any time, during a capture too: the captured calls of other plans
+    stand and replay."""
+    from prefix_tree_attention_attn_gb300 import decode as TD
+    make = lambda: TD.DecodePlan([-1, 0], [700, 5], [1], 4, 2, 64)  # noqa: E731
+    kept, dropped, train = make(), make(), TreePlan([-1, 0], [200, 30])
+    for p in (kept, dropped, train):
+        p.upload()
+    g = torch.Generator(cuda_device).manual_seed(2)
+    draw = lambda *s: torch.randn(s, device=cuda_device, generator=g).bfloat16()  # noqa: E731
+    cache, lens = TD.TreeCache.empty(kept.n_pages, 2, 64, cuda_device), kept.lens()
+    TD.tree_cache_write(kept, cache, draw(705, 2, 64), draw(705, 2, 64))
+    q = draw(1, 4, 64)
+    want = TD.tree_decode(kept, cache, lens, q, 0.1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        TD.tree_decode(kept, cache, lens, q, 0.1)
+        dropped.close()
+        train.close()
+        got = TD.tree_decode(kept, cache, lens, q, 0.1)
+    for _ in range(3):
+        got[0].zero_(), got[1].zero_()
+        graph.replay()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert device_status() == 0
