@@ -1054,7 +1054,7 @@ int launch(const tree_decode_plan_s* P, const CUtensorMap& tk, const DecodeParam
         const int st = current_device(&dev);
         if (st) return st;
         std::call_once(once[dev], [&] {
-            attr[dev] = cudaFuncSetAttribute(decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
+            attr[dev] = launched(cudaFuncSetAttribute(decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem));
         });
         if (attr[dev] != cudaSuccess) return TREE_ATTN_ERR_CUDA;
         if (launch_pdl(decode_kernel<D>, dim3((unsigned)(ctas * P->hkv)), dim3(kThreads), Shape<D>::kSmem, s, tk, a) !=

@@ -98,6 +98,12 @@ __device__ __forceinline__ void bwd_cta_work(const BwdParams& p, int b, int& ite
     item = base + r % n;
 }
 
+// A launch's own status; a refused one leaves nothing behind that a later call could take for its own.
+inline cudaError_t launched(cudaError_t e) {
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
+}
+
 // Launch with programmatic stream serialization (see grid_dep_wait in ptx.cuh):
 // the kernel may begin while the previous kernel on the stream finishes.
 template <typename... KArgs, typename... Args>
@@ -113,7 +119,7 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
+    return launched(cudaLaunchKernelEx(&cfg, kern, args...));
 }
 
 // Launchers return cudaSuccess or the launch error.

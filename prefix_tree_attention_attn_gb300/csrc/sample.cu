@@ -904,7 +904,7 @@ extern "C" int tree_attn_sample(const void* logits, int64_t row_stride, int64_t 
     static std::once_flag once[kMaxDevices];
     static cudaError_t attr[kMaxDevices];
     std::call_once(once[dev], [&] {
-        attr[dev] = cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
+        attr[dev] = launched(cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared)));
     });
     if (attr[dev] != cudaSuccess) return TREE_ATTN_ERR_CUDA;
     const Params p = {static_cast<const uint16_t*>(logits), row_stride, vocab, u, *s, tokens, logprobs, status};
@@ -920,5 +920,5 @@ extern "C" int tree_attn_sample(const void* logits, int64_t row_stride, int64_t 
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, sample_kernel, p) == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA;
+    return launched(cudaLaunchKernelEx(&cfg, sample_kernel, p)) == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA;
 }

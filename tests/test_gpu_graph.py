@@ -78,3 +78,34 @@ def test_plans_dropped_while_a_graph_is_captured(lib, cuda_device):
         graph.replay()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert device_status() == 0
+
+
+def test_a_refused_launch_is_its_own_calls_error(lib, cuda_device):
+    """A plan's first call does not belong into a capture: it and the calls after it in the lost
+    capture are refused; the calls after that are not taken for failed."""
+    from prefix_tree_attention_attn_gb300 import _binding as B
+    from prefix_tree_attention_attn_gb300 import decode as TD
+    from prefix_tree_attention_attn_gb300.sample import sample_tokens
+    make = lambda: TD.DecodePlan([-1, 0], [70, 5], [1], 4, 2, 64, capacity=[70, 60])  # noqa: E731
+    kept, late = make(), make()
+    kept.upload()
+    k = torch.ones((75, 2, 64), dtype=torch.bfloat16, device=cuda_device)
+    q, x, u = torch.ones((1, 4, 64), dtype=torch.bfloat16, device=cuda_device), k.view(75, 128), torch.zeros(75, device=cuda_device)
+    for refused in ("append", "decode", "sample"):
+        cache, lens = TD.TreeCache.empty(kept.n_pages, 2, 64, cuda_device), kept.lens()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with pytest.raises(RuntimeError):
+            with torch.cuda.graph(graph):
+                with pytest.raises(B.TreeAttnError):
+                    TD.tree_decode(late, cache, lens, q, 0.1)
+                with pytest.raises(B.TreeAttnError):
+                    if refused == "append":
+                        TD.tree_cache_append(kept, cache, lens, k[:1], k[:1])
+                    elif refused == "decode":
+                        TD.tree_decode(kept, cache, lens, q, 0.1)
+                    else:
+                        sample_tokens(x, u)
+        TD.tree_cache_write(kept, cache, k, k)              # reports launches by the runtime's last error
+        o, _ = TD.tree_decode(kept, cache, lens, q, 0.1)
+        assert (o == 1).all() and device_status() == 0
