@@ -29,7 +29,13 @@ TILE_PARTIAL = 2
 
 
 def _i32(a) -> np.ndarray:
-    return np.ascontiguousarray(np.asarray(a, dtype=np.int32))
+    """`a` as int32; refused where that would change a value."""
+    a = np.asarray(a)
+    with np.errstate(invalid="ignore"):
+        x = np.ascontiguousarray(a, dtype=np.int32)
+    if x is not a and not np.array_equal(x, a):
+        raise ValueError("integers below 2^31 expected")
+    return x
 
 
 def _ptr_i32(a: np.ndarray):

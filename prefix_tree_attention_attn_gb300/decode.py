@@ -46,6 +46,10 @@ class DecodePlan:
                  cta_pages: int = 0, warp_pages: int = 0):
         self._lib = B.load()
         self._h = None
+        for name, x in (("hq", hq), ("hkv", hkv), ("d", d), ("n_pages", n_pages or 0), ("cta_pages", cta_pages),
+                        ("warp_pages", warp_pages)):
+            if not -2 ** 31 <= x < 2 ** 31:                # ctypes would cut it
+                raise ValueError(f"{name}: {x} is not an int32")
         par, sl, qn = _i32(parent), _i32(seg_len), _i32(query_nodes)
         cap = sl if capacity is None else _i32(capacity)
         if par.ndim != 1 or sl.shape != par.shape or cap.shape != par.shape or qn.ndim != 1:
@@ -56,7 +60,7 @@ class DecodePlan:
             raise ValueError(f"pages: {need} page numbers expected, got shape {pg.shape}")
         if n_pages is None:
             n_pages = need if pg is None else int(pg.max(initial=-1)) + 1
-        fr = None if fresh is None else np.ascontiguousarray(np.asarray(fresh, dtype=np.uint8))
+        fr = None if fresh is None else (np.asarray(fresh) != 0).astype(np.uint8)
         if fr is not None and fr.shape != par.shape:
             raise ValueError("fresh must have one entry per node")
         opts, h = B.DecodeOpts(cta_pages, warp_pages), C.c_void_p()

@@ -216,3 +216,18 @@ def test_a_pool_of_no_pages_is_taken(lib):
     assert lib.tree_attn_cache_append(one.handle, f, f, f, None, 256, 256, None, None, None, None, None) == -1
     some = DecodePlan([-1, 0], [0, 0], [1, 0], 4, 2, 128, n_pages=1)
     assert lib.tree_attn_cache_append(some.handle, f, f, f, f, 256, 256, None, None, None, None, None) == -1
+
+
+def test_values_that_are_no_int32_are_refused(lib):
+    """Nothing is cut to 32 bits or to an integer on the way to the planner."""
+    ok = dict(parent=[-1, 0], seg_len=[100, 3], query_nodes=[1], hq=2, hkv=1, d=64)
+    big = np.array([2 ** 32 + 1], np.int64)
+    for kw in ({"seg_len": np.concatenate([100 + 0 * big, big])}, {"parent": np.concatenate([big - 2 ** 33, 0 * big])},
+               {"query_nodes": big}, {"query_nodes": [1.5]}, {"query_nodes": [float("nan")]},
+               {"capacity": np.concatenate([big + 100, big])}, {"pages": np.array([2 ** 32, 1, 2])}, {"hq": 2 ** 32 + 2},
+               {"hkv": 2 ** 32 + 1}, {"d": 2 ** 32 + 64}, {"n_pages": 2 ** 32 + 9}, {"cta_pages": 2 ** 32 + 3},
+               {"warp_pages": 2 ** 32 + 3}):
+        with pytest.raises((ValueError, OverflowError)):
+            DecodePlan(**{**ok, **kw})
+    p = DecodePlan(**{**ok, "parent": np.array([-1, 0], np.int64), "query_nodes": (np.int64(1),), "fresh": np.array([256, 0])})
+    assert p.info["n_fresh_tokens"] == 100
