@@ -69,7 +69,7 @@ class DecodePlan:
             None if fr is None else fr.ctypes.data_as(B.c_uint8_p), _ptr_i32(qn), len(qn), hq, hkv, d, C.byref(opts),
             C.byref(h)), "tree_attn_decode_plan")
         self._h = h
-        self.seg_len, self.query_nodes = sl, qn
+        self.seg_len, self.query_nodes = sl.copy(), qn.copy()   # the caller's arrays may change
         self.n_nodes, self.n_queries, self.n_pages = len(par), len(qn), int(n_pages)
         self.hq, self.hkv, self.d = hq, hkv, d
         inf = B.DecodeInfo()

@@ -231,3 +231,12 @@ def test_values_that_are_no_int32_are_refused(lib):
             DecodePlan(**{**ok, **kw})
     p = DecodePlan(**{**ok, "parent": np.array([-1, 0], np.int64), "query_nodes": (np.int64(1),), "fresh": np.array([256, 0])})
     assert p.info["n_fresh_tokens"] == 100
+
+
+def test_a_plan_keeps_its_own_lengths(lib):
+    """plan.lens() gives the lengths at plan time, whatever becomes of the arrays given."""
+    seg, queries = np.array([100, 3], np.int32), np.array([1], np.int32)
+    p = DecodePlan(np.array([-1, 0], np.int32), seg, queries, 2, 1, 64, capacity=[100, 60])
+    seg += 7
+    queries[0] = 0
+    assert p.lens("cpu").tolist() == [100, 3] and p.query_nodes.tolist() == [1]
