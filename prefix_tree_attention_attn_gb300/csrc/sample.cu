@@ -233,7 +233,8 @@ __device__ __forceinline__ uint32_t bits_of(int bin, int win) {
 }
 
 // Counts elements [lo, hi) of a row and takes their maximum.
-__device__ __forceinline__ void count(Shared& S, const uint16_t* row, int64_t lo, int64_t hi, uint32_t& flags, float& top) {
+__device__ __forceinline__ void count(Shared& S, const uint16_t* row, int64_t lo, int64_t hi, uint32_t& flags, float& top,
+                                      int* status) {
     const uint16_t* a = row + lo;
     const int64_t n = hi - lo;
     auto slow = [&](uint32_t b) {                // any value
@@ -260,8 +261,12 @@ __device__ __forceinline__ void count(Shared& S, const uint16_t* row, int64_t lo
 #pragma unroll
             for (int i = 0; i < 4; ++i) {            // byte offsets: 4 magnitude + 2^15 sign
                 const uint32_t h = w[i] >> 16;
-                atomicAdd(reinterpret_cast<uint32_t*>(bins + (4 * (w[i] & 0x7fffu) + (w[i] & 0x8000u))), 1u);
-                atomicAdd(reinterpret_cast<uint32_t*>(bins + (4 * (h & 0x7fffu) + (h & 0x8000u))), 1u);
+                const uint32_t a0 = 4 * (w[i] & 0x7fffu) + (w[i] & 0x8000u), a1 = 4 * (h & 0x7fffu) + (h & 0x8000u);
+                if (!ta_ok(status, 541, a0, 4 * kBase, 4 * (kBase + kNegative + kSide)) ||
+                    !ta_ok(status, 541, a1, 4 * kBase, 4 * (kBase + kNegative + kSide)))
+                    continue;
+                atomicAdd(reinterpret_cast<uint32_t*>(bins + a0), 1u);
+                atomicAdd(reinterpret_cast<uint32_t*>(bins + a1), 1u);
             }
         } else {                                     // zeros, and what does not count (masks: no loop)
 #pragma unroll
@@ -578,7 +583,7 @@ __device__ bool draw(Shared& S, const Counts& counts, int first, int windows, co
 constexpr uint32_t kListed = 2048;
 
 __device__ void find(Shared& S, const uint16_t* row, int a, int b, uint32_t key, uint32_t rank, uint32_t matches,
-                     int32_t* out) {
+                     int32_t* out, int* status) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // Parts begin where memory's 16-byte blocks do, so that a lane's eight elements are one
     // load: block k holds elements 8 k - skew .. 8 k - skew + 7; blocks in0 .. in1 - 1 lie inside.
@@ -650,7 +655,7 @@ __device__ void find(Shared& S, const uint16_t* row, int a, int b, uint32_t key,
             uint32_t smaller = 0;
 #pragma unroll 8
             for (uint32_t j = 0; j < matches; ++j) smaller += S.hist[j] < mine;
-            if (smaller == rank) *out = (int32_t)mine;
+            if (smaller == rank && ta_ok(status, 544, (int32_t)mine, a, b)) *out = (int32_t)mine;
         }
         return;
     }
@@ -666,7 +671,10 @@ __device__ void find(Shared& S, const uint16_t* row, int a, int b, uint32_t key,
     uint32_t left = rank - before;
     for (int k = b0; k < b1; k += 32) {
         const uint32_t m = hits(k + lane), c = __popc(m), upto = warp_scan(c);
-        if (left < upto && left >= upto - c) *out = 8 * (k + lane) - skew + (int)__fns(m, 0, (int)(left - (upto - c)) + 1);
+        if (left < upto && left >= upto - c) {
+            const int at = 8 * (k + lane) - skew + (int)__fns(m, 0, (int)(left - (upto - c)) + 1);
+            if (ta_ok(status, 545, at, a, b)) *out = at;
+        }
         const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
         if (left < all) return;
         left -= all;
@@ -710,7 +718,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const Params p) {
     // ---- count the slice ----------------------------------------------------------
     uint32_t flags = 0;
     float top = -INFINITY;
-    count(S, row, lo, hi, flags, top);
+    count(S, row, lo, hi, flags, top, p.status);
     flags = __reduce_or_sync(0xffffffffu, flags);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -810,6 +818,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const Params p) {
             }
             one_all = S.total.one;
         }
+        drawn = drawn && ta_ok(p.status, 542, S.f_bin, 0, 32 * kGroups) && ta_ok(p.status, 543, S.f_rank, 0, p.vocab);
         if (drawn) {
             key = (int)bits_of(S.f_bin, win);
             rank = S.f_rank;
@@ -855,7 +864,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const Params p) {
     const int key = S.key;
     const bool whole = S.owner == 0xffffffffu;      // the leader searches the whole row
     if (key < 0 || (whole ? me != 0 : (int)S.owner != me)) return;
-    find(S, row, whole ? 0 : (int)lo, whole ? (int)p.vocab : (int)hi, (uint32_t)key, S.rank, S.matches, p.tokens + r);
+    find(S, row, whole ? 0 : (int)lo, whole ? (int)p.vocab : (int)hi, (uint32_t)key, S.rank, S.matches, p.tokens + r, p.status);
 }
 
 }  // namespace

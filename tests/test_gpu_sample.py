@@ -16,6 +16,8 @@ import pytest
 import torch
 
 from oracle import sample as OS
+from prefix_tree_attention_attn_gb300 import _binding as B
+from prefix_tree_attention_attn_gb300 import build as _build
 from prefix_tree_attention_attn_gb300 import device_status
 from prefix_tree_attention_attn_gb300.sample import ERR_INVALID_SAMPLING, sample_tokens
 
@@ -258,3 +260,25 @@ def test_rows_split_over_ctas(lib, cuda_device, ctas, rows, offset):
     for r, (_, lp) in zip(sub, want):
         assert abs(float(outs[0][1][r]) - lp) <= 2.0 ** -21 * abs(lp) + V * 2.0 ** -45
     assert device_status() == 0
+
+
+@pytest.mark.parametrize("rows,V", [(1, 152064), (30, 33001), (60, 9000), (200, 4097)])
+def test_debug_build_is_clean_and_gives_the_same_bits(lib, cuda_device, rows, V):
+    """Every split, the short and the full range, few and many equal logits through the
+    bounds-checked build."""
+    rng = np.random.default_rng([rows, V])
+    x = rng.standard_normal((rows, V)) * 4
+    x[1::4] = np.round(x[1::4])                            # many ties, zeros of both signs
+    x[2::8, ::3] = -np.inf
+    x[3::8] *= 1e6                                         # the full range
+    x[5::8, 0] = 1e-20
+    x[6::16] = 0
+    x[7::16] = np.nan
+    logits, u = bf16(x, cuda_device), torch.from_numpy(rng.random(rows).astype(np.float32)).to(cuda_device)
+    T = torch.from_numpy(rng.choice([0.0, 0.7, 1.0, 2.0], rows).astype(np.float32)).to(cuda_device)
+    out = []
+    for path in (_build.LIB, _build.build_library(debug=True)):
+        with B.library(path):
+            out.append(sample_tokens(logits, u, T, 300, 0.9, 0.001) + sample_tokens(logits, u, T))
+            assert device_status() == 0, path
+    assert all(torch.equal(a.view(torch.int32), b.view(torch.int32)) for a, b in zip(*out))
