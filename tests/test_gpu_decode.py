@@ -540,3 +540,26 @@ def test_a_pool_of_no_pages(lib, cuda_device, d):
     assert (o[1] == 7).all() and (lse[:, 1] == 7).all() and device_status() == 0
     TD.tree_cache_append(plan, cache, lens, q[:, :2], q[:, :2])
     assert lens.tolist() == [0, 0] and device_status() == TD.ERR_CACHE_FULL and device_status() == 0
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_random_lengths_beyond_the_room(lib, cuda_device, seed):
+    """Random trees whose lengths of the moment lie below, at and beyond the room (where the room
+    counts), at both kinds of items."""
+    rng = np.random.default_rng([seed, 77])
+    n = int(rng.integers(4, 20))
+    t = WT.random_tree(rng, n, [1, 7, 64, 100, 129, 500], n_roots=int(rng.integers(1, 4)))
+    cap = [x + int(rng.choice([0, 1, 70])) for x in t.seg_len]
+    queries = [int(x) for x in rng.integers(-1, n, size=int(rng.integers(8, 40)))]
+    hq, hkv, d = [(8, 2, 64), (16, 2, 128), (5, 1, 128), (24, 2, 64)][seed]
+    plan, cache, ref, pages = build(rng, t.parent, t.seg_len, queries, hq, hkv, d, cuda_device, cap=cap)
+    # every slot of the room holds a token
+    full = TD.DecodePlan(t.parent, cap, queries, hq, hkv, d, pages=pages, n_pages=plan.n_pages)
+    k, v = (rows(rng, sum(cap), hkv, d, cuda_device) for _ in range(2))
+    write_all(full, cache, ref, t.parent, cap, cap, pages, k, v)
+    lens = [int(rng.choice([x, c, c + 1, c + 1000, 2 ** 31 - 1, 0, -3])) for x, c in zip(t.seg_len, cap)]
+    q = rows(rng, len(queries), hq, d, cuda_device)
+    o, lse = TD.tree_decode(plan, cache, torch.tensor(lens, dtype=torch.int32, device=cuda_device), q, d ** -0.5)
+    now = [max(0, min(a, c)) for a, c in zip(lens, cap)]
+    check(plan, cache, ref, t.parent, now, cap, pages, queries, q, d ** -0.5, o, lse)
+    assert device_status() == 0
