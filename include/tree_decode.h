@@ -33,7 +33,9 @@
  * device; the plan's first call on a device uploads its tables (allocates and
  * synchronises; make it outside stream capture, or call
  * tree_attn_decode_plan_upload).  Calls of one plan may run on several streams
- * at once when they do not touch the same pages or workspace.
+ * at once when they do not touch the same pages or workspace.  A call is ordered
+ * with what came before on its own stream only: its inputs have to be there, and
+ * their memory stays the call's until the stream has passed it.
  */
 #ifndef TREE_DECODE_H
 #define TREE_DECODE_H
@@ -147,9 +149,14 @@ int tree_attn_cache_append(tree_decode_plan_t plan, const int32_t* lens, int32_t
  * v, at most its room).  q bf16, row r at element r * q_stride (a multiple of 8, at
  * least hq * d); o [n_queries, hq, d] bf16; lse [hq, n_queries] fp32.  A query whose
  * path holds no token gets O = 0 and LSE = -inf.  Rows of padding queries are left as
- * they were.  The result is bitwise reproducible.  workspace: workspace_bytes of
- * device memory, 256-byte aligned, contents ignored; calls that may overlap on the
- * GPU need one each. */
+ * they were.  The result is bitwise reproducible.
+ * Precision: scores, statistics and sums are fp32; o is rounded once, to bf16.  A softmax
+ * weight times its page's v_scale is rounded to f16 before it meets the codes: by 2^-11 of
+ * itself, and where it is below 2^-26 of the row's largest such product by at most 2^-37
+ * of that.  q is exact but for features below 2^-14 of their row's largest, which lose at
+ * most 2^-25 of that.
+ * workspace: workspace_bytes of device memory, 256-byte aligned, contents ignored; calls
+ * that may overlap on the GPU need one each. */
 int tree_attn_decode(tree_decode_plan_t plan, const int32_t* lens, const void* q, int64_t q_stride, const void* k8,
                      const void* v8, const float* k_scale, const float* v_scale, void* o, float* lse,
                      float softmax_scale, void* workspace, size_t ws_bytes, void* stream);

@@ -224,7 +224,7 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float r) {
 }
 
 // ---- append: one CTA per query, one warp per (kv-head, K or V) -----------------
-// A few hundred bytes per warp: a chain of dependent loads (length, page, scale), 3.4 us
+// A few hundred bytes per warp: a chain of dependent loads (length, page, scale), 3.0 us
 // for 16 queries of 8 kv-heads.  A value's features lie a page row apart -- the order in
 // which the attention reads them as operands -- so a new token touches one 32-byte sector
 // for each: 33 MB that L2 fetches and writes back at 1,024 queries, which bounds that case
