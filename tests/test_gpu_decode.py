@@ -559,7 +559,9 @@ def test_random_lengths_beyond_the_room(lib, cuda_device, seed):
     write_all(full, cache, ref, t.parent, cap, cap, pages, k, v)
     lens = [int(rng.choice([x, c, c + 1, c + 1000, 2 ** 31 - 1, 0, -3])) for x, c in zip(t.seg_len, cap)]
     q = rows(rng, len(queries), hq, d, cuda_device)
-    o, lse = TD.tree_decode(plan, cache, torch.tensor(lens, dtype=torch.int32, device=cuda_device), q, d ** -0.5)
+    o = torch.zeros((len(queries), hq, d), dtype=torch.bfloat16, device=cuda_device)
+    ln = torch.tensor(lens, dtype=torch.int32, device=cuda_device)
+    o, lse = TD.tree_decode(plan, cache, ln, q, d ** -0.5, o=o, lse=torch.zeros((hq, len(queries)), device=cuda_device))
     now = [max(0, min(a, c)) for a, c in zip(lens, cap)]
     check(plan, cache, ref, t.parent, now, cap, pages, queries, q, d ** -0.5, o, lse)
     assert device_status() == 0
