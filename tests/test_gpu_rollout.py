@@ -204,3 +204,34 @@ def test_side_stream_memory(lib, cuda_device):
         assert not {x.data_ptr() for x in again} & set(held)
         side.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want)) and device_status() == 0
+
+
+def test_side_stream_inside_a_capture(lib, cuda_device):
+    """A captured step whose attention and draw run on two streams at once, with outputs and
+    workspace made inside the calls: replays give the eager results."""
+    g = torch.Generator(cuda_device).manual_seed(10)
+    make = lambda *s: torch.randn(s, device=cuda_device, generator=g).bfloat16()  # noqa: E731
+    seg = [640] + [70] * 20
+    plan = TD.DecodePlan([-1] + [0] * 20, seg, range(1, 21), 16, 2, 128)
+    cache, lens = TD.TreeCache.empty(plan.n_pages, 2, 128, cuda_device), plan.lens()
+    TD.tree_cache_write(plan, cache, make(sum(seg), 2, 128), make(sum(seg), 2, 128))
+    plan.upload()
+    q, logits, u = make(20, 16, 128), make(20, 30000), torch.rand(20, device=cuda_device, generator=g)
+    side, out = torch.cuda.Stream(), []
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        now = torch.cuda.current_stream()
+        side.wait_stream(now)
+        for _ in range(3):
+            out += [*TD.tree_decode(plan, cache, lens, q, 0.1, stream=side), *sample_tokens(logits, u, 0.9, 50)]
+            out += [*TD.tree_decode(plan, cache, lens, q, 0.1), *sample_tokens(logits, u, 0.9, 50, stream=side)]
+        now.wait_stream(side)
+    for _ in range(3):
+        q.copy_(make(20, 16, 128)), logits.copy_(make(20, 30000)), u.copy_(torch.rand(20, device=cuda_device, generator=g))
+        for x in out:
+            x.fill_(7)
+        graph.replay()
+        want = [*TD.tree_decode(plan, cache, lens, q, 0.1), *sample_tokens(logits, u, 0.9, 50)]
+        assert len(out) == 24 and all(torch.equal(a, want[i % 4]) for i, a in enumerate(out))
+    assert device_status() == 0
