@@ -98,6 +98,11 @@ __device__ __forceinline__ void bwd_cta_work(const BwdParams& p, int b, int& ite
     item = base + r % n;
 }
 
+// report_status (ptx.cuh) records a failure of a kernel, after which every wait gives up early.
+// This records something about a call's data (a row, a node) in the word beside it, which no
+// kernel reads: other rows and other calls go on as if nothing had happened.
+__device__ __forceinline__ void report_notice(int* status, int code) { atomicCAS(status + 1, 0, code); }
+
 // A launch's own status; a refused one leaves nothing behind that a later call could take for its own.
 inline cudaError_t launched(cudaError_t e) {
     if (e != cudaSuccess) cudaGetLastError();

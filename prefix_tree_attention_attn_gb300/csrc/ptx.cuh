@@ -19,12 +19,9 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-// Record a failure of a kernel in the device status word (0 = fine; the first one wins): from
-// then on every wait gives up early.  A wait that ran out is stored as -10 - 1000 * where.
+// Record an error in the device status word (0 = fine; the first error wins).
+// A wait that ran out is stored as -10 - 1000 * where.
 __device__ __forceinline__ void report_status(int* status, int code) { atomicCAS(status, 0, code); }
-// Record something about a call's data (a row, a node) in the word beside it, which no kernel
-// reads: other rows and other calls go on as if nothing had happened.
-__device__ __forceinline__ void report_notice(int* status, int code) { atomicCAS(status + 1, 0, code); }
 
 // ---- debug bounds checks -------------------------------------------------------
 // Builds with -DTREE_ATTN_DEBUG check the indices that come from the plan's
