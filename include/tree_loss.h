@@ -88,6 +88,58 @@ int tree_attn_traj_logprobs(tree_attn_plan_t plan, const void* logits, int64_t v
 int tree_attn_subtree_advantage(tree_attn_plan_t plan, const float* leaf_reward, int32_t flags, float eps,
                                 float* leaf_adv, float* node_coef, float* token_coef, void* stream);
 
+/* Clipped policy loss of the trajectories, and its gradient for the compact logits.  The pages
+ * train policies on rollout trees (HARTS, AReaL-DTA: the compact tokens' results equal those of
+ * training every trajectory on its own; TreePO: advantages of segments) and print no loss; this
+ * is the clipped ratio with a penalty towards a reference policy that such training uses.
+ *
+ * Prediction k (as in tree_attn_traj_logprobs) is made by the compact row r of the logits x for
+ * the token y at the next position.  With LSE_r = ln sum_v e^x_rv, p_rv = e^(x_rv - LSE_r),
+ * lp = x_ry - LSE_r, rho = e^(lp - old_k), H_r = LSE_r - sum_v p_rv x_rv and A the advantage:
+ *
+ *   loss = sum_k w_k (-min(rho A, clip(rho, 1 - clip_low, 1 + clip_high) A)
+ *                     + kl_coef (e^(ref_k - lp) - (ref_k - lp) - 1) - entropy_coef H_r)
+ *   g_k  = w_k (dsurrogate + kl_coef (1 - e^(ref_k - lp)))
+ *          dsurrogate = -rho A where the clip does not bind (its borders included), else 0
+ *   dlogits_rv = grad_scale (sum_k g_k (1[v = y_k] - p_rv)
+ *                            + entropy_coef sum_k w_k p_rv (x_rv - LSE_r + H_r))
+ *
+ * over the predictions with w_k != 0.  At the end of a shared segment one row predicts every
+ * child's first token, and above it every trajectory's copy of a prediction counts on its own.
+ * A = 0 gives a surrogate of 0 whatever the ratio.  -inf in the logits is probability 0; a row
+ * with a NaN, a +inf or nothing but -inf, and a token id outside [0, vocab), give NaN.  Where
+ * w_k = 0 the prediction is left out whatever its other inputs hold, and its log-prob is written
+ * as 0; the logits of a row without any weight are not read, its entropy and gradient are 0. */
+typedef struct {
+    const float* old_logprobs;   /* [n_pred], n_pred = n_expanded - n_leaves; NULL: rho = 1, as if old = lp */
+    const float* advantages;     /* [n_leaves] by leaf id ascending, or [n_pred] with per_token */
+    const float* weights;        /* [n_pred]; NULL: 1 / n_pred each */
+    const float* ref_logprobs;   /* [n_pred]; may be NULL when kl_coef is 0 */
+    int32_t per_token;
+    float clip_low;              /* in [0, 1] */
+    float clip_high;             /* >= 0, infinity for no upper clip */
+    float kl_coef;               /* finite, as the next two */
+    float entropy_coef;
+    float grad_scale;            /* of dlogits only */
+} tree_attn_policy_t;
+
+/* Device workspace that tree_attn_policy_loss needs. */
+int tree_attn_policy_loss_workspace(tree_attn_plan_t plan, size_t* ws_bytes);
+
+/* logits bf16, row t at element t * row_stride (>= vocab; any alignment of 2 bytes),
+ * 1 <= vocab <= 262144; tokens int32 [n_tokens]; loss fp32 [1]; logprobs fp32 [n_pred] and entropy
+ * fp32 [n_tokens], either may be NULL; dlogits bf16 [n_tokens] rows of d_stride elements, NULL for the
+ * loss alone, or the logits themselves with the same stride (each row is read before it is
+ * written).  The struct is read during the call.  Log-probs, ratios and sums are fp32 or wider
+ * (whether a ratio lies beyond the clip is decided in pairs of floats); dlogits is
+ * rounded once.  Bitwise reproducible.  workspace: 256-byte aligned, contents ignored; calls that may
+ * overlap need one each.  Asynchronous on `stream`; the plan's first call on a device uploads
+ * its tables (allocates and synchronises once: make it outside stream capture). */
+int tree_attn_policy_loss(tree_attn_plan_t plan, const void* logits, int64_t row_stride, int64_t vocab,
+                          const int32_t* tokens, const tree_attn_policy_t* policy, float* loss, float* logprobs,
+                          float* entropy, void* dlogits, int64_t d_stride, void* workspace, size_t ws_bytes,
+                          void* stream);
+
 #ifdef __cplusplus
 }
 #endif

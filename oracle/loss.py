@@ -91,3 +91,46 @@ def subtree_advantage(parent, seg_len, rewards, norm_std=False, size_weighted=Fa
     node_c = np.array([sum(A[x] for x in below[u]) for u in range(len(parent))], dtype=np.float64)
     tn = layout.token_nodes(parent, seg_len)
     return np.array([A[x] for x in leaves], dtype=np.float64), node_c, node_c[tn]
+
+
+def policy_loss(parent, seg_len, logits, tokens, old, advantages, weights=None, ref=None, per_token=False, clip_low=0.2,
+                clip_high=0.2, kl_coef=0.0, entropy_coef=0.0):
+    """(loss, log-probs, entropies, gradient, bound) of the clipped policy loss, prediction by
+    prediction along the trajectories.  ``bound`` is, for each element of the gradient, the sum of
+    the magnitudes of the terms that make it up (what rounding errors are relative to)."""
+    x = np.asarray(logits, dtype=np.float64)
+    N, V = x.shape
+    with np.errstate(divide="ignore"):
+        logp = x - row_logsumexp(x)[:, None]
+    p = np.exp(logp)
+    finite = np.where(p > 0, logp, 0.0)
+    H = -(p * finite).sum(axis=1)
+    tok = np.asarray(tokens)
+    pairs = [(idx[q], idx[q + 1], l) for l, (_, idx) in enumerate(layout.trajectories(parent, seg_len))
+             for q in range(len(idx) - 1)]
+    w = np.full(len(pairs), 1.0 / max(1, len(pairs))) if weights is None else np.asarray(weights, dtype=np.float64)
+    loss, lp, ent = 0.0, np.zeros(len(pairs)), np.zeros(N)
+    grad, bound = np.zeros((N, V)), np.zeros((N, V))
+    for k, (r, s, l) in enumerate(pairs):
+        if w[k] == 0:
+            continue
+        y = int(tok[s])
+        A = float(advantages[k if per_token else l])
+        lp[k], ent[r] = logp[r, y], H[r]
+        ratio = 1.0 if old is None else float(np.exp(lp[k] - float(old[k])))
+        held = min(max(ratio, 1 - clip_low), 1 + clip_high)
+        term = -min(ratio * A, held * A) - entropy_coef * H[r]
+        g = -ratio * A if ratio * A <= held * A else 0.0
+        size = abs(ratio * A)
+        if kl_coef:
+            far = float(ref[k]) - lp[k]
+            term += kl_coef * (np.exp(far) - far - 1)
+            g += kl_coef * (1 - np.exp(far))
+            size += kl_coef * (1 + np.exp(far))
+        loss += w[k] * term
+        point = np.zeros(V)
+        point[y] = 1.0
+        slope = p[r] * (finite[r] + H[r])
+        grad[r] += w[k] * (g * (point - p[r]) + entropy_coef * slope)
+        bound[r] += abs(w[k]) * (size * (point + p[r]) + abs(entropy_coef) * p[r] * (np.abs(finite[r]) + H[r]))
+    return loss, lp, ent, grad, bound

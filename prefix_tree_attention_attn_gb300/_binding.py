@@ -54,6 +54,13 @@ class Sampling(C.Structure):
                 ("temperature", C.c_float), ("top_k", C.c_int32), ("top_p", C.c_float), ("min_p", C.c_float)]
 
 
+class Policy(C.Structure):
+    _fields_ = [("old_logprobs", C.c_void_p), ("advantages", C.c_void_p), ("weights", C.c_void_p),
+                ("ref_logprobs", C.c_void_p), ("per_token", C.c_int32), ("clip_low", C.c_float),
+                ("clip_high", C.c_float), ("kl_coef", C.c_float), ("entropy_coef", C.c_float),
+                ("grad_scale", C.c_float)]
+
+
 # name -> (restype, argtypes); every symbol include/*.h declares
 SIGNATURES = {
     "tree_attn_plan": (C.c_int, [c_int32_p, c_int32_p, C.c_int32, C.POINTER(PlanOpts), C.POINTER(C.c_void_p)]),
@@ -122,6 +129,10 @@ SIGNATURES = {
     "tree_attn_scale_rows": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_int64, C.c_void_p]),
     "tree_attn_traj_logprobs": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
                                           C.c_void_p]),
+    "tree_attn_policy_loss_workspace": (C.c_int, [C.c_void_p, C.POINTER(C.c_size_t)]),
+    "tree_attn_policy_loss": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.POINTER(Policy),
+                                        C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p,
+                                        C.c_size_t, C.c_void_p]),
     "tree_attn_subtree_advantage": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_float, C.c_void_p,
                                               C.c_void_p, C.c_void_p, C.c_void_p]),
 }

@@ -676,6 +676,7 @@ void tree_attn_plan_destroy(tree_attn_plan_t P) {
         if (P->dev[dev].ready) free_words(dev, P->dev[dev].base);
         if (P->dev[dev].traj_ready) free_words(dev, P->dev[dev].traj_base);
         if (P->dev[dev].lin_ready) free_words(dev, P->dev[dev].lin_base);
+        if (P->dev[dev].policy_ready) free_words(dev, P->dev[dev].policy_base);
     }
     delete P;
 }

@@ -1,0 +1,316 @@
+"""The clipped policy loss and its gradient (include/tree_loss.h) against the oracle.
+
+Tolerances, from the arithmetic.  e^(x - m) is within 2^-22 + |x - m| 2^-24 of itself (at most
+2^-21 where it counts: e^-a a < 1), a sum of at most 8 * 10 terms in a row, then 9 pairwise, is within
+89 * 2^-24; ln S is then within 2^-17 and its own rounding, and a log-prob within
+2^-17 + 2^-23 |lp|, an entropy within 2^-16 (1 + H).  A ratio or e^(ref - lp) is within 2^-16 of
+itself, so the loss is within 2^-15 of the sum of its terms' magnitudes.  A gradient is within
+2^-15 of the magnitudes that make it up (the oracle's bound) before its one rounding to bf16, 2^-8 of
+itself.  Ratios are drawn at least 0.05 away from the clip's borders."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import layout as OL
+from oracle import loss as OLS
+from prefix_tree_attention_attn_gb300 import TreePlan, build as _build, device_status
+from prefix_tree_attention_attn_gb300 import _binding as B
+from prefix_tree_attention_attn_gb300 import loss as TL
+from prefix_tree_attention_attn_gb300.sample import sample_tokens
+
+pytestmark = pytest.mark.gpu
+
+STAR40 = ([-1] + [0] * 40, [6] + [1 + i % 3 for i in range(40)])                  # 40 predictions a root row, 40 children
+MIXED = ([-1, 0, 0, 1, 1, 3, -1], [4, 3, 2, 1, 2, 1, 3])                          # a forest, branches in branches
+WIDE = ([-1, 0] + [1] * 35 + [0], [3, 4] + [1] * 35 + [2])                        # 35 through an inner node, one beside
+
+
+@pytest.fixture(autouse=True)
+def _lib(lib, cuda_device):
+    yield
+    torch.cuda.synchronize()
+    assert device_status() == 0
+
+
+def make(tree, V, seed, per_token=False, zero=0.5, masked=0.0, same=False):
+    parent, seg = tree
+    g = np.random.default_rng(seed)
+    N, L = sum(seg), len(OL.leaves(parent))
+    n = sum(len(i) for _, i in OL.trajectories(parent, seg)) - L
+    tok = g.integers(0, min(V, 3) if same else V, N)
+    x = torch.from_numpy(g.normal(size=(N, V)) * 2).bfloat16()
+    if masked:
+        hide = g.random((N, V)) < masked
+        hide[:, tok] = False                              # (what is predicted keeps a probability)
+        x[torch.from_numpy(hide)] = -float("inf")
+    lp = OLS.traj_logprobs(parent, seg, x.double().numpy(), tok)
+    f32 = lambda a: torch.from_numpy(np.asarray(a, dtype=np.float32))  # noqa: E731
+    old = f32(lp - g.choice([-0.6, -0.1, 0.0, 0.1, 0.6], n))
+    w = f32((g.random(n) - 0.2) * (g.random(n) >= zero))
+    return x, torch.from_numpy(tok).int(), old, f32(g.normal(size=n if per_token else L)), w, f32(lp + 0.5 * g.normal(size=n))
+
+
+def check(tree, data, got, per_token=False, use_old=True, use_w=True, scale=1.0, **kw):
+    x, tok, old, adv, w, ref = data
+    num = lambda t: t.double().cpu().numpy()  # noqa: E731
+    loss, lp, ent, grad, bound = OLS.policy_loss(*tree, num(x), tok.numpy(), num(old) if use_old else None, num(adv),
+                                                 weights=num(w) if use_w else None, ref=num(ref), per_token=per_token, **kw)
+    H = ent.max(initial=0.0)
+    assert np.abs(num(got.logprobs) - lp).max(initial=0) <= 2.0 ** -17 + 2.0 ** -23 * np.abs(lp).max(initial=0)
+    assert np.abs(num(got.entropy) - ent).max() <= 2.0 ** -16 * (1 + H)
+    # the magnitudes of the loss's terms: those of its gradient at the targets, and the penalties'
+    ww = num(w) if use_w else np.full(len(lp), 1 / max(1, len(lp)))
+    a = num(adv) if per_token else np.repeat(num(adv), [len(i) - 1 for _, i in OL.trajectories(*tree)])
+    ratio = np.exp(lp - num(old)) if use_old else np.ones(len(lp))
+    far = num(ref) - lp
+    terms = np.abs(a) * np.maximum(ratio, 2) + kw.get("kl_coef", 0) * (np.exp(far) + np.abs(far) + 1) + kw.get("entropy_coef", 0) * (1 + H)
+    assert abs(float(got.loss) - loss) <= 2.0 ** -15 * (np.abs(ww) * terms).sum() + 1e-30
+    if got.dlogits is not None:
+        e = np.abs(num(got.dlogits) - scale * grad)
+        lim = 2.0 ** -8 * np.abs(scale * grad) + 2.0 ** -15 * abs(scale) * bound + 1e-38
+        assert (e <= lim).all(), (np.unravel_index(np.argmax(e / lim), e.shape), (e / lim).max())
+
+
+def run(tree, data, device, use_old=True, use_w=True, use_ref=True, plan=None, x=None, **kw):
+    d = [t.to(device) for t in data]
+    return TL.policy_loss(plan or TreePlan(*tree), d[0] if x is None else x, d[1], d[2] if use_old else None, d[3],
+                          weights=d[4] if use_w else None, ref_logprobs=d[5] if use_ref else None, **kw)
+
+
+@pytest.mark.parametrize("V", [1, 2, 7, 8, 9, 500, 1000, 4097, 20473, 20481, 50257])
+def test_vocabularies(cuda_device, V):
+    data = make(MIXED, V, V, zero=0.3)
+    kw = dict(kl_coef=0.1, entropy_coef=0.02, clip_high=0.3)
+    check(MIXED, data, run(MIXED, data, cuda_device, **kw), **kw)
+
+
+@pytest.mark.parametrize("V", [152064, 262144])
+def test_largest_vocabularies(cuda_device, V):
+    tree = ([-1, 0, 0], [2, 2, 1])
+    data = make(tree, V, 5, zero=0.0)
+    kw = dict(kl_coef=0.1, entropy_coef=0.02)
+    check(tree, data, run(tree, data, cuda_device, **kw), **kw)
+
+
+@pytest.mark.parametrize("tree", [STAR40, MIXED, WIDE, ([-1], [1]), ([-1], [9]), ([-1, -1], [1, 1]), ([-1, 0, 0], [1, 1, 1])])
+@pytest.mark.parametrize("same", [False, True])
+def test_trees(cuda_device, tree, same):
+    """Many predictions per row, many children per row, children with the same token."""
+    for per_token in (False, True):
+        data = make(tree, 300, 17 + per_token, per_token=per_token, same=same)
+        check(tree, data, run(tree, data, cuda_device, per_token=per_token, kl_coef=0.05), per_token=per_token, kl_coef=0.05)
+
+
+def test_options(cuda_device):
+    data = make(WIDE, 700, 3)
+    for use_old, use_w, kw in ((False, True, {}), (True, False, {}), (False, False, dict(entropy_coef=-0.1)),
+                               (True, True, dict(clip_low=1.0, clip_high=float("inf"))),
+                               (False, True, dict(clip_low=0.0, clip_high=0.0))):
+        check(WIDE, data, run(WIDE, data, cuda_device, use_old=use_old, use_w=use_w, use_ref=False, **kw),
+              use_old=use_old, use_w=use_w, **kw)
+    got = run(WIDE, data, cuda_device, grad_scale=-0.25)
+    check(WIDE, data, got, scale=-0.25)
+    alone = run(WIDE, data, cuda_device, grad=False)
+    assert alone.dlogits is None and torch.equal(alone.loss, got.loss)
+    assert torch.equal(alone.logprobs, got.logprobs) and torch.equal(alone.entropy, got.entropy)
+
+
+@pytest.mark.parametrize("V", [300, 30011])
+def test_strides_alignments_and_in_place(cuda_device, V):
+    """Rows that start anywhere, gradients that lie elsewhere in their vectors, or over the logits."""
+    data = make(STAR40 if V < 1000 else MIXED, V, 8, same=True)
+    tree = STAR40 if V < 1000 else MIXED
+    N = sum(tree[1])
+    want = run(tree, data, cuda_device, entropy_coef=0.01)
+    check(tree, data, want, entropy_coef=0.01)
+    for off, wide, d_off in ((1, V + 5, 0), (8, V + 16, 8), (3, V + 3, 6), (0, V + 1, 0)):
+        room = torch.full((N, wide), 7.0, dtype=torch.bfloat16, device=cuda_device)
+        x = room[:, off:off + V] if off + V <= wide else room[:, :V]
+        x.copy_(data[0])
+        back = torch.full((N, V + 9), 5.0, dtype=torch.bfloat16, device=cuda_device)
+        out = back[:, d_off:d_off + V]
+        got = run(tree, data, cuda_device, x=x, dlogits=out, entropy_coef=0.01)
+        assert got.dlogits is out
+        check(tree, data, got, entropy_coef=0.01)
+        assert (back[:, :d_off] == 5).all() and (back[:, d_off + V:] == 5).all()
+        got = run(tree, data, cuda_device, x=x, dlogits=x, entropy_coef=0.01)
+        check(tree, data, got, entropy_coef=0.01)
+        left = room.clone()
+        left[:, off:off + V] = 7
+        assert (left == 7).all()
+    x = data[0].to(cuda_device)
+    got = run(tree, data, cuda_device, x=x, dlogits=x, entropy_coef=0.01)
+    assert torch.equal(x, want.dlogits) and torch.equal(got.loss, want.loss)
+
+
+def test_masked_logits(cuda_device):
+    for masked in (0.5, 0.999):
+        data = make(MIXED, 5000, 4, masked=masked, zero=0.0)
+        check(MIXED, data, run(MIXED, data, cuda_device, kl_coef=0.1, entropy_coef=0.1), kl_coef=0.1, entropy_coef=0.1)
+    data[0][:, 1:] = torch.finfo(torch.bfloat16).min          # masks of the lowest value, the targets at -inf:
+    data[1][:] = 0                                            # ratios of 0, nothing to learn from
+    data[2][:] = 0
+    data[0][:, 0] = -float("inf")
+    got = run(MIXED, data, cuda_device, use_ref=False, entropy_coef=0.1)
+    seen = got.entropy != 0
+    assert (got.logprobs == -float("inf")).all() and (got.dlogits == 0).all() and seen.sum() == 12
+    assert (got.entropy[seen] - np.log(4999)).abs().max() <= 2.0 ** -16 * 10
+    w, a = data[4].double().numpy(), np.repeat(data[3].double().numpy(), [len(i) - 1 for _, i in OL.trajectories(*MIXED)])
+    terms = w * (np.maximum(-0.8 * a, 0) - 0.1 * np.log(4999))
+    assert abs(float(got.loss) - terms.sum()) <= 2.0 ** -15 * np.abs(terms).sum()
+
+
+def test_one_token_left(cuda_device):
+    """Masks of the lowest value everywhere else: probability 1, entropy 0, no gradient; and -inf likewise."""
+    for low in (torch.finfo(torch.bfloat16).min, -float("inf")):
+        data = make(MIXED, 5000, 4, zero=0.0)
+        data[0][:, 1:] = low
+        data[1][:] = 0
+        data[2][:] = 0
+        got = run(MIXED, data, cuda_device, use_ref=False, entropy_coef=0.1)
+        assert (got.logprobs == 0).all() and (got.entropy == 0).all() and (got.dlogits == 0).all()
+
+
+def test_rows_without_weight_are_not_read(cuda_device):
+    """Whatever they hold: NaN logits, token ids, old log-probs and advantages of what has no weight."""
+    tree = ([-1, 0, 0], [5, 4, 3])
+    data = make(tree, 400, 9, zero=0.0)
+    want = run(tree, data, cuda_device, kl_coef=0.1)
+    x, tok, old, adv, w, ref = (t.clone() for t in data)
+    n0 = 8                                                    # the first trajectory's predictions
+    w[4:8] = 0                                                # its own rows: 5 .. 8 (the last predicts nothing)
+    w[[0, n0 + 0]] = 0                                        # the root's first row, in both
+    clean = run(tree, (x, tok, old, adv, w, ref), cuda_device, kl_coef=0.1)
+    check(tree, (x, tok, old, adv, w, ref), clean, kl_coef=0.1)
+    x[0] = float("nan")
+    x[5:9] = float("inf")
+    x[11] = float("nan")                                      # the second leaf's last token predicts nothing
+    tok[[1, 6, 7, 8]] = torch.tensor([-1, 400, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32)
+    old[[0, 5, n0]] = float("nan")
+    ref[[0, 6, n0]] = float("inf")
+    got = run(tree, (x, tok, old, adv, w, ref), cuda_device, kl_coef=0.1)
+    for a, b in zip(got, clean):
+        assert torch.equal(a, b)
+    assert not got.dlogits[[0, 5, 6, 7, 8, 11]].any() and want.dlogits[0].any()
+
+
+def test_rows_without_a_distribution(cuda_device):
+    """NaN, +inf or nothing but -inf in a row, and token ids out of range, give NaN there alone."""
+    tree = ([-1], [8])
+    data = make(tree, 3000, 10, zero=0.0)
+    clean = run(tree, data, cuda_device)
+    for how in range(4):
+        x, tok = data[0].clone(), data[1].clone()
+        if how == 3:
+            tok[3] = 3000
+        else:
+            x[2, 2999 if how else slice(None)] = (-float("inf"), float("inf"), float("nan"))[how]
+        got = run(tree, (x, tok, *data[2:]), cuda_device)
+        assert torch.isnan(got.loss) and torch.isnan(got.logprobs[2]) and torch.isnan(got.dlogits[2]).all()
+        keep = [0, 1, 3, 4, 5, 6, 7]
+        assert torch.equal(got.dlogits[keep], clean.dlogits[keep])
+        assert how == 3 or torch.isnan(got.entropy[2])
+
+
+def test_gradient_against_differences(cuda_device):
+    """Of the kernel's own loss, along random directions, steps of exact bf16 values."""
+    g = torch.Generator().manual_seed(3)
+    x, tok, old, adv, w, ref = make(WIDE, 40, 6, zero=0.0)
+    x = (x * 8).round().clamp(-24, 24) / 8                    # multiples of 1/8: +-1/16 stays exact
+    kw = dict(kl_coef=0.3, entropy_coef=0.2, clip_low=1.0, clip_high=float("inf"))
+    data = (x, tok, old, adv, w, ref)
+    d = run(WIDE, data, cuda_device, **kw).dlogits.double().cpu()
+    h = 2.0 ** -4
+    for _ in range(5):
+        s = (torch.randint(0, 2, x.shape, generator=g) * 2 - 1) * (torch.rand(x.shape, generator=g) < 0.02)
+        f = [float(run(WIDE, ((x + k * h * s).bfloat16(), *data[1:]), cuda_device, **kw).loss) for k in (2, 1, -1, -2)]
+        slope = (8 * (f[1] - f[2]) - (f[0] - f[3])) / (12 * h)       # error of order h^4 times the fifth derivative
+        exact = float((d * s).sum())
+        size = float((d.abs() * s.abs()).sum())
+        assert abs(slope - exact) <= 2.0 ** -7 * size + 2.0 ** -9 * float(w.abs().sum()), (slope, exact, size)
+
+
+def test_reproducible_and_debug_build(cuda_device):
+    data = make(STAR40, 20000, 12, same=True)
+    a = run(STAR40, data, cuda_device, kl_coef=0.1, entropy_coef=0.01)
+    for _ in range(3):
+        b = run(STAR40, data, cuda_device, kl_coef=0.1, entropy_coef=0.01)
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
+    with B.library(_build.build_library(debug=True)):
+        b = run(STAR40, data, cuda_device, kl_coef=0.1, entropy_coef=0.01)
+        torch.cuda.synchronize()
+        assert device_status() == 0
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+def test_on_sampled_tokens(cuda_device):
+    """What sampling says of a token is its old log-prob: every ratio is 1, so the loss is minus the mean
+    advantage and the gradient that of the log-probs."""
+    tree = ([-1, 0, 0], [6, 5, 7])
+    plan = TreePlan(*tree)
+    x, tok, *_ = make(tree, 2000, 13)
+    x = x.to(cuda_device)
+    nxt, lp = sample_tokens(x, torch.rand(18, device=cuda_device), top_k=50)
+    tok = tok.to(cuda_device)
+    _, ptr, at = TL.trajectories(plan)
+    rows = np.concatenate([at[ptr[i]:ptr[i + 1] - 1] for i in range(2)])
+    targets = np.concatenate([at[ptr[i] + 1:ptr[i + 1]] for i in range(2)])
+    keep = np.array([t != 11 for t in targets])               # the second child's first token is drawn beside the first's
+    tok[torch.from_numpy(targets[keep]).long()] = nxt[torch.from_numpy(rows[keep]).long()]
+    _, old = TL.traj_logprobs(plan, x, tok)
+    drawn = lp[torch.from_numpy(rows).long().to(cuda_device)]
+    assert (old - drawn)[torch.from_numpy(keep).to(cuda_device)].abs().max() <= 2.0 ** -13 * (1 + old.abs().max())
+    adv = torch.tensor([1.0, -0.5], device=cuda_device)
+    got = TL.policy_loss(plan, x, tok, old, adv)
+    n = [10, 12]
+    assert abs(float(got.loss) - -(n[0] - 0.5 * n[1]) / 22) <= 2.0 ** -10
+    assert (got.logprobs - old).abs().max() <= 2.0 ** -12 * (1 + old.abs().max())
+
+
+def test_capture_and_side_stream(cuda_device):
+    data = [t.to(cuda_device) for t in make(WIDE, 9000, 14, same=True)]
+    other = [t.to(cuda_device) for t in make(WIDE, 9000, 15, same=True)]
+    plan, plan2 = TreePlan(*WIDE), TreePlan(*WIDE)
+    call = lambda d, p=plan, **kw: TL.policy_loss(p, d[0], d[1], d[2], d[3], weights=d[4], ref_logprobs=d[5], kl_coef=0.1, **kw)  # noqa: E731
+    want = [call(d) for d in (data, other)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = call(data, plan2, stream=side)                      # a plan's first call
+    side.synchronize()
+    assert all(torch.equal(u, v) for u, v in zip(got, want[0]))
+    held = [t.clone() for t in data]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(held)
+        again = call(held, grad=False)
+    for d, w in ((other, want[1]), (data, want[0])):
+        for a, b in zip(held, d):
+            a.copy_(b)
+        graph.replay()
+        assert all(torch.equal(u, v) for u, v in zip(out, w))
+        assert torch.equal(again.loss, w.loss)
+
+
+def test_rows_behind_32_bit_offsets(cuda_device):
+    """A row that starts beyond 2^32 bytes, element offsets beyond 2^31."""
+    N, V = 17000, 152064
+    tree = ([-1], [N])
+    plan = TreePlan(*tree)
+    x = torch.empty((N, V), dtype=torch.bfloat16, device=cuda_device)
+    g = torch.Generator(cuda_device).manual_seed(2)
+    for i in range(0, N, 2000):
+        x[i:i + 2000] = torch.randn((min(2000, N - i), V), device=cuda_device, generator=g)
+    tok = torch.randint(0, V, (N,), device=cuda_device, generator=g, dtype=torch.int32)
+    w = torch.zeros(N - 1, device=cuda_device)
+    rows = [0, 14123, 16998]
+    w[rows] = 1
+    adv = torch.tensor([2.0], device=cuda_device)
+    d = TL.policy_loss(plan, x, tok, None, adv, weights=w).dlogits
+    live = d.float().abs().amax(1) > 0
+    assert torch.nonzero(live).flatten().tolist() == rows
+    for r in rows:
+        p = torch.softmax(x[r].double(), 0)
+        p[int(tok[r + 1])] -= 1
+        e = (d[r].double() - 2 * p).abs()
+        assert (e <= 2.0 ** -8 * 2 * p.abs() + 2.0 ** -14 * p.abs()).all()
