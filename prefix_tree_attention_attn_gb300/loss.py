@@ -132,6 +132,15 @@ def policy_workspace(plan: TreePlan) -> int:
     return int(b.value)
 
 
+def _policy_sizes(plan: TreePlan):
+    """(trajectories, shape of the predictions, workspace bytes): a plan does not change, asked once."""
+    sizes = getattr(plan, "_policy_sizes", None)
+    if sizes is None:
+        nl, ne = trajectory_info(plan)
+        sizes = plan._policy_sizes = nl, (ne - nl,), policy_workspace(plan)
+    return sizes
+
+
 def policy_loss(plan: TreePlan, logits, tokens, old_logprobs, advantages, weights=None, ref_logprobs=None,
                 per_token: bool = False, clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
                 entropy_coef: float = 0.0, grad: bool = True, grad_scale: float = 1.0, dlogits=None, workspace=None,
@@ -148,8 +157,7 @@ def policy_loss(plan: TreePlan, logits, tokens, old_logprobs, advantages, weight
     N = plan.n_tokens
     stride = _check_matrix(logits, "logits", N, dev)
     V = logits.shape[1]
-    nl, ne = trajectory_info(plan)
-    n_pred = (ne - nl,)
+    nl, n_pred, need = _policy_sizes(plan)
     _check_dense(tokens, "tokens", (N,), torch.int32, dev)
     _check_dense(advantages, "advantages", n_pred if per_token else (nl,), torch.float32, dev)
     s = B.Policy(None, advantages.data_ptr(), None, None, int(bool(per_token)), clip_low, clip_high, kl_coef,
@@ -177,7 +185,7 @@ def policy_loss(plan: TreePlan, logits, tokens, old_logprobs, advantages, weight
         if dlogits.shape != logits.shape:
             raise ValueError(f"dlogits: expected {tuple(logits.shape)}, got {tuple(dlogits.shape)}")
     if workspace is None:
-        workspace = _empty(side, (policy_workspace(plan),), torch.uint8, logits.device)
+        workspace = _empty(side, (need,), torch.uint8, logits.device)
     elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected contiguous cuda:{dev} uint8, got {workspace.device} {workspace.dtype}")
     f32 = (torch.float32, logits.device)
