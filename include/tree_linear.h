@@ -83,6 +83,49 @@ int tree_attn_linear_bwd(tree_attn_plan_t plan, const void* q, const void* k, co
                          void* dq, void* dk, void* dv, const float* decay, int32_t hq, int32_t hkv, int32_t d,
                          float scale, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- growing a tree -------------------------------------------------------------------------
+ * The state of a branch of a growing tree is kept in a slot of a pool
+ *
+ *   states fp32 [n_slots, hkv, d, d]   S[key feature][value feature] = sum_j gamma^(distance) k_j v_j^T
+ *
+ * so whole turns are brought in by tree_attn_linear_prefill, tokens one at a time by
+ * tree_attn_linear_step, and a branch forks by writing to another slot than it reads (HARTS
+ * abstract: the recurrent state is carried from a shared prefix into every branch).  Slot tables
+ * are int32 device arrays; a number outside [-1, n_slots) records TREE_ATTN_ERR_INVALID_SLOT in the
+ * device status word and counts as -1.  A decay outside (0, 1] is recorded as above. */
+
+/* Device status only (tree_attn_get_device_status). */
+#define TREE_ATTN_ERR_INVALID_SLOT -16
+
+/* tree_attn_linear_fwd of a tree or forest of fresh tokens that continues stored states: the path of
+ * a token begins, before its root's first token, with the state in slot_in[root] (node ids; -1: a
+ * zero state; other nodes' entries are not read), and a node with slot_out[node] >= 0 leaves its
+ * last state in that slot.  Either table may be NULL: -1 throughout.  The slots of slot_out are
+ * all different, and none is read by another tree's root (the call's results would depend on which
+ * comes first); a tree may leave a state in the slot that its own root started from.
+ *
+ * States are exact to fp32 rounding: gamma^n v is split into three bf16 numbers for the tensor
+ * cores.  In O each of the two parts, over the chunk and over what came before, meets one
+ * rounding to bf16 before the output's own (chunked scores, entering state).  Non-finite values of a
+ * node's keys or values reach that node and its descendants alone.  Same workspace and argument
+ * rules as tree_attn_linear_fwd; d = 128. */
+int tree_attn_linear_prefill(tree_attn_plan_t plan, const void* q, const void* k, const void* v, void* o, float* states,
+                             int32_t n_slots, const int32_t* slot_in, const int32_t* slot_out, const float* decay,
+                             int32_t hq, int32_t hkv, int32_t d, float scale, void* workspace, size_t ws_bytes,
+                             void* stream);
+
+/* One token of each of n_rows branches:
+ *   S = gamma states[slot_in[r]] + k_r v_r^T,  o_r = scale q_r^T S,  states[slot_out[r]] = S
+ * slot_in[r] = -1: a zero state; slot_out[r] = -1: a padding row, of which nothing is read or
+ * written.  The slots of slot_out are all different, and none is another row's slot_in: rows run
+ * at the same time.  Several rows may start from one slot (a fork).  q, k, v bf16, row r at element
+ * r * stride (multiples of 8, at least heads * d), o bf16 [n_rows, hq, d]; d 64 or 128.  fp32
+ * throughout, o rounded once.  No workspace; n_rows = 0 does nothing. */
+int tree_attn_linear_step(float* states, int32_t n_slots, const int32_t* slot_in, const int32_t* slot_out, const void* q,
+                          const void* k, const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride, void* o,
+                          const float* decay, int64_t n_rows, int32_t hq, int32_t hkv, int32_t d, float scale,
+                          void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -165,3 +165,40 @@ def backward_recurrent(parent, seg_len, q, k, v, do, decay, scale):
             dk[t, g] = R[t] @ v[t, g]
             dv[t, g] = R[t].T @ k[t, g]
     return dq, dk, dv
+
+
+def from_states(parent, seg_len, q, k, v, decay, scale, start, chunk=128):
+    """The recursion node by node, token by token, from given states: ``start[u]`` [hkv, d, d] or
+    None for each root u.  Returns (o [N, hq, d], end state of every node, sums of magnitudes of
+    the terms of o as two matrices are formed for it -- the scores and values of a token's chunk,
+    the query and the state that enters the chunk --, the states' sums of magnitudes)."""
+    q, k, v = _as64(q), _as64(k), _as64(v)
+    gam = np.asarray(decay, dtype=np.float64)
+    N, hq, d = q.shape
+    hkv = k.shape[1]
+    G = hq // hkv
+    order, off, _ = layout.packed_layout(parent, seg_len)
+    o, size = np.zeros((N, hq, d)), np.zeros((N, hq, d))
+    end, mass = {}, {}
+    for u in order:
+        p = parent[u]
+        if p >= 0:
+            S, A = end[p].copy(), mass[p].copy()
+        else:
+            S = np.zeros((hkv, d, d)) if start[u] is None else np.asarray(start[u], dtype=np.float64).copy()
+            A = np.abs(S)
+        for i in range(seg_len[u]):
+            t = off[u] + i
+            if i % chunk == 0:
+                entering, first = S.copy(), t
+            S = gam[:, None, None] * S + k[t][:, :, None] * v[t][:, None, :]
+            A = gam[:, None, None] * A + np.abs(k[t])[:, :, None] * np.abs(v[t])[:, None, :]
+            lag = t - np.arange(first, t + 1)
+            for h in range(hq):
+                g = h // G
+                o[t, h] = scale * q[t, h] @ S[g]
+                w = gam[g] ** lag
+                size[t, h] = scale * ((w * np.abs(k[first:t + 1, g] @ q[t, h])) @ np.abs(v[first:t + 1, g]) +
+                                      gam[g] ** (t - first + 1) * np.abs(q[t, h]) @ np.abs(entering[g]))
+        end[u], mass[u] = S, A
+    return o, end, size, mass

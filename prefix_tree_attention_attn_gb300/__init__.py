@@ -57,7 +57,7 @@ class TreePlan:
         B.check(self._lib.tree_attn_plan(_ptr_i32(par), _ptr_i32(sl), len(par), C.byref(opts), C.byref(h)),
                 "tree_attn_plan")
         self._h = h
-        self.seg_len = sl
+        self.seg_len, self.parent = sl, par.copy()
         inf = B.PlanInfo()
         B.check(self._lib.tree_attn_plan_info(h, C.byref(inf)), "tree_attn_plan_info")
         self.info = {f: getattr(inf, f) for f, _ in B.PlanInfo._fields_}

@@ -104,6 +104,12 @@ SIGNATURES = {
     "tree_attn_linear_bwd": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
                                        C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_int32,
                                        C.c_float, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "tree_attn_linear_prefill": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                           C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32,
+                                           C.c_int32, C.c_float, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "tree_attn_linear_step": (C.c_int, [C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                        C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p,
+                                        C.c_int64, C.c_int32, C.c_int32, C.c_int32, C.c_float, C.c_void_p]),
     # include/tree_decode.h
     "tree_attn_decode_plan": (C.c_int, [c_int32_p, c_int32_p, c_int32_p, C.c_int32, c_int32_p, C.c_int32, c_uint8_p,
                                         c_int32_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.POINTER(DecodeOpts),

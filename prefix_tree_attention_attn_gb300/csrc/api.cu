@@ -12,6 +12,7 @@
 #include "kernels.h"
 #include "plan.h"
 #include "tree_decode.h"
+#include "tree_linear.h"
 #include "tree_sample.h"
 
 namespace treeattn {
@@ -700,6 +701,7 @@ const char* tree_attn_strerror(int s) {
         case TREE_ATTN_ERR_INVALID_DECAY: return "linear-attention decay outside (0, 1]";
         case TREE_ATTN_ERR_DEVICE_BOUNDS: return "a debug bounds check failed";
         case TREE_ATTN_ERR_CACHE_FULL: return "a token was appended to a node without room";
+        case TREE_ATTN_ERR_INVALID_SLOT: return "a state slot outside the pool";
         case TREE_ATTN_ERR_INVALID_SAMPLING: return "invalid sampling parameters of a row";
         default:
             // status words with a site: code - 1000 * site

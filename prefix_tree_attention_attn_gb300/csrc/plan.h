@@ -46,6 +46,7 @@ struct DevicePlan {
                                    //   1 if the last child of its parent}
     int32_t* lvl_nodes = nullptr;  // packed nodes by depth (LinInfo::lvl_ptr gives each depth's range)
     int32_t* kids = nullptr;       // [n_nodes+1] child offsets, then the children in packed order
+    int32_t* lin_ids = nullptr;    // [n_nodes] node id of each packed node
     bool lin_ready = false;
 };
 

@@ -1,0 +1,261 @@
+"""Linear attention from and to states in slots (include/tree_linear.h): whole turns and single
+tokens, against the fp64 oracle.
+
+Tolerances, from the arithmetic.  Step: k v^T is within 2^-24 of itself, its sum with gamma S within
+2^-24 of the result: together below 2^-23 of |gamma S| + |k v|.  o sums d products in fp32: within
+(d + 8) 2^-24 of the sum of their magnitudes, then 2^-8 of itself.  Prefill: an increment sums 3 * 128
+products on the tensor cores, each addition within 2^-23 of the sum of magnitudes; a power
+2^(n log2 gamma) is within 2^-22 (1 + n |log2 gamma|) of itself, and where n |log2 gamma| > 24 it does
+not count; chunks and nodes add as much again once for each of fewer than 16 chunks: states within
+2^-13 of their sums of magnitudes.  o: one rounding to bf16 of each of its two parts, within 2^-8 of the
+magnitudes that are multiplied, 2^-12 for everything in fp32, and 2^-8 of itself.  (The
+rows of a decay below 2^(-100/128) round the scaled query too: 2^-8 of the entering part once more.)"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import layout as OL
+from oracle import linear as OLN
+from prefix_tree_attention_attn_gb300 import TreePlan, device_status
+from prefix_tree_attention_attn_gb300 import linear as TL
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _lib(lib, cuda_device):
+    yield
+    torch.cuda.synchronize()
+    assert device_status() == 0
+
+
+def num(t):
+    return t.double().cpu().numpy()
+
+
+def draw(seed, N, hq, hkv, d, device, size=1.0):
+    g = torch.Generator(device).manual_seed(seed)
+    make = lambda *s: (torch.randn(s, device=device, generator=g) * size).bfloat16()  # noqa: E731
+    return make(N, hq, d), make(N, hkv, d), make(N, hkv, d)
+
+
+def decays(hkv, device, values=(1.0, 0.9, 0.99, 0.999)):
+    return torch.tensor([values[i % len(values)] for i in range(hkv)], device=device)
+
+
+def check_prefill(parent, seg, hq, hkv, device, seed=1, slot_in=None, slot_out=None, values=(1.0, 0.9, 0.99, 0.999), n_slots=9):
+    N, n = sum(seg), len(parent)
+    q, k, v = draw(seed, N, hq, hkv, 128, device)
+    dec = decays(hkv, device, values)
+    g = torch.Generator(device).manual_seed(seed + 100)
+    states = torch.randn((n_slots, hkv, 128, 128), device=device, generator=g) * 3
+    before = states.clone()
+    slot_in = [-1] * n if slot_in is None else slot_in
+    slot_out = list(range(n)) if slot_out is None else slot_out
+    plan = TreePlan(parent, seg)
+    o = TL.tree_linear_prefill(plan, states, TL.StateSlots(slot_in, slot_out, n_slots), q, k, v, dec, 0.125)
+    start = [num(before[s]) if p < 0 and s >= 0 else None for p, s in zip(parent, slot_in)]
+    want, end, size, mass = OLN.from_states(parent, seg, num(q), num(k), num(v), num(dec), 0.125, start)
+    wide = 2 if min(values) < 0.58 else 1
+    lim = 2.0 ** -8 * np.abs(want) + (wide * 2.0 ** -8 + 2.0 ** -12) * size + 1e-30
+    e = np.abs(num(o) - want)
+    assert (e <= lim).all(), (np.unravel_index(np.argmax(e / lim), e.shape), (e / lim).max())
+    for u in range(n):
+        if slot_out[u] >= 0:
+            e = np.abs(num(states[slot_out[u]]) - end[u])
+            assert (e <= 2.0 ** -13 * mass[u] + 1e-30).all(), (u, (e / mass[u]).max())
+    kept = [s for s in range(n_slots) if s not in slot_out]
+    assert torch.equal(states[kept], before[kept])
+    return o, states
+
+
+@pytest.mark.parametrize("parent,seg,hq,hkv", [
+    ([-1], [1], 2, 1),
+    ([-1], [300], 2, 2),
+    ([-1, 0, 0], [127, 129, 1], 8, 2),
+    ([-1, 0, 0, 1, 1, 2], [128, 200, 5, 64, 300, 33], 4, 1),
+    ([-1, 0, 1, -1, 3], [70, 60, 5, 257, 2], 3, 3),
+    ([-1] + [0] * 8, [50] + [(17 * i) % 140 + 1 for i in range(8)], 4, 4),
+])
+def test_prefill_from_zero(cuda_device, parent, seg, hq, hkv):
+    check_prefill(parent, seg, hq, hkv, cuda_device)
+
+
+def test_prefill_continues_states(cuda_device):
+    # two trees from stored states, one from nothing; some states not kept, one left in the slot it came from
+    parent, seg = [-1, 0, 0, -1, -1, 3], [130, 17, 260, 33, 128, 5]
+    check_prefill(parent, seg, 4, 2, cuda_device, 5, slot_in=[7, 7, -1, 2, -1, 0], slot_out=[-1, 7, 3, -1, 0, 2])
+    # two trees fork one state
+    check_prefill([-1, -1], [40, 150], 2, 2, cuda_device, 6, slot_in=[8, 8], slot_out=[1, 0])
+    check_prefill([-1], [5], 2, 2, cuda_device, 7, slot_in=[4], slot_out=[4])
+    check_prefill([-1, 0], [5, 6], 2, 2, cuda_device, 7, slot_in=[4, -1], slot_out=[-1, -1])
+
+
+@pytest.mark.parametrize("values", [(0.58, 0.585), (0.5, 0.1), (0.001, 1.0), (2.0 ** -100, 0.57)])
+def test_prefill_strong_decays(cuda_device, values):
+    check_prefill([-1, 0, 0], [150, 129, 40], 4, 2, cuda_device, 8, slot_in=[3, -1, -1], values=values)
+
+
+def test_prefill_deep_tree(cuda_device):
+    # 40 nested nodes: deeper than the scans by depth take; states on the way, and a second root
+    n = 40
+    parent, seg = [-1] + list(range(n - 1)) + [-1], [(37 * i) % 30 + 1 for i in range(n)] + [12]
+    check_prefill(parent, seg, 2, 1, cuda_device, 9, slot_in=[1] + [-1] * (n - 1) + [0],
+                  slot_out=[-1] * 20 + [2] + [-1] * (n - 22) + [1, 5])
+
+
+def test_prefill_in_two_turns_is_the_whole(cuda_device):
+    """A prompt, then its branches from the prompt's state: the outputs of the tree brought in at once, and the
+    same states, within the bounds of one more rounding of what enters."""
+    parent, seg = [-1, 0, 0], [200, 90, 140]
+    q, k, v = draw(11, 430, 4, 2, 128, cuda_device)
+    dec = decays(2, cuda_device, (0.97, 1.0))
+    whole, parts = (torch.zeros((3, 2, 128, 128), device=cuda_device) for _ in range(2))
+    o = TL.tree_linear_prefill(TreePlan(parent, seg), whole, TL.StateSlots([-1] * 3, [0, 1, 2], 3), q, k, v, dec, 0.1)
+    a = TL.tree_linear_prefill(TreePlan([-1], [200]), parts, TL.StateSlots([-1], [0], 3), q[:200].contiguous(),
+                               k[:200].contiguous(), v[:200].contiguous(), dec, 0.1)
+    b = TL.tree_linear_prefill(TreePlan([-1, -1], [90, 140]), parts, TL.StateSlots([0, 0], [1, 2], 3), q[200:].contiguous(),
+                               k[200:].contiguous(), v[200:].contiguous(), dec, 0.1)
+    assert torch.equal(o, torch.cat([a, b])) and torch.equal(whole, parts)
+
+
+def test_prefill_keeps_other_branches_clean(cuda_device):
+    """Infinities and NaN in one branch reach it and its descendants alone, whatever lies beside it in a tile."""
+    parent, seg = [-1, 0, 0, 2, 0], [30, 21, 35, 9, 77]
+    q, k, v = draw(12, 172, 2, 1, 128, cuda_device)
+    for value in (float("inf"), float("nan")):
+        for values in ((0.99,), (0.3,)):
+            run = lambda k, v: (st := torch.zeros((5, 1, 128, 128), device=cuda_device),  # noqa: E731
+                                TL.tree_linear_prefill(TreePlan(parent, seg), st, TL.StateSlots([-1] * 5, range(5), 5), q, k, v,
+                                                       decays(1, cuda_device, values), 0.1))
+            st0, o0 = run(k, v)
+            k2, v2 = k.clone(), v.clone()
+            k2[51:86, 0, 3], v2[51:86, 0, 100] = value, value          # node 2; node 3 is below it
+            st, o = run(k2, v2)
+            rows = [*range(51), *range(95, 172)]
+            assert torch.equal(o[rows], o0[rows]) and torch.equal(st[[0, 1, 4]], st0[[0, 1, 4]])
+            assert not torch.isfinite(st[2]).all() and not torch.isfinite(st[3]).all()
+
+
+def check_step(R, hq, hkv, d, device, seed, slot_in, slot_out, n_slots, strided=False):
+    g = torch.Generator(device).manual_seed(seed)
+    states = torch.randn((n_slots, hkv, d, d), device=device, generator=g) * 4
+    before = states.clone()
+    if strided:                                                        # rows of one fused projection
+        x = torch.randn((R, (hq + 2 * hkv) * d + 8), device=device, generator=g).bfloat16()
+        q, k, v = (x[:, a:b].view(R, -1, d) for a, b in ((0, hq * d), (hq * d, (hq + hkv) * d), ((hq + hkv) * d, (hq + 2 * hkv) * d)))
+    else:
+        q, k, v = draw(seed, R, hq, hkv, d, device)
+    dec = decays(hkv, device)
+    slots = TL.StateSlots(slot_in, slot_out, n_slots)
+    o = torch.full((R, hq, d), 7.0, dtype=torch.bfloat16, device=device)
+    assert TL.tree_linear_step(states, slots, q, k, v, dec, 0.2, o=o) is o
+    gam = num(dec)[:, None, None]
+    for r in range(R):
+        if slot_out[r] < 0:
+            assert (o[r] == 7).all()
+            continue
+        S0 = num(before[slot_in[r]]) if slot_in[r] >= 0 else np.zeros((hkv, d, d))
+        kv = num(k[r])[:, :, None] * num(v[r])[:, None, :]
+        S = gam * S0 + kv
+        assert (np.abs(num(states[slot_out[r]]) - S) <= 2.0 ** -23 * (np.abs(gam * S0) + np.abs(kv)) + 1e-37).all()
+        S, A = np.repeat(S, hq // hkv, 0), np.repeat(np.abs(gam * S0) + np.abs(kv), hq // hkv, 0)
+        want, size = (0.2 * np.einsum("hk,hkv->hv", f(num(q[r])), x) for f, x in ((lambda y: y, S), (np.abs, A)))
+        e = np.abs(num(o[r]) - want)
+        assert (e <= 2.0 ** -8 * np.abs(want) + (d + 8) * 2.0 ** -24 * size).all()
+    kept = [s for s in range(n_slots) if s not in list(slot_out)]
+    assert torch.equal(states[kept], before[kept])
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(2, 2, 64), (32, 8, 128), (8, 1, 128), (14, 2, 128), (12, 4, 64), (5, 5, 128), (20, 1, 64)])
+def test_step(cuda_device, hq, hkv, d):
+    check_step(1, hq, hkv, d, cuda_device, 1, [0], [0], 1)
+    check_step(1, hq, hkv, d, cuda_device, 2, [-1], [2], 4)
+    check_step(5, hq, hkv, d, cuda_device, 3, [3, 3, 3, 1, -1], [0, 4, -1, 1, 6], 8)       # forks, padding, in place, new
+    check_step(3, hq, hkv, d, cuda_device, 4, [2, 0, 1], [2, 0, 1], 3, strided=True)
+    R = 1 + 400 // hkv
+    perm = np.random.default_rng(5).permutation(R + 3)
+    check_step(R, hq, hkv, d, cuda_device, 5, perm[:R], perm[:R], R + 3)
+
+
+def test_steps_continue_a_prefill(cuda_device):
+    """A turn brought in at once and the same turn token by token leave the same states and give the same outputs:
+    each within its own bounds of the oracle."""
+    seg, hq, hkv = 70, 4, 2
+    q, k, v = draw(21, seg, hq, hkv, 128, cuda_device)
+    dec = decays(hkv, cuda_device, (0.95, 1.0))
+    states = torch.randn((2, hkv, 128, 128), device=cuda_device)
+    start = num(states[0])
+    o = TL.tree_linear_prefill(TreePlan([-1], [seg]), states, TL.StateSlots([0], [1], 2), q, k, v, dec, 0.1)
+    slots = TL.StateSlots([0], [0], 2)
+    steps = torch.cat([TL.tree_linear_step(states, slots, q[i:i + 1], k[i:i + 1], v[i:i + 1], dec, 0.1) for i in range(seg)])
+    want, end, size, mass = OLN.from_states([-1], [seg], num(q), num(k), num(v), num(dec), 0.1, [start])
+    assert (np.abs(num(states[0]) - end[0]) <= seg * 2.0 ** -23 * mass[0]).all()
+    assert (np.abs(num(states[1]) - end[0]) <= 2.0 ** -13 * mass[0]).all()
+    whole = 0.1 * np.einsum("thk,hkv->thv", np.abs(num(q)), np.repeat(mass[0], hq // hkv, 0)) + size
+    assert (np.abs(num(steps) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -15 * whole).all()
+    assert (np.abs(num(o) - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 2.0 ** -12) * size).all()
+
+
+def test_step_capture_and_side_stream(cuda_device):
+    R, hq, hkv = 9, 8, 2
+    q, k, v = draw(31, R, hq, hkv, 128, cuda_device)
+    dec, slots = decays(hkv, cuda_device), TL.StateSlots(range(R), range(R), R)
+    first = torch.randn((R, hkv, 128, 128), device=cuda_device)
+    a, b, c = first.clone(), first.clone(), first.clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = TL.tree_linear_step(c, slots, q, k, v, dec, 0.1, stream=side)      # the tables' first use
+    side.synchronize()
+    want = TL.tree_linear_step(a, slots, q, k, v, dec, 0.1)
+    assert torch.equal(got, want) and torch.equal(a, c)
+    plan, ws = TreePlan([-1] * R, [7] * R), None
+    pq, pk, pv = draw(32, 7 * R, hq, hkv, 128, cuda_device)
+    op = TL.tree_linear_prefill(plan, a, slots, pq, pk, pv, dec, 0.1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = TL.tree_linear_step(b, slots, q, k, v, dec, 0.1)
+        o2 = TL.tree_linear_prefill(plan, b, slots, pq, pk, pv, dec, 0.1, workspace=ws)
+    graph.replay()
+    assert torch.equal(o, want) and torch.equal(o2, op) and torch.equal(a, b)
+    for _ in range(3):
+        want = TL.tree_linear_step(a, slots, q, k, v, dec, 0.1)
+        op = TL.tree_linear_prefill(plan, a, slots, pq, pk, pv, dec, 0.1)
+        graph.replay()
+        assert torch.equal(o, want) and torch.equal(o2, op) and torch.equal(a, b)
+
+
+def test_notices(cuda_device, lib):
+    """Slot numbers outside the pool and decays outside (0, 1], past the binding's own checks."""
+    q, k, v = draw(41, 3, 2, 1, 128, cuda_device)
+    states = torch.zeros((2, 1, 128, 128), device=cuda_device)
+    o = torch.full((3, 2, 128), 5.0, dtype=torch.bfloat16, device=cuda_device)
+    dec = torch.tensor([0.9], device=cuda_device)
+
+    def step(slot_in, slot_out, decay):
+        a, b = (torch.tensor(x, dtype=torch.int32, device=cuda_device) for x in (slot_in, slot_out))
+        assert lib.tree_attn_linear_step(states.data_ptr(), 2, a.data_ptr(), b.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                         256, 128, 128, o.data_ptr(), decay.data_ptr(), 3, 2, 1, 128, 1.0, None) == 0
+        torch.cuda.synchronize()
+        return device_status()
+
+    torch.cuda.synchronize()
+    assert step([0, -1, -1], [0, 2, -5], dec) == TL.ERR_INVALID_SLOT
+    assert (o[1:] == 5).all() and not (o[0] == 5).any() and not states[1].any()
+    states.fill_(1)
+    assert step([2 ** 30, -1, -1], [1, -1, -1], dec) == TL.ERR_INVALID_SLOT
+    kv = k[0, 0].float()[:, None] * v[0, 0].float()[None]
+    assert torch.equal(states[1, 0], kv)                               # as from a zero state
+    assert step([0, -1, -1], [0, -1, -1], torch.tensor([1.5], device=cuda_device)) == -12
+    assert step([0, -1, -1], [0, -1, -1], torch.tensor([float("nan")], device=cuda_device)) == -12
+    plan = TreePlan([-1, 0], [2, 1])
+    bad = torch.tensor([-1, 2], dtype=torch.int32, device=cuda_device)
+    none = torch.tensor([-1, -1], dtype=torch.int32, device=cuda_device)
+    ws = torch.empty(TL.prefill_workspace(plan, 1, 128), dtype=torch.uint8, device=cuda_device)
+    states.fill_(3)
+    assert lib.tree_attn_linear_prefill(plan.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), states.data_ptr(), 2,
+                                        none.data_ptr(), bad.data_ptr(), dec.data_ptr(), 2, 1, 128, 1.0, ws.data_ptr(),
+                                        ws.numel(), None) == 0
+    torch.cuda.synchronize()
+    assert device_status() == TL.ERR_INVALID_SLOT and (states == 3).all()
