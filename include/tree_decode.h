@@ -161,6 +161,22 @@ int tree_attn_decode(tree_decode_plan_t plan, const int32_t* lens, const void* q
                      const void* v8, const float* k_scale, const float* v_scale, void* o, float* lse,
                      float softmax_scale, void* workspace, size_t ws_bytes, void* stream);
 
+/* Copy whole pages inside one or several caches of the same shape (one per layer, say): page
+ * src[i] to page dst[i] of every cache, codes and scales, in one launch for up to 32 caches and 1,024 pages.
+ * A node branches at token s < its length without moving what others read: its full pages below
+ * s stay, a new node gets a copy of the page that holds token s and the tokens of it below s as its
+ * length; the old node's later pages become a node of their own beside it.  (Slots behind a
+ * node's last token are never read; a copied page's scale covers all that was in it.)  The same
+ * call moves pages when a pool is compacted.
+ *   k8, v8, k_scale, v_scale   host arrays of n_caches device pointers, read during the call
+ *   src, dst                   host arrays of n page numbers in [0, n_pages), read during the call.
+ *                              dst are all different and none of them is a source: INVALID_ARG
+ *                              otherwise.  A page may be copied to several.
+ * No plan, no workspace; may be captured.  Asynchronous on `stream`. */
+int tree_attn_cache_copy(int32_t n_caches, void* const* k8, void* const* v8, float* const* k_scale,
+                         float* const* v_scale, int32_t n_pages, int32_t hkv, int32_t d, const int32_t* src,
+                         const int32_t* dst, int64_t n, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

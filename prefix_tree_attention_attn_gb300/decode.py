@@ -8,6 +8,7 @@ nodes' new tokens over it.  Marshalling only.
     tree_cache_write(plan, cache, k, v)                    # the fresh nodes' tokens, e.g. of a prefill
     tree_cache_append(plan, cache, lens, k1, v1)           # one new token per query, lens grows
     o, lse = tree_decode(plan, cache, lens, q, scale)      # q [R, hq, d] bf16
+    tree_cache_copy([cache, ...], src, dst)                # pages of a branch inside a page, of a compaction
 
 A plan stays valid while its nodes grow inside their capacity, so a whole
 segment is decoded with one plan; branching makes a new plan over the same
@@ -277,3 +278,66 @@ def tree_decode(plan: DecodePlan, cache: TreeCache, lens, q, softmax_scale: floa
     if st:
         B.check(st, "tree_attn_decode")
     return o, lse
+
+
+def tree_cache_copy(caches, src, dst, stream=None) -> None:
+    """Copy pages ``src[i]`` to ``dst[i]`` (codes and scales) in one cache, or in each of several
+    of the same shape, e.g. one per layer (``tree_attn_cache_copy``): what a branch inside a page,
+    or a compaction (``PagePool.compact``), asks for.  The targets are all different and no sources."""
+    caches = [caches] if isinstance(caches, TreeCache) else list(caches)
+    if not caches:
+        raise ValueError("caches: none given")
+    dev, c0 = _current_device(), caches[0]
+    for c in caches:
+        if (c.n_pages, c.hkv, c.d) != (c0.n_pages, c0.hkv, c0.d):
+            raise ValueError(f"caches: [{c.n_pages}, {c.hkv}, {PAGE}, {c.d}] beside [{c0.n_pages}, {c0.hkv}, {PAGE}, {c0.d}]")
+        if c.device.index != dev:
+            raise ValueError(f"cache: on {c.device}, the current device is cuda:{dev}")
+    a, b = _i32(src), _i32(dst)
+    if a.ndim != 1 or a.shape != b.shape:
+        raise ValueError("src and dst must be 1-D arrays of equal length")
+    n = len(caches)
+    arrays = [(C.c_void_p * n)(*col) for col in zip(*(c._ptrs for c in caches))]
+    st = B.load().tree_attn_cache_copy(n, *arrays, c0.n_pages, c0.hkv, c0.d, _ptr_i32(a), _ptr_i32(b), len(a),
+                                       _stream_of(_side(stream), dev, *(t for c in caches for t in c._tensors)))
+    if st:
+        B.check(st, "tree_attn_cache_copy")
+
+
+class PagePool:
+    """Which pages of a pool are in use (host only): the lowest free pages are given out first."""
+
+    def __init__(self, n_pages: int):
+        if not 0 <= n_pages < 2 ** 31:
+            raise ValueError(f"n_pages: {n_pages} is not a number of pages")
+        self.n_pages, self._used = int(n_pages), np.zeros(n_pages, bool)
+
+    @property
+    def n_free(self) -> int:
+        return self.n_pages - int(self._used.sum())
+
+    def alloc(self, n: int) -> np.ndarray:
+        """``n`` free pages, ascending; ``MemoryError`` where there are fewer."""
+        free = np.flatnonzero(~self._used)[:n]
+        if n < 0 or len(free) < n:
+            raise MemoryError(f"{n} pages asked for, {self.n_free} free")
+        self._used[free] = True
+        return free.astype(np.int32)
+
+    def free(self, pages) -> None:
+        """Give pages back; refused for a page that is not in use, or given twice."""
+        p = _i32(pages).reshape(-1)
+        if p.size and (p.min() < 0 or p.max() >= self.n_pages or not self._used[p].all() or np.unique(p).size != p.size):
+            raise ValueError("pages: each must be in use, and given once")
+        self._used[p] = False
+
+    def compact(self):
+        """Move the pages in use to the lowest numbers: (src, dst, page), the moves that
+        ``tree_cache_copy`` has to make and every page's new number (``pages = page[pages]``).  Pages
+        below the number of pages in use stay where they are."""
+        n = int(self._used.sum())
+        src, dst = np.flatnonzero(self._used[n:]) + n, np.flatnonzero(~self._used[:n])
+        page = np.arange(self.n_pages, dtype=np.int32)
+        page[src] = dst
+        self._used[:n], self._used[n:] = True, False
+        return src.astype(np.int32), dst.astype(np.int32), page
