@@ -107,8 +107,10 @@ int tree_attn_linear_bwd(tree_attn_plan_t plan, const void* q, const void* k, co
  * States are exact to fp32 rounding: gamma^n v is split into three bf16 numbers for the tensor
  * cores.  In O each of the two parts, over the chunk and over what came before, meets one
  * rounding to bf16 before the output's own (chunked scores, entering state).  Non-finite values of a
- * node's keys or values reach that node and its descendants alone.  Same workspace and argument
- * rules as tree_attn_linear_fwd; d = 128. */
+ * node's keys or values reach that node and its descendants alone.  Argument rules as
+ * tree_attn_linear_fwd; d = 128; workspace of its own size. */
+int tree_attn_linear_prefill_workspace_size(tree_attn_plan_t plan, int32_t hkv, int32_t d, size_t* ws_bytes);
+
 int tree_attn_linear_prefill(tree_attn_plan_t plan, const void* q, const void* k, const void* v, void* o, float* states,
                              int32_t n_slots, const int32_t* slot_in, const int32_t* slot_out, const float* decay,
                              int32_t hq, int32_t hkv, int32_t d, float scale, void* workspace, size_t ws_bytes,

@@ -86,6 +86,10 @@ int make_tensor_map(CUtensorMap* m, const void* base, int64_t rows, int heads, i
     return make_tmap(m, base, rows, heads, d);
 }
 
+int make_tensor_map_rows(CUtensorMap* m, const void* base, int64_t rows, int heads, int d, int box_rows) {
+    return make_tmap(m, base, rows, heads, d, false, box_rows);
+}
+
 int make_byte_map(CUtensorMap* m, const void* base, int64_t rows, int box_rows) {
     EncodeTiledFn enc = get_encode();
     if (!enc) return TREE_ATTN_ERR_CUDA;

@@ -99,12 +99,7 @@ __device__ __forceinline__ size_t state16_index(int chunk, int e, int g, int hkv
 // warps 0-3: lane r = token row r (scaling V) and key feature r (read-out);
 // warp 4: TMEM owner, lane 0 issues the loads and the MMA.
 constexpr int kDeltaSmem = 1024 + kRowStageBytes;   // K, V; then the fp32 staging rows over them
-// kParts = 3 (states that outlive the call): a weighted value is three bf16 numbers that add up to
-// its 24 bits, so the increment is as exact as fp32 sums are.  The second and the third
-// part take turns in a tile of their own, behind K and V, which leaves two CTAs on an SM.
-constexpr int kDeltaSmem3 = 1024 + 3 * kTile;
 
-template <int kParts>
 __global__ void __launch_bounds__(160, 1)
     lin_delta_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const int32_t* __restrict__ chunks, const float* __restrict__ decay, int hkv,
@@ -143,14 +138,12 @@ __global__ void __launch_bounds__(160, 1)
         }
     }
     bool ok = mbar_wait(b_full, 0, status, 81);
-    uint4 third[kParts == 3 ? 16 : 1];   // the last parts of this thread's row
     if (warp < 4 && ok) {
         // V row r times gamma^(L-1-r) (0 past the chunk): the row's 128 bytes in
         // each 64-feature block stay inside that row under the 128-byte swizzle
         const int r = threadIdx.x;
         const float lg = log2f(decay[g]);
         const float w = r < L ? exp2f((float)(L - 1 - r) * lg) : 0.f;
-        const bool past = r >= L;        // (0 times what lies there, an infinity perhaps, would not be 0)
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk) {
             uint4* row = reinterpret_cast<uint4*>(smem + 1024 + kTile + blk * 16384 + r * 128);
@@ -161,79 +154,26 @@ __global__ void __launch_bounds__(160, 1)
                 const int cr = (c + r) & 7;
                 uint4 x = row[cr];
                 uint32_t* u = reinterpret_cast<uint32_t*>(&x);
-                if constexpr (kParts == 1) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        u[e] = pack_bf16x2(__uint_as_float(u[e] << 16) * w, __uint_as_float(u[e] & 0xffff0000u) * w);
-                } else {
-                    uint4 y = make_uint4(0, 0, 0, 0), z = y;
-                    uint32_t *p2 = reinterpret_cast<uint32_t*>(&y), *p3 = reinterpret_cast<uint32_t*>(&z);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float a = past ? 0.f : __uint_as_float(u[e] << 16) * w;
-                        const float b = past ? 0.f : __uint_as_float(u[e] & 0xffff0000u) * w;
-                        u[e] = pack_bf16x2(a, b);
-                        const float a2 = a - __uint_as_float(u[e] << 16), b2 = b - __uint_as_float(u[e] & 0xffff0000u);
-                        // (an infinity or NaN is its first part's)
-                        p2[e] = pack_bf16x2(fabsf(a) < INFINITY ? a2 : 0.f, fabsf(b) < INFINITY ? b2 : 0.f);
-                        p3[e] = pack_bf16x2(fabsf(a) < INFINITY ? a2 - __uint_as_float(p2[e] << 16) : 0.f,
-                                            fabsf(b) < INFINITY ? b2 - __uint_as_float(p2[e] & 0xffff0000u) : 0.f);
-                    }
-                    row[cr + kTile / 16] = y;
-                    third[blk * 8 + c] = z;
-                }
+                for (int e = 0; e < 4; ++e)
+                    u[e] = pack_bf16x2(__uint_as_float(u[e] << 16) * w, __uint_as_float(u[e] & 0xffff0000u) * w);
                 row[cr] = x;
-            }
-        }
-        if constexpr (kParts == 3) {
-            // K past the chunk belongs to other tokens; it meets zeros, so only what is not a number matters
-            if (past) {
-#pragma unroll
-                for (int blk = 0; blk < 2; ++blk) {
-                    uint4* row = reinterpret_cast<uint4*>(smem + 1024 + blk * 16384 + r * 128);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) row[(c + r) & 7] = make_uint4(0, 0, 0, 0);
-                }
             }
         }
         fence_proxy_async_smem();
     }
     ok = __syncthreads_and(ok);
-    constexpr uint32_t ID = idesc_bf16(128, 128, true, true);   // K^T (MN-major) x V_w (MN-major)
     if (ok && threadIdx.x == 128) {
         tc_fence_after();
+        constexpr uint32_t ID = idesc_bf16(128, 128, true, true);   // K^T (MN-major) x V_w (MN-major)
 #pragma unroll
-        for (int part = 0; part < (kParts == 3 ? 2 : 1); ++part)
-#pragma unroll
-            for (int k = 0; k < kChunk / 16; ++k)
-                mma_bf16_ss(tmem, sdesc_sw128(ka + k * 2048, 16384, 1024),
-                            sdesc_sw128(va + part * kTile + k * 2048, 16384, 1024), ID, part > 0 || k > 0);
+        for (int k = 0; k < kChunk / 16; ++k)
+            mma_bf16_ss(tmem, sdesc_sw128(ka + k * 2048, 16384, 1024), sdesc_sw128(va + k * 2048, 16384, 1024), ID,
+                        k > 0);
         mma_commit(b_done);
     }
-    if constexpr (kParts == 3) {
-        if (ok) ok = mbar_wait(b_done, 0, status, 112);
-        if (warp < 4 && ok) {
-            const int r = threadIdx.x;
-#pragma unroll
-            for (int blk = 0; blk < 2; ++blk) {
-                uint4* row = reinterpret_cast<uint4*>(smem + 1024 + 2 * kTile + blk * 16384 + r * 128);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) row[(c + r) & 7] = third[blk * 8 + c];
-            }
-            fence_proxy_async_smem();
-        }
-        ok = __syncthreads_and(ok);
-        if (ok && threadIdx.x == 128) {
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < kChunk / 16; ++k)
-                mma_bf16_ss(tmem, sdesc_sw128(ka + k * 2048, 16384, 1024),
-                            sdesc_sw128(va + kTile + k * 2048, 16384, 1024), ID, 1u);
-            mma_commit(b_done);
-        }
-    }
     if (warp < 4) {
-        if (ok) ok = mbar_wait(b_done, kParts == 3 ? 1 : 0, status, 82);
+        if (ok) ok = mbar_wait(b_done, 0, status, 82);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
             tc_fence_after();
@@ -259,37 +199,15 @@ __global__ void __launch_bounds__(160, 1)
 // per SM, so each keeps kScanBatch increments in flight (loaded before the
 // recurrence uses the first of them); chunk lengths and node ids, the same for
 // every thread, are staged in shared memory a window at a time.
-// States in slots of a pool (kSlots): a root starts from the state in its slot, where
-// it has one, and a node that has one leaves its last state there.
-struct SlotIO {
-    float* states;             // [n_slots, hkv, d, d]
-    const int32_t* in;         // by node id, -1: a zero state; or null
-    const int32_t* out;        // by node id, -1: not kept; or null
-    const int32_t* ids;        // node id of each packed node
-    int32_t n_slots;
-    int* status;
-};
-
-// The node's slot in a table, or -1; numbers outside the pool say so and count as -1.
-__device__ __forceinline__ int slot_of(const SlotIO& io, const int32_t* table, int node) {
-    const int s = table ? table[io.ids[node]] : -1;
-    if (s < -1 || s >= io.n_slots) {
-        report_notice(io.status, TREE_ATTN_ERR_INVALID_SLOT);
-        return -1;
-    }
-    return s;
-}
-
 constexpr int kScanBatch = 16;
 constexpr int kScanWin = 1024;
 constexpr int kMaxScanDepths = 32;   // deeper trees use the one-walk scans (one launch per depth otherwise)
 
-template <bool kSlots>
 __global__ void __launch_bounds__(256) lin_scan_kernel(const int32_t* __restrict__ lnodes, int n_chunks,
                                                      const int32_t* __restrict__ chunks,
                                                      const float* __restrict__ decay, int hkv,
                                                      const float* __restrict__ ds, uint16_t* __restrict__ s_in16,
-                                                     float* __restrict__ s_out, SlotIO io) {
+                                                     float* __restrict__ s_out) {
     __shared__ int w_len[kScanWin], w_node[kScanWin];
     const int e = blockIdx.x * blockDim.x + threadIdx.x;   // state entry (row * d + col)
     const int g = blockIdx.y;
@@ -297,20 +215,6 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(const int32_t* __restrict
     const float lg = log2f(decay[g]);
     float S = 0.f;
     int cur = -1;   // the node whose chunks are being walked
-    auto enter = [&](int node) {
-        if constexpr (kSlots) {
-            const int s = slot_of(io, io.in, node);
-            if (s >= 0) return io.states[((size_t)s * hkv + g) * dd + e];
-        }
-        return 0.f;
-    };
-    auto leave = [&](int node) {
-        s_out[((size_t)node * hkv + g) * dd + e] = S;
-        if constexpr (kSlots) {
-            const int s = slot_of(io, io.out, node);
-            if (s >= 0) io.states[((size_t)s * hkv + g) * dd + e] = S;
-        }
-    };
     for (int w0 = 0; w0 < n_chunks; w0 += kScanWin) {
         const int nw = min(kScanWin, n_chunks - w0);
         __syncthreads();   // the previous window has been read
@@ -330,10 +234,9 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(const int32_t* __restrict
                     const int node = w_node[c + u];
                     if (node != cur) {   // first chunk of a node
                         const int par = lnodes[4 * node];
-                        if (cur >= 0) leave(cur);
+                        if (cur >= 0) s_out[((size_t)cur * hkv + g) * dd + e] = S;
                         // the node right after its parent continues from S itself
-                        if (par < 0) S = enter(node);
-                        else if (par != cur) S = s_out[((size_t)par * hkv + g) * dd + e];
+                        if (par != cur) S = par < 0 ? 0.f : s_out[((size_t)par * hkv + g) * dd + e];
                         cur = node;
                     }
                     s_in16[state16_index(w0 + c + u, e, g, hkv)] = float_to_bf16_bits(S);
@@ -341,7 +244,7 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(const int32_t* __restrict
                 }
         }
     }
-    if (cur >= 0) leave(cur);
+    if (cur >= 0) s_out[((size_t)cur * hkv + g) * dd + e] = S;
 }
 
 // ---- outputs per (chunk, kv-head): the group's q-heads one after another ------
@@ -370,13 +273,6 @@ constexpr int kOutSmem = 2048 + 5 * kTile;   // barriers, mask table, K, V, S_in
 constexpr int kLinWarps = 10;                // 8 element-wise warps, loader, MMA issuer
 constexpr int kLinThreads = 32 * kLinWarps;
 
-// kColumn (states from and to slots): the decay mask split by row and column, O = diag(f) (P V + Q S_in)
-// with P[m, m'] = gamma^-(m'+1) (Q K^T)[m, m'] for m' <= m and f(m) = scale * gamma^(m+1) applied
-// to the sum in registers.  The query is then an exact operand, read from its slot by both
-// products, and each part of O meets one rounding to bf16 (P's or S_in's).  gamma^-128 has to
-// stay far from overflow: a decay below 2^(-100/128) = 0.58, whose state is forgotten within a
-// few tokens, takes the form above.
-template <bool kColumn>
 __global__ void __launch_bounds__(kLinThreads, 1)
     lin_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_s,
@@ -411,10 +307,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const uint32_t ka = sb + 2048, va = ka + kTile, sina = va + kTile, qa0 = sina + kTile;
     // mtab[128 + t] = gamma^t for t = m - m' in [0, 128), 0 for t < 0
     float* mtab = reinterpret_cast<float*>(smem + 1024);
-    const bool column = kColumn && log2f(decay[g]) > -100.f / 128.f;
     if (threadIdx.x < 128) {
-        // (column form: mtab[m'] = gamma^-(m'+1))
-        mtab[threadIdx.x] = column ? exp2f(-(float)(threadIdx.x + 1) * log2f(decay[g])) : 0.f;
+        mtab[threadIdx.x] = 0.f;
         mtab[128 + threadIdx.x] = exp2f((float)threadIdx.x * log2f(decay[g]));
     }
     if (threadIdx.x == 0) {
@@ -454,8 +348,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     const int u = i * G + n, b = u & 1, w = u >> 1;
                     if (w > 0) {   // Q slot b: read by unit u - 2's S product and element-wise warps
                         ok = mbar_wait(b_qe(b), (w - 1) & 1, status, 89);
-                        // (column form: by its output product instead)
-                        if (ok) ok = mbar_wait(column ? b_o2(b) : b_qr(b), (w - 1) & 1, status, 97);
+                        if (ok) ok = mbar_wait(b_qr(b), (w - 1) & 1, status, 97);
                     }
                     if (!ok) break;
                     mbar_expect_tx(b_qf(b), kTile);
@@ -489,23 +382,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 tc_fence_after();
                 // keys 16k .. 16k + 15 of P packed at 64 (k / 4) + 8 (k % 4); features
                 // 16k .. 16k + 15 of f Q 32 columns further
-                const int steps = kColumn ? (chunks[4 * chunk_of(i) + 1] + 15) / 16 : kChunk / 16;
 #pragma unroll
                 for (int k = 0; k < kChunk / 16; ++k)
-                    if (k < steps) mma_bf16_ts(tmem + 256 * b + 128, tmem + 256 * b + (k >> 2) * 64 + (k & 3) * 8,
+                    mma_bf16_ts(tmem + 256 * b + 128, tmem + 256 * b + (k >> 2) * 64 + (k & 3) * 8,
                                 sdesc_sw128(va + k * 2048, 16384, 1024), ID_O, k > 0 ? 1u : 0u);
-                if (column) {
-                    const uint32_t qa = qa0 + b * kTile;
 #pragma unroll
-                    for (int k = 0; k < kD / 16; ++k)
-                        mma_bf16_ss(tmem + 256 * b + 128, sdesc_sw128(qa + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024),
-                                    sdesc_sw128(sina + k * 2048, 16384, 1024), ID_O, 1u);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < kD / 16; ++k)
-                        mma_bf16_ts(tmem + 256 * b + 128, tmem + 256 * b + 32 + (k >> 2) * 64 + (k & 3) * 8,
-                                    sdesc_sw128(sina + k * 2048, 16384, 1024), ID_O, 1u);
-                }
+                for (int k = 0; k < kD / 16; ++k)
+                    mma_bf16_ts(tmem + 256 * b + 128, tmem + 256 * b + 32 + (k >> 2) * 64 + (k & 3) * 8,
+                                sdesc_sw128(sina + k * 2048, 16384, 1024), ID_O, 1u);
                 mma_commit(b_o2(b));
                 if (n == G - 1) mma_commit(b_vfree);   // V and S_in read by the chunk's last products
             };
@@ -567,38 +451,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                         tmem_ld32(tS + col0 + cc * 32, v);
                         tmem_wait_ld();
                         uint32_t pw[16];
-                        if (column) {
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) {
-                                const int c0 = col0 + cc * 32 + 2 * x, c1 = c0 + 1;
-                                pw[x] = pack_bf16x2(c0 <= m ? v[2 * x] * mtab[c0] : 0.f,
-                                                    c1 <= m ? v[2 * x + 1] * mtab[c1] : 0.f);
-                            }
-                        } else {
-#pragma unroll
-                            for (int x = 0; x < 16; ++x) {
-                                const int c0 = col0 + cc * 32 + 2 * x, c1 = c0 + 1;
-                                const float p0 = scale * v[2 * x] * wt[-c0], p1 = scale * v[2 * x + 1] * wt[-c1];
-                                pw[x] = pack_bf16x2(kColumn && c0 > m ? 0.f : p0, kColumn && c1 > m ? 0.f : p1);
-                            }
+                        for (int x = 0; x < 16; ++x) {
+                            const int c0 = col0 + cc * 32 + 2 * x, c1 = c0 + 1;
+                            pw[x] = pack_bf16x2(scale * v[2 * x] * wt[-c0], scale * v[2 * x + 1] * wt[-c1]);
                         }
                         tmem_st16(tS + col0 + cc * 16, pw);
                     }
-                    if (kColumn) {
-                        // the rows behind a ragged chunk are another node's: zeros in the last 16 that the
-                        // product reads (0 times an infinity there would not be 0)
-                        const int i = u / G, Lc = chunks[4 * chunk_of(i) + 1];
-                        if (u % G == 0 && (Lc & 15)) {
-                            ok = mbar_wait(b_v, i & 1, status, 113);
-                            if (ok && m >= Lc && m < ((Lc + 15) & ~15)) {
-                                uint4* vrow = reinterpret_cast<uint4*>(smem + (va - sb) + grp * 16384 + m * 128);
-#pragma unroll
-                                for (int c = 0; c < 8; ++c) vrow[c] = make_uint4(0, 0, 0, 0);
-                            }
-                            fence_proxy_async_smem();
-                        }
-                    }
-                    if (!column) {
                     // f(m) q_m over features [col0, col0 + 64), from the 128B-swizzled Q
                     // slot (block grp holds those features, row m at 128 m)
                     const uint8_t* qrow = smem + (qa0 - sb) + b * kTile + grp * 16384 + m * 128;
@@ -618,7 +477,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                         tmem_st16(tS + col0 + 32 + h2 * 16, qw);
                     }
                     mbar_arrive(b_qr(b));   // Q slot b read (the values are in registers)
-                    }
                     tmem_wait_st();
                     tc_fence_before();
                     mbar_arrive(b_p(b));
@@ -637,10 +495,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                         float v[32];
                         tmem_ld32(tO + col0 + cc * 32, v);
                         tmem_wait_ld();
-                        if (column) {
-#pragma unroll
-                            for (int x = 0; x < 32; ++x) v[x] *= fo;
-                        }
                         if (m < prev_L) {
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {
@@ -726,16 +580,12 @@ int build_lin(tree_attn_plan_s* P) {
             depth[k] = pp < 0 ? 0 : depth[pp] + 1;
             n_depths = std::max(n_depths, depth[k] + 1);
         }
-        X.lvl_ptr.clear();
-        X.lvl_nodes.clear();
-        if (n_depths <= kMaxScanDepths) {
-            X.lvl_ptr.assign((size_t)n_depths + 1, 0);
-            for (int32_t k = 0; k < n; ++k) ++X.lvl_ptr[(size_t)depth[k] + 1];
-            for (int32_t l = 0; l < n_depths; ++l) X.lvl_ptr[(size_t)l + 1] += X.lvl_ptr[l];
-            X.lvl_nodes.resize(n);
-            std::vector<int32_t> fill(X.lvl_ptr.begin(), X.lvl_ptr.end() - 1);
-            for (int32_t k = 0; k < n; ++k) X.lvl_nodes[fill[depth[k]]++] = k;
-        }
+        X.lvl_ptr.assign((size_t)n_depths + 1, 0);
+        for (int32_t k = 0; k < n; ++k) ++X.lvl_ptr[(size_t)depth[k] + 1];
+        for (int32_t l = 0; l < n_depths; ++l) X.lvl_ptr[(size_t)l + 1] += X.lvl_ptr[l];
+        X.lvl_nodes.resize(n);
+        std::vector<int32_t> fill(X.lvl_ptr.begin(), X.lvl_ptr.end() - 1);
+        for (int32_t k = 0; k < n; ++k) X.lvl_nodes[fill[depth[k]]++] = k;
         X.ready = true;
     } catch (const std::bad_alloc&) {
         return TREE_ATTN_ERR_OUT_OF_MEMORY;
@@ -772,6 +622,17 @@ int ensure_lin_device(tree_attn_plan_s* P, DevicePlan** out) {
     *out = &D;
     return TREE_ATTN_OK;
 }
+
+}  // namespace
+
+int ensure_linear(tree_attn_plan_s* P, DevicePlan** out) { return ensure_lin_device(P, out); }
+
+int linear_chunks(tree_attn_plan_s* P) {
+    std::lock_guard<std::mutex> lk(P->mu);
+    return build_lin(P);
+}
+
+namespace {
 
 struct LinWs {
     size_t ds, s_in, s_out, total;
@@ -1002,14 +863,12 @@ __device__ __forceinline__ uint2 bf16x4(float4 v) {
                       (uint32_t)float_to_bf16_bits(v.z) | ((uint32_t)float_to_bf16_bits(v.w) << 16));
 }
 
-template <bool kSlots>
 __global__ void __launch_bounds__(256) lin_scan_depth_kernel(const int32_t* __restrict__ lnodes,
                                                            const int32_t* __restrict__ nodes,
                                                            const int32_t* __restrict__ chunks,
                                                            const float* __restrict__ decay, int hkv,
                                                            const float* __restrict__ ds,
-                                                           uint16_t* __restrict__ s_in16, float* __restrict__ s_out,
-                                                           SlotIO io) {
+                                                           uint16_t* __restrict__ s_in16, float* __restrict__ s_out) {
     const int k = nodes[blockIdx.x / kEntryBlocks];
     const int e = ((blockIdx.x % kEntryBlocks) * 256 + threadIdx.x) * 4;   // first of 4 state entries
     const int g = blockIdx.y;
@@ -1018,10 +877,6 @@ __global__ void __launch_bounds__(256) lin_scan_depth_kernel(const int32_t* __re
     const int par = lnodes[4 * k], c0 = lnodes[4 * k + 1], nc = lnodes[4 * k + 2];
     float4 S = par < 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
                        : *reinterpret_cast<const float4*>(s_out + ((size_t)par * hkv + g) * dd + e);
-    if constexpr (kSlots) {
-        const int s = par < 0 ? slot_of(io, io.in, k) : -1;
-        if (s >= 0) S = *reinterpret_cast<const float4*>(io.states + ((size_t)s * hkv + g) * dd + e);
-    }
     for (int c = c0; c < c0 + nc; c += kDepthBatch) {
         float4 dsv[kDepthBatch];
         int len[kDepthBatch];
@@ -1040,10 +895,6 @@ __global__ void __launch_bounds__(256) lin_scan_depth_kernel(const int32_t* __re
             }
     }
     *reinterpret_cast<float4*>(s_out + ((size_t)k * hkv + g) * dd + e) = S;
-    if constexpr (kSlots) {
-        const int s = slot_of(io, io.out, k);
-        if (s >= 0) *reinterpret_cast<float4*>(io.states + ((size_t)s * hkv + g) * dd + e) = S;
-    }
 }
 
 // Backward: a node's entering sum is its children's entering adjoints, added in
@@ -1360,20 +1211,19 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 // The forward scan: depth by depth where the plan has the depth tables, else
 // one walk over every chunk.
-template <bool kSlots = false>
 int launch_scan(const tree_attn_plan_s* P, const DevicePlan* D, int64_t nc, const float* decay, int hkv,
-                const float* ds, uint16_t* s_in16, float* s_out, cudaStream_t s, const SlotIO& io = {}) {
+                const float* ds, uint16_t* s_in16, float* s_out, cudaStream_t s) {
     const LinInfo& X = P->lin;
-    if (X.lvl_ptr.empty()) {
-        lin_scan_kernel<kSlots><<<dim3(kD * kD / 256, hkv), 256, 0, s>>>(D->lnodes, (int)nc, D->chunks, decay, hkv, ds,
-                                                                         s_in16, s_out, io);
+    if (X.lvl_ptr.size() > (size_t)kMaxScanDepths + 1) {
+        lin_scan_kernel<<<dim3(kD * kD / 256, hkv), 256, 0, s>>>(D->lnodes, (int)nc, D->chunks, decay, hkv, ds,
+                                                                 s_in16, s_out);
         return cudaGetLastError() == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA;
     }
     for (size_t l = 0; l + 1 < X.lvl_ptr.size(); ++l) {
         const int64_t blocks = (int64_t)(X.lvl_ptr[l + 1] - X.lvl_ptr[l]) * kEntryBlocks;
         if (blocks > INT32_MAX) return TREE_ATTN_ERR_TOO_LARGE;
-        lin_scan_depth_kernel<kSlots><<<dim3((unsigned)blocks, hkv), 256, 0, s>>>(
-            D->lnodes, D->lvl_nodes + X.lvl_ptr[l], D->chunks, decay, hkv, ds, s_in16, s_out, io);
+        lin_scan_depth_kernel<<<dim3((unsigned)blocks, hkv), 256, 0, s>>>(D->lnodes, D->lvl_nodes + X.lvl_ptr[l],
+                                                                         D->chunks, decay, hkv, ds, s_in16, s_out);
         if (cudaGetLastError() != cudaSuccess) return TREE_ATTN_ERR_CUDA;
     }
     return TREE_ATTN_OK;
@@ -1383,7 +1233,7 @@ int launch_scan(const tree_attn_plan_s* P, const DevicePlan* D, int64_t nc, cons
 int launch_bwd_scan(const tree_attn_plan_s* P, const DevicePlan* D, int64_t nc, const float* decay, int hkv,
                     const float* f_in, uint16_t* rsum16, float* csum, cudaStream_t s) {
     const LinInfo& X = P->lin;
-    if (X.lvl_ptr.empty()) {
+    if (X.lvl_ptr.size() > (size_t)kMaxScanDepths + 1) {
         lin_bwd_scan_kernel<<<dim3(kD * kD / 256, hkv), 256, 0, s>>>(D->lnodes, (int)nc, D->chunks, decay, hkv,
                                                                      f_in, rsum16, csum);
         return cudaGetLastError() == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA;
@@ -1458,61 +1308,19 @@ int tree_attn_linear_fwd(tree_attn_plan_t P, const void* q, const void* k, const
     if ((st = make_tensor_map(&ts, s_in16, nc * kChunk, hkv, kD))) return st;
     float* s_out = reinterpret_cast<float*>(ws + w.s_out);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (cudaFuncSetAttribute(lin_delta_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDeltaSmem) != cudaSuccess ||
-        cudaFuncSetAttribute(lin_out_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOutSmem) != cudaSuccess)
+    if (cudaFuncSetAttribute(lin_delta_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDeltaSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(lin_out_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOutSmem) != cudaSuccess)
         return TREE_ATTN_ERR_CUDA;
-    lin_delta_kernel<1><<<(unsigned)(nc * hkv), 160, kDeltaSmem, s>>>(tk, tv, D->chunks, decay, hkv, ds, status);
+    lin_delta_kernel<<<(unsigned)(nc * hkv), 160, kDeltaSmem, s>>>(tk, tv, D->chunks, decay, hkv, ds, status);
     if (cudaGetLastError() != cudaSuccess) return TREE_ATTN_ERR_CUDA;
     if ((st = launch_scan(P, D, nc, decay, hkv, ds, s_in16, s_out, s))) return st;
     const int lanes = out_lanes(dev, nc, hkv);
-    lin_out_kernel<false><<<(unsigned)(lanes * hkv), kLinThreads, kOutSmem, s>>>(tq, tk, tv, ts, D->chunks, (int)nc, lanes,
+    lin_out_kernel<<<(unsigned)(lanes * hkv), kLinThreads, kOutSmem, s>>>(tq, tk, tv, ts, D->chunks, (int)nc, lanes,
                                                                       decay, static_cast<uint16_t*>(o), hq, hkv,
                                                                       scale, status);
     return cudaGetLastError() == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA;
 }
 
-int tree_attn_linear_prefill(tree_attn_plan_t P, const void* q, const void* k, const void* v, void* o, float* states,
-                             int32_t n_slots, const int32_t* slot_in, const int32_t* slot_out, const float* decay,
-                             int32_t hq, int32_t hkv, int32_t d, float scale, void* workspace, size_t ws_bytes,
-                             void* stream) {
-    if (!P || !q || !k || !v || !o || !decay || hq <= 0 || hkv <= 0 || hq % hkv != 0) return TREE_ATTN_ERR_INVALID_ARG;
-    if (n_slots < 0 || (n_slots > 0 && !states)) return TREE_ATTN_ERR_INVALID_ARG;
-    if (d != kD || P->block != kChunk) return TREE_ATTN_ERR_UNSUPPORTED;
-    if (!(scale > 0.f) || !std::isfinite(scale)) return TREE_ATTN_ERR_INVALID_ARG;
-    for (const void* p : {q, k, v, (const void*)o, (const void*)states})
-        if (!aligned(p, 16)) return TREE_ATTN_ERR_ALIGNMENT;
-    if (!aligned(decay, 4) || !aligned(slot_in, 4) || !aligned(slot_out, 4) || !aligned(workspace, 256))
-        return TREE_ATTN_ERR_ALIGNMENT;
-    DevicePlan* D = nullptr;
-    int st = ensure_lin_device(P, &D);
-    if (st) return st;
-    const LinWs w = lin_layout(P, hkv);
-    if (!workspace || ws_bytes < w.total) return TREE_ATTN_ERR_WORKSPACE;
-    const int64_t nc = (int64_t)(P->lin.chunks.size() / 4);
-    if (nc * hq > INT32_MAX || nc * hkv > INT32_MAX) return TREE_ATTN_ERR_TOO_LARGE;
-    CUtensorMap tq, tk, tv, ts;
-    if ((st = make_tensor_map(&tq, q, P->N, hq, d)) || (st = make_tensor_map(&tk, k, P->N, hkv, d)) ||
-        (st = make_tensor_map(&tv, v, P->N, hkv, d)))
-        return st;
-    int dev, *status;
-    if ((st = current_device(&dev)) || (st = get_status_ptr(dev, &status))) return st;
-    char* ws = static_cast<char*>(workspace);
-    float* ds = reinterpret_cast<float*>(ws + w.ds);
-    uint16_t* s_in16 = reinterpret_cast<uint16_t*>(ws + w.s_in);
-    if ((st = make_tensor_map(&ts, s_in16, nc * kChunk, hkv, kD))) return st;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (cudaFuncSetAttribute(lin_delta_kernel<3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDeltaSmem3) != cudaSuccess ||
-        cudaFuncSetAttribute(lin_out_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOutSmem) != cudaSuccess)
-        return TREE_ATTN_ERR_CUDA;
-    lin_delta_kernel<3><<<(unsigned)(nc * hkv), 160, kDeltaSmem3, s>>>(tk, tv, D->chunks, decay, hkv, ds, status);
-    if (cudaGetLastError() != cudaSuccess) return TREE_ATTN_ERR_CUDA;
-    const SlotIO io = {states, slot_in, slot_out, D->lin_ids, n_slots, status};
-    if ((st = launch_scan<true>(P, D, nc, decay, hkv, ds, s_in16, reinterpret_cast<float*>(ws + w.s_out), s, io))) return st;
-    const int lanes = out_lanes(dev, nc, hkv);
-    lin_out_kernel<true><<<(unsigned)(lanes * hkv), kLinThreads, kOutSmem, s>>>(
-        tq, tk, tv, ts, D->chunks, (int)nc, lanes, decay, static_cast<uint16_t*>(o), hq, hkv, scale, status);
-    return cudaGetLastError() == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA;
-}
 
 int tree_attn_linear_bwd(tree_attn_plan_t P, const void* q, const void* k, const void* v, const void* dout,
                          void* dq, void* dk, void* dv, const float* decay, int32_t hq, int32_t hkv, int32_t d,
@@ -1546,17 +1354,17 @@ int tree_attn_linear_bwd(tree_attn_plan_t P, const void* q, const void* k, const
     if ((st = make_tensor_map(&tr1, r1, nc * kChunk, hkv, kD))) return st;
     float* r2 = reinterpret_cast<float*>(ws + w.s_out);   // S'_out, then the per-node child sums
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (cudaFuncSetAttribute(lin_delta_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDeltaSmem) != cudaSuccess ||
-        cudaFuncSetAttribute(lin_out_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOutSmem) != cudaSuccess ||
+    if (cudaFuncSetAttribute(lin_delta_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDeltaSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(lin_out_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOutSmem) != cudaSuccess ||
         cudaFuncSetAttribute(lin_bwd_f_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAdjSmem) != cudaSuccess ||
         cudaFuncSetAttribute(lin_bwd_kv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKvSmem) != cudaSuccess)
         return TREE_ATTN_ERR_CUDA;
     // dQ: the forward with (q, k, v) = (dO, V, K)
-    lin_delta_kernel<1><<<(unsigned)(nc * hkv), 160, kDeltaSmem, s>>>(tv, tk, D->chunks, decay, hkv, r0, status);
+    lin_delta_kernel<<<(unsigned)(nc * hkv), 160, kDeltaSmem, s>>>(tv, tk, D->chunks, decay, hkv, r0, status);
     if (cudaGetLastError() != cudaSuccess) return TREE_ATTN_ERR_CUDA;
     if ((st = launch_scan(P, D, nc, decay, hkv, r0, r1, r2, s))) return st;
     const int lanes = out_lanes(dev, nc, hkv);
-    lin_out_kernel<false><<<(unsigned)(lanes * hkv), kLinThreads, kOutSmem, s>>>(tdo, tv, tk, tr1, D->chunks, (int)nc, lanes,
+    lin_out_kernel<<<(unsigned)(lanes * hkv), kLinThreads, kOutSmem, s>>>(tdo, tv, tk, tr1, D->chunks, (int)nc, lanes,
                                                                       decay, static_cast<uint16_t*>(dq), hq, hkv,
                                                                       scale, status);
     if (cudaGetLastError() != cudaSuccess) return TREE_ATTN_ERR_CUDA;

@@ -1,0 +1,689 @@
+// Whole turns of linear attention from and to states in slots (include/tree_linear.h).
+//
+// prefill_state_kernel, one launch per depth of the tree (roots first): a CTA walks the chunks (128
+// tokens at most) of one node for one kv-head and 64 of the 128 value features -- the columns of the
+// state do not meet --, with the state in registers:
+//     S_in of the chunk goes out as bf16, the operand of the outputs;  S = gamma^L S + dS,
+//     dS = sum_m gamma^(L-1-m) k_m v_m^T on the tensor cores.
+//   A weighted value has 24 bits; it is split into three bf16 numbers that add up to it, so the
+//   increment is as exact as sums in fp32 are (two would leave 3e-6 of it).  Warps 0-3 hold the
+//   state, warps 4-7 weigh and split the values, warp 8 loads, warp 9 issues the products; every
+//   stage is double-buffered.  It replaces a product per chunk that left its fp32 increment in memory
+//   and a scan over those (64 KB each way per chunk and kv-head): group star 45 -> see below.
+//
+// prefill_out_kernel, persistent, a unit (chunk, q-head) after the other: A = Q K^T, then
+//     O = diag(f) (P V + Q S_in),  P[m, m'] = gamma^-(m'+1) A[m, m'] for m' <= m,  f(m) = scale gamma^(m+1).
+//   The query is an exact operand of both products and each part of O meets one rounding to
+//   bf16 (P's or S_in's).  gamma^-128 has to stay far from overflow: a decay below 2^(-100/128) = 0.58,
+//   whose state is forgotten within a few tokens, takes P[m, m'] = scale gamma^(m-m') A[m, m'] and diag(f) Q,
+//   rounded to bf16, instead of Q.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+
+#include "kernels.h"
+#include "plan.h"
+#include "ptx.cuh"
+#include "tree_linear.h"
+
+namespace treeattn {
+
+namespace {
+
+constexpr int kChunk = 128;
+constexpr int kD = 128;
+constexpr int kTile = kChunk * kD * 2;         // 32 KB, bf16
+constexpr int kHalf = kTile / 2;               // 64 of its features
+constexpr int kThreads = 320;
+
+// States in slots of a pool: a root starts from the state in its slot, where it has one, and a
+// node that has one leaves its last state there.
+struct SlotIO {
+    float* states;             // [n_slots, hkv, d, d]
+    const int32_t* in;         // by node id, -1: a zero state; or null
+    const int32_t* out;        // by node id, -1: not kept; or null
+    const int32_t* ids;        // node id of each packed node
+    int32_t n_slots;
+    int* status;
+};
+
+// The node's slot in a table, or -1; numbers outside the pool say so and count as -1.
+__device__ __forceinline__ int slot_of(const SlotIO& io, const int32_t* table, int node) {
+    const int s = table ? table[io.ids[node]] : -1;
+    if (s < -1 || s >= io.n_slots) {
+        report_notice(io.status, TREE_ATTN_ERR_INVALID_SLOT);
+        return -1;
+    }
+    return s;
+}
+
+__device__ __forceinline__ uint4 pack8(const float* v) {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// ---- the states that enter the chunks --------------------------------------------------------
+constexpr int kStateK = 1024, kStateV = kStateK + 2 * kTile, kStateW = kStateV + 2 * kHalf,
+              kStateOut = kStateW + 6 * kHalf, kStateSmem = kStateOut + kHalf;
+
+struct StateParams {
+    const int32_t* nodes;      // packed nodes of this depth
+    const int32_t* lnodes;     // [4*n_nodes] {parent's packed index, first chunk, chunks, ..}
+    const int32_t* kids;       // child offsets
+    const int32_t* chunks;     // [4*n_chunks] {first token, tokens, ..}
+    const float* decay;
+    float* s_out;              // [n_nodes, hkv, d, d], nodes with children
+    int32_t hkv, n_nodes, n_chunks;
+    int32_t first_depth;
+    SlotIO io;
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_state_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const __grid_constant__ CUtensorMap tm_s, const StateParams p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sb = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int* status = p.io.status;
+    if (sb & 1023u) {
+        if (threadIdx.x == 0) report_status(status, -5);
+        return;
+    }
+    auto full = [&](int s) { return sb + 8u * s; };           // K, V have come
+    auto empty = [&](int s) { return sb + 16 + 8u * s; };     // and have been multiplied
+    auto wfull = [&](int s) { return sb + 32 + 8u * s; };     // the weighted values are there
+    auto wfree = [&](int s) { return sb + 48 + 8u * s; };
+    auto dfull = [&](int s) { return sb + 64 + 8u * s; };     // the increment is there
+    auto dfree = [&](int s) { return sb + 80 + 8u * s; };
+    const uint32_t drain = sb + 96, holder = sb + 104;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+            mbar_init(wfull(s), 128);
+            mbar_init(wfree(s), 1);
+            mbar_init(dfull(s), 1);
+            mbar_init(dfree(s), 128);
+        }
+        mbar_init(drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == 9) tmem_alloc(holder, 128);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + 104);
+    const int half = blockIdx.x & 1, g = (blockIdx.x >> 1) % p.hkv, node = p.nodes[(blockIdx.x >> 1) / p.hkv];
+    bool ok = ta_ok(status, 620, node, 0, p.n_nodes);
+    const int par = ok ? p.lnodes[4 * node] : -1, c0 = ok ? p.lnodes[4 * node + 1] : 0, n = ok ? p.lnodes[4 * node + 2] : 0;
+    ok = ok && ta_ok(status, 621, c0, 0, p.n_chunks) && ta_ok(status, 622, c0 + n, 0, p.n_chunks + 1);
+    const bool inner = ok && p.kids[node + 1] > p.kids[node];
+    grid_dep_wait();
+    grid_dep_launch();
+    const float gamma = p.decay[g], lg = log2f(gamma);
+    // (once per kv-head; the call's outputs are then undefined)
+    if (p.first_depth && blockIdx.x < 2 * p.hkv && half == 0 && threadIdx.x == 0 && !(gamma > 0.f && gamma <= 1.f))
+        report_notice(status, TREE_ATTN_ERR_INVALID_DECAY);
+    const int to = ok ? slot_of(p.io, p.io.out, node) : -1;
+    const int steps = !ok ? 0 : inner || to >= 0 ? n : n - 1;   // increments that anything needs
+
+    if (warp < 4) {
+        // the state: thread = key feature, 64 value features
+        const int row = threadIdx.x;
+        const size_t at = (size_t)g * kD * kD + (size_t)row * kD + half * 64;
+        float S[64];
+        const int from = ok && par < 0 ? slot_of(p.io, p.io.in, node) : -1;
+        const float* src = par >= 0 ? p.s_out + (size_t)par * p.hkv * kD * kD + at
+                                    : from >= 0 ? p.io.states + (size_t)from * p.hkv * kD * kD + at : nullptr;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float4 v = src ? reinterpret_cast<const float4*>(src)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+            S[4 * i] = v.x;
+            S[4 * i + 1] = v.y;
+            S[4 * i + 2] = v.z;
+            S[4 * i + 3] = v.w;
+        }
+        const uint32_t stage = sb + kStateOut + warp * 4096;
+        for (int i = 0; i < n && ok; ++i) {
+            if (lane == 0) bulk_wait_read_all();   // the last one has left
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const uint4 y = pack8(S + 8 * c);
+                st_shared_v4(stage + sw128_offset(lane, c), y.x, y.y, y.z, y.w);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_3d(&tm_s, stage, half * 64, g, (c0 + i) * kChunk + warp * 32);
+                bulk_commit();
+            }
+            if (i >= steps) break;
+            const int s = i & 1;
+            ok = mbar_wait(dfull(s), (i >> 1) & 1, status, 121);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const float f = exp2f((float)p.chunks[4 * (c0 + i) + 1] * lg);
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+                float v[32];
+                tmem_ld32(tmem + ((uint32_t)(warp << 5) << 16) + s * 64 + cc * 32, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 32; ++x) S[cc * 32 + x] = fmaf(f, S[cc * 32 + x], v[x]);
+            }
+            tc_fence_before();
+            mbar_arrive(dfree(s));
+        }
+        if (ok) {
+            auto leave = [&](float* dst) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    reinterpret_cast<float4*>(dst)[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+            };
+            if (inner) leave(p.s_out + (size_t)node * p.hkv * kD * kD + at);
+            if (to >= 0) leave(p.io.states + (size_t)to * p.hkv * kD * kD + at);
+        }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+    } else if (warp < 8) {
+        // the values: thread = token, its row times gamma^(L-1-r) as three numbers that add up to it
+        const int r = threadIdx.x - 128;
+        for (int i = 0; i < steps && ok; ++i) {
+            const int s = i & 1;
+            ok = mbar_wait(full(s), (i >> 1) & 1, status, 122);
+            if (ok && i >= 2) ok = mbar_wait(wfree(s), ((i >> 1) - 1) & 1, status, 123);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const int L = p.chunks[4 * (c0 + i) + 1];
+            const bool past = r >= L;              // another node's row: zeros, whatever it holds
+            const float w = past ? 0.f : exp2f((float)(L - 1 - r) * lg);
+            const uint4* v = reinterpret_cast<const uint4*>(smem + kStateV + s * kHalf + r * 128);
+            uint4* out = reinterpret_cast<uint4*>(smem + kStateW + s * 3 * kHalf + r * 128);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                // the row's 16-byte pieces in an order rotated by the row: the rows of a warp spread over
+                // all bank groups (a piece keeps its swizzled place)
+                const int cr = (c + r) & 7;
+                const uint4 x = v[cr];
+                const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+                uint32_t p1[4], p2[4], p3[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float a = past ? 0.f : __uint_as_float(u[e] << 16) * w;
+                    const float b = past ? 0.f : __uint_as_float(u[e] & 0xffff0000u) * w;
+                    p1[e] = pack_bf16x2(a, b);
+                    // (an infinity or NaN is its first part's)
+                    const float a1 = __uint_as_float(p1[e] << 16), b1 = __uint_as_float(p1[e] & 0xffff0000u);
+                    const float a2 = fabsf(a1) < INFINITY ? a - a1 : 0.f, b2 = fabsf(b1) < INFINITY ? b - b1 : 0.f;
+                    p2[e] = pack_bf16x2(a2, b2);
+                    p3[e] = pack_bf16x2(a2 - __uint_as_float(p2[e] << 16), b2 - __uint_as_float(p2[e] & 0xffff0000u));
+                }
+                out[cr] = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+                out[kHalf / 16 + cr] = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+                out[2 * kHalf / 16 + cr] = make_uint4(p3[0], p3[1], p3[2], p3[3]);
+            }
+            if (past) {                            // its keys meet those zeros: no infinities there either
+                uint4* k = reinterpret_cast<uint4*>(smem + kStateK + s * kTile + r * 128);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) k[(c + r) & 7] = k[kHalf / 16 + ((c + r) & 7)] = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(wfull(s));
+        }
+    } else if (warp == 8) {
+        if (lane == 0) {
+            int sent = 0;
+            for (int i = 0; i < steps && ok; ++i) {
+                const int s = i & 1, off = p.chunks[4 * (c0 + i)];
+                if (i >= 2) ok = mbar_wait(empty(s), ((i >> 1) - 1) & 1, status, 124);
+                if (!ok) break;
+                mbar_expect_tx(full(s), kTile + kHalf);
+                for (int blk = 0; blk < 2; ++blk)
+                    tma_load_3d(sb + kStateK + s * kTile + blk * kHalf, &tm_k, blk * 64, g, off, full(s));
+                tma_load_3d(sb + kStateV + s * kHalf, &tm_v, half * 64, g, off, full(s));
+                sent = i + 1;
+            }
+            if (!ok)                               // copies still under way
+                for (int i = max(0, sent - 2); i < sent; ++i) mbar_wait(full(i & 1), (i >> 1) & 1, status, 125);
+        }
+        __syncwarp();
+    } else {
+        if (lane == 0) {
+            constexpr uint32_t ID = idesc_bf16(128, 64, true, true);   // K^T (MN-major) x V_w (MN-major)
+            for (int i = 0; i < steps && ok; ++i) {
+                const int s = i & 1;
+                ok = mbar_wait(wfull(s), (i >> 1) & 1, status, 126);
+                if (ok && i >= 2) ok = mbar_wait(dfree(s), ((i >> 1) - 1) & 1, status, 127);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t ka = sb + kStateK + s * kTile, wa = sb + kStateW + s * 3 * kHalf;
+#pragma unroll
+                for (int part = 0; part < 3; ++part)
+#pragma unroll
+                    for (int k = 0; k < kChunk / 16; ++k)
+                        mma_bf16_ss(tmem + s * 64, sdesc_sw128(ka + k * 2048, kHalf, 1024),
+                                    sdesc_sw128(wa + part * kHalf + k * 2048, kHalf, 1024), ID, part > 0 || k > 0);
+                mma_commit(dfull(s));
+                mma_commit(wfree(s));
+                mma_commit(empty(s));
+            }
+            mma_commit(drain);
+            mbar_wait(drain, 0, status, 128);
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 128);
+    }
+}
+
+// ---- the outputs --------------------------------------------------------------------------------
+// A CTA keeps one kv-head (and, where there are few chunks, some of its q-heads) and walks the chunks j0,
+// j0 + lanes, ...  K is loaded once per chunk, V and S_in together once; Q comes through
+// three slots.  TMEM holds two units (buffer b = u & 1): A, then P over it, at [256b, 256b + 128), O at
+// [256b + 128, 256b + 256).  A of unit u is issued before the products of unit u - 1, and unit u - 1's output is
+// read after unit u's mask, so that the products run meanwhile.
+// warps 0-7: query row m = 32 (w % 4) + lane, columns [64 (w / 4), + 64) of A and O; warp 8 loads, warp 9
+// issues.  A warp's 32 x 64 outputs leave by one bulk store out of shared memory: written from
+// registers, 16 bytes of 32 different rows at a time, they kept the store unit busy for 2,000 of a
+// unit's 5,300 cycles.
+constexpr int kOutK = 2048, kOutV = kOutK + kTile, kOutS = kOutV + kTile, kOutQ = kOutS + kTile, kQSlots = 3,
+              kOutStage = kOutQ + kQSlots * kTile, kOutSmem = kOutStage + kTile;
+
+struct OutParams {
+    const int32_t* chunks;
+    const float* decay;
+    uint16_t* out;
+    int32_t n_chunks, lanes, parts;            // a group's q-heads in `parts` parts
+    int32_t hq, hkv;
+    float scale;
+    int* status;
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_s,
+                       const __grid_constant__ CUtensorMap tm_o, const OutParams p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sb = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int* status = p.status;
+    if (sb & 1023u) {
+        if (threadIdx.x == 0) report_status(status, -5);
+        return;
+    }
+    const int part = blockIdx.x % p.parts, g = blockIdx.x / p.parts % p.hkv, j0 = blockIdx.x / p.parts / p.hkv;
+    const int G = p.hq / p.hkv / p.parts, h0 = (g * p.parts + part) * G;   // q-heads [h0, h0 + G)
+    if (j0 >= p.n_chunks) return;              // uniform: nothing set up yet
+    const int n_items = (p.n_chunks - 1 - j0) / p.lanes + 1, U = n_items * G;
+    auto chunk_of = [&](int i) { return j0 + i * p.lanes; };
+    auto bar = [&](int i) { return sb + 8u * (uint32_t)i; };
+    const uint32_t b_k = bar(0), b_v = bar(1), b_kfree = bar(2), b_vfree = bar(3), b_drain = bar(4), holder = bar(5);
+    auto b_qf = [&](int q) { return bar(6 + q); };     // Q slot q has come
+    auto b_sf = [&](int b) { return bar(10 + b); };    // A of buffer b is there
+    auto b_p = [&](int b) { return bar(12 + b); };     // P is
+    auto b_o = [&](int b) { return bar(14 + b); };     // O is
+    auto b_oe = [&](int b) { return bar(16 + b); };    // O has been read
+    auto b_qe = [&](int q) { return bar(18 + q); };    // Q slot q has been read
+    const uint32_t ka = sb + kOutK, va = sb + kOutV, sina = sb + kOutS, qa0 = sb + kOutQ;
+    float* ctab = reinterpret_cast<float*>(smem + 1024);   // gamma^-(m'+1), or gamma^t
+    if (threadIdx.x == 0) {
+        mbar_init(b_k, 1);
+        mbar_init(b_v, 1);
+        mbar_init(b_kfree, 1);
+        mbar_init(b_vfree, 1);
+        mbar_init(b_drain, 1);
+        for (int q = 0; q < kQSlots; ++q) {
+            mbar_init(b_qf(q), 1);
+            mbar_init(b_qe(q), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(b_sf(b), 1);
+            mbar_init(b_p(b), 256);
+            mbar_init(b_o(b), 1);
+            mbar_init(b_oe(b), 256);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 9) tmem_alloc(holder, 512);
+    grid_dep_wait();
+    grid_dep_launch();
+    const float lg = log2f(p.decay[g]);
+    const bool column = lg > -100.f / 128.f;
+    if (threadIdx.x < 128) ctab[threadIdx.x] = column ? exp2f(-(float)(threadIdx.x + 1) * lg) : exp2f((float)threadIdx.x * lg);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + 8 * 5);
+    bool ok = true;
+
+    if (warp == 8) {
+        if (lane == 0) {
+            int qs = 0;                            // Q loads sent; K and V waited for in order of need
+            bool k_sent = false, v_sent = false;
+            for (int i = 0; i < n_items && ok; ++i) {
+                const int chunk = chunk_of(i), off = p.chunks[4 * chunk];
+                k_sent = v_sent = false;
+                if (i > 0) ok = mbar_wait(b_kfree, (i - 1) & 1, status, 131);   // the last chunk's last A has read it
+                if (!ok) break;
+                mbar_expect_tx(b_k, kTile);
+                for (int blk = 0; blk < 2; ++blk) tma_load_3d(ka + blk * kHalf, &tm_k, blk * 64, g, off, b_k);
+                k_sent = true;
+                for (int n = 0; n < G && ok; ++n) {
+                    const int u = i * G + n, q = u % kQSlots;
+                    if (u >= kQSlots) ok = mbar_wait(b_qe(q), (u / kQSlots - 1) & 1, status, 132);
+                    if (!ok) break;
+                    mbar_expect_tx(b_qf(q), kTile);
+                    for (int blk = 0; blk < 2; ++blk)
+                        tma_load_3d(qa0 + q * kTile + blk * kHalf, &tm_q, blk * 64, h0 + n, off, b_qf(q));
+                    qs = u + 1;
+                    // V and S_in after the second q-head's Q (the first's with one q-head): the last chunk's
+                    // last products, which have read them, are issued before this chunk's second A
+                    if (n == (G > 1 ? 1 : 0)) {
+                        if (i > 0) ok = mbar_wait(b_vfree, (i - 1) & 1, status, 133);
+                        if (!ok) break;
+                        mbar_expect_tx(b_v, 2 * kTile);
+                        for (int blk = 0; blk < 2; ++blk) {
+                            tma_load_3d(va + blk * kHalf, &tm_v, blk * 64, g, off, b_v);
+                            tma_load_3d(sina + blk * kHalf, &tm_s, blk * 64, g, chunk * kChunk, b_v);
+                        }
+                        v_sent = true;
+                    }
+                }
+                if (!ok) {                         // copies still under way
+                    if (k_sent) mbar_wait(b_k, i & 1, status, 134);
+                    if (v_sent) mbar_wait(b_v, i & 1, status, 135);
+                }
+            }
+            if (!ok)
+                for (int u = max(0, qs - kQSlots); u < qs; ++u) mbar_wait(b_qf(u % kQSlots), (u / kQSlots) & 1, status, 136);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        if (lane == 0) {
+            constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false);   // Q K^T
+            constexpr uint32_t ID_O = idesc_bf16(128, 128, false, true);    // P V, Q S_in
+            auto issue_o = [&](int u) {
+                const int b = u & 1, i = u / G, n = u % G;
+                ok = mbar_wait(b_p(b), (u >> 1) & 1, status, 137);
+                if (ok && u >= 2) ok = mbar_wait(b_oe(b), ((u >> 1) - 1) & 1, status, 138);   // unit u - 2's output read
+                if (ok && n == 0) ok = mbar_wait(b_v, i & 1, status, 139);                     // this chunk's V and S_in
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t O = tmem + 256 * b + 128, P = tmem + 256 * b, qa = qa0 + u % kQSlots * kTile;
+                const int ksteps = (p.chunks[4 * chunk_of(i) + 1] + 15) / 16;
+                // keys 16k .. 16k + 15 of P packed at 64 (k / 4) + 8 (k % 4); features 16k .. 16k + 15 of f Q (strong
+                // decays) 32 columns further
+#pragma unroll
+                for (int k = 0; k < kChunk / 16; ++k)
+                    if (k < ksteps) mma_bf16_ts(O, P + (k >> 2) * 64 + (k & 3) * 8, sdesc_sw128(va + k * 2048, kHalf, 1024), ID_O, k > 0);
+#pragma unroll
+                for (int k = 0; k < kD / 16; ++k) {
+                    if (column)
+                        mma_bf16_ss(O, sdesc_sw128(qa + (k >> 2) * kHalf + (k & 3) * 32, 16, 1024),
+                                    sdesc_sw128(sina + k * 2048, kHalf, 1024), ID_O, 1u);
+                    else
+                        mma_bf16_ts(O, P + 32 + (k >> 2) * 64 + (k & 3) * 8, sdesc_sw128(sina + k * 2048, kHalf, 1024), ID_O, 1u);
+                }
+                mma_commit(b_o(b));
+                mma_commit(b_qe(u % kQSlots));
+                if (n == G - 1) mma_commit(b_vfree);
+            };
+            for (int u = 0; u < U && ok; ++u) {
+                const int b = u & 1, i = u / G, n = u % G, q = u % kQSlots;
+                ok = mbar_wait(b_qf(q), (u / kQSlots) & 1, status, 140);
+                if (ok && n == 0) ok = mbar_wait(b_k, i & 1, status, 141);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t qa = qa0 + q * kTile;
+#pragma unroll
+                for (int k = 0; k < kD / 16; ++k) {
+                    const uint32_t o = (k >> 2) * kHalf + (k & 3) * 32;
+                    mma_bf16_ss(tmem + 256 * b, sdesc_sw128(qa + o, 16, 1024), sdesc_sw128(ka + o, 16, 1024), ID_S, k > 0);
+                }
+                mma_commit(b_sf(b));
+                if (n == G - 1) mma_commit(b_kfree);
+                if (u > 0) issue_o(u - 1);
+            }
+            if (ok) issue_o(U - 1);
+            mma_commit(b_drain);
+            mbar_wait(b_drain, 0, status, 142);
+        }
+        __syncwarp();
+    } else {
+        const int quarter = warp & 3, m = (quarter << 5) + lane, grp = warp >> 2, col0 = grp * 64;
+        const uint32_t lane_base = tmem + ((uint32_t)(quarter << 5) << 16);
+        const float fo = p.scale * exp2f((float)(m + 1) * lg);
+        const uint32_t stage = sb + kOutStage + warp * 4096;
+        // Unit u's output is read after unit u + 1's mask.
+        int prev_off = 0, prev_L = 0, prev_h = 0;
+        for (int u = 0; u <= U; ++u) {
+            int off = 0, L = 0;
+            if (u < U) {
+                const int b = u & 1, i = u / G, chunk = chunk_of(i);
+                off = p.chunks[4 * chunk];
+                L = p.chunks[4 * chunk + 1];
+                const uint32_t tS = lane_base + 256 * b;
+                ok = mbar_wait(b_sf(b), (u >> 1) & 1, status, 143);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                // (rows m >= L are never stored, and for m < L every m' <= m lies in the chunk)
+#pragma unroll
+                for (int cc = 0; cc < 2; ++cc) {
+                    const int c0 = col0 + cc * 32;         // the warp's rows are [32 quarter, + 32)
+                    uint32_t pw[16];
+                    if (c0 > 32 * quarter) {               // behind all of them
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) pw[x] = 0;
+                    } else {
+                        float v[32];
+                        tmem_ld32(tS + c0, v);
+                        tmem_wait_ld();
+                        if (column) {
+                            const float4* t = reinterpret_cast<const float4*>(ctab + c0);
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) {
+                                const float4 w = t[x];
+                                v[4 * x] *= w.x;
+                                v[4 * x + 1] *= w.y;
+                                v[4 * x + 2] *= w.z;
+                                v[4 * x + 3] *= w.w;
+                            }
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) v[x] *= p.scale * ctab[max(m - c0 - x, 0)];
+                        }
+                        if (c0 == 32 * quarter) {
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) v[x] = x <= lane ? v[x] : 0.f;
+                        }
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) pw[x] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
+                    }
+                    tmem_st16(tS + col0 + cc * 16, pw);    // over columns that this thread has read
+                }
+                // the rows behind a ragged chunk are another node's: zeros in the last 16 that the product
+                // reads (0 times an infinity there would not be 0)
+                if (u % G == 0 && (L & 15)) {
+                    ok = mbar_wait(b_v, i & 1, status, 144);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (m >= L && m < ((L + 15) & ~15)) {
+                        uint4* v = reinterpret_cast<uint4*>(smem + kOutV + grp * kHalf + m * 128);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                if (!column) {
+                    // f(m) q_m over features [col0, col0 + 64) out of the swizzled slot
+                    const uint8_t* qrow = smem + kOutQ + u % kQSlots * kTile + grp * kHalf + m * 128;
+#pragma unroll
+                    for (int h2 = 0; h2 < 2; ++h2) {
+                        uint32_t qw[16];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(qrow + (((h2 * 4 + c) ^ (m & 7)) << 4));
+                            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                qw[4 * c + e] = pack_bf16x2(fo * __uint_as_float(xs[e] << 16),
+                                                            fo * __uint_as_float(xs[e] & 0xffff0000u));
+                        }
+                        tmem_st16(tS + col0 + 32 + h2 * 16, qw);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(b_p(b));
+            }
+            if (u > 0) {
+                const int b = (u - 1) & 1;
+                const uint32_t tO = lane_base + 256 * b + 128 + col0;
+                ok = mbar_wait(b_o(b), ((u - 1) >> 1) & 1, status, 145);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const bool whole = prev_L >= 32 * quarter + 32;   // all of the warp's rows are the chunk's
+                if (whole && lane == 0) bulk_wait_read_all();     // the last store has read its rows
+                __syncwarp();
+                uint4* dst = reinterpret_cast<uint4*>(p.out + ((size_t)(prev_off + m) * p.hq + prev_h) * kD + col0);
+#pragma unroll
+                for (int cc = 0; cc < 2; ++cc) {
+                    float v[32];
+                    tmem_ld32(tO + cc * 32, v);
+                    tmem_wait_ld();
+                    if (column) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) v[x] *= fo;
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint4 y = pack8(v + 8 * x);
+                        if (whole) st_shared_v4(stage + sw128_offset(lane, cc * 4 + x), y.x, y.y, y.z, y.w);
+                        else if (m < prev_L) dst[cc * 4 + x] = y;
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(b_oe(b));              // buffer b's O may take the unit after next
+                if (whole) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_3d(&tm_o, stage, col0, prev_h, prev_off + 32 * quarter);
+                        bulk_commit();
+                    }
+                }
+            }
+            prev_off = off;
+            prev_L = L;
+            prev_h = h0 + u % G;
+        }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+struct Ws {
+    size_t s_in, s_out, total;
+};
+Ws layout(const tree_attn_plan_s* P, int32_t hkv) {
+    const size_t nc = P->lin.chunks.size() / 4, per = (size_t)hkv * kD * kD;
+    return {0, nc * per * 2, nc * per * 2 + (size_t)P->n_nodes * per * 4};
+}
+
+}  // namespace
+
+}  // namespace treeattn
+
+using namespace treeattn;
+
+extern "C" {
+
+int tree_attn_linear_prefill_workspace_size(tree_attn_plan_t P, int32_t hkv, int32_t d, size_t* ws_bytes) {
+    if (!P || hkv <= 0 || !ws_bytes) return TREE_ATTN_ERR_INVALID_ARG;
+    if (d != kD || P->block != kChunk) return TREE_ATTN_ERR_UNSUPPORTED;
+    const int st = linear_chunks(P);
+    if (st) return st;
+    *ws_bytes = layout(P, hkv).total;
+    return TREE_ATTN_OK;
+}
+
+int tree_attn_linear_prefill(tree_attn_plan_t P, const void* q, const void* k, const void* v, void* o, float* states,
+                             int32_t n_slots, const int32_t* slot_in, const int32_t* slot_out, const float* decay,
+                             int32_t hq, int32_t hkv, int32_t d, float scale, void* workspace, size_t ws_bytes,
+                             void* stream) {
+    if (!P || !q || !k || !v || !o || !decay || hq <= 0 || hkv <= 0 || hq % hkv != 0) return TREE_ATTN_ERR_INVALID_ARG;
+    if (n_slots < 0 || (n_slots > 0 && !states)) return TREE_ATTN_ERR_INVALID_ARG;
+    if (d != kD || P->block != kChunk) return TREE_ATTN_ERR_UNSUPPORTED;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return TREE_ATTN_ERR_INVALID_ARG;
+    for (const void* p : {q, k, v, (const void*)o, (const void*)states})
+        if (!aligned(p, 16)) return TREE_ATTN_ERR_ALIGNMENT;
+    if (!aligned(decay, 4) || !aligned(slot_in, 4) || !aligned(slot_out, 4) || !aligned(workspace, 256))
+        return TREE_ATTN_ERR_ALIGNMENT;
+    DevicePlan* D = nullptr;
+    int st = ensure_linear(P, &D);
+    if (st) return st;
+    const Ws w = layout(P, hkv);
+    if (!workspace || ws_bytes < w.total) return TREE_ATTN_ERR_WORKSPACE;
+    const int64_t nc = (int64_t)(P->lin.chunks.size() / 4);
+    if (nc * hq > INT32_MAX || nc * kChunk > INT32_MAX || (int64_t)P->n_nodes * hkv * 2 > INT32_MAX) return TREE_ATTN_ERR_TOO_LARGE;
+    int dev, *status;
+    if ((st = current_device(&dev)) || (st = get_status_ptr(dev, &status))) return st;
+    char* ws = static_cast<char*>(workspace);
+    void* s_in = ws + w.s_in;
+    CUtensorMap tq, tk, tv, ts, ts32, to32;
+    if ((st = make_tensor_map(&tq, q, P->N, hq, d)) || (st = make_tensor_map(&tk, k, P->N, hkv, d)) ||
+        (st = make_tensor_map(&tv, v, P->N, hkv, d)) || (st = make_tensor_map(&ts, s_in, nc * kChunk, hkv, d)) ||
+        (st = make_tensor_map_rows(&ts32, s_in, nc * kChunk, hkv, d, 32)) ||
+        (st = make_tensor_map_rows(&to32, o, P->N, hq, d, 32)))
+        return st;
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t set[kMaxDevices];
+    static int sms[kMaxDevices];
+    std::call_once(once[dev], [&] {
+        set[dev] = launched(cudaFuncSetAttribute(prefill_state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStateSmem));
+        if (set[dev] == cudaSuccess)
+            set[dev] = launched(cudaFuncSetAttribute(prefill_out_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOutSmem));
+        if (cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms[dev] <= 0) sms[dev] = 1;
+    });
+    if (set[dev] != cudaSuccess) return TREE_ATTN_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const LinInfo& X = P->lin;
+    for (size_t l = 0; l + 1 < X.lvl_ptr.size(); ++l) {
+        const StateParams p = {D->lvl_nodes + X.lvl_ptr[l], D->lnodes, D->kids, D->chunks, decay,
+                               reinterpret_cast<float*>(ws + w.s_out), hkv, P->n_nodes, (int32_t)nc, l == 0,
+                               {states, slot_in, slot_out, D->lin_ids, n_slots, status}};
+        const unsigned grid = (unsigned)((int64_t)(X.lvl_ptr[l + 1] - X.lvl_ptr[l]) * hkv * 2);
+        if (launch_pdl(prefill_state_kernel, dim3(grid), dim3(kThreads), kStateSmem, s, tk, tv, ts32, p) != cudaSuccess)
+            return TREE_ATTN_ERR_CUDA;
+    }
+    // about one CTA per SM: lanes of chunks for each kv-head, and where there are fewer chunks than that, the
+    // group's q-heads in parts
+    const int G = hq / hkv;
+    const int lanes = (int)std::max<int64_t>(1, std::min<int64_t>(nc, sms[dev] / hkv));
+    int parts = 1;
+    for (int c = 2; c <= G; ++c)
+        if (G % c == 0 && (int64_t)lanes * hkv * c <= sms[dev]) parts = c;
+    const OutParams p = {D->chunks, decay, static_cast<uint16_t*>(o), (int32_t)nc, lanes, parts, hq, hkv, scale, status};
+    const cudaError_t e = launch_pdl(prefill_out_kernel, dim3((unsigned)(lanes * hkv * parts)), dim3(kThreads), kOutSmem, s,
+                                     tq, tk, tv, ts, to32, p);
+    return e == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA;
+}
+
+}  // extern "C"

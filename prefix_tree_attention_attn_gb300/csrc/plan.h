@@ -54,7 +54,7 @@ struct DevicePlan {
 struct LinInfo {
     std::vector<int32_t> chunks;   // as DevicePlan::chunks
     std::vector<int32_t> lnodes;   // as DevicePlan::lnodes
-    std::vector<int32_t> lvl_ptr;  // [depths+1] ranges of lvl_nodes; empty for trees too deep to scan by depth
+    std::vector<int32_t> lvl_ptr;  // [depths+1] ranges of lvl_nodes
     std::vector<int32_t> lvl_nodes;
     std::vector<int32_t> kids;     // as DevicePlan::kids
     bool ready = false;
@@ -116,8 +116,13 @@ int current_device(int* dev);
 // TMA map of a bf16 [rows, heads, d] tensor: boxes of 64 features x 1 head x
 // 128 rows, 128-byte swizzle.
 int make_tensor_map(CUtensorMap* m, const void* base, int64_t rows, int heads, int d);
+// The same with boxes of box_rows rows.
+int make_tensor_map_rows(CUtensorMap* m, const void* base, int64_t rows, int heads, int d, int box_rows);
 // TMA map of [rows, 128] bytes: boxes of box_rows whole rows, 128-byte swizzle.
 int make_byte_map(CUtensorMap* m, const void* base, int64_t rows, int box_rows);
+// Chunk tables of the linear attention: on the current device (uploaded once), or on the host alone.
+int ensure_linear(tree_attn_plan_s* P, DevicePlan** out);
+int linear_chunks(tree_attn_plan_s* P);
 // Device memory with a copy of n words (the caller's to free).  The copy has ended when the call
 // returns, so kernels on any stream may read it.
 int upload_words(void** out, const int32_t* words, size_t n);

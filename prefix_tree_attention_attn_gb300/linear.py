@@ -153,7 +153,10 @@ def _check_states(states, slots: StateSlots, hkv: int, d: int, dev: int) -> None
 
 def prefill_workspace(plan: TreePlan, hkv: int, d: int) -> int:
     """Bytes of device workspace that ``tree_linear_prefill`` needs."""
-    return linear_workspace(plan, hkv, d)[1]
+    ws = C.c_size_t()
+    B.check(B.load().tree_attn_linear_prefill_workspace_size(plan.handle, hkv, d, C.byref(ws)),
+            "tree_attn_linear_prefill_workspace_size")
+    return int(ws.value)
 
 
 def tree_linear_prefill(plan: TreePlan, states, slots: StateSlots, q, k, v, decay, scale: float, o=None,
