@@ -586,6 +586,10 @@ int build_lin(tree_attn_plan_s* P) {
         X.lvl_nodes.resize(n);
         std::vector<int32_t> fill(X.lvl_ptr.begin(), X.lvl_ptr.end() - 1);
         for (int32_t k = 0; k < n; ++k) X.lvl_nodes[fill[depth[k]]++] = k;
+        // the longest nodes of a depth first: they end last
+        for (int32_t l = 0; l < n_depths; ++l)
+            std::stable_sort(X.lvl_nodes.begin() + X.lvl_ptr[l], X.lvl_nodes.begin() + X.lvl_ptr[(size_t)l + 1],
+                             [&](int32_t a, int32_t b) { return X.lnodes[4 * (size_t)a + 2] > X.lnodes[4 * (size_t)b + 2]; });
         X.ready = true;
     } catch (const std::bad_alloc&) {
         return TREE_ATTN_ERR_OUT_OF_MEMORY;

@@ -7,8 +7,7 @@
 //     dS = sum_m gamma^(L-1-m) k_m v_m^T on the tensor cores.
 //   A weighted value has 24 bits; it is split into three bf16 numbers that add up to it, so the
 //   increment is as exact as sums in fp32 are (two would leave 3e-6 of it).  Warps 0-3 hold the
-//   state, warps 4-7 weigh and split the values, warp 8 loads, warp 9 issues the products; every
-//   stage is double-buffered.  It replaces a product per chunk that left its fp32 increment in memory
+//   state, warps 4-11 weigh and split the values, warp 12 loads, warp 13 issues the products.  It replaces a product per chunk that left its fp32 increment in memory
 //   and a scan over those (64 KB each way per chunk and kv-head): group star 45 -> see below.
 //
 // prefill_out_kernel, persistent, a unit (chunk, q-head) after the other: A = Q K^T, then
@@ -64,8 +63,13 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
 }
 
 // ---- the states that enter the chunks --------------------------------------------------------
-constexpr int kStateK = 1024, kStateV = kStateK + 2 * kTile, kStateW = kStateV + 2 * kHalf,
-              kStateOut = kStateW + 6 * kHalf, kStateSmem = kStateOut + kHalf;
+// K and V in three stages (a chunk's load takes as long as two chunks' products); the values' first part
+// goes over V, the other two into one of two tile pairs.
+constexpr int kStages = 3;
+constexpr int kStateK = 1024, kStateV = kStateK + kStages * kTile, kStateW = kStateV + kStages * kHalf,
+              kStateOut = kStateW + 4 * kHalf, kStateSmem = kStateOut + kHalf;
+constexpr int kStateThreads = 448;             // 4 warps hold the state, 8 weigh, loader, MMA
+constexpr int kAhead = 6;                      // chunks that are brought into L2 ahead of their load
 
 struct StateParams {
     const int32_t* nodes;      // packed nodes of this depth
@@ -79,7 +83,7 @@ struct StateParams {
     SlotIO io;
 };
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kStateThreads, 1)
     prefill_state_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const __grid_constant__ CUtensorMap tm_s, const StateParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -90,30 +94,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 0) report_status(status, -5);
         return;
     }
-    auto full = [&](int s) { return sb + 8u * s; };           // K, V have come
-    auto empty = [&](int s) { return sb + 16 + 8u * s; };     // and have been multiplied
-    auto wfull = [&](int s) { return sb + 32 + 8u * s; };     // the weighted values are there
-    auto wfree = [&](int s) { return sb + 48 + 8u * s; };
-    auto dfull = [&](int s) { return sb + 64 + 8u * s; };     // the increment is there
-    auto dfree = [&](int s) { return sb + 80 + 8u * s; };
-    const uint32_t drain = sb + 96, holder = sb + 104;
+    auto full = [&](int s) { return sb + 8u * s; };           // K, V of stage s have come
+    auto empty = [&](int s) { return sb + 24 + 8u * s; };     // and have been multiplied
+    auto wfull = [&](int s) { return sb + 48 + 8u * s; };     // the weighted values are there
+    auto wfree = [&](int w) { return sb + 72 + 8u * w; };     // tile pair w has been multiplied
+    auto dfull = [&](int w) { return sb + 88 + 8u * w; };     // the increment is there
+    auto dfree = [&](int w) { return sb + 104 + 8u * w; };
+    const uint32_t drain = sb + 120, holder = sb + 128;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
-            mbar_init(wfull(s), 128);
-            mbar_init(wfree(s), 1);
-            mbar_init(dfull(s), 1);
-            mbar_init(dfree(s), 128);
+            mbar_init(wfull(s), 256);
+        }
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(wfree(w), 1);
+            mbar_init(dfull(w), 1);
+            mbar_init(dfree(w), 128);
         }
         mbar_init(drain, 1);
         fence_mbar_init();
     }
-    if (warp == 9) tmem_alloc(holder, 128);
+    if (warp == 13) tmem_alloc(holder, 128);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + 104);
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + 128);
     const int half = blockIdx.x & 1, g = (blockIdx.x >> 1) % p.hkv, node = p.nodes[(blockIdx.x >> 1) / p.hkv];
     bool ok = ta_ok(status, 620, node, 0, p.n_nodes);
     const int par = ok ? p.lnodes[4 * node] : -1, c0 = ok ? p.lnodes[4 * node + 1] : 0, n = ok ? p.lnodes[4 * node + 2] : 0;
@@ -188,25 +194,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) bulk_wait_all();
         __syncwarp();
-    } else if (warp < 8) {
-        // the values: thread = token, its row times gamma^(L-1-r) as three numbers that add up to it
-        const int r = threadIdx.x - 128;
+    } else if (warp < 12) {
+        // the values: thread = token r and 32 features, times gamma^(L-1-r), as three numbers that add up to it
+        const int r = threadIdx.x & 127, piece = (warp - 4) >> 2;
         for (int i = 0; i < steps && ok; ++i) {
-            const int s = i & 1;
-            ok = mbar_wait(full(s), (i >> 1) & 1, status, 122);
-            if (ok && i >= 2) ok = mbar_wait(wfree(s), ((i >> 1) - 1) & 1, status, 123);
+            const int s = i % kStages, w2 = i & 1;
+            ok = mbar_wait(full(s), (i / kStages) & 1, status, 122);
+            if (ok && i >= 2) ok = mbar_wait(wfree(w2), ((i >> 1) - 1) & 1, status, 123);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const int L = p.chunks[4 * (c0 + i) + 1];
             const bool past = r >= L;              // another node's row: zeros, whatever it holds
             const float w = past ? 0.f : exp2f((float)(L - 1 - r) * lg);
-            const uint4* v = reinterpret_cast<const uint4*>(smem + kStateV + s * kHalf + r * 128);
-            uint4* out = reinterpret_cast<uint4*>(smem + kStateW + s * 3 * kHalf + r * 128);
+            uint4* v = reinterpret_cast<uint4*>(smem + kStateV + s * kHalf + r * 128);
+            uint4* out = reinterpret_cast<uint4*>(smem + kStateW + w2 * 2 * kHalf + r * 128);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                // the row's 16-byte pieces in an order rotated by the row: the rows of a warp spread over
-                // all bank groups (a piece keeps its swizzled place)
-                const int cr = (c + r) & 7;
+            for (int c = 0; c < 4; ++c) {
+                // four of the row's eight 16-byte pieces, in an order rotated by the row: the rows of a warp spread
+                // over all bank groups (a piece keeps its swizzled place)
+                const int cr = (4 * piece + c + r) & 7;
                 const uint4 x = v[cr];
                 const uint32_t u[4] = {x.x, x.y, x.z, x.w};
                 uint32_t p1[4], p2[4], p3[4];
@@ -221,53 +227,63 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p2[e] = pack_bf16x2(a2, b2);
                     p3[e] = pack_bf16x2(a2 - __uint_as_float(p2[e] << 16), b2 - __uint_as_float(p2[e] & 0xffff0000u));
                 }
-                out[cr] = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-                out[kHalf / 16 + cr] = make_uint4(p2[0], p2[1], p2[2], p2[3]);
-                out[2 * kHalf / 16 + cr] = make_uint4(p3[0], p3[1], p3[2], p3[3]);
+                v[cr] = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+                out[cr] = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+                out[kHalf / 16 + cr] = make_uint4(p3[0], p3[1], p3[2], p3[3]);
             }
             if (past) {                            // its keys meet those zeros: no infinities there either
-                uint4* k = reinterpret_cast<uint4*>(smem + kStateK + s * kTile + r * 128);
+                uint4* k = reinterpret_cast<uint4*>(smem + kStateK + s * kTile + piece * kHalf + r * 128);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) k[(c + r) & 7] = k[kHalf / 16 + ((c + r) & 7)] = make_uint4(0, 0, 0, 0);
+                for (int c = 0; c < 8; ++c) k[(c + r) & 7] = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             mbar_arrive(wfull(s));
         }
-    } else if (warp == 8) {
+    } else if (warp == 12) {
         if (lane == 0) {
+            auto prefetch = [&](int i) {
+                if (i >= steps) return;
+                const int off = p.chunks[4 * (c0 + i)];
+                for (int blk = 0; blk < 2; ++blk) tma_prefetch_3d(&tm_k, blk * 64, g, off);
+                tma_prefetch_3d(&tm_v, half * 64, g, off);
+            };
+            for (int i = kStages; i < kAhead; ++i) prefetch(i);
             int sent = 0;
             for (int i = 0; i < steps && ok; ++i) {
-                const int s = i & 1, off = p.chunks[4 * (c0 + i)];
-                if (i >= 2) ok = mbar_wait(empty(s), ((i >> 1) - 1) & 1, status, 124);
+                const int s = i % kStages, off = p.chunks[4 * (c0 + i)];
+                if (i >= kStages) ok = mbar_wait(empty(s), (i / kStages - 1) & 1, status, 124);
                 if (!ok) break;
                 mbar_expect_tx(full(s), kTile + kHalf);
                 for (int blk = 0; blk < 2; ++blk)
                     tma_load_3d(sb + kStateK + s * kTile + blk * kHalf, &tm_k, blk * 64, g, off, full(s));
                 tma_load_3d(sb + kStateV + s * kHalf, &tm_v, half * 64, g, off, full(s));
                 sent = i + 1;
+                prefetch(i + kAhead);
             }
             if (!ok)                               // copies still under way
-                for (int i = max(0, sent - 2); i < sent; ++i) mbar_wait(full(i & 1), (i >> 1) & 1, status, 125);
+                for (int i = max(0, sent - kStages); i < sent; ++i) mbar_wait(full(i % kStages), (i / kStages) & 1, status, 125);
         }
         __syncwarp();
     } else {
         if (lane == 0) {
             constexpr uint32_t ID = idesc_bf16(128, 64, true, true);   // K^T (MN-major) x V_w (MN-major)
             for (int i = 0; i < steps && ok; ++i) {
-                const int s = i & 1;
-                ok = mbar_wait(wfull(s), (i >> 1) & 1, status, 126);
-                if (ok && i >= 2) ok = mbar_wait(dfree(s), ((i >> 1) - 1) & 1, status, 127);
+                const int s = i % kStages, w2 = i & 1;
+                ok = mbar_wait(wfull(s), (i / kStages) & 1, status, 126);
+                if (ok && i >= 2) ok = mbar_wait(dfree(w2), ((i >> 1) - 1) & 1, status, 127);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t ka = sb + kStateK + s * kTile, wa = sb + kStateW + s * 3 * kHalf;
+                const uint32_t ka = sb + kStateK + s * kTile;
 #pragma unroll
-                for (int part = 0; part < 3; ++part)
+                for (int part = 0; part < 3; ++part) {
+                    const uint32_t wa = part ? sb + kStateW + w2 * 2 * kHalf + (part - 1) * kHalf : sb + kStateV + s * kHalf;
 #pragma unroll
                     for (int k = 0; k < kChunk / 16; ++k)
-                        mma_bf16_ss(tmem + s * 64, sdesc_sw128(ka + k * 2048, kHalf, 1024),
-                                    sdesc_sw128(wa + part * kHalf + k * 2048, kHalf, 1024), ID, part > 0 || k > 0);
-                mma_commit(dfull(s));
-                mma_commit(wfree(s));
+                        mma_bf16_ss(tmem + w2 * 64, sdesc_sw128(ka + k * 2048, kHalf, 1024),
+                                    sdesc_sw128(wa + k * 2048, kHalf, 1024), ID, part > 0 || k > 0);
+                }
+                mma_commit(dfull(w2));
+                mma_commit(wfree(w2));
                 mma_commit(empty(s));
             }
             mma_commit(drain);
@@ -277,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 13) {
         tc_fence_after();
         tmem_dealloc(tmem, 128);
     }
@@ -670,7 +686,7 @@ int tree_attn_linear_prefill(tree_attn_plan_t P, const void* q, const void* k, c
                                reinterpret_cast<float*>(ws + w.s_out), hkv, P->n_nodes, (int32_t)nc, l == 0,
                                {states, slot_in, slot_out, D->lin_ids, n_slots, status}};
         const unsigned grid = (unsigned)((int64_t)(X.lvl_ptr[l + 1] - X.lvl_ptr[l]) * hkv * 2);
-        if (launch_pdl(prefill_state_kernel, dim3(grid), dim3(kThreads), kStateSmem, s, tk, tv, ts32, p) != cudaSuccess)
+        if (launch_pdl(prefill_state_kernel, dim3(grid), dim3(kStateThreads), kStateSmem, s, tk, tv, ts32, p) != cudaSuccess)
             return TREE_ATTN_ERR_CUDA;
     }
     // about one CTA per SM: lanes of chunks for each kv-head, and where there are fewer chunks than that, the
