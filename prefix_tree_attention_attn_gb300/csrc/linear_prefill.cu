@@ -6,9 +6,13 @@
 //     S_in of the chunk goes out as bf16, the operand of the outputs;  S = gamma^L S + dS,
 //     dS = sum_m gamma^(L-1-m) k_m v_m^T on the tensor cores.
 //   A weighted value has 24 bits; it is split into three bf16 numbers that add up to it, so the
-//   increment is as exact as sums in fp32 are (two would leave 3e-6 of it).  Warps 0-3 hold the
-//   state, warps 4-11 weigh and split the values, warp 12 loads, warp 13 issues the products.  It replaces a product per chunk that left its fp32 increment in memory
-//   and a scan over those (64 KB each way per chunk and kv-head): group star 45 -> see below.
+//   increment is as exact as sums in fp32 are (two would leave 3e-6 of it).  The parts lie side by side in one
+//   product of N = 192, so K is read once, and are added in registers.  Warps 0-7 hold the state,
+//   8-15 weigh and split the values, 16 loads, 17 issues.  208 KB pass through shared memory per
+//   chunk, 1,630 cycles at 128 bytes a cycle, and pace it.
+//   Where a depth has few nodes but long ones, they are cut into segments: a first launch
+//   leaves what each adds to the state, then each segment starts from its node's state with the segments
+//   before it added.
 //
 // prefill_out_kernel, persistent, a unit (chunk, q-head) after the other: A = Q K^T, then
 //     O = diag(f) (P V + Q S_in),  P[m, m'] = gamma^-(m'+1) A[m, m'] for m' <= m,  f(m) = scale gamma^(m+1).
@@ -58,28 +62,39 @@ __device__ __forceinline__ int slot_of(const SlotIO& io, const int32_t* table, i
     return s;
 }
 
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The descriptor of a tile `bytes` further on (shared memory ends below 2^18, so the address field holds the sum).
+__device__ __forceinline__ uint64_t further(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
+
 __device__ __forceinline__ uint4 pack8(const float* v) {
     return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
 // ---- the states that enter the chunks --------------------------------------------------------
-// K and V in three stages (a chunk's load takes as long as two chunks' products); the values' first part
-// goes over V, the other two into one of two tile pairs.
-constexpr int kStages = 3;
-constexpr int kStateK = 1024, kStateV = kStateK + kStages * kTile, kStateW = kStateV + kStages * kHalf,
-              kStateOut = kStateW + 4 * kHalf, kStateSmem = kStateOut + kHalf;
-constexpr int kStateThreads = 448;             // 4 warps hold the state, 8 weigh, loader, MMA
+// K in two stages; V in three, each with room for its other two parts behind it (the first goes over V).
+constexpr int kKStages = 2, kVStages = 3;
+constexpr int kStateK = 1024, kStateV = kStateK + kKStages * kTile, kStateOut = kStateV + kVStages * 3 * kHalf,
+              kStateSmem = kStateOut + kHalf;
+constexpr int kStateThreads = 576;             // 8 warps hold the state, 8 weigh, loader, MMA
 constexpr int kAhead = 6;                      // chunks that are brought into L2 ahead of their load
 
 struct StateParams {
-    const int32_t* nodes;      // packed nodes of this depth
+    const int4* jobs;          // {packed node, first of its chunks, chunks, its first segment's place in `sums`}
     const int32_t* lnodes;     // [4*n_nodes] {parent's packed index, first chunk, chunks, ..}
     const int32_t* kids;       // child offsets
     const int32_t* chunks;     // [4*n_chunks] {first token, tokens, ..}
     const float* decay;
     float* s_out;              // [n_nodes, hkv, d, d], nodes with children
+    float* sums;               // [segments, hkv, d, d] what a segment adds to the state
     int32_t hkv, n_nodes, n_chunks;
     int32_t first_depth;
+    int32_t segment;           // chunks of a segment but a node's last
+    int32_t adding;            // 1: this launch leaves the sums
     SlotIO io;
 };
 
@@ -94,120 +109,152 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         if (threadIdx.x == 0) report_status(status, -5);
         return;
     }
-    auto full = [&](int s) { return sb + 8u * s; };           // K, V of stage s have come
-    auto empty = [&](int s) { return sb + 24 + 8u * s; };     // and have been multiplied
-    auto wfull = [&](int s) { return sb + 48 + 8u * s; };     // the weighted values are there
-    auto wfree = [&](int w) { return sb + 72 + 8u * w; };     // tile pair w has been multiplied
-    auto dfull = [&](int w) { return sb + 88 + 8u * w; };     // the increment is there
-    auto dfree = [&](int w) { return sb + 104 + 8u * w; };
-    const uint32_t drain = sb + 120, holder = sb + 128;
+    auto kfull = [&](int s) { return sb + 8u * s; };          // K of stage s has come
+    auto kfree = [&](int s) { return sb + 16 + 8u * s; };     // and has been multiplied
+    auto vfull = [&](int s) { return sb + 32 + 8u * s; };
+    auto vfree = [&](int s) { return sb + 56 + 8u * s; };
+    auto wfull = [&](int s) { return sb + 80 + 8u * s; };     // the weighted values are there
+    auto dfull = [&](int b) { return sb + 104 + 8u * b; };    // the increment is there
+    auto dfree = [&](int b) { return sb + 120 + 8u * b; };
+    const uint32_t drain = sb + 136, holder = sb + 144;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(full(s), 1);
-            mbar_init(empty(s), 1);
+        for (int s = 0; s < kKStages; ++s) {
+            mbar_init(kfull(s), 1);
+            mbar_init(kfree(s), 1);
+        }
+        for (int s = 0; s < kVStages; ++s) {
+            mbar_init(vfull(s), 1);
+            mbar_init(vfree(s), 1);
             mbar_init(wfull(s), 256);
         }
-        for (int w = 0; w < 2; ++w) {
-            mbar_init(wfree(w), 1);
-            mbar_init(dfull(w), 1);
-            mbar_init(dfree(w), 128);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(dfull(b), 1);
+            mbar_init(dfree(b), 256);
         }
         mbar_init(drain, 1);
         fence_mbar_init();
     }
-    if (warp == 13) tmem_alloc(holder, 128);
+    if (warp == 17) tmem_alloc(holder, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + 128);
-    const int half = blockIdx.x & 1, g = (blockIdx.x >> 1) % p.hkv, node = p.nodes[(blockIdx.x >> 1) / p.hkv];
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + 144);
+    const int half = blockIdx.x & 1, g = (blockIdx.x >> 1) % p.hkv;
+    const int4 job = p.jobs[(blockIdx.x >> 1) / p.hkv];
+    const int node = job.x, n = job.z;
     bool ok = ta_ok(status, 620, node, 0, p.n_nodes);
-    const int par = ok ? p.lnodes[4 * node] : -1, c0 = ok ? p.lnodes[4 * node + 1] : 0, n = ok ? p.lnodes[4 * node + 2] : 0;
+    const int par = ok ? p.lnodes[4 * node] : -1, c0 = ok ? p.lnodes[4 * node + 1] + job.y : 0;
     ok = ok && ta_ok(status, 621, c0, 0, p.n_chunks) && ta_ok(status, 622, c0 + n, 0, p.n_chunks + 1);
-    const bool inner = ok && p.kids[node + 1] > p.kids[node];
+    const bool last = ok && job.y + n == p.lnodes[4 * node + 2];
+    const bool inner = last && p.kids[node + 1] > p.kids[node];
+    const int end = ok ? p.chunks[4 * (c0 + n - 1) + 1] : 0;   // tokens of the last chunk; the others have 128
+    auto tokens = [&](int i) { return i == n - 1 ? end : kChunk; };
     grid_dep_wait();
     grid_dep_launch();
     const float gamma = p.decay[g], lg = log2f(gamma);
     // (once per kv-head; the call's outputs are then undefined)
     if (p.first_depth && blockIdx.x < 2 * p.hkv && half == 0 && threadIdx.x == 0 && !(gamma > 0.f && gamma <= 1.f))
         report_notice(status, TREE_ATTN_ERR_INVALID_DECAY);
-    const int to = ok ? slot_of(p.io, p.io.out, node) : -1;
-    const int steps = !ok ? 0 : inner || to >= 0 ? n : n - 1;   // increments that anything needs
+    const int to = last ? slot_of(p.io, p.io.out, node) : -1;
+    const int steps = !ok ? 0 : p.adding || inner || to >= 0 ? n : n - 1;   // increments that anything needs
 
-    if (warp < 4) {
-        // the state: thread = key feature, 64 value features
-        const int row = threadIdx.x;
-        const size_t at = (size_t)g * kD * kD + (size_t)row * kD + half * 64;
-        float S[64];
+    if (warp < 8) {
+        // the state: thread = key feature, 32 value features
+        const int quarter = warp & 3, row = 32 * quarter + lane, col0 = half * 64 + 32 * (warp >> 2);
+        const size_t at = (size_t)g * kD * kD + (size_t)row * kD + col0;
+        float S[32];
         const int from = ok && par < 0 ? slot_of(p.io, p.io.in, node) : -1;
-        const float* src = par >= 0 ? p.s_out + (size_t)par * p.hkv * kD * kD + at
+        const float* src = p.adding ? nullptr
+                           : par >= 0 ? p.s_out + (size_t)par * p.hkv * kD * kD + at
                                     : from >= 0 ? p.io.states + (size_t)from * p.hkv * kD * kD + at : nullptr;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
             const float4 v = src ? reinterpret_cast<const float4*>(src)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
             S[4 * i] = v.x;
             S[4 * i + 1] = v.y;
             S[4 * i + 2] = v.z;
             S[4 * i + 3] = v.w;
         }
-        const uint32_t stage = sb + kStateOut + warp * 4096;
-        for (int i = 0; i < n && ok; ++i) {
-            if (lane == 0) bulk_wait_read_all();   // the last one has left
-            __syncwarp();
+        if (ok && !p.adding && job.y > 0) {        // the node's segments before this one
+            const float f = exp2f((float)(p.segment * kChunk) * lg);
+            for (int t = 0; t < job.y / p.segment; ++t) {
+                const float4* add = reinterpret_cast<const float4*>(p.sums + (size_t)(job.w + t) * p.hkv * kD * kD + at);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const uint4 y = pack8(S + 8 * c);
-                st_shared_v4(stage + sw128_offset(lane, c), y.x, y.y, y.z, y.w);
+                for (int i = 0; i < 8; ++i) {
+                    const float4 v = add[i];
+                    S[4 * i] = fmaf(f, S[4 * i], v.x);
+                    S[4 * i + 1] = fmaf(f, S[4 * i + 1], v.y);
+                    S[4 * i + 2] = fmaf(f, S[4 * i + 2], v.z);
+                    S[4 * i + 3] = fmaf(f, S[4 * i + 3], v.w);
+                }
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                tma_store_3d(&tm_s, stage, half * 64, g, (c0 + i) * kChunk + warp * 32);
-                bulk_commit();
+        }
+        const uint32_t stage = sb + kStateOut + warp * 2048, tD = tmem + ((uint32_t)(32 * quarter) << 16) + 32 * (warp >> 2);
+        const float f128 = exp2f((float)kChunk * lg);
+        for (int i = 0; i < n && ok; ++i) {
+            if (!p.adding) {
+                if (lane == 0) bulk_wait_read_all();   // the last one has left
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint4 y = pack8(S + 8 * c);
+                    st_shared_v4(stage + lane * 64 + c * 16, y.x, y.y, y.z, y.w);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(&tm_s, stage, col0, g, (c0 + i) * kChunk + 32 * quarter);
+                    bulk_commit();
+                }
             }
             if (i >= steps) break;
-            const int s = i & 1;
-            ok = mbar_wait(dfull(s), (i >> 1) & 1, status, 121);
+            const int b = i & 1;
+            ok = mbar_wait(dfull(b), (i >> 1) & 1, status, 121);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            const float f = exp2f((float)p.chunks[4 * (c0 + i) + 1] * lg);
+            const float f = i == n - 1 ? exp2f((float)end * lg) : f128;
+            float v[32], more[32];                 // the three parts
+            tmem_ld32(tD + b * 192, v);
+            tmem_ld32(tD + b * 192 + 64, more);
+            tmem_wait_ld();
 #pragma unroll
-            for (int cc = 0; cc < 2; ++cc) {
-                float v[32];
-                tmem_ld32(tmem + ((uint32_t)(warp << 5) << 16) + s * 64 + cc * 32, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int x = 0; x < 32; ++x) S[cc * 32 + x] = fmaf(f, S[cc * 32 + x], v[x]);
-            }
+            for (int x = 0; x < 32; ++x) v[x] += more[x];
+            tmem_ld32(tD + b * 192 + 128, more);
+            tmem_wait_ld();
             tc_fence_before();
-            mbar_arrive(dfree(s));
+            mbar_arrive(dfree(b));
+#pragma unroll
+            for (int x = 0; x < 32; ++x) S[x] = fmaf(f, S[x], v[x] + more[x]);
         }
         if (ok) {
             auto leave = [&](float* dst) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
+                for (int i = 0; i < 8; ++i)
                     reinterpret_cast<float4*>(dst)[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
             };
-            if (inner) leave(p.s_out + (size_t)node * p.hkv * kD * kD + at);
-            if (to >= 0) leave(p.io.states + (size_t)to * p.hkv * kD * kD + at);
+            if (p.adding) leave(p.sums + (size_t)(job.w + job.y / p.segment) * p.hkv * kD * kD + at);
+            else if (inner) leave(p.s_out + (size_t)node * p.hkv * kD * kD + at);
+            if (!p.adding && to >= 0) leave(p.io.states + (size_t)to * p.hkv * kD * kD + at);
         }
         if (lane == 0) bulk_wait_all();
         __syncwarp();
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // the values: thread = token r and 32 features, times gamma^(L-1-r), as three numbers that add up to it
-        const int r = threadIdx.x & 127, piece = (warp - 4) >> 2;
+        const int r = threadIdx.x & 127, piece = (warp - 8) >> 2;
+        const float w128 = exp2f((float)(kChunk - 1 - r) * lg);
+        const uint64_t minus = f32x2(-1.f, -1.f);
         for (int i = 0; i < steps && ok; ++i) {
-            const int s = i % kStages, w2 = i & 1;
-            ok = mbar_wait(full(s), (i / kStages) & 1, status, 122);
-            if (ok && i >= 2) ok = mbar_wait(wfree(w2), ((i >> 1) - 1) & 1, status, 123);
+            const int s = i % kVStages, sk = i % kKStages;
+            ok = mbar_wait(vfull(s), (i / kVStages) & 1, status, 122);
+            const int L = tokens(i);
+            const bool past = r >= L;              // another node's row: zeros, whatever it holds
+            if (ok && L < kChunk) ok = mbar_wait(kfull(sk), (i / kKStages) & 1, status, 123);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            const int L = p.chunks[4 * (c0 + i) + 1];
-            const bool past = r >= L;              // another node's row: zeros, whatever it holds
-            const float w = past ? 0.f : exp2f((float)(L - 1 - r) * lg);
-            uint4* v = reinterpret_cast<uint4*>(smem + kStateV + s * kHalf + r * 128);
-            uint4* out = reinterpret_cast<uint4*>(smem + kStateW + w2 * 2 * kHalf + r * 128);
+            const float w = L == kChunk ? w128 : past ? 0.f : exp2f((float)(L - 1 - r) * lg);
+            const uint64_t ww = f32x2(w, w);
+            uint4* v = reinterpret_cast<uint4*>(smem + kStateV + s * 3 * kHalf + r * 128);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 // four of the row's eight 16-byte pieces, in an order rotated by the row: the rows of a warp spread
@@ -218,28 +265,30 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 uint32_t p1[4], p2[4], p3[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float a = past ? 0.f : __uint_as_float(u[e] << 16) * w;
-                    const float b = past ? 0.f : __uint_as_float(u[e] & 0xffff0000u) * w;
+                    // (what is not a number has no parts, and stays none)
+                    float a, b, a1, b1;
+                    const uint64_t y = past ? 0ull : mul_f32x2(f32x2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xffff0000u)), ww);
+                    f32x2_split(y, a, b);
                     p1[e] = pack_bf16x2(a, b);
-                    // (an infinity or NaN is its first part's)
-                    const float a1 = __uint_as_float(p1[e] << 16), b1 = __uint_as_float(p1[e] & 0xffff0000u);
-                    const float a2 = fabsf(a1) < INFINITY ? a - a1 : 0.f, b2 = fabsf(b1) < INFINITY ? b - b1 : 0.f;
-                    p2[e] = pack_bf16x2(a2, b2);
-                    p3[e] = pack_bf16x2(a2 - __uint_as_float(p2[e] << 16), b2 - __uint_as_float(p2[e] & 0xffff0000u));
+                    const uint64_t y2 = fma_f32x2(f32x2(__uint_as_float(p1[e] << 16), __uint_as_float(p1[e] & 0xffff0000u)), minus, y);
+                    f32x2_split(y2, a, b);
+                    p2[e] = pack_bf16x2(a, b);
+                    f32x2_split(fma_f32x2(f32x2(__uint_as_float(p2[e] << 16), __uint_as_float(p2[e] & 0xffff0000u)), minus, y2), a1, b1);
+                    p3[e] = pack_bf16x2(a1, b1);
                 }
                 v[cr] = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-                out[cr] = make_uint4(p2[0], p2[1], p2[2], p2[3]);
-                out[kHalf / 16 + cr] = make_uint4(p3[0], p3[1], p3[2], p3[3]);
+                v[kHalf / 16 + cr] = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+                v[2 * kHalf / 16 + cr] = make_uint4(p3[0], p3[1], p3[2], p3[3]);
             }
             if (past) {                            // its keys meet those zeros: no infinities there either
-                uint4* k = reinterpret_cast<uint4*>(smem + kStateK + s * kTile + piece * kHalf + r * 128);
+                uint4* k = reinterpret_cast<uint4*>(smem + kStateK + sk * kTile + piece * kHalf + r * 128);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) k[(c + r) & 7] = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             mbar_arrive(wfull(s));
         }
-    } else if (warp == 12) {
+    } else if (warp == 16) {
         if (lane == 0) {
             auto prefetch = [&](int i) {
                 if (i >= steps) return;
@@ -247,44 +296,47 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 for (int blk = 0; blk < 2; ++blk) tma_prefetch_3d(&tm_k, blk * 64, g, off);
                 tma_prefetch_3d(&tm_v, half * 64, g, off);
             };
-            for (int i = kStages; i < kAhead; ++i) prefetch(i);
+            for (int i = kKStages; i < kAhead; ++i) prefetch(i);
             int sent = 0;
             for (int i = 0; i < steps && ok; ++i) {
-                const int s = i % kStages, off = p.chunks[4 * (c0 + i)];
-                if (i >= kStages) ok = mbar_wait(empty(s), (i / kStages - 1) & 1, status, 124);
+                const int s = i % kVStages, sk = i % kKStages, off = p.chunks[4 * (c0 + i)];
+                if (i >= kVStages) ok = mbar_wait(vfree(s), (i / kVStages - 1) & 1, status, 124);
                 if (!ok) break;
-                mbar_expect_tx(full(s), kTile + kHalf);
-                for (int blk = 0; blk < 2; ++blk)
-                    tma_load_3d(sb + kStateK + s * kTile + blk * kHalf, &tm_k, blk * 64, g, off, full(s));
-                tma_load_3d(sb + kStateV + s * kHalf, &tm_v, half * 64, g, off, full(s));
+                mbar_expect_tx(vfull(s), kHalf);
+                tma_load_3d(sb + kStateV + s * 3 * kHalf, &tm_v, half * 64, g, off, vfull(s));
                 sent = i + 1;
+                if (i >= kKStages) ok = mbar_wait(kfree(sk), (i / kKStages - 1) & 1, status, 125);
+                if (!ok) break;
+                mbar_expect_tx(kfull(sk), kTile);
+                for (int blk = 0; blk < 2; ++blk)
+                    tma_load_3d(sb + kStateK + sk * kTile + blk * kHalf, &tm_k, blk * 64, g, off, kfull(sk));
                 prefetch(i + kAhead);
             }
-            if (!ok)                               // copies still under way
-                for (int i = max(0, sent - kStages); i < sent; ++i) mbar_wait(full(i % kStages), (i / kStages) & 1, status, 125);
+            if (!ok) {                             // copies still under way
+                for (int i = max(0, sent - kVStages); i < sent; ++i) mbar_wait(vfull(i % kVStages), (i / kVStages) & 1, status, 129);
+                for (int i = max(0, sent - 1 - kKStages); i < sent - 1; ++i)
+                    mbar_wait(kfull(i % kKStages), (i / kKStages) & 1, status, 130);
+            }
         }
         __syncwarp();
     } else {
         if (lane == 0) {
-            constexpr uint32_t ID = idesc_bf16(128, 64, true, true);   // K^T (MN-major) x V_w (MN-major)
+            constexpr uint32_t ID = idesc_bf16(128, 192, true, true);   // K^T (MN-major) x the values' parts (MN-major)
             for (int i = 0; i < steps && ok; ++i) {
-                const int s = i % kStages, w2 = i & 1;
-                ok = mbar_wait(wfull(s), (i / kStages) & 1, status, 126);
-                if (ok && i >= 2) ok = mbar_wait(dfree(w2), ((i >> 1) - 1) & 1, status, 127);
+                const int s = i % kVStages, sk = i % kKStages, b = i & 1;
+                ok = mbar_wait(wfull(s), (i / kVStages) & 1, status, 126);
+                if (ok) ok = mbar_wait(kfull(sk), (i / kKStages) & 1, status, 127);
+                if (ok && i >= 2) ok = mbar_wait(dfree(b), ((i >> 1) - 1) & 1, status, 120);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t ka = sb + kStateK + s * kTile;
+                const uint64_t kd = sdesc_sw128(sb + kStateK + sk * kTile, kHalf, 1024),
+                               vd = sdesc_sw128(sb + kStateV + s * 3 * kHalf, kHalf, 1024);
 #pragma unroll
-                for (int part = 0; part < 3; ++part) {
-                    const uint32_t wa = part ? sb + kStateW + w2 * 2 * kHalf + (part - 1) * kHalf : sb + kStateV + s * kHalf;
-#pragma unroll
-                    for (int k = 0; k < kChunk / 16; ++k)
-                        mma_bf16_ss(tmem + w2 * 64, sdesc_sw128(ka + k * 2048, kHalf, 1024),
-                                    sdesc_sw128(wa + k * 2048, kHalf, 1024), ID, part > 0 || k > 0);
-                }
-                mma_commit(dfull(w2));
-                mma_commit(wfree(w2));
-                mma_commit(empty(s));
+                for (int k = 0; k < kChunk / 16; ++k)
+                    mma_bf16_ss(tmem + b * 192, further(kd, k * 2048), further(vd, k * 2048), ID, k > 0);
+                mma_commit(dfull(b));
+                mma_commit(vfree(s));
+                mma_commit(kfree(sk));
             }
             mma_commit(drain);
             mbar_wait(drain, 0, status, 128);
@@ -293,9 +345,9 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 13) {
+    if (warp == 17) {
         tc_fence_after();
-        tmem_dealloc(tmem, 128);
+        tmem_dealloc(tmem, 512);
     }
 }
 
@@ -425,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false);   // Q K^T
             constexpr uint32_t ID_O = idesc_bf16(128, 128, false, true);    // P V, Q S_in
+            const uint64_t kd = sdesc_sw128(ka, 16, 1024), vd = sdesc_sw128(va, kHalf, 1024), sd = sdesc_sw128(sina, kHalf, 1024);
             auto issue_o = [&](int u) {
                 const int b = u & 1, i = u / G, n = u % G;
                 ok = mbar_wait(b_p(b), (u >> 1) & 1, status, 137);
@@ -432,20 +485,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ok && n == 0) ok = mbar_wait(b_v, i & 1, status, 139);                     // this chunk's V and S_in
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t O = tmem + 256 * b + 128, P = tmem + 256 * b, qa = qa0 + u % kQSlots * kTile;
+                const uint32_t O = tmem + 256 * b + 128, P = tmem + 256 * b;
+                const uint64_t qd = sdesc_sw128(qa0 + u % kQSlots * kTile, 16, 1024);
                 const int ksteps = (p.chunks[4 * chunk_of(i) + 1] + 15) / 16;
                 // keys 16k .. 16k + 15 of P packed at 64 (k / 4) + 8 (k % 4); features 16k .. 16k + 15 of f Q (strong
                 // decays) 32 columns further
 #pragma unroll
                 for (int k = 0; k < kChunk / 16; ++k)
-                    if (k < ksteps) mma_bf16_ts(O, P + (k >> 2) * 64 + (k & 3) * 8, sdesc_sw128(va + k * 2048, kHalf, 1024), ID_O, k > 0);
+                    if (k < ksteps) mma_bf16_ts(O, P + (k >> 2) * 64 + (k & 3) * 8, further(vd, k * 2048), ID_O, k > 0);
 #pragma unroll
                 for (int k = 0; k < kD / 16; ++k) {
-                    if (column)
-                        mma_bf16_ss(O, sdesc_sw128(qa + (k >> 2) * kHalf + (k & 3) * 32, 16, 1024),
-                                    sdesc_sw128(sina + k * 2048, kHalf, 1024), ID_O, 1u);
-                    else
-                        mma_bf16_ts(O, P + 32 + (k >> 2) * 64 + (k & 3) * 8, sdesc_sw128(sina + k * 2048, kHalf, 1024), ID_O, 1u);
+                    if (column) mma_bf16_ss(O, further(qd, (k >> 2) * kHalf + (k & 3) * 32), further(sd, k * 2048), ID_O, 1u);
+                    else mma_bf16_ts(O, P + 32 + (k >> 2) * 64 + (k & 3) * 8, further(sd, k * 2048), ID_O, 1u);
                 }
                 mma_commit(b_o(b));
                 mma_commit(b_qe(u % kQSlots));
@@ -457,11 +508,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ok && n == 0) ok = mbar_wait(b_k, i & 1, status, 141);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t qa = qa0 + q * kTile;
+                const uint64_t qd = sdesc_sw128(qa0 + q * kTile, 16, 1024);
 #pragma unroll
                 for (int k = 0; k < kD / 16; ++k) {
                     const uint32_t o = (k >> 2) * kHalf + (k & 3) * 32;
-                    mma_bf16_ss(tmem + 256 * b, sdesc_sw128(qa + o, 16, 1024), sdesc_sw128(ka + o, 16, 1024), ID_S, k > 0);
+                    mma_bf16_ss(tmem + 256 * b, further(qd, o), further(kd, o), ID_S, k > 0);
                 }
                 mma_commit(b_sf(b));
                 if (n == G - 1) mma_commit(b_kfree);
@@ -616,11 +667,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 struct Ws {
-    size_t s_in, s_out, total;
+    size_t s_in, s_out, sums, total;
 };
 Ws layout(const tree_attn_plan_s* P, int32_t hkv) {
     const size_t nc = P->lin.chunks.size() / 4, per = (size_t)hkv * kD * kD;
-    return {0, nc * per * 2, nc * per * 2 + (size_t)P->n_nodes * per * 4};
+    const size_t s_out = nc * per * 2, sums = s_out + (size_t)P->n_nodes * per * 4;
+    return {0, s_out, sums, sums + (size_t)P->lin.n_segments * per * 4};
 }
 
 }  // namespace
@@ -658,7 +710,7 @@ int tree_attn_linear_prefill(tree_attn_plan_t P, const void* q, const void* k, c
     const Ws w = layout(P, hkv);
     if (!workspace || ws_bytes < w.total) return TREE_ATTN_ERR_WORKSPACE;
     const int64_t nc = (int64_t)(P->lin.chunks.size() / 4);
-    if (nc * hq > INT32_MAX || nc * kChunk > INT32_MAX || (int64_t)P->n_nodes * hkv * 2 > INT32_MAX) return TREE_ATTN_ERR_TOO_LARGE;
+    if (nc * hq > INT32_MAX || nc * kChunk > INT32_MAX || nc * hkv * 2 > INT32_MAX) return TREE_ATTN_ERR_TOO_LARGE;
     int dev, *status;
     if ((st = current_device(&dev)) || (st = get_status_ptr(dev, &status))) return st;
     char* ws = static_cast<char*>(workspace);
@@ -666,7 +718,7 @@ int tree_attn_linear_prefill(tree_attn_plan_t P, const void* q, const void* k, c
     CUtensorMap tq, tk, tv, ts, ts32, to32;
     if ((st = make_tensor_map(&tq, q, P->N, hq, d)) || (st = make_tensor_map(&tk, k, P->N, hkv, d)) ||
         (st = make_tensor_map(&tv, v, P->N, hkv, d)) || (st = make_tensor_map(&ts, s_in, nc * kChunk, hkv, d)) ||
-        (st = make_tensor_map_rows(&ts32, s_in, nc * kChunk, hkv, d, 32)) ||
+        (st = make_tensor_map_plain(&ts32, s_in, nc * kChunk, hkv, d, 32, 32)) ||
         (st = make_tensor_map_rows(&to32, o, P->N, hq, d, 32)))
         return st;
     static std::once_flag once[kMaxDevices];
@@ -681,14 +733,18 @@ int tree_attn_linear_prefill(tree_attn_plan_t P, const void* q, const void* k, c
     if (set[dev] != cudaSuccess) return TREE_ATTN_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const LinInfo& X = P->lin;
-    for (size_t l = 0; l + 1 < X.lvl_ptr.size(); ++l) {
-        const StateParams p = {D->lvl_nodes + X.lvl_ptr[l], D->lnodes, D->kids, D->chunks, decay,
-                               reinterpret_cast<float*>(ws + w.s_out), hkv, P->n_nodes, (int32_t)nc, l == 0,
-                               {states, slot_in, slot_out, D->lin_ids, n_slots, status}};
-        const unsigned grid = (unsigned)((int64_t)(X.lvl_ptr[l + 1] - X.lvl_ptr[l]) * hkv * 2);
-        if (launch_pdl(prefill_state_kernel, dim3(grid), dim3(kStateThreads), kStateSmem, s, tk, tv, ts32, p) != cudaSuccess)
-            return TREE_ATTN_ERR_CUDA;
-    }
+    for (size_t l = 0; l + 1 < X.lvl_ptr.size(); ++l)
+        for (int adding = 1; adding >= 0; --adding) {
+            const int32_t *range = &X.job_ptr[2 * l + (adding ? 0 : 1)], jobs = range[1] - range[0];
+            if (!jobs) continue;
+            const StateParams p = {reinterpret_cast<const int4*>(D->lin_jobs) + range[0], D->lnodes, D->kids, D->chunks, decay,
+                                   reinterpret_cast<float*>(ws + w.s_out), reinterpret_cast<float*>(ws + w.sums), hkv,
+                                   P->n_nodes, (int32_t)nc, l == 0, X.segment[l], adding,
+                                   {states, slot_in, slot_out, D->lin_ids, n_slots, status}};
+            if (launch_pdl(prefill_state_kernel, dim3((unsigned)((int64_t)jobs * hkv * 2)), dim3(kStateThreads), kStateSmem, s, tk,
+                           tv, ts32, p) != cudaSuccess)
+                return TREE_ATTN_ERR_CUDA;
+        }
     // about one CTA per SM: lanes of chunks for each kv-head, and where there are fewer chunks than that, the
     // group's q-heads in parts
     const int G = hq / hkv;

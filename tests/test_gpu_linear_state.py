@@ -104,6 +104,35 @@ def test_prefill_deep_tree(cuda_device):
                   slot_out=[-1] * 20 + [2] + [-1] * (n - 22) + [1, 5])
 
 
+@pytest.mark.parametrize("seg,kept", [([12 * 128 + 1], [0]), ([3500], [2]), ([2100, 40, 1540, 1537], [0, -1, 3, 4]), ([1536, 3072], [5, 6])])
+def test_prefill_in_segments(cuda_device, seg, kept):
+    """Nodes long enough to be walked in segments: against the same tokens as a chain of short nodes, whose
+    states are handed on node by node."""
+    if len(seg) == 4:                                       # a long root, a short and two long children
+        parent, chain = [-1, 0, 0, 0], None
+    else:
+        parent = [-1] + list(range(len(seg) - 1))
+    n_slots, hq, hkv, N = 8, 4, 2, sum(seg)
+    q, k, v = draw(51, N, hq, hkv, 128, cuda_device)
+    dec = decays(hkv, cuda_device, (0.999, 1.0))
+    first = torch.randn((n_slots, hkv, 128, 128), device=cuda_device)
+    a, b = first.clone(), first.clone()
+    o = TL.tree_linear_prefill(TreePlan(parent, seg), a, TL.StateSlots([7] + [-1] * (len(seg) - 1), kept, n_slots), q, k, v, dec, 0.1)
+    short, up, out, tip = [], [], [], {}
+    for u, L in enumerate(seg):                             # pieces of at most 5 chunks
+        for x in range(0, L, 640):
+            up.append((tip[parent[u]] if parent[u] >= 0 else -1) if x == 0 else len(short) - 1)
+            short.append(min(640, L - x))
+            out.append(kept[u] if x + 640 >= L else -1)
+        tip[u] = len(short) - 1
+    o2 = TL.tree_linear_prefill(TreePlan(up, short), b, TL.StateSlots([7] + [-1] * (len(short) - 1), out, n_slots), q, k, v, dec, 0.1)
+    # sums of fewer than 64 chunks in another order, 2^-13 of the magnitudes as above: here 2^-18 of the largest
+    # state of N(0, 1) products, and outputs one rounding of the entering state, of P and of o apart
+    assert (a - b).abs().max() <= 2.0 ** -18 * N
+    assert (o.float() - o2.float()).abs().max() <= 2.0 ** -7 * o.float().abs().max()
+    assert torch.linalg.vector_norm(o.float() - o2.float()) <= 2.0 ** -9 * torch.linalg.vector_norm(o.float())
+
+
 def test_prefill_in_two_turns_is_the_whole(cuda_device):
     """A prompt, then its branches from the prompt's state: the outputs of the tree brought in at once, and the
     same states, within the bounds of one more rounding of what enters."""
