@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 8) {
         if (lane == 0) {
-            int qs = 0;                            // Q loads sent; K and V waited for in order of need
+            int qs = 0, q = 0, round = 0;          // Q loads sent, the next one's slot and its turn
             bool k_sent = false, v_sent = false;
             for (int i = 0; i < n_items && ok; ++i) {
                 const int chunk = chunk_of(i), off = p.chunks[4 * chunk];
@@ -444,13 +444,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int blk = 0; blk < 2; ++blk) tma_load_3d(ka + blk * kHalf, &tm_k, blk * 64, g, off, b_k);
                 k_sent = true;
                 for (int n = 0; n < G && ok; ++n) {
-                    const int u = i * G + n, q = u % kQSlots;
-                    if (u >= kQSlots) ok = mbar_wait(b_qe(q), (u / kQSlots - 1) & 1, status, 132);
+                    if (round) ok = mbar_wait(b_qe(q), (round - 1) & 1, status, 132);
                     if (!ok) break;
                     mbar_expect_tx(b_qf(q), kTile);
                     for (int blk = 0; blk < 2; ++blk)
                         tma_load_3d(qa0 + q * kTile + blk * kHalf, &tm_q, blk * 64, h0 + n, off, b_qf(q));
-                    qs = u + 1;
+                    ++qs;
+                    if (++q == kQSlots) {
+                        q = 0;
+                        ++round;
+                    }
                     // V and S_in after the second q-head's Q (the first's with one q-head): the last chunk's
                     // last products, which have read them, are issued before this chunk's second A
                     if (n == (G > 1 ? 1 : 0)) {
@@ -478,16 +481,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false);   // Q K^T
             constexpr uint32_t ID_O = idesc_bf16(128, 128, false, true);    // P V, Q S_in
             const uint64_t kd = sdesc_sw128(ka, 16, 1024), vd = sdesc_sw128(va, kHalf, 1024), sd = sdesc_sw128(sina, kHalf, 1024);
+            // the unit whose O is next: its place in its chunk, its slot
+            int on = 0, oi = 0, oq = 0;
+            int ksteps = (p.chunks[4 * j0 + 1] + 15) / 16;
             auto issue_o = [&](int u) {
-                const int b = u & 1, i = u / G, n = u % G;
+                const int b = u & 1;
                 ok = mbar_wait(b_p(b), (u >> 1) & 1, status, 137);
                 if (ok && u >= 2) ok = mbar_wait(b_oe(b), ((u >> 1) - 1) & 1, status, 138);   // unit u - 2's output read
-                if (ok && n == 0) ok = mbar_wait(b_v, i & 1, status, 139);                     // this chunk's V and S_in
+                if (ok && on == 0) ok = mbar_wait(b_v, oi & 1, status, 139);                   // this chunk's V and S_in
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t O = tmem + 256 * b + 128, P = tmem + 256 * b;
-                const uint64_t qd = sdesc_sw128(qa0 + u % kQSlots * kTile, 16, 1024);
-                const int ksteps = (p.chunks[4 * chunk_of(i) + 1] + 15) / 16;
+                const uint64_t qd = sdesc_sw128(qa0 + oq * kTile, 16, 1024);
                 // keys 16k .. 16k + 15 of P packed at 64 (k / 4) + 8 (k % 4); features 16k .. 16k + 15 of f Q (strong
                 // decays) 32 columns further
 #pragma unroll
@@ -499,12 +504,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     else mma_bf16_ts(O, P + 32 + (k >> 2) * 64 + (k & 3) * 8, further(sd, k * 2048), ID_O, 1u);
                 }
                 mma_commit(b_o(b));
-                mma_commit(b_qe(u % kQSlots));
-                if (n == G - 1) mma_commit(b_vfree);
+                mma_commit(b_qe(oq));
+                oq = oq == kQSlots - 1 ? 0 : oq + 1;
+                if (++on == G) {
+                    mma_commit(b_vfree);
+                    on = 0;
+                    if (++oi < n_items) ksteps = (p.chunks[4 * chunk_of(oi) + 1] + 15) / 16;
+                }
             };
+            int n = 0, i = 0, q = 0, round = 0;
             for (int u = 0; u < U && ok; ++u) {
-                const int b = u & 1, i = u / G, n = u % G, q = u % kQSlots;
-                ok = mbar_wait(b_qf(q), (u / kQSlots) & 1, status, 140);
+                const int b = u & 1;
+                ok = mbar_wait(b_qf(q), round & 1, status, 140);
                 if (ok && n == 0) ok = mbar_wait(b_k, i & 1, status, 141);
                 if (!ok) break;
                 tc_fence_after();
@@ -515,7 +526,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_bf16_ss(tmem + 256 * b, further(qd, o), further(kd, o), ID_S, k > 0);
                 }
                 mma_commit(b_sf(b));
-                if (n == G - 1) mma_commit(b_kfree);
+                if (++n == G) {
+                    mma_commit(b_kfree);
+                    n = 0;
+                    ++i;
+                }
+                if (++q == kQSlots) {
+                    q = 0;
+                    ++round;
+                }
                 if (u > 0) issue_o(u - 1);
             }
             if (ok) issue_o(U - 1);
@@ -529,13 +548,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float fo = p.scale * exp2f((float)(m + 1) * lg);
         const uint32_t stage = sb + kOutStage + warp * 4096;
         // Unit u's output is read after unit u + 1's mask.
-        int prev_off = 0, prev_L = 0, prev_h = 0;
+        int prev_off = 0, prev_L = 0, prev_h = 0, n = 0, i = 0, q = 0;
+        int off = p.chunks[4 * j0], L = p.chunks[4 * j0 + 1];
         for (int u = 0; u <= U; ++u) {
-            int off = 0, L = 0;
             if (u < U) {
-                const int b = u & 1, i = u / G, chunk = chunk_of(i);
-                off = p.chunks[4 * chunk];
-                L = p.chunks[4 * chunk + 1];
+                const int b = u & 1;
                 const uint32_t tS = lane_base + 256 * b;
                 ok = mbar_wait(b_sf(b), (u >> 1) & 1, status, 143);
                 ok = __all_sync(0xffffffffu, ok);
@@ -554,10 +571,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld32(tS + c0, v);
                         tmem_wait_ld();
                         if (column) {
-                            const float4* t = reinterpret_cast<const float4*>(ctab + c0);
+                            const float4* w4 = reinterpret_cast<const float4*>(ctab + c0);
 #pragma unroll
                             for (int x = 0; x < 8; ++x) {
-                                const float4 w = t[x];
+                                const float4 w = w4[x];
                                 v[4 * x] *= w.x;
                                 v[4 * x + 1] *= w.y;
                                 v[4 * x + 2] *= w.z;
@@ -578,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // the rows behind a ragged chunk are another node's: zeros in the last 16 that the product
                 // reads (0 times an infinity there would not be 0)
-                if (u % G == 0 && (L & 15)) {
+                if (n == 0 && (L & 15)) {
                     ok = mbar_wait(b_v, i & 1, status, 144);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
@@ -591,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!column) {
                     // f(m) q_m over features [col0, col0 + 64) out of the swizzled slot
-                    const uint8_t* qrow = smem + kOutQ + u % kQSlots * kTile + grp * kHalf + m * 128;
+                    const uint8_t* qrow = smem + kOutQ + q * kTile + grp * kHalf + m * 128;
 #pragma unroll
                     for (int h2 = 0; h2 < 2; ++h2) {
                         uint32_t qw[16];
@@ -651,7 +668,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             prev_off = off;
             prev_L = L;
-            prev_h = h0 + u % G;
+            prev_h = h0 + n;
+            q = q == kQSlots - 1 ? 0 : q + 1;
+            if (++n == G) {
+                n = 0;
+                if (++i < n_items) {
+                    off = p.chunks[4 * chunk_of(i)];
+                    L = p.chunks[4 * chunk_of(i) + 1];
+                }
+            }
         }
         if (lane == 0) bulk_wait_all();
         __syncwarp();

@@ -132,6 +132,7 @@ class TreeCache:
                 raise ValueError(f"{name}: on {x.device}, k on {k.device}")
         self._tensors = (k, v, k_scale, v_scale)
         self.n_pages, self.hkv, self.d, self.device = P, hkv, d, k.device
+        self._shape = (P, hkv, d, k.device.index)
 
     # Read-only: a cache is checked once, other tensors are another TreeCache.
     k, v, k_scale, v_scale = (property(lambda self, i=i: self._tensors[i]) for i in range(4))
@@ -289,17 +290,20 @@ def tree_cache_copy(caches, src, dst, stream=None) -> None:
         raise ValueError("caches: none given")
     dev, c0 = _current_device(), caches[0]
     for c in caches:
-        if (c.n_pages, c.hkv, c.d) != (c0.n_pages, c0.hkv, c0.d):
-            raise ValueError(f"caches: [{c.n_pages}, {c.hkv}, {PAGE}, {c.d}] beside [{c0.n_pages}, {c0.hkv}, {PAGE}, {c0.d}]")
-        if c.device.index != dev:
-            raise ValueError(f"cache: on {c.device}, the current device is cuda:{dev}")
+        if c._shape != c0._shape:
+            raise ValueError(f"caches: [{c.n_pages}, {c.hkv}, {PAGE}, {c.d}] on {c.device} beside [{c0.n_pages}, {c0.hkv}, "
+                             f"{PAGE}, {c0.d}] on {c0.device}")
+    if c0.device.index != dev:
+        raise ValueError(f"cache: on {c0.device}, the current device is cuda:{dev}")
     a, b = _i32(src), _i32(dst)
     if a.ndim != 1 or a.shape != b.shape:
         raise ValueError("src and dst must be 1-D arrays of equal length")
-    n = len(caches)
-    arrays = [(C.c_void_p * n)(*col) for col in zip(*(c._ptrs for c in caches))]
-    st = B.load().tree_attn_cache_copy(n, *arrays, c0.n_pages, c0.hkv, c0.d, _ptr_i32(a), _ptr_i32(b), len(a),
-                                       _stream_of(_side(stream), dev, *(t for c in caches for t in c._tensors)))
+    n, side = len(caches), _side(stream)
+    ptrs = (C.c_void_p * (4 * n))(*[c._tensors[i].data_ptr() for i in range(4) for c in caches])
+    at = C.addressof(ptrs)
+    st = B.load().tree_attn_cache_copy(n, at, at + 8 * n, at + 16 * n, at + 24 * n, c0.n_pages, c0.hkv, c0.d, _ptr_i32(a),
+                                       _ptr_i32(b), len(a),
+                                       _stream_of(side, dev, *(() if side is None else (t for c in caches for t in c._tensors))))
     if st:
         B.check(st, "tree_attn_cache_copy")
 

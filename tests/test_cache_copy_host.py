@@ -80,11 +80,14 @@ def test_binding(lib, monkeypatch):
     class Fake(TD.TreeCache):
         def __init__(self, P, hkv=1, d=64, index=0):
             self.n_pages, self.hkv, self.d, self.device, self._tensors = P, hkv, d, torch.device("cuda", index), ()
+            self._shape = (P, hkv, d, index)
 
     with pytest.raises(ValueError, match="beside"):
         TD.tree_cache_copy([Fake(4), Fake(5)], [0], [1])
-    with pytest.raises(ValueError, match="current device"):
+    with pytest.raises(ValueError, match="beside"):
         TD.tree_cache_copy([Fake(4), Fake(4, index=1)], [0], [1])
+    with pytest.raises(ValueError, match="current device"):
+        TD.tree_cache_copy([Fake(4, index=1), Fake(4, index=1)], [0], [1])
     for src, dst in (([0], [1, 2]), ([[0]], [[1]]), ([0.5], [1]), ([2 ** 31], [1])):
         with pytest.raises(ValueError):
             TD.tree_cache_copy(Fake(4), src, dst)
