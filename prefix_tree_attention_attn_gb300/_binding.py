@@ -126,9 +126,9 @@ SIGNATURES = {
     "tree_attn_decode": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
                                    C.c_void_p, C.c_void_p, C.c_void_p, C.c_float, C.c_void_p, C.c_size_t,
                                    C.c_void_p]),
-    # (the four tables of device pointers by address)
+    # (host arrays by address)
     "tree_attn_cache_copy": (C.c_int, [C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32,
-                                       C.c_int32, c_int32_p, c_int32_p, C.c_int64, C.c_void_p]),
+                                       C.c_int32, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p]),
     # include/tree_sample.h
     "tree_attn_sample": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.POINTER(Sampling),
                                    C.c_void_p, C.c_void_p, C.c_void_p]),

@@ -281,6 +281,10 @@ def tree_decode(plan: DecodePlan, cache: TreeCache, lens, q, softmax_scale: floa
     return o, lse
 
 
+def _address(a: np.ndarray) -> int:
+    return a.__array_interface__["data"][0]
+
+
 def tree_cache_copy(caches, src, dst, stream=None) -> None:
     """Copy pages ``src[i]`` to ``dst[i]`` (codes and scales) in one cache, or in each of several
     of the same shape, e.g. one per layer (``tree_attn_cache_copy``): what a branch inside a page,
@@ -299,10 +303,10 @@ def tree_cache_copy(caches, src, dst, stream=None) -> None:
     if a.ndim != 1 or a.shape != b.shape:
         raise ValueError("src and dst must be 1-D arrays of equal length")
     n, side = len(caches), _side(stream)
-    ptrs = (C.c_void_p * (4 * n))(*[c._tensors[i].data_ptr() for i in range(4) for c in caches])
-    at = C.addressof(ptrs)
-    st = B.load().tree_attn_cache_copy(n, at, at + 8 * n, at + 16 * n, at + 24 * n, c0.n_pages, c0.hkv, c0.d, _ptr_i32(a),
-                                       _ptr_i32(b), len(a),
+    ptrs = np.array([c._tensors[i].data_ptr() for i in range(4) for c in caches], dtype=np.uint64)
+    at = _address(ptrs)
+    st = B.load().tree_attn_cache_copy(n, at, at + 8 * n, at + 16 * n, at + 24 * n, c0.n_pages, c0.hkv, c0.d, _address(a),
+                                       _address(b), len(a),
                                        _stream_of(side, dev, *(() if side is None else (t for c in caches for t in c._tensors))))
     if st:
         B.check(st, "tree_attn_cache_copy")

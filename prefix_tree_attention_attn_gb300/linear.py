@@ -146,9 +146,10 @@ class StateSlots:
 
 
 def _check_states(states, slots: StateSlots, hkv: int, d: int, dev: int) -> None:
-    if states.dim() != 4 or states.shape[0] < slots.n_slots:
-        raise ValueError(f"states: at least {slots.n_slots} slots [{hkv}, {d}, {d}] expected, got {tuple(states.shape)}")
-    _check_dense(states, "states", (states.shape[0], hkv, d, d), torch.float32, dev)
+    shape = states.shape
+    if len(shape) != 4 or shape[0] < slots.n_slots:
+        raise ValueError(f"states: at least {slots.n_slots} slots [{hkv}, {d}, {d}] expected, got {tuple(shape)}")
+    _check_dense(states, "states", (shape[0], hkv, d, d), torch.float32, dev)
 
 
 def prefill_workspace(plan: TreePlan, hkv: int, d: int) -> int:
@@ -199,7 +200,7 @@ def tree_linear_step(states, slots: StateSlots, q, k, v, decay, scale: float, o=
     dev = _current_device()
     R, hq, d = q.shape
     hkv = k.shape[1]
-    if R != len(slots):
+    if R != len(slots.slot_in):
         raise ValueError(f"q: {len(slots)} rows expected, got {R}")
     if not slots._rows_apart:
         raise ValueError("slots: a row starts from a slot that another row writes")

@@ -5,7 +5,6 @@ import numpy as np
 import pytest
 import torch
 
-from prefix_tree_attention_attn_gb300 import _binding as B
 from prefix_tree_attention_attn_gb300 import decode as TD
 
 
@@ -54,9 +53,8 @@ def test_bad_arguments(lib):
 
     def status(n=2, k=fake, v=fake, ks=fake, vs=fake, pages=10, hkv=2, d=64, src=(0, 1), dst=(2, 3), m=None):
         arr = lambda x: None if x is None else (C.c_void_p * len(x))(*x)  # noqa: E731
-        i32 = lambda x: None if x is None else np.asarray(x, np.int32).ctypes.data_as(B.c_int32_p)  # noqa: E731
         keep = [np.asarray(x, np.int32) if x is not None else None for x in (src, dst)]
-        ptr = [None if x is None else x.ctypes.data_as(B.c_int32_p) for x in keep]
+        ptr = [None if x is None else x.ctypes.data for x in keep]
         return lib.tree_attn_cache_copy(n, arr(k), arr(v), arr(ks), arr(vs), pages, hkv, d, *ptr, len(src or ()) if m is None else m, None)
 
     for name in ("k", "v", "ks", "vs"):
