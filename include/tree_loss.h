@@ -132,7 +132,8 @@ int tree_attn_policy_loss_workspace(tree_attn_plan_t plan, size_t* ws_bytes);
  * loss alone, or the logits themselves with the same stride (each row is read before it is
  * written).  The struct is read during the call.  Log-probs, ratios and sums are fp32 or wider
  * (whether a ratio lies beyond the clip is decided in pairs of floats); dlogits is
- * rounded once.  Bitwise reproducible.  workspace: 256-byte aligned, contents ignored; calls that may
+ * rounded once.  Bitwise reproducible, and loss, log-probs and entropies are the same bits with and
+ * without dlogits.  workspace: 256-byte aligned, contents ignored; calls that may
  * overlap need one each.  Asynchronous on `stream`; the plan's first call on a device uploads
  * its tables (allocates and synchronises once: make it outside stream capture). */
 int tree_attn_policy_loss(tree_attn_plan_t plan, const void* logits, int64_t row_stride, int64_t vocab,

@@ -1,24 +1,25 @@
 // Clipped policy loss of the trajectories and its gradient for the compact logits
 // (include/tree_loss.h).
 //
-// One pass over the logits.  A cluster of C CTAs takes a row, a slice each in shared memory, and goes
-// from row to row; each logit is read once (2 bytes) and its gradient written once (2 bytes).
+// One pass over the logits.  A cluster of C CTAs takes a row, a slice each, and goes from row to row;
+// each logit is read once (2 bytes) and its gradient written once (2 bytes).  The rows go through a
+// CTA as through a pipe, a few slices in a ring of shared memory at a time, with warps for each part:
 //
-//   producer     a warp of its own: the predictions of the rows to come (their tables, weights,
-//                old log-probs ... are loaded up to three rows ahead, one dependent load a row),
-//                whether a row has any weight, and the bulk copies of the slices.
-//   statistics   m = max x, S = sum 2^a, T = sum 2^a a with a = (x - m) log2 e, by thread and warp; a
-//                warp's three numbers go to every CTA of the cluster by asynchronous stores that
-//                count on its barrier, and each warp joins what comes: LSE = m + ln S,
-//                H = ln S - ln 2 T / S.  With room for two rows or more the next row's statistics are
-//                taken first, so that the exchange is not waited for.
-//   predictions  every warp works out the row's g_k for itself where the row has at most 32 predictions
-//                of one target (inside a segment: one for each trajectory through it), so
-//                nothing is waited for; other rows all warps of the CTA.
+//   producer     whether the next row has any weight, and the bulk copy of its slice.
+//   statistics   S = sum 2^a, T = sum 2^a a with a = (x - m) log2 e, m near the maximum, by thread, warp and CTA;
+//                a CTA's three numbers go to every CTA of the cluster by asynchronous stores that
+//                count on a barrier there.
+//   finishers    two warps, a row each in turn: join them, LSE = m + ln S, H = ln S - ln 2 T / S; the row's g_k, a lane
+//                for each prediction where there are at most 32 of one target (inside a segment: one
+//                for each trajectory through it), whose inputs it has loaded rows ahead; their sums.
 //   gradient     2^a (cG + cE (a - T / S)), cG = -sum g / S, cE = entropy_coef ln 2 sum w / S,
 //                rounded once; the target's g_k are added before that.  A row of several
 //                targets gets those elements afterwards (children with the same token id summed in
 //                their order).
+//
+// (With the same warps doing all parts of a row in turn, and five such CTAs on an SM, the chain from
+// a row's load to its gradient set the pace: 1,022 us for 8,836 rows of 152,064 logits, 7,797 of them with
+// weight, where this takes 810, 6.3 TB/s of reads and writes.)
 //
 // Whether a ratio lies beyond the clip decides a whole gradient, so lp - old is a pair of floats:
 // ln S = k ln 2 + ln f, f near 1, adds no error beyond 3e-8.
@@ -44,9 +45,10 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMaxWarps = 8;                   // that compute
-constexpr int kMaxSlots = 3;
-constexpr int kMaxSlice = 66 * 1024;           // bytes of a CTA's slice
+constexpr int kMaxSlots = 6;
+constexpr int kFinishers = 2;
+constexpr int kMaxStat = 8;                    // statistics warps
+constexpr int kShared = 227 * 1024;            // of an SM, and of a CTA at most
 constexpr int64_t kMaxVocab = 262144;
 constexpr float kFar = -1e30f;                 // in place of -inf where it meets a factor 0
 constexpr float kHuge = 0x1p100f;              // beyond this a multiple of a logit may overflow
@@ -98,6 +100,13 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
     return r;
 }
 
+// Whether either number of a lies above b's.
+__device__ __forceinline__ bool above2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("{\n\t.reg .pred p, q;\n\tsetp.gt.bf16x2 p|q, %1, %2;\n\tor.pred p, p, q;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r) : "r"(a), "r"(b));
+    return r != 0;
+}
+
 // a + b = s + e exactly
 __device__ __forceinline__ float two_sum(float a, float b, float& e) {
     const float s = a + b, bb = s - a;
@@ -105,18 +114,19 @@ __device__ __forceinline__ float two_sum(float a, float b, float& e) {
     return s;
 }
 
-// The exponent of x against the maximum m; far below it counts as 1e30 below, so that 0 meets no infinity
+// The exponent of x against the reference m; far below it counts as 1e30 below, so that 0 meets no infinity
 // (+inf and NaN are told by m alone).
 __device__ __forceinline__ float exponent(float x, float m) { return fmaxf(x - m, kFar) * kLog2e; }
 
-// A maximum m, and the sums of e = 2^exponent and e * exponent over some logits.
+// A reference m, one of the logits and at most 16 below the largest, and the sums of e = 2^exponent and
+// e * exponent over some logits.
 struct Stat {
     float m, s, t;
 };
 
 // What the predictions of a row need of it.
 struct Row {
-    float m;                                   // NaN where the row has no distribution
+    float m;                                   // the reference; NaN where the row has no distribution
     float lk, ll;                              // ln S = lk + ll, lk a multiple of 2^-16
     float h;                                   // entropy
 };
@@ -170,25 +180,28 @@ __device__ __forceinline__ float predict(const Params& p, const Row& row, float 
     return h2 + lo;
 }
 
-// What the producer knows of a row.
-struct Meta {
-    int active, narrow;                        // some weight; at most 32 predictions of one target
-    int first, n, t0, nt;                      // predictions, targets
-    int y;                                     // the one target's token
-    int k[32];                                 // narrow: each lane's prediction
-    float w[32], old[32], a[32], ref[32];
+// What the finisher tells the gradient's warps of a row.
+struct Result {
+    float m, ts, cg, ce;                       // maximum, T / S and the two factors
+    float own;                                 // the one target's element
+    int active, y, t0, nt;                     // some weight; the one target's token; targets
 };
 
+// The ring follows.
 struct Shared {
-    uint64_t full[kMaxSlots], empty[kMaxSlots];
-    uint64_t stat[2];                          // the cluster's warps have sent their sums, rows in turn
-    uint64_t read;                             // the cluster's warps have read a row's targets
-    uint64_t cta;                              // the CTA's warps have come this far
-    float4 stats[2][8 * kMaxWarps];            // {m, S, T, target's logit or 0} by CTA of the cluster and warp
-    Sums sums[kMaxWarps];
-    Meta meta[kMaxSlots];
+    uint64_t full[kMaxSlots], empty[kMaxSlots], done[kMaxSlots];
+    uint64_t stat[2 * kMaxSlots];              // the cluster's CTAs have sent their sums
+    float4 stats[2 * kMaxSlots][8];            // {m, S, T, target's logit or 0} by CTA
+    Stat parts[kMaxSlots][kMaxStat];           // by statistics warp
+    int parts_in[kMaxSlots];
+    uint64_t read[kFinishers];                 // the cluster's finishers have read a row's targets
+    uint64_t cta;                              // the gradient's warps have come this far
+    struct {
+        int active, y;
+    } meta[kMaxSlots];
+    Result result[kMaxSlots];
 };
-constexpr int kSlots0 = (sizeof(Shared) + 127) / 128 * 128;   // where the ring begins
+constexpr int kRing0 = (sizeof(Shared) + 127) / 128 * 128;
 
 __device__ __forceinline__ float advantage(const Params& p, int4 e) { return p.adv[p.per_token ? e.x : e.z]; }
 
@@ -320,7 +333,7 @@ struct Slice {
     }
 };
 
-// The producer's loads of one row, in three steps that depend on one another.
+// The loads of one row's predictions, in three steps that depend on one another.
 struct Ahead {
     int4 info, mine;
     float w, old, a, ref;
@@ -339,251 +352,219 @@ __device__ __forceinline__ void load_pred(const Params& p, int lane, Ahead& x) {
         if (!ta_ok(p.status, 602, x.mine.x, 0, p.n_pred)) x.mine.x = -1;
     }
 }
-__device__ __forceinline__ void load_values(const Params& p, int64_t r, Ahead& x) {
+// `all`: what the predictions need, not the weights alone
+__device__ __forceinline__ void load_values(const Params& p, int64_t r, bool all, Ahead& x) {
     x.w = x.old = x.a = x.ref = 0.f;
     x.y = -1;
     if (x.mine.x >= 0) {
         x.w = p.weights ? p.weights[x.mine.x] : p.each;
-        if (p.old) x.old = p.old[x.mine.x];
-        x.a = p.adv[p.per_token ? x.mine.x : x.mine.z];
-        if (p.kl != 0.f) x.ref = p.ref[x.mine.x];
+        if (all) {
+            if (p.old) x.old = p.old[x.mine.x];
+            x.a = p.adv[p.per_token ? x.mine.x : x.mine.z];
+            if (p.kl != 0.f) x.ref = p.ref[x.mine.x];
+        }
     }
     // one target: it is the next packed row (a node's tokens and its only child follow each other)
     if (x.info.w == 1 && ta_ok(p.status, 603, r + 1, 0, p.N)) x.y = p.tokens[r + 1];
 }
+// Whether the row has any weight (the same in every warp that asks).
+__device__ __forceinline__ bool has_weight(const Params& p, int lane, const Ahead& x) {
+    if (is_narrow(x.info)) return __any_sync(0xffffffffu, x.w != 0.f);
+    if (x.info.y == 0 || !p.weights) return x.info.y > 0;
+    bool any = false;
+    for (int i = lane; i < x.info.y && !any; i += 32) {
+        const int k = p.pred[x.info.x + i].x;
+        any = ta_ok(p.status, 602, k, 0, p.n_pred) && p.weights[k] != 0.f;
+    }
+    return __any_sync(0xffffffffu, any);
+}
 
-__global__ void __maxnreg__(96) policy_kernel(const Params p, int n_slots, int slot_bytes) {
+// How the warps of a CTA are shared out: [0, stat) statistics, [stat, stat + grad) the gradient, then
+// the finishers and the producer.
+struct Split {
+    int stat, grad, slots, slot_bytes;
+};
+
+// (80 registers: 23 warps on an SM)
+__global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
     extern __shared__ __align__(128) uint8_t smem[];
     Shared& S = *reinterpret_cast<Shared*>(smem);
     cg::cluster_group cluster = cg::this_cluster();
-    const int C = (int)cluster.num_blocks(), me = (int)cluster.block_rank();
-    const int log_c = __ffs(C) - 1;
-    const int nw = (int)blockDim.x / 32 - 1, T = 32 * nw, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int C = (int)cluster.num_blocks(), me = (int)cluster.block_rank(), log_c = __ffs(C) - 1;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n_slots = f.slots, n_places = 2 * f.slots;
     const int64_t cluster0 = blockIdx.x / C, clusters = gridDim.x / C;
+    uint8_t* ring = smem + kRing0;
     if (tid == 0) {
         for (int i = 0; i < n_slots; ++i) {
             mbar_init(smem_u32(&S.full[i]), 1);
-            mbar_init(smem_u32(&S.empty[i]), nw);
+            mbar_init(smem_u32(&S.empty[i]), f.stat + f.grad + 1);
+            mbar_init(smem_u32(&S.done[i]), 1);
+            S.parts_in[i] = 0;
         }
-        mbar_init(smem_u32(&S.stat[0]), 1);
-        mbar_init(smem_u32(&S.stat[1]), 1);
-        mbar_init(smem_u32(&S.read), C * nw);
-        mbar_init(smem_u32(&S.cta), nw);
+        for (int i = 0; i < n_places; ++i) mbar_init(smem_u32(&S.stat[i]), 1);
+        for (int i = 0; i < kFinishers; ++i) mbar_init(smem_u32(&S.read[i]), C);
+        mbar_init(smem_u32(&S.cta), max(f.grad, 1));
         fence_mbar_init();
-        for (int i = 0; i < 2; ++i) mbar_expect_tx(smem_u32(&S.stat[i]), 16 * C * nw);   // of the next row on this barrier
+        for (int i = 0; i < n_places; ++i) mbar_expect_tx(smem_u32(&S.stat[i]), 16 * C);   // of the first rows
     }
     cluster.sync();                            // every CTA of the cluster runs, its barriers are set up
     grid_dep_wait();
     grid_dep_launch();
+    bool ok = true;
 
-    if (warp == nw) {
-        // ---- the producer -------------------------------------------------------------------
-        Ahead one, two, three;                 // this row and the next two
-        load_info(p, cluster0, one);
-        load_info(p, cluster0 + clusters, two);
-        load_info(p, cluster0 + 2 * clusters, three);
-        load_pred(p, lane, one);
-        load_pred(p, lane, two);
-        load_values(p, cluster0, one);
-        int it = 0, used = 0;
-        bool ok = true;
-        for (int64_t r = cluster0; r < p.N && ok; r += clusters, ++it) {
-            const int slot = it % n_slots, turn = it / n_slots;
-            Ahead four;
-            load_info(p, r + 3 * clusters, four);
-            load_pred(p, lane, three);
-            load_values(p, r + clusters, two);
-            const bool narrow = is_narrow(one.info);
-            const int n = one.info.y;
-            bool active = n > 0;
-            if (narrow) {
-                active = __any_sync(0xffffffffu, one.w != 0.f);
-            } else if (active && p.weights) {
-                bool any = false;
-                for (int i = lane; i < n && !any; i += 32) {
-                    const int k = p.pred[one.info.x + i].x;
-                    any = ta_ok(p.status, 602, k, 0, p.n_pred) && p.weights[k] != 0.f;
-                }
-                active = __any_sync(0xffffffffu, any);
-            }
-            if (turn > 0) ok = mbar_wait(smem_u32(&S.empty[slot]), (turn - 1) & 1, p.status, 601);
+    // Sums wait in 2 * slots places.  A CTA sends those of a row when its slot is free, so it is done with the row `slots`
+    // before; for that one every CTA had sent its sums, each when it was done with the row `slots` before that: the
+    // row whose place is taken has been joined everywhere.
+    if (warp < f.stat) {
+        // ---- statistics --------------------------------------------------------------------
+        const int T = 32 * f.stat;
+        const uint64_t c2 = f32x2(kLog2e, kLog2e);
+        int slot = 0, turn = 0, place = 0;
+        for (int64_t r = cluster0; r < p.N; r += clusters) {
+            ok = mbar_wait(smem_u32(&S.full[slot]), turn & 1, p.status, 604);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            Meta& m = S.meta[slot];
-            m.k[lane] = one.mine.x;
-            m.w[lane] = one.w;
-            m.old[lane] = one.old;
-            m.a[lane] = one.a;
-            m.ref[lane] = one.ref;
-            if (lane == 0) {
-                m.active = active;
-                m.narrow = narrow;
-                m.first = one.info.x;
-                m.n = n;
-                m.t0 = one.info.z;
-                m.nt = one.info.w;
-                m.y = one.y;
-            }
-            __syncwarp();
-            if (lane == 0) {
-                const uint32_t bar = smem_u32(&S.full[slot]);
+            Stat st = {0.f, 0.f, 0.f};
+            if (S.meta[slot].active) {         // (the same in every CTA of the cluster)
                 const Slice s(p, r, me, log_c);
-                const uint32_t bytes = (uint32_t)(s.last - s.first) * 16;
-                if (active && bytes) {
-                    mbar_expect_tx(bar, bytes);
-                    bulk_load(smem_u32(smem + kSlots0 + (size_t)slot * slot_bytes + (size_t)(s.first - s.lo) * 16),
-                              s.x + s.start(s.first), bytes, bar);
-                } else {
-                    mbar_arrive(bar);
-                }
-            }
-            one = two;
-            two = three;
-            three = four;
-            used = it + 1;
-        }
-        // copies still under way where a wait gave up
-        if (!ok)
-            for (int i = max(0, used - n_slots); i < used; ++i)
-                mbar_wait(smem_u32(&S.full[i % n_slots]), (i / n_slots) & 1, p.status, 602);
-    } else {
-        // ---- the rows ----------------------------------------------------------------------
-        const uint64_t c2 = f32x2(kLog2e, kLog2e);
-        const bool ahead = n_slots > 1;        // the next row's statistics before this row is finished
-        int reads = 0, meets = 0;
-        bool ok = true;
-        // all warps of the CTA have come this far, and see each other's writes
-        auto meet = [&] {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&S.cta));
-            ok = mbar_wait(smem_u32(&S.cta), meets++ & 1, p.status, 603) && ok;
-            ok = __all_sync(0xffffffffu, ok);
-        };
-        struct Begun {
-            int64_t r;
-            int slot, k;                       // its place in the ring, among the rows of some weight (-1: none)
-            Stat st;                           // of this warp, then of the row
-            float xy;
-        };
-
-        auto begin = [&](int64_t r, int it, int actives) {
-            Begun b;
-            b.r = r;
-            b.slot = it % n_slots;
-            b.k = -1;
-            ok = mbar_wait(smem_u32(&S.full[b.slot]), (it / n_slots) & 1, p.status, 604);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok || !S.meta[b.slot].active) return b;   // (the same in every CTA of the cluster)
-            b.k = actives;
-            const Slice s(p, r, me, log_c);
-            const int odd = s.odd(tid, T);
-            const uint4* here = reinterpret_cast<const uint4*>(smem + kSlots0 + (size_t)b.slot * slot_bytes) - s.lo;
-            Stat st;
-            uint32_t m2 = 0xff80ff80u, n2 = 0xff80ff80u;
-#pragma unroll 4
-            for (int v = s.first + tid; v < s.last; v += T) {
-                const uint4 x = here[v];
-                m2 = max2_nan(m2, max2_nan(x.x, x.y));
-                n2 = max2_nan(n2, max2_nan(x.z, x.w));
-            }
-            uint4 rest = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-            if (odd >= 0) {
-                rest = s.part(odd);
-                m2 = max2_nan(m2, max2_nan(rest.x, rest.y));
-                n2 = max2_nan(n2, max2_nan(rest.z, rest.w));
-            }
-            m2 = max2_nan(m2, n2);
-            st.m = max_nan(lo16(m2), hi16(m2));
-            if (fabsf(st.m) < kHuge) {
-                const uint64_t minus = f32x2(-st.m, -st.m);
-                // what lies far enough below is 0 all the same, and then finite
-                const float far = st.m - fmaxf(256.f, fabsf(st.m) * 0x1p-6f);
-                const uint32_t far2 = pack_bf16x2(far, far);
-                uint64_t sum_s = 0, sum_t = 0, more_s = 0, more_t = 0;
-                auto add = [&](uint32_t u, uint64_t& ss, uint64_t& tt) {
-                    u = max2(u, far2);
-                    const uint64_t a = mul_f32x2(add_f32x2(f32x2(lo16(u), hi16(u)), minus), c2);
-                    float a0, a1;
-                    f32x2_split(a, a0, a1);
-                    const uint64_t e = f32x2(fast_exp2(a0), fast_exp2(a1));
-                    ss = add_f32x2(ss, e);
-                    tt = fma_f32x2(e, a, tt);
-                };
-                auto add4 = [&](uint4 x) {
-                    add(x.x, sum_s, sum_t);
-                    add(x.y, more_s, more_t);
-                    add(x.z, sum_s, sum_t);
-                    add(x.w, more_s, more_t);
-                };
-#pragma unroll 2
-                for (int v = s.first + tid; v < s.last; v += T) add4(here[v]);
-                if (odd >= 0) add4(rest);
-                float a0, a1;
-                f32x2_split(add_f32x2(sum_s, more_s), a0, a1);
-                st.s = a0 + a1;
-                f32x2_split(add_f32x2(sum_t, more_t), a0, a1);
-                st.t = a0 + a1;
-            } else {
-                // masks of the lowest value alone, or huge logits (an infinity and NaN: told by m alone)
-                st.s = st.t = 0.f;
-                if (fabsf(st.m) < INFINITY)
-                    for (int v = s.first + tid; v < s.last + T; v += T) {
-                        const uint4 x = v < s.last ? here[v] : rest;
-                        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll 1
-                        for (int i = 0; i < 8; ++i) {
-                            const float a = exponent(__uint_as_float((u[i / 2] >> (16 * (i & 1))) << 16), st.m), e = fast_exp2(a);
-                            st.s += e;
-                            st.t = fmaf(e, a, st.t);
+                const int odd = s.odd(tid, T);
+                const uint8_t* here8 = ring + (size_t)slot * f.slot_bytes;
+                const uint4* here = reinterpret_cast<const uint4*>(here8) - s.lo;
+                const uint4 none = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);   // -inf
+                const uint4 rest = odd >= 0 ? s.part(odd) : none;
+                const bool odds = __any_sync(0xffffffffu, odd >= 0);
+                auto get = [&](int v) { return v < s.last ? here[v] : none; };
+                auto top2 = [&](uint4 x) { return max2_nan(max2_nan(x.x, x.y), max2_nan(x.z, x.w)); };
+                const int v0 = s.first + tid;
+                // One pass: the reference is the maximum of the warp's first vectors, and is raised when a logit lies 16
+                // above it (e^16 is far from overflow), which after the first few vectors it hardly ever does.
+                uint4 x = get(v0), y = get(v0 + T);
+                uint32_t seen = max2_nan(top2(x), top2(y));   // the lane's maximum: an infinity or NaN shows in the end
+                float ref;
+                asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(ref) : "f"(fmaxf(lo16(seen), hi16(seen))));
+                if (fabsf(ref) < kHuge) {
+                    uint64_t minus = f32x2(-ref, -ref), sum_s = 0, sum_t = 0, more_s = 0, more_t = 0;
+                    uint32_t far2, limit2;
+                    auto set = [&] {
+                        minus = f32x2(-ref, -ref);
+                        // what lies far enough below is 0 all the same, and then finite
+                        const float far = ref - fmaxf(256.f, fabsf(ref) * 0x1p-6f), limit = ref + 16.f;
+                        far2 = pack_bf16x2(far, far);
+                        limit2 = pack_bf16x2(limit, limit);
+                    };
+                    set();
+                    auto add = [&](uint32_t u, uint64_t& ss, uint64_t& tt) {
+                        u = max2(u, far2);
+                        const uint64_t a = mul_f32x2(add_f32x2(f32x2(lo16(u), hi16(u)), minus), c2);
+                        float a0, a1;
+                        f32x2_split(a, a0, a1);
+                        const uint64_t e = f32x2(fast_exp2(a0), fast_exp2(a1));
+                        ss = add_f32x2(ss, e);
+                        tt = fma_f32x2(e, a, tt);
+                    };
+                    auto add4 = [&](uint4 z) {
+                        add(z.x, sum_s, sum_t);
+                        add(z.y, more_s, more_t);
+                        add(z.z, sum_s, sum_t);
+                        add(z.w, more_s, more_t);
+                    };
+                    auto look = [&](uint32_t top) {
+                        seen = max2_nan(seen, top);
+                        if (__any_sync(0xffffffffu, above2(top, limit2))) {
+                            const float was = ref;
+                            asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(ref) : "f"(fmaxf(lo16(top), hi16(top))));
+                            set();
+                            const float d = exponent(was, ref), e = fast_exp2(d);
+                            const uint64_t d2 = f32x2(d, d), e2 = f32x2(e, e);
+                            sum_t = mul_f32x2(fma_f32x2(sum_s, d2, sum_t), e2);
+                            more_t = mul_f32x2(fma_f32x2(more_s, d2, more_t), e2);
+                            sum_s = mul_f32x2(sum_s, e2);
+                            more_s = mul_f32x2(more_s, e2);
                         }
+                    };
+                    for (int v = v0, w = s.first + 32 * warp;;) {   // w: the warp's first, for all its lanes alike
+                        add4(x);
+                        add4(y);
+                        v += 2 * T;
+                        w += 2 * T;
+                        if (w >= s.last) break;
+                        x = get(v);
+                        y = get(v + T);
+                        look(max2_nan(top2(x), top2(y)));
                     }
-            }
-            b.st = warp_join(st);
-            return b;
-        };
-
-        // The row's sums out of every warp's of the cluster.
-        auto collect = [&](Begun& b) {
-            ok = wait_cluster(smem_u32(&S.stat[b.k & 1]), (b.k >> 1) & 1, p.status, 605);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) return;
-            if (tid == 0) mbar_expect_tx(smem_u32(&S.stat[b.k & 1]), 16 * C * nw);   // of the row after the next
-            b.st = {-INFINITY, 0.f, 0.f};
-            b.xy = 0.f;
-            for (int i = lane; i < C * nw; i += 32) {
-                const float4 q = S.stats[b.k & 1][i];
-                if (i == lane) {
-                    b.st = {q.x, q.y, q.z};
-                } else {                       // (more than 32 warps: two a lane)
-                    const float m = max_nan(b.st.m, q.x);
-                    const float da = exponent(b.st.m, m), db = exponent(q.x, m), ea = fast_exp2(da), eb = fast_exp2(db);
-                    b.st = {m, b.st.s * ea + q.y * eb, fmaf(b.st.s, da, b.st.t) * ea + fmaf(q.y, db, q.z) * eb};
+                    if (odds) {
+                        look(top2(rest));
+                        add4(rest);
+                    }
+                    float a0, a1;
+                    f32x2_split(add_f32x2(sum_s, more_s), a0, a1);
+                    st.s = a0 + a1;
+                    f32x2_split(add_f32x2(sum_t, more_t), a0, a1);
+                    st.t = a0 + a1;
+                    const float top = max_nan(lo16(seen), hi16(seen));
+                    st.m = top < INFINITY ? ref : top;
+                } else {
+                    // masks to begin with, or huge logits: the maximum first (an infinity and NaN: told by it alone)
+                    for (int v = v0; v < s.last; v += T) seen = max2_nan(seen, top2(here[v]));
+                    seen = max2_nan(seen, top2(rest));
+                    st.m = max_nan(lo16(seen), hi16(seen));
+                    if (fabsf(st.m) < INFINITY)
+                        for (int v = v0; v < s.last + T; v += T) {
+                            const uint4 z = v < s.last ? here[v] : rest;
+                            const uint32_t u[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll 1
+                            for (int i = 0; i < 8; ++i) {
+                                const float a = exponent(__uint_as_float((u[i / 2] >> (16 * (i & 1))) << 16), st.m), e = fast_exp2(a);
+                                st.s += e;
+                                st.t = fmaf(e, a, st.t);
+                            }
+                        }
                 }
-                b.xy += q.w;
+                st = warp_join(st);
             }
-            b.st = warp_join(b.st);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) b.xy += __shfl_xor_sync(0xffffffffu, b.xy, o);
-        };
-        // Only after this warp has collected the row before: when every warp's sums of this row have come, those
-        // of the row before have been read everywhere, and the next row's may take their place.
-        auto send = [&](const Begun& b) {
-            const Slice s(p, b.r, me, log_c);
-            const Meta& M = S.meta[b.slot];
-            float xy = 0.f;
-            if (warp == 0 && M.nt == 1 && s.owns(M.y) >= 0) xy = s.logit(smem + kSlots0 + (size_t)b.slot * slot_bytes, M.y);
-            if (lane < C)
-                remote_store(at_rank(smem_u32(&S.stats[b.k & 1][me * nw + warp]), lane), make_float4(b.st.m, b.st.s, b.st.t, xy),
-                             at_rank(smem_u32(&S.stat[b.k & 1]), lane));
-        };
-
-        auto finish = [&](const Begun& b) {
-            const int64_t r = b.r;
-            const uint8_t* slot = smem + kSlots0 + (size_t)b.slot * slot_bytes;
-            const uint32_t empty = smem_u32(&S.empty[b.slot]);
-            const Meta& M = S.meta[b.slot];
+            // the last of the CTA's warps joins them and sends
+            int last = 0;
+            if (lane == 0) {
+                S.parts[slot][warp] = st;
+                __threadfence_block();
+                last = atomicAdd(&S.parts_in[slot], 1) == f.stat - 1;
+            }
+            if (__shfl_sync(0xffffffffu, last, 0)) {
+                __threadfence_block();
+                const Stat none = {-INFINITY, 0.f, 0.f};
+                st = warp_join(lane < f.stat ? S.parts[slot][lane] : none);
+                float xy = 0.f;
+                if (S.meta[slot].active) {
+                    const Slice s(p, r, me, log_c);
+                    const int y = S.meta[slot].y;
+                    if (s.owns(y) >= 0) xy = s.logit(ring + (size_t)slot * f.slot_bytes, y);
+                }
+                if (lane < C)
+                    remote_store(at_rank(smem_u32(&S.stats[place][me]), lane), make_float4(st.m, st.s, st.t, xy),
+                                 at_rank(smem_u32(&S.stat[place]), lane));
+                if (lane == 0) S.parts_in[slot] = 0;
+            }
+            place = place + 1 == n_places ? 0 : place + 1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&S.empty[slot]));
+            if (++slot == n_slots) {
+                slot = 0;
+                ++turn;
+            }
+        }
+    } else if (warp < f.stat + f.grad) {
+        // ---- the gradient --------------------------------------------------------------------
+        const int at = tid - 32 * f.stat, T = 32 * f.grad;
+        const uint64_t c2 = f32x2(kLog2e, kLog2e);
+        int slot = 0, turn = 0, meets = 0;
+        for (int64_t r = cluster0; r < p.N; r += clusters) {
+            ok = mbar_wait(smem_u32(&S.done[slot]), turn & 1, p.status, 608);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const Result R = S.result[slot];
             const Slice s(p, r, me, log_c);
-            uint16_t* row_d = p.dlogits ? p.dlogits + r * p.d_stride : nullptr;
+            uint16_t* row_d = p.dlogits + r * p.d_stride;
             const bool together = ((reinterpret_cast<uintptr_t>(s.x) ^ reinterpret_cast<uintptr_t>(row_d)) & 15u) == 0;
             auto store = [&](int v, uint4 o) {
                 if (together && v >= s.first && v < s.last) {
@@ -595,212 +576,287 @@ __global__ void __maxnreg__(96) policy_kernel(const Params p, int n_slots, int s
                         if (s.start(v) + i >= 0 && s.start(v) + i < s.V) row_d[s.start(v) + i] = (uint16_t)(u[i / 2] >> (16 * (i & 1)));
                 }
             };
-            auto give_back = [&] {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(empty);
-            };
-            if (b.k < 0) {
-                if (row_d)
-                    for (int v = s.lo + tid; v < s.hi; v += T) store(v, make_uint4(0, 0, 0, 0));
+            if (!R.active) {
+                for (int v = s.lo + at; v < s.hi; v += T) store(v, make_uint4(0, 0, 0, 0));
+            } else {
+                const int odd = s.odd(at, T), yv = R.nt == 1 ? s.owns(R.y) : -1;
+                const uint4* here = reinterpret_cast<const uint4*>(ring + (size_t)slot * f.slot_bytes) - s.lo;
+                auto value = [&](float xv) {
+                    const float a = exponent(xv, R.m);
+                    return fast_exp2(a) * fmaf(R.ce, a - R.ts, R.cg);
+                };
+                auto write = [&](int v, uint32_t (&o)[4]) {
+                    if (v == yv) {
+                        const uint32_t own = pack_bf16x2(R.own, 0.f) & 0xffffu;
+                        const int e = R.y - s.start(v);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (e / 2 == i) o[i] = e & 1 ? (o[i] & 0xffffu) | (own << 16) : (o[i] & 0xffff0000u) | own;
+                    }
+                    store(v, make_uint4(o[0], o[1], o[2], o[3]));
+                };
+                int v = s.first + at;
+                if (fabsf(R.m) < kHuge) {
+                    // (one multiply-add for the exponent: off by 2^-24 of m log2 e, far below the rounding to bf16)
+                    const uint64_t minus = f32x2(-R.m * kLog2e, -R.m * kLog2e), cg2 = f32x2(R.cg, R.cg);
+                    if (R.ce == 0.f) {
+#pragma unroll 2
+                        for (; v < s.last; v += T) {
+                            const uint4 x = here[v];
+                            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+                            uint32_t o[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                float a0, a1;
+                                f32x2_split(fma_f32x2(f32x2(lo16(u[i]), hi16(u[i])), c2, minus), a0, a1);
+                                f32x2_split(mul_f32x2(f32x2(fast_exp2(a0), fast_exp2(a1)), cg2), a0, a1);
+                                o[i] = pack_bf16x2(a0, a1);
+                            }
+                            write(v, o);
+                        }
+                    } else {
+                        // the entropy's term; -inf, where 0 would meet an infinity, as what is 0 all the same
+                        const float far = R.m - fmaxf(256.f, fabsf(R.m) * 0x1p-6f);
+                        const uint32_t far2 = pack_bf16x2(far, far);
+                        const uint64_t ce2 = f32x2(R.ce, R.ce), rest2 = f32x2(fmaf(-R.ce, R.ts, R.cg), fmaf(-R.ce, R.ts, R.cg));
+#pragma unroll 2
+                        for (; v < s.last; v += T) {
+                            const uint4 x = here[v];
+                            const uint32_t u[4] = {max2(x.x, far2), max2(x.y, far2), max2(x.z, far2), max2(x.w, far2)};
+                            uint32_t o[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                float a0, a1;
+                                const uint64_t a = fma_f32x2(f32x2(lo16(u[i]), hi16(u[i])), c2, minus);
+                                f32x2_split(a, a0, a1);
+                                f32x2_split(mul_f32x2(f32x2(fast_exp2(a0), fast_exp2(a1)), fma_f32x2(ce2, a, rest2)), a0, a1);
+                                o[i] = pack_bf16x2(a0, a1);
+                            }
+                            write(v, o);
+                        }
+                    }
+                }
+                // the general form, and the vectors in part
+#pragma unroll 1
+                for (; v < s.last || (odd >= 0 && v < s.last + T); v += T) {
+                    const uint4 x = v < s.last ? here[v] : s.part(odd);
+                    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(value(lo16(u[i])), value(hi16(u[i])));
+                    write(v < s.last ? v : odd, o);
+                }
+                if (R.nt != 1) {
+                    // every warp has written: the targets' elements again
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&S.cta));
+                    ok = mbar_wait(smem_u32(&S.cta), meets++ & 1, p.status, 603);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    for (int j = at; j < R.nt; j += T) {
+                        const int q = p.targets[R.t0 + j].x;
+                        if (!ta_ok(p.status, 604, q, 0, p.N)) continue;
+                        const int yj = p.tokens[q];
+                        if (s.owns(yj) < 0) continue;
+                        bool earlier = false;      // another child has the same token: the first one adds them up
+                        for (int i = 0; i < j && !earlier; ++i) earlier = p.tokens[p.targets[R.t0 + i].x] == yj;
+                        if (earlier) continue;
+                        float g = p.tg[q];
+                        for (int i = j + 1; i < R.nt; ++i) {
+                            const int qi = p.targets[R.t0 + i].x;
+                            if (p.tokens[qi] == yj) g += p.tg[qi];
+                        }
+                        row_d[yj] = (uint16_t)pack_bf16x2(value(p.tx[q]) + p.grad_scale * g, 0.f);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&S.empty[slot]));
+            if (++slot == n_slots) {
+                slot = 0;
+                ++turn;
+            }
+        }
+    } else if (warp < f.stat + f.grad + kFinishers) {
+        // ---- the finishers ------------------------------------------------------------------
+        const int mine = warp - f.stat - f.grad;
+        const int64_t step = kFinishers * clusters, r0 = cluster0 + mine * clusters;
+        Ahead one, two, three;                 // this row and its next two
+        load_info(p, r0, one);
+        load_info(p, r0 + step, two);
+        load_info(p, r0 + 2 * step, three);
+        load_pred(p, lane, one);
+        load_pred(p, lane, two);
+        load_values(p, r0, true, one);
+        int reads = 0;
+        int64_t it = mine;
+        for (int64_t r = r0; r < p.N; r += step, it += kFinishers) {
+            const int slot = (int)(it % n_slots), place = (int)(it % n_places);
+            const int64_t turn = it / n_slots;
+            Ahead four;
+            load_info(p, r + 3 * step, four);
+            load_pred(p, lane, three);
+            load_values(p, r + step, true, two);
+            const int4 info = one.info;
+            const bool active = has_weight(p, lane, one), narrow = is_narrow(info), single = info.w == 1;
+            if (turn > 0) ok = mbar_wait(smem_u32(&S.empty[slot]), (turn - 1) & 1, p.status, 609);
+            if (ok) ok = wait_cluster(smem_u32(&S.stat[place]), (it / n_places) & 1, p.status, 605);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            Stat st = {-INFINITY, 0.f, 0.f};
+            float xy = 0.f;
+            if (lane < C) {
+                const float4 q = S.stats[place][lane];
+                st = {q.x, q.y, q.z};
+                xy = q.w;
+            }
+            st = warp_join(st);
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) xy += __shfl_xor_sync(0xffffffffu, xy, o);   // (lanes 0 to 7)
+            xy = __shfl_sync(0xffffffffu, xy, 0);
+            if (lane == 0) mbar_expect_tx(smem_u32(&S.stat[place]), 16 * C);   // of the place's next row
+            Result R = {0.f, 0.f, 0.f, 0.f, 0.f, active, one.y, info.z, info.w};
+            if (!active) {
                 if (me == 0) {
                     if (p.logprobs)
-                        for (int i = tid; i < M.n; i += T) {
-                            const int k = p.pred[M.first + i].x;
-                            if (ta_ok(p.status, 602, k, 0, p.n_pred)) p.logprobs[k] = 0.f;
+                        for (int i = lane; i < info.y; i += 32) {
+                            const int j = p.pred[info.x + i].x;
+                            if (ta_ok(p.status, 602, j, 0, p.n_pred)) p.logprobs[j] = 0.f;
                         }
-                    if (tid == 0) {
+                    if (lane == 0) {
                         p.row_loss[r] = 0.f;
                         if (p.entropy) p.entropy[r] = 0.f;
                     }
                 }
-                give_back();
-                return;
-            }
-            const bool narrow = M.narrow, single = M.nt == 1;
-            if (!row_d && narrow && (me != 0 || warp != 0)) {   // one warp tells the row's loss
-                give_back();
-                return;
-            }
-
-            // ---- the row ------------------------------------------------------------------------
-            const Stat st = b.st;
-            float xy = b.xy;
-            const int y = M.y, yv = single ? s.owns(y) : -1;
-            if (y < 0 || y >= s.V) xy = __int_as_float(0x7fc00000);
-            const float ts = st.t / st.s;
-            Row row;
-            row.m = fabsf(st.m) < INFINITY ? st.m : __int_as_float(0x7fc00000);
-            {
-                // S = 2^k f, 0.7 <= f < 1.4 (S >= 1);  ln 2 = 45426 / 2^16 + 1.42860682e-6;
-                // ln f = 2 (z + z^3 / 3 + ...), z = (f - 1) / (f + 1), |z| < 0.18: the next term is below 2^-30 z
-                const uint32_t bits = __float_as_uint(st.s);
-                int k = (int)(bits >> 23) - 127;
-                float f = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
-                if (f >= 1.4f) {
-                    f *= 0.5f;
-                    ++k;
-                }
-                const float z = (f - 1.f) / (f + 1.f), z2 = z * z;
-                const float poly = z2 * (1.f / 3 + z2 * (1.f / 5 + z2 * (1.f / 7 + z2 * (1.f / 9 + z2 * (1.f / 11)))));
-                row.lk = (float)k * (45426.f / 65536.f);
-                row.ll = fmaf((float)k, 1.42860682e-6f, 2.f * fmaf(z, poly, z));
-            }
-            row.h = row.m == row.m ? fmaf(-kLn2, ts, row.lk + row.ll) : row.m;
-
-            // ---- the predictions -----------------------------------------------------------------
-            Sums sum = {0.f, 0.f, 0.f};
-            if (narrow) {
-                float lp = 0.f;
-                const float w = M.w[lane];
-                if (w != 0.f) lp = predict(p, row, w, xy, M.old[lane], p.old != nullptr, M.a[lane], M.ref[lane], sum);
-                if (me == 0 && warp == 0 && M.k[lane] >= 0 && p.logprobs) p.logprobs[M.k[lane]] = lp;
-                sum = warp_sum(sum);
             } else {
-                // one target, or a warp for each of several
-                for (int j = single ? 0 : warp; j < M.nt; j += nw) {
-                    const int4 t = single ? make_int4(0, M.first, M.n, 0) : p.targets[M.t0 + j];
-                    if (!ta_ok(p.status, 604, t.x, 0, p.N)) continue;
-                    const int yj = single ? y : p.tokens[t.x];
-                    const float xj = single ? xy : yj >= 0 && yj < s.V ? lo16(s.x[yj]) : __int_as_float(0x7fc00000);
-                    Sums part = {0.f, 0.f, 0.f};
-                    predict_all(p, row, t.y, t.z, xj, single ? tid : lane, single ? T : 32, me == 0, part);
-                    part = warp_sum(part);
-                    if (lane == 0) {
-                        sum.g += part.g;
-                        sum.w += part.w;
-                        sum.loss += part.loss;
-                        if (!single && s.owns(yj) >= 0) {
+                const int V = (int)p.vocab;
+                if (one.y < 0 || one.y >= V) xy = __int_as_float(0x7fc00000);
+                const float ts = st.t / st.s;
+                Row row;
+                row.m = fabsf(st.m) < INFINITY ? st.m : __int_as_float(0x7fc00000);
+                {
+                    // S = 2^k f, 0.7 <= f < 1.4 (S >= 1);  ln 2 = 45426 / 2^16 + 1.42860682e-6;
+                    // ln f = 2 (z + z^3 / 3 + ...), z = (f - 1) / (f + 1), |z| < 0.18: the next term is below 2^-30 z
+                    const uint32_t bits = __float_as_uint(st.s);
+                    int e = (int)(bits >> 23) - 127;
+                    float x = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+                    if (x >= 1.4f) {
+                        x *= 0.5f;
+                        ++e;
+                    }
+                    const float z = (x - 1.f) / (x + 1.f), z2 = z * z;
+                    const float poly = z2 * (1.f / 3 + z2 * (1.f / 5 + z2 * (1.f / 7 + z2 * (1.f / 9 + z2 * (1.f / 11)))));
+                    row.lk = (float)e * (45426.f / 65536.f);
+                    row.ll = fmaf((float)e, 1.42860682e-6f, 2.f * fmaf(z, poly, z));
+                }
+                row.h = row.m == row.m ? fmaf(-kLn2, ts, row.lk + row.ll) : row.m;
+                Sums sum = {0.f, 0.f, 0.f};
+                if (narrow) {
+                    float lp = 0.f;
+                    if (one.w != 0.f) lp = predict(p, row, one.w, xy, one.old, p.old != nullptr, one.a, one.ref, sum);
+                    if (me == 0 && one.mine.x >= 0 && p.logprobs) p.logprobs[one.mine.x] = lp;
+                } else if (single) {
+                    predict_all(p, row, info.x, info.y, xy, lane, 32, me == 0, sum);
+                } else {
+                    // several targets: a lane for each where there are many, the whole warp one after another else
+                    const Slice s(p, r, me, log_c);
+                    const bool lanes = info.w >= 8;
+                    for (int j = lanes ? lane : 0; j < info.w; j += lanes ? 32 : 1) {
+                        const int4 t = p.targets[info.z + j];
+                        if (!ta_ok(p.status, 604, t.x, 0, p.N)) continue;
+                        const int yj = p.tokens[t.x];
+                        const float xj = yj >= 0 && yj < V ? lo16(s.x[yj]) : __int_as_float(0x7fc00000);
+                        Sums part = {0.f, 0.f, 0.f};
+                        predict_all(p, row, t.y, t.z, xj, lanes ? 0 : lane, lanes ? 1 : 32, me == 0, part);
+                        if (!lanes) part = warp_sum(part);
+                        if (lanes || lane == 0) {
+                            sum.g += part.g;
+                            sum.w += part.w;
+                            sum.loss += part.loss;
+                        }
+                        if (p.dlogits && (lanes || lane == 0) && s.owns(yj) >= 0) {
                             p.tx[t.x] = xj;
                             p.tg[t.x] = part.g;
                         }
                     }
-                    if (single) break;
-                }
-                if (!single) {
-                    // the gradient may lie over the logits: the whole cluster has read the targets' logits
                     __syncwarp();
-                    if (lane < C) remote_arrive(at_rank(smem_u32(&S.read), lane));
-                    ok = wait_cluster(smem_u32(&S.read), reads++ & 1, p.status, 606);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) return;
-                }
-                if (lane == 0) S.sums[warp] = sum;
-                meet();
-                if (!ok) return;
-                sum = {0.f, 0.f, 0.f};
-                for (int i = 0; i < nw; ++i) {
-                    sum.g += S.sums[i].g;
-                    sum.w += S.sums[i].w;
-                    sum.loss += S.sums[i].loss;
-                }
-                meet();                        // S.sums has been read
-                if (!ok) return;
-            }
-            if (me == 0 && tid == 0) {
-                p.row_loss[r] = sum.loss;
-                if (p.entropy) p.entropy[r] = row.h;
-            }
-            if (!row_d) {
-                give_back();
-                return;
-            }
-
-            // ---- the gradient ----------------------------------------------------------------
-            const int odd = s.odd(tid, T);
-            const uint4* here = reinterpret_cast<const uint4*>(slot) - s.lo;
-            const float cg_ = row.m == row.m ? -p.grad_scale * sum.g / st.s : row.m;
-            const float ce = p.ent != 0.f ? kLn2 * p.grad_scale * p.ent * sum.w / st.s : 0.f;
-            auto value = [&](float xv) {
-                const float a = exponent(xv, row.m);
-                return fast_exp2(a) * fmaf(ce, a - ts, cg_);
-            };
-            auto write = [&](int v, uint32_t (&o)[4]) {
-                if (v == yv) {
-                    const uint32_t own = pack_bf16x2(value(xy) + p.grad_scale * sum.g, 0.f) & 0xffffu;
-                    const int e = y - s.start(v);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (e / 2 == i) o[i] = e & 1 ? (o[i] & 0xffffu) | (own << 16) : (o[i] & 0xffff0000u) | own;
-                }
-                store(v, make_uint4(o[0], o[1], o[2], o[3]));
-            };
-            int v = s.first + tid;
-            if (ce == 0.f && fabsf(row.m) < kHuge) {
-                // (one multiply-add for the exponent: off by 2^-24 of m log2 e, far below the rounding to bf16)
-                const uint64_t minus = f32x2(-row.m * kLog2e, -row.m * kLog2e), cg2 = f32x2(cg_, cg_);
-#pragma unroll 2
-                for (; v < s.last; v += T) {
-                    const uint4 x = here[v];
-                    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t o[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float a0, a1;
-                        f32x2_split(fma_f32x2(f32x2(lo16(u[i]), hi16(u[i])), c2, minus), a0, a1);
-                        f32x2_split(mul_f32x2(f32x2(fast_exp2(a0), fast_exp2(a1)), cg2), a0, a1);
-                        o[i] = pack_bf16x2(a0, a1);
+                    if (p.dlogits) {
+                        // the gradient may lie over the logits: the whole cluster has read the targets' logits
+                        if (lane < C) remote_arrive(at_rank(smem_u32(&S.read[mine]), lane));
+                        ok = wait_cluster(smem_u32(&S.read[mine]), reads++ & 1, p.status, 606);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
                     }
-                    write(v, o);
                 }
-            }
-            // the general form, and the vectors in part
-#pragma unroll 1
-            for (; v < s.last || (odd >= 0 && v < s.last + T); v += T) {
-                const uint4 x = v < s.last ? here[v] : s.part(odd);
-                const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-                uint32_t o[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(value(lo16(u[i])), value(hi16(u[i])));
-                write(v < s.last ? v : odd, o);
-            }
-            if (!single) {
-                const int t0 = M.t0, nt = M.nt;
-                meet();
-                if (!ok) return;
-                for (int j = tid; j < nt; j += T) {
-                    const int q = p.targets[t0 + j].x;
-                    if (!ta_ok(p.status, 604, q, 0, p.N)) continue;
-                    const int yj = p.tokens[q];
-                    if (s.owns(yj) < 0) continue;
-                    bool earlier = false;          // another child has the same token: the first one adds them up
-                    for (int i = 0; i < j && !earlier; ++i) earlier = p.tokens[p.targets[t0 + i].x] == yj;
-                    if (earlier) continue;
-                    float g = p.tg[q];
-                    for (int i = j + 1; i < nt; ++i) {
-                        const int qi = p.targets[t0 + i].x;
-                        if (p.tokens[qi] == yj) g += p.tg[qi];
-                    }
-                    row_d[yj] = (uint16_t)pack_bf16x2(value(p.tx[q]) + p.grad_scale * g, 0.f);
+                sum = warp_sum(sum);
+                if (me == 0 && lane == 0) {
+                    p.row_loss[r] = sum.loss;
+                    if (p.entropy) p.entropy[r] = row.h;
                 }
+                R.m = row.m;
+                R.ts = ts;
+                R.cg = row.m == row.m ? -p.grad_scale * sum.g / st.s : row.m;
+                R.ce = p.ent != 0.f ? kLn2 * p.grad_scale * p.ent * sum.w / st.s : 0.f;
+                const float a = exponent(xy, row.m);
+                R.own = fast_exp2(a) * fmaf(R.ce, a - ts, R.cg) + p.grad_scale * sum.g;
             }
-            give_back();
-        };
-
-        Begun next, todo;
-        todo.r = -1;
-        int it = 0, actives = 0;
-        for (int64_t r = cluster0; ok; r += clusters, ++it) {
-            const bool more = r < p.N;
-            next.r = -1;
-            next.k = -1;
-            if (more) {
-                next = begin(r, it, actives);
-                if (!ok) break;
-                actives += next.k >= 0;
+            if (lane == 0) {
+                if (f.grad) {
+                    S.result[slot] = R;
+                    mbar_arrive(smem_u32(&S.done[slot]));
+                }
+                mbar_arrive(smem_u32(&S.empty[slot]));
             }
-            if (!ahead) {
-                todo = next;
-                if (todo.k >= 0) send(todo);
-            }
-            if (todo.r >= 0 && todo.k >= 0) {
-                collect(todo);
-                if (!ok) break;
-            }
-            if (ahead && next.k >= 0) send(next);
-            if (todo.r >= 0) finish(todo);
-            if (!more) break;
-            if (ahead) todo = next;
+            one = two;
+            two = three;
+            three = four;
         }
+    } else {
+        // ---- the producer -------------------------------------------------------------------
+        Ahead one, two, three;
+        load_info(p, cluster0, one);
+        load_info(p, cluster0 + clusters, two);
+        load_info(p, cluster0 + 2 * clusters, three);
+        load_pred(p, lane, one);
+        load_pred(p, lane, two);
+        load_values(p, cluster0, false, one);
+        int slot = 0, turn = 0, sent = 0;
+        for (int64_t r = cluster0; r < p.N; r += clusters) {
+            Ahead four;
+            load_info(p, r + 3 * clusters, four);
+            load_pred(p, lane, three);
+            load_values(p, r + clusters, false, two);
+            const bool active = has_weight(p, lane, one);
+            if (turn > 0) ok = mbar_wait(smem_u32(&S.empty[slot]), (turn - 1) & 1, p.status, 601);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) {
+                S.meta[slot].active = active;
+                S.meta[slot].y = one.y;
+                const uint32_t bar = smem_u32(&S.full[slot]);
+                const Slice s(p, r, me, log_c);
+                const uint32_t bytes = (uint32_t)(s.last - s.first) * 16;
+                if (active && bytes) {
+                    mbar_expect_tx(bar, bytes);
+                    bulk_load(smem_u32(ring + (size_t)slot * f.slot_bytes + (size_t)(s.first - s.lo) * 16), s.x + s.start(s.first),
+                              bytes, bar);
+                } else {
+                    mbar_arrive(bar);
+                }
+            }
+            ++sent;
+            if (++slot == n_slots) {
+                slot = 0;
+                ++turn;
+            }
+            one = two;
+            two = three;
+            three = four;
+        }
+        // copies still under way where a wait gave up
+        if (!ok)
+            for (int i = max(0, sent - n_slots); i < sent; ++i)
+                mbar_wait(smem_u32(&S.full[i % n_slots]), (i / n_slots) & 1, p.status, 602);
     }
     cluster.sync();                            // nothing is sent to a CTA that has ended
 }
@@ -924,28 +980,44 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 size_t column(const tree_attn_plan_s* P) { return ((size_t)P->N * 4 + 255) / 256 * 256; }
 
-// How a row is cut up: CTAs, warps that compute, slots of the ring.
+// How a row is cut up: CTAs, and their warps and slots.
 struct Shape {
-    int C, warps, slots, slot_bytes, smem;
+    int C, smem;
+    Split split;
 };
-// What is waited for is the chain from a row's load over its statistics and the exchange to its
-// gradient, so many small CTAs of few warps run side by side and a CTA has the row that it works on
-// alone; only slices of up to 8 KB are small enough for two rows more.  Measured with the gradient, 9 vocabularies x
-// CTAs per row x warps x slots, best first (us, CTAs a row / warps / slots): 152,064 x 4,000 rows
-// 523 (8/3/1) 539 (8/4/1) 546 (4/8/1); 100,000 x 4,000 316 (2/8/1) 316 (4/4/1) 340 (4/3/1); 64,000 x 5,000 271 (2/4/1)
-// 288 (4/3/1); 32,000 x 10,000 272 (1/4/1) 279 (2/3/1); 16,000 x 20,000 283 (1/3/1) 295 (1/4/1); 4,000 x 20,000
-// 143 (1/2/3) 154 (1/2/1).  Few rows are done sooner by more warps: 152,064 x 64 21 (4/8/1) 23 (8/8/1) 25 (8/3/1).
-Shape shape_of(int64_t vocab, int64_t rows) {
+// A slice is at most a third of what an SM has, so that one can be loaded, one be summed and one get its gradient at
+// a time; large slices have an SM to themselves, smaller ones share it, with fewer warps each.  The sums run over the same
+// threads with and without the gradient, so a policy's log-probs of an evaluation are those of its update to the bit.
+// Measured (us; CTAs a row / statistics warps / gradient warps / CTAs an SM): with the gradient 152,064 x 4,000 rows
+// 407 (4/8/12/1) 422 (4/12/12/1) 441 (4/12/8/1) 533 (8/4/4/2); 64,000 x 5,000 223 (2/8/12/1) 253 (4/4/4/2); 32,000 x 10,000
+// 225 (1/8/12/1) 245 (2/4/4/2); 16,000 x 20,000 259 (1/4/4/2) 275 (1/2/3/3); 8,000 x 20,000 160 (1/2/3/3) 170 (1/2/2/3);
+// 4,000 x 20,000 113 (1/1/1/3) 118 (1/2/2/2); 1,000 x 20,000 84 (1/1/1/3) 95 (1/2/2/3); 152,064 x 64 18.5 (8/4/4/2)
+// 18.8 (4/8/12/1).  Without it 152,064 x 4,000 286 (4/8/1) 266 (4/16/1); 32,000 x 10,000 155 (1/8/1) 141 (1/16/1);
+// 16,000 x 20,000 141 (1/4/3) 163 (1/4/2); 8,000 x 20,000 92 (1/2/4) 112 (1/2/3); 4,000 x 20,000 77 (1/1/3) 68 (1/2/4).
+Shape shape_of(int64_t vocab, bool grad) {
     const int64_t vectors = (vocab + 7) / 8 + 1;    // (a row may start inside a vector)
-    Shape f = {1, 0, 0, 0, 0};
-    while (f.C < 8 && (vectors + f.C - 1) / f.C * 16 > kMaxSlice) f.C *= 2;
-    const int64_t per = (vectors + f.C - 1) / f.C;
-    const int64_t bytes = (per * 16 + 127) / 128 * 128;
-    f.warps = rows * f.C <= 304 ? 8 : bytes > 40 * 1024 ? 4 : bytes > 8 * 1024 ? 3 : 2;
-    while (f.warps > 1 && per < 32 * f.warps) --f.warps;
-    f.slots = bytes > 8 * 1024 ? 1 : kMaxSlots;
-    f.slot_bytes = (int)bytes;
-    f.smem = kSlots0 + f.slots * f.slot_bytes;
+    Shape f = {1, 0, {0, 0, 1, 0}};
+    while (f.C < 8 && (vectors + f.C - 1) / f.C * 16 > 76 * 1024) f.C *= 2;
+    Split& s = f.split;
+    s.slot_bytes = (int)((vectors + f.C - 1) / f.C * 16);
+    int per_sm = 3;
+    if (s.slot_bytes > 40 * 1024) {
+        s.stat = kMaxStat;
+        s.grad = 12;
+        per_sm = 1;
+    } else if (s.slot_bytes > 20 * 1024) {
+        s.stat = s.grad = 4;
+        per_sm = grad ? 2 : 3;
+    } else if (s.slot_bytes > 10 * 1024) {
+        s.stat = 2;
+        s.grad = 3;
+        per_sm = grad ? 3 : 4;
+    } else {
+        s.stat = s.grad = 1;
+    }
+    if (!grad) s.grad = 0;
+    while (s.slots < kMaxSlots && kRing0 + (s.slots + 1) * s.slot_bytes <= (kShared + 1024) / per_sm - 1024) ++s.slots;
+    f.smem = kRing0 + s.slots * s.slot_bytes;
     return f;
 }
 
@@ -956,11 +1028,11 @@ int clusters_at_a_time(int dev, const Shape& f, const cudaLaunchConfig_t& cfg) {
     static std::vector<std::array<int, 5>> known;
     std::lock_guard<std::mutex> lk(mu);
     for (const auto& k : known)
-        if (k[0] == dev && k[1] == f.C && k[2] == f.warps && k[3] == f.smem) return k[4];
+        if (k[0] == dev && k[1] == f.C && k[2] == (int)cfg.blockDim.x && k[3] == f.smem) return k[4];
     int n = 0;
     if (launched(cudaOccupancyMaxActiveClusters(&n, policy_kernel, &cfg)) != cudaSuccess) return 0;
     try {
-        known.push_back({dev, f.C, f.warps, f.smem, n});
+        known.push_back({dev, f.C, (int)cfg.blockDim.x, f.smem, n});
     } catch (const std::bad_alloc&) {
     }
     return n;
@@ -1041,15 +1113,15 @@ int tree_attn_policy_loss(tree_attn_plan_t P, const void* logits, int64_t row_st
     p.n_pred = n_pred;
     p.status = status;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const Shape f = shape_of(vocab, P->N);
+    const Shape f = shape_of(vocab, dlogits != nullptr);
     static std::once_flag once[kMaxDevices];
     static cudaError_t set[kMaxDevices];
     std::call_once(once[dev], [&] {
-        set[dev] = launched(cudaFuncSetAttribute(policy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSlots0 + kMaxSlice));
+        set[dev] = launched(cudaFuncSetAttribute(policy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared));
     });
     if (set[dev] != cudaSuccess) return TREE_ATTN_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(32 * (f.warps + 1));
+    cfg.blockDim = dim3(32 * (f.split.stat + f.split.grad + kFinishers + 1));
     cfg.dynamicSmemBytes = f.smem;
     cfg.stream = s;
     cudaLaunchAttribute at[2];
@@ -1063,7 +1135,7 @@ int tree_attn_policy_loss(tree_attn_plan_t P, const void* logits, int64_t row_st
     const int at_a_time = clusters_at_a_time(dev, f, cfg);
     if (at_a_time < 1) return TREE_ATTN_ERR_CUDA;
     cfg.gridDim = dim3((unsigned)(std::min<int64_t>(P->N, at_a_time) * f.C));
-    cudaError_t e = launched(cudaLaunchKernelEx(&cfg, policy_kernel, p, f.slots, f.slot_bytes));
+    cudaError_t e = launched(cudaLaunchKernelEx(&cfg, policy_kernel, p, f.split));
     if (e != cudaSuccess) return TREE_ATTN_ERR_CUDA;
     e = launch_pdl(policy_sum_kernel, dim3(1), dim3(1024), 0, s, (const float*)p.row_loss, (int)P->N, loss);
     return e == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA;

@@ -314,3 +314,64 @@ def test_rows_behind_32_bit_offsets(cuda_device):
         p[int(tok[r + 1])] -= 1
         e = (d[r].double() - 2 * p).abs()
         assert (e <= 2.0 ** -8 * 2 * p.abs() + 2.0 ** -14 * p.abs()).all()
+
+
+@pytest.mark.parametrize("V,N", [(1000, 20000), (6001, 9000), (9000, 6000), (33000, 4000), (100000, 1500), (152064, 2500)])
+@pytest.mark.parametrize("branches", [False, True])
+def test_many_rows(cuda_device, V, N, branches):
+    """More rows than are under way at a time, by far; and the loss alone, its log-probs and its entropies are the
+    same bits as with the gradient.  With a leaf at every third row: rows of two targets, most of them with more than 32
+    predictions.  The same tolerances (ratios of 1: g is the advantage)."""
+    if branches:
+        N = min(N, 1500)
+        parent = [-1] + [2 * (i // 2) for i in range(N // 3 * 2)]      # node 2 i has the children 2 i + 1, a leaf, and 2 i + 2
+        tree = (parent, [2 - (i % 2) for i in range(len(parent))])
+    else:
+        tree = ([-1], [N])
+    plan = TreePlan(*tree)
+    N = plan.n_tokens
+    g = torch.Generator(cuda_device).manual_seed(V + branches)
+    x = torch.empty((N, V), dtype=torch.bfloat16, device=cuda_device)
+    for i in range(0, N, 500):
+        x[i:i + 500] = 2 * torch.randn((min(500, N - i), V), device=cuda_device, generator=g)
+    tok = torch.randint(0, V, (N,), device=cuda_device, generator=g, dtype=torch.int32)
+    _, ptr, at = TL.trajectories(plan)
+    rows = torch.from_numpy(np.concatenate([at[a:b - 1] for a, b in zip(ptr, ptr[1:])])).long().to(cuda_device)
+    to = torch.from_numpy(np.concatenate([at[a + 1:b] for a, b in zip(ptr, ptr[1:])])).long().to(cuda_device)
+    n = len(rows)
+    adv = torch.randn(n, device=cuda_device, generator=g)
+    w = torch.rand(n, device=cuda_device, generator=g) * (rows % 5 != 3)       # (rows without any weight)
+    ent = 0.01
+    kw = dict(weights=w, per_token=True, entropy_coef=ent)
+    got = TL.policy_loss(plan, x, tok, None, adv, **kw)
+    alone = TL.policy_loss(plan, x, tok, None, adv, grad=False, **kw)
+    assert all(torch.equal(u, v) for u, v in zip(got[:3], alone[:3]))
+
+    W, A = w.double(), adv.double()
+    each = torch.zeros(N, dtype=torch.float64, device=cuda_device)
+    sum_w = each.clone().index_add_(0, rows, W)
+    sum_g, size_g = each.clone().index_add_(0, rows, -W * A), each.clone().index_add_(0, rows, (W * A).abs())
+    edge, edge_size = each.clone().index_add_(0, to, -W * A), each.clone().index_add_(0, to, (W * A).abs())
+    parent_row = torch.full((N,), -1, dtype=torch.long, device=cuda_device)
+    parent_row[to] = rows
+    loss = terms = 0.0
+    for i in range(0, N, 250):
+        r = torch.arange(i, min(N, i + 250), device=cuda_device)
+        logp = torch.log_softmax(x[r].double(), 1)
+        p = logp.exp()
+        H = -(p * logp).sum(1)
+        H = torch.where(sum_w[r] != 0, H, 0.0)
+        assert ((got.entropy[r] - H).abs() <= 2.0 ** -16 * (1 + H)).all()
+        here = torch.nonzero((rows >= i) & (rows < i + 250)).flatten()
+        lp = logp[rows[here] - i, tok[to[here]].long()] * (W[here] != 0)
+        assert ((got.logprobs[here] - lp).abs() <= 2.0 ** -17 + 2.0 ** -23 * lp.abs()).all()
+        loss += float((-W[here] * (A[here] + ent * H[rows[here] - i])).sum())
+        terms += float((W[here] * (2 * A[here].abs() + ent * (1 + H[rows[here] - i]))).sum())
+        want = -sum_g[r, None] * p + ent * sum_w[r, None] * p * (logp + H[:, None])
+        bound = size_g[r, None] * p + ent * sum_w[r, None] * p * (logp.abs() + H[:, None])
+        kids = torch.nonzero((parent_row >= i) & (parent_row < i + 250)).flatten()
+        want.index_put_((parent_row[kids] - i, tok[kids].long()), edge[kids], accumulate=True)
+        bound.index_put_((parent_row[kids] - i, tok[kids].long()), edge_size[kids], accumulate=True)
+        e = (got.dlogits[r].double() - want).abs()
+        assert (e <= 2.0 ** -8 * want.abs() + 2.0 ** -15 * bound + 1e-38).all(), i
+    assert abs(float(got.loss) - loss) <= 2.0 ** -15 * terms
