@@ -60,6 +60,27 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const __grid_constant__ 
     }
 }
 
+// Page numbers inside the pool, targets all different and none of them a source.  A table of the pool's pages costs
+// its clearing (0.17 us for 5,000 pages, 27 for a million), sorted targets n log n (16 moves 0.3 us, 256 4.5,
+// 2,000 30): even at 300 to 500 pages per move.
+bool well_formed(const int32_t* src, const int32_t* dst, int64_t n, int32_t n_pages) {
+    for (int64_t i = 0; i < n; ++i)
+        if (src[i] < 0 || src[i] >= n_pages || dst[i] < 0 || dst[i] >= n_pages) return false;
+    if (n_pages / 400 >= n) {
+        std::vector<int32_t> to(dst, dst + n);
+        std::sort(to.begin(), to.end());
+        if (std::adjacent_find(to.begin(), to.end()) != to.end()) return false;
+        return std::none_of(src, src + n, [&](int32_t x) { return std::binary_search(to.begin(), to.end(), x); });
+    }
+    std::vector<uint8_t> seen(n_pages, 0);
+    for (int64_t i = 0; i < n; ++i) seen[src[i]] = 1;
+    for (int64_t i = 0; i < n; ++i) {
+        if (seen[dst[i]]) return false;
+        seen[dst[i]] = 1;
+    }
+    return true;
+}
+
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 }  // namespace
@@ -81,17 +102,8 @@ extern "C" int tree_attn_cache_copy(int32_t n_caches, void* const* k8, void* con
         if (!aligned(k8[c], 16) || !aligned(v8[c], 16) || !aligned(k_scale[c], 4) || !aligned(v_scale[c], 4))
             return TREE_ATTN_ERR_ALIGNMENT;
     }
-    // targets all different, none of them a source
     try {
-        std::vector<uint8_t> seen(n_pages, 0);
-        for (int64_t i = 0; i < n; ++i) {
-            if (src[i] < 0 || src[i] >= n_pages || dst[i] < 0 || dst[i] >= n_pages) return TREE_ATTN_ERR_INVALID_ARG;
-            seen[src[i]] = 1;
-        }
-        for (int64_t i = 0; i < n; ++i) {
-            if (seen[dst[i]]) return TREE_ATTN_ERR_INVALID_ARG;
-            seen[dst[i]] = 2;
-        }
+        if (!well_formed(src, dst, n, n_pages)) return TREE_ATTN_ERR_INVALID_ARG;
     } catch (const std::bad_alloc&) {
         return TREE_ATTN_ERR_OUT_OF_MEMORY;
     }

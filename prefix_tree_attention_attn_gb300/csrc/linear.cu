@@ -613,7 +613,7 @@ int build_lin(tree_attn_plan_s* P) {
                     for (int32_t t = 0; t <= whole; ++t)
                         if (pass == 1 || t < whole)
                             X.jobs.insert(X.jobs.end(), {k, t * seg, std::min(seg, c - t * seg), place});
-                    place += whole;
+                    place += whole + (whole > 0 && X.lnodes[4 * (size_t)k] < 0);   // a root's start state
                 }
                 X.n_segments = place;
                 X.job_ptr.push_back((int32_t)(X.jobs.size() / 4));

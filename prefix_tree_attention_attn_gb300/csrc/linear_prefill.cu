@@ -12,7 +12,8 @@
 //   chunk, 1,630 cycles at 128 bytes a cycle, and pace it.
 //   Where a depth has few nodes but long ones, they are cut into segments: a first launch
 //   leaves what each adds to the state, then each segment starts from its node's state with the segments
-//   before it added.
+//   before it added.  (A root's state is taken from its slot by the first launch: the last segment
+//   may leave another one there before other segments have begun.)
 //
 // prefill_out_kernel, persistent, a unit (chunk, q-head) after the other: A = Q K^T, then
 //     O = diag(f) (P V + Q S_in),  P[m, m'] = gamma^-(m'+1) A[m, m'] for m' <= m,  f(m) = scale gamma^(m+1).
@@ -90,7 +91,7 @@ struct StateParams {
     const int32_t* chunks;     // [4*n_chunks] {first token, tokens, ..}
     const float* decay;
     float* s_out;              // [n_nodes, hkv, d, d], nodes with children
-    float* sums;               // [segments, hkv, d, d] what a segment adds to the state
+    float* sums;               // [segments, hkv, d, d] what a segment adds to the state; behind a root's, its start state
     int32_t hkv, n_nodes, n_chunks;
     int32_t first_depth;
     int32_t segment;           // chunks of a segment but a node's last
@@ -146,6 +147,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     const int par = ok ? p.lnodes[4 * node] : -1, c0 = ok ? p.lnodes[4 * node + 1] + job.y : 0;
     ok = ok && ta_ok(status, 621, c0, 0, p.n_chunks) && ta_ok(status, 622, c0 + n, 0, p.n_chunks + 1);
     const bool last = ok && job.y + n == p.lnodes[4 * node + 2];
+    const int whole = ok ? (p.lnodes[4 * node + 2] - 1) / p.segment : 0;   // segments of the node but its last
     const bool inner = last && p.kids[node + 1] > p.kids[node];
     const int end = ok ? p.chunks[4 * (c0 + n - 1) + 1] : 0;   // tokens of the last chunk; the others have 128
     auto tokens = [&](int i) { return i == n - 1 ? end : kChunk; };
@@ -164,12 +166,18 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         const size_t at = (size_t)g * kD * kD + (size_t)row * kD + col0;
         float S[32];
         const int from = ok && par < 0 ? slot_of(p.io, p.io.in, node) : -1;
-        const float* src = p.adding ? nullptr
-                           : par >= 0 ? p.s_out + (size_t)par * p.hkv * kD * kD + at
-                                    : from >= 0 ? p.io.states + (size_t)from * p.hkv * kD * kD + at : nullptr;
+        const float* src = par >= 0 ? p.s_out + (size_t)par * p.hkv * kD * kD + at
+                           : from >= 0 ? p.io.states + (size_t)from * p.hkv * kD * kD + at : nullptr;
+        if (from >= 0 && whole > 0) {
+            float* start = p.sums + (size_t)(job.w + whole) * p.hkv * kD * kD + at;
+            if (p.adding && job.y == 0)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) reinterpret_cast<float4*>(start)[i] = reinterpret_cast<const float4*>(src)[i];
+            src = start;
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float4 v = src ? reinterpret_cast<const float4*>(src)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 v = src && !p.adding ? reinterpret_cast<const float4*>(src)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
             S[4 * i] = v.x;
             S[4 * i + 1] = v.y;
             S[4 * i + 2] = v.z;

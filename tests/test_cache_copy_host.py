@@ -89,3 +89,18 @@ def test_binding(lib, monkeypatch):
     for src, dst in (([0], [1, 2]), ([[0]], [[1]]), ([0.5], [1]), ([2 ** 31], [1])):
         with pytest.raises(ValueError):
             TD.tree_cache_copy(Fake(4), src, dst)
+
+
+@pytest.mark.parametrize("pages", [2000, 10 ** 6])
+def test_moves_that_meet(lib, pages):
+    """Refusals in small and in large pools, which check the moves in different ways."""
+    def status(src, dst):
+        one = (C.c_void_p * 1)(0x1000)
+        a, b = np.asarray(src, np.int32), np.asarray(dst, np.int32)
+        return lib.tree_attn_cache_copy(1, one, one, one, one, pages, 1, 64, a.ctypes.data, b.ctypes.data, len(a), None)
+
+    many, top = list(range(100)), pages - 1
+    assert status(many, [1000 + i for i in many[:99]] + [1098]) == -1
+    assert status(many, [1000 + i for i in many[:99]] + [50]) == -1
+    assert status([5, 5, 6], [7, 8, 7]) == -1 and status([5, 5, 6], [7, 8, 5]) == -1 and status([top], [top]) == -1
+    assert status([top + 1], [0]) == -1 and status([top], [-1]) == -1

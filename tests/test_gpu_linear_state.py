@@ -104,7 +104,7 @@ def test_prefill_deep_tree(cuda_device):
                   slot_out=[-1] * 20 + [2] + [-1] * (n - 22) + [1, 5])
 
 
-@pytest.mark.parametrize("seg,kept", [([12 * 128 + 1], [0]), ([3500], [2]), ([2100, 40, 1540, 1537], [0, -1, 3, 4]), ([1536, 3072], [5, 6])])
+@pytest.mark.parametrize("seg,kept", [([12 * 128 + 1], [0]), ([3500], [2]), ([2100, 40, 1540, 1537], [0, -1, 3, 4]), ([1536, 4608], [5, 6])])
 def test_prefill_in_segments(cuda_device, seg, kept):
     """Nodes long enough to be walked in segments: against the same tokens as a chain of short nodes, whose
     states are handed on node by node."""
@@ -131,6 +131,22 @@ def test_prefill_in_segments(cuda_device, seg, kept):
     assert (a - b).abs().max() <= 2.0 ** -18 * N
     assert (o.float() - o2.float()).abs().max() <= 2.0 ** -7 * o.float().abs().max()
     assert torch.linalg.vector_norm(o.float() - o2.float()) <= 2.0 ** -9 * torch.linalg.vector_norm(o.float())
+
+
+@pytest.mark.parametrize("seg,hkv", [([20000], 32), ([9000, 4000], 16)])
+def test_prefill_in_segments_over_its_own_slot(cuda_device, seg, hkv):
+    """More segments than run at a time, of a root that leaves its state in the slot that it started from."""
+    q, k, v = draw(61, sum(seg), hkv, hkv, 128, cuda_device)
+    dec = decays(hkv, cuda_device, (0.9999, 1.0))
+    first = torch.randn((3, hkv, 128, 128), device=cuda_device) * 100
+    plan = TreePlan([-1] + [0] * (len(seg) - 1), seg)
+    rest = [-1] * (len(seg) - 1)
+    a, b = first.clone(), first.clone()
+    o = TL.tree_linear_prefill(plan, a, TL.StateSlots([1] + rest, [2] + rest, 3), q, k, v, dec, 0.1)
+    for _ in range(3):
+        b.copy_(first)
+        o2 = TL.tree_linear_prefill(plan, b, TL.StateSlots([1] + rest, [1] + rest, 3), q, k, v, dec, 0.1)
+        assert torch.equal(o, o2) and torch.equal(a[2], b[1]) and torch.equal(b[[0, 2]], first[[0, 2]])
 
 
 def test_prefill_in_two_turns_is_the_whole(cuda_device):
