@@ -6,7 +6,7 @@
 // CTA as through a pipe, a few slices in a ring of shared memory at a time, with warps for each part:
 //
 //   producer     whether the next row has any weight, and the bulk copy of its slice.
-//   statistics   S = sum 2^a, T = sum 2^a a with a = (x - m) log2 e, m near the maximum, by thread, warp and CTA;
+//   statistics   one or two teams: S = sum 2^a, T = sum 2^a a with a = (x - m) log2 e, m near the maximum, by thread, warp and CTA;
 //                a CTA's three numbers go to every CTA of the cluster by asynchronous stores that
 //                count on a barrier there.
 //   finishers    two warps, a row each in turn: join them, LSE = m + ln S, H = ln S - ln 2 T / S; the row's g_k, a lane
@@ -379,10 +379,10 @@ __device__ __forceinline__ bool has_weight(const Params& p, int lane, const Ahea
     return __any_sync(0xffffffffu, any);
 }
 
-// How the warps of a CTA are shared out: [0, stat) statistics, [stat, stat + grad) the gradient, then
-// the finishers and the producer.
+// How the warps of a CTA are shared out: `teams` of `stat` for the statistics, a row each in turn, `grad` for the
+// gradient, then the finishers and the producer.
 struct Split {
-    int stat, grad, slots, slot_bytes;
+    int teams, stat, grad, slots, slot_bytes;
 };
 
 // (80 registers: 23 warps on an SM)
@@ -392,7 +392,7 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), me = (int)cluster.block_rank(), log_c = __ffs(C) - 1;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int n_slots = f.slots, n_places = 2 * f.slots;
+    const int n_slots = f.slots, n_places = 2 * f.slots, grad0 = f.teams * f.stat;
     const int64_t cluster0 = blockIdx.x / C, clusters = gridDim.x / C;
     uint8_t* ring = smem + kRing0;
     if (tid == 0) {
@@ -416,19 +416,24 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
     // Sums wait in 2 * slots places.  A CTA sends those of a row when its slot is free, so it is done with the row `slots`
     // before; for that one every CTA had sent its sums, each when it was done with the row `slots` before that: the
     // row whose place is taken has been joined everywhere.
-    if (warp < f.stat) {
+    //
+    // Two teams that meet in a slot: a barrier tells a phase from the next one alone.  When a team comes to row j, its
+    // row before that, and so every row up to j - slots, is loaded or on its way: the slot was empty for row
+    // j - slots; it waits until it is empty of that one, then for row j.
+    if (warp < f.teams * f.stat) {
         // ---- statistics --------------------------------------------------------------------
-        const int T = 32 * f.stat;
+        const int T = 32 * f.stat, team = warp / f.stat, mine = warp - team * f.stat, at = 32 * mine + lane;
         const uint64_t c2 = f32x2(kLog2e, kLog2e);
-        int slot = 0, turn = 0, place = 0;
-        for (int64_t r = cluster0; r < p.N; r += clusters) {
-            ok = mbar_wait(smem_u32(&S.full[slot]), turn & 1, p.status, 604);
+        int slot = team % n_slots, turn = team / n_slots, place = team;
+        for (int64_t r = cluster0 + team * clusters; r < p.N; r += f.teams * clusters) {
+            if (f.teams > 1 && turn > 0) ok = mbar_wait(smem_u32(&S.empty[slot]), (turn - 1) & 1, p.status, 610);
+            if (ok) ok = mbar_wait(smem_u32(&S.full[slot]), turn & 1, p.status, 604);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             Stat st = {0.f, 0.f, 0.f};
             if (S.meta[slot].active) {         // (the same in every CTA of the cluster)
                 const Slice s(p, r, me, log_c);
-                const int odd = s.odd(tid, T);
+                const int odd = s.odd(at, T);
                 const uint8_t* here8 = ring + (size_t)slot * f.slot_bytes;
                 const uint4* here = reinterpret_cast<const uint4*>(here8) - s.lo;
                 const uint4 none = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);   // -inf
@@ -436,7 +441,7 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                 const bool odds = __any_sync(0xffffffffu, odd >= 0);
                 auto get = [&](int v) { return v < s.last ? here[v] : none; };
                 auto top2 = [&](uint4 x) { return max2_nan(max2_nan(x.x, x.y), max2_nan(x.z, x.w)); };
-                const int v0 = s.first + tid;
+                const int v0 = s.first + at;
                 // One pass: the reference is the maximum of the warp's first vectors, and is raised when a logit lies 16
                 // above it (e^16 is far from overflow), which after the first few vectors it hardly ever does.
                 uint4 x = get(v0), y = get(v0 + T);
@@ -483,7 +488,7 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                             more_s = mul_f32x2(more_s, e2);
                         }
                     };
-                    for (int v = v0, w = s.first + 32 * warp;;) {   // w: the warp's first, for all its lanes alike
+                    for (int v = v0, w = s.first + 32 * mine;;) {   // w: the warp's first, for all its lanes alike
                         add4(x);
                         add4(y);
                         v += 2 * T;
@@ -526,7 +531,7 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
             // the last of the CTA's warps joins them and sends
             int last = 0;
             if (lane == 0) {
-                S.parts[slot][warp] = st;
+                S.parts[slot][mine] = st;
                 __threadfence_block();
                 last = atomicAdd(&S.parts_in[slot], 1) == f.stat - 1;
             }
@@ -545,17 +550,19 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                                  at_rank(smem_u32(&S.stat[place]), lane));
                 if (lane == 0) S.parts_in[slot] = 0;
             }
-            place = place + 1 == n_places ? 0 : place + 1;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&S.empty[slot]));
-            if (++slot == n_slots) {
-                slot = 0;
+            place += f.teams;
+            if (place >= n_places) place -= n_places;
+            slot += f.teams;
+            while (slot >= n_slots) {
+                slot -= n_slots;
                 ++turn;
             }
         }
-    } else if (warp < f.stat + f.grad) {
+    } else if (warp < grad0 + f.grad) {
         // ---- the gradient --------------------------------------------------------------------
-        const int at = tid - 32 * f.stat, T = 32 * f.grad;
+        const int at = tid - 32 * grad0, T = 32 * f.grad;
         const uint64_t c2 = f32x2(kLog2e, kLog2e);
         int slot = 0, turn = 0, meets = 0;
         for (int64_t r = cluster0; r < p.N; r += clusters) {
@@ -677,9 +684,9 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                 ++turn;
             }
         }
-    } else if (warp < f.stat + f.grad + kFinishers) {
+    } else if (warp < grad0 + f.grad + kFinishers) {
         // ---- the finishers ------------------------------------------------------------------
-        const int mine = warp - f.stat - f.grad;
+        const int mine = warp - grad0 - f.grad;
         const int64_t step = kFinishers * clusters, r0 = cluster0 + mine * clusters;
         Ahead one, two, three;                 // this row and its next two
         load_info(p, r0, one);
@@ -986,17 +993,18 @@ struct Shape {
     Split split;
 };
 // A slice is at most a third of what an SM has, so that one can be loaded, one be summed and one get its gradient at
-// a time; large slices have an SM to themselves, smaller ones share it, with fewer warps each.  The sums run over the same
-// threads with and without the gradient, so a policy's log-probs of an evaluation are those of its update to the bit.
-// Measured (us; CTAs a row / statistics warps / gradient warps / CTAs an SM): with the gradient 152,064 x 4,000 rows
-// 407 (4/8/12/1) 422 (4/12/12/1) 441 (4/12/8/1) 533 (8/4/4/2); 64,000 x 5,000 223 (2/8/12/1) 253 (4/4/4/2); 32,000 x 10,000
-// 225 (1/8/12/1) 245 (2/4/4/2); 16,000 x 20,000 259 (1/4/4/2) 275 (1/2/3/3); 8,000 x 20,000 160 (1/2/3/3) 170 (1/2/2/3);
-// 4,000 x 20,000 113 (1/1/1/3) 118 (1/2/2/2); 1,000 x 20,000 84 (1/1/1/3) 95 (1/2/2/3); 152,064 x 64 18.5 (8/4/4/2)
-// 18.8 (4/8/12/1).  Without it 152,064 x 4,000 286 (4/8/1) 266 (4/16/1); 32,000 x 10,000 155 (1/8/1) 141 (1/16/1);
-// 16,000 x 20,000 141 (1/4/3) 163 (1/4/2); 8,000 x 20,000 92 (1/2/4) 112 (1/2/3); 4,000 x 20,000 77 (1/1/3) 68 (1/2/4).
+// a time; large slices have an SM to themselves, smaller ones share it, with fewer warps each.  A row's sums run over
+// as many threads with and without the gradient, so a policy's log-probs of an evaluation are those of its update to
+// the bit; without it two teams take a row each in turn.  Measured (us; CTAs a row / teams / statistics warps each /
+// gradient warps / CTAs an SM): with the gradient 152,064 x 4,000 rows 407 (4/1/8/12/1) 428 (4/2/4/12/1) 533 (8/1/4/4/2);
+// 64,000 x 5,000 223 (2/1/8/12/1) 235 (2/2/4/12/1); 32,000 x 10,000 226 (1/1/8/12/1) 246 (2/1/4/4/2); 16,000 x 20,000 260
+// (1/1/4/4/2) 271 (1/2/2/4/2); 8,000 x 20,000 158 (1/2/1/3/3) 165 (1/1/2/3/3); 4,000 x 20,000 112 (1/2/1/3/3) 114
+// (1/1/1/1/3); 1,000 x 20,000 78 (1/2/1/3/3) 83 (1/1/1/1/3).  Without it 152,064 x 4,000 243 (4/2/8/1) 287 (4/1/8/1)
+// 266 (4/1/16/1); 64,000 x 5,000 134 (2/2/8/1) 155 (2/1/8/1); 32,000 x 10,000 135 (1/2/8/1) 158 (1/1/8/1); 16,000 x 20,000
+// 136 (1/2/4/2) 142 (1/1/4/3); 8,000 x 20,000 96 (1/2/1/3) 87 (1/2/2/3); 4,000 x 20,000 58 (1/2/1/3) 77 (1/1/1/3).
 Shape shape_of(int64_t vocab, bool grad) {
     const int64_t vectors = (vocab + 7) / 8 + 1;    // (a row may start inside a vector)
-    Shape f = {1, 0, {0, 0, 1, 0}};
+    Shape f = {1, 0, {2, 1, 3, 1, 0}};
     while (f.C < 8 && (vectors + f.C - 1) / f.C * 16 > 76 * 1024) f.C *= 2;
     Split& s = f.split;
     s.slot_bytes = (int)((vectors + f.C - 1) / f.C * 16);
@@ -1007,14 +1015,9 @@ Shape shape_of(int64_t vocab, bool grad) {
         per_sm = 1;
     } else if (s.slot_bytes > 20 * 1024) {
         s.stat = s.grad = 4;
-        per_sm = grad ? 2 : 3;
-    } else if (s.slot_bytes > 10 * 1024) {
-        s.stat = 2;
-        s.grad = 3;
-        per_sm = grad ? 3 : 4;
-    } else {
-        s.stat = s.grad = 1;
+        per_sm = 2;
     }
+    if (grad && s.stat > 1) s.teams = 1;
     if (!grad) s.grad = 0;
     while (s.slots < kMaxSlots && kRing0 + (s.slots + 1) * s.slot_bytes <= (kShared + 1024) / per_sm - 1024) ++s.slots;
     f.smem = kRing0 + s.slots * s.slot_bytes;
@@ -1121,7 +1124,7 @@ int tree_attn_policy_loss(tree_attn_plan_t P, const void* logits, int64_t row_st
     });
     if (set[dev] != cudaSuccess) return TREE_ATTN_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(32 * (f.split.stat + f.split.grad + kFinishers + 1));
+    cfg.blockDim = dim3(32 * (f.split.teams * f.split.stat + f.split.grad + kFinishers + 1));
     cfg.dynamicSmemBytes = f.smem;
     cfg.stream = s;
     cudaLaunchAttribute at[2];
