@@ -360,15 +360,18 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 }
 
 // ---- the outputs --------------------------------------------------------------------------------
-// A CTA keeps one kv-head (and, where there are few chunks, some of its q-heads) and walks the chunks j0,
-// j0 + lanes, ...  K is loaded once per chunk, V and S_in together once; Q comes through
-// three slots.  TMEM holds two units (buffer b = u & 1): A, then P over it, at [256b, 256b + 128), O at
-// [256b + 128, 256b + 256).  A of unit u is issued before the products of unit u - 1, and unit u - 1's output is
-// read after unit u's mask, so that the products run meanwhile.
+// A CTA keeps one kv-head and walks the chunks j, j + lanes, ... while all CTAs have one, then its share of the q-heads
+// of the chunks that are left (whole chunks left some CTAs 20 units where the mean is 16.4; shares of
+// chunks in a row throughout took a tenth longer on a long context).  K is loaded once per chunk, V and S_in together
+// once; Q comes through three slots.  TMEM holds two units (buffer b = u & 1): A, then P over it, at
+// [256b, 256b + 128), O at [256b + 128, 256b + 256).  A of unit u is issued before the products of unit u - 1, and
+// unit u - 1's output is read after unit u's mask, so that the products run meanwhile.
 // warps 0-7: query row m = 32 (w % 4) + lane, columns [64 (w / 4), + 64) of A and O; warp 8 loads, warp 9
-// issues.  A warp's 32 x 64 outputs leave by one bulk store out of shared memory: written from
-// registers, 16 bytes of 32 different rows at a time, they kept the store unit busy for 2,000 of a
-// unit's 5,300 cycles.
+// issues.  A warp's 32 x 64 outputs leave by one bulk store out of shared memory (from registers, 16 bytes of 32
+// different rows at a time, they kept the store unit busy for 2,000 cycles of a unit).
+// A unit takes 3,900 cycles: 3,200 of tensor products, 3,500 of the mask, the weights and the roundings, 3,300 of
+// memory at 64 / 8 heads, beside one another.  480,408 tokens of 64 / 8 heads in 123 nodes: 3.9 ms with the states,
+// 4.6 TB/s of what has to be read and written; 8,835 of 32 / 8 heads in 17 nodes 88 us; one turn of 777 23 us.
 constexpr int kOutK = 2048, kOutV = kOutK + kTile, kOutS = kOutV + kTile, kOutQ = kOutS + kTile, kQSlots = 3,
               kOutStage = kOutQ + kQSlots * kTile, kOutSmem = kOutStage + kTile;
 
@@ -376,7 +379,7 @@ struct OutParams {
     const int32_t* chunks;
     const float* decay;
     uint16_t* out;
-    int32_t n_chunks, lanes, parts;            // a group's q-heads in `parts` parts
+    int32_t n_chunks, lanes, share;            // CTAs of a kv-head, units of each of the chunks that are left
     int32_t hq, hkv;
     float scale;
     int* status;
@@ -394,11 +397,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 0) report_status(status, -5);
         return;
     }
-    const int part = blockIdx.x % p.parts, g = blockIdx.x / p.parts % p.hkv, j0 = blockIdx.x / p.parts / p.hkv;
-    const int G = p.hq / p.hkv / p.parts, h0 = (g * p.parts + part) * G;   // q-heads [h0, h0 + G)
-    if (j0 >= p.n_chunks) return;              // uniform: nothing set up yet
-    const int n_items = (p.n_chunks - 1 - j0) / p.lanes + 1, U = n_items * G;
-    auto chunk_of = [&](int i) { return j0 + i * p.lanes; };
+    // `full` whole chunks, and then units [t0, t1) of those that are left
+    const int g = blockIdx.x % p.hkv, lane_no = blockIdx.x / p.hkv, G = p.hq / p.hkv, h0 = g * G, full = p.n_chunks / p.lanes;
+    const int left = (p.n_chunks - full * p.lanes) * G, t0 = min(lane_no * p.share, left), t1 = min(t0 + p.share, left);
+    const int U = full * G + t1 - t0, n_items = full + (t1 > t0 ? (t1 - 1) / G - t0 / G + 1 : 0);
+    if (U == 0) return;                        // uniform: nothing set up yet
+    const int left0 = full * p.lanes + t0 / G - full, n0 = t0 % G;
+    auto chunk_of = [&](int i) { return i < full ? lane_no + i * p.lanes : left0 + i; };
+    auto head_of = [&](int i) { return i == full ? n0 : 0; };   // the chunk's first q-head here
     auto bar = [&](int i) { return sb + 8u * (uint32_t)i; };
     const uint32_t b_k = bar(0), b_v = bar(1), b_kfree = bar(2), b_vfree = bar(3), b_drain = bar(4), holder = bar(5);
     auto b_qf = [&](int q) { return bar(6 + q); };     // Q slot q has come
@@ -441,30 +447,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 8) {
         if (lane == 0) {
-            int qs = 0, q = 0, round = 0;          // Q loads sent, the next one's slot and its turn
+            int sent = 0, q = 0, round = 0;        // Q loads sent, the next one's slot and its turn
             bool k_sent = false, v_sent = false;
-            for (int i = 0; i < n_items && ok; ++i) {
-                const int chunk = chunk_of(i), off = p.chunks[4 * chunk];
+            for (int i = 0, u = 0; i < n_items && ok; ++i) {
+                const int chunk = chunk_of(i), off = p.chunks[4 * chunk], first = head_of(i), end = min(G, first + U - u);
                 k_sent = v_sent = false;
                 if (i > 0) ok = mbar_wait(b_kfree, (i - 1) & 1, status, 131);   // the last chunk's last A has read it
                 if (!ok) break;
                 mbar_expect_tx(b_k, kTile);
                 for (int blk = 0; blk < 2; ++blk) tma_load_3d(ka + blk * kHalf, &tm_k, blk * 64, g, off, b_k);
                 k_sent = true;
-                for (int n = 0; n < G && ok; ++n) {
+                for (int n = first; n < end && ok; ++n, ++u) {
                     if (round) ok = mbar_wait(b_qe(q), (round - 1) & 1, status, 132);
                     if (!ok) break;
                     mbar_expect_tx(b_qf(q), kTile);
                     for (int blk = 0; blk < 2; ++blk)
                         tma_load_3d(qa0 + q * kTile + blk * kHalf, &tm_q, blk * 64, h0 + n, off, b_qf(q));
-                    ++qs;
+                    ++sent;
                     if (++q == kQSlots) {
                         q = 0;
                         ++round;
                     }
-                    // V and S_in after the second q-head's Q (the first's with one q-head): the last chunk's
-                    // last products, which have read them, are issued before this chunk's second A
-                    if (n == (G > 1 ? 1 : 0)) {
+                    // V and S_in after the chunk's second Q here (the only one's, where there is no second): the last
+                    // chunk's last products, which have read them, are issued before this chunk's second A
+                    if (n == min(first + 1, end - 1)) {
                         if (i > 0) ok = mbar_wait(b_vfree, (i - 1) & 1, status, 133);
                         if (!ok) break;
                         mbar_expect_tx(b_v, 2 * kTile);
@@ -481,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok)
-                for (int u = max(0, qs - kQSlots); u < qs; ++u) mbar_wait(b_qf(u % kQSlots), (u / kQSlots) & 1, status, 136);
+                for (int u = max(0, sent - kQSlots); u < sent; ++u) mbar_wait(b_qf(u % kQSlots), (u / kQSlots) & 1, status, 136);
         }
         __syncwarp();
     } else if (warp == 9) {
@@ -490,13 +496,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t ID_O = idesc_bf16(128, 128, false, true);    // P V, Q S_in
             const uint64_t kd = sdesc_sw128(ka, 16, 1024), vd = sdesc_sw128(va, kHalf, 1024), sd = sdesc_sw128(sina, kHalf, 1024);
             // the unit whose O is next: its place in its chunk, its slot
-            int on = 0, oi = 0, oq = 0;
-            int ksteps = (p.chunks[4 * j0 + 1] + 15) / 16;
+            int on = head_of(0), ofirst = on, oi = 0, oq = 0;
+            int ksteps = (p.chunks[4 * chunk_of(0) + 1] + 15) / 16;
             auto issue_o = [&](int u) {
                 const int b = u & 1;
                 ok = mbar_wait(b_p(b), (u >> 1) & 1, status, 137);
                 if (ok && u >= 2) ok = mbar_wait(b_oe(b), ((u >> 1) - 1) & 1, status, 138);   // unit u - 2's output read
-                if (ok && on == 0) ok = mbar_wait(b_v, oi & 1, status, 139);                   // this chunk's V and S_in
+                if (ok && on == ofirst) ok = mbar_wait(b_v, oi & 1, status, 139);                     // this chunk's V and S_in
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t O = tmem + 256 * b + 128, P = tmem + 256 * b;
@@ -516,15 +522,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 oq = oq == kQSlots - 1 ? 0 : oq + 1;
                 if (++on == G) {
                     mma_commit(b_vfree);
-                    on = 0;
-                    if (++oi < n_items) ksteps = (p.chunks[4 * chunk_of(oi) + 1] + 15) / 16;
+                    on = ofirst = head_of(++oi);
+                    if (oi < n_items) ksteps = (p.chunks[4 * chunk_of(oi) + 1] + 15) / 16;
                 }
             };
-            int n = 0, i = 0, q = 0, round = 0;
+            int n = head_of(0), first = n, i = 0, q = 0, round = 0;
             for (int u = 0; u < U && ok; ++u) {
                 const int b = u & 1;
                 ok = mbar_wait(b_qf(q), round & 1, status, 140);
-                if (ok && n == 0) ok = mbar_wait(b_k, i & 1, status, 141);
+                if (ok && n == first) ok = mbar_wait(b_k, i & 1, status, 141);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t qd = sdesc_sw128(qa0 + q * kTile, 16, 1024);
@@ -536,8 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_commit(b_sf(b));
                 if (++n == G) {
                     mma_commit(b_kfree);
-                    n = 0;
-                    ++i;
+                    n = first = head_of(++i);
                 }
                 if (++q == kQSlots) {
                     q = 0;
@@ -556,8 +561,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float fo = p.scale * exp2f((float)(m + 1) * lg);
         const uint32_t stage = sb + kOutStage + warp * 4096;
         // Unit u's output is read after unit u + 1's mask.
-        int prev_off = 0, prev_L = 0, prev_h = 0, n = 0, i = 0, q = 0;
-        int off = p.chunks[4 * j0], L = p.chunks[4 * j0 + 1];
+        int prev_off = 0, prev_L = 0, prev_h = 0, n = head_of(0), i = 0, q = 0;
+        int off = p.chunks[4 * chunk_of(0)], L = p.chunks[4 * chunk_of(0) + 1];
+        int first = n;                             // the chunk's first q-head here
         for (int u = 0; u <= U; ++u) {
             if (u < U) {
                 const int b = u & 1;
@@ -603,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // the rows behind a ragged chunk are another node's: zeros in the last 16 that the product
                 // reads (0 times an infinity there would not be 0)
-                if (n == 0 && (L & 15)) {
+                if (n == first && (L & 15)) {
                     ok = mbar_wait(b_v, i & 1, status, 144);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
@@ -679,8 +685,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             prev_h = h0 + n;
             q = q == kQSlots - 1 ? 0 : q + 1;
             if (++n == G) {
-                n = 0;
-                if (++i < n_items) {
+                n = first = head_of(++i);
+                if (i < n_items) {
                     off = p.chunks[4 * chunk_of(i)];
                     L = p.chunks[4 * chunk_of(i) + 1];
                 }
@@ -778,15 +784,12 @@ int tree_attn_linear_prefill(tree_attn_plan_t P, const void* q, const void* k, c
                            tv, ts32, p) != cudaSuccess)
                 return TREE_ATTN_ERR_CUDA;
         }
-    // about one CTA per SM: lanes of chunks for each kv-head, and where there are fewer chunks than that, the
-    // group's q-heads in parts
-    const int G = hq / hkv;
-    const int lanes = (int)std::max<int64_t>(1, std::min<int64_t>(nc, sms[dev] / hkv));
-    int parts = 1;
-    for (int c = 2; c <= G; ++c)
-        if (G % c == 0 && (int64_t)lanes * hkv * c <= sms[dev]) parts = c;
-    const OutParams p = {D->chunks, decay, static_cast<uint16_t*>(o), (int32_t)nc, lanes, parts, hq, hkv, scale, status};
-    const cudaError_t e = launch_pdl(prefill_out_kernel, dim3((unsigned)(lanes * hkv * parts)), dim3(kThreads), kOutSmem, s,
+    // about one CTA per SM
+    const int G = hq / hkv, lanes = std::max(1, sms[dev] / hkv);
+    const int left = (int)(nc % lanes) * G, share = (left + lanes - 1) / lanes;
+    const int used = nc >= lanes ? lanes : (left + share - 1) / share;
+    const OutParams p = {D->chunks, decay, static_cast<uint16_t*>(o), (int32_t)nc, lanes, share, hq, hkv, scale, status};
+    const cudaError_t e = launch_pdl(prefill_out_kernel, dim3((unsigned)(used * hkv)), dim3(kThreads), kOutSmem, s,
                                      tq, tk, tv, ts, to32, p);
     return e == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA;
 }
