@@ -14,6 +14,10 @@
 //   leaves what each adds to the state, then each segment starts from its node's state with the segments
 //   before it added.  (A root's state is taken from its slot by the first launch: the last segment
 //   may leave another one there before other segments have begun.)
+//   A call's later launches begin while the one before them runs, on SMs that it leaves free: the first
+//   one has waited for all that came before the call, so keys, values, queries and tables are there, and only
+//   the warps that read or write states wait for the launch before (17 nodes of 8,835 tokens: 79 us; 88 one
+//   after another).
 //
 // prefill_out_kernel, persistent, a unit (chunk, q-head) after the other: A = Q K^T, then
 //     O = diag(f) (P V + Q S_in),  P[m, m'] = gamma^-(m'+1) A[m, m'] for m' <= m,  f(m) = scale gamma^(m+1).
@@ -96,6 +100,7 @@ struct StateParams {
     int32_t first_depth;
     int32_t segment;           // chunks of a segment but a node's last
     int32_t adding;            // 1: this launch leaves the sums
+    int32_t leads;             // 1: the call's first launch
     SlotIO io;
 };
 
@@ -151,7 +156,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     const bool inner = last && p.kids[node + 1] > p.kids[node];
     const int end = ok ? p.chunks[4 * (c0 + n - 1) + 1] : 0;   // tokens of the last chunk; the others have 128
     auto tokens = [&](int i) { return i == n - 1 ? end : kChunk; };
-    grid_dep_wait();
+    if (p.leads) grid_dep_wait();
     grid_dep_launch();
     const float gamma = p.decay[g], lg = log2f(gamma);
     // (once per kv-head; the call's outputs are then undefined)
@@ -166,6 +171,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         const size_t at = (size_t)g * kD * kD + (size_t)row * kD + col0;
         float S[32];
         const int from = ok && par < 0 ? slot_of(p.io, p.io.in, node) : -1;
+        if (!p.leads) grid_dep_wait();
         const float* src = par >= 0 ? p.s_out + (size_t)par * p.hkv * kD * kD + at
                            : from >= 0 ? p.io.states + (size_t)from * p.hkv * kD * kD + at : nullptr;
         if (from >= 0 && whole > 0) {
@@ -370,8 +376,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 // issues.  A warp's 32 x 64 outputs leave by one bulk store out of shared memory (from registers, 16 bytes of 32
 // different rows at a time, they kept the store unit busy for 2,000 cycles of a unit).
 // A unit takes 3,900 cycles: 3,200 of tensor products, 3,500 of the mask, the weights and the roundings, 3,300 of
-// memory at 64 / 8 heads, beside one another.  480,408 tokens of 64 / 8 heads in 123 nodes: 3.9 ms with the states,
-// 4.6 TB/s of what has to be read and written; 8,835 of 32 / 8 heads in 17 nodes 88 us; one turn of 777 23 us.
+// memory at 64 / 8 heads, beside one another.  480,408 tokens of 64 / 8 heads in 123 nodes: 3.84 ms with the states,
+// 4.6 TB/s of what has to be read and written; 8,835 of 32 / 8 heads in 17 nodes 79 us; one turn of 777 21 us.
 constexpr int kOutK = 2048, kOutV = kOutK + kTile, kOutS = kOutV + kTile, kOutQ = kOutS + kTile, kQSlots = 3,
               kOutStage = kOutQ + kQSlots * kTile, kOutSmem = kOutStage + kTile;
 
@@ -434,7 +440,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
     }
     if (warp == 9) tmem_alloc(holder, 512);
-    grid_dep_wait();
     grid_dep_launch();
     const float lg = log2f(p.decay[g]);
     const bool column = lg > -100.f / 128.f;
@@ -448,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) {
         if (lane == 0) {
             int sent = 0, q = 0, round = 0;        // Q loads sent, the next one's slot and its turn
-            bool k_sent = false, v_sent = false;
+            bool k_sent = false, v_sent = false, waited = false;
             for (int i = 0, u = 0; i < n_items && ok; ++i) {
                 const int chunk = chunk_of(i), off = p.chunks[4 * chunk], first = head_of(i), end = min(G, first + U - u);
                 k_sent = v_sent = false;
@@ -473,6 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (n == min(first + 1, end - 1)) {
                         if (i > 0) ok = mbar_wait(b_vfree, (i - 1) & 1, status, 133);
                         if (!ok) break;
+                        if (!waited) grid_dep_wait();   // the states
+                        waited = true;
                         mbar_expect_tx(b_v, 2 * kTile);
                         for (int blk = 0; blk < 2; ++blk) {
                             tma_load_3d(va + blk * kHalf, &tm_v, blk * 64, g, off, b_v);
@@ -772,14 +779,16 @@ int tree_attn_linear_prefill(tree_attn_plan_t P, const void* q, const void* k, c
     if (set[dev] != cudaSuccess) return TREE_ATTN_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const LinInfo& X = P->lin;
+    int leads = 1;
     for (size_t l = 0; l + 1 < X.lvl_ptr.size(); ++l)
         for (int adding = 1; adding >= 0; --adding) {
             const int32_t *range = &X.job_ptr[2 * l + (adding ? 0 : 1)], jobs = range[1] - range[0];
             if (!jobs) continue;
             const StateParams p = {reinterpret_cast<const int4*>(D->lin_jobs) + range[0], D->lnodes, D->kids, D->chunks, decay,
                                    reinterpret_cast<float*>(ws + w.s_out), reinterpret_cast<float*>(ws + w.sums), hkv,
-                                   P->n_nodes, (int32_t)nc, l == 0, X.segment[l], adding,
+                                   P->n_nodes, (int32_t)nc, l == 0, X.segment[l], adding, leads,
                                    {states, slot_in, slot_out, D->lin_ids, n_slots, status}};
+            leads = 0;
             if (launch_pdl(prefill_state_kernel, dim3((unsigned)((int64_t)jobs * hkv * 2)), dim3(kStateThreads), kStateSmem, s, tk,
                            tv, ts32, p) != cudaSuccess)
                 return TREE_ATTN_ERR_CUDA;

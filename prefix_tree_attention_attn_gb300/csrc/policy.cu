@@ -910,6 +910,7 @@ int ensure_policy(tree_attn_plan_s* P, DevicePlan** out, int64_t* n_pred) {
     if ((st = build_traj(P))) return st;
     const TrajInfo& X = P->traj;
     const int64_t L = (int64_t)X.leaves.size(), np = (int64_t)X.traj_tok.size() - L;
+    if (np > INT32_MAX) return TREE_ATTN_ERR_TOO_LARGE;
     *n_pred = np;
     DevicePlan& D = P->dev[dev];
     if (!D.policy_ready) {

@@ -9,8 +9,7 @@ Growing a tree, from and to states in slots of a pool fp32 [n_slots, hkv, d, d]:
 
     slots = StateSlots([-1, -1, -1], [-1, 0, 1], n_slots)          # a prompt and two branches: their states kept
     o = tree_linear_prefill(plan, states, slots, q, k, v, decay, scale)
-    fork = StateSlots([0, 0, 1], [0, 2, 1], n_slots)               # refused: row 1 reads what row 0 writes
-    fork = StateSlots([0, 0, 1], [3, 2, 1], n_slots)               # two branches go on from slot 0
+    fork = StateSlots([0, 0, 1], [3, 2, 1], n_slots)               # two branches go on from slot 0, one in its own
     o1 = tree_linear_step(states, fork, q1, k1, v1, decay, scale)  # one token per branch
 """
 from __future__ import annotations

@@ -16,7 +16,8 @@ import torch
 
 from oracle import layout as OL
 from oracle import linear as OLN
-from prefix_tree_attention_attn_gb300 import TreePlan, device_status
+from prefix_tree_attention_attn_gb300 import TreePlan, build as _build, device_status
+from prefix_tree_attention_attn_gb300 import _binding as B
 from prefix_tree_attention_attn_gb300 import linear as TL
 
 pytestmark = pytest.mark.gpu
@@ -269,6 +270,59 @@ def test_step_capture_and_side_stream(cuda_device):
         op = TL.tree_linear_prefill(plan, a, slots, pq, pk, pv, dec, 0.1)
         graph.replay()
         assert torch.equal(o, want) and torch.equal(o2, op) and torch.equal(a, b)
+
+
+def test_reproducible_and_debug_build(cuda_device):
+    parent, seg, hq, hkv = [-1, 0, 0, 1, 1, -1], [2000, 300, 129, 64, 1, 500], 8, 2
+    n, N = len(seg), sum(seg)
+    q, k, v = draw(71, N, hq, hkv, 128, cuda_device)
+    dec = decays(hkv, cuda_device)
+    first = torch.randn((n + 1, hkv, 128, 128), device=cuda_device)
+    fork = TL.StateSlots([0, 0, -1, 3], [1, 2, 4, -1], n + 1)
+
+    def both():
+        s = first.clone()
+        plan = TreePlan(parent, seg)
+        o = TL.tree_linear_prefill(plan, s, TL.StateSlots([n] + [-1] * (n - 1), list(range(n)), n + 1), q, k, v, dec, 0.1)
+        o1 = TL.tree_linear_step(s, fork, q[:4], k[:4], v[:4], dec, 0.1, o=torch.zeros_like(q[:4]))
+        torch.cuda.synchronize()
+        assert device_status() == 0
+        return s, o, o1
+
+    want = both()
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(both(), want))
+    with B.library(_build.build_library(debug=True)):
+        got = both()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_calls_behind_one_another(cuda_device):
+    """Inputs that the kernel before a call writes, and calls that hand states on without a pause between them: launches of
+    one call overlap, calls do not."""
+    parent, seg, hq, hkv = [-1, 0, 0, 1], [300, 140, 700, 33], 8, 4
+    N, plan = sum(seg), TreePlan(parent, seg)
+    q, k, v = draw(81, N, hq, hkv, 128, cuda_device)
+    dec = decays(hkv, cuda_device, (0.9, 0.99))
+    slots, turns = TL.StateSlots([0, -1, -1, -1], [-1, 1, -1, 0], 2), 6
+    slots.upload()
+    factor = torch.tensor([1.0, -0.5, 2.0, 0.25, -1.0, 4.0]).bfloat16().to(cuda_device)
+
+    def chain(wait):
+        s = torch.zeros((2, hkv, 128, 128), device=cuda_device)
+        kk, vv, ws, out = torch.empty_like(k), torch.empty_like(v), None, []
+        ws = torch.empty(TL.prefill_workspace(plan, hkv, 128), dtype=torch.uint8, device=cuda_device)
+        for i in range(turns):
+            torch.mul(k, factor[i], out=kk)
+            torch.mul(v, factor[-i], out=vv)
+            out.append(TL.tree_linear_prefill(plan, s, slots, q, kk, vv, dec, 0.1, workspace=ws))
+            if wait:
+                torch.cuda.synchronize()
+        return [s, *out]
+
+    want = chain(True)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(chain(False), want))
 
 
 def test_notices(cuda_device, lib):
