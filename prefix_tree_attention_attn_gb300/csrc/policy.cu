@@ -6,9 +6,9 @@
 // CTA as through a pipe, a few slices in a ring of shared memory at a time, with warps for each part:
 //
 //   producer     whether the next row has any weight, and the bulk copy of its slice.
-//   statistics   one or two teams: S = sum 2^a, T = sum 2^a a with a = (x - m) log2 e, m near the maximum, by thread, warp and CTA;
-//                a CTA's three numbers go to every CTA of the cluster by asynchronous stores that
-//                count on a barrier there.
+//   statistics   one or two teams: S = sum 2^a, T = sum 2^a a with a = (x - m) log2 e, m near the maximum, by
+//                thread, warp and CTA; a CTA's three numbers go to every CTA of the cluster by asynchronous
+//                stores that count on a barrier there.
 //   finishers    two warps, a row each in turn: join them, LSE = m + ln S, H = ln S - ln 2 T / S; the row's g_k, a lane
 //                for each prediction where there are at most 32 of one target (inside a segment: one
 //                for each trajectory through it), whose inputs it has loaded rows ahead; their sums.
@@ -18,8 +18,8 @@
 //                their order).
 //
 // (With the same warps doing all parts of a row in turn, and five such CTAs on an SM, the chain from
-// a row's load to its gradient set the pace: 1,022 us for 8,836 rows of 152,064 logits, 7,797 of them with
-// weight, where this takes 810, 6.3 TB/s of reads and writes.)
+// a row's load to its gradient set the pace: 1,022 us for 8,835 rows of 152,064 logits, 7,797 of them with
+// weight, where this takes 779, 6.5 TB/s of reads and writes; without the gradient 470.)
 //
 // Whether a ratio lies beyond the clip decides a whole gradient, so lp - old is a pair of floats:
 // ln S = k ln 2 + ln f, f near 1, adds no error beyond 3e-8.
@@ -494,8 +494,13 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                         v += 2 * T;
                         w += 2 * T;
                         if (w >= s.last) break;
-                        x = get(v);
-                        y = get(v + T);
+                        if (w + T + 32 <= s.last) {     // all of the warp's
+                            x = here[v];
+                            y = here[v + T];
+                        } else {
+                            x = get(v);
+                            y = get(v + T);
+                        }
                         look(max2_nan(top2(x), top2(y)));
                     }
                     if (odds) {
@@ -592,22 +597,14 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                     const float a = exponent(xv, R.m);
                     return fast_exp2(a) * fmaf(R.ce, a - R.ts, R.cg);
                 };
-                auto write = [&](int v, uint32_t (&o)[4]) {
-                    if (v == yv) {
-                        const uint32_t own = pack_bf16x2(R.own, 0.f) & 0xffffu;
-                        const int e = R.y - s.start(v);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (e / 2 == i) o[i] = e & 1 ? (o[i] & 0xffffu) | (own << 16) : (o[i] & 0xffff0000u) | own;
-                    }
-                    store(v, make_uint4(o[0], o[1], o[2], o[3]));
-                };
                 int v = s.first + at;
+                uint4* row_d8 = reinterpret_cast<uint4*>(row_d - s.shift);   // (whole vectors lie as the row's do)
                 if (fabsf(R.m) < kHuge) {
-                    // (one multiply-add for the exponent: off by 2^-24 of m log2 e, far below the rounding to bf16)
+                    // (one multiply-add for the exponent: off by 2^-24 of m log2 e, far below the rounding to bf16; 20 warps
+                    // hide the latencies of a loop of one vector: 779 us where two a turn took 795)
                     const uint64_t minus = f32x2(-R.m * kLog2e, -R.m * kLog2e), cg2 = f32x2(R.cg, R.cg);
                     if (R.ce == 0.f) {
-#pragma unroll 2
+#pragma unroll 1
                         for (; v < s.last; v += T) {
                             const uint4 x = here[v];
                             const uint32_t u[4] = {x.x, x.y, x.z, x.w};
@@ -619,14 +616,16 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                                 f32x2_split(mul_f32x2(f32x2(fast_exp2(a0), fast_exp2(a1)), cg2), a0, a1);
                                 o[i] = pack_bf16x2(a0, a1);
                             }
-                            write(v, o);
+                            const uint4 o4 = make_uint4(o[0], o[1], o[2], o[3]);
+                            if (together) __stcs(row_d8 + v, o4);
+                            else store(v, o4);
                         }
                     } else {
                         // the entropy's term; -inf, where 0 would meet an infinity, as what is 0 all the same
                         const float far = R.m - fmaxf(256.f, fabsf(R.m) * 0x1p-6f);
                         const uint32_t far2 = pack_bf16x2(far, far);
                         const uint64_t ce2 = f32x2(R.ce, R.ce), rest2 = f32x2(fmaf(-R.ce, R.ts, R.cg), fmaf(-R.ce, R.ts, R.cg));
-#pragma unroll 2
+#pragma unroll 1
                         for (; v < s.last; v += T) {
                             const uint4 x = here[v];
                             const uint32_t u[4] = {max2(x.x, far2), max2(x.y, far2), max2(x.z, far2), max2(x.w, far2)};
@@ -639,7 +638,9 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                                 f32x2_split(mul_f32x2(f32x2(fast_exp2(a0), fast_exp2(a1)), fma_f32x2(ce2, a, rest2)), a0, a1);
                                 o[i] = pack_bf16x2(a0, a1);
                             }
-                            write(v, o);
+                            const uint4 o4 = make_uint4(o[0], o[1], o[2], o[3]);
+                            if (together) __stcs(row_d8 + v, o4);
+                            else store(v, o4);
                         }
                     }
                 }
@@ -651,8 +652,11 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                     uint32_t o[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(value(lo16(u[i])), value(hi16(u[i])));
-                    write(v < s.last ? v : odd, o);
+                    store(v < s.last ? v : odd, make_uint4(o[0], o[1], o[2], o[3]));
                 }
+                // the one target's element, over what the same thread has written there
+                if (yv >= 0 && (yv == odd || (yv >= s.first && yv < s.last && (yv - s.first) % T == at)))
+                    row_d[R.y] = (uint16_t)pack_bf16x2(R.own, 0.f);
                 if (R.nt != 1) {
                     // every warp has written: the targets' elements again
                     __syncwarp();

@@ -316,6 +316,19 @@ def test_rows_behind_32_bit_offsets(cuda_device):
         assert (e <= 2.0 ** -8 * 2 * p.abs() + 2.0 ** -14 * p.abs()).all()
 
 
+@pytest.mark.parametrize("V,stride,at", [(301, 301, 0), (301, 304, 0), (4001, 4100, 3), (300, 300, 5), (1000, 1013, 1)])
+def test_new_gradients_of_padded_logits(cuda_device, V, stride, at):
+    data = make(MIXED, V, 21)
+    N = len(data[1])
+    x = torch.empty(N * stride + at, dtype=torch.bfloat16, device=cuda_device).as_strided((N, V), (stride, 1), at)
+    x.copy_(data[0])
+    got, dense = run(MIXED, data, cuda_device, x=x, kl_coef=0.1), run(MIXED, data, cuda_device, kl_coef=0.1)
+    check(MIXED, data, got, kl_coef=0.1)
+    assert got.dlogits.shape == (N, V) and (got.dlogits.stride(0) - stride) % 8 == 0
+    assert (got.dlogits.data_ptr() - x.data_ptr()) % 16 == 0
+    assert (got.loss - dense.loss).abs() <= 2.0 ** -12
+
+
 @pytest.mark.parametrize("V,N", [(1000, 20000), (6001, 9000), (9000, 6000), (33000, 4000), (100000, 1500), (152064, 2500)])
 @pytest.mark.parametrize("branches", [False, True])
 def test_many_rows(cuda_device, V, N, branches):
