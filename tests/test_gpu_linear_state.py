@@ -40,6 +40,10 @@ def draw(seed, N, hq, hkv, d, device, size=1.0):
     return make(N, hq, d), make(N, hkv, d), make(N, hkv, d)
 
 
+def randn(shape, device, seed=91):
+    return torch.randn(shape, device=device, generator=torch.Generator(device).manual_seed(seed))
+
+
 def decays(hkv, device, values=(1.0, 0.9, 0.99, 0.999)):
     return torch.tensor([values[i % len(values)] for i in range(hkv)], device=device)
 
@@ -116,7 +120,7 @@ def test_prefill_in_segments(cuda_device, seg, kept):
     n_slots, hq, hkv, N = 8, 4, 2, sum(seg)
     q, k, v = draw(51, N, hq, hkv, 128, cuda_device)
     dec = decays(hkv, cuda_device, (0.999, 1.0))
-    first = torch.randn((n_slots, hkv, 128, 128), device=cuda_device)
+    first = randn((n_slots, hkv, 128, 128), cuda_device)
     a, b = first.clone(), first.clone()
     o = TL.tree_linear_prefill(TreePlan(parent, seg), a, TL.StateSlots([7] + [-1] * (len(seg) - 1), kept, n_slots), q, k, v, dec, 0.1)
     short, up, out, tip = [], [], [], {}
@@ -139,7 +143,7 @@ def test_prefill_in_segments_over_its_own_slot(cuda_device, seg, hkv):
     """More segments than run at a time, of a root that leaves its state in the slot that it started from."""
     q, k, v = draw(61, sum(seg), hkv, hkv, 128, cuda_device)
     dec = decays(hkv, cuda_device, (0.9999, 1.0))
-    first = torch.randn((3, hkv, 128, 128), device=cuda_device) * 100
+    first = randn((3, hkv, 128, 128), cuda_device) * 100
     plan = TreePlan([-1] + [0] * (len(seg) - 1), seg)
     rest = [-1] * (len(seg) - 1)
     a, b = first.clone(), first.clone()
@@ -230,7 +234,7 @@ def test_steps_continue_a_prefill(cuda_device):
     seg, hq, hkv = 70, 4, 2
     q, k, v = draw(21, seg, hq, hkv, 128, cuda_device)
     dec = decays(hkv, cuda_device, (0.95, 1.0))
-    states = torch.randn((2, hkv, 128, 128), device=cuda_device)
+    states = randn((2, hkv, 128, 128), cuda_device)
     start = num(states[0])
     o = TL.tree_linear_prefill(TreePlan([-1], [seg]), states, TL.StateSlots([0], [1], 2), q, k, v, dec, 0.1)
     slots = TL.StateSlots([0], [0], 2)
@@ -247,7 +251,7 @@ def test_step_capture_and_side_stream(cuda_device):
     R, hq, hkv = 9, 8, 2
     q, k, v = draw(31, R, hq, hkv, 128, cuda_device)
     dec, slots = decays(hkv, cuda_device), TL.StateSlots(range(R), range(R), R)
-    first = torch.randn((R, hkv, 128, 128), device=cuda_device)
+    first = randn((R, hkv, 128, 128), cuda_device)
     a, b, c = first.clone(), first.clone(), first.clone()
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
@@ -277,7 +281,7 @@ def test_reproducible_and_debug_build(cuda_device):
     n, N = len(seg), sum(seg)
     q, k, v = draw(71, N, hq, hkv, 128, cuda_device)
     dec = decays(hkv, cuda_device)
-    first = torch.randn((n + 1, hkv, 128, 128), device=cuda_device)
+    first = randn((n + 1, hkv, 128, 128), cuda_device)
     fork = TL.StateSlots([0, 0, -1, 3], [1, 2, 4, -1], n + 1)
 
     def both():

@@ -250,7 +250,7 @@ def test_on_sampled_tokens(cuda_device):
     plan = TreePlan(*tree)
     x, tok, *_ = make(tree, 2000, 13)
     x = x.to(cuda_device)
-    nxt, lp = sample_tokens(x, torch.rand(18, device=cuda_device), top_k=50)
+    nxt, lp = sample_tokens(x, torch.rand(18, device=cuda_device, generator=torch.Generator(cuda_device).manual_seed(6)), top_k=50)
     tok = tok.to(cuda_device)
     _, ptr, at = TL.trajectories(plan)
     rows = np.concatenate([at[ptr[i]:ptr[i + 1] - 1] for i in range(2)])
