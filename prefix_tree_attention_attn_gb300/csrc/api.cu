@@ -90,7 +90,8 @@ int make_tensor_map_rows(CUtensorMap* m, const void* base, int64_t rows, int hea
     return make_tmap(m, base, rows, heads, d, false, box_rows);
 }
 
-int make_tensor_map_plain(CUtensorMap* m, const void* base, int64_t rows, int heads, int d, int box_cols, int box_rows) {
+int make_tensor_map_cols(CUtensorMap* m, const void* base, int64_t rows, int heads, int d, int box_cols, int box_rows,
+                         CUtensorMapSwizzle swizzle) {
     EncodeTiledFn enc = get_encode();
     if (!enc) return TREE_ATTN_ERR_CUDA;
     cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
@@ -98,7 +99,7 @@ int make_tensor_map_plain(CUtensorMap* m, const void* base, int64_t rows, int he
     cuuint32_t box[3] = {(cuuint32_t)box_cols, 1, (cuuint32_t)box_rows};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA;
 }

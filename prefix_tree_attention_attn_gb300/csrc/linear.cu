@@ -201,9 +201,6 @@ __global__ void __launch_bounds__(160, 1)
 // every thread, are staged in shared memory a window at a time.
 constexpr int kScanBatch = 16;
 constexpr int kScanWin = 1024;
-// Walks that a depth is cut into where it has fewer nodes, and the least chunks of a segment: 9 walks of 8
-// kv-heads in halves fill the SMs once, and a walk of fewer chunks takes as long to begin as to run.
-constexpr int kWalks = 9, kMinSegment = 12;
 constexpr int kMaxScanDepths = 32;   // deeper trees use the one-walk scans (one launch per depth otherwise)
 
 __global__ void __launch_bounds__(256) lin_scan_kernel(const int32_t* __restrict__ lnodes, int n_chunks,
@@ -593,32 +590,6 @@ int build_lin(tree_attn_plan_s* P) {
         for (int32_t l = 0; l < n_depths; ++l)
             std::stable_sort(X.lvl_nodes.begin() + X.lvl_ptr[l], X.lvl_nodes.begin() + X.lvl_ptr[(size_t)l + 1],
                              [&](int32_t a, int32_t b) { return X.lnodes[4 * (size_t)a + 2] > X.lnodes[4 * (size_t)b + 2]; });
-        // walks of the states: a depth of few nodes but long ones in segments, about kWalks of them
-        X.jobs.clear();
-        X.job_ptr.assign(1, 0);
-        X.segment.clear();
-        X.n_segments = 0;
-        for (int32_t l = 0; l < n_depths; ++l) {
-            const int32_t lo = X.lvl_ptr[l], hi = X.lvl_ptr[(size_t)l + 1];
-            int64_t total = 0;
-            for (int32_t i = lo; i < hi; ++i) total += X.lnodes[4 * (size_t)X.lvl_nodes[i] + 2];
-            const int32_t seg = hi - lo >= kWalks ? INT32_MAX / kChunk
-                                                  : (int32_t)std::max<int64_t>(kMinSegment, (total + kWalks - 1) / kWalks);
-            X.segment.push_back(seg);
-            const int32_t first = X.n_segments;
-            for (int pass = 0; pass < 2; ++pass) {
-                int32_t place = first;
-                for (int32_t i = lo; i < hi; ++i) {
-                    const int32_t k = X.lvl_nodes[i], c = X.lnodes[4 * (size_t)k + 2], whole = (c - 1) / seg;   // but the last
-                    for (int32_t t = 0; t <= whole; ++t)
-                        if (pass == 1 || t < whole)
-                            X.jobs.insert(X.jobs.end(), {k, t * seg, std::min(seg, c - t * seg), place});
-                    place += whole + (whole > 0 && X.lnodes[4 * (size_t)k] < 0);   // a root's start state
-                }
-                X.n_segments = place;
-                X.job_ptr.push_back((int32_t)(X.jobs.size() / 4));
-            }
-        }
         X.ready = true;
     } catch (const std::bad_alloc&) {
         return TREE_ATTN_ERR_OUT_OF_MEMORY;
@@ -636,9 +607,7 @@ int ensure_lin_device(tree_attn_plan_s* P, DevicePlan** out) {
     if (!D.lin_ready) {
         const size_t a = (P->lin.chunks.size() + 63) / 64 * 64, b = P->lin.lnodes.size(),
                      c = P->lin.lvl_nodes.size(), k = P->lin.kids.size();
-        const size_t j = (a + b + c + k + P->node_order.size() + 3) / 4 * 4;   // int4
-        std::vector<int32_t> h(j + P->lin.jobs.size(), 0);
-        std::copy(P->lin.jobs.begin(), P->lin.jobs.end(), h.begin() + j);
+        std::vector<int32_t> h(a + b + c + k + P->node_order.size(), 0);
         std::copy(P->node_order.begin(), P->node_order.end(), h.begin() + a + b + c + k);
         std::copy(P->lin.chunks.begin(), P->lin.chunks.end(), h.begin());
         std::copy(P->lin.lnodes.begin(), P->lin.lnodes.end(), h.begin() + a);
@@ -652,7 +621,6 @@ int ensure_lin_device(tree_attn_plan_s* P, DevicePlan** out) {
         D.lvl_nodes = static_cast<int32_t*>(buf) + a + b;
         D.kids = static_cast<int32_t*>(buf) + a + b + c;
         D.lin_ids = static_cast<int32_t*>(buf) + a + b + c + k;
-        D.lin_jobs = static_cast<int32_t*>(buf) + j;
         D.lin_ready = true;
     }
     *out = &D;

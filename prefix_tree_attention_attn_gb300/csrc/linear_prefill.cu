@@ -1,15 +1,17 @@
 // Whole turns of linear attention from and to states in slots (include/tree_linear.h).
 //
 // prefill_state_kernel, one launch per depth of the tree (roots first): a CTA walks the chunks (128
-// tokens at most) of one node for one kv-head and 64 of the 128 value features -- the columns of the
+// tokens at most) of one node for one kv-head and F of the 128 value features -- the columns of the
 // state do not meet --, with the state in registers:
 //     S_in of the chunk goes out as bf16, the operand of the outputs;  S = gamma^L S + dS,
 //     dS = sum_m gamma^(L-1-m) k_m v_m^T on the tensor cores.
 //   A weighted value has 24 bits; it is split into three bf16 numbers that add up to it, so the
 //   increment is as exact as sums in fp32 are (two would leave 3e-6 of it).  The parts lie side by side in one
-//   product of N = 192, so K is read once, and are added in registers.  Warps 0-7 hold the state,
-//   8-15 weigh and split the values, 16 loads, 17 issues.  208 KB pass through shared memory per
-//   chunk, 1,630 cycles at 128 bytes a cycle, and pace it.
+//   product of N = 3 F, so K is read once, and are added in registers.  Warps 0-7 (0-3 for F = 32) hold the
+//   state, 8-15 weigh and split the values, 16 loads, 17 issues.  F = 64: 208 KB pass through shared memory per
+//   chunk, 1,630 cycles at 128 bytes a cycle, and pace it (2,300 measured).  F = 32: 136 KB; more CTAs, so
+//   taken where all of a launch run at a time (one turn of 777 tokens: 16.5 us, 20.9 with F = 64; 8 branches of 300, two
+//   waves of them: 33.0 and 31.2).
 //   Where a depth has few nodes but long ones, they are cut into segments: a first launch
 //   leaves what each adds to the state, then each segment starts from its node's state with the segments
 //   before it added.  (A root's state is taken from its slot by the first launch: the last segment
@@ -83,13 +85,32 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
 // ---- the states that enter the chunks --------------------------------------------------------
 // K in two stages; V in three, each with room for its other two parts behind it (the first goes over V).
 constexpr int kKStages = 2, kVStages = 3;
-constexpr int kStateK = 1024, kStateV = kStateK + kKStages * kTile, kStateOut = kStateV + kVStages * 3 * kHalf,
-              kStateSmem = kStateOut + kHalf;
+constexpr int kStateK = 1024, kStateV = kStateK + kKStages * kTile;
+template <int F>                               // value features of a CTA
+struct StateLayout {
+    static constexpr int kV = kChunk * F * 2;  // one part of the values
+    static constexpr int kOut = kStateV + kVStages * 3 * kV, kSmem = kOut + kV;
+};
+// The descriptor of weighted values: rows are tokens, all of a part's F features wide, swizzled over their 128 or 64 bytes.
+template <int F>
+__device__ __forceinline__ uint64_t value_desc(uint32_t at) {
+    constexpr uint64_t k64 = (uint64_t)4 << 61, kMode = (uint64_t)7 << 61;
+    const uint64_t d = sdesc_sw128(at, StateLayout<F>::kV, 16 * F);
+    return F == 64 ? d : (d & ~kMode) | k64;
+}
 constexpr int kStateThreads = 576;             // 8 warps hold the state, 8 weigh, loader, MMA
 constexpr int kAhead = 6;                      // chunks that are brought into L2 ahead of their load
 
+// Where a depth has few nodes, the walks go with the launch.
+constexpr int kSplitNodes = 8, kSplitWalks = 16, kMaxWalks = kSplitNodes + kSplitWalks;
+struct Walk {
+    int32_t node, first, chunks;               // packed node, first of its chunks
+    int32_t place, segment;                    // its first segment's place in `sums`, chunks of a segment but its last
+};
+
 struct StateParams {
-    const int4* jobs;          // {packed node, first of its chunks, chunks, its first segment's place in `sums`}
+    const int32_t* order;      // the depth's packed nodes, a walk each; or null: `walks`
+    Walk walks[kMaxWalks];
     const int32_t* lnodes;     // [4*n_nodes] {parent's packed index, first chunk, chunks, ..}
     const int32_t* kids;       // child offsets
     const int32_t* chunks;     // [4*n_chunks] {first token, tokens, ..}
@@ -98,15 +119,17 @@ struct StateParams {
     float* sums;               // [segments, hkv, d, d] what a segment adds to the state; behind a root's, its start state
     int32_t hkv, n_nodes, n_chunks;
     int32_t first_depth;
-    int32_t segment;           // chunks of a segment but a node's last
     int32_t adding;            // 1: this launch leaves the sums
     int32_t leads;             // 1: the call's first launch
     SlotIO io;
 };
 
+template <int F>
 __global__ void __launch_bounds__(kStateThreads, 1)
     prefill_state_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                         const __grid_constant__ CUtensorMap tm_s, const StateParams p) {
+                         const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ StateParams p) {
+    using Lay = StateLayout<F>;
+    constexpr int kParts = kD / F;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sb = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -135,7 +158,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(dfull(b), 1);
-            mbar_init(dfree(b), 256);
+            mbar_init(dfree(b), 4 * F);
         }
         mbar_init(drain, 1);
         fence_mbar_init();
@@ -145,14 +168,22 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + 144);
-    const int half = blockIdx.x & 1, g = (blockIdx.x >> 1) % p.hkv;
-    const int4 job = p.jobs[(blockIdx.x >> 1) / p.hkv];
-    const int node = job.x, n = job.z;
-    bool ok = ta_ok(status, 620, node, 0, p.n_nodes);
-    const int par = ok ? p.lnodes[4 * node] : -1, c0 = ok ? p.lnodes[4 * node + 1] + job.y : 0;
+    const int part = blockIdx.x % kParts, g = blockIdx.x / kParts % p.hkv;
+    Walk job;
+    bool ok;
+    if (p.order) {
+        job = {p.order[blockIdx.x / kParts / p.hkv], 0, 0, 0, INT32_MAX / kChunk};
+        ok = ta_ok(status, 620, job.node, 0, p.n_nodes);
+        if (ok) job.chunks = p.lnodes[4 * job.node + 2];
+    } else {
+        job = p.walks[blockIdx.x / kParts / p.hkv];
+        ok = ta_ok(status, 620, job.node, 0, p.n_nodes);
+    }
+    const int node = job.node, n = job.chunks;
+    const int par = ok ? p.lnodes[4 * node] : -1, c0 = ok ? p.lnodes[4 * node + 1] + job.first : 0;
     ok = ok && ta_ok(status, 621, c0, 0, p.n_chunks) && ta_ok(status, 622, c0 + n, 0, p.n_chunks + 1);
-    const bool last = ok && job.y + n == p.lnodes[4 * node + 2];
-    const int whole = ok ? (p.lnodes[4 * node + 2] - 1) / p.segment : 0;   // segments of the node but its last
+    const bool last = ok && job.first + n == p.lnodes[4 * node + 2];
+    const int whole = ok ? (p.lnodes[4 * node + 2] - 1) / job.segment : 0;   // segments of the node but its last
     const bool inner = last && p.kids[node + 1] > p.kids[node];
     const int end = ok ? p.chunks[4 * (c0 + n - 1) + 1] : 0;   // tokens of the last chunk; the others have 128
     auto tokens = [&](int i) { return i == n - 1 ? end : kChunk; };
@@ -160,14 +191,14 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     grid_dep_launch();
     const float gamma = p.decay[g], lg = log2f(gamma);
     // (once per kv-head; the call's outputs are then undefined)
-    if (p.first_depth && blockIdx.x < 2 * p.hkv && half == 0 && threadIdx.x == 0 && !(gamma > 0.f && gamma <= 1.f))
+    if (p.first_depth && blockIdx.x < kParts * p.hkv && part == 0 && threadIdx.x == 0 && !(gamma > 0.f && gamma <= 1.f))
         report_notice(status, TREE_ATTN_ERR_INVALID_DECAY);
     const int to = last ? slot_of(p.io, p.io.out, node) : -1;
     const int steps = !ok ? 0 : p.adding || inner || to >= 0 ? n : n - 1;   // increments that anything needs
 
-    if (warp < 8) {
+    if (warp < F / 8) {
         // the state: thread = key feature, 32 value features
-        const int quarter = warp & 3, row = 32 * quarter + lane, col0 = half * 64 + 32 * (warp >> 2);
+        const int quarter = warp & 3, row = 32 * quarter + lane, col0 = part * F + 32 * (warp >> 2);
         const size_t at = (size_t)g * kD * kD + (size_t)row * kD + col0;
         float S[32];
         const int from = ok && par < 0 ? slot_of(p.io, p.io.in, node) : -1;
@@ -175,8 +206,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         const float* src = par >= 0 ? p.s_out + (size_t)par * p.hkv * kD * kD + at
                            : from >= 0 ? p.io.states + (size_t)from * p.hkv * kD * kD + at : nullptr;
         if (from >= 0 && whole > 0) {
-            float* start = p.sums + (size_t)(job.w + whole) * p.hkv * kD * kD + at;
-            if (p.adding && job.y == 0)
+            float* start = p.sums + (size_t)(job.place + whole) * p.hkv * kD * kD + at;
+            if (p.adding && job.first == 0)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) reinterpret_cast<float4*>(start)[i] = reinterpret_cast<const float4*>(src)[i];
             src = start;
@@ -189,10 +220,10 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             S[4 * i + 2] = v.z;
             S[4 * i + 3] = v.w;
         }
-        if (ok && !p.adding && job.y > 0) {        // the node's segments before this one
-            const float f = exp2f((float)(p.segment * kChunk) * lg);
-            for (int t = 0; t < job.y / p.segment; ++t) {
-                const float4* add = reinterpret_cast<const float4*>(p.sums + (size_t)(job.w + t) * p.hkv * kD * kD + at);
+        if (ok && !p.adding && job.first > 0) {        // the node's segments before this one
+            const float f = exp2f((float)(job.segment * kChunk) * lg);
+            for (int t = 0; t < job.first / job.segment; ++t) {
+                const float4* add = reinterpret_cast<const float4*>(p.sums + (size_t)(job.place + t) * p.hkv * kD * kD + at);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float4 v = add[i];
@@ -203,7 +234,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 }
             }
         }
-        const uint32_t stage = sb + kStateOut + warp * 2048, tD = tmem + ((uint32_t)(32 * quarter) << 16) + 32 * (warp >> 2);
+        const uint32_t stage = sb + Lay::kOut + warp * 2048, tD = tmem + ((uint32_t)(32 * quarter) << 16) + 32 * (warp >> 2);
         const float f128 = exp2f((float)kChunk * lg);
         for (int i = 0; i < n && ok; ++i) {
             if (!p.adding) {
@@ -229,12 +260,12 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             tc_fence_after();
             const float f = i == n - 1 ? exp2f((float)end * lg) : f128;
             float v[32], more[32];                 // the three parts
-            tmem_ld32(tD + b * 192, v);
-            tmem_ld32(tD + b * 192 + 64, more);
+            tmem_ld32(tD + b * 3 * F, v);
+            tmem_ld32(tD + b * 3 * F + F, more);
             tmem_wait_ld();
 #pragma unroll
             for (int x = 0; x < 32; ++x) v[x] += more[x];
-            tmem_ld32(tD + b * 192 + 128, more);
+            tmem_ld32(tD + b * 3 * F + 2 * F, more);
             tmem_wait_ld();
             tc_fence_before();
             mbar_arrive(dfree(b));
@@ -247,14 +278,14 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 for (int i = 0; i < 8; ++i)
                     reinterpret_cast<float4*>(dst)[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
             };
-            if (p.adding) leave(p.sums + (size_t)(job.w + job.y / p.segment) * p.hkv * kD * kD + at);
+            if (p.adding) leave(p.sums + (size_t)(job.place + job.first / job.segment) * p.hkv * kD * kD + at);
             else if (inner) leave(p.s_out + (size_t)node * p.hkv * kD * kD + at);
             if (!p.adding && to >= 0) leave(p.io.states + (size_t)to * p.hkv * kD * kD + at);
         }
         if (lane == 0) bulk_wait_all();
         __syncwarp();
-    } else if (warp < 16) {
-        // the values: thread = token r and 32 features, times gamma^(L-1-r), as three numbers that add up to it
+    } else if (warp >= 8 && warp < 16) {
+        // the values: thread = token r and half of the features, times gamma^(L-1-r), as three numbers that add up to it
         const int r = threadIdx.x & 127, piece = (warp - 8) >> 2;
         const float w128 = exp2f((float)(kChunk - 1 - r) * lg);
         const uint64_t minus = f32x2(-1.f, -1.f);
@@ -268,12 +299,12 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             if (!ok) break;
             const float w = L == kChunk ? w128 : past ? 0.f : exp2f((float)(L - 1 - r) * lg);
             const uint64_t ww = f32x2(w, w);
-            uint4* v = reinterpret_cast<uint4*>(smem + kStateV + s * 3 * kHalf + r * 128);
+            uint4* v = reinterpret_cast<uint4*>(smem + kStateV + s * 3 * Lay::kV + r * 2 * F);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                // four of the row's eight 16-byte pieces, in an order rotated by the row: the rows of a warp spread
-                // over all bank groups (a piece keeps its swizzled place)
-                const int cr = (4 * piece + c + r) & 7;
+            for (int c = 0; c < F / 16; ++c) {
+                // half of the row's 16-byte pieces, in an order rotated by the row (by two rows where two lie in 128 bytes):
+                // the rows of a warp spread over all bank groups (a piece keeps its swizzled place)
+                const int cr = (F / 16 * piece + c + (F == 64 ? r : r >> 1)) & (F / 8 - 1);
                 const uint4 x = v[cr];
                 const uint32_t u[4] = {x.x, x.y, x.z, x.w};
                 uint32_t p1[4], p2[4], p3[4];
@@ -291,8 +322,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                     p3[e] = pack_bf16x2(a1, b1);
                 }
                 v[cr] = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-                v[kHalf / 16 + cr] = make_uint4(p2[0], p2[1], p2[2], p2[3]);
-                v[2 * kHalf / 16 + cr] = make_uint4(p3[0], p3[1], p3[2], p3[3]);
+                v[Lay::kV / 16 + cr] = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+                v[2 * Lay::kV / 16 + cr] = make_uint4(p3[0], p3[1], p3[2], p3[3]);
             }
             if (past) {                            // its keys meet those zeros: no infinities there either
                 uint4* k = reinterpret_cast<uint4*>(smem + kStateK + sk * kTile + piece * kHalf + r * 128);
@@ -308,7 +339,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 if (i >= steps) return;
                 const int off = p.chunks[4 * (c0 + i)];
                 for (int blk = 0; blk < 2; ++blk) tma_prefetch_3d(&tm_k, blk * 64, g, off);
-                tma_prefetch_3d(&tm_v, half * 64, g, off);
+                tma_prefetch_3d(&tm_v, part * F, g, off);
             };
             for (int i = kKStages; i < kAhead; ++i) prefetch(i);
             int sent = 0;
@@ -316,8 +347,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 const int s = i % kVStages, sk = i % kKStages, off = p.chunks[4 * (c0 + i)];
                 if (i >= kVStages) ok = mbar_wait(vfree(s), (i / kVStages - 1) & 1, status, 124);
                 if (!ok) break;
-                mbar_expect_tx(vfull(s), kHalf);
-                tma_load_3d(sb + kStateV + s * 3 * kHalf, &tm_v, half * 64, g, off, vfull(s));
+                mbar_expect_tx(vfull(s), Lay::kV);
+                tma_load_3d(sb + kStateV + s * 3 * Lay::kV, &tm_v, part * F, g, off, vfull(s));
                 sent = i + 1;
                 if (i >= kKStages) ok = mbar_wait(kfree(sk), (i / kKStages - 1) & 1, status, 125);
                 if (!ok) break;
@@ -333,9 +364,9 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             }
         }
         __syncwarp();
-    } else {
+    } else if (warp == 17) {
         if (lane == 0) {
-            constexpr uint32_t ID = idesc_bf16(128, 192, true, true);   // K^T (MN-major) x the values' parts (MN-major)
+            constexpr uint32_t ID = idesc_bf16(128, 3 * F, true, true);   // K^T (MN-major) x the values' parts (MN-major)
             for (int i = 0; i < steps && ok; ++i) {
                 const int s = i % kVStages, sk = i % kKStages, b = i & 1;
                 ok = mbar_wait(wfull(s), (i / kVStages) & 1, status, 126);
@@ -344,10 +375,10 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t kd = sdesc_sw128(sb + kStateK + sk * kTile, kHalf, 1024),
-                               vd = sdesc_sw128(sb + kStateV + s * 3 * kHalf, kHalf, 1024);
+                               vd = value_desc<F>(sb + kStateV + s * 3 * Lay::kV);
 #pragma unroll
                 for (int k = 0; k < kChunk / 16; ++k)
-                    mma_bf16_ss(tmem + b * 192, further(kd, k * 2048), further(vd, k * 2048), ID, k > 0);
+                    mma_bf16_ss(tmem + b * 3 * F, further(kd, k * 2048), further(vd, k * 32 * F), ID, k > 0);
                 mma_commit(dfull(b));
                 mma_commit(vfree(s));
                 mma_commit(kfree(sk));
@@ -377,7 +408,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 // different rows at a time, they kept the store unit busy for 2,000 cycles of a unit).
 // A unit takes 3,900 cycles: 3,200 of tensor products, 3,500 of the mask, the weights and the roundings, 3,300 of
 // memory at 64 / 8 heads, beside one another.  480,408 tokens of 64 / 8 heads in 123 nodes: 3.84 ms with the states,
-// 4.6 TB/s of what has to be read and written; 8,835 of 32 / 8 heads in 17 nodes 79 us; one turn of 777 21 us.
+// 4.6 TB/s of what has to be read and written; 8,835 of 32 / 8 heads in 17 nodes 79 us; one turn of 777 16.5 us.
 constexpr int kOutK = 2048, kOutV = kOutK + kTile, kOutS = kOutV + kTile, kOutQ = kOutS + kTile, kQSlots = 3,
               kOutStage = kOutQ + kQSlots * kTile, kOutSmem = kOutStage + kTile;
 
@@ -712,13 +743,55 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// The walks of a depth of few nodes whose long ones are cut into segments: first those whose sums are taken, then all.
+struct Split {
+    Walk sums[kMaxWalks], all[kMaxWalks];
+    int n_sums, n_all, places;                 // places in `sums`: segments but a node's last, a root's start state
+};
+
+// Whether anything is cut.  As many pieces as run at a time in narrow CTAs (four to a kv-head; of 128 chunks on in wide
+// ones, and where that cuts nothing), 16 at most; two launches of s chunks take as long as 2 s + 4 in one.
+// Measured, us of a call of one node, 8 kv-heads: 16 chunks 27 whole, 25.5 in 4 pieces, 28.6 in 2; 24 chunks
+// 37 and 33 (4); 40 chunks 62, 49 (4), 53 (7); 63 chunks 92, 69 (4), 73 (9); 235 chunks 306, 212 (4), 193 (9), 222 (16).
+// Of 2 kv-heads 16 chunks 26 and 22 (4); 40 chunks 56, 41 (5), 37 (10); 235 chunks 290, 147 (9), 135 (16), 153 (20).
+bool split_depth(const LinInfo& X, size_t l, int32_t hkv, int32_t place0, Split& out) {
+    const int32_t lo = X.lvl_ptr[l], m = X.lvl_ptr[l + 1] - lo;
+    if (m > kSplitNodes) return false;
+    int64_t total = 0;
+    for (int32_t i = 0; i < m; ++i) total += X.lnodes[4 * (size_t)X.lvl_nodes[lo + i] + 2];
+    const int narrow = 152 / (4 * hkv), wide = 152 / (2 * hkv);
+    for (const int n : {total < 128 && m <= narrow ? narrow : 0, wide}) {
+        out.n_sums = out.n_all = out.places = 0;
+        for (int32_t i = 0; i < m; ++i) {
+            const int32_t k = X.lvl_nodes[lo + i], c = X.lnodes[4 * (size_t)k + 2];
+            int64_t pieces = std::min<int64_t>(c * (int64_t)std::min(n, kSplitWalks) / total, c / 4);
+            int32_t s = pieces > 1 ? (int32_t)((c + pieces - 1) / pieces) : c;
+            if (2 * s + 4 >= c) s = c;
+            const int32_t whole = (c - 1) / s;
+            for (int32_t t = 0; t <= whole; ++t) {
+                const Walk w = {k, t * s, std::min(s, c - t * s), place0 + out.places, s};
+                if (t < whole) out.sums[out.n_sums++] = w;
+                out.all[out.n_all++] = w;
+            }
+            out.places += whole + (whole > 0 && X.lnodes[4 * (size_t)k] < 0);
+        }
+        if (out.n_sums) return true;
+    }
+    return false;
+}
+
 struct Ws {
     size_t s_in, s_out, sums, total;
 };
 Ws layout(const tree_attn_plan_s* P, int32_t hkv) {
     const size_t nc = P->lin.chunks.size() / 4, per = (size_t)hkv * kD * kD;
     const size_t s_out = nc * per * 2, sums = s_out + (size_t)P->n_nodes * per * 4;
-    return {0, s_out, sums, sums + (size_t)P->lin.n_segments * per * 4};
+    int places = 0;                            // (the depths take turns)
+    for (size_t l = 0; l + 1 < P->lin.lvl_ptr.size(); ++l) {
+        Split x;
+        if (split_depth(P->lin, l, hkv, 0, x)) places = std::max(places, x.places);
+    }
+    return {0, s_out, sums, sums + (size_t)places * per * 4};
 }
 
 }  // namespace
@@ -756,22 +829,27 @@ int tree_attn_linear_prefill(tree_attn_plan_t P, const void* q, const void* k, c
     const Ws w = layout(P, hkv);
     if (!workspace || ws_bytes < w.total) return TREE_ATTN_ERR_WORKSPACE;
     const int64_t nc = (int64_t)(P->lin.chunks.size() / 4);
-    if (nc * hq > INT32_MAX || nc * kChunk > INT32_MAX || nc * hkv * 2 > INT32_MAX) return TREE_ATTN_ERR_TOO_LARGE;
+    if (nc * hq > INT32_MAX || nc * kChunk > INT32_MAX || nc * hkv * 4 > INT32_MAX) return TREE_ATTN_ERR_TOO_LARGE;
     int dev, *status;
     if ((st = current_device(&dev)) || (st = get_status_ptr(dev, &status))) return st;
     char* ws = static_cast<char*>(workspace);
     void* s_in = ws + w.s_in;
-    CUtensorMap tq, tk, tv, ts, ts32, to32;
+    CUtensorMap tq, tk, tv, tv32, ts, ts32, to32;
     if ((st = make_tensor_map(&tq, q, P->N, hq, d)) || (st = make_tensor_map(&tk, k, P->N, hkv, d)) ||
         (st = make_tensor_map(&tv, v, P->N, hkv, d)) || (st = make_tensor_map(&ts, s_in, nc * kChunk, hkv, d)) ||
-        (st = make_tensor_map_plain(&ts32, s_in, nc * kChunk, hkv, d, 32, 32)) ||
+        (st = make_tensor_map_cols(&ts32, s_in, nc * kChunk, hkv, d, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE)) ||
+        (st = make_tensor_map_cols(&tv32, v, P->N, hkv, d, 32, kChunk, CU_TENSOR_MAP_SWIZZLE_64B)) ||
         (st = make_tensor_map_rows(&to32, o, P->N, hq, d, 32)))
         return st;
     static std::once_flag once[kMaxDevices];
     static cudaError_t set[kMaxDevices];
     static int sms[kMaxDevices];
     std::call_once(once[dev], [&] {
-        set[dev] = launched(cudaFuncSetAttribute(prefill_state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStateSmem));
+        set[dev] = launched(cudaFuncSetAttribute(prefill_state_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 StateLayout<64>::kSmem));
+        if (set[dev] == cudaSuccess)
+            set[dev] = launched(cudaFuncSetAttribute(prefill_state_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     StateLayout<32>::kSmem));
         if (set[dev] == cudaSuccess)
             set[dev] = launched(cudaFuncSetAttribute(prefill_out_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOutSmem));
         if (cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms[dev] <= 0) sms[dev] = 1;
@@ -779,27 +857,53 @@ int tree_attn_linear_prefill(tree_attn_plan_t P, const void* q, const void* k, c
     if (set[dev] != cudaSuccess) return TREE_ATTN_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const LinInfo& X = P->lin;
-    int leads = 1;
-    for (size_t l = 0; l + 1 < X.lvl_ptr.size(); ++l)
-        for (int adding = 1; adding >= 0; --adding) {
-            const int32_t *range = &X.job_ptr[2 * l + (adding ? 0 : 1)], jobs = range[1] - range[0];
-            if (!jobs) continue;
-            const StateParams p = {reinterpret_cast<const int4*>(D->lin_jobs) + range[0], D->lnodes, D->kids, D->chunks, decay,
-                                   reinterpret_cast<float*>(ws + w.s_out), reinterpret_cast<float*>(ws + w.sums), hkv,
-                                   P->n_nodes, (int32_t)nc, l == 0, X.segment[l], adding, leads,
-                                   {states, slot_in, slot_out, D->lin_ids, n_slots, status}};
-            leads = 0;
-            if (launch_pdl(prefill_state_kernel, dim3((unsigned)((int64_t)jobs * hkv * 2)), dim3(kStateThreads), kStateSmem, s, tk,
-                           tv, ts32, p) != cudaSuccess)
-                return TREE_ATTN_ERR_CUDA;
+    StateParams p = {};
+    p.lnodes = D->lnodes;
+    p.kids = D->kids;
+    p.chunks = D->chunks;
+    p.decay = decay;
+    p.s_out = reinterpret_cast<float*>(ws + w.s_out);
+    p.sums = reinterpret_cast<float*>(ws + w.sums);
+    p.hkv = hkv;
+    p.n_nodes = P->n_nodes;
+    p.n_chunks = (int32_t)nc;
+    p.leads = 1;
+    p.io = {states, slot_in, slot_out, D->lin_ids, n_slots, status};
+    auto walk = [&](int jobs) {
+        // where they all run at a time, CTAs of 32 value features: a chunk takes them less long
+        const bool narrow = (int64_t)jobs * hkv * 4 <= sms[dev];
+        const dim3 grid((unsigned)((int64_t)jobs * hkv * (narrow ? 4 : 2)));
+        const cudaError_t e =
+            narrow ? launch_pdl(prefill_state_kernel<32>, grid, dim3(kStateThreads), StateLayout<32>::kSmem, s, tk, tv32, ts32, p)
+                   : launch_pdl(prefill_state_kernel<64>, grid, dim3(kStateThreads), StateLayout<64>::kSmem, s, tk, tv, ts32, p);
+        p.leads = 0;
+        return e == cudaSuccess;
+    };
+    for (size_t l = 0; l + 1 < X.lvl_ptr.size(); ++l) {
+        p.first_depth = l == 0;
+        Split x;
+        bool sent;
+        if (split_depth(X, l, hkv, 0, x)) {
+            p.order = nullptr;
+            p.adding = 1;
+            std::copy(x.sums, x.sums + x.n_sums, p.walks);
+            sent = walk(x.n_sums);
+            p.adding = 0;
+            std::copy(x.all, x.all + x.n_all, p.walks);
+            sent = sent && walk(x.n_all);
+        } else {
+            p.order = D->lvl_nodes + X.lvl_ptr[l];
+            sent = walk(X.lvl_ptr[l + 1] - X.lvl_ptr[l]);
         }
+        if (!sent) return TREE_ATTN_ERR_CUDA;
+    }
     // about one CTA per SM
     const int G = hq / hkv, lanes = std::max(1, sms[dev] / hkv);
     const int left = (int)(nc % lanes) * G, share = (left + lanes - 1) / lanes;
     const int used = nc >= lanes ? lanes : (left + share - 1) / share;
-    const OutParams p = {D->chunks, decay, static_cast<uint16_t*>(o), (int32_t)nc, lanes, share, hq, hkv, scale, status};
+    const OutParams po = {D->chunks, decay, static_cast<uint16_t*>(o), (int32_t)nc, lanes, share, hq, hkv, scale, status};
     const cudaError_t e = launch_pdl(prefill_out_kernel, dim3((unsigned)(used * hkv)), dim3(kThreads), kOutSmem, s,
-                                     tq, tk, tv, ts, to32, p);
+                                     tq, tk, tv, ts, to32, po);
     return e == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA;
 }
 

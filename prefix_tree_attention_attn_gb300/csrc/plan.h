@@ -47,7 +47,6 @@ struct DevicePlan {
     int32_t* lvl_nodes = nullptr;  // packed nodes by depth (LinInfo::lvl_ptr gives each depth's range)
     int32_t* kids = nullptr;       // [n_nodes+1] child offsets, then the children in packed order
     int32_t* lin_ids = nullptr;    // [n_nodes] node id of each packed node
-    int32_t* lin_jobs = nullptr;   // LinInfo::jobs, 16-byte aligned
     bool lin_ready = false;
 };
 
@@ -58,12 +57,6 @@ struct LinInfo {
     std::vector<int32_t> lvl_ptr;  // [depths+1] ranges of lvl_nodes
     std::vector<int32_t> lvl_nodes;
     std::vector<int32_t> kids;     // as DevicePlan::kids
-    // Walks of the prefill's states: for each depth the segments whose sums are taken first, then all
-    // segments, {packed node, first of its chunks, chunks, its first segment's number among those summed}.
-    std::vector<int32_t> jobs;
-    std::vector<int32_t> job_ptr;  // [2*depths+1] ranges of jobs
-    std::vector<int32_t> segment;  // [depths] chunks of a segment but a node's last
-    int32_t n_segments = 0;        // that are summed
     bool ready = false;
 };
 
@@ -125,8 +118,9 @@ int current_device(int* dev);
 int make_tensor_map(CUtensorMap* m, const void* base, int64_t rows, int heads, int d);
 // The same with boxes of box_rows rows.
 int make_tensor_map_rows(CUtensorMap* m, const void* base, int64_t rows, int heads, int d, int box_rows);
-// The same with boxes of box_cols features x 1 head x box_rows rows, not swizzled.
-int make_tensor_map_plain(CUtensorMap* m, const void* base, int64_t rows, int heads, int d, int box_cols, int box_rows);
+// The same with boxes of box_cols features x 1 head x box_rows rows, swizzled as told.
+int make_tensor_map_cols(CUtensorMap* m, const void* base, int64_t rows, int heads, int d, int box_cols, int box_rows,
+                         CUtensorMapSwizzle swizzle);
 // TMA map of [rows, 128] bytes: boxes of box_rows whole rows, 128-byte swizzle.
 int make_byte_map(CUtensorMap* m, const void* base, int64_t rows, int box_rows);
 // Chunk tables of the linear attention: on the current device (uploaded once), or on the host alone.

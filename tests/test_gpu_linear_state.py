@@ -111,13 +111,26 @@ def test_prefill_deep_tree(cuda_device):
 
 @pytest.mark.parametrize("seg,kept", [([12 * 128 + 1], [0]), ([3500], [2]), ([2100, 40, 1540, 1537], [0, -1, 3, 4]), ([1536, 4608], [5, 6])])
 def test_prefill_in_segments(cuda_device, seg, kept):
+    # four: a long root, a short and two long children
+    check_segments([-1, 0, 0, 0] if len(seg) == 4 else [-1] + list(range(len(seg) - 1)), seg, kept, 2, cuda_device)
+
+
+@pytest.mark.parametrize("hkv", [1, 4, 8, 16])
+@pytest.mark.parametrize("parent,seg,kept", [
+    ([-1], [14 * 128], [0]), ([-1], [15 * 128 - 3], [7]), ([-1], [2048], [7]), ([-1], [5000], [1]), ([-1], [131 * 128 - 7], [2]),
+    ([-1] + [0] * 8, [300] + [2000] * 3 + [1, 2, 127, 128, 129], [-1, 0, 1, 2, 3, 4, 5, 6, -1]),
+    ([-1] + [0] * 9, [2500] + [1000] * 9, [0, 1, 2, 3, 4, 5, 6, -1, -1, -1]),
+    ([-1, -1, 0, 1], [3000, 2200, 1, 4000], [-1, 1, 2, 0])])
+def test_prefill_in_pieces(cuda_device, parent, seg, kept, hkv):
+    """The numbers of heads and of chunks around which nodes are cut and walks get narrow, some states over the one that
+    their root came from."""
+    check_segments(parent, seg, kept, hkv, cuda_device)
+
+
+def check_segments(parent, seg, kept, hkv, cuda_device):
     """Nodes long enough to be walked in segments: against the same tokens as a chain of short nodes, whose
     states are handed on node by node."""
-    if len(seg) == 4:                                       # a long root, a short and two long children
-        parent, chain = [-1, 0, 0, 0], None
-    else:
-        parent = [-1] + list(range(len(seg) - 1))
-    n_slots, hq, hkv, N = 8, 4, 2, sum(seg)
+    n_slots, hq, N = 8, 2 * hkv, sum(seg)
     q, k, v = draw(51, N, hq, hkv, 128, cuda_device)
     dec = decays(hkv, cuda_device, (0.999, 1.0))
     first = randn((n_slots, hkv, 128, 128), cuda_device)
@@ -131,7 +144,7 @@ def test_prefill_in_segments(cuda_device, seg, kept):
             out.append(kept[u] if x + 640 >= L else -1)
         tip[u] = len(short) - 1
     o2 = TL.tree_linear_prefill(TreePlan(up, short), b, TL.StateSlots([7] + [-1] * (len(short) - 1), out, n_slots), q, k, v, dec, 0.1)
-    # sums of fewer than 64 chunks in another order, 2^-13 of the magnitudes as above: here 2^-18 of the largest
+    # sums of at most 131 chunks in another order, 2^-13 of the magnitudes as above: here 2^-18 of the largest
     # state of N(0, 1) products, and outputs one rounding of the entering state, of P and of o apart
     assert (a - b).abs().max() <= 2.0 ** -18 * N
     assert (o.float() - o2.float()).abs().max() <= 2.0 ** -7 * o.float().abs().max()
