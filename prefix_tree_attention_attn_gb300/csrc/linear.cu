@@ -590,6 +590,12 @@ int build_lin(tree_attn_plan_s* P) {
         for (int32_t l = 0; l < n_depths; ++l)
             std::stable_sort(X.lvl_nodes.begin() + X.lvl_ptr[l], X.lvl_nodes.begin() + X.lvl_ptr[(size_t)l + 1],
                              [&](int32_t a, int32_t b) { return X.lnodes[4 * (size_t)a + 2] > X.lnodes[4 * (size_t)b + 2]; });
+        X.walks.clear();
+        for (const int32_t k : X.lvl_nodes) {
+            const int32_t *node = &X.lnodes[4 * (size_t)k], *last = &X.chunks[4 * (size_t)(node[1] + node[2] - 1)];
+            X.walks.insert(X.walks.end(), {k, node[0], node[1], node[2], X.chunks[4 * (size_t)node[1]], last[1],
+                                           X.kids[(size_t)k + 1] > X.kids[k], P->node_order[k]});
+        }
         X.ready = true;
     } catch (const std::bad_alloc&) {
         return TREE_ATTN_ERR_OUT_OF_MEMORY;
@@ -607,8 +613,9 @@ int ensure_lin_device(tree_attn_plan_s* P, DevicePlan** out) {
     if (!D.lin_ready) {
         const size_t a = (P->lin.chunks.size() + 63) / 64 * 64, b = P->lin.lnodes.size(),
                      c = P->lin.lvl_nodes.size(), k = P->lin.kids.size();
-        std::vector<int32_t> h(a + b + c + k + P->node_order.size(), 0);
-        std::copy(P->node_order.begin(), P->node_order.end(), h.begin() + a + b + c + k);
+        const size_t w = (a + b + c + k + 3) / 4 * 4;   // int4
+        std::vector<int32_t> h(w + P->lin.walks.size(), 0);
+        std::copy(P->lin.walks.begin(), P->lin.walks.end(), h.begin() + w);
         std::copy(P->lin.chunks.begin(), P->lin.chunks.end(), h.begin());
         std::copy(P->lin.lnodes.begin(), P->lin.lnodes.end(), h.begin() + a);
         std::copy(P->lin.lvl_nodes.begin(), P->lin.lvl_nodes.end(), h.begin() + a + b);
@@ -620,7 +627,7 @@ int ensure_lin_device(tree_attn_plan_s* P, DevicePlan** out) {
         D.lnodes = static_cast<int32_t*>(buf) + a;
         D.lvl_nodes = static_cast<int32_t*>(buf) + a + b;
         D.kids = static_cast<int32_t*>(buf) + a + b + c;
-        D.lin_ids = static_cast<int32_t*>(buf) + a + b + c + k;
+        D.lin_walks = static_cast<int32_t*>(buf) + w;
         D.lin_ready = true;
     }
     *out = &D;

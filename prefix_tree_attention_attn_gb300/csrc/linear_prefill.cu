@@ -54,14 +54,13 @@ struct SlotIO {
     float* states;             // [n_slots, hkv, d, d]
     const int32_t* in;         // by node id, -1: a zero state; or null
     const int32_t* out;        // by node id, -1: not kept; or null
-    const int32_t* ids;        // node id of each packed node
     int32_t n_slots;
     int* status;
 };
 
-// The node's slot in a table, or -1; numbers outside the pool say so and count as -1.
-__device__ __forceinline__ int slot_of(const SlotIO& io, const int32_t* table, int node) {
-    const int s = table ? table[io.ids[node]] : -1;
+// The slot of a node (its id) in a table, or -1; numbers outside the pool say so and count as -1.
+__device__ __forceinline__ int slot_of(const SlotIO& io, const int32_t* table, int id) {
+    const int s = table ? table[id] : -1;
     if (s < -1 || s >= io.n_slots) {
         report_notice(io.status, TREE_ATTN_ERR_INVALID_SLOT);
         return -1;
@@ -101,19 +100,19 @@ __device__ __forceinline__ uint64_t value_desc(uint32_t at) {
 constexpr int kStateThreads = 576;             // 8 warps hold the state, 8 weigh, loader, MMA
 constexpr int kAhead = 6;                      // chunks that are brought into L2 ahead of their load
 
+// A CTA's walk, the whole of a node or a segment: what it has to know before its first load, in one piece.
+struct Walk {
+    int32_t node, parent, chunk, chunks;       // packed nodes; the walk's first chunk, its chunks
+    int32_t token, end, inner, id;             // its first token, its last chunk's tokens; 1: has children; node id
+    int32_t first, segment, whole, place;      // first of the node's chunks; chunks of a segment but the node's last,
+                                               // segments but the last; the first one's place in `sums`
+};
 // Where a depth has few nodes, the walks go with the launch.
 constexpr int kSplitNodes = 8, kSplitWalks = 16, kMaxWalks = kSplitNodes + kSplitWalks;
-struct Walk {
-    int32_t node, first, chunks;               // packed node, first of its chunks
-    int32_t place, segment;                    // its first segment's place in `sums`, chunks of a segment but its last
-};
 
 struct StateParams {
-    const int32_t* order;      // the depth's packed nodes, a walk each; or null: `walks`
+    const int4* order;         // LinInfo::walks of the depth, a node each; or null: `walks`
     Walk walks[kMaxWalks];
-    const int32_t* lnodes;     // [4*n_nodes] {parent's packed index, first chunk, chunks, ..}
-    const int32_t* kids;       // child offsets
-    const int32_t* chunks;     // [4*n_chunks] {first token, tokens, ..}
     const float* decay;
     float* s_out;              // [n_nodes, hkv, d, d], nodes with children
     float* sums;               // [segments, hkv, d, d] what a segment adds to the state; behind a root's, its start state
@@ -138,6 +137,21 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         if (threadIdx.x == 0) report_status(status, -5);
         return;
     }
+    const int part = blockIdx.x % kParts, g = blockIdx.x / kParts % p.hkv;
+    Walk job;
+    if (p.order) {
+        const int4* w = p.order + 2 * (blockIdx.x / kParts / p.hkv);
+        const int4 a = w[0], b = w[1];
+        job = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, 0, a.w, 0, 0};
+    } else {
+        job = p.walks[blockIdx.x / kParts / p.hkv];
+    }
+    // (the loads are under way while the barriers are set up)
+    const int node = job.node, n = job.chunks, c0 = job.chunk, end = job.end, whole = job.whole;
+    bool ok = ta_ok(status, 620, node, 0, p.n_nodes) && ta_ok(status, 621, c0, 0, p.n_chunks) &&
+              ta_ok(status, 622, c0 + n, 0, p.n_chunks + 1) && ta_ok(status, 623, job.parent, -1, p.n_nodes);
+    const int par = ok ? job.parent : -1;
+    const bool last = job.first == whole * job.segment, inner = last && job.inner;
     auto kfull = [&](int s) { return sb + 8u * s; };          // K of stage s has come
     auto kfree = [&](int s) { return sb + 16 + 8u * s; };     // and has been multiplied
     auto vfull = [&](int s) { return sb + 32 + 8u * s; };
@@ -168,24 +182,6 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + 144);
-    const int part = blockIdx.x % kParts, g = blockIdx.x / kParts % p.hkv;
-    Walk job;
-    bool ok;
-    if (p.order) {
-        job = {p.order[blockIdx.x / kParts / p.hkv], 0, 0, 0, INT32_MAX / kChunk};
-        ok = ta_ok(status, 620, job.node, 0, p.n_nodes);
-        if (ok) job.chunks = p.lnodes[4 * job.node + 2];
-    } else {
-        job = p.walks[blockIdx.x / kParts / p.hkv];
-        ok = ta_ok(status, 620, job.node, 0, p.n_nodes);
-    }
-    const int node = job.node, n = job.chunks;
-    const int par = ok ? p.lnodes[4 * node] : -1, c0 = ok ? p.lnodes[4 * node + 1] + job.first : 0;
-    ok = ok && ta_ok(status, 621, c0, 0, p.n_chunks) && ta_ok(status, 622, c0 + n, 0, p.n_chunks + 1);
-    const bool last = ok && job.first + n == p.lnodes[4 * node + 2];
-    const int whole = ok ? (p.lnodes[4 * node + 2] - 1) / job.segment : 0;   // segments of the node but its last
-    const bool inner = last && p.kids[node + 1] > p.kids[node];
-    const int end = ok ? p.chunks[4 * (c0 + n - 1) + 1] : 0;   // tokens of the last chunk; the others have 128
     auto tokens = [&](int i) { return i == n - 1 ? end : kChunk; };
     if (p.leads) grid_dep_wait();
     grid_dep_launch();
@@ -193,7 +189,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     // (once per kv-head; the call's outputs are then undefined)
     if (p.first_depth && blockIdx.x < kParts * p.hkv && part == 0 && threadIdx.x == 0 && !(gamma > 0.f && gamma <= 1.f))
         report_notice(status, TREE_ATTN_ERR_INVALID_DECAY);
-    const int to = last ? slot_of(p.io, p.io.out, node) : -1;
+    const int to = ok && last ? slot_of(p.io, p.io.out, job.id) : -1;
     const int steps = !ok ? 0 : p.adding || inner || to >= 0 ? n : n - 1;   // increments that anything needs
 
     if (warp < F / 8) {
@@ -201,7 +197,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         const int quarter = warp & 3, row = 32 * quarter + lane, col0 = part * F + 32 * (warp >> 2);
         const size_t at = (size_t)g * kD * kD + (size_t)row * kD + col0;
         float S[32];
-        const int from = ok && par < 0 ? slot_of(p.io, p.io.in, node) : -1;
+        const int from = ok && par < 0 ? slot_of(p.io, p.io.in, job.id) : -1;
         if (!p.leads) grid_dep_wait();
         const float* src = par >= 0 ? p.s_out + (size_t)par * p.hkv * kD * kD + at
                            : from >= 0 ? p.io.states + (size_t)from * p.hkv * kD * kD + at : nullptr;
@@ -337,14 +333,14 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         if (lane == 0) {
             auto prefetch = [&](int i) {
                 if (i >= steps) return;
-                const int off = p.chunks[4 * (c0 + i)];
+                const int off = job.token + i * kChunk;
                 for (int blk = 0; blk < 2; ++blk) tma_prefetch_3d(&tm_k, blk * 64, g, off);
                 tma_prefetch_3d(&tm_v, part * F, g, off);
             };
             for (int i = kKStages; i < kAhead; ++i) prefetch(i);
             int sent = 0;
             for (int i = 0; i < steps && ok; ++i) {
-                const int s = i % kVStages, sk = i % kKStages, off = p.chunks[4 * (c0 + i)];
+                const int s = i % kVStages, sk = i % kKStages, off = job.token + i * kChunk;
                 if (i >= kVStages) ok = mbar_wait(vfree(s), (i / kVStages - 1) & 1, status, 124);
                 if (!ok) break;
                 mbar_expect_tx(vfull(s), Lay::kV);
@@ -407,8 +403,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 // issues.  A warp's 32 x 64 outputs leave by one bulk store out of shared memory (from registers, 16 bytes of 32
 // different rows at a time, they kept the store unit busy for 2,000 cycles of a unit).
 // A unit takes 3,900 cycles: 3,200 of tensor products, 3,500 of the mask, the weights and the roundings, 3,300 of
-// memory at 64 / 8 heads, beside one another.  480,408 tokens of 64 / 8 heads in 123 nodes: 3.84 ms with the states,
-// 4.6 TB/s of what has to be read and written; 8,835 of 32 / 8 heads in 17 nodes 79 us; one turn of 777 16.5 us.
+// memory at 64 / 8 heads, beside one another.  480,408 tokens of 64 / 8 heads in 123 nodes: 3.83 ms with the states,
+// 4.6 TB/s of what has to be read and written; 8,835 of 32 / 8 heads in 17 nodes 77 us; one turn of 777 16.5 us.
 constexpr int kOutK = 2048, kOutV = kOutK + kTile, kOutS = kOutV + kTile, kOutQ = kOutS + kTile, kQSlots = 3,
               kOutStage = kOutQ + kQSlots * kTile, kOutSmem = kOutStage + kTile;
 
@@ -754,7 +750,7 @@ struct Split {
 // Measured, us of a call of one node, 8 kv-heads: 16 chunks 27 whole, 25.5 in 4 pieces, 28.6 in 2; 24 chunks
 // 37 and 33 (4); 40 chunks 62, 49 (4), 53 (7); 63 chunks 92, 69 (4), 73 (9); 235 chunks 306, 212 (4), 193 (9), 222 (16).
 // Of 2 kv-heads 16 chunks 26 and 22 (4); 40 chunks 56, 41 (5), 37 (10); 235 chunks 290, 147 (9), 135 (16), 153 (20).
-bool split_depth(const LinInfo& X, size_t l, int32_t hkv, int32_t place0, Split& out) {
+bool split_depth(const LinInfo& X, size_t l, int32_t hkv, Split& out) {
     const int32_t lo = X.lvl_ptr[l], m = X.lvl_ptr[l + 1] - lo;
     if (m > kSplitNodes) return false;
     int64_t total = 0;
@@ -769,7 +765,9 @@ bool split_depth(const LinInfo& X, size_t l, int32_t hkv, int32_t place0, Split&
             if (2 * s + 4 >= c) s = c;
             const int32_t whole = (c - 1) / s;
             for (int32_t t = 0; t <= whole; ++t) {
-                const Walk w = {k, t * s, std::min(s, c - t * s), place0 + out.places, s};
+                const int32_t* node = &X.walks[8 * (size_t)(lo + i)];
+                const Walk w = {k, node[1], node[2] + t * s, std::min(s, c - t * s), node[4] + t * s * kChunk,
+                                t < whole ? kChunk : node[5], node[6], node[7], t * s, s, whole, out.places};
                 if (t < whole) out.sums[out.n_sums++] = w;
                 out.all[out.n_all++] = w;
             }
@@ -789,7 +787,7 @@ Ws layout(const tree_attn_plan_s* P, int32_t hkv) {
     int places = 0;                            // (the depths take turns)
     for (size_t l = 0; l + 1 < P->lin.lvl_ptr.size(); ++l) {
         Split x;
-        if (split_depth(P->lin, l, hkv, 0, x)) places = std::max(places, x.places);
+        if (split_depth(P->lin, l, hkv, x)) places = std::max(places, x.places);
     }
     return {0, s_out, sums, sums + (size_t)places * per * 4};
 }
@@ -858,9 +856,6 @@ int tree_attn_linear_prefill(tree_attn_plan_t P, const void* q, const void* k, c
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const LinInfo& X = P->lin;
     StateParams p = {};
-    p.lnodes = D->lnodes;
-    p.kids = D->kids;
-    p.chunks = D->chunks;
     p.decay = decay;
     p.s_out = reinterpret_cast<float*>(ws + w.s_out);
     p.sums = reinterpret_cast<float*>(ws + w.sums);
@@ -868,7 +863,7 @@ int tree_attn_linear_prefill(tree_attn_plan_t P, const void* q, const void* k, c
     p.n_nodes = P->n_nodes;
     p.n_chunks = (int32_t)nc;
     p.leads = 1;
-    p.io = {states, slot_in, slot_out, D->lin_ids, n_slots, status};
+    p.io = {states, slot_in, slot_out, n_slots, status};
     auto walk = [&](int jobs) {
         // where they all run at a time, CTAs of 32 value features: a chunk takes them less long
         const bool narrow = (int64_t)jobs * hkv * 4 <= sms[dev];
@@ -883,7 +878,7 @@ int tree_attn_linear_prefill(tree_attn_plan_t P, const void* q, const void* k, c
         p.first_depth = l == 0;
         Split x;
         bool sent;
-        if (split_depth(X, l, hkv, 0, x)) {
+        if (split_depth(X, l, hkv, x)) {
             p.order = nullptr;
             p.adding = 1;
             std::copy(x.sums, x.sums + x.n_sums, p.walks);
@@ -892,7 +887,7 @@ int tree_attn_linear_prefill(tree_attn_plan_t P, const void* q, const void* k, c
             std::copy(x.all, x.all + x.n_all, p.walks);
             sent = sent && walk(x.n_all);
         } else {
-            p.order = D->lvl_nodes + X.lvl_ptr[l];
+            p.order = reinterpret_cast<const int4*>(D->lin_walks) + 2 * (size_t)X.lvl_ptr[l];
             sent = walk(X.lvl_ptr[l + 1] - X.lvl_ptr[l]);
         }
         if (!sent) return TREE_ATTN_ERR_CUDA;

@@ -46,7 +46,7 @@ struct DevicePlan {
                                    //   1 if the last child of its parent}
     int32_t* lvl_nodes = nullptr;  // packed nodes by depth (LinInfo::lvl_ptr gives each depth's range)
     int32_t* kids = nullptr;       // [n_nodes+1] child offsets, then the children in packed order
-    int32_t* lin_ids = nullptr;    // [n_nodes] node id of each packed node
+    int32_t* lin_walks = nullptr;  // LinInfo::walks, 16-byte aligned
     bool lin_ready = false;
 };
 
@@ -57,6 +57,9 @@ struct LinInfo {
     std::vector<int32_t> lvl_ptr;  // [depths+1] ranges of lvl_nodes
     std::vector<int32_t> lvl_nodes;
     std::vector<int32_t> kids;     // as DevicePlan::kids
+    // [8*n_nodes] for each of lvl_nodes {packed node, parent's or -1, first chunk, chunks, first token, the last
+    // chunk's tokens, 1 with children, node id}
+    std::vector<int32_t> walks;
     bool ready = false;
 };
 
