@@ -3,7 +3,8 @@
 // A copy: every byte read once and written once.  The page numbers and the caches' addresses go
 // with the launch (kernel parameters hold 32 KB), so nothing is uploaded and the host's arrays are
 // its own again when the call returns.  A CTA copies 16 KB of one page of one cache, four 16-byte
-// loads under way in each thread; the CTA of a page's first piece takes its scales along.
+// loads under way in each thread; the CTA of a page's first piece takes its scales along.  2,000 pages of
+// 131 KB: 82 us, 0.95 of the measured copy's rate; 16 pages in each of 32 caches 18.6 (of 25 to 31 that a call takes the host).
 #include <cuda_runtime.h>
 
 #include <algorithm>

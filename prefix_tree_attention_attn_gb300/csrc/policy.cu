@@ -1010,7 +1010,7 @@ struct Shape {
 Shape shape_of(int64_t vocab, bool grad) {
     const int64_t vectors = (vocab + 7) / 8 + 1;    // (a row may start inside a vector)
     Shape f = {1, 0, {2, 1, 3, 1, 0}};
-    while (f.C < 8 && (vectors + f.C - 1) / f.C * 16 > 76 * 1024) f.C *= 2;
+    while (f.C < 8 && (vectors + f.C - 1) / f.C * 16 > (kShared - kRing0) / 3) f.C *= 2;
     Split& s = f.split;
     s.slot_bytes = (int)((vectors + f.C - 1) / f.C * 16);
     int per_sm = 3;

@@ -100,11 +100,8 @@ class StateSlots:
             raise ValueError("slot_out: two states for one slot")
         self.slot_in, self.slot_out, self.n_slots = a.copy(), b.copy(), int(n_slots)
         # a row of a step may read the slot that it writes itself, not another's
-        writer = np.full(n_slots + 1, -1, np.int64)
-        writer[kept] = np.flatnonzero(b >= 0)
-        live = np.flatnonzero((a >= 0) & (b >= 0))
-        of = writer[a[live]]
-        self._rows_apart = bool(((of < 0) | (of == live)).all())
+        live = np.flatnonzero((a >= 0) & (b >= 0) & (a != b))
+        self._rows_apart = not np.isin(a[live], kept).any()
         self._plan = None
         self._on = {}
 

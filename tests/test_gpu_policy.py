@@ -243,6 +243,25 @@ def test_reproducible_and_debug_build(cuda_device):
     assert all(torch.equal(u, v) for u, v in zip(a, b))
 
 
+@pytest.mark.parametrize("V,N", [(300, 3000), (16001, 700), (33000, 900)])
+def test_debug_build_of_many_rows(cuda_device, V, N):
+    """Rows that share slots, with and without the gradient, in the build that checks its bounds."""
+    g = torch.Generator(cuda_device).manual_seed(V)
+    plan = TreePlan([-1, 0, 0], [N - 200, 100, 100])
+    x = torch.randn((N, V), device=cuda_device, generator=g).bfloat16()
+    tok = torch.randint(0, V, (N,), device=cuda_device, generator=g, dtype=torch.int32)
+    adv = torch.tensor([1.0, -2.0], device=cuda_device)
+    call = lambda grad: TL.policy_loss(plan, x, tok, None, adv, entropy_coef=0.1, grad=grad)  # noqa: E731
+    want, alone = call(True), call(False)
+    with B.library(_build.build_library(debug=True)):
+        plan = TreePlan([-1, 0, 0], [N - 200, 100, 100])
+        got, got_alone = call(True), call(False)
+        torch.cuda.synchronize()
+        assert device_status() == 0
+    assert all(torch.equal(u, v) for u, v in zip(got, want)) and all(torch.equal(u, v) for u, v in zip(got_alone[:3], alone[:3]))
+    assert all(torch.equal(u, v) for u, v in zip(alone[:3], want[:3]))
+
+
 def test_on_sampled_tokens(cuda_device):
     """What sampling says of a token is its old log-prob: every ratio is 1, so the loss is minus the mean
     advantage and the gradient that of the log-probs."""

@@ -19,6 +19,7 @@ def test_slots():
     assert apart([0, 1], [0, 1]) and apart([3, 3, 3], [0, 1, 2]) and apart([-1, -1], [0, 1]) and apart([], [])
     assert apart([1, 1], [0, -1]) and apart([0, 1], [-1, 0])           # a padding row reads nothing
     assert not apart([0, 1], [1, 0]) and not apart([0, 0], [0, 1]) and not apart([5, 2], [2, 5])
+    assert apart([2 ** 31 - 2], [0], 2 ** 31 - 1)                      # (nothing of the pool's size on the host)
     a = np.array([0, 1], np.int32)
     s = TL.StateSlots(a, a, 2)
     a[:] = 7
