@@ -130,7 +130,8 @@ int tree_attn_policy_loss_workspace(tree_attn_plan_t plan, size_t* ws_bytes);
  * 1 <= vocab <= 262144; tokens int32 [n_tokens]; loss fp32 [1]; logprobs fp32 [n_pred] and entropy
  * fp32 [n_tokens], either may be NULL; dlogits bf16 [n_tokens] rows of d_stride elements, NULL for the
  * loss alone, or the logits themselves with the same stride (each row is read before it is
- * written); fast where each row's address agrees with the logits' row modulo 16 bytes.  The struct is read during the call.  Log-probs, ratios and sums are fp32 or wider
+ * written); fast where each row's address agrees with the logits' row modulo 16 bytes.  The
+ * struct is read during the call.  Log-probs, ratios and sums are fp32 or wider
  * (whether a ratio lies beyond the clip is decided in pairs of floats); dlogits is
  * rounded once.  Bitwise reproducible, and loss, log-probs and entropies are the same bits with and
  * without dlogits.  workspace: 256-byte aligned, contents ignored; calls that may

@@ -152,8 +152,9 @@ def policy_loss(plan: TreePlan, logits, tokens, old_logprobs, advantages, weight
     ``old_logprobs`` (None: a ratio of 1), ``weights`` (None: 1 / n_pred each; a prediction of
     weight 0 is left out) and ``ref_logprobs``; ``advantages`` per trajectory
     (``subtree_advantage``), or per prediction with ``per_token``.  ``dlogits`` may be the
-    logits themselves (None: a new tensor; its rows are up to 7 elements further apart where the logits' are padded,
-    so that both lie alike in their 16 bytes -- the other way takes four times as long); ``grad=False`` gives the loss, log-probs and entropies alone."""
+    logits themselves (None: a new tensor, whose rows lie up to 7 elements further apart where the
+    logits' are padded: both then lie alike in their 16 bytes, which is four times as fast).
+    ``grad=False`` gives the loss, log-probs and entropies alone."""
     dev = _current_device()
     N = plan.n_tokens
     stride = _check_matrix(logits, "logits", N, dev)
