@@ -52,6 +52,7 @@ constexpr int kShared = 227 * 1024;            // of an SM, and of a CTA at most
 constexpr int64_t kMaxVocab = 262144;
 constexpr float kFar = -1e30f;                 // in place of -inf where it meets a factor 0
 constexpr float kHuge = 0x1p100f;              // beyond this a multiple of a logit may overflow
+constexpr float kNear = 0x1p24f;               // m log2 e is rounded by less than 1 up to here
 
 struct Params {
     const uint16_t* logits;
@@ -599,10 +600,12 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                 };
                 int v = s.first + at;
                 uint4* row_d8 = reinterpret_cast<uint4*>(row_d - s.shift);   // (whole vectors lie as the row's do)
-                if (fabsf(R.m) < kHuge) {
-                    // (one multiply-add for the exponent: off by 2^-24 of m log2 e, far below the rounding to bf16; 20 warps
-                    // hide the latencies of a loop of one vector: 779 us where two a turn took 795)
-                    const uint64_t minus = f32x2(-R.m * kLog2e, -R.m * kLog2e), cg2 = f32x2(R.cg, R.cg);
+                if (fabsf(R.m) <= kNear) {
+                    // One multiply-add for the exponent, x log2 e - mc with mc = m log2 e rounded.  Every exponent of the
+                    // row is then short of the same number, mc - m log2 e (exact: m has 8 bits), which goes into the factors.
+                    // (20 warps hide the latencies of a loop of one vector: 779 us where two a turn took 795)
+                    const float mc = R.m * kLog2e, off = fmaf(-R.m, kLog2e, mc), more = fast_exp2(off), cg = R.cg * more;
+                    const uint64_t minus = f32x2(-mc, -mc), cg2 = f32x2(cg, cg);
                     if (R.ce == 0.f) {
 #pragma unroll 1
                         for (; v < s.last; v += T) {
@@ -624,7 +627,8 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                         // the entropy's term; -inf, where 0 would meet an infinity, as what is 0 all the same
                         const float far = R.m - fmaxf(256.f, fabsf(R.m) * 0x1p-6f);
                         const uint32_t far2 = pack_bf16x2(far, far);
-                        const uint64_t ce2 = f32x2(R.ce, R.ce), rest2 = f32x2(fmaf(-R.ce, R.ts, R.cg), fmaf(-R.ce, R.ts, R.cg));
+                        const float ce = R.ce * more, rest = fmaf(ce, off - R.ts, cg);
+                        const uint64_t ce2 = f32x2(ce, ce), rest2 = f32x2(rest, rest);
 #pragma unroll 1
                         for (; v < s.last; v += T) {
                             const uint4 x = here[v];

@@ -407,3 +407,24 @@ def test_many_rows(cuda_device, V, N, branches):
         e = (got.dlogits[r].double() - want).abs()
         assert (e <= 2.0 ** -8 * want.abs() + 2.0 ** -15 * bound + 1e-38).all(), i
     assert abs(float(got.loss) - loss) <= 2.0 ** -15 * terms
+
+
+@pytest.mark.parametrize("base", [3e2, 5e3, 2e4, 1e5, 1e6, 2.0 ** 24, 3e7, 1e9, 1e20, 1e31])
+@pytest.mark.parametrize("entropy", [0.0, 0.05])
+def test_rows_far_from_zero(cuda_device, base, entropy):
+    """Logits around any number: several largest ones, among them every token that is predicted, the others up to three
+    steps of bf16 below.  A shift changes nothing, and these differences are exact: the same tolerances."""
+    for tree, V in ((([-1], [9]), 700), (MIXED, 700), (STAR40, 90), (([-1, 0, 0], [3, 2, 2]), 21000)):
+        for sign in (1, -1):
+            _, tok, _, adv, w, _ = make(tree, V, 23, zero=0.0)
+            g = np.random.default_rng(abs(int(base) % 1000 + sign))
+            steps = g.integers(0, 4, (len(tok), V)).astype(np.int16)
+            steps[:, tok.numpy()] = 0
+            top = torch.tensor(sign * base).bfloat16()
+            x = (top.view(torch.int16) - sign * torch.from_numpy(steps)).view(torch.bfloat16)
+            near = x.double() - top.double()
+            lp = OLS.traj_logprobs(*tree, near.numpy(), tok)
+            f32 = lambda a: torch.from_numpy(a.astype(np.float32))  # noqa: E731
+            data = [near, tok, f32(lp - g.choice([-0.6, -0.1, 0.0, 0.1, 0.6], len(lp))), adv, w, f32(lp + 0.5 * g.normal(size=len(lp)))]
+            got = run(tree, data, cuda_device, x=x.to(cuda_device), kl_coef=0.05, entropy_coef=entropy)
+            check(tree, data, got, kl_coef=0.05, entropy_coef=entropy)
