@@ -3,7 +3,7 @@
 // prefill_state_kernel, one launch per depth of the tree (roots first): a CTA walks the chunks (128
 // tokens at most) of one node for one kv-head and F of the 128 value features -- the columns of the
 // state do not meet --, with the state in registers:
-//     S_in of the chunk goes out as bf16, the operand of the outputs;  S = gamma^L S + dS,
+//     gamma^64 S_in of the chunk goes out as bf16, the operand of the outputs;  S = gamma^L S + dS,
 //     dS = sum_m gamma^(L-1-m) k_m v_m^T on the tensor cores.
 //   A weighted value has 24 bits; it is split into three bf16 numbers that add up to it, so the
 //   increment is as exact as sums in fp32 are (two would leave 3e-6 of it).  The parts lie side by side in one
@@ -22,11 +22,13 @@
 //   after another).
 //
 // prefill_out_kernel, persistent, a unit (chunk, q-head) after the other: A = Q K^T, then
-//     O = diag(f) (P V + Q S_in),  P[m, m'] = gamma^-(m'+1) A[m, m'] for m' <= m,  f(m) = scale gamma^(m+1).
+//     O = diag(f) (P V + Q gamma^64 S_in),  P[m, m'] = gamma^(64-(m'+1)) A[m, m'] for m' <= m,
+//     f(m) = scale gamma^(m+1-64).
 //   The query is an exact operand of both products and each part of O meets one rounding to
-//   bf16 (P's or S_in's).  gamma^-128 has to stay far from overflow: a decay below 2^(-100/128) = 0.58,
-//   whose state is forgotten within a few tokens, takes P[m, m'] = scale gamma^(m-m') A[m, m'] and diag(f) Q,
-//   rounded to bf16, instead of Q.
+//   bf16 (P's or S_in's; a second part of each would take five products in place of three and twice the states'
+//   bytes).  The powers are counted from the chunk's middle and stay within 2^+-50, so scores times values may
+//   go up to 2^77: a decay below 2^(-100/128) = 0.58, whose state is forgotten within a few tokens, takes
+//   P[m, m'] = scale gamma^(m-m') A[m, m'], S_in as it is and diag(scale gamma^(m+1)) Q, rounded to bf16, instead of Q.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -73,6 +75,10 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+
+// Whether the powers of a decay (its log2) over half a chunk stay within 2^+-50: they are then factors of rows and columns.
+__device__ __forceinline__ bool by_columns(float lg) { return lg > -100.f / kChunk; }
+constexpr int kMiddle = kChunk / 2;            // the powers are counted from here
 
 // The descriptor of a tile `bytes` further on (shared memory ends below 2^18, so the address field holds the sum).
 __device__ __forceinline__ uint64_t further(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
@@ -231,14 +237,17 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             }
         }
         const uint32_t stage = sb + Lay::kOut + warp * 2048, tD = tmem + ((uint32_t)(32 * quarter) << 16) + 32 * (warp >> 2);
-        const float f128 = exp2f((float)kChunk * lg);
+        const float f128 = exp2f((float)kChunk * lg), entering = by_columns(lg) ? exp2f((float)kMiddle * lg) : 1.f;
         for (int i = 0; i < n && ok; ++i) {
             if (!p.adding) {
                 if (lane == 0) bulk_wait_read_all();   // the last one has left
                 __syncwarp();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const uint4 y = pack8(S + 8 * c);
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = entering * S[8 * c + e];
+                    const uint4 y = pack8(x);
                     st_shared_v4(stage + lane * 64 + c * 16, y.x, y.y, y.z, y.w);
                 }
                 fence_proxy_async_smem();
@@ -447,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto b_oe = [&](int b) { return bar(16 + b); };    // O has been read
     auto b_qe = [&](int q) { return bar(18 + q); };    // Q slot q has been read
     const uint32_t ka = sb + kOutK, va = sb + kOutV, sina = sb + kOutS, qa0 = sb + kOutQ;
-    float* ctab = reinterpret_cast<float*>(smem + 1024);   // gamma^-(m'+1), or gamma^t
+    float* ctab = reinterpret_cast<float*>(smem + 1024);   // gamma^(64-(m'+1)), or gamma^t
     if (threadIdx.x == 0) {
         mbar_init(b_k, 1);
         mbar_init(b_v, 1);
@@ -469,8 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 9) tmem_alloc(holder, 512);
     grid_dep_launch();
     const float lg = log2f(p.decay[g]);
-    const bool column = lg > -100.f / 128.f;
-    if (threadIdx.x < 128) ctab[threadIdx.x] = column ? exp2f(-(float)(threadIdx.x + 1) * lg) : exp2f((float)threadIdx.x * lg);
+    const bool column = by_columns(lg);
+    if (threadIdx.x < 128) ctab[threadIdx.x] = exp2f((float)(column ? kMiddle - 1 - (int)threadIdx.x : (int)threadIdx.x) * lg);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -592,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         const int quarter = warp & 3, m = (quarter << 5) + lane, grp = warp >> 2, col0 = grp * 64;
         const uint32_t lane_base = tmem + ((uint32_t)(quarter << 5) << 16);
-        const float fo = p.scale * exp2f((float)(m + 1) * lg);
+        const float fo = p.scale * exp2f((float)(column ? m + 1 - kMiddle : m + 1) * lg);
         const uint32_t stage = sb + kOutStage + warp * 4096;
         // Unit u's output is read after unit u + 1's mask.
         int prev_off = 0, prev_L = 0, prev_h = 0, n = head_of(0), i = 0, q = 0;

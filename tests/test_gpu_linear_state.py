@@ -375,3 +375,23 @@ def test_notices(cuda_device, lib):
                                         ws.numel(), None) == 0
     torch.cuda.synchronize()
     assert device_status() == TL.ERR_INVALID_SLOT and (states == 3).all()
+
+
+@pytest.mark.parametrize("size", [300.0, 30000.0, 1e-9])
+@pytest.mark.parametrize("values", [(0.585, 0.6), (0.65, 0.7), (0.58, 0.9), (0.5, 1.0)])
+def test_prefill_of_large_and_small_inputs(cuda_device, values, size):
+    """Scores and values far from 1: no power of the decay may take what lies between them out of the numbers' range.
+    Bounds relative to the magnitudes, as above."""
+    parent, seg, hq, hkv = [-1, 0, 0], [150, 129, 40], 4, 2
+    N = sum(seg)
+    q, k, v = draw(9, N, hq, hkv, 128, cuda_device, size)
+    dec = decays(hkv, cuda_device, values)
+    states = randn((4, hkv, 128, 128), cuda_device) * size * size
+    start = [num(states[3]), None, None]
+    o = TL.tree_linear_prefill(TreePlan(parent, seg), states, TL.StateSlots([3, -1, -1], [0, 1, 2], 4), q, k, v, dec, 0.088)
+    want, end, mag, mass = OLN.from_states(parent, seg, num(q), num(k), num(v), num(dec), 0.088, start)
+    wide = 2 if min(values) < 0.58 else 1
+    assert torch.isfinite(o).all()
+    assert (np.abs(num(o) - want) <= 2.0 ** -8 * np.abs(want) + (wide * 2.0 ** -8 + 2.0 ** -12) * mag).all()
+    for u in range(3):
+        assert (np.abs(num(states[u]) - end[u]) <= 2.0 ** -13 * mass[u]).all()
