@@ -8,18 +8,20 @@
 //   producer     whether the next row has any weight, and the bulk copy of its slice.
 //   statistics   one or two teams: S = sum 2^a, T = sum 2^a a with a = (x - m) log2 e, m near the maximum, by
 //                thread, warp and CTA; a CTA's three numbers go to every CTA of the cluster by asynchronous
-//                stores that count on a barrier there.
+//                stores that count on a barrier there.  One element stays apart: the target, or the likeliest of
+//                several (1 - p of a token that is nearly certain is the others' share of S, and no difference).
 //   finishers    two warps, a row each in turn: join them, LSE = m + ln S, H = ln S - ln 2 T / S; the row's g_k, a lane
 //                for each prediction where there are at most 32 of one target (inside a segment: one
 //                for each trajectory through it), whose inputs it has loaded rows ahead; their sums.
 //   gradient     2^a (cG + cE (a - T / S)), cG = -sum g / S, cE = entropy_coef ln 2 sum w / S,
-//                rounded once; the target's g_k are added before that.  A row of several
-//                targets gets those elements afterwards (children with the same token id summed in
-//                their order).
+//                rounded once.  The element that stayed apart is g (1 - p) - p (the other targets' sum of g) and its
+//                entropy term from the others' sums; the finishers have it.  A row of several
+//                targets gets the others' elements afterwards, with their g_k added before the rounding (children with
+//                the same token id summed in their order).
 //
 // (With the same warps doing all parts of a row in turn, and five such CTAs on an SM, the chain from
 // a row's load to its gradient set the pace: 1,022 us for 8,835 rows of 152,064 logits, 7,797 of them with
-// weight, where this takes 779, 6.5 TB/s of reads and writes; without the gradient 470.)
+// weight, where this takes 790, 6.4 TB/s of reads and writes; without the gradient 437.)
 //
 // Whether a ratio lies beyond the clip decides a whole gradient, so lp - old is a pair of floats:
 // ln S = k ln 2 + ln f, f near 1, adds no error beyond 3e-8.
@@ -184,22 +186,23 @@ __device__ __forceinline__ float predict(const Params& p, const Row& row, float 
 // What the finisher tells the gradient's warps of a row.
 struct Result {
     float m, ts, cg, ce;                       // maximum, T / S and the two factors
-    float own;                                 // the one target's element
-    int active, y, t0, nt;                     // some weight; the one target's token; targets
+    float own;                                 // the element that stayed apart
+    int active, y, t0, nt;                     // some weight; that element's token; targets
 };
 
 // The ring follows.
 struct Shared {
     uint64_t full[kMaxSlots], empty[kMaxSlots], done[kMaxSlots];
     uint64_t stat[2 * kMaxSlots];              // the cluster's CTAs have sent their sums
-    float4 stats[2 * kMaxSlots][8];            // {m, S, T, target's logit or 0} by CTA
+    float4 stats[2 * kMaxSlots][8];            // {m, S, T of all but one element, that one's logit or -inf} by CTA
     Stat parts[kMaxSlots][kMaxStat];           // by statistics warp
     int parts_in[kMaxSlots];
     uint64_t read[kFinishers];                 // the cluster's finishers have read a row's targets
     uint64_t cta;                              // the gradient's warps have come this far
     struct {
-        int active, y;
+        int active, y;                         // y: the token whose element stays apart
     } meta[kMaxSlots];
+    float apart[kMaxSlots];                    // its logit, in the CTA that has it
     Result result[kMaxSlots];
 };
 constexpr int kRing0 = (sizeof(Shared) + 127) / 128 * 128;
@@ -231,13 +234,21 @@ __device__ __forceinline__ Sums warp_sum(Sums s) {
     return s;
 }
 
+// The same sums against the reference m (far below it they are 0, whatever their exponents add up to).
+__device__ __forceinline__ Stat against(Stat a, float m) {
+    const float d = exponent(a.m, m), e = fast_exp2(d);
+    return {m, a.s * e, e > 0.f ? fmaf(a.s, d, a.t) * e : 0.f};
+}
+
+__device__ __forceinline__ float warp_max(float a) {
+    float m;
+    asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(a));
+    return m;
+}
+
 // The sums of a warp's lanes against their common maximum.
 __device__ __forceinline__ Stat warp_join(Stat a) {
-    Stat r;
-    asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r.m) : "f"(a.m));
-    const float d = exponent(a.m, r.m), e = fast_exp2(d);
-    r.s = a.s * e;
-    r.t = fmaf(a.s, d, a.t) * e;
+    Stat r = against(a, warp_max(a.m));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         r.s += __shfl_xor_sync(0xffffffffu, r.s, o);
@@ -250,6 +261,13 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+
+// Puts a 16-bit word of shared memory in another's place (no other thread is near it).
+__device__ __forceinline__ uint32_t swap_shared_u16(uint32_t addr, uint32_t with) {
+    uint16_t was;
+    asm volatile("ld.shared.u16 %0, [%1];\n\tst.shared.u16 [%1], %2;" : "=h"(was) : "r"(addr), "h"((uint16_t)with) : "memory");
+    return was;
 }
 
 // The address of this CTA's shared memory word in another CTA of the cluster.
@@ -326,11 +344,6 @@ struct Slice {
     // the vector in part that falls to this thread: the last one's, and the one's before it; or -1
     __device__ __forceinline__ int odd(int tid, int T) const {
         return tid == T - 1 && lo < first ? lo : tid == T - 2 && last < hi ? last : -1;
-    }
-    __device__ __forceinline__ float logit(const uint8_t* slot, int y) const {
-        const int v = (y + shift) / 8;
-        return lo16(v >= first && v < last ? *reinterpret_cast<const uint16_t*>(slot + (size_t)(v - lo) * 16 + (y - start(v)) * 2)
-                                           : x[y]);
     }
 };
 
@@ -438,7 +451,24 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                 const uint8_t* here8 = ring + (size_t)slot * f.slot_bytes;
                 const uint4* here = reinterpret_cast<const uint4*>(here8) - s.lo;
                 const uint4 none = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);   // -inf
-                const uint4 rest = odd >= 0 ? s.part(odd) : none;
+                uint4 rest = odd >= 0 ? s.part(odd) : none;
+                // The thread that comes by the element that stays apart takes it out of its vector: -inf, probability 0
+                // (a whole vector in the ring; the gradient has no use for this element either)
+                const int apart = S.meta[slot].y, av = s.owns(apart);
+                if (av >= s.first && av < s.last) {
+                    if (((av - s.first) & (T - 1)) == at)      // (T is a power of two)
+                        S.apart[slot] = lo16(swap_shared_u16(smem_u32(here8) + (av - s.lo) * 16 + (apart - s.start(av)) * 2, 0xff80u));
+                } else if (av >= 0 && av == odd) {
+                    uint32_t u[4] = {rest.x, rest.y, rest.z, rest.w};
+                    const int e = apart - s.start(av);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i == e / 2) {
+                            S.apart[slot] = e & 1 ? hi16(u[i]) : lo16(u[i]);
+                            u[i] = e & 1 ? (u[i] & 0xffffu) | 0xff800000u : (u[i] & 0xffff0000u) | 0xff80u;
+                        }
+                    rest = make_uint4(u[0], u[1], u[2], u[3]);
+                }
                 const bool odds = __any_sync(0xffffffffu, odd >= 0);
                 auto get = [&](int v) { return v < s.last ? here[v] : none; };
                 auto top2 = [&](uint4 x) { return max2_nan(max2_nan(x.x, x.y), max2_nan(x.z, x.w)); };
@@ -536,6 +566,7 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
             }
             // the last of the CTA's warps joins them and sends
             int last = 0;
+            __syncwarp();
             if (lane == 0) {
                 S.parts[slot][mine] = st;
                 __threadfence_block();
@@ -545,12 +576,7 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                 __threadfence_block();
                 const Stat none = {-INFINITY, 0.f, 0.f};
                 st = warp_join(lane < f.stat ? S.parts[slot][lane] : none);
-                float xy = 0.f;
-                if (S.meta[slot].active) {
-                    const Slice s(p, r, me, log_c);
-                    const int y = S.meta[slot].y;
-                    if (s.owns(y) >= 0) xy = s.logit(ring + (size_t)slot * f.slot_bytes, y);
-                }
+                const float xy = S.meta[slot].active && Slice(p, r, me, log_c).owns(S.meta[slot].y) >= 0 ? S.apart[slot] : -INFINITY;
                 if (lane < C)
                     remote_store(at_rank(smem_u32(&S.stats[place][me]), lane), make_float4(st.m, st.s, st.t, xy),
                                  at_rank(smem_u32(&S.stat[place]), lane));
@@ -592,7 +618,7 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
             if (!R.active) {
                 for (int v = s.lo + at; v < s.hi; v += T) store(v, make_uint4(0, 0, 0, 0));
             } else {
-                const int odd = s.odd(at, T), yv = R.nt == 1 ? s.owns(R.y) : -1;
+                const int odd = s.odd(at, T), yv = s.owns(R.y);
                 const uint4* here = reinterpret_cast<const uint4*>(ring + (size_t)slot * f.slot_bytes) - s.lo;
                 auto value = [&](float xv) {
                     const float a = exponent(xv, R.m);
@@ -658,7 +684,7 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                     for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(value(lo16(u[i])), value(hi16(u[i])));
                     store(v < s.last ? v : odd, make_uint4(o[0], o[1], o[2], o[3]));
                 }
-                // the one target's element, over what the same thread has written there
+                // the element that stayed apart, over what the same thread has written there
                 if (yv >= 0 && (yv == odd || (yv >= s.first && yv < s.last && (yv - s.first) % T == at)))
                     row_d[R.y] = (uint16_t)pack_bf16x2(R.own, 0.f);
                 if (R.nt != 1) {
@@ -672,7 +698,7 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                         const int q = p.targets[R.t0 + j].x;
                         if (!ta_ok(p.status, 604, q, 0, p.N)) continue;
                         const int yj = p.tokens[q];
-                        if (s.owns(yj) < 0) continue;
+                        if (s.owns(yj) < 0 || yj == R.y) continue;
                         bool earlier = false;      // another child has the same token: the first one adds them up
                         for (int i = 0; i < j && !earlier; ++i) earlier = p.tokens[p.targets[R.t0 + i].x] == yj;
                         if (earlier) continue;
@@ -718,19 +744,36 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
             if (ok) ok = wait_cluster(smem_u32(&S.stat[place]), (it / n_places) & 1, p.status, 605);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            Stat st = {-INFINITY, 0.f, 0.f};
-            float xy = 0.f;
+            Stat others = {-INFINITY, 0.f, 0.f};
+            float xy = -INFINITY;
             if (lane < C) {
                 const float4 q = S.stats[place][lane];
-                st = {q.x, q.y, q.z};
+                others = {q.x, q.y, q.z};
                 xy = q.w;
             }
-            st = warp_join(st);
+            // both against their common maximum; the sums lie in lanes 0 to 7
+            others = against(others, warp_max(max_nan(others.m, xy)));
+            xy = warp_max(xy);
 #pragma unroll
-            for (int o = 4; o > 0; o >>= 1) xy += __shfl_xor_sync(0xffffffffu, xy, o);   // (lanes 0 to 7)
-            xy = __shfl_sync(0xffffffffu, xy, 0);
-            if (lane == 0) mbar_expect_tx(smem_u32(&S.stat[place]), 16 * C);   // of the place's next row
-            Result R = {0.f, 0.f, 0.f, 0.f, 0.f, active, one.y, info.z, info.w};
+            for (int o = 4; o > 0; o >>= 1) {
+                others.s += __shfl_xor_sync(0xffffffffu, others.s, o);
+                others.t += __shfl_xor_sync(0xffffffffu, others.t, o);
+            }
+            others.s = __shfl_sync(0xffffffffu, others.s, 0);
+            others.t = __shfl_sync(0xffffffffu, others.t, 0);
+            int chosen = one.y;
+            if (active && !single) {           // the producer's choice (its copy has come, or there would be no sums)
+                ok = mbar_wait(smem_u32(&S.full[slot]), turn & 1, p.status, 607);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                chosen = S.meta[slot].y;
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_expect_tx(smem_u32(&S.stat[place]), 16 * C);   // of the place's next row
+                mbar_arrive(smem_u32(&S.empty[slot]));             // nothing more of this row from the slot or the place
+            }
+            Result R = {0.f, 0.f, 0.f, 0.f, 0.f, active, chosen, info.z, info.w};
             if (!active) {
                 if (me == 0) {
                     if (p.logprobs)
@@ -745,8 +788,12 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                 }
             } else {
                 const int V = (int)p.vocab;
-                if (one.y < 0 || one.y >= V) xy = __int_as_float(0x7fc00000);
-                const float ts = st.t / st.s;
+                const bool apart = R.y >= 0 && R.y < V;
+                if (!apart) xy = __int_as_float(0x7fc00000);
+                const float ay = exponent(xy, others.m), ey = apart ? fast_exp2(ay) : 0.f;
+                const Stat st = {others.m, others.s + ey, ey > 0.f ? fmaf(ey, ay, others.t) : others.t};
+                // (1 / S of a row without a distribution is not used)
+                const float each = 1.f / st.s, ts = st.t * each, share = others.s * each, py = ey * each;
                 Row row;
                 row.m = fabsf(st.m) < INFINITY ? st.m : __int_as_float(0x7fc00000);
                 {
@@ -766,6 +813,7 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                 }
                 row.h = row.m == row.m ? fmaf(-kLn2, ts, row.lk + row.ll) : row.m;
                 Sums sum = {0.f, 0.f, 0.f};
+                float beside = 0.f;            // g of other targets than the one whose element stayed apart
                 if (narrow) {
                     float lp = 0.f;
                     if (one.w != 0.f) lp = predict(p, row, one.w, xy, one.old, p.old != nullptr, one.a, one.ref, sum);
@@ -785,7 +833,8 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                         predict_all(p, row, t.y, t.z, xj, lanes ? 0 : lane, lanes ? 1 : 32, me == 0, part);
                         if (!lanes) part = warp_sum(part);
                         if (lanes || lane == 0) {
-                            sum.g += part.g;
+                            if (yj == R.y) sum.g += part.g;
+                            else beside += part.g;
                             sum.w += part.w;
                             sum.loss += part.loss;
                         }
@@ -804,23 +853,24 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                     }
                 }
                 sum = warp_sum(sum);
+                if (!single)
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) beside += __shfl_xor_sync(0xffffffffu, beside, o);
                 if (me == 0 && lane == 0) {
                     p.row_loss[r] = sum.loss;
                     if (p.entropy) p.entropy[r] = row.h;
                 }
                 R.m = row.m;
                 R.ts = ts;
-                R.cg = row.m == row.m ? -p.grad_scale * sum.g / st.s : row.m;
-                R.ce = p.ent != 0.f ? kLn2 * p.grad_scale * p.ent * sum.w / st.s : 0.f;
-                const float a = exponent(xy, row.m);
-                R.own = fast_exp2(a) * fmaf(R.ce, a - ts, R.cg) + p.grad_scale * sum.g;
+                R.cg = row.m == row.m ? -p.grad_scale * (sum.g + beside) * each : row.m;
+                R.ce = p.ent != 0.f ? kLn2 * p.grad_scale * p.ent * sum.w * each : 0.f;
+                // g (1 - p) - p beside + cE 2^a (a - T / S), without the differences of near numbers in it
+                R.own = p.grad_scale * (sum.g * share - beside * py);
+                if (ey > 0.f) R.own = fmaf(R.ce * py, fmaf(ay, others.s, -others.t), R.own);
             }
-            if (lane == 0) {
-                if (f.grad) {
-                    S.result[slot] = R;
-                    mbar_arrive(smem_u32(&S.done[slot]));
-                }
-                mbar_arrive(smem_u32(&S.empty[slot]));
+            if (lane == 0 && f.grad) {
+                S.result[slot] = R;
+                mbar_arrive(smem_u32(&S.done[slot]));
             }
             one = two;
             two = three;
@@ -835,23 +885,60 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
         load_pred(p, lane, one);
         load_pred(p, lane, two);
         load_values(p, cluster0, false, one);
+        // Several targets: a lane's target row, and its token, the same rows ahead.
+        auto target = [&](const Ahead& x) {
+            const int q = x.info.w > 1 && lane < x.info.w ? p.targets[x.info.z + lane].x : -1;
+            return q >= 0 && ta_ok(p.status, 604, q, 0, p.N) ? q : -1;
+        };
+        auto token = [&](int q) { return q >= 0 ? p.tokens[q] : -1; };
+        int y1 = token(target(one)), q2 = target(two);
         int slot = 0, turn = 0, sent = 0;
         for (int64_t r = cluster0; r < p.N; r += clusters) {
             Ahead four;
             load_info(p, r + 3 * clusters, four);
             load_pred(p, lane, three);
+            const int q3 = target(three);
             load_values(p, r + clusters, false, two);
+            const int y2 = token(q2);
             const bool active = has_weight(p, lane, one);
+            int apart = one.y;
+            if (active && one.info.w > 1) {
+                // the likeliest, of equals the lowest token: the only one whose p may be above 1/2
+                const uint16_t* x = p.logits + r * p.stride;
+                float best = -INFINITY;
+                for (int j = lane, y = y1; j < one.info.w; j += 32) {
+                    if (j >= 32) {
+                        const int q = p.targets[one.info.z + j].x;
+                        y = ta_ok(p.status, 604, q, 0, p.N) ? p.tokens[q] : -1;
+                    }
+                    if (y < 0 || y >= p.vocab) continue;
+                    const float xj = lo16(x[y]);
+                    if (apart < 0 || xj > best || (xj == best && y < apart)) {
+                        best = xj;
+                        apart = y;
+                    }
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    const float xj = __shfl_xor_sync(0xffffffffu, best, o);
+                    const int y = __shfl_xor_sync(0xffffffffu, apart, o);
+                    if (y >= 0 && (apart < 0 || xj > best || (xj == best && y < apart))) {
+                        best = xj;
+                        apart = y;
+                    }
+                }
+            }
             if (turn > 0) ok = mbar_wait(smem_u32(&S.empty[slot]), (turn - 1) & 1, p.status, 601);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (lane == 0) {
                 S.meta[slot].active = active;
-                S.meta[slot].y = one.y;
+                S.meta[slot].y = apart;
                 const uint32_t bar = smem_u32(&S.full[slot]);
                 const Slice s(p, r, me, log_c);
                 const uint32_t bytes = (uint32_t)(s.last - s.first) * 16;
                 if (active && bytes) {
+                    fence_proxy_async_smem();  // a thread may have written to the slot, taking an element out of it
                     mbar_expect_tx(bar, bytes);
                     bulk_load(smem_u32(ring + (size_t)slot * f.slot_bytes + (size_t)(s.first - s.lo) * 16), s.x + s.start(s.first),
                               bytes, bar);
@@ -867,6 +954,8 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
             one = two;
             two = three;
             three = four;
+            y1 = y2;
+            q2 = q3;
         }
         // copies still under way where a wait gave up
         if (!ok)

@@ -428,3 +428,79 @@ def test_rows_far_from_zero(cuda_device, base, entropy):
             data = [near, tok, f32(lp - g.choice([-0.6, -0.1, 0.0, 0.1, 0.6], len(lp))), adv, w, f32(lp + 0.5 * g.normal(size=len(lp)))]
             got = run(tree, data, cuda_device, x=x.to(cuda_device), kl_coef=0.05, entropy_coef=entropy)
             check(tree, data, got, kl_coef=0.05, entropy_coef=entropy)
+
+
+def rest_of(x, y):
+    """(1 - p, p, H + ln p, sum of magnitudes of p_v (x_v - x_y)) of element y of a row, the first from the others alone."""
+    others = torch.cat([x[:y], x[y + 1:]]) - x[y]
+    e = others.exp()
+    s, t = e.sum(), torch.where(e > 0, e * others, 0.0)
+    return s / (1 + s), 1 / (1 + s), -t.sum() / (1 + s), t.abs().sum() / (1 + s)
+
+
+@pytest.mark.parametrize("V", [2, 90, 301, 5000, 30011, 152064])
+@pytest.mark.parametrize("entropy", [0.0, 0.05])
+def test_confident_targets(cuda_device, V, entropy):
+    """Targets of probability 1 - 10^-1 to 1 - 10^-9: their own element is g (1 - p), within the tolerances above of that, not
+    of g (1 - p has the relative error of a sum and a ratio of sums, 2^-16); and the others' add up to its opposite."""
+    N = 25
+    g = torch.Generator().manual_seed(V)
+    x = torch.randn((N, V), generator=g) * 2
+    tok = torch.randint(0, V, (N,), generator=g, dtype=torch.int32)
+    tok[1:4] = torch.tensor([0, V - 1, V // 2])               # first, last: vectors that a row owns in part
+    for r in range(N - 1):
+        y = int(tok[r + 1])
+        others = torch.cat([x[r, :y], x[r, y + 1:]])
+        x[r, y] = torch.logsumexp(others.double(), 0).float() + 2.302585 * (0.3 + (r % 10) * 0.95)
+    x = x.bfloat16()
+    adv, w = torch.randn(N - 1, generator=g), torch.rand(N - 1, generator=g) + 0.5
+    plan = TreePlan([-1], [N])
+    room = torch.empty((N, V + 3), dtype=torch.bfloat16, device=cuda_device)
+    for xd, over in ((x.to(cuda_device), False), (room[:, 1:V + 1], False), (room[:, 3:], True)):
+        xd.copy_(x)
+        d = TL.policy_loss(plan, xd, tok.to(cuda_device), None, adv.to(cuda_device), weights=w.to(cuda_device), per_token=True,
+                           entropy_coef=entropy, dlogits=xd if over else None).dlogits.double().cpu()
+        for r in range(N - 1):
+            y, G = int(tok[r + 1]), -float(w[r]) * float(adv[r])
+            q, p, h, size = rest_of(x[r].double(), y)
+            want = G * q + entropy * float(w[r]) * p * h
+            bound = abs(G) * q + entropy * float(w[r]) * p * size
+            assert abs(d[r, y] - want) <= 2.0 ** -8 * abs(want) + 2.0 ** -16 * bound, (r, y, float(q), float(d[r, y] / want))
+        assert not d[N - 1].any()
+
+
+@pytest.mark.parametrize("V,kids", [(400, 3), (400, 20), (30011, 7), (152064, 40)])
+def test_confident_targets_of_several(cuda_device, V, kids):
+    """A row whose children begin with a certain token, some of them, or with others: the certain token's element is
+    sum g (1 - p) of its children minus p times the others' sum, where those may be 0."""
+    g = torch.Generator().manual_seed(V + kids)
+    tree = ([-1] + [0] * kids, [2] + [1] * kids)
+    N = 2 + kids
+    x = torch.randn((N, V), generator=g)
+    tok = torch.randint(0, V, (N,), generator=g, dtype=torch.int32)
+    sure = V - 3
+    tok[2::2] = sure                                          # every other child, the first among them
+    plan = TreePlan(*tree)
+    for gap in (2.0, 5.0, 9.0, 14.0, 19.0):
+        x[1, sure] = -100.0
+        x[1, sure] = torch.logsumexp(x[1].double(), 0).float() + gap
+        xb = x.bfloat16()
+        q, p, h, size = rest_of(xb[1].double(), sure)
+        for others in (0.0, 1.0):
+            adv = torch.randn(kids, generator=g) + 2
+            adv[1::2] *= others
+            r = TL.policy_loss(plan, xb.to(cuda_device), tok.to(cuda_device), None, adv.to(cuda_device), entropy_coef=0.01,
+                               weights=torch.cat([torch.tensor([float(i % 3 == 0), 1.0]) for i in range(kids)]).to(cuda_device))
+            d = r.dlogits.double().cpu()
+            G = -adv.double()
+            here = tok[2:] == sure
+            want = G[here].sum() * q - p * G[~here].sum() + 0.01 * kids * p * h
+            bound = G[here].abs().sum() * q + p * G[~here].abs().sum() + 0.01 * kids * p * size
+            assert abs(d[1, sure] - want) <= 2.0 ** -8 * abs(want) + 2.0 ** -16 * bound, (gap, others, float(d[1, sure] / want))
+            logp = torch.log_softmax(xb[1].double(), 0)
+            H = -(logp.exp() * logp).sum()
+            full = -G.sum() * logp.exp() + 0.01 * kids * logp.exp() * (logp + H)
+            full.index_add_(0, tok[2:].long(), G)
+            size_full = G.abs().sum() * logp.exp() + 0.01 * kids * logp.exp() * (logp.abs() + H)
+            size_full.index_add_(0, tok[2:].long(), G.abs())
+            assert ((d[1] - full).abs() <= 2.0 ** -8 * full.abs() + 2.0 ** -15 * size_full).all()
