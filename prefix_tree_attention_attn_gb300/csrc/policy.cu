@@ -393,6 +393,93 @@ __device__ __forceinline__ bool has_weight(const Params& p, int lane, const Ahea
     return __any_sync(0xffffffffu, any);
 }
 
+// The sum of g over the lanes in `alike`, in their order behind `from`; for the first of them.
+__device__ __forceinline__ float sum_alike(uint32_t alike, int lane, float g, float from) {
+    uint32_t left = __ffs(alike) - 1 == lane ? alike : 0u;
+    while (__any_sync(0xffffffffu, left != 0)) {
+        const float v = __shfl_sync(0xffffffffu, g, left ? __ffs(left) - 1 : lane);
+        if (left) from += v;
+        left &= left - 1;
+    }
+    return from;
+}
+
+// An element of the gradient without any g of its own, from its logit.
+__device__ __forceinline__ float element(const Result& R, float x) {
+    const float a = exponent(x, R.m);
+    return fast_exp2(a) * fmaf(R.ce, a - R.ts, R.cg);
+}
+
+// The elements of a row's targets in this CTA but the one that stayed apart, where children with the same token are added
+// up in their order.  One warp, a lane for each of 32 targets in turn; of more than 32 the sums so far lie by token
+// in the row's slot (`room`), which has space for half of its tokens at a time.  (Not inlined: within the kernel it
+// cost the gradient's loop 5 % by its registers alone.)
+struct Targets {
+    const int4* targets;
+    const int32_t* tokens;
+    const float *tx, *tg;
+    uint16_t* row_d;
+    float* room;
+    int room_bytes, lo, hi, shift, V, N;       // the slice's vectors
+    Result R;
+    float grad_scale;
+    int* status;
+};
+__device__ __noinline__ void add_targets(const Targets& t) {
+    const int lane = threadIdx.x & 31, nt = t.R.nt;
+    // target j where its token is in [y0, y1), or -1
+    auto load = [&](int j, int y0, int y1, int& y) {
+        const int q = j < nt ? t.targets[j].x : -1;
+        if (q < 0 || !ta_ok(t.status, 604, q, 0, t.N)) return -1;
+        y = t.tokens[q];
+        return y >= y0 && y < y1 && y != t.R.y ? q : -1;
+    };
+    auto write = [&](int y, float x, float g) { t.row_d[y] = (uint16_t)pack_bf16x2(element(t.R, x) + t.grad_scale * g, 0.f); };
+    const int window = nt <= 32 ? t.hi - t.lo : t.room_bytes / 32;
+    for (int v = t.lo; v < t.hi; v += window) {
+        const int base = 8 * v - t.shift, y0 = max(base, 0), y1 = min(8 * min(v + window, t.hi) - t.shift, t.V);
+        if (nt <= 32) {
+            int y = 0;
+            const int q = load(lane, y0, y1, y);
+            const float g = q >= 0 ? t.tg[q] : 0.f;
+            const uint32_t alike = __match_any_sync(0xffffffffu, q >= 0 ? y : -1 - lane);
+            const float sum = sum_alike(alike, lane, g, 0.f);
+            if (q >= 0 && __ffs(alike) - 1 == lane) write(y, t.tx[q], sum);
+            continue;
+        }
+        constexpr int kAtOnce = 4;             // loads under way
+        auto all = [&](auto step) {
+            for (int j = lane; j - lane < nt; j += 32 * kAtOnce) {
+                int q[kAtOnce], y[kAtOnce];
+                float g[kAtOnce], x[kAtOnce];
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) q[i] = load(j + 32 * i, y0, y1, y[i]);
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) {
+                    g[i] = q[i] >= 0 ? t.tg[q[i]] : 0.f;
+                    x[i] = q[i] >= 0 ? t.tx[q[i]] : 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) step(q[i] >= 0, y[i], g[i], x[i]);
+            }
+            __syncwarp();
+        };
+        all([&](bool here, int y, float, float) {
+            if (here) t.room[y - base] = 0.f;
+        });
+        all([&](bool here, int y, float g, float) {
+            const uint32_t alike = __match_any_sync(0xffffffffu, here ? y : -1 - lane);
+            const float sum = sum_alike(alike, lane, g, here ? t.room[y - base] : 0.f);
+            __syncwarp();
+            if (here && __ffs(alike) - 1 == lane) t.room[y - base] = sum;
+            __syncwarp();
+        });
+        all([&](bool here, int y, float, float x) {
+            if (here) write(y, x, t.room[y - base]);
+        });
+    }
+}
+
 // How the warps of a CTA are shared out: `teams` of `stat` for the statistics, a row each in turn, `grad` for the
 // gradient, then the finishers and the producer.
 struct Split {
@@ -620,10 +707,6 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
             } else {
                 const int odd = s.odd(at, T), yv = s.owns(R.y);
                 const uint4* here = reinterpret_cast<const uint4*>(ring + (size_t)slot * f.slot_bytes) - s.lo;
-                auto value = [&](float xv) {
-                    const float a = exponent(xv, R.m);
-                    return fast_exp2(a) * fmaf(R.ce, a - R.ts, R.cg);
-                };
                 int v = s.first + at;
                 uint4* row_d8 = reinterpret_cast<uint4*>(row_d - s.shift);   // (whole vectors lie as the row's do)
                 if (fabsf(R.m) <= kNear) {
@@ -681,33 +764,22 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                     const uint32_t u[4] = {x.x, x.y, x.z, x.w};
                     uint32_t o[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(value(lo16(u[i])), value(hi16(u[i])));
+                    for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(element(R, lo16(u[i])), element(R, hi16(u[i])));
                     store(v < s.last ? v : odd, make_uint4(o[0], o[1], o[2], o[3]));
                 }
                 // the element that stayed apart, over what the same thread has written there
                 if (yv >= 0 && (yv == odd || (yv >= s.first && yv < s.last && (yv - s.first) % T == at)))
                     row_d[R.y] = (uint16_t)pack_bf16x2(R.own, 0.f);
                 if (R.nt != 1) {
-                    // every warp has written: the targets' elements again
+                    // every warp has written, and read the slot: one of them does the other targets' elements again
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&S.cta));
-                    ok = mbar_wait(smem_u32(&S.cta), meets++ & 1, p.status, 603);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    for (int j = at; j < R.nt; j += T) {
-                        const int q = p.targets[R.t0 + j].x;
-                        if (!ta_ok(p.status, 604, q, 0, p.N)) continue;
-                        const int yj = p.tokens[q];
-                        if (s.owns(yj) < 0 || yj == R.y) continue;
-                        bool earlier = false;      // another child has the same token: the first one adds them up
-                        for (int i = 0; i < j && !earlier; ++i) earlier = p.tokens[p.targets[R.t0 + i].x] == yj;
-                        if (earlier) continue;
-                        float g = p.tg[q];
-                        for (int i = j + 1; i < R.nt; ++i) {
-                            const int qi = p.targets[R.t0 + i].x;
-                            if (p.tokens[qi] == yj) g += p.tg[qi];
-                        }
-                        row_d[yj] = (uint16_t)pack_bf16x2(value(p.tx[q]) + p.grad_scale * g, 0.f);
+                    if (at < 32) {
+                        ok = mbar_wait(smem_u32(&S.cta), meets++ & 1, p.status, 603);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        add_targets({p.targets + R.t0, p.tokens, p.tx, p.tg, row_d, reinterpret_cast<float*>(ring + (size_t)slot * f.slot_bytes),
+                                     f.slot_bytes, s.lo, s.hi, s.shift, s.V, p.N, R, p.grad_scale, p.status});
                     }
                 }
             }
@@ -938,7 +1010,7 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                 const Slice s(p, r, me, log_c);
                 const uint32_t bytes = (uint32_t)(s.last - s.first) * 16;
                 if (active && bytes) {
-                    fence_proxy_async_smem();  // a thread may have written to the slot, taking an element out of it
+                    fence_proxy_async_smem();  // threads may have written to the slot: an element taken out, sums by token
                     mbar_expect_tx(bar, bytes);
                     bulk_load(smem_u32(ring + (size_t)slot * f.slot_bytes + (size_t)(s.first - s.lo) * 16), s.x + s.start(s.first),
                               bytes, bar);

@@ -504,3 +504,52 @@ def test_confident_targets_of_several(cuda_device, V, kids):
             size_full = G.abs().sum() * logp.exp() + 0.01 * kids * logp.exp() * (logp.abs() + H)
             size_full.index_add_(0, tok[2:].long(), G.abs())
             assert ((d[1] - full).abs() <= 2.0 ** -8 * full.abs() + 2.0 ** -15 * size_full).all()
+
+
+@pytest.mark.parametrize("V,kids,distinct", [(600, 6000, 600), (600, 3000, 3), (7001, 5000, 7001), (40000, 3000, 900), (152064, 1500, 5)])
+def test_many_children(cuda_device, V, kids, distinct):
+    """A row of thousands of children, many of which begin alike: the sum of their g in each element.  n terms in a row are
+    within n 2^-24 of the sum of their magnitudes, at most 2^-12 here with the pairwise sums behind it; else as above."""
+    tree = ([-1] + [0] * kids, [2] + [1] * kids)
+    N = 2 + kids
+    g = torch.Generator(cuda_device).manual_seed(V + kids)
+    x = torch.randn((N, V), device=cuda_device, generator=g).bfloat16()
+    tok = torch.randint(0, distinct, (N,), device=cuda_device, generator=g, dtype=torch.int32) * (V // distinct)
+    adv = torch.randn(kids, device=cuda_device, generator=g)
+    w = torch.rand(2 * kids, device=cuda_device, generator=g) * (torch.rand(2 * kids, device=cuda_device, generator=g) < 0.8)
+    call = lambda: TL.policy_loss(plan, x, tok, None, adv, weights=w, entropy_coef=0.01)  # noqa: E731
+    plan = TreePlan(*tree)
+    got = call()
+    again = call()
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    for row, here, to in ((0, slice(0, None, 2), tok[1:2].expand(kids)), (1, slice(1, None, 2), tok[2:])):
+        G, W = -(w.double() * adv.double().repeat_interleave(2))[here], w.double()[here]
+        logp = torch.log_softmax(x[row].double(), 0)
+        p, H = logp.exp(), -(logp.exp() * logp).sum()
+        want = -G.sum() * p + 0.01 * W.sum() * p * (logp + H)
+        size = G.abs().sum() * p + 0.01 * W.sum() * p * (logp.abs() + H)
+        want.index_add_(0, to.long(), G)
+        size.index_add_(0, to.long(), G.abs())
+        e = (got.dlogits[row].double() - want).abs()
+        assert (e <= 2.0 ** -8 * want.abs() + 2.0 ** -12 * size).all()
+    assert not got.dlogits[2:].any()
+
+
+def test_time_of_many_children(cuda_device):
+    """Eight times the children of a row, at most twenty times the time (what goes with their square: some thirty)."""
+    def once(kids):
+        plan, N = TreePlan([-1] + [0] * kids, [2] + [1] * kids), kids + 2
+        g = torch.Generator(cuda_device).manual_seed(kids)
+        x = torch.randn((N, 600), device=cuda_device, generator=g).bfloat16()
+        tok = torch.randint(0, 600, (N,), device=cuda_device, generator=g, dtype=torch.int32)
+        adv, took = torch.randn(kids, device=cuda_device, generator=g), []
+        for _ in range(6):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            TL.policy_loss(plan, x, tok, None, adv)
+            b.record()
+            b.synchronize()
+            took.append(a.elapsed_time(b))
+        return min(took)
+
+    assert once(16000) <= 20 * once(2000)
