@@ -395,3 +395,77 @@ def test_prefill_of_large_and_small_inputs(cuda_device, values, size):
     assert (np.abs(num(o) - want) <= 2.0 ** -8 * np.abs(want) + (wide * 2.0 ** -8 + 2.0 ** -12) * mag).all()
     for u in range(3):
         assert (np.abs(num(states[u]) - end[u]) <= 2.0 ** -13 * mass[u]).all()
+
+
+def from_states_64(parent, seg, q, k, v, dec, scale, start):
+    """What ``oracle.linear.from_states`` gives, on the device: (o, states by node, the magnitudes of both), the tokens of a
+    chunk of 128 at once, in 64 bits."""
+    off, end, mass, hkv = OL.packed_layout(parent, seg)[1], {}, {}, k.shape[1]
+    order, G, gam = OL.packed_layout(parent, seg)[0], q.shape[1] // hkv, dec.double()
+    o, size = torch.empty(q.shape, dtype=torch.float64, device=q.device), torch.empty(q.shape, dtype=torch.float64, device=q.device)
+    i = torch.arange(128, device=q.device)
+    for u in order:
+        if parent[u] >= 0:
+            S, A = end[parent[u]], mass[parent[u]]
+        else:
+            S = start[u].double() if start[u] is not None else torch.zeros((hkv, 128, 128), dtype=torch.float64, device=q.device)
+            A = S.abs()
+        for t in range(off[u], off[u] + seg[u], 128):
+            m = min(128, off[u] + seg[u] - t)
+            Q = q[t:t + m].double().view(m, hkv, G, 128).permute(1, 2, 0, 3) * scale
+            K, V = (x[t:t + m].double().transpose(0, 1) for x in (k, v))
+            lag = i[:m, None] - i[None, :m]
+            w = torch.where(lag >= 0, gam[:, None, None] ** lag.clamp_min(0), 0.0)
+            P = (Q @ K[:, None].transpose(-1, -2)) * w[:, None]
+            f = (gam[:, None] ** (i[:m] + 1))[:, None, :, None]
+            o[t:t + m] = (P @ V[:, None] + f * (Q @ S[:, None])).permute(2, 0, 1, 3).reshape(m, -1, 128)
+            size[t:t + m] = (P.abs() @ V.abs()[:, None] + f * (Q.abs() @ S.abs()[:, None])).permute(2, 0, 1, 3).reshape(m, -1, 128)
+            left = (gam[:, None] ** (m - 1 - i[:m]))[..., None]
+            S = (gam ** m)[:, None, None] * S + (K * left).transpose(1, 2) @ V
+            A = (gam ** m)[:, None, None] * A + (K.abs() * left).transpose(1, 2) @ V.abs()
+        end[u], mass[u] = S, A
+    return o, end, size, mass
+
+
+@pytest.mark.parametrize("hq,hkv,nodes,longest", [
+    (8, 8, 90, 400), (40, 8, 31, 700), (64, 8, 40, 260), (64, 8, 140, 129), (40, 2, 300, 200), (16, 16, 70, 300), (152, 152, 4, 600),
+    (20, 1, 420, 150), (5, 5, 100, 900), (48, 6, 53, 300)])
+def test_outputs_of_many_chunks(cuda_device, hq, hkv, nodes, longest):
+    """More chunks than CTAs of a kv-head, by far: whole chunks one after another, then a share of the q-heads of those that are
+    left, where a CTA may begin and end within a chunk; short chunks among them.  Groups of 1, 5, 8 and 20 heads.
+    States from as many as (longest / 128) chunks in three depths: the bounds above."""
+    g = np.random.default_rng(hq * nodes)
+    parent = [-1] + [int(g.integers(0, max(1, u // 2))) if u % 7 else -1 for u in range(1, nodes)]
+    depth = []
+    for u, p in enumerate(parent):
+        if p >= 0 and depth[p] >= 2:
+            parent[u] = p = 0
+        depth.append(0 if p < 0 else depth[p] + 1)
+    seg = [int(x) for x in np.exp(g.uniform(0, np.log(longest), nodes)).round()]
+    seg[0] = longest
+    N = sum(seg)
+    q, k, v = draw(nodes, N, hq, hkv, 128, cuda_device)
+    dec = decays(hkv, cuda_device, (1.0, 0.9, 0.99, 0.62))
+    states = randn((nodes + 2, hkv, 128, 128), cuda_device, 3) * 3
+    slot_in = [nodes + u % 2 if p < 0 and u % 3 else -1 for u, p in enumerate(parent)]
+    start = [states[s].clone() if s >= 0 else None for s in slot_in]
+    o = TL.tree_linear_prefill(TreePlan(parent, seg), states, TL.StateSlots(slot_in, list(range(nodes)), nodes + 2), q, k, v, dec, 0.125)
+    want, end, size, mass = from_states_64(parent, seg, q, k, v, dec, 0.125, start)
+    for a in range(0, N, 4096):
+        W = want[a:a + 4096]
+        lim = 2.0 ** -8 * W.abs() + (2.0 ** -8 + 2.0 ** -12) * size[a:a + 4096] + 1e-30
+        assert ((o[a:a + 4096].double() - W).abs() <= lim).all(), a
+    for u in range(nodes):
+        assert ((states[u].double() - end[u]).abs() <= 2.0 ** -13 * mass[u] + 1e-30).all(), u
+
+
+def test_64_bit_form(cuda_device):
+    """The form above against the oracle, token by token."""
+    parent, seg = [-1, 0, 0, -1], [130, 17, 140, 9]
+    q, k, v = draw(5, sum(seg), 4, 2, 128, cuda_device)
+    dec = decays(2, cuda_device, (0.9, 0.62))
+    S0 = randn((2, 128, 128), cuda_device)
+    got = from_states_64(parent, seg, q, k, v, dec, 0.2, [S0, None, None, None])
+    want = OLN.from_states(parent, seg, num(q), num(k), num(v), num(dec), 0.2, [num(S0), None, None, None])
+    for a, b in ((got[0], want[0]), (got[2], want[2]), *((got[i][u], want[i][u]) for i in (1, 3) for u in range(4))):
+        assert (np.abs(num(a) - b) <= 1e-11 * np.abs(b).max()).all()
