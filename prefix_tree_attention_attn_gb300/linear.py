@@ -84,7 +84,10 @@ class StateSlots:
     """Which slot of a pool of ``n_slots`` states each branch (row of a step, node of a
     prefill) starts from and leaves its state in: ``slot_in`` (-1: a zero state) and
     ``slot_out`` (-1: not kept; in a step, a padding row).  The slots of ``slot_out`` are all
-    different.  Checked and uploaded once; call ``upload()`` before a stream capture."""
+    different.  Checked and uploaded once, without waiting for what the device still has to do; call
+    ``upload()`` before a stream capture, and keep the object as long as the graph is replayed."""
+
+    _copies = {}                                           # a stream by device
 
     def __init__(self, slot_in, slot_out, n_slots: int):
         a, b = _i32(slot_in), _i32(slot_out)
@@ -103,7 +106,7 @@ class StateSlots:
         live = np.flatnonzero((a >= 0) & (b >= 0) & (a != b))
         self._rows_apart = not np.isin(a[live], kept).any()
         self._plan = None
-        self._on = {}
+        self._on, self._readers = {}, {}
 
     def __len__(self):
         return len(self.slot_in)
@@ -114,9 +117,23 @@ class StateSlots:
         t = self._on.get(dev)
         if t is None:
             d = torch.device("cuda", dev)
-            t = self._on[dev] = tuple(torch.from_numpy(x.copy()).to(d) for x in (self.slot_in, self.slot_out))
-            torch.cuda.current_stream(d).synchronize()     # a side stream may read them next
+            s = self._copies.get(dev)
+            if s is None:
+                s = self._copies[dev] = torch.cuda.Stream(d)
+            with torch.cuda.stream(s):                     # its own: the copy alone is waited for, any stream may read next
+                t = self._on[dev] = tuple(torch.from_numpy(np.stack([self.slot_in, self.slot_out])).to(d))
+            self._readers[dev] = set()
         return t
+
+    def _tables(self, dev: int, side):
+        """The addresses of the tables, for a call on the current stream or on ``side``: their memory is kept until
+        it has read them."""
+        a, b = self.upload()
+        s = torch._C._cuda_getCurrentRawStream(dev) if side is None else side.cuda_stream
+        if s not in self._readers[dev] and len(self):
+            a.record_stream(torch.cuda.current_stream() if side is None else side)   # (one memory: b's too)
+            self._readers[dev].add(s)
+        return a.data_ptr(), b.data_ptr()
 
     def _check_plan(self, plan: TreePlan) -> None:
         """No tree starts from a slot that another tree, or another root beside it, leaves a state in."""
@@ -179,11 +196,11 @@ def tree_linear_prefill(plan: TreePlan, states, slots: StateSlots, q, k, v, deca
         workspace = _empty(side, (max(prefill_workspace(plan, hkv, d), 256),), torch.uint8, q.device)
     elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected contiguous cuda:{dev} uint8, got {workspace.device} {workspace.dtype}")
-    a, b = slots.upload()
+    a, b = slots._tables(dev, side)
     st = B.load().tree_attn_linear_prefill(
         plan.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), states.data_ptr() or None, states.shape[0],
-        a.data_ptr(), b.data_ptr(), decay.data_ptr(), hq, hkv, d, scale, workspace.data_ptr(), workspace.numel(),
-        _stream_of(side, dev, q, k, v, o, states, decay, workspace, a, b))
+        a, b, decay.data_ptr(), hq, hkv, d, scale, workspace.data_ptr(), workspace.numel(),
+        _stream_of(side, dev, q, k, v, o, states, decay, workspace))
     if st:
         B.check(st, "tree_attn_linear_prefill")
     return o
@@ -208,11 +225,10 @@ def tree_linear_step(states, slots: StateSlots, q, k, v, decay, scale: float, o=
         o = _empty(side, (R, hq, d), torch.bfloat16, q.device)
     else:
         _check_dense(o, "o", (R, hq, d), torch.bfloat16, dev)
-    a, b = slots.upload()
+    a, b = slots._tables(dev, side)
     st = B.load().tree_attn_linear_step(
-        states.data_ptr() or None, states.shape[0], a.data_ptr(), b.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), qs,
-        ks, vs, o.data_ptr(), decay.data_ptr(), R, hq, hkv, d, scale,
-        _stream_of(side, dev, states, a, b, q, k, v, o, decay))
+        states.data_ptr() or None, states.shape[0], a, b, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
+        o.data_ptr(), decay.data_ptr(), R, hq, hkv, d, scale, _stream_of(side, dev, states, q, k, v, o, decay))
     if st:
         B.check(st, "tree_attn_linear_step")
     return o

@@ -469,3 +469,35 @@ def test_64_bit_form(cuda_device):
     want = OLN.from_states(parent, seg, num(q), num(k), num(v), num(dec), 0.2, [num(S0), None, None, None])
     for a, b in ((got[0], want[0]), (got[2], want[2]), *((got[i][u], want[i][u]) for i in (1, 3) for u in range(4))):
         assert (np.abs(num(a) - b) <= 1e-11 * np.abs(b).max()).all()
+
+
+def test_new_slots_do_not_wait_for_queued_work(cuda_device):
+    """A fork is a new table: it comes to the device while what was launched before still runs, and stays there until its
+    readers are done, on whatever stream they are."""
+    R, hq, hkv = 5, 4, 2
+    q, k, v = draw(33, R, hq, hkv, 128, cuda_device)
+    dec, first = decays(hkv, cuda_device), randn((2 * R, hkv, 128, 128), cuda_device)
+    fork = lambda x: TL.StateSlots(range(R), [R + (i + x) % R for i in range(R)], 2 * R)  # noqa: E731
+    want = []
+    for x in range(R):
+        s = first.clone()
+        want.append((TL.tree_linear_step(s, fork(x), q, k, v, dec, 0.1), s))
+    torch.cuda.synchronize()
+    done = torch.cuda.Event()
+    torch.cuda._sleep(400_000_000)                              # some 0.2 s
+    done.record()
+    fork(1).upload()
+    assert not done.query()
+    streams = [torch.cuda.Stream() for _ in range(R)]
+    got = [first.clone() for _ in range(R)]
+    torch.cuda.synchronize()
+    for x, side in enumerate(streams):                          # each table dropped while its reader waits
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(40_000_000)
+        if x % 2:
+            TL.tree_linear_step(got[x], fork(x), q, k, v, dec, 0.1, stream=side)
+        else:
+            with torch.cuda.stream(side):
+                TL.tree_linear_step(got[x], fork(x), q, k, v, dec, 0.1)
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[x], want[x][1]) for x in range(R))
