@@ -590,11 +590,15 @@ int build_lin(tree_attn_plan_s* P) {
         for (int32_t l = 0; l < n_depths; ++l)
             std::stable_sort(X.lvl_nodes.begin() + X.lvl_ptr[l], X.lvl_nodes.begin() + X.lvl_ptr[(size_t)l + 1],
                              [&](int32_t a, int32_t b) { return X.lnodes[4 * (size_t)a + 2] > X.lnodes[4 * (size_t)b + 2]; });
+        std::vector<int32_t> place(n, -1);
+        X.n_inner = 0;
+        for (int32_t k = 0; k < n; ++k)
+            if (X.kids[(size_t)k + 1] > X.kids[k]) place[k] = X.n_inner++;
         X.walks.clear();
         for (const int32_t k : X.lvl_nodes) {
             const int32_t *node = &X.lnodes[4 * (size_t)k], *last = &X.chunks[4 * (size_t)(node[1] + node[2] - 1)];
-            X.walks.insert(X.walks.end(), {k, node[0], node[1], node[2], X.chunks[4 * (size_t)node[1]], last[1],
-                                           X.kids[(size_t)k + 1] > X.kids[k], P->node_order[k]});
+            X.walks.insert(X.walks.end(), {place[k], node[0] < 0 ? -1 : place[node[0]], node[1], node[2],
+                                           X.chunks[4 * (size_t)node[1]], last[1], P->node_order[k], 0});
         }
         X.ready = true;
     } catch (const std::bad_alloc&) {

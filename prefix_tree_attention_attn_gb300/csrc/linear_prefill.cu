@@ -108,8 +108,8 @@ constexpr int kAhead = 6;                      // chunks that are brought into L
 
 // A CTA's walk, the whole of a node or a segment: what it has to know before its first load, in one piece.
 struct Walk {
-    int32_t node, parent, chunk, chunks;       // packed nodes; the walk's first chunk, its chunks
-    int32_t token, end, inner, id;             // its first token, its last chunk's tokens; 1: has children; node id
+    int32_t leaves, parent, chunk, chunks;     // places of end states, or -1; the walk's first chunk, its chunks
+    int32_t token, end, id, unused;            // its first token, its last chunk's tokens; node id
     int32_t first, segment, whole, place;      // first of the node's chunks; chunks of a segment but the node's last,
                                                // segments but the last; the first one's place in `sums`
 };
@@ -120,9 +120,9 @@ struct StateParams {
     const int4* order;         // LinInfo::walks of the depth, a node each; or null: `walks`
     Walk walks[kMaxWalks];
     const float* decay;
-    float* s_out;              // [n_nodes, hkv, d, d], nodes with children
+    float* s_out;              // [n_inner, hkv, d, d], end states of the nodes with children
     float* sums;               // [segments, hkv, d, d] what a segment adds to the state; behind a root's, its start state
-    int32_t hkv, n_nodes, n_chunks;
+    int32_t hkv, n_inner, n_chunks;
     int32_t first_depth;
     int32_t adding;            // 1: this launch leaves the sums
     int32_t leads;             // 1: the call's first launch
@@ -153,11 +153,11 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         job = p.walks[blockIdx.x / kParts / p.hkv];
     }
     // (the loads are under way while the barriers are set up)
-    const int node = job.node, n = job.chunks, c0 = job.chunk, end = job.end, whole = job.whole;
-    bool ok = ta_ok(status, 620, node, 0, p.n_nodes) && ta_ok(status, 621, c0, 0, p.n_chunks) &&
-              ta_ok(status, 622, c0 + n, 0, p.n_chunks + 1) && ta_ok(status, 623, job.parent, -1, p.n_nodes);
+    const int n = job.chunks, c0 = job.chunk, end = job.end, whole = job.whole;
+    bool ok = ta_ok(status, 620, job.leaves, -1, p.n_inner) && ta_ok(status, 621, c0, 0, p.n_chunks) &&
+              ta_ok(status, 622, c0 + n, 0, p.n_chunks + 1) && ta_ok(status, 623, job.parent, -1, p.n_inner);
     const int par = ok ? job.parent : -1;
-    const bool last = job.first == whole * job.segment, inner = last && job.inner;
+    const bool last = job.first == whole * job.segment, inner = last && job.leaves >= 0;
     auto kfull = [&](int s) { return sb + 8u * s; };          // K of stage s has come
     auto kfree = [&](int s) { return sb + 16 + 8u * s; };     // and has been multiplied
     auto vfull = [&](int s) { return sb + 32 + 8u * s; };
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                     reinterpret_cast<float4*>(dst)[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
             };
             if (p.adding) leave(p.sums + (size_t)(job.place + job.first / job.segment) * p.hkv * kD * kD + at);
-            else if (inner) leave(p.s_out + (size_t)node * p.hkv * kD * kD + at);
+            else if (inner) leave(p.s_out + (size_t)job.leaves * p.hkv * kD * kD + at);
             if (!p.adding && to >= 0) leave(p.io.states + (size_t)to * p.hkv * kD * kD + at);
         }
         if (lane == 0) bulk_wait_all();
@@ -775,8 +775,8 @@ bool split_depth(const LinInfo& X, size_t l, int32_t hkv, Split& out) {
             const int32_t whole = (c - 1) / s;
             for (int32_t t = 0; t <= whole; ++t) {
                 const int32_t* node = &X.walks[8 * (size_t)(lo + i)];
-                const Walk w = {k, node[1], node[2] + t * s, std::min(s, c - t * s), node[4] + t * s * kChunk,
-                                t < whole ? kChunk : node[5], node[6], node[7], t * s, s, whole, out.places};
+                const Walk w = {node[0], node[1], node[2] + t * s, std::min(s, c - t * s), node[4] + t * s * kChunk,
+                                t < whole ? kChunk : node[5], node[6], 0, t * s, s, whole, out.places};
                 if (t < whole) out.sums[out.n_sums++] = w;
                 out.all[out.n_all++] = w;
             }
@@ -792,7 +792,7 @@ struct Ws {
 };
 Ws layout(const tree_attn_plan_s* P, int32_t hkv) {
     const size_t nc = P->lin.chunks.size() / 4, per = (size_t)hkv * kD * kD;
-    const size_t s_out = nc * per * 2, sums = s_out + (size_t)P->n_nodes * per * 4;
+    const size_t s_out = nc * per * 2, sums = s_out + (size_t)P->lin.n_inner * per * 4;
     int places = 0;                            // (the depths take turns)
     for (size_t l = 0; l + 1 < P->lin.lvl_ptr.size(); ++l) {
         Split x;
@@ -869,7 +869,7 @@ int tree_attn_linear_prefill(tree_attn_plan_t P, const void* q, const void* k, c
     p.s_out = reinterpret_cast<float*>(ws + w.s_out);
     p.sums = reinterpret_cast<float*>(ws + w.sums);
     p.hkv = hkv;
-    p.n_nodes = P->n_nodes;
+    p.n_inner = P->lin.n_inner;
     p.n_chunks = (int32_t)nc;
     p.leads = 1;
     p.io = {states, slot_in, slot_out, n_slots, status};

@@ -57,9 +57,10 @@ struct LinInfo {
     std::vector<int32_t> lvl_ptr;  // [depths+1] ranges of lvl_nodes
     std::vector<int32_t> lvl_nodes;
     std::vector<int32_t> kids;     // as DevicePlan::kids
-    // [8*n_nodes] for each of lvl_nodes {packed node, parent's or -1, first chunk, chunks, first token, the last
-    // chunk's tokens, 1 with children, node id}
+    // [8*n_nodes] for each of lvl_nodes {place of its end state among those of nodes with children or -1, its
+    // parent's or -1, first chunk, chunks, first token, the last chunk's tokens, node id, 0}
     std::vector<int32_t> walks;
+    int32_t n_inner = 0;           // nodes with children
     bool ready = false;
 };
 

@@ -80,3 +80,11 @@ def test_binding_refuses_before_the_library(lib, monkeypatch):
         TL.tree_linear_step(states, TL.StateSlots([0, 1], [0, 1], 2), x, x[:, :2], x[:, :2], None, 1.0)
     with pytest.raises(ValueError, match="q: expected"):
         TL.tree_linear_prefill(TreePlan([-1], [2]), states, TL.StateSlots([0], [1], 2), x, x[:, :2], x[:, :2], None, 1.0)
+
+
+def test_workspace_holds_what_is_written(lib):
+    """The states that enter the chunks, in bf16, and the end states of the nodes with children, in fp32: nothing for leaves."""
+    for parent, seg, chunks, inner in (([-1] * 1024, [300] * 1024, 3072, 0), ([-1] + [0] * 40, [128] * 41, 41, 1),
+                                       ([-1, 0, 1, 2, 0, 0, 0, 0, 0, 0, 0], [129] * 11, 22, 3)):
+        for hkv in (1, 8):
+            assert TL.prefill_workspace(TreePlan(parent, seg), hkv, 128) == hkv * 128 * 128 * (2 * chunks + 4 * inner)
