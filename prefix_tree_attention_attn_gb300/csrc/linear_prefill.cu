@@ -764,7 +764,7 @@ bool split_depth(const LinInfo& X, size_t l, int32_t hkv, Split& out) {
     if (m > kSplitNodes) return false;
     int64_t total = 0;
     for (int32_t i = 0; i < m; ++i) total += X.lnodes[4 * (size_t)X.lvl_nodes[lo + i] + 2];
-    const int narrow = 152 / (4 * hkv), wide = 152 / (2 * hkv);
+    const int narrow = (int)(152 / (4 * (int64_t)hkv)), wide = (int)(152 / (2 * (int64_t)hkv));
     for (const int n : {total < 128 && m <= narrow ? narrow : 0, wide}) {
         out.n_sums = out.n_all = out.places = 0;
         for (int32_t i = 0; i < m; ++i) {

@@ -88,3 +88,12 @@ def test_workspace_holds_what_is_written(lib):
                                        ([-1, 0, 1, 2, 0, 0, 0, 0, 0, 0, 0], [129] * 11, 22, 3)):
         for hkv in (1, 8):
             assert TL.prefill_workspace(TreePlan(parent, seg), hkv, 128) == hkv * 128 * 128 * (2 * chunks + 4 * inner)
+
+
+@pytest.mark.parametrize("hkv", [39, 77, 2 ** 20, 2 ** 29, 2 ** 30, 2 ** 31 - 1])
+def test_any_number_of_heads_is_answered(lib, hkv):
+    """A size, or a refusal of the call."""
+    p, fake = TreePlan([-1, 0], [2000, 60]), C.c_void_p(0x1000)
+    assert TL.prefill_workspace(p, hkv, 128) >= hkv * 128 * 128 * (2 * 17 + 4)
+    assert lib.tree_attn_linear_prefill(p.handle, fake, fake, fake, fake, fake, 4, fake, fake, fake, hkv, hkv, 128, 1.0, fake,
+                                        256, None) < 0
