@@ -303,8 +303,6 @@ __global__ void __launch_bounds__(512) append_kernel(const AppendParams p) {
     if (threadIdx.x == 0) p.lens_out[node] = at + 1;
 }
 
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
 int check_cache(const tree_decode_plan_s* P, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
                 const void* k8, const void* v8, const void* ks, const void* vs) {
     if (!k || !v) return TREE_ATTN_ERR_INVALID_ARG;

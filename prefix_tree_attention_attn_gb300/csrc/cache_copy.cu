@@ -82,8 +82,6 @@ bool well_formed(const int32_t* src, const int32_t* dst, int64_t n, int32_t n_pa
     return true;
 }
 
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
 }  // namespace
 
 }  // namespace treeattn

@@ -103,6 +103,9 @@ __device__ __forceinline__ void bwd_cta_work(const BwdParams& p, int b, int& ite
 // kernel reads: other rows and other calls go on as if nothing had happened.
 __device__ __forceinline__ void report_notice(int* status, int code) { atomicCAS(status + 1, 0, code); }
 
+// Whether an address is a multiple of a power of two.
+inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
 // A launch's own status; a refused one leaves nothing behind that a later call could take for its own.
 inline cudaError_t launched(cudaError_t e) {
     if (e != cudaSuccess) cudaGetLastError();

@@ -1222,8 +1222,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 // The forward scan: depth by depth where the plan has the depth tables, else
 // one walk over every chunk.
 int launch_scan(const tree_attn_plan_s* P, const DevicePlan* D, int64_t nc, const float* decay, int hkv,

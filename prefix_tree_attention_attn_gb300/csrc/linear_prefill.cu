@@ -70,12 +70,6 @@ __device__ __forceinline__ int slot_of(const SlotIO& io, const int32_t* table, i
     return s;
 }
 
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // Whether the powers of a decay (its log2) over half a chunk stay within 2^+-50: they are then factors of rows and columns.
 __device__ __forceinline__ bool by_columns(float lg) { return lg > -100.f / kChunk; }
 constexpr int kMiddle = kChunk / 2;            // the powers are counted from here
@@ -745,8 +739,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_dealloc(tmem, 512);
     }
 }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // The walks of a depth of few nodes whose long ones are cut into segments: first those whose sums are taken, then all.
 struct Split {

@@ -129,8 +129,6 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepParams p) {
     }
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 template <int D>
 cudaError_t launch(int64_t units, cudaStream_t s, const StepParams& p) {
     // Few large states: narrow blocks of columns while a wave holds them.  Measured, us in blocks of 32 and of 64: 8 states of

@@ -36,7 +36,7 @@ struct DevicePlan {
     // predictions by row of the policy loss (uploaded on its first use)
     void* policy_base = nullptr;
     int32_t* policy_rows = nullptr;     // [4*N] {first prediction, predictions, first target, targets}
-    int32_t* policy_pred = nullptr;     // [4*n_pred] {prediction, target row, trajectory, 0} by row, then target
+    int32_t* policy_pred = nullptr;     // [2*n_pred] {prediction, trajectory} by row, then target
     int32_t* policy_targets = nullptr;  // [4*targets] {target row, first prediction, predictions, 0} by row
     bool policy_ready = false;
     // chunk tables of the linear-attention calls (uploaded on their first use)

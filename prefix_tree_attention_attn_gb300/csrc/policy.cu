@@ -70,7 +70,7 @@ struct Params {
     float top_log, top_log_lo, low_log, low_log_lo;
     float kl, ent, grad_scale;
     const int4* rows;                          // {first prediction, predictions, first target, targets}
-    const int4* pred;                          // {prediction, target row, trajectory, 0} by row, then target
+    const int2* pred;                          // {prediction, trajectory} by row, then target
     const int4* targets;                       // {target row, first prediction, predictions, 0}
     float* logprobs;
     float* entropy;
@@ -207,13 +207,13 @@ struct Shared {
 };
 constexpr int kRing0 = (sizeof(Shared) + 127) / 128 * 128;
 
-__device__ __forceinline__ float advantage(const Params& p, int4 e) { return p.adv[p.per_token ? e.x : e.z]; }
+__device__ __forceinline__ float advantage(const Params& p, int2 e) { return p.adv[p.per_token ? e.x : e.y]; }
 
 // The predictions [first, first + n) of one target with logit x, by the threads `at`, `at` + step, ...
 __device__ __forceinline__ void predict_all(const Params& p, const Row& row, int first, int n, float x, int at, int step,
                                             bool writes, Sums& sum) {
     for (int i = at; i < n; i += step) {
-        const int4 e = p.pred[first + i];
+        const int2 e = p.pred[first + i];
         if (!ta_ok(p.status, 602, e.x, 0, p.n_pred)) continue;
         const float w = p.weights ? p.weights[e.x] : p.each;
         float lp = 0.f;
@@ -254,12 +254,6 @@ __device__ __forceinline__ Stat warp_join(Stat a) {
         r.s += __shfl_xor_sync(0xffffffffu, r.s, o);
         r.t += __shfl_xor_sync(0xffffffffu, r.t, o);
     }
-    return r;
-}
-
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 
@@ -349,7 +343,8 @@ struct Slice {
 
 // The loads of one row's predictions, in three steps that depend on one another.
 struct Ahead {
-    int4 info, mine;
+    int4 info;
+    int2 mine;
     float w, old, a, ref;
     int y;
 };
@@ -360,7 +355,7 @@ __device__ __forceinline__ void load_info(const Params& p, int64_t r, Ahead& x) 
         x.info = make_int4(0, 0, 0, 0);
 }
 __device__ __forceinline__ void load_pred(const Params& p, int lane, Ahead& x) {
-    x.mine = make_int4(-1, 0, 0, 0);
+    x.mine = make_int2(-1, 0);
     if (is_narrow(x.info) && lane < x.info.y) {
         x.mine = p.pred[x.info.x + lane];
         if (!ta_ok(p.status, 602, x.mine.x, 0, p.n_pred)) x.mine.x = -1;
@@ -374,7 +369,7 @@ __device__ __forceinline__ void load_values(const Params& p, int64_t r, bool all
         x.w = p.weights ? p.weights[x.mine.x] : p.each;
         if (all) {
             if (p.old) x.old = p.old[x.mine.x];
-            x.a = p.adv[p.per_token ? x.mine.x : x.mine.z];
+            x.a = advantage(p, x.mine);
             if (p.kl != 0.f) x.ref = p.ref[x.mine.x];
         }
     }
@@ -1089,7 +1084,6 @@ int ensure_policy(tree_attn_plan_s* P, DevicePlan** out, int64_t* n_pred) {
             // a target's predictions are the trajectories through it, its row the one before it
             const int64_t N = P->N;
             std::vector<int32_t> row_of(N, -1);
-            std::vector<int64_t> first(N + 1, 0);
             for (int64_t l = 0; l < L; ++l)
                 for (int64_t q = X.traj_ptr[l]; q + 1 < X.traj_ptr[l + 1]; ++q) row_of[X.traj_tok[q + 1]] = X.traj_tok[q];
             std::vector<int32_t> count(N, 0);                       // targets of each row
@@ -1101,7 +1095,7 @@ int ensure_policy(tree_attn_plan_s* P, DevicePlan** out, int64_t* n_pred) {
                 target_at[r] = n_targets;
                 n_targets += count[r];
             }
-            const int64_t rows_words = 4 * N, pred_words = 4 * std::max<int64_t>(np, 1);
+            const int64_t rows_words = 4 * N, pred_words = 2 * std::max<int64_t>(np, 1);
             at_pred = (rows_words + 63) / 64 * 64;
             at_target = at_pred + (pred_words + 63) / 64 * 64;
             h.assign(at_target + 4 * std::max<int64_t>(n_targets, 1), 0);
@@ -1133,10 +1127,9 @@ int ensure_policy(tree_attn_plan_s* P, DevicePlan** out, int64_t* n_pred) {
             for (int64_t l = 0; l < L; ++l)
                 for (int64_t q = X.traj_ptr[l]; q + 1 < X.traj_ptr[l + 1]; ++q, ++k) {
                     const int32_t s = X.traj_tok[q + 1];
-                    int32_t* e = pred + 4 * pred_at[s]++;
+                    int32_t* e = pred + 2 * pred_at[s]++;
                     e[0] = (int32_t)k;
-                    e[1] = s;
-                    e[2] = (int32_t)l;
+                    e[1] = (int32_t)l;
                 }
         } catch (const std::bad_alloc&) {
             return TREE_ATTN_ERR_OUT_OF_MEMORY;
@@ -1152,8 +1145,6 @@ int ensure_policy(tree_attn_plan_s* P, DevicePlan** out, int64_t* n_pred) {
     *out = &D;
     return TREE_ATTN_OK;
 }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 size_t column(const tree_attn_plan_s* P) { return ((size_t)P->N * 4 + 255) / 256 * 256; }
 
@@ -1272,7 +1263,7 @@ int tree_attn_policy_loss(tree_attn_plan_t P, const void* logits, int64_t row_st
     p.ent = c->entropy_coef;
     p.grad_scale = c->grad_scale;
     p.rows = reinterpret_cast<const int4*>(D->policy_rows);
-    p.pred = reinterpret_cast<const int4*>(D->policy_pred);
+    p.pred = reinterpret_cast<const int2*>(D->policy_pred);
     p.targets = reinterpret_cast<const int4*>(D->policy_targets);
     p.logprobs = logprobs;
     p.entropy = entropy;
