@@ -199,8 +199,9 @@ struct Shared {
     int parts_in[kMaxSlots];
     uint64_t read[kFinishers];                 // the cluster's finishers have read a row's targets
     uint64_t cta;                              // the gradient's warps have come this far
-    struct {
+    struct __align__(16) {
         int active, y;                         // y: the token whose element stays apart
+        int owner, at;                         // statistics thread of it in this CTA or -1; its byte in the slot, -1: in no whole vector
     } meta[kMaxSlots];
     float apart[kMaxSlots];                    // its logit, in the CTA that has it
     Result result[kMaxSlots];
@@ -527,7 +528,8 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             Stat st = {0.f, 0.f, 0.f};
-            if (S.meta[slot].active) {         // (the same in every CTA of the cluster)
+            const int4 meta = *reinterpret_cast<const int4*>(&S.meta[slot]);
+            if (meta.x) {                      // (the same in every CTA of the cluster)
                 const Slice s(p, r, me, log_c);
                 const int odd = s.odd(at, T);
                 const uint8_t* here8 = ring + (size_t)slot * f.slot_bytes;
@@ -536,13 +538,11 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                 uint4 rest = odd >= 0 ? s.part(odd) : none;
                 // The thread that comes by the element that stays apart takes it out of its vector: -inf, probability 0
                 // (a whole vector in the ring; the gradient has no use for this element either)
-                const int apart = S.meta[slot].y, av = s.owns(apart);
-                if (av >= s.first && av < s.last) {
-                    if (((av - s.first) & (T - 1)) == at)      // (T is a power of two)
-                        S.apart[slot] = lo16(swap_shared_u16(smem_u32(here8) + (av - s.lo) * 16 + (apart - s.start(av)) * 2, 0xff80u));
-                } else if (av >= 0 && av == odd) {
+                if (meta.z == at && meta.w >= 0) {
+                    S.apart[slot] = lo16(swap_shared_u16(smem_u32(here8) + meta.w, 0xff80u));
+                } else if (meta.z == at) {
                     uint32_t u[4] = {rest.x, rest.y, rest.z, rest.w};
-                    const int e = apart - s.start(av);
+                    const int e = meta.y - s.start(odd);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if (i == e / 2) {
@@ -658,7 +658,7 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
                 __threadfence_block();
                 const Stat none = {-INFINITY, 0.f, 0.f};
                 st = warp_join(lane < f.stat ? S.parts[slot][lane] : none);
-                const float xy = S.meta[slot].active && Slice(p, r, me, log_c).owns(S.meta[slot].y) >= 0 ? S.apart[slot] : -INFINITY;
+                const float xy = meta.x && meta.z >= 0 ? S.apart[slot] : -INFINITY;
                 if (lane < C)
                     remote_store(at_rank(smem_u32(&S.stats[place][me]), lane), make_float4(st.m, st.s, st.t, xy),
                                  at_rank(smem_u32(&S.stat[place]), lane));
@@ -999,10 +999,14 @@ __global__ void __maxnreg__(80) policy_kernel(const Params p, const Split f) {
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (lane == 0) {
-                S.meta[slot].active = active;
-                S.meta[slot].y = apart;
                 const uint32_t bar = smem_u32(&S.full[slot]);
                 const Slice s(p, r, me, log_c);
+                const int av = s.owns(apart), T = 32 * f.stat;   // (a power of two)
+                const bool whole = av >= s.first && av < s.last;
+                S.meta[slot].active = active;
+                S.meta[slot].y = apart;
+                S.meta[slot].owner = av < 0 ? -1 : whole ? (av - s.first) & (T - 1) : av == s.lo && s.lo < s.first ? T - 1 : T - 2;
+                S.meta[slot].at = whole ? 16 * (av - s.lo) + 2 * (apart - s.start(av)) : -1;
                 const uint32_t bytes = (uint32_t)(s.last - s.first) * 16;
                 if (active && bytes) {
                     fence_proxy_async_smem();  // threads may have written to the slot: an element taken out, sums by token
