@@ -172,7 +172,8 @@ int tree_attn_decode(tree_decode_plan_t plan, const int32_t* lens, const void* q
  *   src, dst                   host arrays of n page numbers in [0, n_pages), read during the call.
  *                              dst are all different and none of them is a source: INVALID_ARG
  *                              otherwise.  A page may be copied to several.
- * No plan, no workspace; may be captured.  Asynchronous on `stream`. */
+ * No plan, no workspace; may be captured: a replay copies the pages of the captured call again.
+ * Asynchronous on `stream`. */
 int tree_attn_cache_copy(int32_t n_caches, void* const* k8, void* const* v8, float* const* k_scale,
                          float* const* v_scale, int32_t n_pages, int32_t hkv, int32_t d, const int32_t* src,
                          const int32_t* dst, int64_t n, void* stream);

@@ -106,7 +106,8 @@ int tree_attn_linear_bwd(tree_attn_plan_t plan, const void* q, const void* k, co
  *
  * States are exact to fp32 rounding: gamma^n v is split into three bf16 numbers for the tensor
  * cores.  In O each of the two parts, over the chunk and over what came before, meets one
- * rounding to bf16 before the output's own (chunked scores, entering state).  Non-finite values of a
+ * rounding to bf16 before the output's own (chunked scores, entering state); scores times values
+ * may go up to 2^77.  Non-finite values of a
  * node's keys or values reach that node and its descendants alone.  Argument rules as
  * tree_attn_linear_fwd; d = 128; workspace of its own size. */
 int tree_attn_linear_prefill_workspace_size(tree_attn_plan_t plan, int32_t hkv, int32_t d, size_t* ws_bytes);
@@ -122,7 +123,9 @@ int tree_attn_linear_prefill(tree_attn_plan_t plan, const void* q, const void* k
  * written.  The slots of slot_out are all different, and none is another row's slot_in: rows run
  * at the same time.  Several rows may start from one slot (a fork).  q, k, v bf16, row r at element
  * r * stride (multiples of 8, at least heads * d), o bf16 [n_rows, hq, d]; d 64 or 128.  fp32
- * throughout, o rounded once.  No workspace; n_rows = 0 does nothing. */
+ * throughout, o rounded once.  `scale` is any finite number (a prefill's is positive, as
+ * tree_attn_linear_fwd's: for a negative one negate its q).  A prefill takes d = 128: a state of
+ * d 64 grows by steps alone.  No workspace; n_rows = 0 does nothing. */
 int tree_attn_linear_step(float* states, int32_t n_slots, const int32_t* slot_in, const int32_t* slot_out, const void* q,
                           const void* k, const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride, void* o,
                           const float* decay, int64_t n_rows, int32_t hq, int32_t hkv, int32_t d, float scale,

@@ -405,8 +405,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 // warps 0-7: query row m = 32 (w % 4) + lane, columns [64 (w / 4), + 64) of A and O; warp 8 loads, warp 9
 // issues.  A warp's 32 x 64 outputs leave by one bulk store out of shared memory (from registers, 16 bytes of 32
 // different rows at a time, they kept the store unit busy for 2,000 cycles of a unit).
-// A unit takes 3,900 cycles: 3,200 of tensor products, 3,500 of the mask, the weights and the roundings, 3,300 of
-// memory at 64 / 8 heads, beside one another.  480,408 tokens of 64 / 8 heads in 123 nodes: 3.83 ms with the states,
+// A unit takes 3,900 cycles: 1,650 of tensor products, 3,500 of the mask, the weights and the roundings (latency: loads,
+// conversions and stores of eight warps one after another), 3,300 of memory at 64 / 8 heads, beside one another.  480,408 tokens of 64 / 8 heads in 123 nodes: 3.83 ms with the states,
 // 4.6 TB/s of what has to be read and written; 8,835 of 32 / 8 heads in 17 nodes 77 us; one turn of 777 16.5 us.
 constexpr int kOutK = 2048, kOutV = kOutK + kTile, kOutS = kOutV + kTile, kOutQ = kOutS + kTile, kQSlots = 3,
               kOutStage = kOutQ + kQSlots * kTile, kOutSmem = kOutStage + kTile;
@@ -746,7 +746,8 @@ struct Split {
     int n_sums, n_all, places;                 // places in `sums`: segments but a node's last, a root's start state
 };
 
-// Whether anything is cut.  As many pieces as run at a time in narrow CTAs (four to a kv-head; of 128 chunks on in wide
+// Whether anything is cut (by a GB300's SMs, whatever the device has: the workspace's size is known without one; where
+// fewer run at a time the pieces take turns).  As many pieces as run at a time in narrow CTAs (four to a kv-head; of 128 chunks on in wide
 // ones, and where that cuts nothing), 16 at most; two launches of s chunks take as long as 2 s + 4 in one.
 // Measured, us of a call of one node, 8 kv-heads: 16 chunks 27 whole, 25.5 in 4 pieces, 28.6 in 2; 24 chunks
 // 37 and 33 (4); 40 chunks 62, 49 (4), 53 (7); 63 chunks 92, 69 (4), 73 (9); 235 chunks 306, 212 (4), 193 (9), 222 (16).

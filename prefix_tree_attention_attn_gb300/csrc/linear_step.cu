@@ -6,8 +6,8 @@
 // Memory-bound: 2 + 2 G multiply-adds per 8 bytes.  A column of S goes with its value feature alone, so
 // a CTA takes a block of CB columns of one (branch, kv-head) and nothing is joined between CTAs.  A
 // thread holds 4 columns of some rows in registers, all its loads under way at once; the sums over the rows
-// of four query heads at a time meet in shared memory.  1,024 branches of 8 kv-heads and 32 query heads at d 128: 173 us,
-// 6.3 TB/s of states; 64 branches 12.6 us (the states stay in L2 between steps); one 2.8.
+// of four query heads at a time meet in shared memory.  1,024 branches of 8 kv-heads and 32 query heads at d 128: 168 us,
+// 6.5 TB/s of states; 64 branches 12.6 us (the states stay in L2 between steps); one 2.8.
 #include <cuda_runtime.h>
 
 #include <algorithm>

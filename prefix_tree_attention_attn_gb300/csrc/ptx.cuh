@@ -61,7 +61,11 @@ __device__ __forceinline__ long long ta_clamp(int* status, int site, long long v
 // completed and its writes are visible: every kernel calls it before it reads
 // anything a previous kernel may have written and before it writes anything.
 // grid_dep_launch(), called after the wait, lets the next kernel start early in
-// turn (so at most two grids overlap).
+// turn (so at most two grids overlap).  The launches of one linear-attention prefill
+// go further: the first of a call does as above; the later ones signal before they
+// wait, read the call's inputs (not its states) at once, and may be several at a time.
+// Every CTA of theirs waits before it ends, so a launch has ended only when all before
+// it have, and what follows the call waits for the whole of it.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
