@@ -10,6 +10,7 @@
 
 #include <algorithm>
 
+#include "align.h"
 #include "decode.h"
 #include "kernels.h"
 

@@ -11,6 +11,7 @@
 #include <new>
 #include <vector>
 
+#include "align.h"
 #include "decode.h"
 #include "kernels.h"
 

@@ -1041,6 +1041,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
     if (lane == 0) p.lse[(int64_t)head * p.R + qi] = out_lse(mtop, l);
 }
 
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
 template <int D>
 int launch(const tree_decode_plan_s* P, const CUtensorMap& tk, const DecodeParams& a, const CombineParams& b,
            cudaStream_t s) {

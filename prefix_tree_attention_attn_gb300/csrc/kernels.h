@@ -103,8 +103,12 @@ __device__ __forceinline__ void bwd_cta_work(const BwdParams& p, int b, int& ite
 // kernel reads: other rows and other calls go on as if nothing had happened.
 __device__ __forceinline__ void report_notice(int* status, int code) { atomicCAS(status + 1, 0, code); }
 
-// Whether an address is a multiple of a power of two.
-inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+// a * b per lane of a pair of floats
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 
 // A launch's own status; a refused one leaves nothing behind that a later call could take for its own.
 inline cudaError_t launched(cudaError_t e) {
@@ -113,7 +117,11 @@ inline cudaError_t launched(cudaError_t e) {
 }
 
 // Launch with programmatic stream serialization (see grid_dep_wait in ptx.cuh):
-// the kernel may begin while the previous kernel on the stream finishes.
+// the kernel may begin while the previous kernel on the stream finishes.  The launches of one
+// linear-attention prefill overlap further than is said there: the call's first one waits before
+// it signals; the later ones signal before they wait and read the call's inputs (not its states)
+// at once, so several may run at a time.  Every CTA of theirs waits before it ends: a launch has
+// ended only when all before it have, and what follows the call waits for the whole of it.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                        Args... args) {

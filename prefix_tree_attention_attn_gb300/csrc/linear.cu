@@ -30,6 +30,7 @@
 #include <mutex>
 #include <vector>
 
+#include "align.h"
 #include "kernels.h"
 #include "plan.h"
 #include "ptx.cuh"

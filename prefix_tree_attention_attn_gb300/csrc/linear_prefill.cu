@@ -35,6 +35,7 @@
 #include <cmath>
 #include <mutex>
 
+#include "align.h"
 #include "kernels.h"
 #include "plan.h"
 #include "ptx.cuh"

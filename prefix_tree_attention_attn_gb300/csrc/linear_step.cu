@@ -13,6 +13,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "align.h"
 #include "kernels.h"
 #include "plan.h"
 #include "tree_linear.h"

@@ -36,6 +36,7 @@
 #include <mutex>
 #include <vector>
 
+#include "align.h"
 #include "kernels.h"
 #include "plan.h"
 #include "tree_loss.h"

@@ -61,11 +61,7 @@ __device__ __forceinline__ long long ta_clamp(int* status, int site, long long v
 // completed and its writes are visible: every kernel calls it before it reads
 // anything a previous kernel may have written and before it writes anything.
 // grid_dep_launch(), called after the wait, lets the next kernel start early in
-// turn (so at most two grids overlap).  The launches of one linear-attention prefill
-// go further: the first of a call does as above; the later ones signal before they
-// wait, read the call's inputs (not its states) at once, and may be several at a time.
-// Every CTA of theirs waits before it ends, so a launch has ended only when all before
-// it have, and what follows the call waits for the whole of it.
+// turn (so at most two grids overlap).
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -353,11 +349,6 @@ __device__ __forceinline__ void f32x2_split(uint64_t x, float& lo, float& hi) {
 __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
