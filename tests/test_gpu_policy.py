@@ -553,3 +553,13 @@ def test_time_of_many_children(cuda_device):
         return min(took)
 
     assert once(16000) <= 20 * once(2000)
+
+
+@pytest.mark.parametrize("kids", [31, 32, 33, 64, 127, 128, 129, 130, 257])
+@pytest.mark.parametrize("V", [50, 701])
+def test_children_around_the_sizes_of_a_pass(cuda_device, kids, V):
+    """Whatever way the targets of a row are added up in, some with the same token: the oracle's, within the same tolerances."""
+    tree = ([-1] + [0] * kids, [2] + [1] * kids)
+    for same in (False, True):
+        data = make(tree, V, kids + V, same=same)
+        check(tree, data, run(tree, data, cuda_device, kl_coef=0.05, entropy_coef=0.01), kl_coef=0.05, entropy_coef=0.01)
