@@ -294,7 +294,12 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             ok = mbar_wait(vfull(s), (i / kVStages) & 1, status, 122);
             const int L = tokens(i);
             const bool past = r >= L;              // another node's row: zeros, whatever it holds
-            if (ok && L < kChunk) ok = mbar_wait(kfull(sk), (i / kKStages) & 1, status, 123);
+            if (L < kChunk) {
+                // A barrier tells a phase from the next one alone, and these warps have not waited for the stage's keys before:
+                // first until the ones before them, which may still be under way, have been multiplied
+                if (ok && i >= kKStages) ok = mbar_wait(kfree(sk), (i / kKStages - 1) & 1, status, 146);
+                if (ok) ok = mbar_wait(kfull(sk), (i / kKStages) & 1, status, 123);
+            }
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const float w = L == kChunk ? w128 : past ? 0.f : exp2f((float)(L - 1 - r) * lg);
@@ -602,6 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int prev_off = 0, prev_L = 0, prev_h = 0, n = head_of(0), i = 0, q = 0;
         int off = p.chunks[4 * chunk_of(0)], L = p.chunks[4 * chunk_of(0) + 1];
         int first = n;                             // the chunk's first q-head here
+        bool alone = false;                        // the chunk before it has one unit here
         for (int u = 0; u <= U; ++u) {
             if (u < U) {
                 const int b = u & 1;
@@ -648,7 +654,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the rows behind a ragged chunk are another node's: zeros in the last 16 that the product
                 // reads (0 times an infinity there would not be 0)
                 if (n == first && (L & 15)) {
-                    ok = mbar_wait(b_v, i & 1, status, 144);
+                    // A barrier tells a phase from the next one alone: of a chunk before this one with one unit here, V
+                    // may still be under way until its products have ended (with more units the first ones' are behind A)
+                    if (alone) ok = mbar_wait(b_o((u - 1) & 1), ((u - 1) >> 1) & 1, status, 147);
+                    if (ok) ok = mbar_wait(b_v, i & 1, status, 144);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     if (m >= L && m < ((L + 15) & ~15)) {
@@ -723,6 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             prev_h = h0 + n;
             q = q == kQSlots - 1 ? 0 : q + 1;
             if (++n == G) {
+                alone = first == G - 1;
                 n = first = head_of(++i);
                 if (i < n_items) {
                     off = p.chunks[4 * chunk_of(i)];

@@ -501,3 +501,33 @@ def test_new_slots_do_not_wait_for_queued_work(cuda_device):
                 TL.tree_linear_step(got[x], fork(x), q, k, v, dec, 0.1)
     torch.cuda.synchronize()
     assert all(torch.equal(got[x], want[x][1]) for x in range(R))
+
+
+@pytest.mark.parametrize("hq,hkv", [(16, 16), (8, 8), (2, 2), (40, 2), (152, 152)])
+def test_whole_and_short_chunks_in_turn(cuda_device, hq, hkv):
+    """Single units of a chunk, whole chunks (128 tokens) before short ones: a short chunk's rows behind its last are set to
+    zero in a buffer that the chunk before it has used.  Inputs that are in no cache, again and again the same bits, and
+    those of the 64-bit form."""
+    g = np.random.default_rng(hq)
+    nodes = 240 if hkv < 100 else 12
+    parent = [-1] + [int(g.integers(0, 3)) if u > 3 else 0 for u in range(1, nodes)]
+    seg = [int(x) for x in g.choice([128, 256, 384, 1, 3, 17, 65, 130, 259, 385, 401], nodes)]
+    N = sum(seg)
+    q, k, v = draw(nodes + hq, N, hq, hkv, 128, cuda_device)
+    dec = decays(hkv, cuda_device, (1.0, 0.62, 0.99, 0.3))
+    first = randn((nodes + 1, hkv, 128, 128), cuda_device, 4)
+    plan, slots = TreePlan(parent, seg), TL.StateSlots([nodes] + [-1] * (nodes - 1), list(range(nodes)), nodes + 1)
+    cold = torch.empty(1 << 28, dtype=torch.uint8, device=cuda_device)
+    states = first.clone()
+    o = TL.tree_linear_prefill(plan, states, slots, q, k, v, dec, 0.1)
+    for _ in range(12):
+        again = first.clone()
+        cold.zero_()
+        assert torch.equal(TL.tree_linear_prefill(plan, again, slots, q, k, v, dec, 0.1), o) and torch.equal(again, states)
+    want, end, size, mass = from_states_64(parent, seg, q, k, v, dec, 0.1, [first[nodes]] + [None] * (nodes - 1))
+    # (a score is within 2^-16 of the sum of its products' magnitudes, which its own size may be far below)
+    scores = from_states_64(parent, seg, q.abs(), k.abs(), v.abs(), dec, 0.1, [first[nodes].abs()] + [None] * (nodes - 1))[0]
+    lim = 2.0 ** -8 * want.abs() + (2 * 2.0 ** -8 + 2.0 ** -12) * size + 2.0 ** -16 * scores
+    assert ((o.double() - want).abs() <= lim).all()
+    for u in range(nodes):
+        assert ((states[u].double() - end[u]).abs() <= 2.0 ** -13 * mass[u] + 1e-30).all(), u
