@@ -21,7 +21,7 @@
 //
 // (With the same warps doing all parts of a row in turn, and five such CTAs on an SM, the chain from
 // a row's load to its gradient set the pace: 1,022 us for 8,835 rows of 152,064 logits, 7,797 of them with
-// weight, where this takes 790, 6.4 TB/s of reads and writes; without the gradient 437.)
+// weight, where this takes 783, 6.5 TB/s of reads and writes; without the gradient 435.)
 //
 // Whether a ratio lies beyond the clip decides a whole gradient, so lp - old is a pair of floats:
 // ln S = k ln 2 + ln f, f near 1, adds no error beyond 3e-8.  What is left is S's own: a power of two is within 2^-22 and
@@ -1180,12 +1180,12 @@ struct Shape {
 // a time; large slices have an SM to themselves, smaller ones share it, with fewer warps each.  A row's sums run over
 // as many threads with and without the gradient, so a policy's log-probs of an evaluation are those of its update to
 // the bit; without it two teams take a row each in turn.  Measured (us; CTAs a row / teams / statistics warps each /
-// gradient warps / CTAs an SM): with the gradient 152,064 x 4,000 rows 407 (4/1/8/12/1) 428 (4/2/4/12/1) 533 (8/1/4/4/2);
-// 64,000 x 5,000 223 (2/1/8/12/1) 235 (2/2/4/12/1); 32,000 x 10,000 226 (1/1/8/12/1) 246 (2/1/4/4/2); 16,000 x 20,000 260
-// (1/1/4/4/2) 271 (1/2/2/4/2); 8,000 x 20,000 158 (1/2/1/3/3) 165 (1/1/2/3/3); 4,000 x 20,000 112 (1/2/1/3/3) 114
-// (1/1/1/1/3); 1,000 x 20,000 78 (1/2/1/3/3) 83 (1/1/1/1/3).  Without it 152,064 x 4,000 243 (4/2/8/1) 287 (4/1/8/1)
-// 266 (4/1/16/1); 64,000 x 5,000 134 (2/2/8/1) 155 (2/1/8/1); 32,000 x 10,000 135 (1/2/8/1) 158 (1/1/8/1); 16,000 x 20,000
-// 136 (1/2/4/2) 142 (1/1/4/3); 8,000 x 20,000 96 (1/2/1/3) 87 (1/2/2/3); 4,000 x 20,000 58 (1/2/1/3) 77 (1/1/1/3).
+// gradient warps / CTAs an SM): with the gradient 152,064 x 4,000 rows 391 (4/1/8/12/1) 423 (4/2/4/12/1) 499 (8/1/4/4/2);
+// 64,000 x 5,000 216 (2/1/8/12/1) 230 (2/2/4/12/1); 32,000 x 10,000 220 (1/1/8/12/1) 226 (2/1/4/4/2); 16,000 x 20,000 241
+// (1/1/4/4/2) 259 (1/2/2/4/2); 8,000 x 20,000 148 (1/2/1/3/3) 157 (1/1/2/3/3); 4,000 x 20,000 96 (1/2/1/3/3) 98
+// (1/1/1/1/3); 1,000 x 20,000 71 (1/2/1/3/3) 79 (1/1/1/1/3).  Without it 152,064 x 4,000 220 (4/2/8/1) 289 (4/1/8/1)
+// 260 (4/1/16/1); 64,000 x 5,000 119 (2/2/8/1) 152 (2/1/8/1); 32,000 x 10,000 119 (1/2/8/1) 152 (1/1/8/1); 16,000 x 20,000
+// 128 (1/2/4/2) 140 (1/1/4/3); 8,000 x 20,000 98 (1/2/1/3) 87 (1/2/2/3); 4,000 x 20,000 60 (1/2/1/3) 78 (1/1/1/3).
 Shape shape_of(int64_t vocab, bool grad) {
     const int64_t vectors = (vocab + 7) / 8 + 1;    // (a row may start inside a vector)
     Shape f = {1, 0, {2, 1, 3, 1, 0}};
